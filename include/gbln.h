@@ -4,7 +4,9 @@
  * Operators: RMSNorm with fused residual add (forward, backward, weight-gradient
  * finalize), rotary position embedding on Q and K (forward, backward, cos/sin
  * table, per-document positions) and SwiGLU (forward, backward); LayerNorm,
- * other gated and plain activations, and MXFP8 outputs for the next GEMM.
+ * other gated and plain activations, MXFP8 and row-scaled FP8 outputs for the
+ * next GEMM, 8-bit activation checkpoints with the backward passes that read
+ * them, and a quantised K/V cache.
  *
  * Sources that name these operators (they print no formulas; the standard
  * definitions are used and written out at each entry point):
@@ -97,7 +99,9 @@ int gbln_version(void);
  *      out; the kernel stopped early instead of hanging, so its outputs are
  *      incomplete;
  *   2  a RoPE call met a position outside [0, max_pos); that token's outputs
- *      are NaN (the table is not read).
+ *      are NaN (the table is not read);
+ *   4  a cache call met a slot beyond the cache's last one: nothing was stored
+ *      for that token, its read-back is NaN.
  * *code receives the word; clear != 0 resets it to zero.  Synchronous
  * (device-wide copy): call it outside hot loops.  Errors: INVALID_ARG for a
  * null code, CUDA if the device is unreachable.
@@ -438,6 +442,164 @@ gbln_status gbln_glu_fwd_mxfp8(const void* gate, const void* up, uint8_t* out_e4
                                uint8_t* out_scale, int64_t T, int64_t I, int64_t ld_gate,
                                int64_t ld_up, gbln_act act, gbln_dtype io,
                                gbln_stream_t stream);
+
+/* ------------------------------------------------------------------------- */
+/* 8-bit storage with float32 scales: the next GEMM's operand, activation      */
+/* checkpoints and the K/V cache ([HF] Kernels intro and §Liger: fusing a       */
+/* producer with its consumer's conversion, training memory)                   */
+/* ------------------------------------------------------------------------- */
+
+/*
+ * A group of values v shares one float32 scale; each value is one byte, an INT8
+ * integer or an E4M3 code.  In float32, every operation rounded to nearest even:
+ *   a     = max(max |v|, 2^-100)
+ *   code  = nearest(v * (qmax / a))    to an integer (INT8, qmax = 127) or to E4M3
+ *                                      (qmax = 448), ties to even
+ *   scale = a / qmax                   value = code * scale
+ * The codes of given values are therefore the same on every run and in any
+ * float32 implementation of these steps.  An all-zero group has the scale
+ * 2^-100 / qmax and codes 0.  A group that holds an infinity or a NaN gets the
+ * scale NaN (its codes are unspecified): all of it reads back as NaN.
+ * INT8 is off by at most a / 254 per value, E4M3 by 2^-4 of the value: INT8 is the
+ * closer one for values of one size, E4M3 where a group holds outliers.
+ */
+typedef enum { GBLN_Q8_INT8 = 0, GBLN_Q8_E4M3 = 1 } gbln_q8;
+
+/*
+ * gbln_rmsnorm_fwd with y also (or only) delivered as E4M3 with one scale per row
+ * (group = row), the operand of a row-scaled FP8 GEMM.  With u = weight * h in
+ * float32, y = u * rstd; rstd cancels out of the codes:
+ *   a = max(max_j |u_j|, 2^-100);  y_e4m3 = E4M3(u * (448 / a));  y_scale = a * rstd / 448
+ * y_e4m3 [T, H] bytes and y_scale [T] float32, both written; y [T, H] io may be
+ * NULL.  Any H and any alignment.  Other arguments, aliasing and errors as
+ * gbln_rmsnorm_fwd; INVALID_ARG also for a null y_e4m3 / y_scale.
+ */
+gbln_status gbln_rmsnorm_fwd_fp8(const void* x, const void* residual, const void* weight,
+                                 void* y, uint8_t* y_e4m3, float* y_scale, void* residual_out,
+                                 float* rstd, int64_t T, int64_t H, float eps, gbln_dtype io,
+                                 gbln_dtype wt, gbln_stream_t stream);
+
+/*
+ * Gated unit forward delivered as E4M3 with one scale per row only: the float32
+ * result f(gate) * up (as gbln_glu_fwd, row strides ld_gate, ld_up >= I) quantised
+ * with group = row.  out_e4m3 [T, I] bytes (contiguous), out_scale [T] float32.
+ * Any I and any alignment; T < 2^31.  Errors as gbln_glu_fwd.
+ */
+gbln_status gbln_glu_fwd_fp8(const void* gate, const void* up, uint8_t* out_e4m3,
+                             float* out_scale, int64_t T, int64_t I, int64_t ld_gate,
+                             int64_t ld_up, gbln_act act, gbln_dtype io, gbln_stream_t stream);
+
+/*
+ * Activation checkpoints: what a backward pass needs of its forward's input, kept
+ * in 8 bits.  A group is 128 consecutive values of a row (the last one of a row may be
+ * shorter): a [T, N] tensor becomes [T, N] bytes and [T, ceil(N / 128)] float32, both
+ * contiguous, 1.03 bytes per value.
+ */
+
+/*
+ * gbln_rmsnorm_fwd that also writes the checkpoint of h (= x + residual rounded to io,
+ * or x) in the same pass: h8 [T, H] bytes, h8_scale [T, ceil(H / 128)] float32.  y, h
+ * and rstd are those of gbln_rmsnorm_fwd.  Any H and alignment.  Arguments, aliasing
+ * and errors as gbln_rmsnorm_fwd; INVALID_ARG also for an unknown fmt or a null h8 /
+ * h8_scale.
+ */
+gbln_status gbln_rmsnorm_fwd_ckpt8(const void* x, const void* residual, const void* weight,
+                                   void* y, void* residual_out, float* rstd, uint8_t* h8,
+                                   float* h8_scale, int64_t T, int64_t H, float eps, gbln_q8 fmt,
+                                   gbln_dtype io, gbln_dtype wt, gbln_stream_t stream);
+
+/* Rows P of the [P, H] float32 dW workspace of gbln_rmsnorm_bwd_ckpt8 (as gbln_rmsnorm_bwd_num_partials). */
+int64_t gbln_rmsnorm_bwd_ckpt8_num_partials(int64_t T, int64_t H, gbln_dtype io);
+
+/*
+ * gbln_rmsnorm_bwd with h read from its checkpoint: n = (h8 * h8_scale) * rstd, the rest
+ * as there (rstd is the forward's, of the exact h).  dw_partial is finished by
+ * gbln_rmsnorm_dw_finalize.  dx may alias dy or dresidual_out exactly.  Bitwise
+ * reproducible for a fixed shape, alignment and GPU model.  Errors as gbln_rmsnorm_bwd;
+ * INVALID_ARG also for an unknown fmt or a null h8 / h8_scale.
+ */
+gbln_status gbln_rmsnorm_bwd_ckpt8(const void* dy, const void* dresidual_out, const uint8_t* h8,
+                                   const float* h8_scale, const void* weight, const float* rstd,
+                                   void* dx, float* dw_partial, int64_t P_cap, int64_t T,
+                                   int64_t H, gbln_q8 fmt, gbln_dtype io, gbln_dtype wt,
+                                   gbln_stream_t stream);
+
+/*
+ * gbln_glu_fwd that also writes the checkpoints of gate and up in the same pass:
+ * gate8, up8 [T, I] bytes and gate_scale, up_scale [T, ceil(I / 128)] float32, all
+ * contiguous.  out may alias gate or up exactly: their checkpoints are of the values
+ * read.  Any I and alignment.  Errors as gbln_glu_fwd; INVALID_ARG also for an unknown
+ * fmt or a null checkpoint pointer.
+ */
+gbln_status gbln_glu_fwd_ckpt8(const void* gate, const void* up, void* out, uint8_t* gate8,
+                               float* gate_scale, uint8_t* up8, float* up_scale, int64_t T,
+                               int64_t I, int64_t ld_gate, int64_t ld_up, int64_t ld_out,
+                               gbln_act act, gbln_q8 fmt, gbln_dtype io, gbln_stream_t stream);
+
+/*
+ * gbln_glu_bwd with gate and up read from their checkpoints: with g = gate8 * gate_scale
+ * and u = up8 * up_scale, dgate = dout * u * f'(g), dup = dout * f(g).  dout, dgate and dup
+ * may be strided rows (each ld >= I).  dgate or dup may alias dout exactly.  Errors as
+ * gbln_glu_bwd; INVALID_ARG also for an unknown fmt.
+ */
+gbln_status gbln_glu_bwd_ckpt8(const void* dout, const uint8_t* gate8, const float* gate_scale,
+                               const uint8_t* up8, const float* up_scale, void* dgate, void* dup,
+                               int64_t T, int64_t I, int64_t ld_dout, int64_t ld_dgate,
+                               int64_t ld_dup, gbln_act act, gbln_q8 fmt, gbln_dtype io,
+                               gbln_stream_t stream);
+
+/*
+ * One 8-bit cache (of K, or of V): `pages` pages of `page_size` slots, a slot holding
+ * one token: Hk heads of D bytes and Hk scales.  Slot s is slot s % page_size of page
+ * s / page_size.  Head h of slot o of page p starts at
+ *   codes + p * page_stride + o * slot_stride + h * head_stride               (bytes)
+ *   scale + p * scale_page_stride + o * scale_slot_stride + h * scale_head_stride (floats)
+ * so pages may be [page_size, Hk, D] or [Hk, page_size, D], and K and V may be
+ * interleaved in one allocation.  The strides must keep pages, slots and heads apart.
+ */
+typedef struct {
+  uint8_t* codes;
+  float* scale;
+  int64_t pages, page_size;
+  int64_t page_stride, slot_stride, head_stride;
+  int64_t scale_page_stride, scale_slot_stride, scale_head_stride;
+} gbln_cache8;
+
+/*
+ * gbln_rope_fwd_ex for serving: rotates q and k by their tokens' positions, and
+ * instead of writing k back quantises the rotated k (float32, unrounded) and v into
+ * their caches at the tokens' slots; a group is one head of one token.
+ * q [T, Hq, D], k, v [T, Hk, D] io with token strides ld_q, ld_k, ld_v (e.g. inside one
+ * packed QKV row); q_out as q with ld_q_out (may alias q exactly).  Hq may be 0 (q and
+ * q_out ignored); Hk >= 1.
+ * positions [T] int32, cos_sin as gbln_rope_fwd.  A position outside [0, max_pos): q_out
+ * is NaN, k's scales are NaN, v is stored as usual, bit 2 of the error word is set.
+ * slots [T] int64, distinct where they are not negative: token t goes to slot slots[t];
+ * a negative one is padding (nothing is stored, its position matters only if Hq > 0); one
+ * at or beyond pages * page_size stores nothing and sets bit 4.  Slots not named keep
+ * their contents.  With two tokens on one slot, that slot's contents are unspecified.
+ * k_cache, v_cache: host structs, read during the call; same pages and page_size.
+ * Errors: INVALID_ARG as gbln_rope_fwd_ex, and for Hk < 1, an unknown fmt, a null or
+ * inconsistent cache, strides that let pages, slots or heads overlap; CUDA.
+ */
+gbln_status gbln_rope_fwd_cache8(const void* q, const void* k, const void* v, void* q_out,
+                                 const int32_t* positions, const float* cos_sin, int64_t max_pos,
+                                 const int64_t* slots, const gbln_cache8* k_cache,
+                                 const gbln_cache8* v_cache, int64_t T, int32_t Hq, int32_t Hk,
+                                 int32_t D, int64_t ld_q, int64_t ld_k, int64_t ld_v,
+                                 int64_t ld_q_out, gbln_rope_pairing pairing, gbln_q8 fmt,
+                                 gbln_dtype io, gbln_stream_t stream);
+
+/*
+ * Read-back: k_out[t] and v_out[t] [Hk, D] io = the values of slot slots[t] (code * scale,
+ * rounded once to io), for t < T in any order and with repeats.  A negative slot gives
+ * zeros; one at or beyond pages * page_size gives NaN and sets bit 4 of the error word.
+ * ld_k_out, ld_v_out >= Hk * D.  Errors as gbln_rope_fwd_cache8.
+ */
+gbln_status gbln_cache8_read(const int64_t* slots, const gbln_cache8* k_cache,
+                             const gbln_cache8* v_cache, void* k_out, void* v_out, int64_t T,
+                             int32_t Hk, int32_t D, int64_t ld_k_out, int64_t ld_v_out,
+                             gbln_q8 fmt, gbln_dtype io, gbln_stream_t stream);
 
 #ifdef __cplusplus
 }

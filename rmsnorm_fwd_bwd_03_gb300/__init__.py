@@ -25,7 +25,9 @@ __all__ = [
     "rope_table", "rope_fwd", "rope_bwd", "rope_fwd_ex", "rope_bwd_ex", "positions_from_cu_seqlens",
     "swiglu_fwd", "swiglu_bwd", "glu_fwd", "glu_bwd", "act_fwd", "act_bwd", "ACT",
     "rmsnorm_fwd_mxfp8", "glu_fwd_mxfp8", "selftest_wait_timeout", "ERR_WAIT_TIMEOUT",
-    "ERR_BAD_POSITION", "PAIRING", "F32", "BF16",
+    "ERR_BAD_POSITION", "PAIRING", "F32", "BF16", "rmsnorm_fwd_fp8", "glu_fwd_fp8",
+    "rmsnorm_fwd_ckpt8", "rmsnorm_bwd_ckpt8", "rmsnorm_bwd_ckpt8_num_partials", "glu_fwd_ckpt8",
+    "glu_bwd_ckpt8", "rope_fwd_cache8", "cache8_read", "ERR_BAD_SLOT", "Q8", "CKPT_GROUP",
 ]
 
 F32 = 0
@@ -33,12 +35,26 @@ BF16 = 1
 # gbln_act
 ACT = {"silu": 0, "gelu_tanh": 1, "gelu_erf": 2, "relu": 3}
 _DTYPE = {torch.float32: F32, torch.bfloat16: BF16}
+# gbln_q8, and the torch dtype that holds the codes of each format
+Q8 = {"int8": 0, "e4m3": 1}
+_CODE_DTYPE = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
+_CODE_FMT = {torch.int8: 0, torch.float8_e4m3fn: 1}
+CKPT_GROUP = 128  # values per scale of an activation checkpoint
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
 _f32 = ctypes.c_float
 _f64 = ctypes.c_double
+
+
+class _Cache8(ctypes.Structure):
+    """``gbln_cache8``."""
+
+    _fields_ = [("codes", _vp), ("scale", _vp)] + [(n, _i64) for n in (
+        "pages", "page_size", "page_stride", "slot_stride", "head_stride",
+        "scale_page_stride", "scale_slot_stride", "scale_head_stride")]
+
 
 # name -> (restype, argtypes); mirrors include/gbln.h
 _SIGNATURES = {
@@ -69,6 +85,15 @@ _SIGNATURES = {
     "gbln_act_bwd": (ctypes.c_int, [_vp, _vp, _vp, _i64, ctypes.c_int, ctypes.c_int, _vp]),
     "gbln_rmsnorm_fwd_mxfp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _f32, ctypes.c_int, ctypes.c_int, _vp]),
     "gbln_glu_fwd_mxfp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, _vp]),
+    "gbln_rmsnorm_fwd_fp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _f32, ctypes.c_int, ctypes.c_int, _vp]),
+    "gbln_glu_fwd_fp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, _vp]),
+    "gbln_rmsnorm_fwd_ckpt8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _f32, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp]),
+    "gbln_rmsnorm_bwd_ckpt8_num_partials": (_i64, [_i64, _i64, ctypes.c_int]),
+    "gbln_rmsnorm_bwd_ckpt8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp]),
+    "gbln_glu_fwd_ckpt8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp]),
+    "gbln_glu_bwd_ckpt8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp]),
+    "gbln_rope_fwd_cache8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, ctypes.POINTER(_Cache8), ctypes.POINTER(_Cache8), _i64, _i32, _i32, _i32, _i64, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp]),
+    "gbln_cache8_read": (ctypes.c_int, [_vp, ctypes.POINTER(_Cache8), ctypes.POINTER(_Cache8), _vp, _vp, _i64, _i32, _i32, _i64, _i64, ctypes.c_int, ctypes.c_int, _vp]),
 }
 
 _lib = None
@@ -114,11 +139,12 @@ def version() -> int:
 
 ERR_WAIT_TIMEOUT = 1   # bits of the device error word
 ERR_BAD_POSITION = 2
+ERR_BAD_SLOT = 4
 
 
 def device_error(clear: bool = False) -> int:
     """``gbln_device_error``: the current device's error word (0 = nothing reported;
-    ERR_WAIT_TIMEOUT, ERR_BAD_POSITION)."""
+    ERR_WAIT_TIMEOUT, ERR_BAD_POSITION, ERR_BAD_SLOT)."""
     v = ctypes.c_uint32(0)
     _check("gbln_device_error", library().gbln_device_error(ctypes.byref(v), 1 if clear else 0))
     return int(v.value)
@@ -643,3 +669,268 @@ def act_bwd(dy, x, act="silu", dx=None):
                                 _stream(x))
     _check("gbln_act_bwd", st)
     return dx
+
+
+# ---------------------------------------------------------------------------
+# 8-bit storage with float32 scales: row-scaled FP8 outputs, activation
+# checkpoints, the K/V cache.  Codes are int8 or float8_e4m3fn tensors (the dtype
+# is the format); value = code * scale.
+# ---------------------------------------------------------------------------
+
+def _code_dtype(fmt):
+    try:
+        return _CODE_DTYPE[fmt]
+    except KeyError:
+        raise ValueError(f"unknown 8-bit format {fmt!r}; expected one of {sorted(_CODE_DTYPE)}") from None
+
+
+def _code_fmt(codes, name):
+    try:
+        return _CODE_FMT[codes.dtype]
+    except KeyError:
+        raise TypeError(f"{name} must be int8 or float8_e4m3fn, not {codes.dtype}") from None
+
+
+def _groups(n):
+    return -(-n // CKPT_GROUP)
+
+
+def _ckpt(codes, scale, shape, name):
+    """The format of a checkpoint of a tensor of that shape."""
+    if tuple(codes.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(codes.shape)}")
+    want = tuple(shape[:-1]) + (_groups(shape[-1]),)
+    if tuple(scale.shape) != want or scale.dtype != torch.float32:
+        raise ValueError(f"{name}_scale must be float32 {want}, not {scale.dtype} {tuple(scale.shape)}")
+    return _code_fmt(codes, name)
+
+
+def rmsnorm_fwd_fp8(x, weight, eps, residual=None, *, want_y=True, residual_out=None):
+    """``gbln_rmsnorm_fwd_fp8``.  Returns ``(y, y_e4m3, y_scale, h, rstd)``.
+
+    y_e4m3: float8_e4m3fn of x's shape; y_scale: float32, one per row; y (x's dtype) is
+    None unless ``want_y``.
+    """
+    H = x.shape[-1]
+    T = x.numel() // H if H else 0
+    _like(residual, x, "residual", "x")
+    _like(residual_out if residual is not None else None, x, "residual_out", "x")
+    _vec(weight, H, "weight")
+    y = torch.empty_like(x) if want_y else None
+    q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    sc = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(x)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    st = library().gbln_rmsnorm_fwd_fp8(
+        _dev(x, "x"), _opt(residual, "residual"), _dev(weight, "weight"), _opt(y, "y"),
+        q.data_ptr(), sc.data_ptr(),
+        _opt(residual_out, "residual_out") if residual is not None else None, rstd.data_ptr(),
+        T, H, float(eps), _io(x), _io(weight), _stream(x))
+    _check("gbln_rmsnorm_fwd_fp8", st)
+    return y, q, sc, (residual_out if residual is not None else x), rstd
+
+
+def glu_fwd_fp8(gate, up, act="silu"):
+    """``gbln_glu_fwd_fp8``: f(gate) * up delivered as E4M3 with one scale per row.  Returns
+    ``(out_e4m3, out_scale)``: float8_e4m3fn [T, I] and float32 [T].  gate and up may be
+    strided row views (e.g. halves of a packed [T, 2I] tensor)."""
+    _like(up, gate, "up", "gate")
+    T, I, ldg = _rows2d(gate, "gate")
+    _, _, ldu = _rows2d(up, "up")
+    q = torch.empty((T, I), dtype=torch.float8_e4m3fn, device=gate.device)
+    sc = torch.empty(T, dtype=torch.float32, device=gate.device)
+    st = library().gbln_glu_fwd_fp8(gate.data_ptr(), up.data_ptr(), q.data_ptr(), sc.data_ptr(),
+                                    T, I, ldg, ldu, ACT[act], _io(gate), _stream(gate))
+    _check("gbln_glu_fwd_fp8", st)
+    return q, sc
+
+
+def rmsnorm_fwd_ckpt8(x, weight, eps, residual=None, *, fmt="int8", y=None, residual_out=None):
+    """``gbln_rmsnorm_fwd_ckpt8``: :func:`rmsnorm_fwd` that also saves h in 8 bits (``fmt``
+    "int8" or "e4m3").  Returns ``(y, h, rstd, h8, h8_scale)``: h8 of x's shape (int8 or
+    float8_e4m3fn), h8_scale float32 with one scale per 128 values of a row.  The backward
+    pass, :func:`rmsnorm_bwd_ckpt8`, needs h8, h8_scale and rstd, not h."""
+    H = x.shape[-1]
+    T = x.numel() // H if H else 0
+    _like(residual, x, "residual", "x")
+    _like(y, x, "y", "x")
+    _like(residual_out if residual is not None else None, x, "residual_out", "x")
+    _vec(weight, H, "weight")
+    h8 = torch.empty(x.shape, dtype=_code_dtype(fmt), device=x.device)
+    sc = torch.empty(x.shape[:-1] + (_groups(H),), dtype=torch.float32, device=x.device)
+    if y is None:
+        y = torch.empty_like(x)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(x)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    st = library().gbln_rmsnorm_fwd_ckpt8(
+        _dev(x, "x"), _opt(residual, "residual"), _dev(weight, "weight"), _dev(y, "y"),
+        _opt(residual_out, "residual_out") if residual is not None else None, rstd.data_ptr(),
+        h8.data_ptr(), sc.data_ptr(), T, H, float(eps), Q8[fmt], _io(x), _io(weight), _stream(x))
+    _check("gbln_rmsnorm_fwd_ckpt8", st)
+    return y, (residual_out if residual is not None else x), rstd, h8, sc
+
+
+def rmsnorm_bwd_ckpt8_num_partials(T: int, H: int, dtype=torch.bfloat16) -> int:
+    """``gbln_rmsnorm_bwd_ckpt8_num_partials``: rows P of the [P, H] float32 dW workspace."""
+    P = library().gbln_rmsnorm_bwd_ckpt8_num_partials(int(T), int(H), _DTYPE[dtype])
+    if P < 0:
+        raise GblnError("gbln_rmsnorm_bwd_ckpt8_num_partials", 1)
+    return int(P)
+
+
+def rmsnorm_bwd_ckpt8(dy, h8, h8_scale, weight, rstd, dresidual_out=None, *, dx=None, dw_partial=None):
+    """``gbln_rmsnorm_bwd_ckpt8``: :func:`rmsnorm_bwd` with h read from its 8-bit checkpoint.
+    Returns ``(dx, dw_partial, P)``; finish dW with :func:`rmsnorm_dw_finalize`."""
+    H = dy.shape[-1]
+    T = dy.numel() // H if H else 0
+    fmt = _ckpt(h8, h8_scale, dy.shape, "h8")
+    _like(dresidual_out, dy, "dresidual_out", "dy")
+    _like(dx, dy, "dx", "dy")
+    _vec(weight, H, "weight")
+    _vec(rstd, T, "rstd", torch.float32)
+    _rows_f32(dw_partial, H, "dw_partial")
+    P = rmsnorm_bwd_ckpt8_num_partials(T, H, dy.dtype)
+    if dx is None:
+        dx = torch.empty_like(dy)
+    if dw_partial is None:
+        dw_partial = torch.empty((max(P, 1), H), dtype=torch.float32, device=dy.device)
+    st = library().gbln_rmsnorm_bwd_ckpt8(
+        _dev(dy, "dy"), _opt(dresidual_out, "dresidual_out"), _dev(h8, "h8"), _dev(h8_scale, "h8_scale"),
+        _dev(weight, "weight"), _dev(rstd, "rstd"), _dev(dx, "dx"), _dev(dw_partial, "dw_partial"),
+        dw_partial.shape[0], T, H, fmt, _io(dy), _io(weight), _stream(dy))
+    _check("gbln_rmsnorm_bwd_ckpt8", st)
+    return dx, dw_partial, P
+
+
+def glu_fwd_ckpt8(gate, up, act="silu", *, fmt="int8", out=None):
+    """``gbln_glu_fwd_ckpt8``: :func:`glu_fwd` that also saves gate and up in 8 bits (``fmt``
+    "int8" or "e4m3").  Returns ``(out, gate8, gate_scale, up8, up_scale)``: codes [T, I] and
+    float32 scales [T, ceil(I / 128)], contiguous."""
+    _like(up, gate, "up", "gate")
+    _like(out, gate, "out", "gate")
+    T, I, ldg = _rows2d(gate, "gate")
+    _, _, ldu = _rows2d(up, "up")
+    dt = _code_dtype(fmt)
+    gq, uq = (torch.empty((T, I), dtype=dt, device=gate.device) for _ in range(2))
+    gs, us = (torch.empty((T, _groups(I)), dtype=torch.float32, device=gate.device) for _ in range(2))
+    if out is None:
+        out = torch.empty((T, I), dtype=gate.dtype, device=gate.device)
+    _, _, ldo = _rows2d(out, "out")
+    st = library().gbln_glu_fwd_ckpt8(gate.data_ptr(), up.data_ptr(), out.data_ptr(), gq.data_ptr(),
+                                      gs.data_ptr(), uq.data_ptr(), us.data_ptr(), T, I, ldg, ldu, ldo,
+                                      ACT[act], Q8[fmt], _io(gate), _stream(gate))
+    _check("gbln_glu_fwd_ckpt8", st)
+    return out, gq, gs, uq, us
+
+
+def glu_bwd_ckpt8(dout, gate8, gate_scale, up8, up_scale, act="silu", dgate=None, dup=None):
+    """``gbln_glu_bwd_ckpt8``: :func:`glu_bwd` with gate and up read from their 8-bit
+    checkpoints.  Returns ``(dgate, dup)``, which may be views of one [T, 2I] tensor."""
+    if dout.dim() != 2:
+        raise ValueError("dout must be [T, I]")
+    fmt = _ckpt(gate8, gate_scale, dout.shape, "gate8")
+    if _ckpt(up8, up_scale, dout.shape, "up8") != fmt:
+        raise TypeError("gate8 and up8 must have the same dtype")
+    _like(dgate, dout, "dgate", "dout")
+    _like(dup, dout, "dup", "dout")
+    T, I, ldd = _rows2d(dout, "dout")
+    if dgate is None:
+        dgate = torch.empty((T, I), dtype=dout.dtype, device=dout.device)
+    if dup is None:
+        dup = torch.empty((T, I), dtype=dout.dtype, device=dout.device)
+    _, _, lddg = _rows2d(dgate, "dgate")
+    _, _, lddu = _rows2d(dup, "dup")
+    st = library().gbln_glu_bwd_ckpt8(dout.data_ptr(), _dev(gate8, "gate8"), _dev(gate_scale, "gate_scale"),
+                                      _dev(up8, "up8"), _dev(up_scale, "up_scale"), dgate.data_ptr(),
+                                      dup.data_ptr(), T, I, ldd, lddg, lddu, ACT[act], fmt, _io(dout),
+                                      _stream(dout))
+    _check("gbln_glu_bwd_ckpt8", st)
+    return dgate, dup
+
+
+def _cache8(codes, scale, Hk, D, name):
+    """``gbln_cache8`` of codes [pages, page_size, Hk, D] and scales [pages, page_size, Hk], each
+    with any page, slot and head strides; and its format."""
+    fmt = _code_fmt(codes, f"{name}_cache")
+    if codes.dim() != 4 or codes.shape[1] < 1 or codes.shape[2:] != (Hk, D):
+        raise ValueError(f"{name}_cache must be [pages, page_size, {Hk}, {D}], not {tuple(codes.shape)}")
+    if scale.dtype != torch.float32 or scale.shape != codes.shape[:3]:
+        raise ValueError(f"{name}_scale must be float32 {tuple(codes.shape[:3])}, not {scale.dtype} {tuple(scale.shape)}")
+    if D > 1 and codes.stride(3) != 1:
+        raise ValueError(f"{name}_cache must hold the {D} values of a head next to one another")
+    for t, n in ((codes, f"{name}_cache"), (scale, f"{name}_scale")):
+        if not t.is_cuda:
+            raise ValueError(f"{n} must be a CUDA tensor")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{n} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    a, b = codes.stride(), scale.stride()
+    return _Cache8(codes.data_ptr(), scale.data_ptr(), codes.shape[0], codes.shape[1],
+                   a[0], a[1], a[2], b[0], b[1], b[2]), fmt
+
+
+def rope_fwd_cache8(q, k, v, positions, cos_sin, slots, k_cache, k_scale, v_cache, v_scale, *,
+                    q_out=None, pairing="half"):
+    """``gbln_rope_fwd_cache8``: rotate q [T, Hq, D] (None: no queries) and k [T, Hk, D], and store
+    the rotated k and v [T, Hk, D] quantised at slots [T] (int64; negative: padding, nothing stored;
+    otherwise distinct) of the paged caches: int8 or float8_e4m3fn [pages, page_size, Hk, D] and
+    float32 scales [pages, page_size, Hk], of any page, slot and head strides.  Slot s is slot
+    ``s % page_size`` of page ``s // page_size``.  q, k and v may have strided token rows (slices of
+    one packed QKV tensor).  Returns ``q_out`` (pass ``q_out=q`` to rotate in place)."""
+    T, Hk, D, ldk = _heads(k, "k")
+    Tq, Hq, Dq, ldq = _heads(q, "q")
+    Tv, Hv, Dv, ldv = _heads(v, "v")
+    if (Tv, Hv, Dv) != (T, Hk, D) or v.dtype != k.dtype:
+        raise ValueError("v must have k's shape and dtype")
+    if q is not None and (Tq != T or Dq != D or q.dtype != k.dtype):
+        raise ValueError("q must be [T, Hq, D] with k's T, D and dtype")
+    if q is None and q_out is not None:
+        raise ValueError("q_out without q")
+    if q_out is not None and (q_out.shape != q.shape or q_out.dtype != q.dtype):
+        raise ValueError(f"q_out must have the shape {tuple(q.shape)} and dtype {q.dtype}")
+    _vec(positions, T, "positions", torch.int32)
+    _vec(slots, T, "slots", torch.int64)
+    _table(cos_sin, D)
+    kc, fmt = _cache8(k_cache, k_scale, Hk, D, "k")
+    vc, vfmt = _cache8(v_cache, v_scale, Hk, D, "v")
+    if vfmt != fmt or v_cache.shape != k_cache.shape:
+        raise ValueError("v_cache must have k_cache's shape and dtype")
+    if q is not None and q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+    _, _, _, ldqo = _heads(q_out, "q_out")
+    st = library().gbln_rope_fwd_cache8(
+        None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        None if q is None else q_out.data_ptr(), _dev(positions, "positions"), _dev(cos_sin, "cos_sin"),
+        cos_sin.shape[0], _dev(slots, "slots"), ctypes.byref(kc), ctypes.byref(vc), T, Hq, Hk, D,
+        ldq, ldk, ldv, ldqo, PAIRING[pairing], fmt, _io(k), _stream(k))
+    _check("gbln_rope_fwd_cache8", st)
+    return q_out
+
+
+def cache8_read(slots, k_cache, k_scale, v_cache, v_scale, *, dtype=torch.bfloat16, k_out=None, v_out=None):
+    """``gbln_cache8_read``: the values of slots [N] (int64; any order, repeats allowed; negative:
+    zeros) of the paged caches as k_out, v_out [N, Hk, D] of ``dtype`` (their token rows may be
+    strided).  Returns ``(k_out, v_out)``."""
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [pages, page_size, Hk, D]")
+    Hk, D = k_cache.shape[2:]
+    N = slots.numel()
+    _vec(slots, N, "slots", torch.int64)
+    for o, n in ((k_out, "k_out"), (v_out, "v_out")):
+        if o is not None and (tuple(o.shape) != (N, Hk, D) or o.dtype != dtype):
+            raise ValueError(f"{n} must have the shape {(N, Hk, D)} and dtype {dtype}")
+    kc, fmt = _cache8(k_cache, k_scale, Hk, D, "k")
+    vc, vfmt = _cache8(v_cache, v_scale, Hk, D, "v")
+    if vfmt != fmt or v_cache.shape != k_cache.shape:
+        raise ValueError("v_cache must have k_cache's shape and dtype")
+    if k_out is None:
+        k_out = torch.empty((N, Hk, D), dtype=dtype, device=slots.device)
+    if v_out is None:
+        v_out = torch.empty((N, Hk, D), dtype=dtype, device=slots.device)
+    _, _, _, ldk = _heads(k_out, "k_out")
+    _, _, _, ldv = _heads(v_out, "v_out")
+    st = library().gbln_cache8_read(_dev(slots, "slots"), ctypes.byref(kc), ctypes.byref(vc), k_out.data_ptr(),
+                                    v_out.data_ptr(), N, Hk, D, ldk, ldv, fmt, _io(k_out), _stream(slots))
+    _check("gbln_cache8_read", st)
+    return k_out, v_out

@@ -12,14 +12,22 @@ computes anything itself.
 * ``rotary(q, k, positions, cos_sin)`` -> ``(q', k')``: RoPE on Q and K
   (rotate-half pairing); the backward pass is the inverse rotation.
 * ``swiglu(gate, up)`` -> ``silu(gate) * up``.
+
+``rms_norm`` and ``swiglu`` take ``checkpoint="int8"`` or ``"e4m3"``: what the backward
+pass needs of the input is then kept in 8 bits (one float32 scale per 128 values
+of a row, 1.03 bytes per value) instead of in the input's dtype, and the backward
+kernels read the codes.  The outputs are the same; the gradients are those of the
+8-bit values.  Memory is saved where nothing else keeps the input: the
+normalised tensor where the residual stream moves on, gate and up always.
 """
 
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
-from . import (rmsnorm_bwd, rmsnorm_dw_finalize, rmsnorm_fwd, rope_bwd, rope_fwd, swiglu_bwd,
-               swiglu_fwd)
+from . import (glu_bwd_ckpt8, glu_fwd_ckpt8, rmsnorm_bwd, rmsnorm_bwd_ckpt8, rmsnorm_dw_finalize,
+               rmsnorm_fwd, rmsnorm_fwd_ckpt8, rope_bwd, rope_fwd, swiglu_bwd, swiglu_fwd)
 
 
 def _c(t):
@@ -44,8 +52,32 @@ class _RMSNorm(torch.autograd.Function):
         return dx, (dx if ctx.has_residual else None), dw, None
 
 
-def rms_norm(x, weight, eps, residual=None):
-    return _RMSNorm.apply(x, residual, weight, float(eps))
+class _RMSNormCkpt8(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps, fmt):
+        ctx.set_materialize_grads(False)
+        weight = weight.contiguous()
+        y, h, rstd, h8, scale = rmsnorm_fwd_ckpt8(x.contiguous(), weight, eps, _c(residual), fmt=fmt)
+        ctx.save_for_backward(h8, scale, weight, rstd)
+        if residual is None:
+            return y
+        return y, h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh=None):
+        h8, scale, weight, rstd = ctx.saved_tensors
+        if dy is None:  # only the residual stream was used
+            return dh, dh, None, None, None
+        dx, part, P = rmsnorm_bwd_ckpt8(dy.contiguous(), h8, scale, weight, rstd, _c(dh))
+        dw = rmsnorm_dw_finalize(part, P).to(weight.dtype)
+        return dx, (dx if ctx.needs_input_grad[1] else None), dw, None, None
+
+
+def rms_norm(x, weight, eps, residual=None, checkpoint=None):
+    if checkpoint is None:
+        return _RMSNorm.apply(x, residual, weight, float(eps))
+    return _RMSNormCkpt8.apply(x, residual, weight, float(eps), checkpoint)
 
 
 class _Rotary(torch.autograd.Function):
@@ -78,5 +110,27 @@ class _SwiGLU(torch.autograd.Function):
         return swiglu_bwd(dout.contiguous(), gate, up)
 
 
-def swiglu(gate, up):
-    return _SwiGLU.apply(gate, up)
+class _SwiGLUCkpt8(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, gate, up, fmt):
+        if gate.shape != up.shape or gate.dtype != up.dtype:
+            raise ValueError("gate and up must have the same shape and dtype")
+        g, u = (t.flatten(0, -2) if t.dim() > 1 else t.unsqueeze(0) for t in (gate, up))
+        # rows of a packed projection output are taken as they lie
+        g, u = (t if t.stride(1) == 1 and t.stride(0) >= t.shape[1] else t.contiguous() for t in (g, u))
+        out, *saved = glu_fwd_ckpt8(g, u, "silu", fmt=fmt)
+        ctx.save_for_backward(*saved)
+        return out.view(gate.shape)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        saved = ctx.saved_tensors
+        dgate, dup = glu_bwd_ckpt8(dout.contiguous().view(saved[0].shape), *saved, "silu")
+        return dgate.view(dout.shape), dup.view(dout.shape), None
+
+
+def swiglu(gate, up, checkpoint=None):
+    if checkpoint is None:
+        return _SwiGLU.apply(gate, up)
+    return _SwiGLUCkpt8.apply(gate, up, checkpoint)

@@ -64,7 +64,7 @@ extern "C" const char* gbln_status_string(int status) {
   }
 }
 
-extern "C" int gbln_version(void) { return 10100; }
+extern "C" int gbln_version(void) { return 10200; }
 
 extern "C" gbln_status gbln_device_error(uint32_t* code, int clear) {
   if (!code) return GBLN_ERR_INVALID_ARG;

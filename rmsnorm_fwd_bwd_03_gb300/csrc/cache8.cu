@@ -1,0 +1,508 @@
+// RoPE on Q and K with K and V quantised into a paged 8-bit cache in the same
+// launch, and the read-back of any slots of that cache.
+//
+// Operator: "Fast-LLM: 高效大语言模型训练框架", §三 框架结构 (attention with RoPE; heads /
+// head_groups / head_size for grouped-query attention) and 训练配置示例 (rotary);
+// "LLaMA-Factory Kernels 系统" (fused RoPE); fusing the conversion into the pass
+// that produces K, as "Kernels（自定义内核）" §Liger fuses a producer with what follows.
+//
+// A group is one head of one token: D codes (INT8 or E4M3) and one float32
+// scale.  HBM-bound: Q is read and written once, K and V are read once and
+// written as one byte per value; decode steps are bound by their single launch.
+
+#include "q8.cuh"
+
+namespace gbln {
+
+namespace {
+
+// Where a cache's slot and head lie (strides in elements).
+struct CacheAt {
+  int64_t page, slot, head;
+  __device__ __forceinline__ int64_t at(int64_t p, int64_t o, int h) const {
+    return p * page + o * slot + (int64_t)h * head;
+  }
+};
+struct Cache {
+  uint8_t* q;
+  float* sc;
+  CacheAt cq, cs;
+};
+
+struct Slots {
+  const int64_t* slots;
+  int64_t total, page_size;  // total = pages * page_size
+  bool small;                // slots fit 32 bits
+  // The page and the slot in it of token t's slot; -1 for "none" (negative), -2
+  // for a slot outside the cache.
+  __device__ __forceinline__ int64_t page_of(int64_t t, int64_t& off) const {
+    const int64_t s = __ldg(slots + t);
+    if (s < 0) return -1;
+    if (s >= total) return -2;
+    if (small) {
+      const uint32_t p = (uint32_t)s / (uint32_t)page_size;
+      off = (int64_t)((uint32_t)s - p * (uint32_t)page_size);
+      return p;
+    }
+    const int64_t p = s / page_size;
+    off = s - p * page_size;
+    return p;
+  }
+};
+
+template <typename T>
+struct WriteArgs {
+  const T* q;
+  const T* k;
+  const T* v;
+  T* qo;
+  const int32_t* pos;
+  const float2* table;
+  int64_t max_pos, rows;
+  int Hq, Hk, D;
+  int64_t ldq, ldk, ldv, ldqo;
+  Slots S;
+  Cache K, V;
+  unsigned int* err;
+  __device__ __forceinline__ const T* src(int64_t t, int h) const {
+    if (h < Hq) return q + t * ldq + (int64_t)h * D;
+    if (h < Hq + Hk) return k + t * ldk + (int64_t)(h - Hq) * D;
+    return v + t * ldv + (int64_t)(h - Hq - Hk) * D;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Vector path: a warp takes one token and up to kWriteHeads head rows per lane.
+// A lane owns two vectors of a head row and the VEC table entries that turn
+// them, whichever pairing: elements v*VEC.. of each half (rotate-half), or the
+// 2*VEC elements from 2*v*VEC (interleaved).  A head row takes nu = D / (2 VEC)
+// lanes out of a group of the next power of two, so 80 or 96 wide heads run here
+// with idle lanes.  The table entries are loaded once per token and lane, and all
+// of a lane's row loads are issued before the first is used.
+// ---------------------------------------------------------------------------
+constexpr int kWriteHeads = 6;
+
+template <typename T, bool IL, int FMT>
+__global__ void __launch_bounds__(256)
+cache8_write_vec(const WriteArgs<T> A, int nu, int lanes, int nchunk, int ch) {
+  constexpr int VEC = VecOf<T>::N;
+  const int half = A.D / 2, HR = A.Hq + A.Hk, HT = HR + A.Hk;
+  const int G = 32 / lanes;
+  const int lane = threadIdx.x & 31;
+  const int v = lane % lanes, g = lane / lanes;
+  const bool on = v < nu;
+  const int64_t item = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int64_t t = item / nchunk;
+  if (t >= A.rows) return;  // uniform per warp
+  const int c = (int)(item - t * nchunk);
+  const int hb = g + G * c * ch;
+  const int ia = IL ? 2 * v * VEC : v * VEC, ib = IL ? ia + VEC : half + ia;
+  int64_t off = 0;
+  const int64_t page = A.S.page_of(t, off);
+  const int p = __ldg(A.pos + t);
+  uint4 a[kWriteHeads], b[kWriteHeads];
+#pragma unroll
+  for (int j = 0; j < kWriteHeads; ++j) {
+    const int h = hb + G * j;
+    if (j < ch && on && h < HT && (h < A.Hq || page >= 0)) {
+      const T* src = A.src(t, h);
+      a[j] = ld_stream(src + ia);
+      b[j] = ld_stream(src + ib);
+    } else {
+      a[j] = b[j] = make_uint4(0, 0, 0, 0);
+    }
+  }
+  const bool ok = p >= 0 && (int64_t)p < A.max_pos;
+  if (c == 0 && lane == 0) {
+    if (!ok && (A.Hq > 0 || page >= 0)) atomicOr(A.err, kErrBadPosition);
+    if (page == -2) atomicOr(A.err, kErrBadSlot);
+  }
+  float2 cs[VEC];
+  if (ok && on) {
+    const float4* e = reinterpret_cast<const float4*>(A.table + (size_t)p * half + v * VEC);
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2) {
+      const float4 f = __ldg(e + i / 2);
+      cs[i] = make_float2(f.x, f.y);
+      cs[i + 1] = make_float2(f.z, f.w);
+    }
+  } else {
+    const float x = ok ? 0.f : __int_as_float(0x7fc00000);  // an idle lane adds nothing to a maximum
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) cs[i] = make_float2(x, x);
+  }
+#pragma unroll
+  for (int j = 0; j < kWriteHeads; ++j) {
+    if (j >= ch) break;
+    const int h = hb + G * j;
+    float xa[VEC], xb[VEC];
+    unpack<VEC>(a[j], xa);
+    unpack<VEC>(b[j], xb);
+    if (h < HR) {
+      float ya[VEC], yb[VEC];
+      if constexpr (IL) {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+          const float2 f = cs[e / 2], f2 = cs[VEC / 2 + e / 2];
+          ya[e] = xa[e] * f.x - xa[e + 1] * f.y;
+          ya[e + 1] = xa[e + 1] * f.x + xa[e] * f.y;
+          yb[e] = xb[e] * f2.x - xb[e + 1] * f2.y;
+          yb[e + 1] = xb[e + 1] * f2.x + xb[e] * f2.y;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          ya[e] = xa[e] * cs[e].x - xb[e] * cs[e].y;
+          yb[e] = xb[e] * cs[e].x + xa[e] * cs[e].y;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        xa[e] = ya[e];
+        xb[e] = yb[e];
+      }
+    }
+    const bool kv = h >= A.Hq && h < HT && page >= 0;
+    if (h < A.Hq && on) {
+      T* dst = A.qo + t * A.ldqo + (int64_t)h * A.D;
+      st_vec(dst + ia, pack<T, VEC>(xa));
+      st_vec(dst + ib, pack<T, VEC>(xb));
+    }
+    if (__any_sync(0xffffffffu, kv)) {  // a warp's head rows may be both Q and K
+      uint32_t m = on ? max(abs_max_bits<VEC>(xa), abs_max_bits<VEC>(xb)) : 0u;
+      for (int o = lanes >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (kv && on) {
+        const float am = q8_amax(m), inv = q8_inv<FMT>(am);
+        const bool isk = h < HR;
+        const int hk = h - (isk ? A.Hq : HR);
+        uint8_t* dst = (isk ? A.K.q : A.V.q) + (isk ? A.K.cq.at(page, off, hk) : A.V.cq.at(page, off, hk));
+        q8_store<FMT, VEC>(xa, inv, dst + ia);
+        q8_store<FMT, VEC>(xb, inv, dst + ib);
+        if (v == 0) {
+          float* sc = isk ? A.K.sc + A.K.cs.at(page, off, hk) : A.V.sc + A.V.cs.at(page, off, hk);
+          *sc = q8_scale<FMT>(am, m);
+        }
+      }
+    }
+  }
+}
+
+// Element path (any head size, alignment and stride): a warp per head row, a
+// lane the pairs l, l + 32, ...; K and V are read twice, the second time from L1.
+template <typename T, bool IL, int FMT>
+__global__ void __launch_bounds__(256) cache8_write_elem(const WriteArgs<T> A) {
+  const int half = A.D / 2, HR = A.Hq + A.Hk, HT = HR + A.Hk;
+  const int lane = threadIdx.x & 31;
+  const int64_t step = ((int64_t)gridDim.x * blockDim.x) >> 5;
+  for (int64_t item = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; item < A.rows * HT; item += step) {
+    const int64_t t = item / HT;
+    const int h = (int)(item - t * HT);
+    int64_t off = 0;
+    const int64_t page = A.S.page_of(t, off);
+    const int p = __ldg(A.pos + t);
+    const bool ok = p >= 0 && (int64_t)p < A.max_pos;
+    if (h == 0 && lane == 0) {
+      if (!ok && (A.Hq > 0 || page >= 0)) atomicOr(A.err, kErrBadPosition);
+      if (page == -2) atomicOr(A.err, kErrBadSlot);
+    }
+    if (h >= A.Hq && page < 0) continue;
+    const T* src = A.src(t, h);
+    auto pair = [&](int i, float& y1, float& y2) {
+      const float x1 = to_f32(src[IL ? 2 * i : i]), x2 = to_f32(src[IL ? 2 * i + 1 : half + i]);
+      if (h < HR) {
+        const float qnan = __int_as_float(0x7fc00000);
+        const float2 f = ok ? __ldg(A.table + (size_t)p * half + i) : make_float2(qnan, qnan);
+        y1 = x1 * f.x - x2 * f.y;
+        y2 = x2 * f.x + x1 * f.y;
+      } else {
+        y1 = x1;
+        y2 = x2;
+      }
+    };
+    if (h < A.Hq) {
+      T* dst = A.qo + t * A.ldqo + (int64_t)h * A.D;
+      for (int i = lane; i < half; i += 32) {
+        float y1, y2;
+        pair(i, y1, y2);
+        dst[IL ? 2 * i : i] = from_f32<T>(y1);
+        dst[IL ? 2 * i + 1 : half + i] = from_f32<T>(y2);
+      }
+      continue;
+    }
+    uint32_t m = 0;
+    for (int i = lane; i < half; i += 32) {
+      float y1, y2;
+      pair(i, y1, y2);
+      m = max(m, max(abs_bits(y1), abs_bits(y2)));
+    }
+    m = group_max<32>(m);
+    const float am = q8_amax(m), inv = q8_inv<FMT>(am);
+    const bool isk = h < HR;
+    const int hk = h - (isk ? A.Hq : HR);
+    const Cache& C = isk ? A.K : A.V;
+    uint8_t* dst = C.q + C.cq.at(page, off, hk);
+    for (int i = lane; i < half; i += 32) {
+      float y1, y2;
+      pair(i, y1, y2);
+      dst[IL ? 2 * i : i] = (uint8_t)q8_code1<FMT>(y1, inv);
+      dst[IL ? 2 * i + 1 : half + i] = (uint8_t)q8_code1<FMT>(y2, inv);
+    }
+    if (lane == 0) C.sc[C.cs.at(page, off, hk)] = q8_scale<FMT>(am, m);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Read-back: a warp per token.  A unit is N consecutive codes of one head (16 on
+// the vector path: one 16-byte load, 32 or 64 bytes stored); the lanes walk the
+// token's units of K, then of V.
+// ---------------------------------------------------------------------------
+template <typename T>
+struct ReadArgs {
+  Slots S;
+  Cache K, V;
+  T* ko;
+  T* vo;
+  int64_t rows;
+  int Hk, D;
+  int64_t ldk, ldv;
+  unsigned int* err;
+};
+
+template <typename T, int FMT, int N>
+__global__ void __launch_bounds__(256) cache8_read_kernel(const ReadArgs<T> A) {
+  constexpr int U = 4;  // units in flight per lane
+  const int lane = threadIdx.x & 31;
+  const int64_t t = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (t >= A.rows) return;  // uniform per warp
+  int64_t off = 0;
+  const int64_t page = A.S.page_of(t, off);
+  if (page == -2 && lane == 0) atomicOr(A.err, kErrBadSlot);
+  const int per = A.D / N, half = A.Hk * per;
+  const float fill = page == -2 ? __int_as_float(0x7fc00000) : 0.f;  // no slot: zeros
+  for (int u0 = lane; u0 < 2 * half; u0 += 32 * U) {
+    uint4 w[U];
+    float sc[U];
+    T* dst[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int u = u0 + 32 * k;
+      if (u >= 2 * half) continue;
+      const bool isk = u < half;
+      const int r = isk ? u : u - half;
+      const int h = r / per, d = (r - h * per) * N;
+      dst[k] = isk ? A.ko + t * A.ldk + (int64_t)h * A.D + d : A.vo + t * A.ldv + (int64_t)h * A.D + d;
+      w[k] = make_uint4(0, 0, 0, 0);
+      sc[k] = fill;
+      if (page >= 0) {
+        const Cache& C = isk ? A.K : A.V;
+        const uint8_t* src = C.q + C.cq.at(page, off, h) + d;
+        if constexpr (N == 16) w[k] = ld_stream(src);
+        else w[k].x = *src;
+        sc[k] = __ldg(C.sc + C.cs.at(page, off, h));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (u0 + 32 * k >= 2 * half) continue;
+      // An empty slot has codes 0 (value 0): 0 * fill is 0 or NaN.
+      const uint32_t* ww = reinterpret_cast<const uint32_t*>(&w[k]);
+      if constexpr (N == 16) {
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q8_decode4<FMT>(ww[i], v + 4 * i);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = __fmul_rn(v[e], sc[k]);
+        constexpr int VEC = VecOf<T>::N;
+#pragma unroll
+        for (int i = 0; i < 16; i += VEC) {
+          float o[VEC];
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) o[e] = v[i + e];
+          st_vec(dst[k] + i, pack<T, VEC>(o));
+        }
+      } else {
+        float v[4];
+        q8_decode4<FMT>(ww[0], v);
+        *dst[k] = from_f32<T>(__fmul_rn(v[0], sc[k]));
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+constexpr int64_t kLim = 1LL << 40;  // strides and sizes (elements)
+constexpr int64_t kMaxTokens = 1LL << 33;
+
+// Whether the pages, slots and heads of a cache lie apart: each stride reaches
+// past all that the smaller ones span (dimensions of size 1 have no stride).
+bool apart(int64_t pages, int64_t page, int64_t slots, int64_t slot, int64_t heads, int64_t head, int64_t width) {
+  int64_t n[3] = {pages, slots, heads}, st[3] = {page, slot, head};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (st[j] < st[i]) {
+        const int64_t a = n[i], b = st[i];
+        n[i] = n[j]; st[i] = st[j];
+        n[j] = a; st[j] = b;
+      }
+  double span = (double)width;  // 2^62 and more would overflow an integer
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] <= 1) continue;
+    if (st[i] < 0 || (double)st[i] < span) return false;
+    span += (double)st[i] * (double)(n[i] - 1);
+  }
+  return span < 1.0e18;
+}
+
+bool cache_ok(const gbln_cache8* c, int32_t Hk, int32_t D) {
+  if (!c || c->pages < 0 || c->page_size <= 0 || c->pages > kLim || c->page_size > kLim) return false;
+  if (c->pages > 0 && c->page_size > kLim / c->pages) return false;
+  return apart(c->pages, c->page_stride, c->page_size, c->slot_stride, Hk, c->head_stride, D) &&
+         apart(c->pages, c->scale_page_stride, c->page_size, c->scale_slot_stride, Hk, c->scale_head_stride, 1);
+}
+
+// A token stride: at least the row's width, the last row far from overflow.
+bool ld_fits(int64_t T, int64_t w, int64_t ld) { return ld >= w && ld <= kLim && (double)T * (double)ld < 1.0e18; }
+
+Cache cache_of(const gbln_cache8* c) {
+  return {c->codes, c->scale, {c->page_stride, c->slot_stride, c->head_stride},
+          {c->scale_page_stride, c->scale_slot_stride, c->scale_head_stride}};
+}
+bool strides_multiple(const gbln_cache8* c, int n) {
+  return c->page_stride % n == 0 && c->slot_stride % n == 0 && c->head_stride % n == 0;
+}
+Slots slots_of(const gbln_cache8* c, const int64_t* slots) {
+  const int64_t total = c->pages * c->page_size;
+  return {slots, total, c->page_size, total < (1LL << 31) && c->page_size < (1LL << 31)};
+}
+
+template <typename T, bool IL, int FMT>
+gbln_status write_launch(const WriteArgs<T>& A, bool cache_aligned, cudaStream_t s) {
+  constexpr int VEC = VecOf<T>::N;
+  const int HT = A.Hq + 2 * A.Hk;
+  const auto row16 = [](const void* p, int64_t ld) { return aligned16(p) && (ld * (int64_t)sizeof(T)) % 16 == 0; };
+  const bool vec = A.D % (2 * VEC) == 0 && A.D / (2 * VEC) <= 32 && aligned16(A.table) && cache_aligned &&
+                   (A.Hq == 0 || (row16(A.q, A.ldq) && row16(A.qo, A.ldqo))) && row16(A.k, A.ldk) && row16(A.v, A.ldv);
+  if (vec) {
+    const int nu = A.D / (2 * VEC);
+    int lanes = 1;
+    while (lanes < nu) lanes *= 2;
+    const int G = 32 / lanes, L = (HT + G - 1) / G;  // head rows per lane and token
+    const int nchunk = (L + kWriteHeads - 1) / kWriteHeads;
+    const int ch = (L + nchunk - 1) / nchunk;
+    const int64_t blocks = (A.rows * nchunk + 7) / 8;  // 8 warps per block
+    if (blocks <= 0x7fffffffLL) {
+      cache8_write_vec<T, IL, FMT><<<(unsigned)blocks, 256, 0, s>>>(A, nu, lanes, nchunk, ch);
+      return launch_status();
+    }
+  }
+  cache8_write_elem<T, IL, FMT><<<grid_for(A.rows * HT, 8, 1 << 20), 256, 0, s>>>(A);
+  return launch_status();
+}
+
+template <typename T>
+gbln_status write_typed(const WriteArgs<T>& A, bool il, int fmt, bool cache_aligned, cudaStream_t s) {
+  if (fmt == GBLN_Q8_INT8)
+    return il ? write_launch<T, true, GBLN_Q8_INT8>(A, cache_aligned, s)
+              : write_launch<T, false, GBLN_Q8_INT8>(A, cache_aligned, s);
+  return il ? write_launch<T, true, GBLN_Q8_E4M3>(A, cache_aligned, s)
+            : write_launch<T, false, GBLN_Q8_E4M3>(A, cache_aligned, s);
+}
+
+template <typename T>
+gbln_status read_typed(const ReadArgs<T>& A, int fmt, bool cache_aligned, cudaStream_t s) {
+  const bool vec = A.D % 16 == 0 && cache_aligned && aligned16(A.ko) && aligned16(A.vo) &&
+                   (A.ldk * (int64_t)sizeof(T)) % 16 == 0 && (A.ldv * (int64_t)sizeof(T)) % 16 == 0;
+  const int64_t blocks = (A.rows + 7) / 8;  // at most 2^30 for kMaxTokens
+#define GBLN_READ8(FMT, N) cache8_read_kernel<T, FMT, N><<<(unsigned)blocks, 256, 0, s>>>(A)
+  if (fmt == GBLN_Q8_INT8) {
+    if (vec) GBLN_READ8(GBLN_Q8_INT8, 16);
+    else GBLN_READ8(GBLN_Q8_INT8, 1);
+  } else {
+    if (vec) GBLN_READ8(GBLN_Q8_E4M3, 16);
+    else GBLN_READ8(GBLN_Q8_E4M3, 1);
+  }
+#undef GBLN_READ8
+  return launch_status();
+}
+
+}  // namespace
+
+}  // namespace gbln
+
+using namespace gbln;
+
+extern "C" gbln_status gbln_rope_fwd_cache8(const void* q, const void* k, const void* v, void* q_out,
+                                            const int32_t* positions, const float* cos_sin,
+                                            int64_t max_pos, const int64_t* slots,
+                                            const gbln_cache8* k_cache, const gbln_cache8* v_cache,
+                                            int64_t T, int32_t Hq, int32_t Hk, int32_t D, int64_t ld_q,
+                                            int64_t ld_k, int64_t ld_v, int64_t ld_q_out,
+                                            gbln_rope_pairing pairing, gbln_q8 fmt, gbln_dtype io,
+                                            gbln_stream_t stream) {
+  if (!dtype_ok(io) || !q8_ok(fmt) || (pairing != GBLN_ROPE_HALF && pairing != GBLN_ROPE_INTERLEAVED))
+    return GBLN_ERR_INVALID_ARG;
+  if (T < 0 || T > kMaxTokens || Hq < 0 || Hk <= 0 || D <= 0 || (D & 1) || max_pos < 0) return GBLN_ERR_INVALID_ARG;
+  if (((int64_t)Hq + 2 * (int64_t)Hk) * D > (1 << 24)) return GBLN_ERR_INVALID_ARG;
+  const int64_t qw = (int64_t)Hq * D, kw = (int64_t)Hk * D;
+  if ((Hq > 0 && (!ld_fits(T, qw, ld_q) || !ld_fits(T, qw, ld_q_out))) || !ld_fits(T, kw, ld_k) || !ld_fits(T, kw, ld_v))
+    return GBLN_ERR_INVALID_ARG;
+  if (!cache_ok(k_cache, Hk, D) || !cache_ok(v_cache, Hk, D)) return GBLN_ERR_INVALID_ARG;
+  if (k_cache->pages != v_cache->pages || k_cache->page_size != v_cache->page_size) return GBLN_ERR_INVALID_ARG;
+  if (T == 0) return GBLN_OK;  // nothing is read or written: pointers are not examined
+  if (!k || !v || !positions || !cos_sin || !slots || (Hq > 0 && (!q || !q_out))) return GBLN_ERR_INVALID_ARG;
+  if (k_cache->pages > 0 && (!k_cache->codes || !k_cache->scale || !v_cache->codes || !v_cache->scale))
+    return GBLN_ERR_INVALID_ARG;
+  if (!aligned_to(cos_sin, 8) || !aligned_to(slots, 8)) return GBLN_ERR_INVALID_ARG;  // float2, int64
+  unsigned int* err = device_error_word();
+  if (!err) return GBLN_ERR_CUDA;
+  const bool il = pairing == GBLN_ROPE_INTERLEAVED;
+  const int n = io == GBLN_F32 ? 4 : 8;  // codes per store
+  const bool ca = aligned_to(k_cache->codes, n) && aligned_to(v_cache->codes, n) && strides_multiple(k_cache, n) &&
+                  strides_multiple(v_cache, n);
+  cudaStream_t s = (cudaStream_t)stream;
+#define GBLN_WRITE_ARGS(TY)                                                                               \
+  const WriteArgs<TY> A{(const TY*)q, (const TY*)k, (const TY*)v, (TY*)q_out, positions, (const float2*)cos_sin, \
+                        max_pos, T, Hq, Hk, D, ld_q, ld_k, ld_v, ld_q_out, slots_of(k_cache, slots),       \
+                        cache_of(k_cache), cache_of(v_cache), err}
+  if (io == GBLN_F32) {
+    GBLN_WRITE_ARGS(float);
+    return write_typed<float>(A, il, fmt, ca, s);
+  }
+  GBLN_WRITE_ARGS(bf16);
+  return write_typed<bf16>(A, il, fmt, ca, s);
+#undef GBLN_WRITE_ARGS
+}
+
+extern "C" gbln_status gbln_cache8_read(const int64_t* slots, const gbln_cache8* k_cache,
+                                        const gbln_cache8* v_cache, void* k_out, void* v_out, int64_t T,
+                                        int32_t Hk, int32_t D, int64_t ld_k_out, int64_t ld_v_out,
+                                        gbln_q8 fmt, gbln_dtype io, gbln_stream_t stream) {
+  if (!dtype_ok(io) || !q8_ok(fmt)) return GBLN_ERR_INVALID_ARG;
+  if (T < 0 || T > kMaxTokens || Hk <= 0 || D <= 0) return GBLN_ERR_INVALID_ARG;
+  if (2 * (int64_t)Hk * D > (1 << 24)) return GBLN_ERR_INVALID_ARG;
+  const int64_t kw = (int64_t)Hk * D;
+  if (!ld_fits(T, kw, ld_k_out) || !ld_fits(T, kw, ld_v_out)) return GBLN_ERR_INVALID_ARG;
+  if (!cache_ok(k_cache, Hk, D) || !cache_ok(v_cache, Hk, D)) return GBLN_ERR_INVALID_ARG;
+  if (k_cache->pages != v_cache->pages || k_cache->page_size != v_cache->page_size) return GBLN_ERR_INVALID_ARG;
+  if (T == 0) return GBLN_OK;  // nothing is read or written: pointers are not examined
+  if (!slots || !k_out || !v_out || !aligned_to(slots, 8)) return GBLN_ERR_INVALID_ARG;
+  if (k_cache->pages > 0 && (!k_cache->codes || !k_cache->scale || !v_cache->codes || !v_cache->scale))
+    return GBLN_ERR_INVALID_ARG;
+  unsigned int* err = device_error_word();
+  if (!err) return GBLN_ERR_CUDA;
+  const bool ca = aligned16(k_cache->codes) && aligned16(v_cache->codes) && strides_multiple(k_cache, 16) &&
+                  strides_multiple(v_cache, 16);
+  cudaStream_t s = (cudaStream_t)stream;
+#define GBLN_READ_ARGS(TY)                                                                             \
+  const ReadArgs<TY> A{slots_of(k_cache, slots), cache_of(k_cache), cache_of(v_cache), (TY*)k_out, (TY*)v_out, \
+                       T, Hk, D, ld_k_out, ld_v_out, err}
+  if (io == GBLN_F32) {
+    GBLN_READ_ARGS(float);
+    return read_typed<float>(A, fmt, ca, s);
+  }
+  GBLN_READ_ARGS(bf16);
+  return read_typed<bf16>(A, fmt, ca, s);
+#undef GBLN_READ_ARGS
+}

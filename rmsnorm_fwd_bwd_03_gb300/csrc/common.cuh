@@ -364,6 +364,7 @@ constexpr uint32_t kWaitPolls = 1u << 22;
 // Bits of the per-device error word (see gbln_device_error).
 constexpr uint32_t kErrWaitTimeout = 1u;   // a bounded wait on an mbarrier ran out
 constexpr uint32_t kErrBadPosition = 2u;   // a RoPE position outside [0, max_pos)
+constexpr uint32_t kErrBadSlot = 4u;       // a cache slot outside the cache
 
 // ---------------------------------------------------------------------------
 // Host side

@@ -14,9 +14,11 @@
 // projection output, for instance) by (row group, column block) units.  The
 // activation is recomputed in the backward pass; nothing is saved.  The gated
 // forward can also deliver its output as MXFP8 (E4M3 codes and one E8M0 scale
-// per 32 values of a row) for the down projection.
+// per 32 values of a row) or as E4M3 with one float32 scale per row for the down
+// projection, and save gate and up as 8-bit checkpoints (one float32 scale per
+// 128 values of a row) that a backward pass reads.
 
-#include "common.cuh"
+#include "q8.cuh"
 
 namespace gbln {
 
@@ -399,6 +401,248 @@ glu_fwd_mx(const T* gate, const T* up, MxOut mx, int64_t T_, int64_t ncol, int64
 }
 
 // ---------------------------------------------------------------------------
+// Forward with row-scaled E4M3 output: one block per row.  The scale needs the
+// whole row's maximum before the first code, so the outputs wait for it in
+// float32 registers (VPT vectors per thread): gate and up are read once.
+// ---------------------------------------------------------------------------
+template <typename T, int ACT, int TPR, int VPT>
+__global__ void __launch_bounds__(TPR)
+glu_fwd_row8(const T* gate, const T* up, uint8_t* q, float* sc, int64_t rows, int I, int64_t ldg,
+             int64_t ldu) {
+  constexpr int VEC = VecOf<T>::N;
+  constexpr int FMT = GBLN_Q8_E4M3;
+  __shared__ uint32_t redm[TPR / 32];
+  const int64_t row = blockIdx.x;
+  const int nvec = I / VEC, l = threadIdx.x;
+  uint4 ga[VPT], ua[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int iv = l + v * TPR;
+    if (iv < nvec) {
+      ga[v] = ld_stream(gate + row * ldg + (int64_t)iv * VEC);
+      ua[v] = ld_stream(up + row * ldu + (int64_t)iv * VEC);
+    }
+  }
+  float o[VPT][VEC];
+  uint32_t m = 0;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    if (l + v * TPR < nvec) {
+      float g[VEC], u[VEC];
+      unpack<VEC>(ga[v], g);
+      unpack<VEC>(ua[v], u);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) o[v][e] = act_f<T, ACT>(g[e]) * u[e];
+      m = max(m, abs_max_bits<VEC>(o[v]));
+    }
+  }
+  m = group_max<32>(m);
+  if constexpr (TPR > 32) {
+    if ((l & 31) == 0) redm[l >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TPR / 32; ++i) m = max(m, redm[i]);
+  }
+  const float a = q8_amax(m), inv = q8_inv<FMT>(a);
+  if (l == 0) sc[row] = q8_scale<FMT>(a, m);
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int iv = l + v * TPR;
+    if (iv < nvec) q8_store<FMT, VEC>(o[v], inv, q + row * I + (int64_t)iv * VEC);
+  }
+}
+
+// The same for any alignment and width: the row is read a second time to write
+// the codes, from L2 for all but the widest rows.
+template <typename T, int ACT>
+__global__ void __launch_bounds__(512)
+glu_fwd_row8_elem(const T* gate, const T* up, uint8_t* q, float* sc, int64_t rows, int64_t I,
+                  int64_t ldg, int64_t ldu) {
+  constexpr int FMT = GBLN_Q8_E4M3;
+  __shared__ uint32_t redm[16];
+  const int64_t row = blockIdx.x;
+  const T* gr = gate + row * ldg;
+  const T* ur = up + row * ldu;
+  uint32_t m = 0;
+#pragma unroll 4
+  for (int64_t j = threadIdx.x; j < I; j += blockDim.x)
+    m = max(m, abs_bits(act_f<T, ACT>(to_f32(gr[j])) * to_f32(ur[j])));
+  m = group_max<32>(m);
+  if ((threadIdx.x & 31) == 0) redm[threadIdx.x >> 5] = m;
+  __syncthreads();
+  for (int i = 0; i < (int)blockDim.x / 32; ++i) m = max(m, redm[i]);
+  const float a = q8_amax(m), inv = q8_inv<FMT>(a);
+  if (threadIdx.x == 0) sc[row] = q8_scale<FMT>(a, m);
+#pragma unroll 4
+  for (int64_t j = threadIdx.x; j < I; j += blockDim.x)
+    q[row * I + j] = (uint8_t)q8_code1<FMT>(act_f<T, ACT>(to_f32(gr[j])) * to_f32(ur[j]), inv);
+}
+
+// ---------------------------------------------------------------------------
+// Forward that also saves gate and up as 8-bit checkpoints.  Units as in
+// glu_fwd_rows; a checkpoint group is 128 / VEC consecutive column vectors, held
+// by consecutive lanes (blockDim is a multiple of 32, so column blocks start at
+// a group), and every lane takes part in its maximum.
+// ---------------------------------------------------------------------------
+struct GluCkpt {
+  uint8_t* gq;
+  float* gs;
+  uint8_t* uq;
+  float* us;
+};
+struct GluCkptIn {
+  const uint8_t* gq;
+  const float* gs;
+  const uint8_t* uq;
+  const float* us;
+};
+
+template <int FMT, int VEC>
+__device__ __forceinline__ void ckpt_store(const float (&v)[VEC], bool on, int64_t row, int64_t c, int64_t I,
+                                           int64_t ng, uint8_t* q, float* sc) {
+  constexpr int LPG = kCkptGroup / VEC;
+  const uint32_t m = group_max<LPG>(abs_max_bits<VEC>(v));
+  if (on) {
+    const float a = q8_amax(m);
+    q8_store<FMT, VEC>(v, q8_inv<FMT>(a), q + row * I + c * VEC);
+    if (c % LPG == 0) sc[row * ng + c / LPG] = q8_scale<FMT>(a, m);
+  }
+}
+
+template <typename T, int ACT, int FMT, int UNROLL>
+__global__ void __launch_bounds__(kGluBlock)
+glu_fwd_ckpt(const T* gate, const T* up, T* out, const GluCkpt C, int64_t T_, int64_t ncol, int64_t ldg,
+             int64_t ldu, int64_t ldo) {
+  constexpr int VEC = VecOf<T>::N;
+  constexpr int LPG = kCkptGroup / VEC;
+  const int64_t I = ncol * VEC, ng = (ncol + LPG - 1) / LPG;
+  const int cb = blockDim.x;
+  const int64_t ncb = (ncol + cb - 1) / cb;
+  const int64_t units = (T_ + UNROLL - 1) / UNROLL * ncb;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int64_t rg = u / ncb;
+    const int64_t c = (u - rg * ncb) * cb + threadIdx.x;
+    const bool on = c < ncol;
+    const int64_t r0 = rg * UNROLL;
+    Packed<T, VEC> g[UNROLL], v[UNROLL];
+#pragma unroll
+    for (int k = 0; k < UNROLL; ++k) {
+      if (on && r0 + k < T_) {
+        g[k].load(gate + (r0 + k) * ldg + c * VEC);
+        v[k].load(up + (r0 + k) * ldu + c * VEC);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < UNROLL; ++k) {
+      if (r0 + k >= T_) break;  // uniform across the block
+      float gf[VEC], uf[VEC], o[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) gf[e] = uf[e] = 0.f;
+      if (on) {
+        g[k].get(gf);
+        v[k].get(uf);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = act_f<T, ACT>(gf[e]) * uf[e];
+        store_n<T, VEC>(out + (r0 + k) * ldo + c * VEC, o);
+      }
+      ckpt_store<FMT, VEC>(gf, on, r0 + k, c, I, ng, C.gq, C.gs);
+      ckpt_store<FMT, VEC>(uf, on, r0 + k, c, I, ng, C.uq, C.us);
+    }
+  }
+}
+
+// Any alignment and width: one warp per checkpoint group, lane l the values l,
+// l + 32, l + 64, l + 96 of it.
+template <typename T, int ACT, int FMT>
+__global__ void __launch_bounds__(kGluBlock)
+glu_fwd_ckpt_elem(const T* gate, const T* up, T* out, const GluCkpt C, int64_t T_, int64_t I, int64_t ldg,
+                  int64_t ldu, int64_t ldo) {
+  const int lane = threadIdx.x & 31;
+  const int64_t ng = (I + kCkptGroup - 1) / kCkptGroup;
+  const int64_t step = (int64_t)gridDim.x * (kGluBlock / 32);
+  for (int64_t u = (int64_t)blockIdx.x * (kGluBlock / 32) + (threadIdx.x >> 5); u < T_ * ng; u += step) {
+    const int64_t row = u / ng;
+    const int64_t j0 = (u - row * ng) * kCkptGroup + lane;
+    float g[4], v[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int64_t j = j0 + 32 * m;
+      g[m] = j < I ? to_f32(gate[row * ldg + j]) : 0.f;
+      v[m] = j < I ? to_f32(up[row * ldu + j]) : 0.f;
+    }
+    const uint32_t gm = group_max<32>(abs_max_bits<4>(g)), um = group_max<32>(abs_max_bits<4>(v));
+    const float ga = q8_amax(gm), ua = q8_amax(um);
+    const float gi = q8_inv<FMT>(ga), ui = q8_inv<FMT>(ua);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int64_t j = j0 + 32 * m;
+      if (j < I) {
+        out[row * ldo + j] = from_f32<T>(act_f<T, ACT>(g[m]) * v[m]);
+        C.gq[row * I + j] = (uint8_t)q8_code1<FMT>(g[m], gi);
+        C.uq[row * I + j] = (uint8_t)q8_code1<FMT>(v[m], ui);
+      }
+    }
+    if (lane == 0) {
+      C.gs[u] = q8_scale<FMT>(ga, gm);
+      C.us[u] = q8_scale<FMT>(ua, um);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward from the checkpoints, units as in glu_bwd_rows (VEC = 1: any
+// alignment).  A lane's VEC columns lie in one group: VEC divides 128 and c * VEC
+// is a multiple of VEC.
+// ---------------------------------------------------------------------------
+template <typename T, int VEC, int ACT, int FMT, int UNROLL>
+__global__ void __launch_bounds__(kGluBlock)
+glu_bwd_ckpt(const T* dout, const GluCkptIn C, T* dgate, T* dup, int64_t T_, int64_t ncol, int64_t ldd,
+             int64_t lddg, int64_t lddu) {
+  constexpr int LPG = kCkptGroup / VEC;
+  const int64_t I = ncol * VEC, ng = (ncol + LPG - 1) / LPG;
+  const int cb = blockDim.x;
+  const int64_t ncb = (ncol + cb - 1) / cb;
+  const int64_t units = (T_ + UNROLL - 1) / UNROLL * ncb;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int64_t rg = u / ncb;
+    const int64_t c = (u - rg * ncb) * cb + threadIdx.x;
+    if (c >= ncol) continue;
+    const int64_t r0 = rg * UNROLL;
+    Packed<T, VEC> d[UNROLL];
+    Codes<FMT, VEC> g[UNROLL], v[UNROLL];
+    float gs[UNROLL], us[UNROLL];
+#pragma unroll
+    for (int k = 0; k < UNROLL; ++k) {
+      if (r0 + k < T_) {
+        d[k].load(dout + (r0 + k) * ldd + c * VEC);
+        g[k].load(C.gq + (r0 + k) * I + c * VEC);
+        v[k].load(C.uq + (r0 + k) * I + c * VEC);
+        gs[k] = __ldg(C.gs + (r0 + k) * ng + c / LPG);
+        us[k] = __ldg(C.us + (r0 + k) * ng + c / LPG);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < UNROLL; ++k) {
+      if (r0 + k < T_) {
+        float df[VEC], gf[VEC], uf[VEC], dg[VEC], du[VEC];
+        d[k].get(df);
+        g[k].get(gf, gs[k]);
+        v[k].get(uf, us[k]);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          float f, fp;
+          act_fd<T, ACT>(gf[e], f, fp);
+          du[e] = df[e] * f;
+          dg[e] = df[e] * uf[e] * fp;
+        }
+        store_n<T, VEC>(dgate + (r0 + k) * lddg + c * VEC, dg);
+        store_n<T, VEC>(dup + (r0 + k) * lddu + c * VEC, du);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
 
@@ -528,6 +772,69 @@ void act_bwd_launch(const void* dy, const void* x, void* dx, int64_t n, cudaStre
     act_bwd_kernel<T, 1, ACT, U><<<resident_grid((n + U - 1) / U / kGluBlock + 1), kGluBlock, 0, s>>>(
         (const T*)dy, (const T*)x, (T*)dx, n);
   }
+}
+
+// Threads per row of glu_fwd_row8: four vectors each, up to 1024 threads.
+constexpr int64_t kRow8MaxVec = 4096;
+
+template <typename T, int ACT>
+void glu_fwd_row8_launch(const void* g, const void* u, uint8_t* q, float* sc, int64_t rows, int64_t I,
+                         int64_t ldg, int64_t ldu, cudaStream_t s) {
+  constexpr int VEC = VecOf<T>::N;
+  const int64_t nvec = I / VEC;
+  const bool vec = I % VEC == 0 && nvec <= kRow8MaxVec && aligned16(g) && aligned16(u) && ldg % VEC == 0 &&
+                   ldu % VEC == 0 && aligned_to(q, VEC);
+  const unsigned grid = (unsigned)rows;
+  if (!vec) {
+    const int block = I <= 1024 ? 128 : 512;
+    glu_fwd_row8_elem<T, ACT><<<grid, block, 0, s>>>((const T*)g, (const T*)u, q, sc, rows, I, ldg, ldu);
+    return;
+  }
+#define GBLN_ROW8(TPR, VPT) \
+  glu_fwd_row8<T, ACT, TPR, VPT><<<grid, TPR, 0, s>>>((const T*)g, (const T*)u, q, sc, rows, (int)I, ldg, ldu)
+  if (nvec <= 128) GBLN_ROW8(64, 2);
+  else if (nvec <= 256) GBLN_ROW8(64, 4);
+  else if (nvec <= 512) GBLN_ROW8(128, 4);
+  else if (nvec <= 1024) GBLN_ROW8(256, 4);
+  else if (nvec <= 2048) GBLN_ROW8(512, 4);
+  else GBLN_ROW8(1024, 4);
+#undef GBLN_ROW8
+}
+
+template <typename T, int ACT, int FMT>
+void glu_fwd_ckpt_launch(const void* g, const void* u, void* o, GluCkpt C, int64_t rows, int64_t I,
+                         int64_t ldg, int64_t ldu, int64_t ldo, cudaStream_t s) {
+  constexpr int VEC = VecOf<T>::N;
+  const bool vec = I % VEC == 0 && aligned16(g) && aligned16(u) && aligned16(o) && ldg % VEC == 0 &&
+                   ldu % VEC == 0 && ldo % VEC == 0 && aligned_to(C.gq, VEC) && aligned_to(C.uq, VEC);
+  if (vec) {
+    constexpr int U = 4;
+    const int64_t ncol = I / VEC;
+    const int cb = col_block(ncol);
+    const int64_t units = (rows + U - 1) / U * ((ncol + cb - 1) / cb);
+    glu_fwd_ckpt<T, ACT, FMT, U><<<resident_grid(units, cb), cb, 0, s>>>((const T*)g, (const T*)u, (T*)o, C,
+                                                                           rows, ncol, ldg, ldu, ldo);
+  } else {
+    const int64_t units = rows * ((I + kCkptGroup - 1) / kCkptGroup);
+    glu_fwd_ckpt_elem<T, ACT, FMT><<<resident_grid((units + 7) / 8), kGluBlock, 0, s>>>(
+        (const T*)g, (const T*)u, (T*)o, C, rows, I, ldg, ldu, ldo);
+  }
+}
+
+template <typename T, int ACT, int FMT>
+void glu_bwd_ckpt_launch(const void* d, GluCkptIn C, void* dg, void* du, int64_t rows, int64_t I,
+                         int64_t ldd, int64_t lddg, int64_t lddu, cudaStream_t s) {
+  constexpr int VEC = VecOf<T>::N;
+  constexpr int U = 2;
+  const bool vec = I % VEC == 0 && aligned16(d) && aligned16(dg) && aligned16(du) && ldd % VEC == 0 &&
+                   lddg % VEC == 0 && lddu % VEC == 0 && aligned_to(C.gq, VEC) && aligned_to(C.uq, VEC);
+  const int64_t ncol = vec ? I / VEC : I;
+  const int cb = col_block(ncol);
+  const unsigned grid = resident_grid((rows + U - 1) / U * ((ncol + cb - 1) / cb), cb);
+  if (vec)
+    glu_bwd_ckpt<T, VEC, ACT, FMT, U><<<grid, cb, 0, s>>>((const T*)d, C, (T*)dg, (T*)du, rows, ncol, ldd, lddg, lddu);
+  else
+    glu_bwd_ckpt<T, 1, ACT, FMT, U><<<grid, cb, 0, s>>>((const T*)d, C, (T*)dg, (T*)du, rows, ncol, ldd, lddg, lddu);
 }
 
 // Dispatch on (io, act) to a templated launcher F<T, ACT>::run(args...).
@@ -663,5 +970,75 @@ extern "C" gbln_status gbln_act_bwd(const void* dy, const void* x, void* dx, int
     GBLN_DISPATCH_ACT(bf16, act, GBLN_ACT_BWD)
   }
 #undef GBLN_ACT_BWD
+  return launch_status();
+}
+
+extern "C" gbln_status gbln_glu_fwd_fp8(const void* gate, const void* up, uint8_t* out_e4m3,
+                                        float* out_scale, int64_t T, int64_t I, int64_t ld_gate,
+                                        int64_t ld_up, gbln_act act, gbln_dtype io,
+                                        gbln_stream_t stream) {
+  if (!dtype_ok(io) || !act_ok(act) || !sizes_ok(T, I) || T > (1LL << 31) - 1) return GBLN_ERR_INVALID_ARG;
+  if (!ld_ok(T, I, ld_gate) || !ld_ok(T, I, ld_up)) return GBLN_ERR_INVALID_ARG;
+  if (T == 0) return GBLN_OK;  // nothing is read or written: pointers are not examined
+  if (!gate || !up || !out_e4m3 || !out_scale) return GBLN_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+#define GBLN_GLU_FWD_FP8(TY, A) \
+  glu_fwd_row8_launch<TY, A>(gate, up, out_e4m3, out_scale, T, I, ld_gate, ld_up, s)
+  if (io == GBLN_F32) {
+    GBLN_DISPATCH_ACT(float, act, GBLN_GLU_FWD_FP8)
+  } else {
+    GBLN_DISPATCH_ACT(bf16, act, GBLN_GLU_FWD_FP8)
+  }
+#undef GBLN_GLU_FWD_FP8
+  return launch_status();
+}
+
+extern "C" gbln_status gbln_glu_fwd_ckpt8(const void* gate, const void* up, void* out, uint8_t* gate8,
+                                          float* gate_scale, uint8_t* up8, float* up_scale, int64_t T,
+                                          int64_t I, int64_t ld_gate, int64_t ld_up, int64_t ld_out,
+                                          gbln_act act, gbln_q8 fmt, gbln_dtype io,
+                                          gbln_stream_t stream) {
+  if (!dtype_ok(io) || !act_ok(act) || !q8_ok(fmt) || !sizes_ok(T, I)) return GBLN_ERR_INVALID_ARG;
+  if (!ld_ok(T, I, ld_gate) || !ld_ok(T, I, ld_up) || !ld_ok(T, I, ld_out)) return GBLN_ERR_INVALID_ARG;
+  if (T == 0) return GBLN_OK;  // nothing is read or written: pointers are not examined
+  if (!gate || !up || !out || !gate8 || !gate_scale || !up8 || !up_scale) return GBLN_ERR_INVALID_ARG;
+  if (sm_count() <= 0) return GBLN_ERR_CUDA;
+  cudaStream_t s = (cudaStream_t)stream;
+  const GluCkpt C{gate8, gate_scale, up8, up_scale};
+#define GBLN_GLU_FWD_CKPT(TY, A)                                                              \
+  fmt == GBLN_Q8_INT8                                                                         \
+      ? glu_fwd_ckpt_launch<TY, A, GBLN_Q8_INT8>(gate, up, out, C, T, I, ld_gate, ld_up, ld_out, s) \
+      : glu_fwd_ckpt_launch<TY, A, GBLN_Q8_E4M3>(gate, up, out, C, T, I, ld_gate, ld_up, ld_out, s)
+  if (io == GBLN_F32) {
+    GBLN_DISPATCH_ACT(float, act, GBLN_GLU_FWD_CKPT)
+  } else {
+    GBLN_DISPATCH_ACT(bf16, act, GBLN_GLU_FWD_CKPT)
+  }
+#undef GBLN_GLU_FWD_CKPT
+  return launch_status();
+}
+
+extern "C" gbln_status gbln_glu_bwd_ckpt8(const void* dout, const uint8_t* gate8, const float* gate_scale,
+                                          const uint8_t* up8, const float* up_scale, void* dgate,
+                                          void* dup, int64_t T, int64_t I, int64_t ld_dout,
+                                          int64_t ld_dgate, int64_t ld_dup, gbln_act act, gbln_q8 fmt,
+                                          gbln_dtype io, gbln_stream_t stream) {
+  if (!dtype_ok(io) || !act_ok(act) || !q8_ok(fmt) || !sizes_ok(T, I)) return GBLN_ERR_INVALID_ARG;
+  if (!ld_ok(T, I, ld_dout) || !ld_ok(T, I, ld_dgate) || !ld_ok(T, I, ld_dup)) return GBLN_ERR_INVALID_ARG;
+  if (T == 0) return GBLN_OK;  // nothing is read or written: pointers are not examined
+  if (!dout || !gate8 || !gate_scale || !up8 || !up_scale || !dgate || !dup) return GBLN_ERR_INVALID_ARG;
+  if (sm_count() <= 0) return GBLN_ERR_CUDA;
+  cudaStream_t s = (cudaStream_t)stream;
+  const GluCkptIn C{gate8, gate_scale, up8, up_scale};
+#define GBLN_GLU_BWD_CKPT(TY, A)                                                                   \
+  fmt == GBLN_Q8_INT8                                                                              \
+      ? glu_bwd_ckpt_launch<TY, A, GBLN_Q8_INT8>(dout, C, dgate, dup, T, I, ld_dout, ld_dgate, ld_dup, s) \
+      : glu_bwd_ckpt_launch<TY, A, GBLN_Q8_E4M3>(dout, C, dgate, dup, T, I, ld_dout, ld_dgate, ld_dup, s)
+  if (io == GBLN_F32) {
+    GBLN_DISPATCH_ACT(float, act, GBLN_GLU_BWD_CKPT)
+  } else {
+    GBLN_DISPATCH_ACT(bf16, act, GBLN_GLU_BWD_CKPT)
+  }
+#undef GBLN_GLU_BWD_CKPT
   return launch_status();
 }

@@ -1,0 +1,147 @@
+// 8-bit storage with float32 scales: INT8 or E4M3 codes and one scale per group
+// of values (a whole row, 128 consecutive values of a row, one head of one
+// token).  Every operation below is a float32 operation rounded to nearest, and
+// none may be contracted or reassociated: together they define the codes.
+//
+//   a     = max(max |v|, 2^-100)       (the floor keeps qmax / a finite)
+//   inv   = qmax / a                   qmax = 127 (INT8), 448 (E4M3)
+//   code  = RNE(v * inv)               to an integer / to E4M3
+//   scale = a / qmax                   value = code * scale
+//
+// |v * inv| <= qmax (1 + 2^-22), which rounds to at most qmax: no clamp.  A
+// group that holds an infinity or a NaN gets the scale NaN, so that all of it
+// reads back as NaN.  The scale is exact to half a float32 step, so INT8 is off
+// by at most a / 254 per value and E4M3 by 2^-4 of the value (plus a / 448 * 2^-10
+// among its subnormals).
+#pragma once
+
+#include "common.cuh"
+
+namespace gbln {
+
+constexpr float kQ8AmaxMin = 7.888609052210118e-31f;  // 2^-100
+constexpr int kCkptGroup = 128;                       // values per checkpoint scale
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+template <int FMT>
+struct Q8Max {
+  static constexpr float v = FMT == GBLN_Q8_INT8 ? 127.0f : 448.0f;
+};
+
+inline bool q8_ok(int fmt) { return fmt == GBLN_Q8_INT8 || fmt == GBLN_Q8_E4M3; }
+
+// Magnitudes are compared as the bit patterns of |v|: an unsigned maximum
+// orders finite < infinity < NaN, so a NaN is never lost.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+template <int N>
+__device__ __forceinline__ uint32_t abs_max_bits(const float (&v)[N]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < N; ++e) m = max(m, abs_bits(v[e]));
+  return m;
+}
+
+// Maximum over groups of W consecutive lanes; every lane gets it.
+template <int W>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  if constexpr (W == 32) {
+    return __reduce_max_sync(0xffffffffu, v);
+  } else {
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o, W));
+    return v;
+  }
+}
+
+__device__ __forceinline__ float q8_amax(uint32_t amax_bits) {
+  return fmaxf(__uint_as_float(amax_bits), kQ8AmaxMin);
+}
+template <int FMT>
+__device__ __forceinline__ float q8_inv(float a) { return __fdiv_rn(Q8Max<FMT>::v, a); }
+// The stored scale; NaN where the group is not finite.
+template <int FMT>
+__device__ __forceinline__ float q8_scale(float a, uint32_t amax_bits) {
+  return amax_bits < kInfBits ? __fdiv_rn(a, Q8Max<FMT>::v) : __int_as_float(0x7fc00000);
+}
+
+// Adding 1.5 * 2^23 rounds |t| <= 2^22 to the nearest integer (ties to even)
+// and leaves its two's complement in the low bits of the sum.
+constexpr float kRoundMagic = 12582912.0f;
+
+// Codes of N values, packed little-endian.
+template <int FMT>
+__device__ __forceinline__ uint32_t q8_code1(float v, float inv) {
+  const float t = __fmul_rn(v, inv);
+  if constexpr (FMT == GBLN_Q8_INT8) return __float_as_uint(__fadd_rn(t, kRoundMagic)) & 0xffu;
+  else return e4m3x2(t, 0.f) & 0xffu;
+}
+template <int FMT>
+__device__ __forceinline__ uint32_t q8_code4(float v0, float v1, float v2, float v3, float inv) {
+  const float t0 = __fmul_rn(v0, inv), t1 = __fmul_rn(v1, inv), t2 = __fmul_rn(v2, inv), t3 = __fmul_rn(v3, inv);
+  if constexpr (FMT == GBLN_Q8_INT8) {
+    const uint32_t a = __float_as_uint(__fadd_rn(t0, kRoundMagic)), b = __float_as_uint(__fadd_rn(t1, kRoundMagic));
+    const uint32_t c = __float_as_uint(__fadd_rn(t2, kRoundMagic)), d = __float_as_uint(__fadd_rn(t3, kRoundMagic));
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+  } else {
+    return e4m3x2(t0, t1) | (e4m3x2(t2, t3) << 16);
+  }
+}
+// N consecutive codes to q, aligned to N bytes when N > 1.
+template <int FMT, int N>
+__device__ __forceinline__ void q8_store(const float (&v)[N], float inv, uint8_t* q) {
+  static_assert(N == 1 || N == 4 || N == 8, "1, 4 or 8 codes");
+  if constexpr (N == 1) *q = (uint8_t)q8_code1<FMT>(v[0], inv);
+  else if constexpr (N == 4) *reinterpret_cast<uint32_t*>(q) = q8_code4<FMT>(v[0], v[1], v[2], v[3], inv);
+  else
+    *reinterpret_cast<uint2*>(q) = make_uint2(q8_code4<FMT>(v[0], v[1], v[2], v[3], inv),
+                                              q8_code4<FMT>(v[4], v[5], v[6], v[7], inv));
+}
+
+// Four codes as float32 (not yet scaled).  INT8: the byte, biased by 128, becomes
+// the low mantissa byte of 2^23 + byte, from which 2^23 + 128 is subtracted.
+template <int FMT>
+__device__ __forceinline__ void q8_decode4(uint32_t w, float* v) {
+  if constexpr (FMT == GBLN_Q8_INT8) {
+    const uint32_t x = w ^ 0x80808080u;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      v[e] = __uint_as_float(__byte_perm(x, 0x4b000000u, 0x7540 + e)) - 8388736.0f;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * e)), __NV_E4M3);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      v[2 * e] = f.x;
+      v[2 * e + 1] = f.y;
+    }
+  }
+}
+
+// N codes kept packed between load and use.
+template <int FMT, int N>
+struct Codes {
+  static_assert(N == 1 || N == 4 || N == 8, "1, 4 or 8 codes");
+  uint32_t w[N == 8 ? 2 : 1];
+  __device__ __forceinline__ void load(const uint8_t* p) {
+    if constexpr (N == 8) {
+      asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+    } else if constexpr (N == 4) {
+      asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+    } else {
+      w[0] = *p;
+    }
+  }
+  // code * scale, rounded to float32
+  __device__ __forceinline__ void get(float (&v)[N], float scale) const {
+    float t[N == 1 ? 4 : N];
+    q8_decode4<FMT>(w[0], t);
+    if constexpr (N == 8) q8_decode4<FMT>(w[1], t + 4);
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = __fmul_rn(t[e], scale);
+  }
+};
+
+inline bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+}  // namespace gbln

@@ -1,0 +1,791 @@
+// RMSNorm with 8-bit results: the forward (fused residual add) whose output is
+// E4M3 with one float32 scale per row, the forward that also saves its input as
+// an 8-bit checkpoint (INT8 or E4M3, one float32 scale per 128 values of a row),
+// and the backward that reads the checkpoint.
+//
+// Operator: "Fast-LLM: 高效大语言模型训练框架", §三 技术架构, "Transformer Block 结构"
+// (normalization RMSNorm); fused form as in "LLaMA-Factory Kernels 系统" (fused
+// RMSNorm) and "Kernels（自定义内核）" §Liger (fusion saves memory and traffic).
+//
+// HBM-bound, as the plain operator: every row is read once, held in registers
+// across its reduction, and written once.
+//
+// Row scale: with u = w h, the output is y = u rstd and its largest magnitude is
+// rstd max|u|.  rstd cancels out of the codes, RNE(u * 448 / max|u|), so the sum
+// of squares and the maximum come out of ONE reduction over the row, and the
+// scale is max|u| rstd / 448.
+//
+// Checkpoint: 128 values are 16 lanes of 16-byte bf16 vectors (32 of float32);
+// their maximum takes 4 shuffles (one redux), and the codes are written from the
+// registers that hold h.  The backward reads 1.03 bytes per value instead of 2
+// or 4.
+
+#include "q8.cuh"
+
+namespace gbln {
+
+namespace {
+
+// What a forward writes in 8 bits.
+enum Mode { kRowE4m3 = 0, kCkptInt8 = 1, kCkptE4m3 = 2 };
+constexpr int mode_fmt(int m) { return m == kCkptInt8 ? GBLN_Q8_INT8 : GBLN_Q8_E4M3; }
+
+template <typename T, typename W>
+struct Fwd8 {
+  const T* x;
+  const T* r;
+  const W* w;
+  T* y;  // may be null with kRowE4m3
+  T* hout;
+  float* rstd;
+  uint8_t* q;
+  float* sc;
+  int64_t rows;
+  int H;
+  int ng;  // scales per row
+  float inv_H, eps;
+};
+
+template <typename T, typename W>
+struct Bwd8 {
+  const T* dy;
+  const T* dres;
+  const uint8_t* hq;
+  const float* hs;
+  const W* w;
+  const float* rstd;
+  T* dx;
+  float* partial;
+  int64_t rows;
+  int H;
+  int ng;
+  float inv_H;
+};
+
+// Sum and maximum over the TPR threads of a row in one barrier pair (TPR > 32:
+// one row per block).
+template <int TPR>
+__device__ __forceinline__ void row_sum_max(float& s, uint32_t& m, float* red, uint32_t* redm) {
+  s = group_sum<32>(s);
+  m = group_max<32>(m);
+  if constexpr (TPR > 32) {
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) {
+      red[warp] = s;
+      redm[warp] = m;
+    }
+    __syncthreads();
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < TPR / 32; ++i) {
+      s += red[i];
+      m = max(m, redm[i]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Forward, vector path: TPR threads per row, VPT 16-byte vectors per thread,
+// BLOCK / TPR rows per block; no loop over rows, so the block scheduler keeps the
+// loads of other rows in flight while one is reduced.  h stays packed: it is
+// exact in T.
+// ---------------------------------------------------------------------------
+template <typename T, typename W, int TPR, int VPT, int BLOCK, bool RES, int MODE>
+__global__ void __launch_bounds__(BLOCK) rms8_fwd_vec(const Fwd8<T, W> A) {
+  constexpr int VEC = VecOf<T>::N;
+  constexpr int FMT = mode_fmt(MODE);
+  constexpr int LPG = kCkptGroup / VEC;  // lanes per checkpoint group
+  __shared__ float red[TPR / 32];
+  __shared__ uint32_t redm[TPR / 32];
+  const int g = threadIdx.x / TPR, l = threadIdx.x % TPR;
+  const int64_t row = (int64_t)blockIdx.x * (BLOCK / TPR) + g;
+  if (row >= A.rows) return;  // uniform per row group; one row per block when TPR > 32
+  const int nvec = A.H / VEC;
+  const size_t base = (size_t)row * A.H;
+
+  uint4 xa[VPT], ra[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int iv = l + v * TPR;
+    if (iv < nvec) {
+      xa[v] = ld_stream(A.x + base + (size_t)iv * VEC);
+      if constexpr (RES) ra[v] = ld_stream(A.r + base + (size_t)iv * VEC);
+    }
+  }
+  float ss = 0.f;
+  uint32_t am = 0;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int iv = l + v * TPR;
+    float h[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) h[e] = 0.f;
+    if (iv < nvec) {
+      unpack<VEC>(xa[v], h);
+      if constexpr (RES) {
+        float b[VEC];
+        unpack<VEC>(ra[v], b);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) h[e] += b[e];
+        xa[v] = pack<T, VEC>(h);  // the stored h is what gets normalised and saved
+        unpack<VEC>(xa[v], h);
+        st_vec(A.hout + base + (size_t)iv * VEC, xa[v]);
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) ss = fmaf(h[e], h[e], ss);
+    }
+    if constexpr (MODE == kRowE4m3) {
+      if (iv < nvec) {
+        float wv[VEC];
+        load_weight<W, VEC>(A.w, iv, wv);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) am = max(am, abs_bits(__fmul_rn(wv[e], h[e])));
+      }
+    } else {
+      // All lanes of a warp take part; those past the row's end hold zeros.
+      const uint32_t gm = group_max<LPG>(abs_max_bits<VEC>(h));
+      if (iv < nvec) {
+        const float a = q8_amax(gm);
+        q8_store<FMT, VEC>(h, q8_inv<FMT>(a), A.q + base + (size_t)iv * VEC);
+        if (iv % LPG == 0) A.sc[(size_t)row * A.ng + iv / LPG] = q8_scale<FMT>(a, gm);
+      }
+    }
+  }
+  if constexpr (MODE == kRowE4m3) {
+    row_sum_max<TPR>(ss, am, red, redm);
+  } else {
+    ss = row_sum<TPR>(ss, red);
+  }
+  const float rs = rsqrtf(ss * A.inv_H + A.eps);
+  if (l == 0) A.rstd[row] = rs;
+  float inv = 0.f;
+  if constexpr (MODE == kRowE4m3) {
+    const float a = q8_amax(am);
+    inv = q8_inv<FMT>(a);
+    if (l == 0) A.sc[row] = q8_scale<FMT>(__fmul_rn(a, rs), am);
+  }
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int iv = l + v * TPR;
+    if (iv < nvec) {
+      float h[VEC], wv[VEC], o[VEC];
+      unpack<VEC>(xa[v], h);
+      load_weight<W, VEC>(A.w, iv, wv);
+      if (MODE != kRowE4m3 || A.y) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = wv[e] * (h[e] * rs);
+        st_vec(A.y + base + (size_t)iv * VEC, pack<T, VEC>(o));
+      }
+      if constexpr (MODE == kRowE4m3) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = __fmul_rn(wv[e], h[e]);
+        q8_store<FMT, VEC>(o, inv, A.q + base + (size_t)iv * VEC);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Forward, element path (any alignment and width).  A warp takes chunks of 128
+// consecutive values, lane l the values l, l + 32, l + 64, l + 96: every access
+// of a warp is contiguous, and a chunk is a checkpoint group.  NW warps per row
+// take chunks wi, wi + NW, ...; CACHED keeps up to kElemChunks of them per warp
+// in registers, wider rows are read again (from the thread's own stores, where
+// there is a residual).  One row per NW warps, blockDim / (32 NW) rows per block.
+// ---------------------------------------------------------------------------
+constexpr int kElemChunks = 4;
+
+template <typename T, typename W, bool RES, int MODE, bool CACHED>
+__global__ void __launch_bounds__(1024) rms8_fwd_elem(const Fwd8<T, W> A, int NW) {
+  constexpr int FMT = mode_fmt(MODE);
+  __shared__ float red[32];
+  __shared__ uint32_t redm[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = warp / NW, wi = warp - g * NW;
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / (32 * NW)) + g;
+  const bool live = row < A.rows;  // the barrier below is reached by every warp
+  const size_t base = (size_t)(live ? row : 0) * A.H;
+  const int nchunk = (A.H + kCkptGroup - 1) / kCkptGroup;
+  const int H = live ? A.H : 0;
+
+  float hc[CACHED ? kElemChunks : 1][4];
+  KahanSum ks;
+  uint32_t am = 0;
+
+  auto load = [&](int c, float (&h)[4]) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int j = c * kCkptGroup + m * 32 + lane;
+      h[m] = 0.f;
+      if (j < H) {
+        float a = to_f32(A.x[base + j]);
+        if constexpr (RES) a += to_f32(A.r[base + j]);
+        h[m] = a;
+      }
+    }
+  };
+  auto first = [&](int c, float (&h)[4]) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int j = c * kCkptGroup + m * 32 + lane;
+      if constexpr (RES) {
+        const T hv = from_f32<T>(h[m]);
+        h[m] = to_f32(hv);
+        if (j < H) A.hout[base + j] = hv;
+      }
+      ks.add(h[m] * h[m]);
+      if constexpr (MODE == kRowE4m3)
+        if (j < H) am = max(am, abs_bits(__fmul_rn(to_f32(A.w[j]), h[m])));
+    }
+    if constexpr (MODE != kRowE4m3) {
+      const uint32_t gm = group_max<32>(abs_max_bits<4>(h));
+      const float a = q8_amax(gm), inv = q8_inv<FMT>(a);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int j = c * kCkptGroup + m * 32 + lane;
+        if (j < H) A.q[base + j] = (uint8_t)q8_code1<FMT>(h[m], inv);
+      }
+      if (lane == 0 && live) A.sc[(size_t)row * A.ng + c] = q8_scale<FMT>(a, gm);
+    }
+  };
+  if constexpr (CACHED) {
+#pragma unroll
+    for (int k = 0; k < kElemChunks; ++k)
+      if (wi + k * NW < nchunk) load(wi + k * NW, hc[k]);
+#pragma unroll
+    for (int k = 0; k < kElemChunks; ++k)
+      if (wi + k * NW < nchunk) first(wi + k * NW, hc[k]);
+  } else {
+    for (int c = wi; c < nchunk; c += NW) {
+      load(c, hc[0]);
+      first(c, hc[0]);
+    }
+  }
+
+  float ss = group_sum<32>(ks.s);
+  if constexpr (MODE == kRowE4m3) am = group_max<32>(am);
+  if (NW > 1) {
+    if (lane == 0) {
+      red[warp] = ss;
+      redm[warp] = am;
+    }
+    __syncthreads();
+    ss = 0.f;
+    for (int i = 0; i < NW; ++i) {
+      ss += red[g * NW + i];
+      am = max(am, redm[g * NW + i]);
+    }
+  }
+  const float rs = rsqrtf(ss * A.inv_H + A.eps);
+  if (live && wi == 0 && lane == 0) A.rstd[row] = rs;
+  float inv = 0.f;
+  if constexpr (MODE == kRowE4m3) {
+    const float a = q8_amax(am);
+    inv = q8_inv<FMT>(a);
+    if (live && wi == 0 && lane == 0) A.sc[row] = q8_scale<FMT>(__fmul_rn(a, rs), am);
+  }
+  auto second = [&](int c, const float (&h)[4]) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int j = c * kCkptGroup + m * 32 + lane;
+      if (j < H) {
+        const float wv = to_f32(A.w[j]);
+        if (MODE != kRowE4m3 || A.y) A.y[base + j] = from_f32<T>(wv * (h[m] * rs));
+        if constexpr (MODE == kRowE4m3) A.q[base + j] = (uint8_t)q8_code1<FMT>(__fmul_rn(wv, h[m]), inv);
+      }
+    }
+  };
+  if constexpr (CACHED) {
+#pragma unroll
+    for (int k = 0; k < kElemChunks; ++k)
+      if (wi + k * NW < nchunk) second(wi + k * NW, hc[k]);
+  } else {
+    for (int c = wi; c < nchunk; c += NW) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int j = c * kCkptGroup + m * 32 + lane;
+        if (j < H) hc[0][m] = RES ? to_f32(A.hout[base + j]) : to_f32(A.x[base + j]);
+      }
+      second(c, hc[0]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward, vector path.  gridDim.x = P blocks; block p owns the contiguous rows
+// [p*rows/P, (p+1)*rows/P), its GPB groups of TPR threads take every GPB-th of
+// them.  dW is accumulated per thread in float32 registers, then the groups'
+// sums are added in order: no atomics, one partial row per block.  Only packed
+// inputs stay in registers across the row's reduction.
+// ---------------------------------------------------------------------------
+template <typename T, typename W, int TPR, int VPT, int GPB, bool DRES, int FMT>
+__global__ void __launch_bounds__(TPR * GPB) rms8_bwd_vec(const Bwd8<T, W> A, bool prefetch) {
+  constexpr int VEC = VecOf<T>::N;
+  constexpr int LPG = kCkptGroup / VEC;
+  constexpr int NWG = TPR / 32;
+  __shared__ float red[GPB][2][NWG];
+  const int g = threadIdx.x / TPR, l = threadIdx.x % TPR, lane = threadIdx.x & 31;
+  const int nvec = A.H / VEC;
+  const int64_t P = gridDim.x, p = blockIdx.x;
+  const int64_t r0 = p * A.rows / P, r1 = (p + 1) * A.rows / P;
+
+  float acc[VPT][VEC];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc[v][e] = 0.f;
+
+  int par = 0;
+  for (int64_t row = r0 + g; row < r1; row += GPB) {
+    const size_t base = (size_t)row * A.H;
+    // One row per block: thread 0 asks for the block's next row in L2 while this
+    // one is processed.
+    if constexpr (GPB == 1) {
+      if (threadIdx.x == 0 && row + 1 < r1) {
+        const size_t nb = base + A.H;
+        const uint32_t rb = (uint32_t)(A.H * sizeof(T));
+        prefetch_l2(A.dy + nb, rb);
+        if constexpr (DRES) prefetch_l2(A.dres + nb, rb);
+        if (prefetch) prefetch_l2(A.hq + nb, (uint32_t)A.H);
+      }
+    }
+    uint4 dya[VPT], dra[VPT];
+    Codes<FMT, VEC> ha[VPT];
+    float hs[VPT];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int iv = l + v * TPR;
+      if (iv < nvec) {
+        dya[v] = ld_stream(A.dy + base + (size_t)iv * VEC);
+        ha[v].load(A.hq + base + (size_t)iv * VEC);
+        if constexpr (DRES) dra[v] = ld_stream(A.dres + base + (size_t)iv * VEC);
+        hs[v] = __ldg(A.hs + (size_t)row * A.ng + iv / LPG);
+      }
+    }
+    const float rs = __ldg(A.rstd + row);
+    float dot = 0.f;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int iv = l + v * TPR;
+      if (iv < nvec) {
+        float d[VEC], n[VEC], wv[VEC];
+        unpack<VEC>(dya[v], d);
+        ha[v].get(n, hs[v]);
+        load_weight<W, VEC>(A.w, iv, wv);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          n[e] *= rs;
+          dot = fmaf(d[e] * wv[e], n[e], dot);
+          acc[v][e] = fmaf(d[e], n[e], acc[v][e]);
+        }
+      }
+    }
+    dot = group_sum<32>(dot);
+    if constexpr (TPR > 32) {
+      // red is double-buffered: a buffer is written again only after the group's
+      // next barrier, which every thread reaches after reading it.
+      if (lane == 0) red[g][par][l / 32] = dot;
+      bar_sync_named(1 + g, TPR);
+      dot = red[g][par][0];
+#pragma unroll
+      for (int k = 1; k < NWG; ++k) dot += red[g][par][k];
+      par ^= 1;
+    }
+    const float c = dot * A.inv_H;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int iv = l + v * TPR;
+      if (iv < nvec) {
+        float d[VEC], n[VEC], wv[VEC], o[VEC];
+        unpack<VEC>(dya[v], d);
+        ha[v].get(n, hs[v]);
+        load_weight<W, VEC>(A.w, iv, wv);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = rs * (d[e] * wv[e] - (n[e] * rs) * c);
+        if constexpr (DRES) {
+          float d2[VEC];
+          unpack<VEC>(dra[v], d2);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) o[e] += d2[e];
+        }
+        st_vec(A.dx + base + (size_t)iv * VEC, pack<T, VEC>(o));
+      }
+    }
+  }
+
+  float* prow = A.partial + (size_t)p * A.H;
+  if constexpr (GPB == 1) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int iv = l + v * TPR;
+      if (iv < nvec) {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4)
+          *reinterpret_cast<float4*>(prow + (size_t)iv * VEC + e) =
+              make_float4(acc[v][e], acc[v][e + 1], acc[v][e + 2], acc[v][e + 3]);
+      }
+    }
+  } else {
+    __shared__ float sacc[GPB][TPR * VPT * VEC];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int iv = l + v * TPR;
+      if (iv < nvec) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) sacc[g][iv * VEC + e] = acc[v][e];
+      }
+    }
+    __syncthreads();
+    for (int j = threadIdx.x; j < A.H; j += TPR * GPB) {
+      float s = 0.f;
+#pragma unroll
+      for (int q = 0; q < GPB; ++q) s += sacc[q][j];
+      prow[j] = s;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward, element path: chunks of 128 values per warp as in rms8_fwd_elem.
+// CACHED: the row's values and the dW sums stay in registers; wider rows are
+// read twice and their dW sums are kept in the block's partial row (one row
+// group per block then).
+// ---------------------------------------------------------------------------
+template <typename T, typename W, bool DRES, int FMT, bool CACHED>
+__global__ void __launch_bounds__(CACHED ? 1024 : 512) rms8_bwd_elem(const Bwd8<T, W> A, int NW) {
+  constexpr int C = CACHED ? kElemChunks : 1;
+  extern __shared__ float sacc[];  // CACHED with several groups: one row of dW sums
+  __shared__ float red[2][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int GPB = (int)(blockDim.x / (32 * NW));
+  const int g = warp / NW, wi = warp - g * NW;
+  const int H = A.H, nchunk = (H + kCkptGroup - 1) / kCkptGroup;
+  const int64_t P = gridDim.x, p = blockIdx.x;
+  const int64_t r0 = p * A.rows / P, r1 = (p + 1) * A.rows / P;
+  float* prow = A.partial + (size_t)p * H;
+
+  float acc[C][4], d[C][4], n[C][4];
+#pragma unroll
+  for (int k = 0; k < C; ++k)
+#pragma unroll
+    for (int m = 0; m < 4; ++m) acc[k][m] = 0.f;
+  if constexpr (!CACHED)
+    for (int c = wi; c < nchunk; c += NW)
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        if (const int j = c * kCkptGroup + m * 32 + lane; j < H) prow[j] = 0.f;
+
+  int par = 0;
+  for (int64_t row = r0 + g; row < r1; row += GPB) {
+    const size_t base = (size_t)row * H;
+    const float rs = __ldg(A.rstd + row);
+    KahanSum ks;
+    auto load = [&](int c, float (&dk)[4], float (&nk)[4]) {
+      const float s = __ldg(A.hs + (size_t)row * A.ng + c);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int j = c * kCkptGroup + m * 32 + lane;
+        dk[m] = nk[m] = 0.f;
+        if (j < H) {
+          Codes<FMT, 1> q;
+          float v[1];
+          q.load(A.hq + base + j);
+          q.get(v, s);
+          dk[m] = to_f32(A.dy[base + j]);
+          nk[m] = v[0] * rs;
+        }
+      }
+    };
+    auto dots = [&](int c, const float (&dk)[4], const float (&nk)[4]) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int j = c * kCkptGroup + m * 32 + lane;
+        if (j < H) ks.add(dk[m] * to_f32(A.w[j]) * nk[m]);
+      }
+    };
+    if constexpr (CACHED) {
+#pragma unroll
+      for (int k = 0; k < C; ++k)
+        if (wi + k * NW < nchunk) load(wi + k * NW, d[k], n[k]);
+#pragma unroll
+      for (int k = 0; k < C; ++k)
+        if (wi + k * NW < nchunk) {
+          dots(wi + k * NW, d[k], n[k]);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) acc[k][m] = fmaf(d[k][m], n[k][m], acc[k][m]);
+        }
+    } else {
+      for (int c = wi; c < nchunk; c += NW) {
+        load(c, d[0], n[0]);
+        dots(c, d[0], n[0]);
+      }
+    }
+    float dot = group_sum<32>(ks.s);
+    if (NW > 1) {
+      if (lane == 0) red[par][warp] = dot;
+      bar_sync_named(1 + g, 32 * NW);
+      dot = 0.f;
+      for (int i = 0; i < NW; ++i) dot += red[par][g * NW + i];
+      par ^= 1;
+    }
+    const float cc = dot * A.inv_H;
+    auto store = [&](int c, const float (&dk)[4], const float (&nk)[4]) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int j = c * kCkptGroup + m * 32 + lane;
+        if (j < H) {
+          float o = rs * (dk[m] * to_f32(A.w[j]) - nk[m] * cc);
+          if constexpr (DRES) o += to_f32(A.dres[base + j]);
+          A.dx[base + j] = from_f32<T>(o);
+        }
+      }
+    };
+    if constexpr (CACHED) {
+#pragma unroll
+      for (int k = 0; k < C; ++k)
+        if (wi + k * NW < nchunk) store(wi + k * NW, d[k], n[k]);
+    } else {
+      for (int c = wi; c < nchunk; c += NW) {
+        load(c, d[0], n[0]);  // before the store: dx may alias dy
+        store(c, d[0], n[0]);
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          if (const int j = c * kCkptGroup + m * 32 + lane; j < H) prow[j] = fmaf(d[0][m], n[0][m], prow[j]);
+      }
+    }
+  }
+
+  if constexpr (CACHED) {
+    if (GPB == 1) {
+#pragma unroll
+      for (int k = 0; k < C; ++k)
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          if (const int j = (wi + k * NW) * kCkptGroup + m * 32 + lane; j < H) prow[j] = acc[k][m];
+    } else {
+      for (int q = 0; q < GPB; ++q) {  // groups add in order
+        if (q == g) {
+#pragma unroll
+          for (int k = 0; k < C; ++k)
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+              if (const int j = (wi + k * NW) * kCkptGroup + m * 32 + lane; j < H) {
+                const float s = q == 0 ? acc[k][m] : sacc[j] + acc[k][m];
+                if (q == GPB - 1) prow[j] = s;
+                else sacc[j] = s;
+              }
+        }
+        __syncthreads();
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Launch geometry.
+// ---------------------------------------------------------------------------
+constexpr int64_t kMaxH = 1 << 24;
+constexpr int64_t kMaxRows = (1LL << 31) - 1;
+constexpr int64_t kMaxVecPerRow = 2048;  // 512 threads x 4 vectors
+
+// Element path: warps per row so that a warp holds at most kElemChunks chunks
+// (a power of two up to 32, then the row is not held in registers).
+struct Elem {
+  bool cached;
+  int nw;      // warps per row
+  int block;   // threads
+  int groups;  // rows per block and pass
+};
+Elem elem_geometry(int64_t H) {
+  const int64_t nchunk = (H + kCkptGroup - 1) / kCkptGroup;
+  if (nchunk > 32 * kElemChunks) return {false, 16, 512, 1};
+  int nw = 1;
+  while ((int64_t)nw * kElemChunks < nchunk) nw *= 2;
+  const int block = nw < 8 ? 256 : nw * 32;
+  return {true, nw, block, block / (nw * 32)};
+}
+
+bool vec_width(int64_t H, size_t io) {
+  return (H * (int64_t)io) % 16 == 0 && H * (int64_t)io / 16 <= kMaxVecPerRow;
+}
+
+struct BwdGeometry {
+  int tpr, vpt, gpb;  // tpr 0: element path
+  int bps;            // blocks per SM
+};
+BwdGeometry bwd_geometry(int64_t H, size_t io) {
+  if (!vec_width(H, io)) {
+    const Elem e = elem_geometry(H);
+    return {0, 0, e.groups, e.cached ? 1024 / e.block : 4};
+  }
+  const int64_t nvec = H * (int64_t)io / 16;
+  if (nvec <= 32) return {32, 1, 8, 4};
+  if (nvec <= 64) return {32, 2, 8, 4};
+  if (nvec <= 128) return {64, 2, 4, 4};
+  int tpr = 64;
+  while ((int64_t)tpr * 4 < nvec) tpr *= 2;
+  return {tpr, 4, 1, 512 / tpr > 0 ? 512 / tpr : 1};
+}
+
+int64_t partials_for(int64_t T, const BwdGeometry& g, int sms) {
+  if (T <= 0) return 0;
+  int64_t P = (int64_t)sms * g.bps;
+  const int64_t groups = (T + g.gpb - 1) / g.gpb;
+  if (P > groups) P = groups;
+  return P < 1 ? 1 : P;
+}
+
+template <typename T, typename W, bool RES, int MODE>
+gbln_status fwd_launch(const Fwd8<T, W>& A, cudaStream_t s) {
+  constexpr int VEC = VecOf<T>::N;
+  const bool vec = vec_width(A.H, sizeof(T)) && aligned16(A.x) && aligned16(A.w) && aligned16(A.y) &&
+                   (!RES || (aligned16(A.r) && aligned16(A.hout))) && aligned_to(A.q, VEC);
+  if (!vec) {
+    const Elem e = elem_geometry(A.H);
+    const int64_t blocks = (A.rows + e.groups - 1) / e.groups;
+    if (e.cached) rms8_fwd_elem<T, W, RES, MODE, true><<<(unsigned)blocks, e.block, 0, s>>>(A, e.nw);
+    else rms8_fwd_elem<T, W, RES, MODE, false><<<(unsigned)blocks, e.block, 0, s>>>(A, e.nw);
+    return launch_status();
+  }
+  const int nvec = A.H / VEC;
+#define GBLN_FWD8(TPR, VPT, BLOCK) \
+  rms8_fwd_vec<T, W, TPR, VPT, BLOCK, RES, MODE><<<(unsigned)((A.rows + BLOCK / TPR - 1) / (BLOCK / TPR)), BLOCK, 0, s>>>(A)
+  if (nvec <= 32) GBLN_FWD8(32, 1, 256);
+  else if (nvec <= 64) GBLN_FWD8(32, 2, 256);
+  else if (nvec <= 128) GBLN_FWD8(32, 4, 256);
+  else if (nvec <= 256) GBLN_FWD8(64, 4, 64);
+  else if (nvec <= 512) GBLN_FWD8(128, 4, 128);
+  else if (nvec <= 1024) GBLN_FWD8(256, 4, 256);
+  else GBLN_FWD8(512, 4, 512);
+#undef GBLN_FWD8
+  return launch_status();
+}
+
+template <typename T, typename W, int MODE>
+gbln_status fwd_typed(const void* x, const void* r, const void* w, void* y, void* ho, float* rstd,
+                      uint8_t* q, float* sc, int64_t rows, int64_t H, float eps, cudaStream_t s) {
+  const Fwd8<T, W> A{(const T*)x, (const T*)r, (const W*)w, (T*)y, (T*)ho, rstd, q, sc, rows, (int)H,
+                     (int)((H + kCkptGroup - 1) / kCkptGroup), 1.0f / (float)H, eps};
+  return r ? fwd_launch<T, W, true, MODE>(A, s) : fwd_launch<T, W, false, MODE>(A, s);
+}
+
+template <typename T, typename W, bool DRES, int FMT>
+gbln_status bwd_launch(const Bwd8<T, W>& A, int64_t P, cudaStream_t s) {
+  constexpr int VEC = VecOf<T>::N;
+  const BwdGeometry g = bwd_geometry(A.H, sizeof(T));
+  const bool vec = g.tpr && aligned16(A.dy) && aligned16(A.w) && aligned16(A.dx) && aligned16(A.partial) &&
+                   (!DRES || aligned16(A.dres)) && aligned_to(A.hq, VEC);
+  const unsigned grid = (unsigned)P;
+  if (!vec) {
+    const Elem e = elem_geometry(A.H);
+    const size_t smem = e.groups > 1 ? (size_t)A.H * sizeof(float) : 0;  // at most 2048 values
+    if (e.cached) rms8_bwd_elem<T, W, DRES, FMT, true><<<grid, e.block, smem, s>>>(A, e.nw);
+    else rms8_bwd_elem<T, W, DRES, FMT, false><<<grid, e.block, 0, s>>>(A, e.nw);
+    return launch_status();
+  }
+  const bool prefetch = aligned16(A.hq) && A.H % 16 == 0;
+#define GBLN_BWD8(TPR, VPT, GPB) rms8_bwd_vec<T, W, TPR, VPT, GPB, DRES, FMT><<<grid, TPR * GPB, 0, s>>>(A, prefetch)
+  if (g.tpr == 32 && g.vpt == 1) GBLN_BWD8(32, 1, 8);
+  else if (g.tpr == 32) GBLN_BWD8(32, 2, 8);
+  else if (g.vpt == 2) GBLN_BWD8(64, 2, 4);
+  else if (g.tpr == 64) GBLN_BWD8(64, 4, 1);
+  else if (g.tpr == 128) GBLN_BWD8(128, 4, 1);
+  else if (g.tpr == 256) GBLN_BWD8(256, 4, 1);
+  else GBLN_BWD8(512, 4, 1);
+#undef GBLN_BWD8
+  return launch_status();
+}
+
+template <typename T, typename W>
+gbln_status bwd_typed(const void* dy, const void* dr, const uint8_t* hq, const float* hs, const void* w,
+                      const float* rstd, void* dx, float* partial, int64_t P, int64_t rows, int64_t H,
+                      int fmt, cudaStream_t s) {
+  const Bwd8<T, W> A{(const T*)dy, (const T*)dr, hq, hs, (const W*)w, rstd, (T*)dx, partial, rows, (int)H,
+                     (int)((H + kCkptGroup - 1) / kCkptGroup), 1.0f / (float)H};
+  if (fmt == GBLN_Q8_INT8)
+    return dr ? bwd_launch<T, W, true, GBLN_Q8_INT8>(A, P, s) : bwd_launch<T, W, false, GBLN_Q8_INT8>(A, P, s);
+  return dr ? bwd_launch<T, W, true, GBLN_Q8_E4M3>(A, P, s) : bwd_launch<T, W, false, GBLN_Q8_E4M3>(A, P, s);
+}
+
+gbln_status sizes_and_types(int64_t T, int64_t H, int io, int wt) {
+  if (!dtype_ok(io) || !dtype_ok(wt)) return GBLN_ERR_INVALID_ARG;
+  if (T < 0 || T > kMaxRows || H <= 0 || H > kMaxH) return GBLN_ERR_INVALID_ARG;
+  const bool pair = (io == GBLN_F32 && wt == GBLN_F32) || io == GBLN_BF16;
+  return pair ? GBLN_OK : GBLN_ERR_UNSUPPORTED;
+}
+
+template <int MODE>
+gbln_status fwd_entry(const void* x, const void* residual, const void* w, void* y, uint8_t* q, float* sc,
+                      void* residual_out, float* rstd, int64_t T, int64_t H, float eps, gbln_dtype io,
+                      gbln_dtype wt, gbln_stream_t stream) {
+  if (!(eps >= 0.0f && eps <= 3.4028235e38f)) return GBLN_ERR_INVALID_ARG;  // also rejects NaN
+  const gbln_status st = sizes_and_types(T, H, io, wt);
+  if (st != GBLN_OK) return st;
+  if (T == 0) return GBLN_OK;  // nothing is read or written: pointers are not examined
+  if (!x || !w || !q || !sc || !rstd || (MODE != kRowE4m3 && !y)) return GBLN_ERR_INVALID_ARG;
+  if (residual && !residual_out) return GBLN_ERR_INVALID_ARG;
+  void* ho = residual ? residual_out : nullptr;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (io == GBLN_F32) return fwd_typed<float, float, MODE>(x, residual, w, y, ho, rstd, q, sc, T, H, eps, s);
+  if (wt == GBLN_BF16) return fwd_typed<bf16, bf16, MODE>(x, residual, w, y, ho, rstd, q, sc, T, H, eps, s);
+  return fwd_typed<bf16, float, MODE>(x, residual, w, y, ho, rstd, q, sc, T, H, eps, s);
+}
+
+}  // namespace
+
+}  // namespace gbln
+
+using namespace gbln;
+
+extern "C" gbln_status gbln_rmsnorm_fwd_fp8(const void* x, const void* residual, const void* weight,
+                                            void* y, uint8_t* y_e4m3, float* y_scale,
+                                            void* residual_out, float* rstd, int64_t T, int64_t H,
+                                            float eps, gbln_dtype io, gbln_dtype wt,
+                                            gbln_stream_t stream) {
+  return fwd_entry<kRowE4m3>(x, residual, weight, y, y_e4m3, y_scale, residual_out, rstd, T, H, eps, io,
+                             wt, stream);
+}
+
+extern "C" gbln_status gbln_rmsnorm_fwd_ckpt8(const void* x, const void* residual, const void* weight,
+                                              void* y, void* residual_out, float* rstd, uint8_t* h8,
+                                              float* h8_scale, int64_t T, int64_t H, float eps,
+                                              gbln_q8 fmt, gbln_dtype io, gbln_dtype wt,
+                                              gbln_stream_t stream) {
+  if (!q8_ok(fmt)) return GBLN_ERR_INVALID_ARG;
+  if (fmt == GBLN_Q8_INT8)
+    return fwd_entry<kCkptInt8>(x, residual, weight, y, h8, h8_scale, residual_out, rstd, T, H, eps, io,
+                                wt, stream);
+  return fwd_entry<kCkptE4m3>(x, residual, weight, y, h8, h8_scale, residual_out, rstd, T, H, eps, io, wt,
+                              stream);
+}
+
+extern "C" int64_t gbln_rmsnorm_bwd_ckpt8_num_partials(int64_t T, int64_t H, gbln_dtype io) {
+  if (!dtype_ok(io) || T < 0 || T > kMaxRows || H <= 0 || H > kMaxH) return -1;
+  if (T == 0) return 0;
+  const int sms = sm_count();
+  if (sms <= 0) return -1;
+  return partials_for(T, bwd_geometry(H, dtype_size(io)), sms);
+}
+
+extern "C" gbln_status gbln_rmsnorm_bwd_ckpt8(const void* dy, const void* dresidual_out,
+                                              const uint8_t* h8, const float* h8_scale,
+                                              const void* weight, const float* rstd, void* dx,
+                                              float* dw_partial, int64_t P_cap, int64_t T, int64_t H,
+                                              gbln_q8 fmt, gbln_dtype io, gbln_dtype wt,
+                                              gbln_stream_t stream) {
+  if (!q8_ok(fmt) || P_cap < 0) return GBLN_ERR_INVALID_ARG;
+  const gbln_status st = sizes_and_types(T, H, io, wt);
+  if (st != GBLN_OK) return st;
+  if (T == 0) return GBLN_OK;  // nothing is read or written: pointers are not examined
+  if (!dy || !h8 || !h8_scale || !weight || !rstd || !dx || !dw_partial) return GBLN_ERR_INVALID_ARG;
+  const int sms = sm_count();
+  if (sms <= 0) return GBLN_ERR_CUDA;
+  const int64_t P = partials_for(T, bwd_geometry(H, dtype_size(io)), sms);
+  if (P_cap < P) return GBLN_ERR_WORKSPACE;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (io == GBLN_F32)
+    return bwd_typed<float, float>(dy, dresidual_out, h8, h8_scale, weight, rstd, dx, dw_partial, P, T, H, fmt, s);
+  if (wt == GBLN_BF16)
+    return bwd_typed<bf16, bf16>(dy, dresidual_out, h8, h8_scale, weight, rstd, dx, dw_partial, P, T, H, fmt, s);
+  return bwd_typed<bf16, float>(dy, dresidual_out, h8, h8_scale, weight, rstd, dx, dw_partial, P, T, H, fmt, s);
+}
