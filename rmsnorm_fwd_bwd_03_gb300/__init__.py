@@ -168,13 +168,27 @@ def _io(t: torch.Tensor) -> int:
         raise TypeError(f"unsupported dtype {t.dtype}; expected float32 or bfloat16") from None
 
 
+# The checks below run on every call and stand beside kernels of a few
+# microseconds, so they ask torch only for plain integers: get_device() is -1 on a
+# CPU tensor, and the raw stream handle comes without a Stream object around it.
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _on_device(t: torch.Tensor, name: str) -> None:
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if d != _current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
 def _dev(t: torch.Tensor, name: str) -> int:
-    if not t.is_cuda:
+    if t.get_device() < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    _on_device(t, name)
     return t.data_ptr()
 
 
@@ -183,14 +197,14 @@ def _opt(t, name):
 
 
 def _stream(t: torch.Tensor):
-    return torch.cuda.current_stream(t.device).cuda_stream
+    return _raw_stream(t.get_device())
 
 
 # Shape and dtype checks.  The C entry points receive bare pointers and sizes, so a
 # tensor smaller than the sizes passed would be read or written out of bounds:
 # every tensor is checked against them here, before any call.
 def _like(t, ref, name, ref_name):
-    if t is not None and (tuple(t.shape) != tuple(ref.shape) or t.dtype != ref.dtype):
+    if t is not None and (t.shape != ref.shape or t.dtype is not ref.dtype):
         raise ValueError(f"{name} must have the shape {tuple(ref.shape)} and dtype {ref.dtype} of {ref_name}")
 
 
@@ -481,14 +495,16 @@ def _heads(t, name):
     """(T, H, D, token stride) of a [T, H, D] view whose heads are contiguous in each token row."""
     if t is None:
         return 0, 0, 0, 0
-    if not t.is_cuda:
+    if t.get_device() < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    if t.dim() != 3:
         raise ValueError(f"{name} must be [T, H, D] with contiguous heads in each token row")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
     T, H, D = t.shape
-    return T, H, D, (t.stride(0) if T > 1 else H * D)
+    a, b, c = t.stride()
+    if c != 1 or (H > 1 and b != D):
+        raise ValueError(f"{name} must be [T, H, D] with contiguous heads in each token row")
+    _on_device(t, name)
+    return T, H, D, (a if T > 1 else H * D)
 
 
 def _rope_ex(name, q, k, positions, cos_sin, q_out, k_out, pairing):
@@ -586,13 +602,13 @@ def swiglu_bwd(dout, gate, up, dgate=None, dup=None):
 
 def _rows2d(t, name):
     """(T, I, ld) of a 2-D view whose rows may be strided (last dim contiguous)."""
-    if not t.is_cuda:
+    if t.get_device() < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dim() != 2 or t.stride(1) != 1:
         raise ValueError(f"{name} must be 2-D with contiguous rows")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return t.shape[0], t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    _on_device(t, name)
+    T, I = t.shape
+    return T, I, (t.stride(0) if T > 1 else I)
 
 
 def glu_fwd(gate, up, act="silu", out=None):
@@ -854,20 +870,17 @@ def _cache8(codes, scale, Hk, D, name):
     """``gbln_cache8`` of codes [pages, page_size, Hk, D] and scales [pages, page_size, Hk], each
     with any page, slot and head strides; and its format."""
     fmt = _code_fmt(codes, f"{name}_cache")
-    if codes.dim() != 4 or codes.shape[1] < 1 or codes.shape[2:] != (Hk, D):
-        raise ValueError(f"{name}_cache must be [pages, page_size, {Hk}, {D}], not {tuple(codes.shape)}")
-    if scale.dtype != torch.float32 or scale.shape != codes.shape[:3]:
-        raise ValueError(f"{name}_scale must be float32 {tuple(codes.shape[:3])}, not {scale.dtype} {tuple(scale.shape)}")
-    if D > 1 and codes.stride(3) != 1:
+    shape = codes.shape
+    if len(shape) != 4 or shape[1] < 1 or shape[2:] != (Hk, D):
+        raise ValueError(f"{name}_cache must be [pages, page_size, {Hk}, {D}], not {tuple(shape)}")
+    if scale.dtype is not torch.float32 or scale.shape != shape[:3]:
+        raise ValueError(f"{name}_scale must be float32 {tuple(shape[:3])}, not {scale.dtype} {tuple(scale.shape)}")
+    stride = codes.stride()
+    if D > 1 and stride[3] != 1:
         raise ValueError(f"{name}_cache must hold the {D} values of a head next to one another")
-    for t, n in ((codes, f"{name}_cache"), (scale, f"{name}_scale")):
-        if not t.is_cuda:
-            raise ValueError(f"{n} must be a CUDA tensor")
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{n} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    a, b = codes.stride(), scale.stride()
-    return _Cache8(codes.data_ptr(), scale.data_ptr(), codes.shape[0], codes.shape[1],
-                   a[0], a[1], a[2], b[0], b[1], b[2]), fmt
+    _on_device(codes, f"{name}_cache")
+    _on_device(scale, f"{name}_scale")
+    return _Cache8(codes.data_ptr(), scale.data_ptr(), *shape[:2], *stride[:3], *scale.stride()), fmt
 
 
 def rope_fwd_cache8(q, k, v, positions, cos_sin, slots, k_cache, k_scale, v_cache, v_scale, *,

@@ -33,10 +33,9 @@ struct Slots {
   const int64_t* slots;
   int64_t total, page_size;  // total = pages * page_size
   bool small;                // slots fit 32 bits
-  // The page and the slot in it of token t's slot; -1 for "none" (negative), -2
+  // The page of slot s and the slot's place in it; -1 for "none" (negative), -2
   // for a slot outside the cache.
-  __device__ __forceinline__ int64_t page_of(int64_t t, int64_t& off) const {
-    const int64_t s = __ldg(slots + t);
+  __device__ __forceinline__ int64_t page_of(int64_t s, int64_t& off) const {
     if (s < 0) return -1;
     if (s >= total) return -2;
     if (small) {
@@ -73,17 +72,18 @@ struct WriteArgs {
 
 // ---------------------------------------------------------------------------
 // Vector path: a warp takes one token and up to kWriteHeads head rows per lane.
-// A lane owns two vectors of a head row and the VEC table entries that turn
-// them, whichever pairing: elements v*VEC.. of each half (rotate-half), or the
-// 2*VEC elements from 2*v*VEC (interleaved).  A head row takes nu = D / (2 VEC)
-// lanes out of a group of the next power of two, so 80 or 96 wide heads run here
-// with idle lanes.  The table entries are loaded once per token and lane, and all
-// of a lane's row loads are issued before the first is used.
+// A lane owns the vectors at v*VEC of both halves of a head row, whichever
+// pairing, so a warp's accesses are whole lines: with rotate-half pairing they
+// turn into each other by VEC table entries, with interleaved pairing each holds
+// VEC / 2 pairs of its own.  A head row takes nu = D / (2 VEC) lanes out of a group
+// of the next power of two, so 80 or 96 wide heads run here with idle lanes.  The
+// table entries are loaded once per token and lane, and all of a lane's row
+// loads are issued before anything that depends on the token's slot or position.
 // ---------------------------------------------------------------------------
-constexpr int kWriteHeads = 6;
+constexpr int kWriteHeads = 4;
 
 template <typename T, bool IL, int FMT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 3)
 cache8_write_vec(const WriteArgs<T> A, int nu, int lanes, int nchunk, int ch) {
   constexpr int VEC = VecOf<T>::N;
   const int half = A.D / 2, HR = A.Hq + A.Hk, HT = HR + A.Hk;
@@ -96,15 +96,14 @@ cache8_write_vec(const WriteArgs<T> A, int nu, int lanes, int nchunk, int ch) {
   if (t >= A.rows) return;  // uniform per warp
   const int c = (int)(item - t * nchunk);
   const int hb = g + G * c * ch;
-  const int ia = IL ? 2 * v * VEC : v * VEC, ib = IL ? ia + VEC : half + ia;
-  int64_t off = 0;
-  const int64_t page = A.S.page_of(t, off);
+  const int ia = v * VEC, ib = half + ia;
   const int p = __ldg(A.pos + t);
+  const int64_t slot = __ldg(A.S.slots + t);
   uint4 a[kWriteHeads], b[kWriteHeads];
 #pragma unroll
   for (int j = 0; j < kWriteHeads; ++j) {
     const int h = hb + G * j;
-    if (j < ch && on && h < HT && (h < A.Hq || page >= 0)) {
+    if (j < ch && on && h < HT) {
       const T* src = A.src(t, h);
       a[j] = ld_stream(src + ia);
       b[j] = ld_stream(src + ib);
@@ -113,23 +112,28 @@ cache8_write_vec(const WriteArgs<T> A, int nu, int lanes, int nchunk, int ch) {
     }
   }
   const bool ok = p >= 0 && (int64_t)p < A.max_pos;
-  if (c == 0 && lane == 0) {
-    if (!ok && (A.Hq > 0 || page >= 0)) atomicOr(A.err, kErrBadPosition);
-    if (page == -2) atomicOr(A.err, kErrBadSlot);
-  }
+  // (cos, sin) of the lane's pairs: entries v*VEC.. (rotate-half), or half as many
+  // for each of its two vectors (interleaved)
   float2 cs[VEC];
   if (ok && on) {
-    const float4* e = reinterpret_cast<const float4*>(A.table + (size_t)p * half + v * VEC);
+    const float2* e = A.table + (size_t)p * half;
 #pragma unroll
     for (int i = 0; i < VEC; i += 2) {
-      const float4 f = __ldg(e + i / 2);
+      const int at = !IL ? ia + i : i < VEC / 2 ? ia / 2 + i : ib / 2 + i - VEC / 2;
+      const float4 f = __ldg(reinterpret_cast<const float4*>(e + at));
       cs[i] = make_float2(f.x, f.y);
       cs[i + 1] = make_float2(f.z, f.w);
     }
   } else {
-    const float x = ok ? 0.f : __int_as_float(0x7fc00000);  // an idle lane adds nothing to a maximum
+    const float x = ok ? 0.f : __int_as_float(0x7fc00000);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) cs[i] = make_float2(x, x);
+  }
+  int64_t off = 0;
+  const int64_t page = A.S.page_of(slot, off);
+  if (c == 0 && lane == 0) {
+    if (!ok && (A.Hq > 0 || page >= 0)) atomicOr(A.err, kErrBadPosition);
+    if (page == -2) atomicOr(A.err, kErrBadSlot);
   }
 #pragma unroll
   for (int j = 0; j < kWriteHeads; ++j) {
@@ -198,7 +202,7 @@ __global__ void __launch_bounds__(256) cache8_write_elem(const WriteArgs<T> A) {
     const int64_t t = item / HT;
     const int h = (int)(item - t * HT);
     int64_t off = 0;
-    const int64_t page = A.S.page_of(t, off);
+    const int64_t page = A.S.page_of(__ldg(A.S.slots + t), off);
     const int p = __ldg(A.pos + t);
     const bool ok = p >= 0 && (int64_t)p < A.max_pos;
     if (h == 0 && lane == 0) {
@@ -252,8 +256,9 @@ __global__ void __launch_bounds__(256) cache8_write_elem(const WriteArgs<T> A) {
 }
 
 // ---------------------------------------------------------------------------
-// Read-back: a warp per token.  A unit is N consecutive codes of one head (16 on
-// the vector path: one 16-byte load, 32 or 64 bytes stored); the lanes walk the
+// Read-back: a warp per token.  A unit is N consecutive codes of one head: on the
+// vector path as many as fill a 16-byte store (8 codes at bf16, 4 at float32), so
+// that a warp's loads and its stores are both contiguous.  The lanes walk the
 // token's units of K, then of V.
 // ---------------------------------------------------------------------------
 template <typename T>
@@ -270,61 +275,47 @@ struct ReadArgs {
 
 template <typename T, int FMT, int N>
 __global__ void __launch_bounds__(256) cache8_read_kernel(const ReadArgs<T> A) {
-  constexpr int U = 4;  // units in flight per lane
+  constexpr int U = 8;  // units in flight per lane
   const int lane = threadIdx.x & 31;
   const int64_t t = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   if (t >= A.rows) return;  // uniform per warp
   int64_t off = 0;
-  const int64_t page = A.S.page_of(t, off);
+  const int64_t page = A.S.page_of(__ldg(A.S.slots + t), off);
   if (page == -2 && lane == 0) atomicOr(A.err, kErrBadSlot);
   const int per = A.D / N, half = A.Hk * per;
   const float fill = page == -2 ? __int_as_float(0x7fc00000) : 0.f;  // no slot: zeros
+  const uint8_t *kq = nullptr, *vq = nullptr;
+  const float *ks = nullptr, *vs = nullptr;
+  if (page >= 0) {
+    kq = A.K.q + A.K.cq.at(page, off, 0);
+    vq = A.V.q + A.V.cq.at(page, off, 0);
+    ks = A.K.sc + A.K.cs.at(page, off, 0);
+    vs = A.V.sc + A.V.cs.at(page, off, 0);
+  }
+  T *ko = A.ko + t * A.ldk, *vo = A.vo + t * A.ldv;
   for (int u0 = lane; u0 < 2 * half; u0 += 32 * U) {
-    uint4 w[U];
+    Codes<FMT, N> w[U];
     float sc[U];
-    T* dst[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const int u = u0 + 32 * k;
-      if (u >= 2 * half) continue;
       const bool isk = u < half;
       const int r = isk ? u : u - half;
-      const int h = r / per, d = (r - h * per) * N;
-      dst[k] = isk ? A.ko + t * A.ldk + (int64_t)h * A.D + d : A.vo + t * A.ldv + (int64_t)h * A.D + d;
-      w[k] = make_uint4(0, 0, 0, 0);
+      const int h = r / per;
+      w[k].zero();
       sc[k] = fill;
-      if (page >= 0) {
-        const Cache& C = isk ? A.K : A.V;
-        const uint8_t* src = C.q + C.cq.at(page, off, h) + d;
-        if constexpr (N == 16) w[k] = ld_stream(src);
-        else w[k].x = *src;
-        sc[k] = __ldg(C.sc + C.cs.at(page, off, h));
+      if (u < 2 * half && page >= 0) {
+        w[k].load((isk ? kq + (int64_t)h * A.K.cq.head : vq + (int64_t)h * A.V.cq.head) + (r - h * per) * N);
+        sc[k] = __ldg(isk ? ks + (int64_t)h * A.K.cs.head : vs + (int64_t)h * A.V.cs.head);
       }
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      if (u0 + 32 * k >= 2 * half) continue;
-      // An empty slot has codes 0 (value 0): 0 * fill is 0 or NaN.
-      const uint32_t* ww = reinterpret_cast<const uint32_t*>(&w[k]);
-      if constexpr (N == 16) {
-        float v[16];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) q8_decode4<FMT>(ww[i], v + 4 * i);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = __fmul_rn(v[e], sc[k]);
-        constexpr int VEC = VecOf<T>::N;
-#pragma unroll
-        for (int i = 0; i < 16; i += VEC) {
-          float o[VEC];
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) o[e] = v[i + e];
-          st_vec(dst[k] + i, pack<T, VEC>(o));
-        }
-      } else {
-        float v[4];
-        q8_decode4<FMT>(ww[0], v);
-        *dst[k] = from_f32<T>(__fmul_rn(v[0], sc[k]));
-      }
+      const int u = u0 + 32 * k;
+      if (u >= 2 * half) break;
+      float v[N];
+      w[k].get(v, sc[k]);  // no slot: 0 * fill is 0 or NaN
+      store_n<T, N>(u < half ? ko + (int64_t)u * N : vo + (int64_t)(u - half) * N, v);
     }
   }
 }
@@ -372,6 +363,11 @@ Cache cache_of(const gbln_cache8* c) {
 bool strides_multiple(const gbln_cache8* c, int n) {
   return c->page_stride % n == 0 && c->slot_stride % n == 0 && c->head_stride % n == 0;
 }
+// Whether every head starts at a multiple of the codes of one access.
+bool codes_aligned(const gbln_cache8* k, const gbln_cache8* v, gbln_dtype io) {
+  const int n = io == GBLN_F32 ? 4 : 8;
+  return aligned_to(k->codes, n) && aligned_to(v->codes, n) && strides_multiple(k, n) && strides_multiple(v, n);
+}
 Slots slots_of(const gbln_cache8* c, const int64_t* slots) {
   const int64_t total = c->pages * c->page_size;
   return {slots, total, c->page_size, total < (1LL << 31) && c->page_size < (1LL << 31)};
@@ -412,15 +408,16 @@ gbln_status write_typed(const WriteArgs<T>& A, bool il, int fmt, bool cache_alig
 
 template <typename T>
 gbln_status read_typed(const ReadArgs<T>& A, int fmt, bool cache_aligned, cudaStream_t s) {
-  const bool vec = A.D % 16 == 0 && cache_aligned && aligned16(A.ko) && aligned16(A.vo) &&
+  constexpr int VEC = VecOf<T>::N;
+  const bool vec = A.D % VEC == 0 && cache_aligned && aligned16(A.ko) && aligned16(A.vo) &&
                    (A.ldk * (int64_t)sizeof(T)) % 16 == 0 && (A.ldv * (int64_t)sizeof(T)) % 16 == 0;
   const int64_t blocks = (A.rows + 7) / 8;  // at most 2^30 for kMaxTokens
 #define GBLN_READ8(FMT, N) cache8_read_kernel<T, FMT, N><<<(unsigned)blocks, 256, 0, s>>>(A)
   if (fmt == GBLN_Q8_INT8) {
-    if (vec) GBLN_READ8(GBLN_Q8_INT8, 16);
+    if (vec) GBLN_READ8(GBLN_Q8_INT8, VEC);
     else GBLN_READ8(GBLN_Q8_INT8, 1);
   } else {
-    if (vec) GBLN_READ8(GBLN_Q8_E4M3, 16);
+    if (vec) GBLN_READ8(GBLN_Q8_E4M3, VEC);
     else GBLN_READ8(GBLN_Q8_E4M3, 1);
   }
 #undef GBLN_READ8
@@ -458,9 +455,7 @@ extern "C" gbln_status gbln_rope_fwd_cache8(const void* q, const void* k, const 
   unsigned int* err = device_error_word();
   if (!err) return GBLN_ERR_CUDA;
   const bool il = pairing == GBLN_ROPE_INTERLEAVED;
-  const int n = io == GBLN_F32 ? 4 : 8;  // codes per store
-  const bool ca = aligned_to(k_cache->codes, n) && aligned_to(v_cache->codes, n) && strides_multiple(k_cache, n) &&
-                  strides_multiple(v_cache, n);
+  const bool ca = codes_aligned(k_cache, v_cache, io);
   cudaStream_t s = (cudaStream_t)stream;
 #define GBLN_WRITE_ARGS(TY)                                                                               \
   const WriteArgs<TY> A{(const TY*)q, (const TY*)k, (const TY*)v, (TY*)q_out, positions, (const float2*)cos_sin, \
@@ -492,8 +487,7 @@ extern "C" gbln_status gbln_cache8_read(const int64_t* slots, const gbln_cache8*
     return GBLN_ERR_INVALID_ARG;
   unsigned int* err = device_error_word();
   if (!err) return GBLN_ERR_CUDA;
-  const bool ca = aligned16(k_cache->codes) && aligned16(v_cache->codes) && strides_multiple(k_cache, 16) &&
-                  strides_multiple(v_cache, 16);
+  const bool ca = codes_aligned(k_cache, v_cache, io);
   cudaStream_t s = (cudaStream_t)stream;
 #define GBLN_READ_ARGS(TY)                                                                             \
   const ReadArgs<TY> A{slots_of(k_cache, slots), cache_of(k_cache), cache_of(v_cache), (TY*)k_out, (TY*)v_out, \

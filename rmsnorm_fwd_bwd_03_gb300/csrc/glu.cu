@@ -18,6 +18,8 @@
 // projection, and save gate and up as 8-bit checkpoints (one float32 scale per
 // 128 values of a row) that a backward pass reads.
 
+#include <cooperative_groups.h>
+
 #include "q8.cuh"
 
 namespace gbln {
@@ -400,24 +402,76 @@ glu_fwd_mx(const T* gate, const T* up, MxOut mx, int64_t T_, int64_t ncol, int64
   }
 }
 
+// f(gate) * up of N values for the kernels that also quantise.  With bf16 inputs
+// the multiplications and additions of act_f go two at a time (the same
+// operations, so the same bits); the exponentials and reciprocals stay single.
+template <int ACT>
+__device__ __forceinline__ float2 act_f2(float2 x) {
+  if constexpr (ACT == GBLN_ACT_RELU) {
+    return make_float2(x.x > 0.f ? x.x : 0.f, x.y > 0.f ? x.y : 0.f);
+  } else if constexpr (ACT == GBLN_ACT_GELU_ERF) {
+    const float2 z = mul2(make_float2(fabsf(x.x), fabsf(x.y)), both(kInvSqrt2));
+    const float2 pz = fma2(both(kAsP), z, both(1.0f));
+    const float2 t = make_float2(rcp_ftz(pz.x), rcp_ftz(pz.y));
+    const float2 a = mul2(mul2(make_float2(-z.x, -z.y), z), both(kLog2e));
+    const float2 ex = make_float2(ex2_ftz(a.x), ex2_ftz(a.y));
+    const float2 poly = mul2(t, fma2(t, fma2(t, fma2(t, fma2(t, both(kAsA5), both(kAsA4)), both(kAsA3)), both(kAsA2)), both(kAsA1)));
+    const float2 h = mul2(mul2(both(0.5f), poly), ex);
+    const float2 up = add2(both(1.0f), make_float2(-h.x, -h.y));
+    return mul2(x, make_float2(x.x >= 0.f ? up.x : h.x, x.y >= 0.f ? up.y : h.y));
+  } else {
+    float2 a;  // argument of the sigmoid
+    if constexpr (ACT == GBLN_ACT_SILU) {
+      a = x;
+    } else {
+      const float2 cube = mul2(mul2(mul2(both(kGeluC), x), x), x);
+      a = mul2(both(kGeluK), add2(x, cube));
+    }
+    const float2 n = mul2(make_float2(-a.x, -a.y), both(kLog2e));
+    const float2 d = add2(both(1.0f), make_float2(ex2_ftz(n.x), ex2_ftz(n.y)));
+    return mul2(x, make_float2(rcp_ftz(d.x), rcp_ftz(d.y)));
+  }
+}
+template <typename T, int ACT, int N>
+__device__ __forceinline__ void glu_values(const float (&g)[N], const float (&u)[N], float (&o)[N]) {
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      const float2 r = mul2(act_f2<ACT>(make_float2(g[e], g[e + 1])), make_float2(u[e], u[e + 1]));
+      o[e] = r.x;
+      o[e + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[e] = act_f<T, ACT>(g[e]) * u[e];
+  }
+}
+
 // ---------------------------------------------------------------------------
-// Forward with row-scaled E4M3 output: one block per row.  The scale needs the
-// whole row's maximum before the first code, so the outputs wait for it in
-// float32 registers (VPT vectors per thread): gate and up are read once.
+// Forward with row-scaled E4M3 output.  The scale needs the whole row's maximum
+// before the first code, so the outputs wait for it in float32 registers (VPT
+// vectors per thread): gate and up are read once.  TPR threads per row and
+// block: several rows per block when TPR is a warp; one row per block beyond;
+// one row per cluster of CL blocks for rows beyond 1024 threads' registers, whose
+// maxima meet through distributed shared memory (a pair of 512-thread blocks is
+// no faster than one block of 1024: 536 against 493 us at 16383 x 28672).
 // ---------------------------------------------------------------------------
-template <typename T, int ACT, int TPR, int VPT>
-__global__ void __launch_bounds__(TPR)
-glu_fwd_row8(const T* gate, const T* up, uint8_t* q, float* sc, int64_t rows, int I, int64_t ldg,
-             int64_t ldu) {
+template <typename T, int ACT, int TPR, int VPT, int RPB, int CL>
+__device__ __forceinline__ void glu_row8(const T* gate, const T* up, uint8_t* q, float* sc, int64_t rows,
+                                         int I, int64_t ldg, int64_t ldu) {
+  static_assert((RPB == 1 || TPR == 32) && (CL == 1 || RPB == 1), "row split");
   constexpr int VEC = VecOf<T>::N;
   constexpr int FMT = GBLN_Q8_E4M3;
+  constexpr int STEP = TPR * CL;  // vectors between two of a thread's
   __shared__ uint32_t redm[TPR / 32];
-  const int64_t row = blockIdx.x;
-  const int nvec = I / VEC, l = threadIdx.x;
+  __shared__ uint32_t blockm;
+  const int64_t row = CL > 1 ? blockIdx.x / CL : (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+  if (row >= rows) return;  // uniform per warp; never with one row per block or cluster
+  const int nvec = I / VEC, l = (CL > 1 ? (int)(blockIdx.x % CL) * TPR : 0) + threadIdx.x % TPR;
   uint4 ga[VPT], ua[VPT];
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    const int iv = l + v * TPR;
+    const int iv = l + v * STEP;
     if (iv < nvec) {
       ga[v] = ld_stream(gate + row * ldg + (int64_t)iv * VEC);
       ua[v] = ld_stream(up + row * ldu + (int64_t)iv * VEC);
@@ -427,62 +481,132 @@ glu_fwd_row8(const T* gate, const T* up, uint8_t* q, float* sc, int64_t rows, in
   uint32_t m = 0;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    if (l + v * TPR < nvec) {
+    if (l + v * STEP < nvec) {
       float g[VEC], u[VEC];
       unpack<VEC>(ga[v], g);
       unpack<VEC>(ua[v], u);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) o[v][e] = act_f<T, ACT>(g[e]) * u[e];
+      glu_values<T, ACT, VEC>(g, u, o[v]);
       m = max(m, abs_max_bits<VEC>(o[v]));
     }
   }
   m = group_max<32>(m);
   if constexpr (TPR > 32) {
-    if ((l & 31) == 0) redm[l >> 5] = m;
+    if ((threadIdx.x & 31) == 0) redm[threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < TPR / 32; ++i) m = max(m, redm[i]);
+  }
+  if constexpr (CL > 1) {
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    if (threadIdx.x == 0) blockm = m;
+    cluster.sync();
+#pragma unroll
+    for (int i = 0; i < CL; ++i) m = max(m, *cluster.map_shared_rank(&blockm, i));
+    cluster.barrier_arrive();  // this block has read its peers; waited for before it ends
   }
   const float a = q8_amax(m), inv = q8_inv<FMT>(a);
   if (l == 0) sc[row] = q8_scale<FMT>(a, m);
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    const int iv = l + v * TPR;
+    const int iv = l + v * STEP;
     if (iv < nvec) q8_store<FMT, VEC>(o[v], inv, q + row * I + (int64_t)iv * VEC);
   }
+  if constexpr (CL > 1) cooperative_groups::this_cluster().barrier_wait();
 }
 
-// The same for any alignment and width: the row is read a second time to write
-// the codes, from L2 for all but the widest rows.
-template <typename T, int ACT>
-__global__ void __launch_bounds__(512)
+template <typename T, int ACT, int TPR, int VPT, int RPB>
+__global__ void __launch_bounds__(TPR * RPB)
+glu_fwd_row8(const T* gate, const T* up, uint8_t* q, float* sc, int64_t rows, int I, int64_t ldg,
+             int64_t ldu) {
+  glu_row8<T, ACT, TPR, VPT, RPB, 1>(gate, up, q, sc, rows, I, ldg, ldu);
+}
+template <typename T, int ACT, int CL>
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(512)
+glu_fwd_row8_cluster(const T* gate, const T* up, uint8_t* q, float* sc, int64_t rows, int I, int64_t ldg,
+                     int64_t ldu) {
+  glu_row8<T, ACT, 512, 4, 1, CL>(gate, up, q, sc, rows, I, ldg, ldu);
+}
+
+// The same for any alignment and width.  A warp takes runs of 128 values, lane l
+// the values l, l + 32, l + 64, l + 96 of each; up to kRow8Runs runs per warp wait
+// in registers (blocks of up to 1024 threads: 16384 values), wider rows are read
+// a second time to write the codes.
+constexpr int kRow8Runs = 4;
+
+template <typename T, int ACT, bool FITS>
+__global__ void __launch_bounds__(1024)
 glu_fwd_row8_elem(const T* gate, const T* up, uint8_t* q, float* sc, int64_t rows, int64_t I,
                   int64_t ldg, int64_t ldu) {
   constexpr int FMT = GBLN_Q8_E4M3;
-  __shared__ uint32_t redm[16];
+  __shared__ uint32_t redm[32];
   const int64_t row = blockIdx.x;
+  const int nw = blockDim.x / 32;
+  const int64_t j0 = (threadIdx.x >> 5) * 128 + (threadIdx.x & 31);
   const T* gr = gate + row * ldg;
   const T* ur = up + row * ldu;
+  uint8_t* qr = q + row * I;
+  float o[FITS ? kRow8Runs : 1][4];
   uint32_t m = 0;
-#pragma unroll 4
-  for (int64_t j = threadIdx.x; j < I; j += blockDim.x)
-    m = max(m, abs_bits(act_f<T, ACT>(to_f32(gr[j])) * to_f32(ur[j])));
+  if constexpr (FITS) {
+    T g[kRow8Runs][4], u[kRow8Runs][4];
+#pragma unroll
+    for (int k = 0; k < kRow8Runs; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = (int)j0 + k * nw * 128 + 32 * e;
+        g[k][e] = u[k][e] = from_f32<T>(0.f);
+        if (j < I) {
+          g[k][e] = gr[j];
+          u[k][e] = ur[j];
+        }
+      }
+#pragma unroll
+    for (int k = 0; k < kRow8Runs; ++k)
+      if (((int)(threadIdx.x >> 5) + k * nw) * 128 < I) {
+        float gf[4], uf[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          gf[e] = to_f32(g[k][e]);
+          uf[e] = to_f32(u[k][e]);
+        }
+        glu_values<T, ACT, 4>(gf, uf, o[k]);
+        m = max(m, abs_max_bits<4>(o[k]));
+      }
+  } else {
+    for (int64_t j = threadIdx.x; j < I; j += blockDim.x)
+      m = max(m, abs_bits(act_f<T, ACT>(to_f32(gr[j])) * to_f32(ur[j])));
+  }
   m = group_max<32>(m);
   if ((threadIdx.x & 31) == 0) redm[threadIdx.x >> 5] = m;
   __syncthreads();
-  for (int i = 0; i < (int)blockDim.x / 32; ++i) m = max(m, redm[i]);
+  for (int i = 0; i < nw; ++i) m = max(m, redm[i]);
   const float a = q8_amax(m), inv = q8_inv<FMT>(a);
   if (threadIdx.x == 0) sc[row] = q8_scale<FMT>(a, m);
-#pragma unroll 4
-  for (int64_t j = threadIdx.x; j < I; j += blockDim.x)
-    q[row * I + j] = (uint8_t)q8_code1<FMT>(act_f<T, ACT>(to_f32(gr[j])) * to_f32(ur[j]), inv);
+  if constexpr (FITS) {
+#pragma unroll
+    for (int k = 0; k < kRow8Runs; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (const int j = (int)j0 + k * nw * 128 + 32 * e; j < I) qr[j] = (uint8_t)q8_code1<FMT>(o[k][e], inv);
+  } else {
+    for (int64_t j = threadIdx.x; j < I; j += blockDim.x)
+      qr[j] = (uint8_t)q8_code1<FMT>(act_f<T, ACT>(to_f32(gr[j])) * to_f32(ur[j]), inv);
+  }
 }
 
 // ---------------------------------------------------------------------------
 // Forward that also saves gate and up as 8-bit checkpoints.  Units as in
-// glu_fwd_rows; a checkpoint group is 128 / VEC consecutive column vectors, held
-// by consecutive lanes (blockDim is a multiple of 32, so column blocks start at
-// a group), and every lane takes part in its maximum.
+// glu_fwd_rows; a checkpoint group is LPG = 128 / VEC consecutive column vectors,
+// held by consecutive lanes (blockDim is a multiple of 32, so column blocks start
+// at a group), and every lane takes part in the reductions.
+//
+// Four rows of gate and up give a lane eight groups to reduce.  Each halving step
+// of the reduction also halves the number of groups a lane looks after, so that
+// eight reductions cost eight shuffles instead of thirty-two, and leave each
+// group's maximum with two lanes (four at float32): one divides for 1 / scale,
+// the other for the scale.  With a reduction and two divisions per lane and
+// group instead, the kernel ran at 81% of the copy rate, bound by instructions.
 // ---------------------------------------------------------------------------
 struct GluCkpt {
   uint8_t* gq;
@@ -497,107 +621,176 @@ struct GluCkptIn {
   const float* us;
 };
 
-template <int FMT, int VEC>
-__device__ __forceinline__ void ckpt_store(const float (&v)[VEC], bool on, int64_t row, int64_t c, int64_t I,
-                                           int64_t ng, uint8_t* q, float* sc) {
-  constexpr int LPG = kCkptGroup / VEC;
-  const uint32_t m = group_max<LPG>(abs_max_bits<VEC>(v));
-  if (on) {
-    const float a = q8_amax(m);
-    q8_store<FMT, VEC>(v, q8_inv<FMT>(a), q + row * I + c * VEC);
-    if (c % LPG == 0) sc[row * ng + c / LPG] = q8_scale<FMT>(a, m);
-  }
-}
+constexpr int kCkptRows = 4;
 
-template <typename T, int ACT, int FMT, int UNROLL>
+template <typename T, int ACT, int FMT>
 __global__ void __launch_bounds__(kGluBlock)
 glu_fwd_ckpt(const T* gate, const T* up, T* out, const GluCkpt C, int64_t T_, int64_t ncol, int64_t ldg,
              int64_t ldu, int64_t ldo) {
   constexpr int VEC = VecOf<T>::N;
-  constexpr int LPG = kCkptGroup / VEC;
+  constexpr int LPG = kCkptGroup / VEC;  // 16 or 32 lanes per group
+  constexpr int U = kCkptRows;
+  constexpr int SH = LPG == 16 ? 1 : 2;  // lane bits below those that name a group
   const int64_t I = ncol * VEC, ng = (ncol + LPG - 1) / LPG;
-  const int cb = blockDim.x;
+  const int cb = blockDim.x, lane = threadIdx.x & 31;
   const int64_t ncb = (ncol + cb - 1) / cb;
-  const int64_t units = (T_ + UNROLL - 1) / UNROLL * ncb;
+  const int64_t units = (T_ + U - 1) / U * ncb;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int64_t rg = u / ncb;
     const int64_t c = (u - rg * ncb) * cb + threadIdx.x;
     const bool on = c < ncol;
-    const int64_t r0 = rg * UNROLL;
-    Packed<T, VEC> g[UNROLL], v[UNROLL];
+    const int64_t r0 = rg * U;
+    const int nr = (int)(T_ - r0 < U ? T_ - r0 : (int64_t)U);
+    uint4 g[U], v[U];
 #pragma unroll
-    for (int k = 0; k < UNROLL; ++k) {
-      if (on && r0 + k < T_) {
-        g[k].load(gate + (r0 + k) * ldg + c * VEC);
-        v[k].load(up + (r0 + k) * ldu + c * VEC);
+    for (int k = 0; k < U; ++k) {
+      g[k] = v[k] = make_uint4(0, 0, 0, 0);
+      if (on && k < nr) {
+        g[k] = ld_stream(gate + (r0 + k) * ldg + c * VEC);
+        v[k] = ld_stream(up + (r0 + k) * ldu + c * VEC);
+      }
+    }
+    uint32_t m[2 * U];  // gate and up of row 0, of row 1, ...
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      m[2 * k] = AbsMax<T>::part(g[k]);
+      m[2 * k + 1] = AbsMax<T>::part(v[k]);
+    }
+#pragma unroll
+    for (int n = U, o = LPG / 2; n >= 1; n /= 2, o /= 2) {  // n groups kept per lane
+      const bool hi = (lane & o) != 0;
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? m[i] : m[i + n], o);
+        m[i] = AbsMax<T>::join(hi ? m[i + n] : m[i], got);
       }
     }
 #pragma unroll
-    for (int k = 0; k < UNROLL; ++k) {
-      if (r0 + k >= T_) break;  // uniform across the block
-      float gf[VEC], uf[VEC], o[VEC];
+    for (int o = 1 << (SH - 1); o > 0; o >>= 1) m[0] = AbsMax<T>::join(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+    const int mine = (lane & (LPG - 1)) >> SH;  // the group left with this lane: 2 * row + (up)
+    const uint32_t bits = AbsMax<T>::bits(m[0]);
+    const float a = q8_amax(bits);
+    const bool scales = (lane & 1) != 0;
+    const float d = __fdiv_rn(scales ? a : Q8Max<FMT>::v, scales ? Q8Max<FMT>::v : a);
+    if (scales && (SH == 1 || (lane & 2) == 0) && (mine >> 1) < nr && (c & ~(int64_t)(LPG - 1)) < ncol)
+      (mine & 1 ? C.us : C.gs)[(r0 + (mine >> 1)) * ng + c / LPG] = bits < kInfBits ? d : __int_as_float(0x7fc00000);
+    const int base = lane & ~(LPG - 1);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) gf[e] = uf[e] = 0.f;
-      if (on) {
-        g[k].get(gf);
-        v[k].get(uf);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) o[e] = act_f<T, ACT>(gf[e]) * uf[e];
-        store_n<T, VEC>(out + (r0 + k) * ldo + c * VEC, o);
+    for (int k = 0; k < U; ++k) {
+      const float gi = __shfl_sync(0xffffffffu, d, base | ((2 * k) << SH));
+      const float ui = __shfl_sync(0xffffffffu, d, base | ((2 * k + 1) << SH));
+      if (on && k < nr) {
+        float gf[VEC], uf[VEC], o[VEC];
+        unpack<VEC>(g[k], gf);
+        unpack<VEC>(v[k], uf);
+        q8_store<FMT, VEC>(gf, gi, C.gq + (r0 + k) * I + c * VEC);
+        q8_store<FMT, VEC>(uf, ui, C.uq + (r0 + k) * I + c * VEC);
+        glu_values<T, ACT, VEC>(gf, uf, o);
+        st_vec(out + (r0 + k) * ldo + c * VEC, pack<T, VEC>(o));
       }
-      ckpt_store<FMT, VEC>(gf, on, r0 + k, c, I, ng, C.gq, C.gs);
-      ckpt_store<FMT, VEC>(uf, on, r0 + k, c, I, ng, C.uq, C.us);
     }
   }
 }
 
-// Any alignment and width: one warp per checkpoint group, lane l the values l,
-// l + 32, l + 64, l + 96 of it.
+// Any alignment and width: one warp per checkpoint group and pass, lane l the
+// values l, l + 32, l + 64, l + 96 of it.  Two groups are in flight per warp;
+// offsets within a group are immediates, and only a row's last group is
+// predicated.
+template <bool FULL, typename T>
+__device__ __forceinline__ void load_run(const T* p, int rem, T (&v)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = FULL || 32 * e < rem ? p[32 * e] : T(0.f);
+}
+template <bool FULL>
+__device__ __forceinline__ uint32_t load_run_codes(const uint8_t* p, int rem) {
+  uint32_t b[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) b[e] = FULL || 32 * e < rem ? (uint32_t)p[32 * e] : 0u;
+  return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+}
+template <bool FULL, typename T>
+__device__ __forceinline__ void store_run(T* p, int rem, const float (&v)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (FULL || 32 * e < rem) p[32 * e] = from_f32<T>(v[e]);
+}
+template <bool FULL, int FMT>
+__device__ __forceinline__ void store_run_codes(uint8_t* p, int rem, const float (&v)[4], float inv) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (FULL || 32 * e < rem) p[32 * e] = (uint8_t)q8_code1<FMT>(v[e], inv);
+}
+
+constexpr int kElemFlight = 2;
+
 template <typename T, int ACT, int FMT>
 __global__ void __launch_bounds__(kGluBlock)
 glu_fwd_ckpt_elem(const T* gate, const T* up, T* out, const GluCkpt C, int64_t T_, int64_t I, int64_t ldg,
                   int64_t ldu, int64_t ldo) {
+  constexpr int F = kElemFlight;
   const int lane = threadIdx.x & 31;
-  const int64_t ng = (I + kCkptGroup - 1) / kCkptGroup;
-  const int64_t step = (int64_t)gridDim.x * (kGluBlock / 32);
-  for (int64_t u = (int64_t)blockIdx.x * (kGluBlock / 32) + (threadIdx.x >> 5); u < T_ * ng; u += step) {
-    const int64_t row = u / ng;
-    const int64_t j0 = (u - row * ng) * kCkptGroup + lane;
-    float g[4], v[4];
+  const int64_t ng = (I + kCkptGroup - 1) / kCkptGroup, n = T_ * ng;
+  const int64_t step = (int64_t)gridDim.x * (kGluBlock / 32) * F;
+  for (int64_t u = ((int64_t)blockIdx.x * (kGluBlock / 32) + (threadIdx.x >> 5)) * F; u < n; u += step) {
+    T g[F][4], v[F][4];
+    int64_t row[F], j0[F];
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int64_t j = j0 + 32 * m;
-      g[m] = j < I ? to_f32(gate[row * ldg + j]) : 0.f;
-      v[m] = j < I ? to_f32(up[row * ldu + j]) : 0.f;
-    }
-    const uint32_t gm = group_max<32>(abs_max_bits<4>(g)), um = group_max<32>(abs_max_bits<4>(v));
-    const float ga = q8_amax(gm), ua = q8_amax(um);
-    const float gi = q8_inv<FMT>(ga), ui = q8_inv<FMT>(ua);
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int64_t j = j0 + 32 * m;
-      if (j < I) {
-        out[row * ldo + j] = from_f32<T>(act_f<T, ACT>(g[m]) * v[m]);
-        C.gq[row * I + j] = (uint8_t)q8_code1<FMT>(g[m], gi);
-        C.uq[row * I + j] = (uint8_t)q8_code1<FMT>(v[m], ui);
+    for (int f = 0; f < F; ++f) {
+      row[f] = (u + f) / ng;
+      j0[f] = (u + f - row[f] * ng) * kCkptGroup + lane;
+      if (u + f >= n) continue;
+      const T *gp = gate + row[f] * ldg + j0[f], *up_ = up + row[f] * ldu + j0[f];
+      const int rem = (int)(I - j0[f] < kCkptGroup ? I - j0[f] : (int64_t)kCkptGroup);
+      if (j0[f] - lane + kCkptGroup <= I) {
+        load_run<true>(gp, rem, g[f]);
+        load_run<true>(up_, rem, v[f]);
+      } else {
+        load_run<false>(gp, rem, g[f]);
+        load_run<false>(up_, rem, v[f]);
       }
     }
-    if (lane == 0) {
-      C.gs[u] = q8_scale<FMT>(ga, gm);
-      C.us[u] = q8_scale<FMT>(ua, um);
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      if (u + f >= n) break;  // uniform per warp
+      float gf[4], uf[4], o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        gf[e] = to_f32(g[f][e]);
+        uf[e] = to_f32(v[f][e]);
+      }
+      glu_values<T, ACT, 4>(gf, uf, o);
+      const uint32_t gm = group_max<32>(abs_max_bits<4>(gf)), um = group_max<32>(abs_max_bits<4>(uf));
+      // even lanes divide for 1 / scale, odd ones for the scale; lanes 2 and 3 of up
+      const uint32_t mine = lane & 2 ? um : gm;
+      const float a = q8_amax(mine);
+      const float d = __fdiv_rn(lane & 1 ? a : Q8Max<FMT>::v, lane & 1 ? Q8Max<FMT>::v : a);
+      const float gi = __shfl_sync(0xffffffffu, d, 0), ui = __shfl_sync(0xffffffffu, d, 2);
+      if (lane == 1 || lane == 3) (lane == 1 ? C.gs : C.us)[u + f] = mine < kInfBits ? d : __int_as_float(0x7fc00000);
+      const int rem = (int)(I - j0[f] < kCkptGroup ? I - j0[f] : (int64_t)kCkptGroup);
+      T* op = out + row[f] * ldo + j0[f];
+      uint8_t *gq = C.gq + row[f] * I + j0[f], *uq = C.uq + row[f] * I + j0[f];
+      if (j0[f] - lane + kCkptGroup <= I) {
+        store_run<true>(op, rem, o);
+        store_run_codes<true, FMT>(gq, rem, gf, gi);
+        store_run_codes<true, FMT>(uq, rem, uf, ui);
+      } else {
+        store_run<false>(op, rem, o);
+        store_run_codes<false, FMT>(gq, rem, gf, gi);
+        store_run_codes<false, FMT>(uq, rem, uf, ui);
+      }
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Backward from the checkpoints, units as in glu_bwd_rows (VEC = 1: any
-// alignment).  A lane's VEC columns lie in one group: VEC divides 128 and c * VEC
-// is a multiple of VEC.
+// Backward from the checkpoints, units as in glu_bwd_rows.  A lane's VEC columns
+// lie in one group: VEC divides 128.
 // ---------------------------------------------------------------------------
-template <typename T, int VEC, int ACT, int FMT, int UNROLL>
+template <typename T, int ACT, int FMT, int UNROLL>
 __global__ void __launch_bounds__(kGluBlock)
 glu_bwd_ckpt(const T* dout, const GluCkptIn C, T* dgate, T* dup, int64_t T_, int64_t ncol, int64_t ldd,
              int64_t lddg, int64_t lddu) {
+  constexpr int VEC = VecOf<T>::N;
   constexpr int LPG = kCkptGroup / VEC;
   const int64_t I = ncol * VEC, ng = (ncol + LPG - 1) / LPG;
   const int cb = blockDim.x;
@@ -637,6 +830,67 @@ glu_bwd_ckpt(const T* dout, const GluCkptIn C, T* dgate, T* dup, int64_t T_, int
         }
         store_n<T, VEC>(dgate + (r0 + k) * lddg + c * VEC, dg);
         store_n<T, VEC>(dup + (r0 + k) * lddu + c * VEC, du);
+      }
+    }
+  }
+}
+
+// Any alignment and width, as glu_fwd_ckpt_elem.
+template <typename T, int ACT, int FMT>
+__global__ void __launch_bounds__(kGluBlock)
+glu_bwd_ckpt_elem(const T* dout, const GluCkptIn C, T* dgate, T* dup, int64_t T_, int64_t I, int64_t ldd,
+                  int64_t lddg, int64_t lddu) {
+  constexpr int F = kElemFlight;
+  const int lane = threadIdx.x & 31;
+  const int64_t ng = (I + kCkptGroup - 1) / kCkptGroup, n = T_ * ng;
+  const int64_t step = (int64_t)gridDim.x * (kGluBlock / 32) * F;
+  for (int64_t u = ((int64_t)blockIdx.x * (kGluBlock / 32) + (threadIdx.x >> 5)) * F; u < n; u += step) {
+    T d[F][4];
+    uint32_t g[F], v[F];
+    float gs[F], us[F];
+    int64_t row[F], j0[F];
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      row[f] = (u + f) / ng;
+      j0[f] = (u + f - row[f] * ng) * kCkptGroup + lane;
+      if (u + f >= n) continue;
+      const T* dp = dout + row[f] * ldd + j0[f];
+      const uint8_t *gp = C.gq + row[f] * I + j0[f], *vp = C.uq + row[f] * I + j0[f];
+      const int rem = (int)(I - j0[f] < kCkptGroup ? I - j0[f] : (int64_t)kCkptGroup);
+      gs[f] = __ldg(C.gs + u + f);
+      us[f] = __ldg(C.us + u + f);
+      if (j0[f] - lane + kCkptGroup <= I) {
+        load_run<true>(dp, rem, d[f]);
+        g[f] = load_run_codes<true>(gp, rem);
+        v[f] = load_run_codes<true>(vp, rem);
+      } else {
+        load_run<false>(dp, rem, d[f]);
+        g[f] = load_run_codes<false>(gp, rem);
+        v[f] = load_run_codes<false>(vp, rem);
+      }
+    }
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      if (u + f >= n) break;
+      float gf[4], uf[4], dg[4], du[4];
+      q8_decode4<FMT>(g[f], gf);
+      q8_decode4<FMT>(v[f], uf);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float df = to_f32(d[f][e]);
+        float fx, fp;
+        act_fd<T, ACT>(__fmul_rn(gf[e], gs[f]), fx, fp);
+        du[e] = df * fx;
+        dg[e] = df * __fmul_rn(uf[e], us[f]) * fp;
+      }
+      const int rem = (int)(I - j0[f] < kCkptGroup ? I - j0[f] : (int64_t)kCkptGroup);
+      T *gp = dgate + row[f] * lddg + j0[f], *up_ = dup + row[f] * lddu + j0[f];
+      if (j0[f] - lane + kCkptGroup <= I) {
+        store_run<true>(gp, rem, dg);
+        store_run<true>(up_, rem, du);
+      } else {
+        store_run<false>(gp, rem, dg);
+        store_run<false>(up_, rem, du);
       }
     }
   }
@@ -774,31 +1028,43 @@ void act_bwd_launch(const void* dy, const void* x, void* dx, int64_t n, cudaStre
   }
 }
 
-// Threads per row of glu_fwd_row8: four vectors each, up to 1024 threads.
-constexpr int64_t kRow8MaxVec = 4096;
-
+// Row-scaled output: a warp per row up to 128 vectors, then a block of 64 to 1024
+// threads with four vectors each, then a cluster of 512-thread blocks.
 template <typename T, int ACT>
 void glu_fwd_row8_launch(const void* g, const void* u, uint8_t* q, float* sc, int64_t rows, int64_t I,
                          int64_t ldg, int64_t ldu, cudaStream_t s) {
   constexpr int VEC = VecOf<T>::N;
+  constexpr int64_t kMaxGrid = 0x7fffffff;
   const int64_t nvec = I / VEC;
-  const bool vec = I % VEC == 0 && nvec <= kRow8MaxVec && aligned16(g) && aligned16(u) && ldg % VEC == 0 &&
-                   ldu % VEC == 0 && aligned_to(q, VEC);
-  const unsigned grid = (unsigned)rows;
+  const int cl = nvec <= 4096 ? 1 : nvec <= 8192 ? 4 : 8;
+  const bool vec = I % VEC == 0 && nvec <= 8 * 2048 && rows * cl <= kMaxGrid && aligned16(g) && aligned16(u) &&
+                   ldg % VEC == 0 && ldu % VEC == 0 && aligned_to(q, VEC);
+  const T *gt = (const T*)g, *ut = (const T*)u;
   if (!vec) {
-    const int block = I <= 1024 ? 128 : 512;
-    glu_fwd_row8_elem<T, ACT><<<grid, block, 0, s>>>((const T*)g, (const T*)u, q, sc, rows, I, ldg, ldu);
+    int nw = 1;
+    while (nw < 32 && (int64_t)nw * 128 * kRow8Runs < I) nw *= 2;
+    if ((int64_t)nw * 128 * kRow8Runs >= I)
+      glu_fwd_row8_elem<T, ACT, true><<<(unsigned)rows, nw * 32, 0, s>>>(gt, ut, q, sc, rows, I, ldg, ldu);
+    else
+      glu_fwd_row8_elem<T, ACT, false><<<(unsigned)rows, 512, 0, s>>>(gt, ut, q, sc, rows, I, ldg, ldu);
     return;
   }
-#define GBLN_ROW8(TPR, VPT) \
-  glu_fwd_row8<T, ACT, TPR, VPT><<<grid, TPR, 0, s>>>((const T*)g, (const T*)u, q, sc, rows, (int)I, ldg, ldu)
-  if (nvec <= 128) GBLN_ROW8(64, 2);
-  else if (nvec <= 256) GBLN_ROW8(64, 4);
-  else if (nvec <= 512) GBLN_ROW8(128, 4);
-  else if (nvec <= 1024) GBLN_ROW8(256, 4);
-  else if (nvec <= 2048) GBLN_ROW8(512, 4);
-  else GBLN_ROW8(1024, 4);
+#define GBLN_ROW8(TPR, VPT, RPB) \
+  glu_fwd_row8<T, ACT, TPR, VPT, RPB><<<(unsigned)((rows + RPB - 1) / RPB), TPR * RPB, 0, s>>>(gt, ut, q, sc, rows, (int)I, ldg, ldu)
+#define GBLN_ROW8_CLUSTER(CL) \
+  glu_fwd_row8_cluster<T, ACT, CL><<<(unsigned)(rows * CL), 512, 0, s>>>(gt, ut, q, sc, rows, (int)I, ldg, ldu)
+  if (nvec <= 32) GBLN_ROW8(32, 1, 8);
+  else if (nvec <= 64) GBLN_ROW8(32, 2, 8);
+  else if (nvec <= 128) GBLN_ROW8(32, 4, 8);
+  else if (nvec <= 256) GBLN_ROW8(64, 4, 1);
+  else if (nvec <= 512) GBLN_ROW8(128, 4, 1);
+  else if (nvec <= 1024) GBLN_ROW8(256, 4, 1);
+  else if (nvec <= 2048) GBLN_ROW8(512, 4, 1);
+  else if (cl == 1) GBLN_ROW8(1024, 4, 1);
+  else if (cl == 4) GBLN_ROW8_CLUSTER(4);
+  else GBLN_ROW8_CLUSTER(8);
 #undef GBLN_ROW8
+#undef GBLN_ROW8_CLUSTER
 }
 
 template <typename T, int ACT, int FMT>
@@ -808,15 +1074,14 @@ void glu_fwd_ckpt_launch(const void* g, const void* u, void* o, GluCkpt C, int64
   const bool vec = I % VEC == 0 && aligned16(g) && aligned16(u) && aligned16(o) && ldg % VEC == 0 &&
                    ldu % VEC == 0 && ldo % VEC == 0 && aligned_to(C.gq, VEC) && aligned_to(C.uq, VEC);
   if (vec) {
-    constexpr int U = 4;
     const int64_t ncol = I / VEC;
     const int cb = col_block(ncol);
-    const int64_t units = (rows + U - 1) / U * ((ncol + cb - 1) / cb);
-    glu_fwd_ckpt<T, ACT, FMT, U><<<resident_grid(units, cb), cb, 0, s>>>((const T*)g, (const T*)u, (T*)o, C,
-                                                                           rows, ncol, ldg, ldu, ldo);
+    const int64_t units = (rows + kCkptRows - 1) / kCkptRows * ((ncol + cb - 1) / cb);
+    glu_fwd_ckpt<T, ACT, FMT><<<resident_grid(units, cb), cb, 0, s>>>((const T*)g, (const T*)u, (T*)o, C,
+                                                                        rows, ncol, ldg, ldu, ldo);
   } else {
-    const int64_t units = rows * ((I + kCkptGroup - 1) / kCkptGroup);
-    glu_fwd_ckpt_elem<T, ACT, FMT><<<resident_grid((units + 7) / 8), kGluBlock, 0, s>>>(
+    const int64_t units = rows * ((I + kCkptGroup - 1) / kCkptGroup), per = kGluBlock / 32 * kElemFlight;
+    glu_fwd_ckpt_elem<T, ACT, FMT><<<resident_grid((units + per - 1) / per), kGluBlock, 0, s>>>(
         (const T*)g, (const T*)u, (T*)o, C, rows, I, ldg, ldu, ldo);
   }
 }
@@ -828,13 +1093,16 @@ void glu_bwd_ckpt_launch(const void* d, GluCkptIn C, void* dg, void* du, int64_t
   constexpr int U = 2;
   const bool vec = I % VEC == 0 && aligned16(d) && aligned16(dg) && aligned16(du) && ldd % VEC == 0 &&
                    lddg % VEC == 0 && lddu % VEC == 0 && aligned_to(C.gq, VEC) && aligned_to(C.uq, VEC);
-  const int64_t ncol = vec ? I / VEC : I;
-  const int cb = col_block(ncol);
-  const unsigned grid = resident_grid((rows + U - 1) / U * ((ncol + cb - 1) / cb), cb);
-  if (vec)
-    glu_bwd_ckpt<T, VEC, ACT, FMT, U><<<grid, cb, 0, s>>>((const T*)d, C, (T*)dg, (T*)du, rows, ncol, ldd, lddg, lddu);
-  else
-    glu_bwd_ckpt<T, 1, ACT, FMT, U><<<grid, cb, 0, s>>>((const T*)d, C, (T*)dg, (T*)du, rows, ncol, ldd, lddg, lddu);
+  if (vec) {
+    const int64_t ncol = I / VEC;
+    const int cb = col_block(ncol);
+    const unsigned grid = resident_grid((rows + U - 1) / U * ((ncol + cb - 1) / cb), cb);
+    glu_bwd_ckpt<T, ACT, FMT, U><<<grid, cb, 0, s>>>((const T*)d, C, (T*)dg, (T*)du, rows, ncol, ldd, lddg, lddu);
+  } else {
+    const int64_t units = rows * ((I + kCkptGroup - 1) / kCkptGroup), per = kGluBlock / 32 * kElemFlight;
+    glu_bwd_ckpt_elem<T, ACT, FMT><<<resident_grid((units + per - 1) / per), kGluBlock, 0, s>>>(
+        (const T*)d, C, (T*)dg, (T*)du, rows, I, ldd, lddg, lddu);
+  }
 }
 
 // Dispatch on (io, act) to a templated launcher F<T, ACT>::run(args...).

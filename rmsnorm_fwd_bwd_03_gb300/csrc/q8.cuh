@@ -30,6 +30,31 @@ struct Q8Max {
 
 inline bool q8_ok(int fmt) { return fmt == GBLN_Q8_INT8 || fmt == GBLN_Q8_E4M3; }
 
+// Two float32 operations in one instruction (each rounded to nearest even by
+// itself): the codes cost two to three operations per value beside the kernels'
+// own arithmetic, and issue slots, not HBM, are what runs out first.
+#define GBLN_F2_OP(name, op)                                                                           \
+  __device__ __forceinline__ float2 name(float2 a, float2 b) {                                         \
+    float2 r;                                                                                          \
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t" op             \
+        " z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"                                                       \
+        : "=f"(r.x), "=f"(r.y)                                                                         \
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));                                                     \
+    return r;                                                                                          \
+  }
+GBLN_F2_OP(mul2, "mul.rn.f32x2")
+GBLN_F2_OP(add2, "add.rn.f32x2")
+#undef GBLN_F2_OP
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 // Magnitudes are compared as the bit patterns of |v|: an unsigned maximum
 // orders finite < infinity < NaN, so a NaN is never lost.
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
@@ -53,6 +78,33 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v) {
     return v;
   }
 }
+
+// The same of values as they lie in memory, without unpacking: bf16 magnitudes
+// are compared two at a time (a NaN wins, as above).  part() of the words of a
+// thread, join() across threads, bits() of the result as float32.
+template <typename T>
+struct AbsMax;
+template <>
+struct AbsMax<float> {
+  static __device__ __forceinline__ uint32_t join(uint32_t a, uint32_t b) { return max(a, b); }
+  static __device__ __forceinline__ uint32_t part(uint4 w) {
+    const uint32_t k = 0x7fffffffu;
+    return max(max(w.x & k, w.y & k), max(w.z & k, w.w & k));
+  }
+  static __device__ __forceinline__ uint32_t bits(uint32_t m) { return m; }
+};
+template <>
+struct AbsMax<bf16> {
+  static __device__ __forceinline__ uint32_t join(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
+  static __device__ __forceinline__ uint32_t part(uint4 w) {
+    const uint32_t k = 0x7fff7fffu;
+    return join(join(w.x & k, w.y & k), join(w.z & k, w.w & k));
+  }
+  static __device__ __forceinline__ uint32_t bits(uint32_t m) { return max(m & 0xffffu, m >> 16) << 16; }
+};
 
 __device__ __forceinline__ float q8_amax(uint32_t amax_bits) {
   return fmaxf(__uint_as_float(amax_bits), kQ8AmaxMin);
@@ -78,13 +130,16 @@ __device__ __forceinline__ uint32_t q8_code1(float v, float inv) {
 }
 template <int FMT>
 __device__ __forceinline__ uint32_t q8_code4(float v0, float v1, float v2, float v3, float inv) {
-  const float t0 = __fmul_rn(v0, inv), t1 = __fmul_rn(v1, inv), t2 = __fmul_rn(v2, inv), t3 = __fmul_rn(v3, inv);
   if constexpr (FMT == GBLN_Q8_INT8) {
-    const uint32_t a = __float_as_uint(__fadd_rn(t0, kRoundMagic)), b = __float_as_uint(__fadd_rn(t1, kRoundMagic));
-    const uint32_t c = __float_as_uint(__fadd_rn(t2, kRoundMagic)), d = __float_as_uint(__fadd_rn(t3, kRoundMagic));
-    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+    // Single multiplications: a paired one followed by the paired addition came
+    // out fused (one rounding instead of two), which moves codes next to a tie.
+    const float2 t = add2(make_float2(__fmul_rn(v0, inv), __fmul_rn(v1, inv)), both(kRoundMagic));
+    const float2 u = add2(make_float2(__fmul_rn(v2, inv), __fmul_rn(v3, inv)), both(kRoundMagic));
+    return __byte_perm(__byte_perm(__float_as_uint(t.x), __float_as_uint(t.y), 0x0040),
+                       __byte_perm(__float_as_uint(u.x), __float_as_uint(u.y), 0x0040), 0x5410);
   } else {
-    return e4m3x2(t0, t1) | (e4m3x2(t2, t3) << 16);
+    const float2 t = mul2(make_float2(v0, v1), both(inv)), u = mul2(make_float2(v2, v3), both(inv));
+    return e4m3x2(t.x, t.y) | (e4m3x2(u.x, u.y) << 16);
   }
 }
 // N consecutive codes to q, aligned to N bytes when N > 1.
@@ -105,8 +160,13 @@ __device__ __forceinline__ void q8_decode4(uint32_t w, float* v) {
   if constexpr (FMT == GBLN_Q8_INT8) {
     const uint32_t x = w ^ 0x80808080u;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      v[e] = __uint_as_float(__byte_perm(x, 0x4b000000u, 0x7540 + e)) - 8388736.0f;
+    for (int e = 0; e < 4; e += 2) {
+      const float2 f = add2(make_float2(__uint_as_float(__byte_perm(x, 0x4b000000u, 0x7540 + e)),
+                                        __uint_as_float(__byte_perm(x, 0x4b000000u, 0x7541 + e))),
+                            both(-8388736.0f));
+      v[e] = f.x;
+      v[e + 1] = f.y;
+    }
   } else {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -123,6 +183,10 @@ template <int FMT, int N>
 struct Codes {
   static_assert(N == 1 || N == 4 || N == 8, "1, 4 or 8 codes");
   uint32_t w[N == 8 ? 2 : 1];
+  __device__ __forceinline__ void zero() {
+    w[0] = 0;
+    if constexpr (N == 8) w[1] = 0;
+  }
   __device__ __forceinline__ void load(const uint8_t* p) {
     if constexpr (N == 8) {
       asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
@@ -137,8 +201,16 @@ struct Codes {
     float t[N == 1 ? 4 : N];
     q8_decode4<FMT>(w[0], t);
     if constexpr (N == 8) q8_decode4<FMT>(w[1], t + 4);
+    if constexpr (N == 1) {
+      v[0] = __fmul_rn(t[0], scale);
+    } else {
 #pragma unroll
-    for (int e = 0; e < N; ++e) v[e] = __fmul_rn(t[e], scale);
+      for (int e = 0; e < N; e += 2) {
+        const float2 f = mul2(make_float2(t[e], t[e + 1]), both(scale));
+        v[e] = f.x;
+        v[e + 1] = f.y;
+      }
+    }
   }
 };
 

@@ -186,16 +186,50 @@ __global__ void __launch_bounds__(BLOCK) rms8_fwd_vec(const Fwd8<T, W> A) {
 }
 
 // ---------------------------------------------------------------------------
-// Forward, element path (any alignment and width).  A warp takes chunks of 128
-// consecutive values, lane l the values l, l + 32, l + 64, l + 96: every access
-// of a warp is contiguous, and a chunk is a checkpoint group.  NW warps per row
-// take chunks wi, wi + NW, ...; CACHED keeps up to kElemChunks of them per warp
-// in registers, wider rows are read again (from the thread's own stores, where
-// there is a residual).  One row per NW warps, blockDim / (32 NW) rows per block.
+// Forward, element path (any alignment, rows of up to 16384 values).  A warp
+// takes chunks of 128 consecutive values, lane l the values l, l + 32, l + 64,
+// l + 96: every access of a warp is contiguous, and a chunk is a checkpoint
+// group.  NW warps per row take chunks wi, wi + NW, ..., at most kElemChunks
+// each, which stay in registers.  Offsets within a chunk are immediates and only
+// a row's last chunk is predicated: at one value per lane and access these
+// kernels are bound by their instructions, not by HBM.
 // ---------------------------------------------------------------------------
 constexpr int kElemChunks = 4;
 
-template <typename T, typename W, bool RES, int MODE, bool CACHED>
+// Values l, l + 32, l + 64, l + 96 of a chunk; rem = values from the lane's first
+// one to the row's end (FULL: the chunk is whole).
+template <bool FULL, typename T>
+__device__ __forceinline__ void load_chunk(const T* p, int rem, T (&v)[4]) {
+#pragma unroll
+  for (int m = 0; m < 4; ++m) v[m] = FULL || 32 * m < rem ? p[32 * m] : from_f32<T>(0.f);
+}
+template <bool FULL>
+__device__ __forceinline__ void load_chunk(const uint8_t* p, int rem, uint8_t (&v)[4]) {
+#pragma unroll
+  for (int m = 0; m < 4; ++m) v[m] = FULL || 32 * m < rem ? p[32 * m] : (uint8_t)0;
+}
+template <bool FULL, typename T>
+__device__ __forceinline__ void store_chunk(T* p, int rem, const float (&v)[4]) {
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+    if (FULL || 32 * m < rem) p[32 * m] = from_f32<T>(v[m]);
+}
+template <bool FULL, int FMT>
+__device__ __forceinline__ void store_codes(uint8_t* p, int rem, const float (&v)[4], float inv) {
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+    if (FULL || 32 * m < rem) p[32 * m] = (uint8_t)q8_code1<FMT>(v[m], inv);
+}
+// Run f(true_type) for a whole chunk, f(false_type) for a row's last, shorter one.
+struct FullChunk { static constexpr bool v = true; };
+struct PartChunk { static constexpr bool v = false; };
+template <typename F>
+__device__ __forceinline__ void chunk_of(int c0, int H, F&& f) {
+  if (c0 + kCkptGroup <= H) f(FullChunk{});
+  else if (c0 < H) f(PartChunk{});
+}
+
+template <typename T, typename W, bool RES, int MODE>
 __global__ void __launch_bounds__(1024) rms8_fwd_elem(const Fwd8<T, W> A, int NW) {
   constexpr int FMT = mode_fmt(MODE);
   __shared__ float red[32];
@@ -204,65 +238,46 @@ __global__ void __launch_bounds__(1024) rms8_fwd_elem(const Fwd8<T, W> A, int NW
   const int g = warp / NW, wi = warp - g * NW;
   const int64_t row = (int64_t)blockIdx.x * (blockDim.x / (32 * NW)) + g;
   const bool live = row < A.rows;  // the barrier below is reached by every warp
-  const size_t base = (size_t)(live ? row : 0) * A.H;
-  const int nchunk = (A.H + kCkptGroup - 1) / kCkptGroup;
   const int H = live ? A.H : 0;
+  const size_t at = (size_t)(live ? row : 0) * A.H + wi * kCkptGroup + lane;
+  const int c0 = wi * kCkptGroup, cs = NW * kCkptGroup;  // first chunk, and the step to the next
 
-  float hc[CACHED ? kElemChunks : 1][4];
-  KahanSum ks;
+  T xr[kElemChunks][4], rr[kElemChunks][4];
+#pragma unroll
+  for (int k = 0; k < kElemChunks; ++k)
+    chunk_of(c0 + k * cs, H, [&](auto full) {
+      const int rem = H - (c0 + k * cs) - lane;
+      load_chunk<decltype(full)::v>(A.x + at + k * cs, rem, xr[k]);
+      if constexpr (RES) load_chunk<decltype(full)::v>(A.r + at + k * cs, rem, rr[k]);
+    });
+  float h[kElemChunks][4];
+  float ss = 0.f;
   uint32_t am = 0;
-
-  auto load = [&](int c, float (&h)[4]) {
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int j = c * kCkptGroup + m * 32 + lane;
-      h[m] = 0.f;
-      if (j < H) {
-        float a = to_f32(A.x[base + j]);
-        if constexpr (RES) a += to_f32(A.r[base + j]);
-        h[m] = a;
-      }
-    }
-  };
-  auto first = [&](int c, float (&h)[4]) {
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int j = c * kCkptGroup + m * 32 + lane;
-      if constexpr (RES) {
-        const T hv = from_f32<T>(h[m]);
-        h[m] = to_f32(hv);
-        if (j < H) A.hout[base + j] = hv;
-      }
-      ks.add(h[m] * h[m]);
-      if constexpr (MODE == kRowE4m3)
-        if (j < H) am = max(am, abs_bits(__fmul_rn(to_f32(A.w[j]), h[m])));
-    }
-    if constexpr (MODE != kRowE4m3) {
-      const uint32_t gm = group_max<32>(abs_max_bits<4>(h));
-      const float a = q8_amax(gm), inv = q8_inv<FMT>(a);
+  for (int k = 0; k < kElemChunks; ++k)
+    chunk_of(c0 + k * cs, H, [&](auto full) {
+      constexpr bool FULL = decltype(full)::v;
+      const int rem = H - (c0 + k * cs) - lane;
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        const int j = c * kCkptGroup + m * 32 + lane;
-        if (j < H) A.q[base + j] = (uint8_t)q8_code1<FMT>(h[m], inv);
+        h[k][m] = to_f32(xr[k][m]);
+        if constexpr (RES) h[k][m] = to_f32(from_f32<T>(h[k][m] + to_f32(rr[k][m])));
+        ss = fmaf(h[k][m], h[k][m], ss);
       }
-      if (lane == 0 && live) A.sc[(size_t)row * A.ng + c] = q8_scale<FMT>(a, gm);
-    }
-  };
-  if constexpr (CACHED) {
+      if constexpr (RES) store_chunk<FULL>(A.hout + at + k * cs, rem, h[k]);
+      if constexpr (MODE == kRowE4m3) {
+        W w[4];
+        load_chunk<FULL>(A.w + c0 + k * cs + lane, rem, w);
 #pragma unroll
-    for (int k = 0; k < kElemChunks; ++k)
-      if (wi + k * NW < nchunk) load(wi + k * NW, hc[k]);
-#pragma unroll
-    for (int k = 0; k < kElemChunks; ++k)
-      if (wi + k * NW < nchunk) first(wi + k * NW, hc[k]);
-  } else {
-    for (int c = wi; c < nchunk; c += NW) {
-      load(c, hc[0]);
-      first(c, hc[0]);
-    }
-  }
-
-  float ss = group_sum<32>(ks.s);
+        for (int m = 0; m < 4; ++m) am = max(am, abs_bits(__fmul_rn(to_f32(w[m]), h[k][m])));
+      } else {
+        const uint32_t gm = group_max<32>(abs_max_bits<4>(h[k]));
+        const float a = q8_amax(gm);
+        store_codes<FULL, FMT>(A.q + at + k * cs, rem, h[k], q8_inv<FMT>(a));
+        if (lane == 0) A.sc[(size_t)row * A.ng + wi + k * NW] = q8_scale<FMT>(a, gm);
+      }
+    });
+  ss = group_sum<32>(ss);
   if constexpr (MODE == kRowE4m3) am = group_max<32>(am);
   if (NW > 1) {
     if (lane == 0) {
@@ -284,29 +299,87 @@ __global__ void __launch_bounds__(1024) rms8_fwd_elem(const Fwd8<T, W> A, int NW
     inv = q8_inv<FMT>(a);
     if (live && wi == 0 && lane == 0) A.sc[row] = q8_scale<FMT>(__fmul_rn(a, rs), am);
   }
-  auto second = [&](int c, const float (&h)[4]) {
+#pragma unroll
+  for (int k = 0; k < kElemChunks; ++k)
+    chunk_of(c0 + k * cs, H, [&](auto full) {
+      constexpr bool FULL = decltype(full)::v;
+      const int rem = H - (c0 + k * cs) - lane;
+      W w[4];
+      load_chunk<FULL>(A.w + c0 + k * cs + lane, rem, w);
+      float o[4];
+      if (MODE != kRowE4m3 || A.y) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) o[m] = to_f32(w[m]) * (h[k][m] * rs);
+        store_chunk<FULL>(A.y + at + k * cs, rem, o);
+      }
+      if constexpr (MODE == kRowE4m3) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) o[m] = __fmul_rn(to_f32(w[m]), h[k][m]);
+        store_codes<FULL, FMT>(A.q + at + k * cs, rem, o, inv);
+      }
+    });
+}
+
+// Forward for rows too wide for the registers of either path: one block per row,
+// which it reads a second time for the output (its own stores, where there is a
+// residual).  Chunks as above; compensated sums, since a thread may add up tens
+// of thousands of terms.
+constexpr int kWideBlock = 512;
+
+template <typename T, typename W, bool RES, int MODE>
+__global__ void __launch_bounds__(kWideBlock) rms8_fwd_wide(const Fwd8<T, W> A) {
+  constexpr int FMT = mode_fmt(MODE), NW = kWideBlock / 32;
+  __shared__ float red[NW];
+  __shared__ uint32_t redm[NW];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = blockIdx.x;
+  const size_t base = (size_t)row * A.H;
+  KahanSum ks;
+  uint32_t am = 0;
+  for (int c0 = warp * kCkptGroup; c0 < A.H; c0 += NW * kCkptGroup) {
+    float h[4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      const int j = c * kCkptGroup + m * 32 + lane;
-      if (j < H) {
-        const float wv = to_f32(A.w[j]);
-        if (MODE != kRowE4m3 || A.y) A.y[base + j] = from_f32<T>(wv * (h[m] * rs));
-        if constexpr (MODE == kRowE4m3) A.q[base + j] = (uint8_t)q8_code1<FMT>(__fmul_rn(wv, h[m]), inv);
+      const int j = c0 + 32 * m + lane;
+      h[m] = 0.f;
+      if (j < A.H) {
+        h[m] = to_f32(A.x[base + j]);
+        if constexpr (RES) {
+          const T hv = from_f32<T>(h[m] + to_f32(A.r[base + j]));
+          A.hout[base + j] = hv;
+          h[m] = to_f32(hv);
+        }
+        ks.add(h[m] * h[m]);
+        if constexpr (MODE == kRowE4m3) am = max(am, abs_bits(__fmul_rn(to_f32(A.w[j]), h[m])));
       }
     }
-  };
-  if constexpr (CACHED) {
+    if constexpr (MODE != kRowE4m3) {
+      const uint32_t gm = group_max<32>(abs_max_bits<4>(h));
+      const float a = q8_amax(gm);
+      store_codes<false, FMT>(A.q + base + c0 + lane, A.H - c0 - lane, h, q8_inv<FMT>(a));
+      if (lane == 0) A.sc[(size_t)row * A.ng + c0 / kCkptGroup] = q8_scale<FMT>(a, gm);
+    }
+  }
+  float ss = ks.s;
+  row_sum_max<kWideBlock>(ss, am, red, redm);
+  const float rs = rsqrtf(ss * A.inv_H + A.eps);
+  if (threadIdx.x == 0) A.rstd[row] = rs;
+  float inv = 0.f;
+  if constexpr (MODE == kRowE4m3) {
+    const float a = q8_amax(am);
+    inv = q8_inv<FMT>(a);
+    if (threadIdx.x == 0) A.sc[row] = q8_scale<FMT>(__fmul_rn(a, rs), am);
+  }
+  for (int c0 = warp * kCkptGroup; c0 < A.H; c0 += NW * kCkptGroup) {
 #pragma unroll
-    for (int k = 0; k < kElemChunks; ++k)
-      if (wi + k * NW < nchunk) second(wi + k * NW, hc[k]);
-  } else {
-    for (int c = wi; c < nchunk; c += NW) {
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const int j = c * kCkptGroup + m * 32 + lane;
-        if (j < H) hc[0][m] = RES ? to_f32(A.hout[base + j]) : to_f32(A.x[base + j]);
+    for (int m = 0; m < 4; ++m) {
+      const int j = c0 + 32 * m + lane;
+      if (j < A.H) {
+        const float h = RES ? to_f32(A.hout[base + j]) : to_f32(A.x[base + j]);  // own write
+        const float wv = to_f32(A.w[j]);
+        if (MODE != kRowE4m3 || A.y) A.y[base + j] = from_f32<T>(wv * (h * rs));
+        if constexpr (MODE == kRowE4m3) A.q[base + j] = (uint8_t)q8_code1<FMT>(__fmul_rn(wv, h), inv);
       }
-      second(c, hc[0]);
     }
   }
 }
@@ -446,82 +519,67 @@ __global__ void __launch_bounds__(TPR * GPB) rms8_bwd_vec(const Bwd8<T, W> A, bo
 }
 
 // ---------------------------------------------------------------------------
-// Backward, element path: chunks of 128 values per warp as in rms8_fwd_elem.
-// CACHED: the row's values and the dW sums stay in registers; wider rows are
-// read twice and their dW sums are kept in the block's partial row (one row
-// group per block then).
+// Backward, element path: chunks of 128 values per warp as in rms8_fwd_elem.  The
+// row's inputs stay in registers as loaded, the dW sums in float32; n is rebuilt
+// from the codes for each use.
 // ---------------------------------------------------------------------------
-template <typename T, typename W, bool DRES, int FMT, bool CACHED>
-__global__ void __launch_bounds__(CACHED ? 1024 : 512) rms8_bwd_elem(const Bwd8<T, W> A, int NW) {
-  constexpr int C = CACHED ? kElemChunks : 1;
-  extern __shared__ float sacc[];  // CACHED with several groups: one row of dW sums
-  __shared__ float red[2][32];
+template <typename T, typename W, bool DRES, int FMT, int BLOCK>
+__global__ void __launch_bounds__(BLOCK, 768 / BLOCK) rms8_bwd_elem(const Bwd8<T, W> A, int NW) {
+  constexpr int C = kElemChunks;
+  extern __shared__ float sacc[];  // several row groups: one row of dW sums
+  __shared__ float red[2][BLOCK / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int GPB = (int)(blockDim.x / (32 * NW));
+  const int GPB = BLOCK / (32 * NW);
   const int g = warp / NW, wi = warp - g * NW;
-  const int H = A.H, nchunk = (H + kCkptGroup - 1) / kCkptGroup;
+  const int H = A.H;
   const int64_t P = gridDim.x, p = blockIdx.x;
   const int64_t r0 = p * A.rows / P, r1 = (p + 1) * A.rows / P;
-  float* prow = A.partial + (size_t)p * H;
+  const int c0 = wi * kCkptGroup, cs = NW * kCkptGroup;
+  const W* wp = A.w + c0 + lane;
 
-  float acc[C][4], d[C][4], n[C][4];
+  float acc[C][4];
 #pragma unroll
   for (int k = 0; k < C; ++k)
 #pragma unroll
     for (int m = 0; m < 4; ++m) acc[k][m] = 0.f;
-  if constexpr (!CACHED)
-    for (int c = wi; c < nchunk; c += NW)
-#pragma unroll
-      for (int m = 0; m < 4; ++m)
-        if (const int j = c * kCkptGroup + m * 32 + lane; j < H) prow[j] = 0.f;
 
   int par = 0;
   for (int64_t row = r0 + g; row < r1; row += GPB) {
-    const size_t base = (size_t)row * H;
+    const size_t at = (size_t)row * H + c0 + lane;
+    T dy[C][4], dr[C][4];
+    uint32_t q[C];
+    float sc[C];
+#pragma unroll
+    for (int k = 0; k < C; ++k)
+      chunk_of(c0 + k * cs, H, [&](auto full) {
+        constexpr bool FULL = decltype(full)::v;
+        const int rem = H - (c0 + k * cs) - lane;
+        uint8_t b[4];
+        load_chunk<FULL>(A.dy + at + k * cs, rem, dy[k]);
+        load_chunk<FULL>(A.hq + at + k * cs, rem, b);
+        if constexpr (DRES) load_chunk<FULL>(A.dres + at + k * cs, rem, dr[k]);
+        sc[k] = __ldg(A.hs + (size_t)row * A.ng + wi + k * NW);
+        q[k] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+      });
     const float rs = __ldg(A.rstd + row);
-    KahanSum ks;
-    auto load = [&](int c, float (&dk)[4], float (&nk)[4]) {
-      const float s = __ldg(A.hs + (size_t)row * A.ng + c);
+    float dot = 0.f;
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const int j = c * kCkptGroup + m * 32 + lane;
-        dk[m] = nk[m] = 0.f;
-        if (j < H) {
-          Codes<FMT, 1> q;
-          float v[1];
-          q.load(A.hq + base + j);
-          q.get(v, s);
-          dk[m] = to_f32(A.dy[base + j]);
-          nk[m] = v[0] * rs;
+    for (int k = 0; k < C; ++k)
+      chunk_of(c0 + k * cs, H, [&](auto full) {
+        W w[4];
+        load_chunk<decltype(full)::v>(wp + k * cs, H - (c0 + k * cs) - lane, w);
+        float n[4];
+        q8_decode4<FMT>(q[k], n);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          n[m] = __fmul_rn(n[m], sc[k]) * rs;
+          const float d = to_f32(dy[k][m]);
+          dot = fmaf(d * to_f32(w[m]), n[m], dot);
+          acc[k][m] = fmaf(d, n[m], acc[k][m]);
         }
-      }
-    };
-    auto dots = [&](int c, const float (&dk)[4], const float (&nk)[4]) {
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const int j = c * kCkptGroup + m * 32 + lane;
-        if (j < H) ks.add(dk[m] * to_f32(A.w[j]) * nk[m]);
-      }
-    };
-    if constexpr (CACHED) {
-#pragma unroll
-      for (int k = 0; k < C; ++k)
-        if (wi + k * NW < nchunk) load(wi + k * NW, d[k], n[k]);
-#pragma unroll
-      for (int k = 0; k < C; ++k)
-        if (wi + k * NW < nchunk) {
-          dots(wi + k * NW, d[k], n[k]);
-#pragma unroll
-          for (int m = 0; m < 4; ++m) acc[k][m] = fmaf(d[k][m], n[k][m], acc[k][m]);
-        }
-    } else {
-      for (int c = wi; c < nchunk; c += NW) {
-        load(c, d[0], n[0]);
-        dots(c, d[0], n[0]);
-      }
-    }
-    float dot = group_sum<32>(ks.s);
-    if (NW > 1) {
+      });
+    dot = group_sum<32>(dot);
+    if (NW > 1) {  // double-buffered as in rms8_bwd_vec
       if (lane == 0) red[par][warp] = dot;
       bar_sync_named(1 + g, 32 * NW);
       dot = 0.f;
@@ -529,54 +587,74 @@ __global__ void __launch_bounds__(CACHED ? 1024 : 512) rms8_bwd_elem(const Bwd8<
       par ^= 1;
     }
     const float cc = dot * A.inv_H;
-    auto store = [&](int c, const float (&dk)[4], const float (&nk)[4]) {
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const int j = c * kCkptGroup + m * 32 + lane;
-        if (j < H) {
-          float o = rs * (dk[m] * to_f32(A.w[j]) - nk[m] * cc);
-          if constexpr (DRES) o += to_f32(A.dres[base + j]);
-          A.dx[base + j] = from_f32<T>(o);
+    for (int k = 0; k < C; ++k)
+      chunk_of(c0 + k * cs, H, [&](auto full) {
+        constexpr bool FULL = decltype(full)::v;
+        const int rem = H - (c0 + k * cs) - lane;
+        W w[4];
+        load_chunk<FULL>(wp + k * cs, rem, w);
+        float n[4], o[4];
+        q8_decode4<FMT>(q[k], n);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          n[m] = __fmul_rn(n[m], sc[k]) * rs;
+          o[m] = rs * (to_f32(dy[k][m]) * to_f32(w[m]) - n[m] * cc);
+          if constexpr (DRES) o[m] += to_f32(dr[k][m]);
         }
-      }
-    };
-    if constexpr (CACHED) {
-#pragma unroll
-      for (int k = 0; k < C; ++k)
-        if (wi + k * NW < nchunk) store(wi + k * NW, d[k], n[k]);
-    } else {
-      for (int c = wi; c < nchunk; c += NW) {
-        load(c, d[0], n[0]);  // before the store: dx may alias dy
-        store(c, d[0], n[0]);
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-          if (const int j = c * kCkptGroup + m * 32 + lane; j < H) prow[j] = fmaf(d[0][m], n[0][m], prow[j]);
-      }
-    }
+        store_chunk<FULL>(A.dx + at + k * cs, rem, o);
+      });
   }
 
-  if constexpr (CACHED) {
-    if (GPB == 1) {
+  float* prow = A.partial + (size_t)p * H + c0 + lane;
+  float* srow = sacc + c0 + lane;
+  for (int t = 0; t < GPB; ++t) {  // groups add in order
+    if (t == g) {
 #pragma unroll
       for (int k = 0; k < C; ++k)
 #pragma unroll
         for (int m = 0; m < 4; ++m)
-          if (const int j = (wi + k * NW) * kCkptGroup + m * 32 + lane; j < H) prow[j] = acc[k][m];
-    } else {
-      for (int q = 0; q < GPB; ++q) {  // groups add in order
-        if (q == g) {
-#pragma unroll
-          for (int k = 0; k < C; ++k)
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-              if (const int j = (wi + k * NW) * kCkptGroup + m * 32 + lane; j < H) {
-                const float s = q == 0 ? acc[k][m] : sacc[j] + acc[k][m];
-                if (q == GPB - 1) prow[j] = s;
-                else sacc[j] = s;
-              }
-        }
-        __syncthreads();
-      }
+          if (c0 + k * cs + 32 * m + lane < H) {
+            const int j = k * cs + 32 * m;
+            const float v = t == 0 ? acc[k][m] : srow[j] + acc[k][m];
+            if (t == GPB - 1) prow[j] = v;
+            else srow[j] = v;
+          }
+    }
+    __syncthreads();
+  }
+}
+
+// Backward for wider rows: one block per row at a time, read twice; dW sums are
+// kept in the block's partial row.
+template <typename T, typename W, bool DRES, int FMT>
+__global__ void __launch_bounds__(kWideBlock) rms8_bwd_wide(const Bwd8<T, W> A) {
+  __shared__ float red[kWideBlock / 32];
+  const int H = A.H;
+  const int64_t P = gridDim.x, p = blockIdx.x;
+  const int64_t r0 = p * A.rows / P, r1 = (p + 1) * A.rows / P;
+  float* prow = A.partial + (size_t)p * H;
+  for (int j = threadIdx.x; j < H; j += kWideBlock) prow[j] = 0.f;
+  for (int64_t row = r0; row < r1; ++row) {
+    const size_t base = (size_t)row * H;
+    const float rs = __ldg(A.rstd + row);
+    const auto norm = [&](int j) {
+      Codes<FMT, 1> q;
+      float v[1];
+      q.load(A.hq + base + j);
+      q.get(v, __ldg(A.hs + (size_t)row * A.ng + j / kCkptGroup));
+      return v[0] * rs;
+    };
+    KahanSum ks;
+    for (int j = threadIdx.x; j < H; j += kWideBlock)
+      ks.add(to_f32(A.dy[base + j]) * to_f32(A.w[j]) * norm(j));
+    const float c = row_sum<kWideBlock>(ks.s, red) * A.inv_H;
+    for (int j = threadIdx.x; j < H; j += kWideBlock) {
+      const float d = to_f32(A.dy[base + j]), n = norm(j);
+      float o = rs * (d * to_f32(A.w[j]) - n * c);
+      if constexpr (DRES) o += to_f32(A.dres[base + j]);
+      prow[j] = fmaf(d, n, prow[j]);
+      A.dx[base + j] = from_f32<T>(o);
     }
   }
 }
@@ -588,17 +666,18 @@ constexpr int64_t kMaxH = 1 << 24;
 constexpr int64_t kMaxRows = (1LL << 31) - 1;
 constexpr int64_t kMaxVecPerRow = 2048;  // 512 threads x 4 vectors
 
-// Element path: warps per row so that a warp holds at most kElemChunks chunks
-// (a power of two up to 32, then the row is not held in registers).
+// Element path: warps per row (a power of two) so that a warp holds at most
+// kElemChunks chunks; beyond 32 warps (16 in the backward, which holds twice as
+// much per value) the row does not fit the registers.
 struct Elem {
-  bool cached;
+  bool fits;
   int nw;      // warps per row
   int block;   // threads
   int groups;  // rows per block and pass
 };
-Elem elem_geometry(int64_t H) {
+Elem elem_geometry(int64_t H, int most_warps) {
   const int64_t nchunk = (H + kCkptGroup - 1) / kCkptGroup;
-  if (nchunk > 32 * kElemChunks) return {false, 16, 512, 1};
+  if (nchunk > most_warps * kElemChunks) return {false, kWideBlock / 32, kWideBlock, 1};
   int nw = 1;
   while ((int64_t)nw * kElemChunks < nchunk) nw *= 2;
   const int block = nw < 8 ? 256 : nw * 32;
@@ -615,13 +694,13 @@ struct BwdGeometry {
 };
 BwdGeometry bwd_geometry(int64_t H, size_t io) {
   if (!vec_width(H, io)) {
-    const Elem e = elem_geometry(H);
-    return {0, 0, e.groups, e.cached ? 1024 / e.block : 4};
+    const Elem e = elem_geometry(H, 16);
+    return {0, 0, e.groups, e.fits ? 768 / e.block : 2};
   }
   const int64_t nvec = H * (int64_t)io / 16;
   if (nvec <= 32) return {32, 1, 8, 4};
-  if (nvec <= 64) return {32, 2, 8, 4};
-  if (nvec <= 128) return {64, 2, 4, 4};
+  if (nvec <= 64) return {32, 2, 8, 3};
+  if (nvec <= 128) return {64, 2, 4, 3};
   int tpr = 64;
   while ((int64_t)tpr * 4 < nvec) tpr *= 2;
   return {tpr, 4, 1, 512 / tpr > 0 ? 512 / tpr : 1};
@@ -641,10 +720,10 @@ gbln_status fwd_launch(const Fwd8<T, W>& A, cudaStream_t s) {
   const bool vec = vec_width(A.H, sizeof(T)) && aligned16(A.x) && aligned16(A.w) && aligned16(A.y) &&
                    (!RES || (aligned16(A.r) && aligned16(A.hout))) && aligned_to(A.q, VEC);
   if (!vec) {
-    const Elem e = elem_geometry(A.H);
+    const Elem e = elem_geometry(A.H, 32);
     const int64_t blocks = (A.rows + e.groups - 1) / e.groups;
-    if (e.cached) rms8_fwd_elem<T, W, RES, MODE, true><<<(unsigned)blocks, e.block, 0, s>>>(A, e.nw);
-    else rms8_fwd_elem<T, W, RES, MODE, false><<<(unsigned)blocks, e.block, 0, s>>>(A, e.nw);
+    if (e.fits) rms8_fwd_elem<T, W, RES, MODE><<<(unsigned)blocks, e.block, 0, s>>>(A, e.nw);
+    else rms8_fwd_wide<T, W, RES, MODE><<<(unsigned)A.rows, kWideBlock, 0, s>>>(A);
     return launch_status();
   }
   const int nvec = A.H / VEC;
@@ -677,10 +756,11 @@ gbln_status bwd_launch(const Bwd8<T, W>& A, int64_t P, cudaStream_t s) {
                    (!DRES || aligned16(A.dres)) && aligned_to(A.hq, VEC);
   const unsigned grid = (unsigned)P;
   if (!vec) {
-    const Elem e = elem_geometry(A.H);
+    const Elem e = elem_geometry(A.H, 16);
     const size_t smem = e.groups > 1 ? (size_t)A.H * sizeof(float) : 0;  // at most 2048 values
-    if (e.cached) rms8_bwd_elem<T, W, DRES, FMT, true><<<grid, e.block, smem, s>>>(A, e.nw);
-    else rms8_bwd_elem<T, W, DRES, FMT, false><<<grid, e.block, 0, s>>>(A, e.nw);
+    if (e.fits && e.block == 256) rms8_bwd_elem<T, W, DRES, FMT, 256><<<grid, 256, smem, s>>>(A, e.nw);
+    else if (e.fits) rms8_bwd_elem<T, W, DRES, FMT, 512><<<grid, 512, 0, s>>>(A, e.nw);
+    else rms8_bwd_wide<T, W, DRES, FMT><<<grid, kWideBlock, 0, s>>>(A);
     return launch_status();
   }
   const bool prefetch = aligned16(A.hq) && A.H % 16 == 0;
