@@ -80,111 +80,144 @@ struct WriteArgs {
 // table entries are loaded once per token and lane, and all of a lane's row
 // loads are issued before anything that depends on the token's slot or position.
 // ---------------------------------------------------------------------------
-constexpr int kWriteHeads = 4;
+// Six head rows per lane (two blocks of 256 threads per SM) measured faster than
+// four (three blocks): 236 against 247 us for 65536 tokens of 32 / 8 heads of 128.
+constexpr int kWriteHeads = 6;
+constexpr int kWriteWarps = 8;  // per block: chunks of a token, then tokens
+// A warp walks tokens t, t + step, ... and asks for the next one's rows in L2
+// while it works on this one.  Eight times the resident blocks leave a warp a
+// few tokens to do that for and the scheduler something to balance: 236 us, with
+// one token per warp 283, with the resident blocks alone 266.
+constexpr int kWriteGrid = 2 * 8;  // blocks per SM
 
 template <typename T, bool IL, int FMT>
-__global__ void __launch_bounds__(256, 3)
-cache8_write_vec(const WriteArgs<T> A, int nu, int lanes, int nchunk, int ch) {
+__global__ void __launch_bounds__(32 * kWriteWarps, 2)
+cache8_write_vec(const WriteArgs<T> A, int nu, int lg, int ch) {
   constexpr int VEC = VecOf<T>::N;
+  constexpr int LINE = 128 / sizeof(T);
   const int half = A.D / 2, HR = A.Hq + A.Hk, HT = HR + A.Hk;
-  const int G = 32 / lanes;
-  const int lane = threadIdx.x & 31;
-  const int v = lane % lanes, g = lane / lanes;
+  const int lanes = 1 << lg, G = 32 >> lg;
+  const int lane = threadIdx.x;
+  const int v = lane & (lanes - 1);
   const bool on = v < nu;
-  const int64_t item = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int64_t t = item / nchunk;
-  if (t >= A.rows) return;  // uniform per warp
-  const int c = (int)(item - t * nchunk);
-  const int hb = g + G * c * ch;
+  const int c = blockIdx.y * blockDim.y + threadIdx.y;
+  const int hf = G * c * ch, hb = (lane >> lg) + hf;
+  const int64_t step = (int64_t)gridDim.x * blockDim.z;
+  int64_t t = (int64_t)blockIdx.x * blockDim.z + threadIdx.z;
+  if (t >= A.rows || hf >= HT) return;  // uniform per warp
   const int ia = v * VEC, ib = half + ia;
-  const int p = __ldg(A.pos + t);
-  const int64_t slot = __ldg(A.S.slots + t);
-  uint4 a[kWriteHeads], b[kWriteHeads];
+  int p = __ldg(A.pos + t);
+  int64_t slot = __ldg(A.S.slots + t);
+#pragma unroll 1
+  for (; t < A.rows; t += step) {
+    // rows of the three inputs, offset so that head h is at + h * D in each
+    const T* qp = A.q + t * A.ldq;
+    const T* kp = A.k + t * A.ldk - (int64_t)A.Hq * A.D;
+    const T* vp = A.v + t * A.ldv - (int64_t)HR * A.D;
+    uint4 a[kWriteHeads], b[kWriteHeads];
 #pragma unroll
-  for (int j = 0; j < kWriteHeads; ++j) {
-    const int h = hb + G * j;
-    if (j < ch && on && h < HT) {
-      const T* src = A.src(t, h);
-      a[j] = ld_stream(src + ia);
-      b[j] = ld_stream(src + ib);
-    } else {
+    for (int j = 0; j < kWriteHeads; ++j) {
+      const int h = hb + G * j;
       a[j] = b[j] = make_uint4(0, 0, 0, 0);
+      if (j < ch && on && h < HT) {
+        const T* src = (h < A.Hq ? qp : h < HR ? kp : vp) + h * A.D + ia;
+        a[j] = ld_stream(src);
+        b[j] = ld_stream(src + half);
+      }
     }
-  }
-  const bool ok = p >= 0 && (int64_t)p < A.max_pos;
-  // (cos, sin) of the lane's pairs: entries v*VEC.. (rotate-half), or half as many
-  // for each of its two vectors (interleaved)
-  float2 cs[VEC];
-  if (ok && on) {
-    const float2* e = A.table + (size_t)p * half;
+    const bool ok = p >= 0 && (int64_t)p < A.max_pos;
+    // (cos, sin) of the lane's pairs: entries v*VEC.. (rotate-half), or half as many
+    // for each of its two vectors (interleaved)
+    float2 cs[VEC];
+    if (ok && on) {
+      const float2* e = A.table + (size_t)p * half;
 #pragma unroll
-    for (int i = 0; i < VEC; i += 2) {
-      const int at = !IL ? ia + i : i < VEC / 2 ? ia / 2 + i : ib / 2 + i - VEC / 2;
-      const float4 f = __ldg(reinterpret_cast<const float4*>(e + at));
-      cs[i] = make_float2(f.x, f.y);
-      cs[i + 1] = make_float2(f.z, f.w);
+      for (int i = 0; i < VEC; i += 2) {
+        const int at = !IL ? ia + i : i < VEC / 2 ? ia / 2 + i : ib / 2 + i - VEC / 2;
+        const float4 f = __ldg(reinterpret_cast<const float4*>(e + at));
+        cs[i] = make_float2(f.x, f.y);
+        cs[i + 1] = make_float2(f.z, f.w);
+      }
+    } else {
+      const float x = ok ? 0.f : __int_as_float(0x7fc00000);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) cs[i] = make_float2(x, x);
     }
-  } else {
-    const float x = ok ? 0.f : __int_as_float(0x7fc00000);
+    int64_t off = 0;
+    const int64_t page = A.S.page_of(slot, off);
+    // the warp's next token: its position and slot, and its rows on their way to L2
+    if (t + step < A.rows) {
+      p = __ldg(A.pos + t + step);
+      slot = __ldg(A.S.slots + t + step);
+      const int last = min(hf + G * ch, HT) * A.D;
+      for (int x = hf * A.D + lane * LINE; x < last; x += 32 * LINE)
+        prefetch_line((x < A.Hq * A.D ? qp + step * A.ldq : x < HR * A.D ? kp + step * A.ldk : vp + step * A.ldv) + x);
+    }
+    if (c == 0 && lane == 0) {
+      if (!ok && (A.Hq > 0 || page >= 0)) atomicOr(A.err, kErrBadPosition);
+      if (page == -2) atomicOr(A.err, kErrBadSlot);
+    }
+    T* qo = A.qo + t * A.ldqo + ia;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) cs[i] = make_float2(x, x);
-  }
-  int64_t off = 0;
-  const int64_t page = A.S.page_of(slot, off);
-  if (c == 0 && lane == 0) {
-    if (!ok && (A.Hq > 0 || page >= 0)) atomicOr(A.err, kErrBadPosition);
-    if (page == -2) atomicOr(A.err, kErrBadSlot);
-  }
+    for (int j = 0; j < kWriteHeads; ++j) {
+      if (j >= ch) break;
+      const int h = hb + G * j;
+      float xa[VEC], xb[VEC];
+      unpack<VEC>(a[j], xa);
+      unpack<VEC>(b[j], xb);
+      if (h < HR) {
+        float ya[VEC], yb[VEC];
+        if constexpr (IL) {
 #pragma unroll
-  for (int j = 0; j < kWriteHeads; ++j) {
-    if (j >= ch) break;
-    const int h = hb + G * j;
-    float xa[VEC], xb[VEC];
-    unpack<VEC>(a[j], xa);
-    unpack<VEC>(b[j], xb);
-    if (h < HR) {
-      float ya[VEC], yb[VEC];
-      if constexpr (IL) {
+          for (int e = 0; e < VEC; e += 2) {
+            const float2 f = cs[e / 2], f2 = cs[VEC / 2 + e / 2];
+            ya[e] = xa[e] * f.x - xa[e + 1] * f.y;
+            ya[e + 1] = xa[e + 1] * f.x + xa[e] * f.y;
+            yb[e] = xb[e] * f2.x - xb[e + 1] * f2.y;
+            yb[e + 1] = xb[e + 1] * f2.x + xb[e] * f2.y;
+          }
+        } else {
 #pragma unroll
-        for (int e = 0; e < VEC; e += 2) {
-          const float2 f = cs[e / 2], f2 = cs[VEC / 2 + e / 2];
-          ya[e] = xa[e] * f.x - xa[e + 1] * f.y;
-          ya[e + 1] = xa[e + 1] * f.x + xa[e] * f.y;
-          yb[e] = xb[e] * f2.x - xb[e + 1] * f2.y;
-          yb[e + 1] = xb[e + 1] * f2.x + xb[e] * f2.y;
+          for (int e = 0; e < VEC; ++e) {
+            ya[e] = xa[e] * cs[e].x - xb[e] * cs[e].y;
+            yb[e] = xb[e] * cs[e].x + xa[e] * cs[e].y;
+          }
         }
-      } else {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          ya[e] = xa[e] * cs[e].x - xb[e] * cs[e].y;
-          yb[e] = xb[e] * cs[e].x + xa[e] * cs[e].y;
+          xa[e] = ya[e];
+          xb[e] = yb[e];
         }
       }
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        xa[e] = ya[e];
-        xb[e] = yb[e];
+      if (h < A.Hq && on) {
+        T* dst = qo + h * A.D;
+        st_vec(dst, pack<T, VEC>(xa));
+        st_vec(dst + half, pack<T, VEC>(xb));
       }
-    }
-    const bool kv = h >= A.Hq && h < HT && page >= 0;
-    if (h < A.Hq && on) {
-      T* dst = A.qo + t * A.ldqo + (int64_t)h * A.D;
-      st_vec(dst + ia, pack<T, VEC>(xa));
-      st_vec(dst + ib, pack<T, VEC>(xb));
-    }
-    if (__any_sync(0xffffffffu, kv)) {  // a warp's head rows may be both Q and K
-      uint32_t m = on ? max(abs_max_bits<VEC>(xa), abs_max_bits<VEC>(xb)) : 0u;
-      for (int o = lanes >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (kv && on) {
-        const float am = q8_amax(m), inv = q8_inv<FMT>(am);
-        const bool isk = h < HR;
-        const int hk = h - (isk ? A.Hq : HR);
-        uint8_t* dst = (isk ? A.K.q : A.V.q) + (isk ? A.K.cq.at(page, off, hk) : A.V.cq.at(page, off, hk));
-        q8_store<FMT, VEC>(xa, inv, dst + ia);
-        q8_store<FMT, VEC>(xb, inv, dst + ib);
-        if (v == 0) {
-          float* sc = isk ? A.K.sc + A.K.cs.at(page, off, hk) : A.V.sc + A.V.cs.at(page, off, hk);
-          *sc = q8_scale<FMT>(am, m);
+      const bool kv = h >= A.Hq && h < HT && page >= 0;
+      if (__any_sync(0xffffffffu, kv)) {  // a warp's head rows may be both Q and K
+        uint32_t m = on ? max(abs_max_bits<VEC>(xa), abs_max_bits<VEC>(xb)) : 0u;
+        for (int o = lanes >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        // even lanes divide for 1 / scale, odd ones for the scale
+        const float am = q8_amax(m);
+        const bool odd = (lane & 1) != 0;
+        const float d = __fdiv_rn(odd ? am : Q8Max<FMT>::v, odd ? Q8Max<FMT>::v : am);
+        float inv = __shfl_sync(0xffffffffu, d, lane & ~1);
+        float scale = d;
+        if (lanes == 1) {  // a head per lane: both divisions are its own
+          inv = q8_inv<FMT>(am);
+          scale = __fdiv_rn(am, Q8Max<FMT>::v);
+        }
+        if (kv && on) {
+          const bool isk = h < HR;
+          const int hk = h - (isk ? A.Hq : HR);
+          uint8_t* dst = (isk ? A.K.q : A.V.q) + (isk ? A.K.cq.at(page, off, hk) : A.V.cq.at(page, off, hk)) + ia;
+          q8_store<FMT, VEC>(xa, inv, dst);
+          q8_store<FMT, VEC>(xb, inv, dst + half);
+          if (v == (lanes == 1 ? 0 : 1)) {
+            float* sc = isk ? A.K.sc + A.K.cs.at(page, off, hk) : A.V.sc + A.V.cs.at(page, off, hk);
+            *sc = m < kInfBits ? scale : __int_as_float(0x7fc00000);
+          }
         }
       }
     }
@@ -256,10 +289,14 @@ __global__ void __launch_bounds__(256) cache8_write_elem(const WriteArgs<T> A) {
 }
 
 // ---------------------------------------------------------------------------
-// Read-back: a warp per token.  A unit is N consecutive codes of one head: on the
-// vector path as many as fill a 16-byte store (8 codes at bf16, 4 at float32), so
-// that a warp's loads and its stores are both contiguous.  The lanes walk the
-// token's units of K, then of V.
+// Read-back: a warp per token, then the next one (the slot of which it has
+// loaded by then).  A unit is N consecutive codes of one head: on the vector path
+// as many as fill a 16-byte store (8 codes at bf16, 4 at float32), so that a
+// warp's loads and its stores are both contiguous.  A head takes a power of two of
+// lanes, which spares the units a division; four heads per lane of K and of V are
+// in flight, in one block of code without branches (with a branch per load the
+// INT8 form waited 40% longer).  66 us for 65536 tokens of 8 heads of 128, 60 us
+// at the copy rate; two heads per lane at five blocks per SM 79, eight at two 76.
 // ---------------------------------------------------------------------------
 template <typename T>
 struct ReadArgs {
@@ -273,50 +310,64 @@ struct ReadArgs {
   unsigned int* err;
 };
 
+constexpr int kReadHeads = 4;
+constexpr int kReadGrid = 3;  // blocks per SM, all resident
+
 template <typename T, int FMT, int N>
-__global__ void __launch_bounds__(256) cache8_read_kernel(const ReadArgs<T> A) {
-  constexpr int U = 8;  // units in flight per lane
+__global__ void __launch_bounds__(256) cache8_read_kernel(const ReadArgs<T> A, int per, int lg) {
+  constexpr int U = kReadHeads;
   const int lane = threadIdx.x & 31;
-  const int64_t t = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
+  int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= A.rows) return;  // uniform per warp
-  int64_t off = 0;
-  const int64_t page = A.S.page_of(__ldg(A.S.slots + t), off);
-  if (page == -2 && lane == 0) atomicOr(A.err, kErrBadSlot);
-  const int per = A.D / N, half = A.Hk * per;
-  const float fill = page == -2 ? __int_as_float(0x7fc00000) : 0.f;  // no slot: zeros
-  const uint8_t *kq = nullptr, *vq = nullptr;
-  const float *ks = nullptr, *vs = nullptr;
-  if (page >= 0) {
-    kq = A.K.q + A.K.cq.at(page, off, 0);
-    vq = A.V.q + A.V.cq.at(page, off, 0);
-    ks = A.K.sc + A.K.cs.at(page, off, 0);
-    vs = A.V.sc + A.V.cs.at(page, off, 0);
-  }
-  T *ko = A.ko + t * A.ldk, *vo = A.vo + t * A.ldv;
-  for (int u0 = lane; u0 < 2 * half; u0 += 32 * U) {
-    Codes<FMT, N> w[U];
-    float sc[U];
+  const int lanes = 1 << lg, G = 32 >> lg;
+  const int d0 = lane & (lanes - 1), hb = lane >> lg;
+  int64_t off = 0, page = A.S.page_of(__ldg(A.S.slots + t), off);
+#pragma unroll 1
+  for (; t < A.rows; t += step) {
+    const bool more = t + step < A.rows;
+    const int64_t next = more ? __ldg(A.S.slots + t + step) : -1;
+    T *ko = A.ko + t * A.ldk, *vo = A.vo + t * A.ldv;
+    if (page >= 0) {
+      const uint8_t *kq = A.K.q + A.K.cq.at(page, off, 0), *vq = A.V.q + A.V.cq.at(page, off, 0);
+      const float *ks = A.K.sc + A.K.cs.at(page, off, 0), *vs = A.V.sc + A.V.cs.at(page, off, 0);
+      for (int d = d0; d < per; d += lanes) {  // once, for heads of up to 32 units
+        for (int h0 = hb; h0 < A.Hk; h0 += U * G) {
+          Codes<FMT, N> kw[U], vw[U];
+          float kc[U], vc[U];
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int u = u0 + 32 * k;
-      const bool isk = u < half;
-      const int r = isk ? u : u - half;
-      const int h = r / per;
-      w[k].zero();
-      sc[k] = fill;
-      if (u < 2 * half && page >= 0) {
-        w[k].load((isk ? kq + (int64_t)h * A.K.cq.head : vq + (int64_t)h * A.V.cq.head) + (r - h * per) * N);
-        sc[k] = __ldg(isk ? ks + (int64_t)h * A.K.cs.head : vs + (int64_t)h * A.V.cs.head);
+          for (int j = 0; j < U; ++j) {
+            const int h = min(h0 + j * G, A.Hk - 1);  // past the last head: that one again, not stored
+            kw[j].load(kq + h * A.K.cq.head + d * N);
+            vw[j].load(vq + h * A.V.cq.head + d * N);
+            kc[j] = __ldg(ks + h * A.K.cs.head);
+            vc[j] = __ldg(vs + h * A.V.cs.head);
+          }
+#pragma unroll
+          for (int j = 0; j < U; ++j) {
+            const int h = h0 + j * G;
+            if (h < A.Hk) {
+              float v[N];
+              kw[j].get(v, kc[j]);
+              store_n<T, N>(ko + h * A.D + d * N, v);
+              vw[j].get(v, vc[j]);
+              store_n<T, N>(vo + h * A.D + d * N, v);
+            }
+          }
+        }
       }
-    }
+    } else {  // no slot: zeros; a slot outside the cache: NaN
+      if (page == -2 && lane == 0) atomicOr(A.err, kErrBadSlot);
+      float fill[N];
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int u = u0 + 32 * k;
-      if (u >= 2 * half) break;
-      float v[N];
-      w[k].get(v, sc[k]);  // no slot: 0 * fill is 0 or NaN
-      store_n<T, N>(u < half ? ko + (int64_t)u * N : vo + (int64_t)(u - half) * N, v);
+      for (int e = 0; e < N; ++e) fill[e] = page == -2 ? __int_as_float(0x7fc00000) : 0.f;
+      for (int d = d0; d < per; d += lanes)
+        for (int h = hb; h < A.Hk; h += G) {
+          store_n<T, N>(ko + h * A.D + d * N, fill);
+          store_n<T, N>(vo + h * A.D + d * N, fill);
+        }
     }
+    page = A.S.page_of(next, off);
   }
 }
 
@@ -382,14 +433,18 @@ gbln_status write_launch(const WriteArgs<T>& A, bool cache_aligned, cudaStream_t
                    (A.Hq == 0 || (row16(A.q, A.ldq) && row16(A.qo, A.ldqo))) && row16(A.k, A.ldk) && row16(A.v, A.ldv);
   if (vec) {
     const int nu = A.D / (2 * VEC);
-    int lanes = 1;
-    while (lanes < nu) lanes *= 2;
-    const int G = 32 / lanes, L = (HT + G - 1) / G;  // head rows per lane and token
+    int lg = 0;
+    while ((1 << lg) < nu) ++lg;
+    const int G = 32 >> lg, L = (HT + G - 1) / G;  // head rows per lane and token
     const int nchunk = (L + kWriteHeads - 1) / kWriteHeads;
     const int ch = (L + nchunk - 1) / nchunk;
-    const int64_t blocks = (A.rows * nchunk + 7) / 8;  // 8 warps per block
-    if (blocks <= 0x7fffffffLL) {
-      cache8_write_vec<T, IL, FMT><<<(unsigned)blocks, 256, 0, s>>>(A, nu, lanes, nchunk, ch);
+    const int cy = nchunk < kWriteWarps ? nchunk : kWriteWarps, tz = kWriteWarps / cy;
+    const int sms = sm_count();
+    if (sms <= 0) return GBLN_ERR_CUDA;
+    const int64_t gy = (nchunk + cy - 1) / cy;
+    if (gy <= 65535) {
+      const unsigned gx = grid_for(A.rows, tz, (int64_t)sms * kWriteGrid);
+      cache8_write_vec<T, IL, FMT><<<dim3(gx, (unsigned)gy), dim3(32, cy, tz), 0, s>>>(A, nu, lg, ch);
       return launch_status();
     }
   }
@@ -411,8 +466,13 @@ gbln_status read_typed(const ReadArgs<T>& A, int fmt, bool cache_aligned, cudaSt
   constexpr int VEC = VecOf<T>::N;
   const bool vec = A.D % VEC == 0 && cache_aligned && aligned16(A.ko) && aligned16(A.vo) &&
                    (A.ldk * (int64_t)sizeof(T)) % 16 == 0 && (A.ldv * (int64_t)sizeof(T)) % 16 == 0;
-  const int64_t blocks = (A.rows + 7) / 8;  // at most 2^30 for kMaxTokens
-#define GBLN_READ8(FMT, N) cache8_read_kernel<T, FMT, N><<<(unsigned)blocks, 256, 0, s>>>(A)
+  const int sms = sm_count();
+  if (sms <= 0) return GBLN_ERR_CUDA;
+  const unsigned grid = grid_for(A.rows, 8, (int64_t)sms * kReadGrid);
+  const int per = A.D / (vec ? VEC : 1);  // units per head
+  int lg = 0;
+  while (lg < 5 && (1 << lg) < per) ++lg;
+#define GBLN_READ8(FMT, N) cache8_read_kernel<T, FMT, N><<<grid, 256, 0, s>>>(A, per, lg)
   if (fmt == GBLN_Q8_INT8) {
     if (vec) GBLN_READ8(GBLN_Q8_INT8, VEC);
     else GBLN_READ8(GBLN_Q8_INT8, 1);

@@ -586,9 +586,12 @@ glu_fwd_row8_elem(const T* gate, const T* up, uint8_t* q, float* sc, int64_t row
   if constexpr (FITS) {
 #pragma unroll
     for (int k = 0; k < kRow8Runs; ++k)
+      if (const int j = (int)j0 + k * nw * 128; j < I) {
+        const uint32_t c = q8_code4<FMT>(o[k][0], o[k][1], o[k][2], o[k][3], inv);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (const int j = (int)j0 + k * nw * 128 + 32 * e; j < I) qr[j] = (uint8_t)q8_code1<FMT>(o[k][e], inv);
+        for (int e = 0; e < 4; ++e)
+          if (j + 32 * e < I) qr[j + 32 * e] = (uint8_t)(c >> (8 * e));
+      }
   } else {
     for (int64_t j = threadIdx.x; j < I; j += blockDim.x)
       qr[j] = (uint8_t)q8_code1<FMT>(act_f<T, ACT>(to_f32(gr[j])) * to_f32(ur[j]), inv);
@@ -623,6 +626,12 @@ struct GluCkptIn {
 
 constexpr int kCkptRows = 4;
 
+// u / n of unit numbers, which fit 32 bits in all but absurd sizes (a 64-bit
+// division takes as long as a dozen values).
+__device__ __forceinline__ int64_t unit_div(int64_t u, int64_t n, bool small) {
+  return small ? (int64_t)((uint32_t)u / (uint32_t)n) : u / n;
+}
+
 template <typename T, int ACT, int FMT>
 __global__ void __launch_bounds__(kGluBlock)
 glu_fwd_ckpt(const T* gate, const T* up, T* out, const GluCkpt C, int64_t T_, int64_t ncol, int64_t ldg,
@@ -635,8 +644,9 @@ glu_fwd_ckpt(const T* gate, const T* up, T* out, const GluCkpt C, int64_t T_, in
   const int cb = blockDim.x, lane = threadIdx.x & 31;
   const int64_t ncb = (ncol + cb - 1) / cb;
   const int64_t units = (T_ + U - 1) / U * ncb;
+  const bool small = units <= 0xffffffffLL;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int64_t rg = u / ncb;
+    const int64_t rg = unit_div(u, ncb, small);
     const int64_t c = (u - rg * ncb) * cb + threadIdx.x;
     const bool on = c < ncol;
     const int64_t r0 = rg * U;
@@ -716,9 +726,10 @@ __device__ __forceinline__ void store_run(T* p, int rem, const float (&v)[4]) {
 }
 template <bool FULL, int FMT>
 __device__ __forceinline__ void store_run_codes(uint8_t* p, int rem, const float (&v)[4], float inv) {
+  const uint32_t q = q8_code4<FMT>(v[0], v[1], v[2], v[3], inv);
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-    if (FULL || 32 * e < rem) p[32 * e] = (uint8_t)q8_code1<FMT>(v[e], inv);
+    if (FULL || 32 * e < rem) p[32 * e] = (uint8_t)(q >> (8 * e));
 }
 
 constexpr int kElemFlight = 2;
@@ -730,13 +741,14 @@ glu_fwd_ckpt_elem(const T* gate, const T* up, T* out, const GluCkpt C, int64_t T
   constexpr int F = kElemFlight;
   const int lane = threadIdx.x & 31;
   const int64_t ng = (I + kCkptGroup - 1) / kCkptGroup, n = T_ * ng;
+  const bool small = n + F <= 0xffffffffLL;
   const int64_t step = (int64_t)gridDim.x * (kGluBlock / 32) * F;
   for (int64_t u = ((int64_t)blockIdx.x * (kGluBlock / 32) + (threadIdx.x >> 5)) * F; u < n; u += step) {
     T g[F][4], v[F][4];
     int64_t row[F], j0[F];
 #pragma unroll
     for (int f = 0; f < F; ++f) {
-      row[f] = (u + f) / ng;
+      row[f] = unit_div(u + f, ng, small);
       j0[f] = (u + f - row[f] * ng) * kCkptGroup + lane;
       if (u + f >= n) continue;
       const T *gp = gate + row[f] * ldg + j0[f], *up_ = up + row[f] * ldu + j0[f];
@@ -749,23 +761,34 @@ glu_fwd_ckpt_elem(const T* gate, const T* up, T* out, const GluCkpt C, int64_t T
         load_run<false>(up_, rem, v[f]);
       }
     }
+    // Maxima of the F groups of gate and of up; lane 4 f + 2 (up) divides for that
+    // group's 1 / scale, the lane after it for the scale.
+    uint32_t gm[F], um[F];
 #pragma unroll
     for (int f = 0; f < F; ++f) {
-      if (u + f >= n) break;  // uniform per warp
-      float gf[4], uf[4], o[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        gf[e] = to_f32(g[f][e]);
-        uf[e] = to_f32(v[f][e]);
+      if (u + f >= n) {
+        gm[f] = um[f] = 0;
+        continue;  // uniform per warp
       }
+      const float gf[4] = {to_f32(g[f][0]), to_f32(g[f][1]), to_f32(g[f][2]), to_f32(g[f][3])};
+      const float uf[4] = {to_f32(v[f][0]), to_f32(v[f][1]), to_f32(v[f][2]), to_f32(v[f][3])};
+      gm[f] = group_max<32>(abs_max_bits<4>(gf));
+      um[f] = group_max<32>(abs_max_bits<4>(uf));
+    }
+    static_assert(F == 2, "one lane bit names a group");
+    const uint32_t mine = lane & 4 ? (lane & 2 ? um[1] : gm[1]) : (lane & 2 ? um[0] : gm[0]);
+    const float a = q8_amax(mine);
+    const float d = __fdiv_rn(lane & 1 ? a : Q8Max<FMT>::v, lane & 1 ? Q8Max<FMT>::v : a);
+    if (lane < 8 && (lane & 1) && u + (lane >> 2) < n)
+      (lane & 2 ? C.us : C.gs)[u + (lane >> 2)] = mine < kInfBits ? d : __int_as_float(0x7fc00000);
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      const float gi = __shfl_sync(0xffffffffu, d, 4 * f), ui = __shfl_sync(0xffffffffu, d, 4 * f + 2);
+      if (u + f >= n) break;  // uniform per warp
+      const float gf[4] = {to_f32(g[f][0]), to_f32(g[f][1]), to_f32(g[f][2]), to_f32(g[f][3])};
+      const float uf[4] = {to_f32(v[f][0]), to_f32(v[f][1]), to_f32(v[f][2]), to_f32(v[f][3])};
+      float o[4];
       glu_values<T, ACT, 4>(gf, uf, o);
-      const uint32_t gm = group_max<32>(abs_max_bits<4>(gf)), um = group_max<32>(abs_max_bits<4>(uf));
-      // even lanes divide for 1 / scale, odd ones for the scale; lanes 2 and 3 of up
-      const uint32_t mine = lane & 2 ? um : gm;
-      const float a = q8_amax(mine);
-      const float d = __fdiv_rn(lane & 1 ? a : Q8Max<FMT>::v, lane & 1 ? Q8Max<FMT>::v : a);
-      const float gi = __shfl_sync(0xffffffffu, d, 0), ui = __shfl_sync(0xffffffffu, d, 2);
-      if (lane == 1 || lane == 3) (lane == 1 ? C.gs : C.us)[u + f] = mine < kInfBits ? d : __int_as_float(0x7fc00000);
       const int rem = (int)(I - j0[f] < kCkptGroup ? I - j0[f] : (int64_t)kCkptGroup);
       T* op = out + row[f] * ldo + j0[f];
       uint8_t *gq = C.gq + row[f] * I + j0[f], *uq = C.uq + row[f] * I + j0[f];
@@ -796,8 +819,9 @@ glu_bwd_ckpt(const T* dout, const GluCkptIn C, T* dgate, T* dup, int64_t T_, int
   const int cb = blockDim.x;
   const int64_t ncb = (ncol + cb - 1) / cb;
   const int64_t units = (T_ + UNROLL - 1) / UNROLL * ncb;
+  const bool small = units <= 0xffffffffLL;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int64_t rg = u / ncb;
+    const int64_t rg = unit_div(u, ncb, small);
     const int64_t c = (u - rg * ncb) * cb + threadIdx.x;
     if (c >= ncol) continue;
     const int64_t r0 = rg * UNROLL;
@@ -843,6 +867,7 @@ glu_bwd_ckpt_elem(const T* dout, const GluCkptIn C, T* dgate, T* dup, int64_t T_
   constexpr int F = kElemFlight;
   const int lane = threadIdx.x & 31;
   const int64_t ng = (I + kCkptGroup - 1) / kCkptGroup, n = T_ * ng;
+  const bool small = n + F <= 0xffffffffLL;
   const int64_t step = (int64_t)gridDim.x * (kGluBlock / 32) * F;
   for (int64_t u = ((int64_t)blockIdx.x * (kGluBlock / 32) + (threadIdx.x >> 5)) * F; u < n; u += step) {
     T d[F][4];
@@ -851,7 +876,7 @@ glu_bwd_ckpt_elem(const T* dout, const GluCkptIn C, T* dgate, T* dup, int64_t T_
     int64_t row[F], j0[F];
 #pragma unroll
     for (int f = 0; f < F; ++f) {
-      row[f] = (u + f) / ng;
+      row[f] = unit_div(u + f, ng, small);
       j0[f] = (u + f - row[f] * ng) * kCkptGroup + lane;
       if (u + f >= n) continue;
       const T* dp = dout + row[f] * ldd + j0[f];

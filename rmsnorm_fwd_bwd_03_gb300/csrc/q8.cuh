@@ -59,12 +59,22 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 // orders finite < infinity < NaN, so a NaN is never lost.
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
+// max(|a|, |b|, |c|) in one instruction; a NaN wins.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 template <int N>
 __device__ __forceinline__ uint32_t abs_max_bits(const float (&v)[N]) {
-  uint32_t m = 0;
+  if constexpr (N == 1) {
+    return abs_bits(v[0]);
+  } else {
+    float m = max3_abs(v[0], v[1], v[N > 2 ? 2 : 1]);
 #pragma unroll
-  for (int e = 0; e < N; ++e) m = max(m, abs_bits(v[e]));
-  return m;
+    for (int e = 3; e < N; e += 2) m = max3_abs(m, v[e], v[e + 1 < N ? e + 1 : e]);
+    return __float_as_uint(m);
+  }
 }
 
 // Maximum over groups of W consecutive lanes; every lane gets it.
@@ -213,6 +223,11 @@ struct Codes {
     }
   }
 };
+
+// Ask for the line at p (any alignment) in L2 ahead of use.
+__device__ __forceinline__ void prefetch_line(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 
 inline bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 

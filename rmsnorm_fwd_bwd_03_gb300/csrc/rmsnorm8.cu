@@ -209,16 +209,25 @@ __device__ __forceinline__ void load_chunk(const uint8_t* p, int rem, uint8_t (&
   for (int m = 0; m < 4; ++m) v[m] = FULL || 32 * m < rem ? p[32 * m] : (uint8_t)0;
 }
 template <bool FULL, typename T>
-__device__ __forceinline__ void store_chunk(T* p, int rem, const float (&v)[4]) {
+__device__ __forceinline__ void store_chunk(T* p, int rem, const float2 (&v)[2]) {
+  const float f[4] = {v[0].x, v[0].y, v[1].x, v[1].y};
 #pragma unroll
   for (int m = 0; m < 4; ++m)
-    if (FULL || 32 * m < rem) p[32 * m] = from_f32<T>(v[m]);
+    if (FULL || 32 * m < rem) p[32 * m] = from_f32<T>(f[m]);
 }
 template <bool FULL, int FMT>
-__device__ __forceinline__ void store_codes(uint8_t* p, int rem, const float (&v)[4], float inv) {
+__device__ __forceinline__ void store_codes(uint8_t* p, int rem, const float2 (&v)[2], float inv) {
+  const uint32_t q = q8_code4<FMT>(v[0].x, v[0].y, v[1].x, v[1].y, inv);
 #pragma unroll
   for (int m = 0; m < 4; ++m)
-    if (FULL || 32 * m < rem) p[32 * m] = (uint8_t)q8_code1<FMT>(v[m], inv);
+    if (FULL || 32 * m < rem) p[32 * m] = (uint8_t)(q >> (8 * m));
+}
+// Round to T and back.
+template <typename T>
+__device__ __forceinline__ float2 round2(float2 v) {
+  if constexpr (sizeof(T) == 4) return v;
+  const uint32_t w = pack_bf16x2(v.x, v.y);
+  return make_float2(bf16_lo(w), bf16_hi(w));
 }
 // Run f(true_type) for a whole chunk, f(false_type) for a row's last, shorter one.
 struct FullChunk { static constexpr bool v = true; };
@@ -250,34 +259,53 @@ __global__ void __launch_bounds__(1024) rms8_fwd_elem(const Fwd8<T, W> A, int NW
       load_chunk<decltype(full)::v>(A.x + at + k * cs, rem, xr[k]);
       if constexpr (RES) load_chunk<decltype(full)::v>(A.r + at + k * cs, rem, rr[k]);
     });
-  float h[kElemChunks][4];
-  float ss = 0.f;
-  uint32_t am = 0;
+  float2 h[kElemChunks][2];  // values l and l + 32, l + 64 and l + 96
+  float2 sq = both(0.f);
+  uint32_t am = 0, cm[kElemChunks];
 #pragma unroll
-  for (int k = 0; k < kElemChunks; ++k)
+  for (int k = 0; k < kElemChunks; ++k) {
+    cm[k] = 0;
     chunk_of(c0 + k * cs, H, [&](auto full) {
       constexpr bool FULL = decltype(full)::v;
       const int rem = H - (c0 + k * cs) - lane;
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        h[k][m] = to_f32(xr[k][m]);
-        if constexpr (RES) h[k][m] = to_f32(from_f32<T>(h[k][m] + to_f32(rr[k][m])));
-        ss = fmaf(h[k][m], h[k][m], ss);
+      h[k][0] = make_float2(to_f32(xr[k][0]), to_f32(xr[k][1]));
+      h[k][1] = make_float2(to_f32(xr[k][2]), to_f32(xr[k][3]));
+      if constexpr (RES) {
+        h[k][0] = round2<T>(add2(h[k][0], make_float2(to_f32(rr[k][0]), to_f32(rr[k][1]))));
+        h[k][1] = round2<T>(add2(h[k][1], make_float2(to_f32(rr[k][2]), to_f32(rr[k][3]))));
+        store_chunk<FULL>(A.hout + at + k * cs, rem, h[k]);
       }
-      if constexpr (RES) store_chunk<FULL>(A.hout + at + k * cs, rem, h[k]);
+      sq = fma2(h[k][0], h[k][0], fma2(h[k][1], h[k][1], sq));
       if constexpr (MODE == kRowE4m3) {
         W w[4];
         load_chunk<FULL>(A.w + c0 + k * cs + lane, rem, w);
-#pragma unroll
-        for (int m = 0; m < 4; ++m) am = max(am, abs_bits(__fmul_rn(to_f32(w[m]), h[k][m])));
+        const float2 u = mul2(make_float2(to_f32(w[0]), to_f32(w[1])), h[k][0]);
+        const float2 v = mul2(make_float2(to_f32(w[2]), to_f32(w[3])), h[k][1]);
+        am = max(am, __float_as_uint(max3_abs(max3_abs(u.x, u.y, v.x), v.y, v.y)));
       } else {
-        const uint32_t gm = group_max<32>(abs_max_bits<4>(h[k]));
-        const float a = q8_amax(gm);
-        store_codes<FULL, FMT>(A.q + at + k * cs, rem, h[k], q8_inv<FMT>(a));
-        if (lane == 0) A.sc[(size_t)row * A.ng + wi + k * NW] = q8_scale<FMT>(a, gm);
+        cm[k] = group_max<32>(__float_as_uint(
+            max3_abs(max3_abs(h[k][0].x, h[k][0].y, h[k][1].x), h[k][1].y, h[k][1].y)));
       }
     });
-  ss = group_sum<32>(ss);
+  }
+  if constexpr (MODE != kRowE4m3) {
+    // Lanes 2 k and 2 k + 1 divide for chunk k's 1 / scale and scale: one division
+    // per lane instead of two per chunk.
+    static_assert(kElemChunks == 4, "two lane bits name a chunk");
+    const uint32_t mine = lane & 4 ? (lane & 2 ? cm[3] : cm[2]) : (lane & 2 ? cm[1] : cm[0]);
+    const float a = q8_amax(mine);
+    const float d = __fdiv_rn(lane & 1 ? a : Q8Max<FMT>::v, lane & 1 ? Q8Max<FMT>::v : a);
+    if (lane < 8 && (lane & 1) && c0 + (lane >> 1) * cs < H)
+      A.sc[(size_t)row * A.ng + wi + (lane >> 1) * NW] = mine < kInfBits ? d : __int_as_float(0x7fc00000);
+#pragma unroll
+    for (int k = 0; k < kElemChunks; ++k) {
+      const float inv = __shfl_sync(0xffffffffu, d, 2 * k);
+      chunk_of(c0 + k * cs, H, [&](auto full) {
+        store_codes<decltype(full)::v, FMT>(A.q + at + k * cs, H - (c0 + k * cs) - lane, h[k], inv);
+      });
+    }
+  }
+  float ss = group_sum<32>(sq.x + sq.y);
   if constexpr (MODE == kRowE4m3) am = group_max<32>(am);
   if (NW > 1) {
     if (lane == 0) {
@@ -306,15 +334,13 @@ __global__ void __launch_bounds__(1024) rms8_fwd_elem(const Fwd8<T, W> A, int NW
       const int rem = H - (c0 + k * cs) - lane;
       W w[4];
       load_chunk<FULL>(A.w + c0 + k * cs + lane, rem, w);
-      float o[4];
+      const float2 w0 = make_float2(to_f32(w[0]), to_f32(w[1])), w1 = make_float2(to_f32(w[2]), to_f32(w[3]));
       if (MODE != kRowE4m3 || A.y) {
-#pragma unroll
-        for (int m = 0; m < 4; ++m) o[m] = to_f32(w[m]) * (h[k][m] * rs);
+        const float2 o[2] = {mul2(w0, mul2(h[k][0], both(rs))), mul2(w1, mul2(h[k][1], both(rs)))};
         store_chunk<FULL>(A.y + at + k * cs, rem, o);
       }
       if constexpr (MODE == kRowE4m3) {
-#pragma unroll
-        for (int m = 0; m < 4; ++m) o[m] = __fmul_rn(to_f32(w[m]), h[k][m]);
+        const float2 o[2] = {mul2(w0, h[k][0]), mul2(w1, h[k][1])};
         store_codes<FULL, FMT>(A.q + at + k * cs, rem, o, inv);
       }
     });
@@ -356,7 +382,8 @@ __global__ void __launch_bounds__(kWideBlock) rms8_fwd_wide(const Fwd8<T, W> A) 
     if constexpr (MODE != kRowE4m3) {
       const uint32_t gm = group_max<32>(abs_max_bits<4>(h));
       const float a = q8_amax(gm);
-      store_codes<false, FMT>(A.q + base + c0 + lane, A.H - c0 - lane, h, q8_inv<FMT>(a));
+      const float2 hp[2] = {make_float2(h[0], h[1]), make_float2(h[2], h[3])};
+      store_codes<false, FMT>(A.q + base + c0 + lane, A.H - c0 - lane, hp, q8_inv<FMT>(a));
       if (lane == 0) A.sc[(size_t)row * A.ng + c0 / kCkptGroup] = q8_scale<FMT>(a, gm);
     }
   }
@@ -519,13 +546,17 @@ __global__ void __launch_bounds__(TPR * GPB) rms8_bwd_vec(const Bwd8<T, W> A, bo
 }
 
 // ---------------------------------------------------------------------------
-// Backward, element path: chunks of 128 values per warp as in rms8_fwd_elem.  The
-// row's inputs stay in registers as loaded, the dW sums in float32; n is rebuilt
-// from the codes for each use.
+// Backward, element path: chunks of 128 values per warp as in rms8_fwd_elem, two
+// per warp: with their weights, dW sums and inputs they fill 64 registers, and
+// 1024 threads per SM are resident.  The warp asks for its next row in L2 while
+// it works on this one.
 // ---------------------------------------------------------------------------
+constexpr int kElemBwdChunks = 2;
+
 template <typename T, typename W, bool DRES, int FMT, int BLOCK>
-__global__ void __launch_bounds__(BLOCK, 768 / BLOCK) rms8_bwd_elem(const Bwd8<T, W> A, int NW) {
-  constexpr int C = kElemChunks;
+__global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) rms8_bwd_elem(const Bwd8<T, W> A, int NW) {
+  constexpr int C = kElemBwdChunks;
+  constexpr int LINE = 128 / sizeof(T);
   extern __shared__ float sacc[];  // several row groups: one row of dW sums
   __shared__ float red[2][BLOCK / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -535,50 +566,64 @@ __global__ void __launch_bounds__(BLOCK, 768 / BLOCK) rms8_bwd_elem(const Bwd8<T
   const int64_t P = gridDim.x, p = blockIdx.x;
   const int64_t r0 = p * A.rows / P, r1 = (p + 1) * A.rows / P;
   const int c0 = wi * kCkptGroup, cs = NW * kCkptGroup;
-  const W* wp = A.w + c0 + lane;
 
-  float acc[C][4];
+  float2 acc[C][2], w[C][2];
 #pragma unroll
-  for (int k = 0; k < C; ++k)
-#pragma unroll
-    for (int m = 0; m < 4; ++m) acc[k][m] = 0.f;
+  for (int k = 0; k < C; ++k) {
+    acc[k][0] = acc[k][1] = w[k][0] = w[k][1] = both(0.f);
+    chunk_of(c0 + k * cs, H, [&](auto full) {
+      W v[4];
+      load_chunk<decltype(full)::v>(A.w + c0 + k * cs + lane, H - (c0 + k * cs) - lane, v);
+      w[k][0] = make_float2(to_f32(v[0]), to_f32(v[1]));
+      w[k][1] = make_float2(to_f32(v[2]), to_f32(v[3]));
+    });
+  }
 
   int par = 0;
   for (int64_t row = r0 + g; row < r1; row += GPB) {
-    const size_t at = (size_t)row * H + c0 + lane;
+    const size_t base = (size_t)row * H, at = base + c0 + lane;
     T dy[C][4], dr[C][4];
-    uint32_t q[C];
-    float sc[C];
+    float2 n[C][2];
+    const float rs = __ldg(A.rstd + row);
 #pragma unroll
     for (int k = 0; k < C; ++k)
       chunk_of(c0 + k * cs, H, [&](auto full) {
         constexpr bool FULL = decltype(full)::v;
         const int rem = H - (c0 + k * cs) - lane;
-        uint8_t b[4];
         load_chunk<FULL>(A.dy + at + k * cs, rem, dy[k]);
-        load_chunk<FULL>(A.hq + at + k * cs, rem, b);
         if constexpr (DRES) load_chunk<FULL>(A.dres + at + k * cs, rem, dr[k]);
-        sc[k] = __ldg(A.hs + (size_t)row * A.ng + wi + k * NW);
-        q[k] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
       });
-    const float rs = __ldg(A.rstd + row);
-    float dot = 0.f;
 #pragma unroll
     for (int k = 0; k < C; ++k)
       chunk_of(c0 + k * cs, H, [&](auto full) {
-        W w[4];
-        load_chunk<decltype(full)::v>(wp + k * cs, H - (c0 + k * cs) - lane, w);
-        float n[4];
-        q8_decode4<FMT>(q[k], n);
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          n[m] = __fmul_rn(n[m], sc[k]) * rs;
-          const float d = to_f32(dy[k][m]);
-          dot = fmaf(d * to_f32(w[m]), n[m], dot);
-          acc[k][m] = fmaf(d, n[m], acc[k][m]);
-        }
+        const int rem = H - (c0 + k * cs) - lane;
+        uint8_t b[4];
+        load_chunk<decltype(full)::v>(A.hq + at + k * cs, rem, b);
+        const float sc = __ldg(A.hs + (size_t)row * A.ng + wi + k * NW);
+        float v[4];
+        q8_decode4<FMT>(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410), v);
+        n[k][0] = mul2(mul2(make_float2(v[0], v[1]), both(sc)), both(rs));
+        n[k][1] = mul2(mul2(make_float2(v[2], v[3]), both(sc)), both(rs));
       });
-    dot = group_sum<32>(dot);
+    if (row + GPB < r1) {
+      const size_t nb = base + (size_t)GPB * H;
+      for (int j = wi * 32 * LINE + lane * LINE; j < H; j += NW * 32 * LINE) {
+        prefetch_line(A.dy + nb + j);
+        if constexpr (DRES) prefetch_line(A.dres + nb + j);
+      }
+      for (int j = (wi * 32 + lane) * 128; j < H; j += NW * 32 * 128) prefetch_line(A.hq + nb + j);
+    }
+    float2 dot2 = both(0.f);
+#pragma unroll
+    for (int k = 0; k < C; ++k)
+      if (c0 + k * cs < H) {
+        const float2 d0 = make_float2(to_f32(dy[k][0]), to_f32(dy[k][1]));
+        const float2 d1 = make_float2(to_f32(dy[k][2]), to_f32(dy[k][3]));
+        dot2 = fma2(mul2(d0, w[k][0]), n[k][0], fma2(mul2(d1, w[k][1]), n[k][1], dot2));
+        acc[k][0] = fma2(d0, n[k][0], acc[k][0]);
+        acc[k][1] = fma2(d1, n[k][1], acc[k][1]);
+      }
+    float dot = group_sum<32>(dot2.x + dot2.y);
     if (NW > 1) {  // double-buffered as in rms8_bwd_vec
       if (lane == 0) red[par][warp] = dot;
       bar_sync_named(1 + g, 32 * NW);
@@ -586,23 +631,19 @@ __global__ void __launch_bounds__(BLOCK, 768 / BLOCK) rms8_bwd_elem(const Bwd8<T
       for (int i = 0; i < NW; ++i) dot += red[par][g * NW + i];
       par ^= 1;
     }
-    const float cc = dot * A.inv_H;
+    const float2 mc = both(-dot * A.inv_H);
 #pragma unroll
     for (int k = 0; k < C; ++k)
       chunk_of(c0 + k * cs, H, [&](auto full) {
-        constexpr bool FULL = decltype(full)::v;
         const int rem = H - (c0 + k * cs) - lane;
-        W w[4];
-        load_chunk<FULL>(wp + k * cs, rem, w);
-        float n[4], o[4];
-        q8_decode4<FMT>(q[k], n);
+        float2 o[2];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          n[m] = __fmul_rn(n[m], sc[k]) * rs;
-          o[m] = rs * (to_f32(dy[k][m]) * to_f32(w[m]) - n[m] * cc);
-          if constexpr (DRES) o[m] += to_f32(dr[k][m]);
+        for (int i = 0; i < 2; ++i) {
+          const float2 d = make_float2(to_f32(dy[k][2 * i]), to_f32(dy[k][2 * i + 1]));
+          o[i] = mul2(both(rs), fma2(n[k][i], mc, mul2(d, w[k][i])));
+          if constexpr (DRES) o[i] = add2(o[i], make_float2(to_f32(dr[k][2 * i]), to_f32(dr[k][2 * i + 1])));
         }
-        store_chunk<FULL>(A.dx + at + k * cs, rem, o);
+        store_chunk<decltype(full)::v>(A.dx + at + k * cs, rem, o);
       });
   }
 
@@ -611,15 +652,17 @@ __global__ void __launch_bounds__(BLOCK, 768 / BLOCK) rms8_bwd_elem(const Bwd8<T
   for (int t = 0; t < GPB; ++t) {  // groups add in order
     if (t == g) {
 #pragma unroll
-      for (int k = 0; k < C; ++k)
+      for (int k = 0; k < C; ++k) {
+        const float a[4] = {acc[k][0].x, acc[k][0].y, acc[k][1].x, acc[k][1].y};
 #pragma unroll
         for (int m = 0; m < 4; ++m)
           if (c0 + k * cs + 32 * m + lane < H) {
             const int j = k * cs + 32 * m;
-            const float v = t == 0 ? acc[k][m] : srow[j] + acc[k][m];
+            const float v = t == 0 ? a[m] : srow[j] + a[m];
             if (t == GPB - 1) prow[j] = v;
             else srow[j] = v;
           }
+      }
     }
     __syncthreads();
   }
@@ -666,20 +709,19 @@ constexpr int64_t kMaxH = 1 << 24;
 constexpr int64_t kMaxRows = (1LL << 31) - 1;
 constexpr int64_t kMaxVecPerRow = 2048;  // 512 threads x 4 vectors
 
-// Element path: warps per row (a power of two) so that a warp holds at most
-// kElemChunks chunks; beyond 32 warps (16 in the backward, which holds twice as
-// much per value) the row does not fit the registers.
+// Element path: warps per row (a power of two up to 32) so that a warp holds at
+// most `chunks` chunks; wider rows do not fit the registers.
 struct Elem {
   bool fits;
   int nw;      // warps per row
   int block;   // threads
   int groups;  // rows per block and pass
 };
-Elem elem_geometry(int64_t H, int most_warps) {
+Elem elem_geometry(int64_t H, int chunks) {
   const int64_t nchunk = (H + kCkptGroup - 1) / kCkptGroup;
-  if (nchunk > most_warps * kElemChunks) return {false, kWideBlock / 32, kWideBlock, 1};
+  if (nchunk > 32 * chunks) return {false, kWideBlock / 32, kWideBlock, 1};
   int nw = 1;
-  while ((int64_t)nw * kElemChunks < nchunk) nw *= 2;
+  while ((int64_t)nw * chunks < nchunk) nw *= 2;
   const int block = nw < 8 ? 256 : nw * 32;
   return {true, nw, block, block / (nw * 32)};
 }
@@ -694,8 +736,8 @@ struct BwdGeometry {
 };
 BwdGeometry bwd_geometry(int64_t H, size_t io) {
   if (!vec_width(H, io)) {
-    const Elem e = elem_geometry(H, 16);
-    return {0, 0, e.groups, e.fits ? 768 / e.block : 2};
+    const Elem e = elem_geometry(H, kElemBwdChunks);
+    return {0, 0, e.groups, e.fits ? 1024 / e.block : 2};
   }
   const int64_t nvec = H * (int64_t)io / 16;
   if (nvec <= 32) return {32, 1, 8, 4};
@@ -720,7 +762,7 @@ gbln_status fwd_launch(const Fwd8<T, W>& A, cudaStream_t s) {
   const bool vec = vec_width(A.H, sizeof(T)) && aligned16(A.x) && aligned16(A.w) && aligned16(A.y) &&
                    (!RES || (aligned16(A.r) && aligned16(A.hout))) && aligned_to(A.q, VEC);
   if (!vec) {
-    const Elem e = elem_geometry(A.H, 32);
+    const Elem e = elem_geometry(A.H, kElemChunks);
     const int64_t blocks = (A.rows + e.groups - 1) / e.groups;
     if (e.fits) rms8_fwd_elem<T, W, RES, MODE><<<(unsigned)blocks, e.block, 0, s>>>(A, e.nw);
     else rms8_fwd_wide<T, W, RES, MODE><<<(unsigned)A.rows, kWideBlock, 0, s>>>(A);
@@ -756,10 +798,11 @@ gbln_status bwd_launch(const Bwd8<T, W>& A, int64_t P, cudaStream_t s) {
                    (!DRES || aligned16(A.dres)) && aligned_to(A.hq, VEC);
   const unsigned grid = (unsigned)P;
   if (!vec) {
-    const Elem e = elem_geometry(A.H, 16);
-    const size_t smem = e.groups > 1 ? (size_t)A.H * sizeof(float) : 0;  // at most 2048 values
+    const Elem e = elem_geometry(A.H, kElemBwdChunks);
+    const size_t smem = e.groups > 1 ? (size_t)A.H * sizeof(float) : 0;  // at most 1024 values
     if (e.fits && e.block == 256) rms8_bwd_elem<T, W, DRES, FMT, 256><<<grid, 256, smem, s>>>(A, e.nw);
-    else if (e.fits) rms8_bwd_elem<T, W, DRES, FMT, 512><<<grid, 512, 0, s>>>(A, e.nw);
+    else if (e.fits && e.block == 512) rms8_bwd_elem<T, W, DRES, FMT, 512><<<grid, 512, 0, s>>>(A, e.nw);
+    else if (e.fits) rms8_bwd_elem<T, W, DRES, FMT, 1024><<<grid, 1024, 0, s>>>(A, e.nw);
     else rms8_bwd_wide<T, W, DRES, FMT><<<grid, kWideBlock, 0, s>>>(A);
     return launch_status();
   }
