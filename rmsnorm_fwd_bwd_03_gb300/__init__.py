@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -56,6 +57,9 @@ class _Cache8(ctypes.Structure):
         "scale_page_stride", "scale_slot_stride", "scale_head_stride")]
 
 
+_pack_cache8 = struct.Struct("=2Q8q").pack  # the same bytes, without an object per field
+
+
 # name -> (restype, argtypes); mirrors include/gbln.h
 _SIGNATURES = {
     "gbln_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -92,8 +96,8 @@ _SIGNATURES = {
     "gbln_rmsnorm_bwd_ckpt8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp]),
     "gbln_glu_fwd_ckpt8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp]),
     "gbln_glu_bwd_ckpt8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp]),
-    "gbln_rope_fwd_cache8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, ctypes.POINTER(_Cache8), ctypes.POINTER(_Cache8), _i64, _i32, _i32, _i32, _i64, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp]),
-    "gbln_cache8_read": (ctypes.c_int, [_vp, ctypes.POINTER(_Cache8), ctypes.POINTER(_Cache8), _vp, _vp, _i64, _i32, _i32, _i64, _i64, ctypes.c_int, ctypes.c_int, _vp]),
+    "gbln_rope_fwd_cache8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i64, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp]),
+    "gbln_cache8_read": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i64, _i64, ctypes.c_int, ctypes.c_int, _vp]),
 }
 
 _lib = None
@@ -213,7 +217,7 @@ def _vec(t, n, name, dtype=None):
         return
     if t.numel() != n:
         raise ValueError(f"{name} must hold {n} elements, not {t.numel()}")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
 
 
@@ -447,7 +451,7 @@ def rope_table(max_pos: int, D: int, theta: float, device=None, out=None):
 
 
 def _table(cos_sin, D):
-    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 3 or cos_sin.shape[1:] != (D // 2, 2):
+    if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 3 or cos_sin.shape[1:] != (D // 2, 2):
         raise ValueError(f"cos_sin must be float32 [max_pos, {D // 2}, 2], not {cos_sin.dtype} {tuple(cos_sin.shape)}")
 
 
@@ -693,6 +697,19 @@ def act_bwd(dy, x, act="silu", dx=None):
 # is the format); value = code * scale.
 # ---------------------------------------------------------------------------
 
+def _here(t, name):
+    """t's device index: t is a CUDA tensor on the current device."""
+    _on_device(t, name)
+    return t.get_device()
+
+
+def _ptr(t, dev, name):
+    """Address of a contiguous tensor on device dev, the current one."""
+    if t.get_device() != dev or not t.is_contiguous():
+        return _dev(t, name)  # says what is wrong
+    return t.data_ptr()
+
+
 def _code_dtype(fmt):
     try:
         return _CODE_DTYPE[fmt]
@@ -713,12 +730,29 @@ def _groups(n):
 
 def _ckpt(codes, scale, shape, name):
     """The format of a checkpoint of a tensor of that shape."""
-    if tuple(codes.shape) != tuple(shape):
+    if codes.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(codes.shape)}")
-    want = tuple(shape[:-1]) + (_groups(shape[-1]),)
-    if tuple(scale.shape) != want or scale.dtype != torch.float32:
-        raise ValueError(f"{name}_scale must be float32 {want}, not {scale.dtype} {tuple(scale.shape)}")
+    if scale.dtype is not torch.float32 or scale.shape != (*shape[:-1], _groups(shape[-1])):
+        raise ValueError(f"{name}_scale must be float32 {(*shape[:-1], _groups(shape[-1]))}, "
+                         f"not {scale.dtype} {tuple(scale.shape)}")
     return _code_fmt(codes, name)
+
+
+def _norm_in(x, weight, residual, residual_out):
+    """Checks of a norm's forward inputs: (rows' shape, T, H, the device, their addresses)."""
+    shape = x.shape
+    H = shape[-1]
+    _like(residual, x, "residual", "x")
+    _like(residual_out if residual is not None else None, x, "residual_out", "x")
+    _vec(weight, H, "weight")
+    dev = _here(x, "x")
+    if residual is None:
+        r = ro = None
+    else:
+        residual_out = torch.empty_like(x) if residual_out is None else residual_out
+        r, ro = _ptr(residual, dev, "residual"), _ptr(residual_out, dev, "residual_out")
+    return (shape[:-1], x.numel() // H if H else 0, H, dev, _ptr(x, dev, "x"), r, _ptr(weight, dev, "weight"), ro,
+            x if residual is None else residual_out)
 
 
 def rmsnorm_fwd_fp8(x, weight, eps, residual=None, *, want_y=True, residual_out=None):
@@ -727,24 +761,15 @@ def rmsnorm_fwd_fp8(x, weight, eps, residual=None, *, want_y=True, residual_out=
     y_e4m3: float8_e4m3fn of x's shape; y_scale: float32, one per row; y (x's dtype) is
     None unless ``want_y``.
     """
-    H = x.shape[-1]
-    T = x.numel() // H if H else 0
-    _like(residual, x, "residual", "x")
-    _like(residual_out if residual is not None else None, x, "residual_out", "x")
-    _vec(weight, H, "weight")
+    rows, T, H, dev, xp, rp, wp, hp, h = _norm_in(x, weight, residual, residual_out)
     y = torch.empty_like(x) if want_y else None
-    q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-    sc = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(x)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    st = library().gbln_rmsnorm_fwd_fp8(
-        _dev(x, "x"), _opt(residual, "residual"), _dev(weight, "weight"), _opt(y, "y"),
-        q.data_ptr(), sc.data_ptr(),
-        _opt(residual_out, "residual_out") if residual is not None else None, rstd.data_ptr(),
-        T, H, float(eps), _io(x), _io(weight), _stream(x))
+    q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+    sc = torch.empty(rows, dtype=torch.float32, device=x.device)
+    rstd = torch.empty_like(sc)
+    st = library().gbln_rmsnorm_fwd_fp8(xp, rp, wp, y.data_ptr() if want_y else None, q.data_ptr(), sc.data_ptr(), hp,
+                                        rstd.data_ptr(), T, H, float(eps), _io(x), _io(weight), _raw_stream(dev))
     _check("gbln_rmsnorm_fwd_fp8", st)
-    return y, q, sc, (residual_out if residual is not None else x), rstd
+    return y, q, sc, h, rstd
 
 
 def glu_fwd_fp8(gate, up, act="silu"):
@@ -767,55 +792,49 @@ def rmsnorm_fwd_ckpt8(x, weight, eps, residual=None, *, fmt="int8", y=None, resi
     "int8" or "e4m3").  Returns ``(y, h, rstd, h8, h8_scale)``: h8 of x's shape (int8 or
     float8_e4m3fn), h8_scale float32 with one scale per 128 values of a row.  The backward
     pass, :func:`rmsnorm_bwd_ckpt8`, needs h8, h8_scale and rstd, not h."""
-    H = x.shape[-1]
-    T = x.numel() // H if H else 0
-    _like(residual, x, "residual", "x")
+    code = _code_dtype(fmt)
     _like(y, x, "y", "x")
-    _like(residual_out if residual is not None else None, x, "residual_out", "x")
-    _vec(weight, H, "weight")
-    h8 = torch.empty(x.shape, dtype=_code_dtype(fmt), device=x.device)
-    sc = torch.empty(x.shape[:-1] + (_groups(H),), dtype=torch.float32, device=x.device)
-    if y is None:
-        y = torch.empty_like(x)
-    if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(x)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    st = library().gbln_rmsnorm_fwd_ckpt8(
-        _dev(x, "x"), _opt(residual, "residual"), _dev(weight, "weight"), _dev(y, "y"),
-        _opt(residual_out, "residual_out") if residual is not None else None, rstd.data_ptr(),
-        h8.data_ptr(), sc.data_ptr(), T, H, float(eps), Q8[fmt], _io(x), _io(weight), _stream(x))
+    rows, T, H, dev, xp, rp, wp, hp, h = _norm_in(x, weight, residual, residual_out)
+    y = torch.empty_like(x) if y is None else y
+    h8 = torch.empty_like(x, dtype=code)
+    sc = torch.empty((*rows, _groups(H)), dtype=torch.float32, device=x.device)
+    rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+    st = library().gbln_rmsnorm_fwd_ckpt8(xp, rp, wp, _ptr(y, dev, "y"), hp, rstd.data_ptr(), h8.data_ptr(),
+                                          sc.data_ptr(), T, H, float(eps), Q8[fmt], _io(x), _io(weight), _raw_stream(dev))
     _check("gbln_rmsnorm_fwd_ckpt8", st)
-    return y, (residual_out if residual is not None else x), rstd, h8, sc
+    return y, h, rstd, h8, sc
 
 
 def rmsnorm_bwd_ckpt8_num_partials(T: int, H: int, dtype=torch.bfloat16) -> int:
     """``gbln_rmsnorm_bwd_ckpt8_num_partials``: rows P of the [P, H] float32 dW workspace."""
-    P = library().gbln_rmsnorm_bwd_ckpt8_num_partials(int(T), int(H), _DTYPE[dtype])
+    P = library().gbln_rmsnorm_bwd_ckpt8_num_partials(T, H, _DTYPE[dtype])
     if P < 0:
         raise GblnError("gbln_rmsnorm_bwd_ckpt8_num_partials", 1)
-    return int(P)
+    return P
 
 
 def rmsnorm_bwd_ckpt8(dy, h8, h8_scale, weight, rstd, dresidual_out=None, *, dx=None, dw_partial=None):
     """``gbln_rmsnorm_bwd_ckpt8``: :func:`rmsnorm_bwd` with h read from its 8-bit checkpoint.
     Returns ``(dx, dw_partial, P)``; finish dW with :func:`rmsnorm_dw_finalize`."""
-    H = dy.shape[-1]
+    shape = dy.shape
+    H = shape[-1]
     T = dy.numel() // H if H else 0
-    fmt = _ckpt(h8, h8_scale, dy.shape, "h8")
+    fmt = _ckpt(h8, h8_scale, shape, "h8")
     _like(dresidual_out, dy, "dresidual_out", "dy")
     _like(dx, dy, "dx", "dy")
     _vec(weight, H, "weight")
     _vec(rstd, T, "rstd", torch.float32)
     _rows_f32(dw_partial, H, "dw_partial")
+    dev = _here(dy, "dy")
     P = rmsnorm_bwd_ckpt8_num_partials(T, H, dy.dtype)
-    if dx is None:
-        dx = torch.empty_like(dy)
+    dx = torch.empty_like(dy) if dx is None else dx
     if dw_partial is None:
-        dw_partial = torch.empty((max(P, 1), H), dtype=torch.float32, device=dy.device)
+        dw_partial = torch.empty((P or 1, H), dtype=torch.float32, device=dy.device)
     st = library().gbln_rmsnorm_bwd_ckpt8(
-        _dev(dy, "dy"), _opt(dresidual_out, "dresidual_out"), _dev(h8, "h8"), _dev(h8_scale, "h8_scale"),
-        _dev(weight, "weight"), _dev(rstd, "rstd"), _dev(dx, "dx"), _dev(dw_partial, "dw_partial"),
-        dw_partial.shape[0], T, H, fmt, _io(dy), _io(weight), _stream(dy))
+        _ptr(dy, dev, "dy"), None if dresidual_out is None else _ptr(dresidual_out, dev, "dresidual_out"),
+        _ptr(h8, dev, "h8"), _ptr(h8_scale, dev, "h8_scale"), _ptr(weight, dev, "weight"), _ptr(rstd, dev, "rstd"),
+        _ptr(dx, dev, "dx"), _ptr(dw_partial, dev, "dw_partial"), dw_partial.shape[0], T, H, fmt, _io(dy), _io(weight),
+        _raw_stream(dev))
     _check("gbln_rmsnorm_bwd_ckpt8", st)
     return dx, dw_partial, P
 
@@ -824,16 +843,19 @@ def glu_fwd_ckpt8(gate, up, act="silu", *, fmt="int8", out=None):
     """``gbln_glu_fwd_ckpt8``: :func:`glu_fwd` that also saves gate and up in 8 bits (``fmt``
     "int8" or "e4m3").  Returns ``(out, gate8, gate_scale, up8, up_scale)``: codes [T, I] and
     float32 scales [T, ceil(I / 128)], contiguous."""
+    code = _code_dtype(fmt)
     _like(up, gate, "up", "gate")
     _like(out, gate, "out", "gate")
     T, I, ldg = _rows2d(gate, "gate")
     _, _, ldu = _rows2d(up, "up")
-    dt = _code_dtype(fmt)
-    gq, uq = (torch.empty((T, I), dtype=dt, device=gate.device) for _ in range(2))
-    gs, us = (torch.empty((T, _groups(I)), dtype=torch.float32, device=gate.device) for _ in range(2))
+    device = gate.device
+    gq = torch.empty((T, I), dtype=code, device=device)
+    gs = torch.empty((T, _groups(I)), dtype=torch.float32, device=device)
+    uq, us = torch.empty_like(gq), torch.empty_like(gs)
     if out is None:
-        out = torch.empty((T, I), dtype=gate.dtype, device=gate.device)
-    _, _, ldo = _rows2d(out, "out")
+        out, ldo = torch.empty((T, I), dtype=gate.dtype, device=device), I
+    else:
+        _, _, ldo = _rows2d(out, "out")
     st = library().gbln_glu_fwd_ckpt8(gate.data_ptr(), up.data_ptr(), out.data_ptr(), gq.data_ptr(),
                                       gs.data_ptr(), uq.data_ptr(), us.data_ptr(), T, I, ldg, ldu, ldo,
                                       ACT[act], Q8[fmt], _io(gate), _stream(gate))
@@ -844,43 +866,54 @@ def glu_fwd_ckpt8(gate, up, act="silu", *, fmt="int8", out=None):
 def glu_bwd_ckpt8(dout, gate8, gate_scale, up8, up_scale, act="silu", dgate=None, dup=None):
     """``gbln_glu_bwd_ckpt8``: :func:`glu_bwd` with gate and up read from their 8-bit
     checkpoints.  Returns ``(dgate, dup)``, which may be views of one [T, 2I] tensor."""
-    if dout.dim() != 2:
+    shape = dout.shape
+    if len(shape) != 2:
         raise ValueError("dout must be [T, I]")
-    fmt = _ckpt(gate8, gate_scale, dout.shape, "gate8")
-    if _ckpt(up8, up_scale, dout.shape, "up8") != fmt:
+    fmt = _ckpt(gate8, gate_scale, shape, "gate8")
+    if _ckpt(up8, up_scale, shape, "up8") != fmt:
         raise TypeError("gate8 and up8 must have the same dtype")
     _like(dgate, dout, "dgate", "dout")
     _like(dup, dout, "dup", "dout")
     T, I, ldd = _rows2d(dout, "dout")
+    dev = dout.get_device()  # _rows2d has seen that it is the current one
     if dgate is None:
-        dgate = torch.empty((T, I), dtype=dout.dtype, device=dout.device)
+        dgate, lddg = torch.empty((T, I), dtype=dout.dtype, device=dout.device), I
+    else:
+        _, _, lddg = _rows2d(dgate, "dgate")
     if dup is None:
-        dup = torch.empty((T, I), dtype=dout.dtype, device=dout.device)
-    _, _, lddg = _rows2d(dgate, "dgate")
-    _, _, lddu = _rows2d(dup, "dup")
-    st = library().gbln_glu_bwd_ckpt8(dout.data_ptr(), _dev(gate8, "gate8"), _dev(gate_scale, "gate_scale"),
-                                      _dev(up8, "up8"), _dev(up_scale, "up_scale"), dgate.data_ptr(),
+        dup, lddu = torch.empty((T, I), dtype=dout.dtype, device=dout.device), I
+    else:
+        _, _, lddu = _rows2d(dup, "dup")
+    st = library().gbln_glu_bwd_ckpt8(dout.data_ptr(), _ptr(gate8, dev, "gate8"), _ptr(gate_scale, dev, "gate_scale"),
+                                      _ptr(up8, dev, "up8"), _ptr(up_scale, dev, "up_scale"), dgate.data_ptr(),
                                       dup.data_ptr(), T, I, ldd, lddg, lddu, ACT[act], fmt, _io(dout),
-                                      _stream(dout))
+                                      _raw_stream(dev))
     _check("gbln_glu_bwd_ckpt8", st)
     return dgate, dup
 
 
 def _cache8(codes, scale, Hk, D, name):
-    """``gbln_cache8`` of codes [pages, page_size, Hk, D] and scales [pages, page_size, Hk], each
-    with any page, slot and head strides; and its format."""
-    fmt = _code_fmt(codes, f"{name}_cache")
-    shape = codes.shape
-    if len(shape) != 4 or shape[1] < 1 or shape[2:] != (Hk, D):
+    """The bytes of ``gbln_cache8`` for codes [pages, page_size, Hk, D] and scales [pages, page_size,
+    Hk], each with any page, slot and head strides."""
+    shape, stride = codes.shape, codes.stride()
+    if len(shape) != 4 or shape[1] < 1 or shape[2] != Hk or shape[3] != D:
         raise ValueError(f"{name}_cache must be [pages, page_size, {Hk}, {D}], not {tuple(shape)}")
     if scale.dtype is not torch.float32 or scale.shape != shape[:3]:
         raise ValueError(f"{name}_scale must be float32 {tuple(shape[:3])}, not {scale.dtype} {tuple(scale.shape)}")
-    stride = codes.stride()
     if D > 1 and stride[3] != 1:
         raise ValueError(f"{name}_cache must hold the {D} values of a head next to one another")
     _on_device(codes, f"{name}_cache")
     _on_device(scale, f"{name}_scale")
-    return _Cache8(codes.data_ptr(), scale.data_ptr(), *shape[:2], *stride[:3], *scale.stride()), fmt
+    return _pack_cache8(codes.data_ptr(), scale.data_ptr(), shape[0], shape[1], stride[0], stride[1], stride[2],
+                        *scale.stride())
+
+
+def _caches8(k_cache, k_scale, v_cache, v_scale, Hk, D):
+    """``gbln_cache8`` of K and of V, and their format."""
+    fmt = _code_fmt(k_cache, "k_cache")
+    if v_cache.dtype is not k_cache.dtype or v_cache.shape != k_cache.shape:
+        raise ValueError("v_cache must have k_cache's shape and dtype")
+    return _cache8(k_cache, k_scale, Hk, D, "k"), _cache8(v_cache, v_scale, Hk, D, "v"), fmt
 
 
 def rope_fwd_cache8(q, k, v, positions, cos_sin, slots, k_cache, k_scale, v_cache, v_scale, *,
@@ -892,31 +925,34 @@ def rope_fwd_cache8(q, k, v, positions, cos_sin, slots, k_cache, k_scale, v_cach
     ``s % page_size`` of page ``s // page_size``.  q, k and v may have strided token rows (slices of
     one packed QKV tensor).  Returns ``q_out`` (pass ``q_out=q`` to rotate in place)."""
     T, Hk, D, ldk = _heads(k, "k")
-    Tq, Hq, Dq, ldq = _heads(q, "q")
     Tv, Hv, Dv, ldv = _heads(v, "v")
-    if (Tv, Hv, Dv) != (T, Hk, D) or v.dtype != k.dtype:
+    if (Tv, Hv, Dv) != (T, Hk, D) or v.dtype is not k.dtype:
         raise ValueError("v must have k's shape and dtype")
-    if q is not None and (Tq != T or Dq != D or q.dtype != k.dtype):
-        raise ValueError("q must be [T, Hq, D] with k's T, D and dtype")
-    if q is None and q_out is not None:
+    if q is not None:
+        Tq, Hq, Dq, ldq = _heads(q, "q")
+        if Tq != T or Dq != D or q.dtype is not k.dtype:
+            raise ValueError("q must be [T, Hq, D] with k's T, D and dtype")
+        if q_out is None:
+            q_out, ldqo = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device), Hq * D
+        else:
+            if q_out.shape != q.shape or q_out.dtype is not q.dtype:
+                raise ValueError(f"q_out must have the shape {tuple(q.shape)} and dtype {q.dtype}")
+            ldqo = _heads(q_out, "q_out")[3]
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
         raise ValueError("q_out without q")
-    if q_out is not None and (q_out.shape != q.shape or q_out.dtype != q.dtype):
-        raise ValueError(f"q_out must have the shape {tuple(q.shape)} and dtype {q.dtype}")
+    else:
+        Hq = ldq = ldqo = 0
+        qp = qop = None
     _vec(positions, T, "positions", torch.int32)
     _vec(slots, T, "slots", torch.int64)
     _table(cos_sin, D)
-    kc, fmt = _cache8(k_cache, k_scale, Hk, D, "k")
-    vc, vfmt = _cache8(v_cache, v_scale, Hk, D, "v")
-    if vfmt != fmt or v_cache.shape != k_cache.shape:
-        raise ValueError("v_cache must have k_cache's shape and dtype")
-    if q is not None and q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-    _, _, _, ldqo = _heads(q_out, "q_out")
+    kc, vc, fmt = _caches8(k_cache, k_scale, v_cache, v_scale, Hk, D)
+    dev = k.get_device()  # _heads has seen that it is the current one
     st = library().gbln_rope_fwd_cache8(
-        None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
-        None if q is None else q_out.data_ptr(), _dev(positions, "positions"), _dev(cos_sin, "cos_sin"),
-        cos_sin.shape[0], _dev(slots, "slots"), ctypes.byref(kc), ctypes.byref(vc), T, Hq, Hk, D,
-        ldq, ldk, ldv, ldqo, PAIRING[pairing], fmt, _io(k), _stream(k))
+        qp, k.data_ptr(), v.data_ptr(), qop, _ptr(positions, dev, "positions"), _ptr(cos_sin, dev, "cos_sin"),
+        cos_sin.shape[0], _ptr(slots, dev, "slots"), kc, vc, T, Hq, Hk, D, ldq, ldk, ldv, ldqo, PAIRING[pairing], fmt,
+        _io(k), _raw_stream(dev))
     _check("gbln_rope_fwd_cache8", st)
     return q_out
 
@@ -931,19 +967,20 @@ def cache8_read(slots, k_cache, k_scale, v_cache, v_scale, *, dtype=torch.bfloat
     N = slots.numel()
     _vec(slots, N, "slots", torch.int64)
     for o, n in ((k_out, "k_out"), (v_out, "v_out")):
-        if o is not None and (tuple(o.shape) != (N, Hk, D) or o.dtype != dtype):
+        if o is not None and (o.shape != (N, Hk, D) or o.dtype is not dtype):
             raise ValueError(f"{n} must have the shape {(N, Hk, D)} and dtype {dtype}")
-    kc, fmt = _cache8(k_cache, k_scale, Hk, D, "k")
-    vc, vfmt = _cache8(v_cache, v_scale, Hk, D, "v")
-    if vfmt != fmt or v_cache.shape != k_cache.shape:
-        raise ValueError("v_cache must have k_cache's shape and dtype")
+    kc, vc, fmt = _caches8(k_cache, k_scale, v_cache, v_scale, Hk, D)
+    dev = _here(slots, "slots")
+    ldk = ldv = Hk * D
     if k_out is None:
         k_out = torch.empty((N, Hk, D), dtype=dtype, device=slots.device)
+    else:
+        ldk = _heads(k_out, "k_out")[3]
     if v_out is None:
         v_out = torch.empty((N, Hk, D), dtype=dtype, device=slots.device)
-    _, _, _, ldk = _heads(k_out, "k_out")
-    _, _, _, ldv = _heads(v_out, "v_out")
-    st = library().gbln_cache8_read(_dev(slots, "slots"), ctypes.byref(kc), ctypes.byref(vc), k_out.data_ptr(),
-                                    v_out.data_ptr(), N, Hk, D, ldk, ldv, fmt, _io(k_out), _stream(slots))
+    else:
+        ldv = _heads(v_out, "v_out")[3]
+    st = library().gbln_cache8_read(_ptr(slots, dev, "slots"), kc, vc, k_out.data_ptr(), v_out.data_ptr(), N, Hk, D,
+                                    ldk, ldv, fmt, _io(k_out), _raw_stream(dev))
     _check("gbln_cache8_read", st)
     return k_out, v_out
