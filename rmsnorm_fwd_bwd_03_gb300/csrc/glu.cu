@@ -18,6 +18,8 @@
 // projection, and save gate and up as 8-bit checkpoints (one float32 scale per
 // 128 values of a row) that a backward pass reads.
 
+#include <atomic>
+
 #include <cooperative_groups.h>
 
 #include "q8.cuh"
@@ -453,8 +455,7 @@ __device__ __forceinline__ void glu_values(const float (&g)[N], const float (&u)
 // vectors per thread): gate and up are read once.  TPR threads per row and
 // block: several rows per block when TPR is a warp; one row per block beyond;
 // one row per cluster of CL blocks for rows beyond 1024 threads' registers, whose
-// maxima meet through distributed shared memory (a pair of 512-thread blocks is
-// no faster than one block of 1024: 536 against 493 us at 16383 x 28672).
+// maxima meet through distributed shared memory.
 // ---------------------------------------------------------------------------
 template <typename T, int ACT, int TPR, int VPT, int RPB, int CL>
 __device__ __forceinline__ void glu_row8(const T* gate, const T* up, uint8_t* q, float* sc, int64_t rows,
@@ -526,6 +527,123 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(512)
 glu_fwd_row8_cluster(const T* gate, const T* up, uint8_t* q, float* sc, int64_t rows, int I, int64_t ldg,
                      int64_t ldu) {
   glu_row8<T, ACT, 512, 4, 1, CL>(gate, up, q, sc, rows, I, ldg, ldu);
+}
+
+// ---------------------------------------------------------------------------
+// Row-scaled output for many rows of 2049 to 4096 vectors (bf16: up to 32768
+// values).  One such row fills an SM's registers while it waits for its maximum,
+// so no second block covers the wait with loads of its own.  Here a persistent
+// block keeps HBM busy itself: a producer warp streams gate and up of this row
+// and the next through a ring of shared-memory stages (TMA bulk copies, 512
+// vectors of each per stage), and 512 consumer threads turn a stage into float32
+// outputs in registers, meet once per row for the maximum, and store the codes.
+// 16383 x 28672 bf16: 331 us (346 us at the copy rate; this pass mostly reads),
+// with a block of 1024 threads per row 497 us.
+// ---------------------------------------------------------------------------
+constexpr int kRingThreads = 512;                             // consumers
+constexpr int kRingStages = 12;                               // 16 KB each
+constexpr int kRingBytes = kRingThreads * 16;                 // of gate, and of up, per stage
+constexpr int kRingVpt = 8;                                   // stages per row, at most
+
+struct RingBarriers {
+  uint64_t full[kRingStages], empty[kRingStages];
+  uint32_t maxima[2][kRingThreads / 32];
+};
+constexpr size_t kRingSmem = (size_t)kRingStages * 2 * kRingBytes + sizeof(RingBarriers);
+
+template <typename T, int ACT>
+__global__ void __launch_bounds__(kRingThreads + 32, 1)
+glu_fwd_row8_ring(const T* gate, const T* up, uint8_t* q, float* sc, int64_t rows, int I, int64_t ldg,
+                  int64_t ldu, unsigned int* err) {
+  constexpr int VEC = VecOf<T>::N;
+  constexpr int FMT = GBLN_Q8_E4M3;
+  extern __shared__ __align__(128) unsigned char ring[];
+  RingBarriers& B = *reinterpret_cast<RingBarriers*>(ring + (size_t)kRingStages * 2 * kRingBytes);
+  const int nvec = I / VEC, per = (nvec + kRingThreads - 1) / kRingThreads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kRingStages; ++s) {
+      mbar_init(&B.full[s], 1);
+      mbar_init(&B.empty[s], kRingThreads / 32);
+    }
+    mbar_init_fence();
+  }
+  __syncthreads();
+
+  if (warp == kRingThreads / 32) {  // producer: one thread
+    if (lane != 0) return;
+    int stage = 0;
+    uint32_t round = 0;  // times the ring has been filled
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+      for (int v = 0; v < per; ++v) {
+        if (round > 0 && !mbar_wait(&B.empty[stage], (round - 1) & 1, kWaitPolls)) {
+          atomicOr(err, kErrWaitTimeout);
+          row = rows;  // nothing more is issued
+          break;
+        }
+        const int n = nvec - v * kRingThreads < kRingThreads ? nvec - v * kRingThreads : kRingThreads;
+        unsigned char* dst = ring + (size_t)stage * 2 * kRingBytes;
+        const int64_t at = (int64_t)v * kRingThreads * VEC;
+        mbar_arrive_expect_tx(&B.full[stage], (uint32_t)n * 32);
+        bulk_load(dst, gate + row * ldg + at, (uint32_t)n * 16, &B.full[stage]);
+        bulk_load(dst + kRingBytes, up + row * ldu + at, (uint32_t)n * 16, &B.full[stage]);
+        if (++stage == kRingStages) {
+          stage = 0;
+          ++round;
+        }
+      }
+    }
+    // The block's memory outlives its copies: wait for those still in flight.
+    for (int s = 0; s < kRingStages; ++s) {
+      const uint32_t fills = round + (s < stage ? 1 : 0);
+      if (fills > 0 && !mbar_wait(&B.full[s], (fills - 1) & 1, kWaitPolls)) atomicOr(err, kErrWaitTimeout);
+    }
+    return;
+  }
+
+  int stage = 0;
+  uint32_t phase = 0;
+  int par = 0;
+  bool good = true;  // false: a wait ran out, results are void, nothing waits any more
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, par ^= 1) {
+    float o[kRingVpt][VEC];
+    uint32_t m = 0;
+#pragma unroll
+    for (int v = 0; v < kRingVpt; ++v) {
+      if (v < per) {
+        if (good && !mbar_wait(&B.full[stage], phase, kWaitPolls)) {
+          good = false;
+          atomicOr(err, kErrWaitTimeout);
+        }
+        const unsigned char* src = ring + (size_t)stage * 2 * kRingBytes + (size_t)threadIdx.x * 16;
+        const uint4 ga = ld_shared_v4(src), ua = ld_shared_v4(src + kRingBytes);
+        float g[VEC], u[VEC];
+        unpack<VEC>(ga, g);
+        unpack<VEC>(ua, u);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.empty[stage]);
+        if (++stage == kRingStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+        glu_values<T, ACT, VEC>(g, u, o[v]);
+        if (v * kRingThreads + (int)threadIdx.x < nvec) m = max(m, abs_max_bits<VEC>(o[v]));
+      }
+    }
+    m = group_max<32>(m);
+    if (lane == 0) B.maxima[par][warp] = m;
+    // a buffer is written again two rows later, past the next barrier
+    bar_sync_named(1, kRingThreads);
+#pragma unroll
+    for (int i = 0; i < kRingThreads / 32; ++i) m = max(m, B.maxima[par][i]);
+    const float a = q8_amax(m), inv = q8_inv<FMT>(a);
+    if (threadIdx.x == 0) sc[row] = q8_scale<FMT>(a, m);
+#pragma unroll
+    for (int v = 0; v < kRingVpt; ++v) {
+      const int iv = v * kRingThreads + threadIdx.x;
+      if (v < per && iv < nvec) q8_store<FMT, VEC>(o[v], inv, q + row * I + (int64_t)iv * VEC);
+    }
+  }
 }
 
 // The same for any alignment and width.  A warp takes runs of 128 values, lane l
@@ -633,7 +751,7 @@ __device__ __forceinline__ int64_t unit_div(int64_t u, int64_t n, bool small) {
 }
 
 template <typename T, int ACT, int FMT>
-__global__ void __launch_bounds__(kGluBlock)
+__global__ void __launch_bounds__(kGluBlock, 3)
 glu_fwd_ckpt(const T* gate, const T* up, T* out, const GluCkpt C, int64_t T_, int64_t ncol, int64_t ldg,
              int64_t ldu, int64_t ldo) {
   constexpr int VEC = VecOf<T>::N;
@@ -1053,11 +1171,34 @@ void act_bwd_launch(const void* dy, const void* x, void* dx, int64_t n, cudaStre
   }
 }
 
+template <typename T, int ACT>
+gbln_status glu_fwd_row8_ring_launch(const T* g, const T* u, uint8_t* q, float* sc, int64_t rows, int I, int64_t ldg,
+                                     int64_t ldu, int sms, cudaStream_t s) {
+  static std::atomic<uint64_t> attr_done{0};  // one bit per device
+  int dev = 0;
+  unsigned int* err = device_error_word();
+  if (!err || cudaGetDevice(&dev) != cudaSuccess) { cudaGetLastError(); return GBLN_ERR_CUDA; }
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(attr_done.load(std::memory_order_acquire) & bit)) {
+    if (cudaFuncSetAttribute(glu_fwd_row8_ring<T, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingSmem) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return GBLN_ERR_CUDA;
+    }
+    attr_done.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  glu_fwd_row8_ring<T, ACT><<<grid_for(rows, 1, sms), kRingThreads + 32, kRingSmem, s>>>(g, u, q, sc, rows, I, ldg,
+                                                                                         ldu, err);
+  return launch_status();
+}
+
 // Row-scaled output: a warp per row up to 128 vectors, then a block of 64 to 1024
 // threads with four vectors each, then a cluster of 512-thread blocks.
 template <typename T, int ACT>
-void glu_fwd_row8_launch(const void* g, const void* u, uint8_t* q, float* sc, int64_t rows, int64_t I,
-                         int64_t ldg, int64_t ldu, cudaStream_t s) {
+gbln_status glu_fwd_row8_launch(const void* g, const void* u, uint8_t* q, float* sc, int64_t rows, int64_t I,
+                                int64_t ldg, int64_t ldu, cudaStream_t s) {
+  const int sms = sm_count();
+  if (sms <= 0) return GBLN_ERR_CUDA;
   constexpr int VEC = VecOf<T>::N;
   constexpr int64_t kMaxGrid = 0x7fffffff;
   const int64_t nvec = I / VEC;
@@ -1072,7 +1213,7 @@ void glu_fwd_row8_launch(const void* g, const void* u, uint8_t* q, float* sc, in
       glu_fwd_row8_elem<T, ACT, true><<<(unsigned)rows, nw * 32, 0, s>>>(gt, ut, q, sc, rows, I, ldg, ldu);
     else
       glu_fwd_row8_elem<T, ACT, false><<<(unsigned)rows, 512, 0, s>>>(gt, ut, q, sc, rows, I, ldg, ldu);
-    return;
+    return launch_status();
   }
 #define GBLN_ROW8(TPR, VPT, RPB) \
   glu_fwd_row8<T, ACT, TPR, VPT, RPB><<<(unsigned)((rows + RPB - 1) / RPB), TPR * RPB, 0, s>>>(gt, ut, q, sc, rows, (int)I, ldg, ldu)
@@ -1085,11 +1226,14 @@ void glu_fwd_row8_launch(const void* g, const void* u, uint8_t* q, float* sc, in
   else if (nvec <= 512) GBLN_ROW8(128, 4, 1);
   else if (nvec <= 1024) GBLN_ROW8(256, 4, 1);
   else if (nvec <= 2048) GBLN_ROW8(512, 4, 1);
+  else if (cl == 1 && rows > sms)  // a row for each SM: 6.7 us either way; 2000 rows of 28672: 48 against 66 us
+    return glu_fwd_row8_ring_launch<T, ACT>(gt, ut, q, sc, rows, (int)I, ldg, ldu, sms, s);
   else if (cl == 1) GBLN_ROW8(1024, 4, 1);
   else if (cl == 4) GBLN_ROW8_CLUSTER(4);
   else GBLN_ROW8_CLUSTER(8);
 #undef GBLN_ROW8
 #undef GBLN_ROW8_CLUSTER
+  return launch_status();
 }
 
 template <typename T, int ACT, int FMT>
@@ -1276,14 +1420,13 @@ extern "C" gbln_status gbln_glu_fwd_fp8(const void* gate, const void* up, uint8_
   if (!gate || !up || !out_e4m3 || !out_scale) return GBLN_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;
 #define GBLN_GLU_FWD_FP8(TY, A) \
-  glu_fwd_row8_launch<TY, A>(gate, up, out_e4m3, out_scale, T, I, ld_gate, ld_up, s)
+  return glu_fwd_row8_launch<TY, A>(gate, up, out_e4m3, out_scale, T, I, ld_gate, ld_up, s)
   if (io == GBLN_F32) {
     GBLN_DISPATCH_ACT(float, act, GBLN_GLU_FWD_FP8)
   } else {
     GBLN_DISPATCH_ACT(bf16, act, GBLN_GLU_FWD_FP8)
   }
 #undef GBLN_GLU_FWD_FP8
-  return launch_status();
 }
 
 extern "C" gbln_status gbln_glu_fwd_ckpt8(const void* gate, const void* up, void* out, uint8_t* gate8,

@@ -266,8 +266,8 @@ __global__ void __launch_bounds__(1024) rms8_fwd_elem(const Fwd8<T, W> A, int NW
   for (int k = 0; k < kElemChunks; ++k) {
     cm[k] = 0;
     chunk_of(c0 + k * cs, H, [&](auto full) {
-      constexpr bool FULL = decltype(full)::v;
-      const int rem = H - (c0 + k * cs) - lane;
+      [[maybe_unused]] constexpr bool FULL = decltype(full)::v;
+      [[maybe_unused]] const int rem = H - (c0 + k * cs) - lane;
       h[k][0] = make_float2(to_f32(xr[k][0]), to_f32(xr[k][1]));
       h[k][1] = make_float2(to_f32(xr[k][2]), to_f32(xr[k][3]));
       if constexpr (RES) {
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kWideBlock) rms8_fwd_wide(const Fwd8<T, W> A) 
 // inputs stay in registers across the row's reduction.
 // ---------------------------------------------------------------------------
 template <typename T, typename W, int TPR, int VPT, int GPB, bool DRES, int FMT>
-__global__ void __launch_bounds__(TPR * GPB) rms8_bwd_vec(const Bwd8<T, W> A, bool prefetch) {
+__global__ void __launch_bounds__(TPR * GPB, GPB > 1 ? 3 : 512 / TPR) rms8_bwd_vec(const Bwd8<T, W> A, bool prefetch) {
   constexpr int VEC = VecOf<T>::N;
   constexpr int LPG = kCkptGroup / VEC;
   constexpr int NWG = TPR / 32;
@@ -438,9 +438,18 @@ __global__ void __launch_bounds__(TPR * GPB) rms8_bwd_vec(const Bwd8<T, W> A, bo
   int par = 0;
   for (int64_t row = r0 + g; row < r1; row += GPB) {
     const size_t base = (size_t)row * A.H;
-    // One row per block: thread 0 asks for the block's next row in L2 while this
-    // one is processed.
-    if constexpr (GPB == 1) {
+    // The group's next row is asked for in L2 while this one is processed: by one
+    // bulk prefetch per tensor where a block has one row, else line by line.
+    if constexpr (GPB > 1) {
+      constexpr int LINE = 128 / sizeof(T), SEG = TPR / 4;  // at most SEG lines per tensor
+      const int seg = l / SEG, i = l % SEG;
+      if (row + GPB < r1) {
+        const size_t nb = base + (size_t)GPB * A.H;
+        if (seg == 0 && i * LINE < A.H) prefetch_line(A.dy + nb + i * LINE);
+        if (DRES && seg == 1 && i * LINE < A.H) prefetch_line(A.dres + nb + i * LINE);
+        if (seg == 2 && i * 128 < A.H) prefetch_line(A.hq + nb + i * 128);
+      }
+    } else {
       if (threadIdx.x == 0 && row + 1 < r1) {
         const size_t nb = base + A.H;
         const uint32_t rb = (uint32_t)(A.H * sizeof(T));
@@ -740,7 +749,7 @@ BwdGeometry bwd_geometry(int64_t H, size_t io) {
     return {0, 0, e.groups, e.fits ? 1024 / e.block : 2};
   }
   const int64_t nvec = H * (int64_t)io / 16;
-  if (nvec <= 32) return {32, 1, 8, 4};
+  if (nvec <= 32) return {32, 1, 8, 3};
   if (nvec <= 64) return {32, 2, 8, 3};
   if (nvec <= 128) return {64, 2, 4, 3};
   int tpr = 64;
