@@ -429,11 +429,11 @@ __global__ void __launch_bounds__(TPR * GPB, GPB > 1 ? 3 : 512 / TPR) rms8_bwd_v
   const int64_t P = gridDim.x, p = blockIdx.x;
   const int64_t r0 = p * A.rows / P, r1 = (p + 1) * A.rows / P;
 
-  float acc[VPT][VEC];
+  float2 acc[VPT][VEC / 2];
 #pragma unroll
   for (int v = 0; v < VPT; ++v)
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) acc[v][e] = 0.f;
+    for (int e = 0; e < VEC / 2; ++e) acc[v][e] = both(0.f);
 
   int par = 0;
   for (int64_t row = r0 + g; row < r1; row += GPB) {
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(TPR * GPB, GPB > 1 ? 3 : 512 / TPR) rms8_bwd_v
       }
     }
     const float rs = __ldg(A.rstd + row);
-    float dot = 0.f;
+    float2 dot2 = both(0.f);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int iv = l + v * TPR;
@@ -482,14 +482,14 @@ __global__ void __launch_bounds__(TPR * GPB, GPB > 1 ? 3 : 512 / TPR) rms8_bwd_v
         ha[v].get(n, hs[v]);
         load_weight<W, VEC>(A.w, iv, wv);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          n[e] *= rs;
-          dot = fmaf(d[e] * wv[e], n[e], dot);
-          acc[v][e] = fmaf(d[e], n[e], acc[v][e]);
+        for (int e = 0; e < VEC; e += 2) {
+          const float2 d2 = make_float2(d[e], d[e + 1]), n2 = mul2(make_float2(n[e], n[e + 1]), both(rs));
+          dot2 = fma2(mul2(d2, make_float2(wv[e], wv[e + 1])), n2, dot2);
+          acc[v][e / 2] = fma2(d2, n2, acc[v][e / 2]);
         }
       }
     }
-    dot = group_sum<32>(dot);
+    float dot = group_sum<32>(dot2.x + dot2.y);
     if constexpr (TPR > 32) {
       // red is double-buffered: a buffer is written again only after the group's
       // next barrier, which every thread reaches after reading it.
@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(TPR * GPB, GPB > 1 ? 3 : 512 / TPR) rms8_bwd_v
       for (int k = 1; k < NWG; ++k) dot += red[g][par][k];
       par ^= 1;
     }
-    const float c = dot * A.inv_H;
+    const float2 mc = both(-dot * A.inv_H);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int iv = l + v * TPR;
@@ -510,7 +510,12 @@ __global__ void __launch_bounds__(TPR * GPB, GPB > 1 ? 3 : 512 / TPR) rms8_bwd_v
         ha[v].get(n, hs[v]);
         load_weight<W, VEC>(A.w, iv, wv);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) o[e] = rs * (d[e] * wv[e] - (n[e] * rs) * c);
+        for (int e = 0; e < VEC; e += 2) {
+          const float2 g2 = mul2(make_float2(d[e], d[e + 1]), make_float2(wv[e], wv[e + 1]));
+          const float2 o2 = mul2(both(rs), fma2(mul2(make_float2(n[e], n[e + 1]), both(rs)), mc, g2));
+          o[e] = o2.x;
+          o[e + 1] = o2.y;
+        }
         if constexpr (DRES) {
           float d2[VEC];
           unpack<VEC>(dra[v], d2);
@@ -531,7 +536,7 @@ __global__ void __launch_bounds__(TPR * GPB, GPB > 1 ? 3 : 512 / TPR) rms8_bwd_v
 #pragma unroll
         for (int e = 0; e < VEC; e += 4)
           *reinterpret_cast<float4*>(prow + (size_t)iv * VEC + e) =
-              make_float4(acc[v][e], acc[v][e + 1], acc[v][e + 2], acc[v][e + 3]);
+              make_float4(acc[v][e / 2].x, acc[v][e / 2].y, acc[v][e / 2 + 1].x, acc[v][e / 2 + 1].y);
       }
     }
   } else {
@@ -541,7 +546,7 @@ __global__ void __launch_bounds__(TPR * GPB, GPB > 1 ? 3 : 512 / TPR) rms8_bwd_v
       const int iv = l + v * TPR;
       if (iv < nvec) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) sacc[g][iv * VEC + e] = acc[v][e];
+        for (int e = 0; e < VEC; e += 2) *reinterpret_cast<float2*>(&sacc[g][iv * VEC + e]) = acc[v][e / 2];
       }
     }
     __syncthreads();
