@@ -646,6 +646,35 @@ glu_fwd_row8_ring(const T* gate, const T* up, uint8_t* q, float* sc, int64_t row
   }
 }
 
+// Runs of 128 consecutive values of a row for the element-wise paths: lane l holds
+// the values l, l + 32, l + 64, l + 96 (offsets are immediates); rem = values from
+// the lane's first one to the row's end, looked at where the run is not FULL.
+template <bool FULL, typename T>
+__device__ __forceinline__ void load_run(const T* p, int rem, T (&v)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = FULL || 32 * e < rem ? p[32 * e] : T(0.f);
+}
+template <bool FULL>
+__device__ __forceinline__ uint32_t load_run_codes(const uint8_t* p, int rem) {
+  uint32_t b[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) b[e] = FULL || 32 * e < rem ? (uint32_t)p[32 * e] : 0u;
+  return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+}
+template <bool FULL, typename T>
+__device__ __forceinline__ void store_run(T* p, int rem, const float (&v)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (FULL || 32 * e < rem) p[32 * e] = from_f32<T>(v[e]);
+}
+template <bool FULL, int FMT>
+__device__ __forceinline__ void store_run_codes(uint8_t* p, int rem, const float (&v)[4], float inv) {
+  const uint32_t q = q8_code4<FMT>(v[0], v[1], v[2], v[3], inv);
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (FULL || 32 * e < rem) p[32 * e] = (uint8_t)(q >> (8 * e));
+}
+
 // The same for any alignment and width.  A warp takes runs of 128 values, lane l
 // the values l, l + 32, l + 64, l + 96 of each; up to kRow8Runs runs per warp wait
 // in registers (blocks of up to 1024 threads: 16384 values), wider rows are read
@@ -659,8 +688,8 @@ glu_fwd_row8_elem(const T* gate, const T* up, uint8_t* q, float* sc, int64_t row
   constexpr int FMT = GBLN_Q8_E4M3;
   __shared__ uint32_t redm[32];
   const int64_t row = blockIdx.x;
-  const int nw = blockDim.x / 32;
-  const int64_t j0 = (threadIdx.x >> 5) * 128 + (threadIdx.x & 31);
+  const int nw = blockDim.x / 32, warp = warp_index(), lane = threadIdx.x & 31;
+  const int j0 = warp * 128;  // the warp's first run
   const T* gr = gate + row * ldg;
   const T* ur = up + row * ldu;
   uint8_t* qr = q + row * I;
@@ -669,19 +698,19 @@ glu_fwd_row8_elem(const T* gate, const T* up, uint8_t* q, float* sc, int64_t row
   if constexpr (FITS) {
     T g[kRow8Runs][4], u[kRow8Runs][4];
 #pragma unroll
-    for (int k = 0; k < kRow8Runs; ++k)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = (int)j0 + k * nw * 128 + 32 * e;
-        g[k][e] = u[k][e] = from_f32<T>(0.f);
-        if (j < I) {
-          g[k][e] = gr[j];
-          u[k][e] = ur[j];
-        }
+    for (int k = 0; k < kRow8Runs; ++k) {
+      const int j = j0 + k * nw * 128;
+      if (j + 128 <= I) {
+        load_run<true>(gr + j + lane, 0, g[k]);
+        load_run<true>(ur + j + lane, 0, u[k]);
+      } else {
+        load_run<false>(gr + j + lane, (int)I - j - lane, g[k]);
+        load_run<false>(ur + j + lane, (int)I - j - lane, u[k]);
       }
+    }
 #pragma unroll
     for (int k = 0; k < kRow8Runs; ++k)
-      if (((int)(threadIdx.x >> 5) + k * nw) * 128 < I) {
+      if (j0 + k * nw * 128 < I) {
         float gf[4], uf[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -704,12 +733,8 @@ glu_fwd_row8_elem(const T* gate, const T* up, uint8_t* q, float* sc, int64_t row
   if constexpr (FITS) {
 #pragma unroll
     for (int k = 0; k < kRow8Runs; ++k)
-      if (const int j = (int)j0 + k * nw * 128; j < I) {
-        const uint32_t c = q8_code4<FMT>(o[k][0], o[k][1], o[k][2], o[k][3], inv);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (j + 32 * e < I) qr[j + 32 * e] = (uint8_t)(c >> (8 * e));
-      }
+      if (const int j = j0 + k * nw * 128; j + 128 <= I) store_run_codes<true, FMT>(qr + j + lane, 0, o[k], inv);
+      else if (j < I) store_run_codes<false, FMT>(qr + j + lane, (int)I - j - lane, o[k], inv);
   } else {
     for (int64_t j = threadIdx.x; j < I; j += blockDim.x)
       qr[j] = (uint8_t)q8_code1<FMT>(act_f<T, ACT>(to_f32(gr[j])) * to_f32(ur[j]), inv);
@@ -824,32 +849,6 @@ glu_fwd_ckpt(const T* gate, const T* up, T* out, const GluCkpt C, int64_t T_, in
 // values l, l + 32, l + 64, l + 96 of it.  Two groups are in flight per warp;
 // offsets within a group are immediates, and only a row's last group is
 // predicated.
-template <bool FULL, typename T>
-__device__ __forceinline__ void load_run(const T* p, int rem, T (&v)[4]) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = FULL || 32 * e < rem ? p[32 * e] : T(0.f);
-}
-template <bool FULL>
-__device__ __forceinline__ uint32_t load_run_codes(const uint8_t* p, int rem) {
-  uint32_t b[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) b[e] = FULL || 32 * e < rem ? (uint32_t)p[32 * e] : 0u;
-  return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-}
-template <bool FULL, typename T>
-__device__ __forceinline__ void store_run(T* p, int rem, const float (&v)[4]) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (FULL || 32 * e < rem) p[32 * e] = from_f32<T>(v[e]);
-}
-template <bool FULL, int FMT>
-__device__ __forceinline__ void store_run_codes(uint8_t* p, int rem, const float (&v)[4], float inv) {
-  const uint32_t q = q8_code4<FMT>(v[0], v[1], v[2], v[3], inv);
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (FULL || 32 * e < rem) p[32 * e] = (uint8_t)(q >> (8 * e));
-}
-
 constexpr int kElemFlight = 2;
 
 template <typename T, int ACT, int FMT>
@@ -861,7 +860,7 @@ glu_fwd_ckpt_elem(const T* gate, const T* up, T* out, const GluCkpt C, int64_t T
   const int64_t ng = (I + kCkptGroup - 1) / kCkptGroup, n = T_ * ng;
   const bool small = n + F <= 0xffffffffLL;
   const int64_t step = (int64_t)gridDim.x * (kGluBlock / 32) * F;
-  for (int64_t u = ((int64_t)blockIdx.x * (kGluBlock / 32) + (threadIdx.x >> 5)) * F; u < n; u += step) {
+  for (int64_t u = ((int64_t)blockIdx.x * (kGluBlock / 32) + warp_index()) * F; u < n; u += step) {
     T g[F][4], v[F][4];
     int64_t row[F], j0[F];
 #pragma unroll
@@ -987,7 +986,7 @@ glu_bwd_ckpt_elem(const T* dout, const GluCkptIn C, T* dgate, T* dup, int64_t T_
   const int64_t ng = (I + kCkptGroup - 1) / kCkptGroup, n = T_ * ng;
   const bool small = n + F <= 0xffffffffLL;
   const int64_t step = (int64_t)gridDim.x * (kGluBlock / 32) * F;
-  for (int64_t u = ((int64_t)blockIdx.x * (kGluBlock / 32) + (threadIdx.x >> 5)) * F; u < n; u += step) {
+  for (int64_t u = ((int64_t)blockIdx.x * (kGluBlock / 32) + warp_index()) * F; u < n; u += step) {
     T d[F][4];
     uint32_t g[F], v[F];
     float gs[F], us[F];

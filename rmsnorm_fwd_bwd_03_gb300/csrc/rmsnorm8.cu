@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(1024) rms8_fwd_elem(const Fwd8<T, W> A, int NW
   constexpr int FMT = mode_fmt(MODE);
   __shared__ float red[32];
   __shared__ uint32_t redm[32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = warp_index();
   const int g = warp / NW, wi = warp - g * NW;
   const int64_t row = (int64_t)blockIdx.x * (blockDim.x / (32 * NW)) + g;
   const bool live = row < A.rows;  // the barrier below is reached by every warp
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kWideBlock) rms8_fwd_wide(const Fwd8<T, W> A) 
   constexpr int FMT = mode_fmt(MODE), NW = kWideBlock / 32;
   __shared__ float red[NW];
   __shared__ uint32_t redm[NW];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = warp_index();
   const int64_t row = blockIdx.x;
   const size_t base = (size_t)row * A.H;
   KahanSum ks;
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) rms8_bwd_elem(const Bwd8<
   constexpr int LINE = 128 / sizeof(T);
   extern __shared__ float sacc[];  // several row groups: one row of dW sums
   __shared__ float red[2][BLOCK / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = warp_index();
   const int GPB = BLOCK / (32 * NW);
   const int g = warp / NW, wi = warp - g * NW;
   const int H = A.H;
