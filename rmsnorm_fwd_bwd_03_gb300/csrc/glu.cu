@@ -1206,10 +1206,9 @@ gbln_status glu_fwd_row8_launch(const void* g, const void* u, uint8_t* q, float*
                    ldg % VEC == 0 && ldu % VEC == 0 && aligned_to(q, VEC);
   const T *gt = (const T*)g, *ut = (const T*)u;
   if (!vec) {
-    int nw = 1;
-    while (nw < 32 && (int64_t)nw * 128 * kRow8Runs < I) nw *= 2;
-    if ((int64_t)nw * 128 * kRow8Runs >= I)
-      glu_fwd_row8_elem<T, ACT, true><<<(unsigned)rows, nw * 32, 0, s>>>(gt, ut, q, sc, rows, I, ldg, ldu);
+    const int64_t nw = (I + 128 * kRow8Runs - 1) / (128 * kRow8Runs);
+    if (nw <= 32)
+      glu_fwd_row8_elem<T, ACT, true><<<(unsigned)rows, (int)nw * 32, 0, s>>>(gt, ut, q, sc, rows, I, ldg, ldu);
     else
       glu_fwd_row8_elem<T, ACT, false><<<(unsigned)rows, 512, 0, s>>>(gt, ut, q, sc, rows, I, ldg, ldu);
     return launch_status();

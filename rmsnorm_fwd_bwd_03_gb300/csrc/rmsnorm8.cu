@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) rms8_bwd_elem(const Bwd8<
   extern __shared__ float sacc[];  // several row groups: one row of dW sums
   __shared__ float red[2][BLOCK / 32];
   const int lane = threadIdx.x & 31, warp = warp_index();
-  const int GPB = BLOCK / (32 * NW);
+  const int GPB = (int)blockDim.x / (32 * NW);
   const int g = warp / NW, wi = warp - g * NW;
   const int H = A.H;
   const int64_t P = gridDim.x, p = blockIdx.x;
@@ -723,8 +723,9 @@ constexpr int64_t kMaxH = 1 << 24;
 constexpr int64_t kMaxRows = (1LL << 31) - 1;
 constexpr int64_t kMaxVecPerRow = 2048;  // 512 threads x 4 vectors
 
-// Element path: warps per row (a power of two up to 32) so that a warp holds at
-// most `chunks` chunks; wider rows do not fit the registers.
+// Element path: as few warps per row (up to 32) as hold it with at most `chunks`
+// chunks each, and rows for about eight warps per block; wider rows do not fit the
+// registers.
 struct Elem {
   bool fits;
   int nw;      // warps per row
@@ -734,10 +735,9 @@ struct Elem {
 Elem elem_geometry(int64_t H, int chunks) {
   const int64_t nchunk = (H + kCkptGroup - 1) / kCkptGroup;
   if (nchunk > 32 * chunks) return {false, kWideBlock / 32, kWideBlock, 1};
-  int nw = 1;
-  while ((int64_t)nw * chunks < nchunk) nw *= 2;
-  const int block = nw < 8 ? 256 : nw * 32;
-  return {true, nw, block, block / (nw * 32)};
+  const int nw = (int)((nchunk + chunks - 1) / chunks);
+  const int groups = nw < 8 ? 8 / nw : 1;
+  return {true, nw, 32 * nw * groups, groups};
 }
 
 bool vec_width(int64_t H, size_t io) {
@@ -751,7 +751,10 @@ struct BwdGeometry {
 BwdGeometry bwd_geometry(int64_t H, size_t io) {
   if (!vec_width(H, io)) {
     const Elem e = elem_geometry(H, kElemBwdChunks);
-    return {0, 0, e.groups, e.fits ? 1024 / e.block : 2};
+    // At 64 registers each of an SM's four partitions holds eight warps, and a
+    // block's warps go to them in turn: five warps fit four times, not six (99 us
+    // against 125 for 30476 rows of 1101 values).
+    return {0, 0, e.groups, e.fits ? 8 / ((e.block + 127) / 128) : 2};
   }
   const int64_t nvec = H * (int64_t)io / 16;
   if (nvec <= 32) return {32, 1, 8, 3};
@@ -814,9 +817,9 @@ gbln_status bwd_launch(const Bwd8<T, W>& A, int64_t P, cudaStream_t s) {
   if (!vec) {
     const Elem e = elem_geometry(A.H, kElemBwdChunks);
     const size_t smem = e.groups > 1 ? (size_t)A.H * sizeof(float) : 0;  // at most 1024 values
-    if (e.fits && e.block == 256) rms8_bwd_elem<T, W, DRES, FMT, 256><<<grid, 256, smem, s>>>(A, e.nw);
-    else if (e.fits && e.block == 512) rms8_bwd_elem<T, W, DRES, FMT, 512><<<grid, 512, 0, s>>>(A, e.nw);
-    else if (e.fits) rms8_bwd_elem<T, W, DRES, FMT, 1024><<<grid, 1024, 0, s>>>(A, e.nw);
+    if (e.fits && e.block <= 256) rms8_bwd_elem<T, W, DRES, FMT, 256><<<grid, e.block, smem, s>>>(A, e.nw);
+    else if (e.fits && e.block <= 512) rms8_bwd_elem<T, W, DRES, FMT, 512><<<grid, e.block, 0, s>>>(A, e.nw);
+    else if (e.fits) rms8_bwd_elem<T, W, DRES, FMT, 1024><<<grid, e.block, 0, s>>>(A, e.nw);
     else rms8_bwd_wide<T, W, DRES, FMT><<<grid, kWideBlock, 0, s>>>(A);
     return launch_status();
   }
