@@ -294,3 +294,60 @@ def test_decode_loop_in_a_graph_on_a_side_stream():
             amax = np.abs(want).max(-1, keepdims=True)
             assert (err <= (2.0 ** -4 + 2.0 ** -8 + 2.0 ** -12) * np.abs(want) + amax / 448 * 2.0 ** -10 * 1.01).all()
     assert gb.device_error() == 0
+
+
+def test_empty_calls():
+    Hk, D = 2, 64
+    cache = _caches(2, 4, Hk, D, "int8")
+    none = _caches(0, 4, Hk, D, "int8")
+    table = gb.rope_table(4, D, THETA)
+    kv = torch.empty((0, Hk, D), dtype=torch.bfloat16, device="cuda")
+    i32, i64 = (torch.empty(0, dtype=t, device="cuda") for t in (torch.int32, torch.int64))
+    assert gb.rope_fwd_cache8(None, kv, kv, i32, table, i64, *cache) is None
+    assert gb.rope_fwd_cache8(torch.empty((0, 4, D), dtype=torch.bfloat16, device="cuda"), kv, kv, i32, table, i64, *cache).shape == (0, 4, D)
+    ko, vo = gb.cache8_read(i64, *cache)
+    assert ko.shape == vo.shape == (0, Hk, D)
+    # a cache of no pages: padding stores nothing and reads as zeros, any slot is outside it
+    one = _randn((1, Hk, D), torch.bfloat16, 1)
+    pad = torch.full((1,), -1, device="cuda")
+    gb.rope_fwd_cache8(None, one, one, torch.zeros(1, dtype=torch.int32, device="cuda"), table, pad, *none)
+    ko, vo = gb.cache8_read(pad, *none)
+    assert (ko == 0).all() and (vo == 0).all() and gb.device_error() == 0
+    ko, _ = gb.cache8_read(torch.zeros(1, dtype=torch.int64, device="cuda"), *none)
+    assert torch.isnan(ko).all() and gb.device_error(clear=True) == gb.ERR_BAD_SLOT
+
+
+def test_prefill_then_decode_attention():
+    # a prompt stored at once, tokens stored one by one, attention over what is read back:
+    # against the same attention in float64 over the quantised values
+    Hq, Hk, D, page, n, new = 4, 2, 64, 8, 37, 5
+    table = gb.rope_table(n + new, D, THETA)
+    cache = _caches(8, page, Hk, D, "int8", "HND")
+    blocks = torch.tensor([5, 2, 7, 0, 1, 6], device="cuda")
+    slot = lambda p: blocks[p // page] * page + p % page  # noqa: E731
+    qkv = _randn((n + new, (Hq + 2 * Hk) * D), torch.bfloat16, 1)
+    q, k, v = (t.unflatten(1, (-1, D)) for t in qkv.split([Hq * D, Hk * D, Hk * D], dim=1))
+    pos = torch.arange(n + new, dtype=torch.int32, device="cuda")
+    Q64 = oracle.rope_fwd(to64(q), pos.cpu().numpy(), THETA)
+    K64 = q8.values(*q8.quantize(oracle.rope_fwd(to64(k), pos.cpu().numpy(), THETA), "int8"))
+    V64 = q8.values(*q8.quantize(to64(v), "int8"))
+
+    def attend(Q, K, V):
+        out = np.zeros((Hq, D))
+        for h in range(Hq):
+            s = K[:, h // (Hq // Hk)] @ Q[h] / D ** 0.5
+            p = np.exp(s - s.max())
+            out[h] = p @ V[:, h // (Hq // Hk)] / p.sum()
+        return out
+
+    steps = [slice(0, n)] + [slice(i, i + 1) for i in range(n, n + new)]
+    for s in steps:
+        qo = gb.rope_fwd_cache8(q[s], k[s], v[s], pos[s], table, slot(pos[s].long()), *cache)
+        ko, vo = gb.cache8_read(slot(torch.arange(s.stop, device="cuda")), *cache, dtype=torch.float32)
+        got = attend(to64(qo)[-1], to64(ko), to64(vo))
+        want = attend(Q64[s.stop - 1], K64[:s.stop], V64[:s.stop])
+        # q is rounded to bf16 (2^-9 of each value): a score moves by at most 2^-9 sum |q k| / sqrt(D), a
+        # weight by twice that, relatively; a rotated K next to a tie may take the other code (a step of
+        # its scale: 1/127 of its largest value) in a few of its values, far less than that
+        d = 2 * 2.0 ** -9 * max((np.abs(K64[:s.stop, h // (Hq // Hk)]) @ np.abs(Q64[s.stop - 1, h])).max() for h in range(Hq)) / D ** 0.5
+        assert (np.abs(got - want) <= 1.5 * d * np.abs(V64[:s.stop]).max()).all()

@@ -536,3 +536,102 @@ def test_more_than_two_to_the_31_values():
         dg, du = oracle.glu_bwd("relu", to64(out[r]), k, k)
         check_io(to64(dgate[r]), dg, "bf16", "dgate")
         check_io(to64(dup[r]), du, "bf16", "dup")
+
+
+def test_captured_training_step_matches_eager():
+    # forward, backward and dW of a norm and a gated unit with checkpoints, through
+    # autograd, captured once and replayed on new inputs
+    T, H, dt = 96, 512, torch.bfloat16
+    x = _randn((T, H), dt, 1).requires_grad_()
+    r = _randn((T, H), dt, 2).requires_grad_()
+    w = _weight(H, dt).requires_grad_()
+    cy, ch = _randn((T, H // 2), dt, 3), _randn((T, H), dt, 4)
+    leaves = (x, r, w)
+
+    def step():
+        y, h = ga.rms_norm(x, w, 1e-5, r, checkpoint="int8")
+        out = ga.swiglu(*y.chunk(2, dim=-1), checkpoint="e4m3")
+        return torch.autograd.grad([out, h], leaves, [cy, ch])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        grads = step()
+    for seed in (10, 20):
+        with torch.no_grad():
+            x.copy_(_randn((T, H), dt, seed))
+            r.copy_(_randn((T, H), dt, seed + 1))
+            cy.copy_(_randn((T, H // 2), dt, seed + 2))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [g.clone() for g in grads]
+        for a, b in zip(got, step()):
+            assert _same_bits(a, b)
+
+
+def test_fp8_operands_through_a_layer():
+    # norm -> projection -> gated unit -> projection, the projections on the E4M3 operands
+    # and their row scales (float64 products of the values they stand for)
+    T, H, I = 40, 256, 384
+    x, r = _randn((T, H), torch.bfloat16, 1), _randn((T, H), torch.bfloat16, 2)
+    w = _weight(H, torch.bfloat16)
+    w1, w2 = _randn((H, 2 * I), torch.float32, 3).double() / H ** 0.5, _randn((I, H), torch.float32, 4).double() / I ** 0.5
+    _, y8, ys, h, _ = gb.rmsnorm_fwd_fp8(x, w, 1e-5, r, want_y=False)
+    gate_up = ((y8.double() @ w1) * ys.double()[:, None]).to(torch.bfloat16)
+    o8, os_ = gb.glu_fwd_fp8(*gate_up.chunk(2, dim=-1))
+    got = to64((o8.double() @ w2) * os_.double()[:, None])
+    # each operand is within 2^-4 of its value (normal E4M3 range), so is every term of a product:
+    # the first projection's error passes a slope of at most 1.1 (silu) and a factor up
+    y64 = q8.rmsnorm_fwd_fp8(to64(x), to64(r), to64(w), 1e-5, "bf16")[2]
+    W1, W2 = w1.cpu().numpy(), w2.cpu().numpy()
+    gu = y64 @ W1
+    G, U = gu[:, :I], gu[:, I:]
+    dgu = (2.0 ** -4 + 2.0 ** -8) * (np.abs(y64) @ np.abs(W1)) + 2.0 ** -8 * np.abs(gu)
+    out = q8.glu_out("silu", G, U)
+    f = oracle.act("silu", G)
+    dout = 1.1 * dgu[:, :I] * (np.abs(U) + dgu[:, I:]) + np.abs(f) * dgu[:, I:]
+    dout = dout + (2.0 ** -4 + 2.0 ** -8) * (np.abs(out) + dout) + np.abs(out).max(-1, keepdims=True) / 448 * 2.0 ** -9
+    assert (np.abs(got - out @ W2) <= dout @ np.abs(W2)).all()
+
+
+def test_backward_is_reproducible_and_accumulates():
+    for T, H in ((3000, 640), (700, 4096), (500, 1023), (40, 20001)):
+        dt = torch.bfloat16
+        x, dy = _randn((T, H), dt, 1), _randn((T, H), dt, 2)
+        w = _weight(H, dt)
+        _, _, rstd, h8, hs = gb.rmsnorm_fwd_ckpt8(x, w, 1e-5)
+        dx, part, P = gb.rmsnorm_bwd_ckpt8(dy, h8, hs, w, rstd)
+        dw = gb.rmsnorm_dw_finalize(part, P)
+        for _ in range(3):
+            dx2, part2, _ = gb.rmsnorm_bwd_ckpt8(dy, h8, hs, w, rstd)
+            assert _same_bits(dx, dx2) and _same_bits(dw, gb.rmsnorm_dw_finalize(part2, P))
+        acc = gb.rmsnorm_dw_finalize(part, P, dw=dw.clone(), accumulate=True)
+        assert torch.equal(acc, dw + dw)
+        assert P == gb.rmsnorm_bwd_ckpt8_num_partials(T, H, dt)
+
+
+def test_norm_of_more_than_two_to_the_31_values():
+    T, H = 150001, 14336
+    x = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+    x.normal_(generator=torch.Generator(device="cuda").manual_seed(2))
+    w = _weight(H, torch.bfloat16)
+    y, _, rstd, h8, hs = gb.rmsnorm_fwd_ckpt8(x, w, 1e-5, fmt="e4m3")
+    _, yq, ys, _, _ = gb.rmsnorm_fwd_fp8(x, w, 1e-5, want_y=False)
+    dx, part, P = gb.rmsnorm_bwd_ckpt8(x, h8, hs, w, rstd, x)
+    W = to64(w)
+    for t in (0, 74898, 74899, 149796, 149797, T - 1):
+        t = slice(t, t + 1)
+        X = to64(x[t])
+        c, s, y64, _, rs = q8.rmsnorm_fwd_fp8(X, None, W, 1e-5)
+        check_io(to64(y[t]), y64, "bf16", "y")
+        assert np.array_equal(codes64(yq[t]), c)
+        check_rstd(to64(ys[t]), s)
+        check_exact(h8[t], hs[t], X, "e4m3", "h8", 128)
+        kept = q8.values(codes64(h8[t]), codes64(hs[t]), 128)
+        check_io(to64(dx[t]), q8.rmsnorm_bwd_kept(X, X, kept, W, rs)[0], "bf16", "dx")
