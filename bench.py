@@ -613,7 +613,8 @@ def run_single_op(args, wl, device):
 def run_next_ops(args, wl, device):
     """Time the operators beyond the step (gated units with other activations and
     packed layouts, plain activations, strided / interleaved RoPE, LayerNorm,
-    MXFP8 outputs of the RMSNorm and SwiGLU forwards) at
+    MXFP8 and row-scaled FP8 outputs of the RMSNorm and SwiGLU forwards, 8-bit
+    activation checkpoints with their backward passes, the quantised K/V cache) at
     the workload's widths: K launches each, CUDA events around each launch, L2
     flushed in between.  One JSON line with per-operator time and GB/s."""
     import rmsnorm_fwd_bwd_03_gb300 as gb
@@ -681,6 +682,32 @@ def run_next_ops(args, wl, device):
         ops["rmsnorm_fwd_mxfp8_and_y"] = (lib.gbln_rmsnorm_fwd_mxfp8, (p(xl), p(rl), p(wr), p(yl), p(yq), p(ysc), p(hl), p(rstd), T, H, wl.eps, io, io, s), mx_rms + T * H * b)
         gq, gsc = torch.empty(T, I, dtype=torch.uint8, device=device), torch.empty(T, I // 32, dtype=torch.uint8, device=device)
         ops["swiglu_fwd_packed_mxfp8"] = (lib.gbln_glu_fwd_mxfp8, (p(packed), p(packed) + I * b, p(gq), p(gsc), T, I, 2 * I, 2 * I, gb.ACT["silu"], io, s), 2 * T * I * b + T * I + T * I // 32)
+
+    # 8-bit storage with float32 scales: row-scaled E4M3 operands, checkpoints of the
+    # norm's and the gated unit's inputs with the backward passes that read them, and
+    # K and V of a packed QKV tensor stored in, and read back from, pages of 16 slots.
+    u8 = lambda *shape: torch.empty(shape, dtype=torch.uint8, device=device)  # noqa: E731
+    f32 = lambda *shape: torch.empty(shape, device=device)  # noqa: E731
+    int8, gh, gi = gb.Q8["int8"], -(-H // gb.CKPT_GROUP), -(-I // gb.CKPT_GROUP)
+    wn, rowsc = (1 + 0.1 * torch.randn(H, generator=g, device=device)).to(dt), f32(T)
+    h8, hs = u8(T, H), f32(T, gh)
+    ops["rmsnorm_fwd_fp8"] = (lib.gbln_rmsnorm_fwd_fp8, (p(xl), p(rl), p(wn), None, p(h8), p(rowsc), p(hl), p(rstd), T, H, wl.eps, io, io, s), 3 * T * H * b + T * H + 8 * T + H * b)
+    ops["rmsnorm_fwd_ckpt8"] = (lib.gbln_rmsnorm_fwd_ckpt8, (p(xl), p(rl), p(wn), p(yl), p(hl), p(rstd), p(h8), p(hs), T, H, wl.eps, int8, io, io, s), 4 * T * H * b + T * H + 4 * T * gh + 4 * T + H * b)
+    P8 = gb.rmsnorm_bwd_ckpt8_num_partials(T, H, dt)
+    part8 = f32(P8, H)
+    ops["rmsnorm_bwd_ckpt8"] = (lib.gbln_rmsnorm_bwd_ckpt8, (p(dyl), p(drl), p(h8), p(hs), p(wn), p(rstd), p(dxl), p(part8), P8, T, H, int8, io, io, s), 3 * T * H * b + T * H + 4 * T * gh + 4 * T + H * b)
+    g8, u8_, gs8, us8 = u8(T, I), u8(T, I), f32(T, gi), f32(T, gi)
+    silu = gb.ACT["silu"]
+    ops["swiglu_fwd_packed_fp8"] = (lib.gbln_glu_fwd_fp8, (p(packed), p(packed) + I * b, p(g8), p(rowsc), T, I, 2 * I, 2 * I, silu, io, s), 2 * T * I * b + T * I + 4 * T)
+    ops["swiglu_fwd_packed_ckpt8"] = (lib.gbln_glu_fwd_ckpt8, (p(packed), p(packed) + I * b, p(out), p(g8), p(gs8), p(u8_), p(us8), T, I, 2 * I, 2 * I, I, silu, int8, io, s), 3 * T * I * b + 2 * T * I + 8 * T * gi)
+    ops["swiglu_bwd_packed_ckpt8"] = (lib.gbln_glu_bwd_ckpt8, (p(dout), p(g8), p(gs8), p(u8_), p(us8), p(grad), p(grad) + I * b, T, I, I, 2 * I, 2 * I, silu, int8, io, s), 3 * T * I * b + 2 * T * I + 8 * T * gi)
+    page = 16
+    caches = [(torch.zeros((-(-T // page), page, Hk, D), dtype=torch.int8, device=device), f32(-(-T // page), page, Hk)) for _ in range(2)]
+    kv8 = [gb._cache8(c, sc, Hk, D, n) for (c, sc), n in zip(caches, "kv")]
+    slots = torch.randperm(T, generator=g, device=device)
+    head8 = 2 * Hk * (D + 4)
+    ops["rope_fwd_packed_qkv_cache8"] = (lib.gbln_rope_fwd_cache8, (p(qkv), p(qkv) + Hq * D * b, p(qkv) + (Hq + Hk) * D * b, p(q), p(pos), p(table), table.shape[0], p(slots), *kv8, T, Hq, Hk, D, W, W, W, Hq * D, 0, int8, io, s), T * (2 * Hq * D * b + 2 * Hk * D * b + head8 + 12))
+    ops["cache8_read"] = (lib.gbln_cache8_read, (p(slots), *kv8, p(ko), p(k), T, Hk, D, Hk * D, Hk * D, int8, io, s), T * (head8 + 2 * Hk * D * b + 8))
 
     flush = L2Flush(device)
     peak, peak_kind = _measured_peak()
