@@ -71,154 +71,234 @@ struct WriteArgs {
 };
 
 // ---------------------------------------------------------------------------
-// Vector path: a warp takes one token and up to kWriteHeads head rows per lane.
-// A lane owns the vectors at v*VEC of both halves of a head row, whichever
-// pairing, so a warp's accesses are whole lines: with rotate-half pairing they
-// turn into each other by VEC table entries, with interleaved pairing each holds
-// VEC / 2 pairs of its own.  A head row takes nu = D / (2 VEC) lanes out of a group
-// of the next power of two, so 80 or 96 wide heads run here with idle lanes.  The
-// table entries are loaded once per token and lane, and all of a lane's row
-// loads are issued before anything that depends on the token's slot or position.
+// Vector path.  A warp works either on queries (up to kWriteQ head rows per lane:
+// rotate and store) or on K and V (one or two heads of both per lane: rotate K,
+// quantise both), one token after the other; where a token's heads leave lanes
+// over, several tokens at a time.  A lane owns the vectors at v*VEC of both halves
+// of a head row, whichever pairing, so a warp's accesses are whole lines: with
+// rotate-half pairing they turn into each other by VEC table entries, with
+// interleaved pairing each holds VEC / 2 pairs of its own.  A head row takes
+// nu = D / (2 VEC) lanes out of a group of the next power of two, so 80 or 96 wide
+// heads run here with idle lanes.  All of a lane's row loads are issued before
+// anything that depends on the token's slot or position, and the maxima and
+// divisions of its K and V heads run side by side.  (With queries, K and V taken
+// alike, head after head, the chain of each one's reduction and division showed:
+// 95 us instead of 77 for 32768 tokens of 16 / 8 heads of 128, 70 us at the copy
+// rate.)
 // ---------------------------------------------------------------------------
-// Six head rows per lane (two blocks of 256 threads per SM) measured faster than
-// four (three blocks): 236 against 247 us for 65536 tokens of 32 / 8 heads of 128.
-constexpr int kWriteHeads = 6;
+// Head rows per lane and pass of a query warp: 8 measured 112 us, 6 119 and 4 117 for
+// 32768 tokens of 32 / 8 heads of 128 (110 us at the copy rate).
+constexpr int kWriteQ = 8;
 constexpr int kWriteWarps = 8;  // per block: chunks of a token, then tokens
-// A warp walks tokens t, t + step, ... and asks for the next one's rows in L2
-// while it works on this one.  Eight times the resident blocks leave a warp a
-// few tokens to do that for and the scheduler something to balance: 236 us, with
-// one token per warp 283, with the resident blocks alone 266.
-constexpr int kWriteGrid = 2 * 8;  // blocks per SM
+// A warp walks its tokens and asks for the next ones' rows in L2 while it works
+// on these.  Eight times the resident blocks leave a warp a few steps to do that
+// for and the scheduler something to balance.
+constexpr int kWriteBlocks = 2;               // resident per SM
+constexpr int kWriteGrid = kWriteBlocks * 8;  // blocks per SM
 
-template <typename T, bool IL, int FMT>
-__global__ void __launch_bounds__(32 * kWriteWarps, 2)
-cache8_write_vec(const WriteArgs<T> A, int nu, int lg, int ch) {
+struct WriteShape {
+  int nu, lg;         // lanes in use per head row, log2 of the lanes of its group
+  int nq, qch, qlt;   // query chunks, head rows per lane in each, log2 of tokens per warp
+  int nkv, kch, klt;  // the same of K and V heads
+};
+
+// (cos, sin) of a lane's pairs: entries ia.. (rotate-half), or half as many for
+// each of its two vectors (interleaved); NaN for a position outside the table.
+template <int VEC, bool IL>
+__device__ __forceinline__ void load_turns(const float2* table, int half, int p, bool ok, bool on, int ia, float2 (&cs)[VEC]) {
+  if (ok && on) {
+    const float2* e = table + (size_t)p * half;
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2) {
+      const int at = !IL ? ia + i : i < VEC / 2 ? ia / 2 + i : (half + ia) / 2 + i - VEC / 2;
+      const float4 f = __ldg(reinterpret_cast<const float4*>(e + at));
+      cs[i] = make_float2(f.x, f.y);
+      cs[i + 1] = make_float2(f.z, f.w);
+    }
+  } else {
+    const float x = ok ? 0.f : __int_as_float(0x7fc00000);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) cs[i] = make_float2(x, x);
+  }
+}
+template <int VEC, bool IL>
+__device__ __forceinline__ void turn(float (&xa)[VEC], float (&xb)[VEC], const float2 (&cs)[VEC]) {
+  if constexpr (IL) {
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) {
+      const float2 f = cs[e / 2], f2 = cs[VEC / 2 + e / 2];
+      const float a = xa[e] * f.x - xa[e + 1] * f.y, b = xa[e + 1] * f.x + xa[e] * f.y;
+      const float c = xb[e] * f2.x - xb[e + 1] * f2.y, d = xb[e + 1] * f2.x + xb[e] * f2.y;
+      xa[e] = a;
+      xa[e + 1] = b;
+      xb[e] = c;
+      xb[e + 1] = d;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float a = xa[e] * cs[e].x - xb[e] * cs[e].y, b = xb[e] * cs[e].x + xa[e] * cs[e].y;
+      xa[e] = a;
+      xb[e] = b;
+    }
+  }
+}
+
+template <typename T, bool IL, int FMT, int KP>
+__global__ void __launch_bounds__(32 * kWriteWarps, kWriteBlocks)
+cache8_write_vec(const WriteArgs<T> A, const WriteShape W) {
   constexpr int VEC = VecOf<T>::N;
   constexpr int LINE = 128 / sizeof(T);
-  const int half = A.D / 2, HR = A.Hq + A.Hk, HT = HR + A.Hk;
-  const int lanes = 1 << lg, G = 32 >> lg;
+  const int half = A.D / 2;
+  const int lanes = 1 << W.lg;
   const int lane = threadIdx.x;
   const int v = lane & (lanes - 1);
-  const bool on = v < nu;
+  const bool on = v < W.nu;
   const int c = blockIdx.y * blockDim.y + threadIdx.y;
-  const int hf = G * c * ch, hb = (lane >> lg) + hf;
-  const int64_t step = (int64_t)gridDim.x * blockDim.z;
-  int64_t t = (int64_t)blockIdx.x * blockDim.z + threadIdx.z;
-  if (t >= A.rows || hf >= HT) return;  // uniform per warp
-  const int ia = v * VEC, ib = half + ia;
-  int p = __ldg(A.pos + t);
-  int64_t slot = __ldg(A.S.slots + t);
+  if (c >= W.nq + W.nkv) return;  // uniform per warp
+  const bool isq = c < W.nq;
+  // the lanes of a group take a head of one of the warp's 2^lt tokens
+  const int lt = isq ? W.qlt : W.klt, G = 32 >> (W.lg + lt);
+  const int sub = (lane >> W.lg) >> (5 - W.lg - lt), g = (lane >> W.lg) & (G - 1);
+  const int li = lane & ((32 >> lt) - 1);  // the lane's number among its token's
+  const int64_t step = ((int64_t)gridDim.x * blockDim.z) << lt;
+  int64_t t0 = ((int64_t)blockIdx.x * blockDim.z + threadIdx.z) << lt;
+  if (t0 >= A.rows) return;
+  const int64_t end = A.rows - 1;
+  const int ia = v * VEC;
+  const int64_t first = min(t0 + sub, end);
+  int p = __ldg(A.pos + first);
+  float2 cs[VEC];
+
+  if (isq) {
+    const int hf = G * c * W.qch, hb = hf + g;
+    const int last = min(hf + G * W.qch, A.Hq) * A.D;
 #pragma unroll 1
-  for (; t < A.rows; t += step) {
-    // rows of the three inputs, offset so that head h is at + h * D in each
-    const T* qp = A.q + t * A.ldq;
-    const T* kp = A.k + t * A.ldk - (int64_t)A.Hq * A.D;
-    const T* vp = A.v + t * A.ldv - (int64_t)HR * A.D;
-    uint4 a[kWriteHeads], b[kWriteHeads];
+    for (; t0 < A.rows; t0 += step) {
+      const int64_t t = t0 + sub;
+      const bool live = on && t < A.rows;
+      const T* qp = A.q + min(t, end) * A.ldq;
+      T* qo = A.qo + min(t, end) * A.ldqo;
+      uint4 a[kWriteQ], b[kWriteQ];
 #pragma unroll
-    for (int j = 0; j < kWriteHeads; ++j) {
-      const int h = hb + G * j;
+      for (int j = 0; j < kWriteQ; ++j) {
+        const int h = hb + G * j;
+        if (j < W.qch && live && h < A.Hq) {
+          a[j] = ld_stream(qp + h * A.D + ia);
+          b[j] = ld_stream(qp + h * A.D + ia + half);
+        }
+      }
+      const bool ok = p >= 0 && (int64_t)p < A.max_pos;
+      load_turns<VEC, IL>(A.table, half, p, ok, on, ia, cs);
+      if (!ok && live && c == 0 && li == 0) atomicOr(A.err, kErrBadPosition);
+      if (t0 + step < A.rows) {  // the warp's next tokens
+        const int64_t n = min(t + step, end);
+        p = __ldg(A.pos + n);
+        for (int x = hf * A.D + li * LINE; x < last; x += (32 >> lt) * LINE) prefetch_line(A.q + n * A.ldq + x);
+      }
+#pragma unroll
+      for (int j = 0; j < kWriteQ; ++j) {
+        const int h = hb + G * j;
+        if (j < W.qch && live && h < A.Hq) {
+          float xa[VEC], xb[VEC];
+          unpack<VEC>(a[j], xa);
+          unpack<VEC>(b[j], xb);
+          turn<VEC, IL>(xa, xb, cs);
+          st_vec(qo + h * A.D + ia, pack<T, VEC>(xa));
+          st_vec(qo + h * A.D + ia + half, pack<T, VEC>(xb));
+        }
+      }
+    }
+    return;
+  }
+
+  const int ck = c - W.nq;
+  const int hf = G * ck * W.kch, hb = hf + g;
+  const int last = min(hf + G * W.kch, A.Hk) * A.D;
+  int64_t slot = __ldg(A.S.slots + first);
+#pragma unroll 1
+  for (; t0 < A.rows; t0 += step) {
+    const int64_t t = t0 + sub;
+    const bool live = on && t < A.rows;
+    const T *kp = A.k + min(t, end) * A.ldk, *vp = A.v + min(t, end) * A.ldv;
+    constexpr int N = 2 * KP;  // K of each head, then V of each
+    uint4 a[N], b[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int h = hb + G * (j % KP);
       a[j] = b[j] = make_uint4(0, 0, 0, 0);
-      if (j < ch && on && h < HT) {
-        const T* src = (h < A.Hq ? qp : h < HR ? kp : vp) + h * A.D + ia;
+      if (j % KP < W.kch && live && h < A.Hk) {
+        const T* src = (j < KP ? kp : vp) + h * A.D + ia;
         a[j] = ld_stream(src);
         b[j] = ld_stream(src + half);
       }
     }
     const bool ok = p >= 0 && (int64_t)p < A.max_pos;
-    // (cos, sin) of the lane's pairs: entries v*VEC.. (rotate-half), or half as many
-    // for each of its two vectors (interleaved)
-    float2 cs[VEC];
-    if (ok && on) {
-      const float2* e = A.table + (size_t)p * half;
-#pragma unroll
-      for (int i = 0; i < VEC; i += 2) {
-        const int at = !IL ? ia + i : i < VEC / 2 ? ia / 2 + i : ib / 2 + i - VEC / 2;
-        const float4 f = __ldg(reinterpret_cast<const float4*>(e + at));
-        cs[i] = make_float2(f.x, f.y);
-        cs[i + 1] = make_float2(f.z, f.w);
-      }
-    } else {
-      const float x = ok ? 0.f : __int_as_float(0x7fc00000);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) cs[i] = make_float2(x, x);
-    }
+    load_turns<VEC, IL>(A.table, half, p, ok, on, ia, cs);
     int64_t off = 0;
     const int64_t page = A.S.page_of(slot, off);
-    // the warp's next token: its position and slot, and its rows on their way to L2
-    if (t + step < A.rows) {
-      p = __ldg(A.pos + t + step);
-      slot = __ldg(A.S.slots + t + step);
-      const int last = min(hf + G * ch, HT) * A.D;
-      for (int x = hf * A.D + lane * LINE; x < last; x += 32 * LINE)
-        prefetch_line((x < A.Hq * A.D ? qp + step * A.ldq : x < HR * A.D ? kp + step * A.ldk : vp + step * A.ldv) + x);
-    }
-    if (c == 0 && lane == 0) {
-      if (!ok && (A.Hq > 0 || page >= 0)) atomicOr(A.err, kErrBadPosition);
+    if (ck == 0 && li == 0 && live) {
+      if (!ok && page >= 0) atomicOr(A.err, kErrBadPosition);
       if (page == -2) atomicOr(A.err, kErrBadSlot);
     }
-    T* qo = A.qo + t * A.ldqo + ia;
-#pragma unroll
-    for (int j = 0; j < kWriteHeads; ++j) {
-      if (j >= ch) break;
-      const int h = hb + G * j;
-      float xa[VEC], xb[VEC];
-      unpack<VEC>(a[j], xa);
-      unpack<VEC>(b[j], xb);
-      if (h < HR) {
-        float ya[VEC], yb[VEC];
-        if constexpr (IL) {
-#pragma unroll
-          for (int e = 0; e < VEC; e += 2) {
-            const float2 f = cs[e / 2], f2 = cs[VEC / 2 + e / 2];
-            ya[e] = xa[e] * f.x - xa[e + 1] * f.y;
-            ya[e + 1] = xa[e + 1] * f.x + xa[e] * f.y;
-            yb[e] = xb[e] * f2.x - xb[e + 1] * f2.y;
-            yb[e + 1] = xb[e + 1] * f2.x + xb[e] * f2.y;
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            ya[e] = xa[e] * cs[e].x - xb[e] * cs[e].y;
-            yb[e] = xb[e] * cs[e].x + xa[e] * cs[e].y;
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          xa[e] = ya[e];
-          xb[e] = yb[e];
-        }
+    if (t0 + step < A.rows) {  // the warp's next tokens
+      const int64_t n = min(t + step, end);
+      p = __ldg(A.pos + n);
+      slot = __ldg(A.S.slots + n);
+      for (int x = hf * A.D + li * LINE; x < last; x += (32 >> lt) * LINE) {
+        prefetch_line(A.k + n * A.ldk + x);
+        prefetch_line(A.v + n * A.ldv + x);
       }
-      if (h < A.Hq && on) {
-        T* dst = qo + h * A.D;
-        st_vec(dst, pack<T, VEC>(xa));
-        st_vec(dst + half, pack<T, VEC>(xb));
+    }
+    float xa[N][VEC], xb[N][VEC];
+    uint32_t m[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      unpack<VEC>(a[j], xa[j]);
+      unpack<VEC>(b[j], xb[j]);
+      if (j < KP) turn<VEC, IL>(xa[j], xb[j], cs);
+      m[j] = on ? max(abs_max_bits<VEC>(xa[j]), abs_max_bits<VEC>(xb[j])) : 0u;
+    }
+    float inv[N], sc[N];
+    for (int o = 1; o < lanes; o <<= 1)
+#pragma unroll
+      for (int j = 0; j < N; ++j) m[j] = max(m[j], __shfl_xor_sync(0xffffffffu, m[j], o));
+    if (lanes >= 2 * N) {
+      // lanes 2 j and 2 j + 1 of a group divide for 1 / scale and for the scale of j
+      uint32_t mine = m[0];
+#pragma unroll
+      for (int j = 1; j < N; ++j)
+        if (((lane >> 1) & (N - 1)) == j) mine = m[j];
+      const float am = q8_amax(mine);
+      const float d = __fdiv_rn(lane & 1 ? am : Q8Max<FMT>::v, lane & 1 ? Q8Max<FMT>::v : am);
+      const int base = lane & ~(lanes - 1);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        inv[j] = __shfl_sync(0xffffffffu, d, base | (2 * j));
+        sc[j] = __shfl_sync(0xffffffffu, d, base | (2 * j + 1));
       }
-      const bool kv = h >= A.Hq && h < HT && page >= 0;
-      if (__any_sync(0xffffffffu, kv)) {  // a warp's head rows may be both Q and K
-        uint32_t m = on ? max(abs_max_bits<VEC>(xa), abs_max_bits<VEC>(xb)) : 0u;
-        for (int o = lanes >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        // even lanes divide for 1 / scale, odd ones for the scale
-        const float am = q8_amax(m);
-        const bool odd = (lane & 1) != 0;
-        const float d = __fdiv_rn(odd ? am : Q8Max<FMT>::v, odd ? Q8Max<FMT>::v : am);
-        float inv = __shfl_sync(0xffffffffu, d, lane & ~1);
-        float scale = d;
-        if (lanes == 1) {  // a head per lane: both divisions are its own
-          inv = q8_inv<FMT>(am);
-          scale = __fdiv_rn(am, Q8Max<FMT>::v);
-        }
-        if (kv && on) {
-          const bool isk = h < HR;
-          const int hk = h - (isk ? A.Hq : HR);
-          uint8_t* dst = (isk ? A.K.q : A.V.q) + (isk ? A.K.cq.at(page, off, hk) : A.V.cq.at(page, off, hk)) + ia;
-          q8_store<FMT, VEC>(xa, inv, dst);
-          q8_store<FMT, VEC>(xb, inv, dst + half);
-          if (v == (lanes == 1 ? 0 : 1)) {
-            float* sc = isk ? A.K.sc + A.K.cs.at(page, off, hk) : A.V.sc + A.V.cs.at(page, off, hk);
-            *sc = m < kInfBits ? scale : __int_as_float(0x7fc00000);
-          }
-        }
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const float am = q8_amax(m[j]);
+        inv[j] = q8_inv<FMT>(am);
+        sc[j] = __fdiv_rn(am, Q8Max<FMT>::v);
+      }
+    }
+    if (page < 0 || !live) continue;  // nothing to store; no shuffles below
+    const int64_t kq = A.K.cq.at(page, off, hb) + ia, vq = A.V.cq.at(page, off, hb) + ia;
+    const int64_t ks = A.K.cs.at(page, off, hb), vs = A.V.cs.at(page, off, hb);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int i = j % KP;
+      if (i < W.kch && hb + G * i < A.Hk) {
+        const bool isk = j < KP;
+        uint8_t* dst = isk ? A.K.q + kq + G * i * A.K.cq.head : A.V.q + vq + G * i * A.V.cq.head;
+        q8_store<FMT, VEC>(xa[j], inv[j], dst);
+        q8_store<FMT, VEC>(xb[j], inv[j], dst + half);
+        if (v == 0)
+          *(isk ? A.K.sc + ks + G * i * A.K.cs.head : A.V.sc + vs + G * i * A.V.cs.head) =
+              m[j] < kInfBits ? sc[j] : __int_as_float(0x7fc00000);
       }
     }
   }
@@ -432,19 +512,31 @@ gbln_status write_launch(const WriteArgs<T>& A, bool cache_aligned, cudaStream_t
   const bool vec = A.D % (2 * VEC) == 0 && A.D / (2 * VEC) <= 32 && aligned16(A.table) && cache_aligned &&
                    (A.Hq == 0 || (row16(A.q, A.ldq) && row16(A.qo, A.ldqo))) && row16(A.k, A.ldk) && row16(A.v, A.ldv);
   if (vec) {
-    const int nu = A.D / (2 * VEC);
-    int lg = 0;
-    while ((1 << lg) < nu) ++lg;
-    const int G = 32 >> lg, L = (HT + G - 1) / G;  // head rows per lane and token
-    const int nchunk = (L + kWriteHeads - 1) / kWriteHeads;
-    const int ch = (L + nchunk - 1) / nchunk;
-    const int cy = nchunk < kWriteWarps ? nchunk : kWriteWarps, tz = kWriteWarps / cy;
+    WriteShape W{};
+    W.nu = A.D / (2 * VEC);
+    while ((1 << W.lg) < W.nu) ++W.lg;
+    const int lgG = 5 - W.lg, G = 1 << lgG;
+    // log2 of the tokens whose n heads share a warp's G groups
+    const auto tokens = [&](int n) {
+      int lt = lgG;
+      while (lt > 0 && (n << lt) > G) --lt;
+      return lt;
+    };
+    const int Lq = (A.Hq + G - 1) / G, Lk = (A.Hk + G - 1) / G;  // head rows per lane and token
+    W.nq = (Lq + kWriteQ - 1) / kWriteQ;
+    W.qch = W.nq ? (Lq + W.nq - 1) / W.nq : 0;
+    W.qlt = W.nq ? tokens(A.Hq) : 0;
+    W.nkv = (Lk + 1) / 2;
+    W.kch = (Lk + W.nkv - 1) / W.nkv;
+    W.klt = tokens(A.Hk);
+    const int n = W.nq + W.nkv, cy = n < kWriteWarps ? n : kWriteWarps, tz = kWriteWarps / cy;
     const int sms = sm_count();
     if (sms <= 0) return GBLN_ERR_CUDA;
-    const int64_t gy = (nchunk + cy - 1) / cy;
+    const int64_t gy = (n + cy - 1) / cy;
     if (gy <= 65535) {
-      const unsigned gx = grid_for(A.rows, tz, (int64_t)sms * kWriteGrid);
-      cache8_write_vec<T, IL, FMT><<<dim3(gx, (unsigned)gy), dim3(32, cy, tz), 0, s>>>(A, nu, lg, ch);
+      const dim3 grid(grid_for(A.rows, tz, (int64_t)sms * kWriteGrid), (unsigned)gy), block(32, cy, tz);
+      if (W.kch == 1) cache8_write_vec<T, IL, FMT, 1><<<grid, block, 0, s>>>(A, W);
+      else cache8_write_vec<T, IL, FMT, 2><<<grid, block, 0, s>>>(A, W);
       return launch_status();
     }
   }
