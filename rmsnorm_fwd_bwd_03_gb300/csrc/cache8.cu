@@ -369,8 +369,8 @@ __global__ void __launch_bounds__(256) cache8_write_elem(const WriteArgs<T> A) {
 }
 
 // ---------------------------------------------------------------------------
-// Read-back: a warp per token, then the next one (the slot of which it has
-// loaded by then).  A unit is N consecutive codes of one head: on the vector path
+// Read-back: a warp per token (several, where their heads leave lanes over), then
+// the next one (the slot of which it has loaded by then).  A unit is N consecutive codes of one head: on the vector path
 // as many as fill a 16-byte store (8 codes at bf16, 4 at float32), so that a
 // warp's loads and its stores are both contiguous.  A head takes a power of two of
 // lanes, which spares the units a division; four heads per lane of K and of V are
@@ -390,62 +390,67 @@ struct ReadArgs {
   unsigned int* err;
 };
 
-constexpr int kReadHeads = 4;
-constexpr int kReadGrid = 3;  // blocks per SM, all resident
+// Blocks per SM, all resident: three at four heads of K and V per lane, four below.
+constexpr int read_blocks(int heads) { return heads == 4 ? 3 : 4; }
 
-template <typename T, int FMT, int N>
-__global__ void __launch_bounds__(256) cache8_read_kernel(const ReadArgs<T> A, int per, int lg) {
-  constexpr int U = kReadHeads;
+template <typename T, int FMT, int N, int U>
+__global__ void __launch_bounds__(256) cache8_read_kernel(const ReadArgs<T> A, int per, int lg, int lt) {
   const int lane = threadIdx.x & 31;
-  const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
-  int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (t >= A.rows) return;  // uniform per warp
-  const int lanes = 1 << lg, G = 32 >> lg;
-  const int d0 = lane & (lanes - 1), hb = lane >> lg;
-  int64_t off = 0, page = A.S.page_of(__ldg(A.S.slots + t), off);
+  const int64_t step = ((int64_t)gridDim.x * (blockDim.x >> 5)) << lt;
+  int64_t t0 = ((int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) << lt;
+  if (t0 >= A.rows) return;  // uniform per warp
+  // the lanes of a group take a head of one of the warp's 2^lt tokens
+  const int lanes = 1 << lg, G = 32 >> (lg + lt);
+  const int sub = (lane >> lg) >> (5 - lg - lt), hb = (lane >> lg) & (G - 1);
+  const int d0 = lane & (lanes - 1);
+  const bool lead = (lane & ((32 >> lt) - 1)) == 0;
+  int64_t off = 0, page = -1;
+  if (t0 + sub < A.rows) page = A.S.page_of(__ldg(A.S.slots + t0 + sub), off);
 #pragma unroll 1
-  for (; t < A.rows; t += step) {
-    const bool more = t + step < A.rows;
-    const int64_t next = more ? __ldg(A.S.slots + t + step) : -1;
-    T *ko = A.ko + t * A.ldk, *vo = A.vo + t * A.ldv;
-    if (page >= 0) {
-      const uint8_t *kq = A.K.q + A.K.cq.at(page, off, 0), *vq = A.V.q + A.V.cq.at(page, off, 0);
-      const float *ks = A.K.sc + A.K.cs.at(page, off, 0), *vs = A.V.sc + A.V.cs.at(page, off, 0);
-      for (int d = d0; d < per; d += lanes) {  // once, for heads of up to 32 units
-        for (int h0 = hb; h0 < A.Hk; h0 += U * G) {
-          Codes<FMT, N> kw[U], vw[U];
-          float kc[U], vc[U];
+  for (; t0 < A.rows; t0 += step) {
+    const int64_t t = t0 + sub;
+    const int64_t next = t + step < A.rows ? __ldg(A.S.slots + t + step) : -1;
+    if (t < A.rows) {
+      T *ko = A.ko + t * A.ldk, *vo = A.vo + t * A.ldv;
+      if (page >= 0) {
+        const uint8_t *kq = A.K.q + A.K.cq.at(page, off, 0), *vq = A.V.q + A.V.cq.at(page, off, 0);
+        const float *ks = A.K.sc + A.K.cs.at(page, off, 0), *vs = A.V.sc + A.V.cs.at(page, off, 0);
+        for (int d = d0; d < per; d += lanes) {  // once, for heads of up to 32 units
+          for (int h0 = hb; h0 < A.Hk; h0 += U * G) {
+            Codes<FMT, N> kw[U], vw[U];
+            float kc[U], vc[U];
 #pragma unroll
-          for (int j = 0; j < U; ++j) {
-            const int h = min(h0 + j * G, A.Hk - 1);  // past the last head: that one again, not stored
-            kw[j].load(kq + h * A.K.cq.head + d * N);
-            vw[j].load(vq + h * A.V.cq.head + d * N);
-            kc[j] = __ldg(ks + h * A.K.cs.head);
-            vc[j] = __ldg(vs + h * A.V.cs.head);
-          }
+            for (int j = 0; j < U; ++j) {
+              const int h = min(h0 + j * G, A.Hk - 1);  // past the last head: that one again, not stored
+              kw[j].load(kq + h * A.K.cq.head + d * N);
+              vw[j].load(vq + h * A.V.cq.head + d * N);
+              kc[j] = __ldg(ks + h * A.K.cs.head);
+              vc[j] = __ldg(vs + h * A.V.cs.head);
+            }
 #pragma unroll
-          for (int j = 0; j < U; ++j) {
-            const int h = h0 + j * G;
-            if (h < A.Hk) {
-              float v[N];
-              kw[j].get(v, kc[j]);
-              store_n<T, N>(ko + h * A.D + d * N, v);
-              vw[j].get(v, vc[j]);
-              store_n<T, N>(vo + h * A.D + d * N, v);
+            for (int j = 0; j < U; ++j) {
+              const int h = h0 + j * G;
+              if (h < A.Hk) {
+                float v[N];
+                kw[j].get(v, kc[j]);
+                store_n<T, N>(ko + h * A.D + d * N, v);
+                vw[j].get(v, vc[j]);
+                store_n<T, N>(vo + h * A.D + d * N, v);
+              }
             }
           }
         }
-      }
-    } else {  // no slot: zeros; a slot outside the cache: NaN
-      if (page == -2 && lane == 0) atomicOr(A.err, kErrBadSlot);
-      float fill[N];
+      } else {  // no slot: zeros; a slot outside the cache: NaN
+        if (page == -2 && lead) atomicOr(A.err, kErrBadSlot);
+        float fill[N];
 #pragma unroll
-      for (int e = 0; e < N; ++e) fill[e] = page == -2 ? __int_as_float(0x7fc00000) : 0.f;
-      for (int d = d0; d < per; d += lanes)
-        for (int h = hb; h < A.Hk; h += G) {
-          store_n<T, N>(ko + h * A.D + d * N, fill);
-          store_n<T, N>(vo + h * A.D + d * N, fill);
-        }
+        for (int e = 0; e < N; ++e) fill[e] = page == -2 ? __int_as_float(0x7fc00000) : 0.f;
+        for (int d = d0; d < per; d += lanes)
+          for (int h = hb; h < A.Hk; h += G) {
+            store_n<T, N>(ko + h * A.D + d * N, fill);
+            store_n<T, N>(vo + h * A.D + d * N, fill);
+          }
+      }
     }
     page = A.S.page_of(next, off);
   }
@@ -560,11 +565,21 @@ gbln_status read_typed(const ReadArgs<T>& A, int fmt, bool cache_aligned, cudaSt
                    (A.ldk * (int64_t)sizeof(T)) % 16 == 0 && (A.ldv * (int64_t)sizeof(T)) % 16 == 0;
   const int sms = sm_count();
   if (sms <= 0) return GBLN_ERR_CUDA;
-  const unsigned grid = grid_for(A.rows, 8, (int64_t)sms * kReadGrid);
   const int per = A.D / (vec ? VEC : 1);  // units per head
   int lg = 0;
   while (lg < 5 && (1 << lg) < per) ++lg;
-#define GBLN_READ8(FMT, N) cache8_read_kernel<T, FMT, N><<<grid, 256, 0, s>>>(A, per, lg)
+  int lt = 5 - lg;  // log2 of the tokens whose heads share a warp's groups
+  while (lt > 0 && ((int64_t)A.Hk << (lt + lg)) > 32) --lt;
+  const int G = 32 >> (lg + lt), steps = (A.Hk + G - 1) / G;  // heads per lane
+  const int64_t warps = (A.rows + (1 << lt) - 1) >> lt;
+#define GBLN_READ8_U(FMT, N, U) \
+  cache8_read_kernel<T, FMT, N, U><<<grid_for(warps, 8, (int64_t)sms * read_blocks(U)), 256, 0, s>>>(A, per, lg, lt)
+#define GBLN_READ8(FMT, N)                  \
+  do {                                      \
+    if (steps == 1) GBLN_READ8_U(FMT, N, 1);      \
+    else if (steps == 2) GBLN_READ8_U(FMT, N, 2); \
+    else GBLN_READ8_U(FMT, N, 4);                 \
+  } while (0)
   if (fmt == GBLN_Q8_INT8) {
     if (vec) GBLN_READ8(GBLN_Q8_INT8, VEC);
     else GBLN_READ8(GBLN_Q8_INT8, 1);
@@ -573,6 +588,7 @@ gbln_status read_typed(const ReadArgs<T>& A, int fmt, bool cache_aligned, cudaSt
     else GBLN_READ8(GBLN_Q8_E4M3, 1);
   }
 #undef GBLN_READ8
+#undef GBLN_READ8_U
   return launch_status();
 }
 
