@@ -351,3 +351,50 @@ def test_prefill_then_decode_attention():
         # its scale: 1/127 of its largest value) in a few of its values, far less than that
         d = 2 * 2.0 ** -9 * max((np.abs(K64[:s.stop, h // (Hq // Hk)]) @ np.abs(Q64[s.stop - 1, h])).max() for h in range(Hq)) / D ** 0.5
         assert (np.abs(got - want) <= 1.5 * d * np.abs(V64[:s.stop]).max()).all()
+
+
+def test_more_than_two_to_the_31_slots():
+    # slot numbers past 31 bits (13 GB for each of K and V): page and offset come from a
+    # 64-bit division
+    Hk, D, page, pages = 1, 2, 16, 2 ** 27 + 5
+    cache = [torch.empty((pages, page, Hk, D), dtype=torch.int8, device="cuda"), torch.empty((pages, page, Hk), device="cuda"),
+             torch.empty((pages, page, Hk, D), dtype=torch.int8, device="cuda"), torch.empty((pages, page, Hk), device="cuda")]
+    slots = torch.tensor([0, 2 ** 31 - 1, 2 ** 31, pages * page - 1, 12345678], device="cuda")
+    T = len(slots)
+    k, v = _randn((T, Hk, D), torch.float32, 1), _randn((T, Hk, D), torch.float32, 2)
+    gb.rope_fwd_cache8(None, k, v, torch.zeros(T, dtype=torch.int32, device="cuda"), gb.rope_table(1, D, THETA), slots, *cache)
+    ko, vo = gb.cache8_read(slots, *cache, dtype=torch.float32)
+    for got, x in ((ko, k), (vo, v)):
+        assert np.array_equal(to64(got), q8.values(*q8.quantize(to64(x), "int8")).astype(np.float32).astype(np.float64))
+    gb.cache8_read(torch.tensor([pages * page], device="cuda"), *cache)
+    assert gb.device_error(clear=True) == gb.ERR_BAD_SLOT
+
+
+def test_two_streams_write_and_read_the_same_caches():
+    # two halves of a batch stored at once from two streams, then read at once
+    T, Hq, Hk, D, page = 4096, 8, 4, 128, 16
+    qkv = _randn((T, (Hq + 2 * Hk) * D), torch.bfloat16, 1)
+    q, k, v = (t.unflatten(1, (-1, D)) for t in qkv.split([Hq * D, Hk * D, Hk * D], dim=1))
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    table = gb.rope_table(T, D, THETA)
+    slots = torch.randperm(T, generator=torch.Generator().manual_seed(3)).cuda()
+    one, two = _caches(T // page, page, Hk, D, "e4m3"), _caches(T // page, page, Hk, D, "e4m3")
+    qo = gb.rope_fwd_cache8(q, k, v, pos, table, slots, *one)
+    ko, vo = gb.cache8_read(slots, *one)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    halves = (slice(0, 2050), slice(2050, T))
+    torch.cuda.synchronize()
+    outs = []
+    for st, s in zip(streams, halves):
+        with torch.cuda.stream(st):
+            outs.append(gb.rope_fwd_cache8(q[s], k[s], v[s], pos[s], table, slots[s], *two))
+    torch.cuda.synchronize()
+    assert torch.equal(torch.cat(outs), qo)
+    for a, b in zip(one, two):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    outs = []
+    for st, s in zip(streams, halves):
+        with torch.cuda.stream(st):
+            outs.append(gb.cache8_read(slots[s], *two))
+    torch.cuda.synchronize()
+    assert torch.equal(torch.cat([o[0] for o in outs]), ko) and torch.equal(torch.cat([o[1] for o in outs]), vo)

@@ -635,3 +635,22 @@ def test_norm_of_more_than_two_to_the_31_values():
         check_exact(h8[t], hs[t], X, "e4m3", "h8", 128)
         kept = q8.values(codes64(h8[t]), codes64(hs[t]), 128)
         check_io(to64(dx[t]), q8.rmsnorm_bwd_kept(X, X, kept, W, rs)[0], "bf16", "dx")
+
+
+def test_two_streams_at_once():
+    T, H = 2000, 2048
+    states = []
+    for seed in (1, 100):
+        s = {n: _randn((T, H), torch.bfloat16, seed + i) for i, n in enumerate(("x", "r", "dres", "y", "h"))}
+        s |= {"w": _weight(H, torch.bfloat16), "dout": _randn((T, H // 2), torch.bfloat16, seed + 7), "out": _randn((T, H // 2), torch.bfloat16, 0)}
+        states.append((s, [t.clone() for t in _step(s)]))
+    streams = [torch.cuda.Stream() for _ in states]
+    torch.cuda.synchronize()
+    got = []
+    for st, (s, _) in zip(streams, states):
+        with torch.cuda.stream(st):
+            got.append(_step(s))
+    torch.cuda.synchronize()
+    for g, (_, want) in zip(got, states):
+        for p, q in zip(g, want):
+            assert _same_bits(p, q)
