@@ -768,6 +768,12 @@ struct GluCkptIn {
 };
 
 constexpr int kCkptRows = 4;
+// Blocks per SM, far more than are resident: blocks that end and start at different
+// times keep loads and stores mixed, where resident ones that loop over all the
+// units fall into step (forward 549..556 us from 64 to 128 blocks, 573 at 24, 620
+// at the 3 that are resident; 32768 x 14336 bf16, 558 us at the copy rate).  With
+// one unit per block the GeLU forms lose what the loop overlaps (655 us).
+constexpr int kCkptGrid = 64;
 
 // u / n of unit numbers, which fit 32 bits in all but absurd sizes (a 64-bit
 // division takes as long as a dozen values).
@@ -802,6 +808,14 @@ glu_fwd_ckpt(const T* gate, const T* up, T* out, const GluCkpt C, int64_t T_, in
         g[k] = ld_stream(gate + (r0 + k) * ldg + c * VEC);
         v[k] = ld_stream(up + (r0 + k) * ldu + c * VEC);
       }
+    }
+    // The block's next unit on its way to L2: cb / 8 lines of each row and tensor, one
+    // per thread.
+    if (u + gridDim.x < units) {
+      const int64_t un = u + gridDim.x, rn = unit_div(un, ncb, small);
+      const int n = cb / 8, row8 = threadIdx.x / n, line = threadIdx.x - row8 * n;
+      const int64_t col = ((un - rn * ncb) * cb + line * 8) * VEC, r = rn * U + (row8 >> 1);
+      if (r < T_ && col < I) prefetch_line((row8 & 1 ? up + r * ldu : gate + r * ldg) + col);
     }
     uint32_t m[2 * U];  // gate and up of row 0, of row 1, ...
 #pragma unroll
@@ -1244,11 +1258,11 @@ void glu_fwd_ckpt_launch(const void* g, const void* u, void* o, GluCkpt C, int64
     const int64_t ncol = I / VEC;
     const int cb = col_block(ncol);
     const int64_t units = (rows + kCkptRows - 1) / kCkptRows * ((ncol + cb - 1) / cb);
-    glu_fwd_ckpt<T, ACT, FMT><<<resident_grid(units, cb), cb, 0, s>>>((const T*)g, (const T*)u, (T*)o, C,
+    glu_fwd_ckpt<T, ACT, FMT><<<grid_for(units, 1, (int64_t)sm_count() * kCkptGrid), cb, 0, s>>>((const T*)g, (const T*)u, (T*)o, C,
                                                                         rows, ncol, ldg, ldu, ldo);
   } else {
     const int64_t units = rows * ((I + kCkptGroup - 1) / kCkptGroup), per = kGluBlock / 32 * kElemFlight;
-    glu_fwd_ckpt_elem<T, ACT, FMT><<<resident_grid((units + per - 1) / per), kGluBlock, 0, s>>>(
+    glu_fwd_ckpt_elem<T, ACT, FMT><<<grid_for((units + per - 1) / per, 1, (int64_t)sm_count() * kCkptGrid), kGluBlock, 0, s>>>(
         (const T*)g, (const T*)u, (T*)o, C, rows, I, ldg, ldu, ldo);
   }
 }
@@ -1257,17 +1271,17 @@ template <typename T, int ACT, int FMT>
 void glu_bwd_ckpt_launch(const void* d, GluCkptIn C, void* dg, void* du, int64_t rows, int64_t I,
                          int64_t ldd, int64_t lddg, int64_t lddu, cudaStream_t s) {
   constexpr int VEC = VecOf<T>::N;
-  constexpr int U = 2;
+  constexpr int U = kCkptRows;
   const bool vec = I % VEC == 0 && aligned16(d) && aligned16(dg) && aligned16(du) && ldd % VEC == 0 &&
                    lddg % VEC == 0 && lddu % VEC == 0 && aligned_to(C.gq, VEC) && aligned_to(C.uq, VEC);
   if (vec) {
     const int64_t ncol = I / VEC;
     const int cb = col_block(ncol);
-    const unsigned grid = resident_grid((rows + U - 1) / U * ((ncol + cb - 1) / cb), cb);
+    const unsigned grid = grid_for((rows + U - 1) / U * ((ncol + cb - 1) / cb), 1, (int64_t)sm_count() * kCkptGrid);
     glu_bwd_ckpt<T, ACT, FMT, U><<<grid, cb, 0, s>>>((const T*)d, C, (T*)dg, (T*)du, rows, ncol, ldd, lddg, lddu);
   } else {
     const int64_t units = rows * ((I + kCkptGroup - 1) / kCkptGroup), per = kGluBlock / 32 * kElemFlight;
-    glu_bwd_ckpt_elem<T, ACT, FMT><<<resident_grid((units + per - 1) / per), kGluBlock, 0, s>>>(
+    glu_bwd_ckpt_elem<T, ACT, FMT><<<grid_for((units + per - 1) / per, 1, (int64_t)sm_count() * kCkptGrid), kGluBlock, 0, s>>>(
         (const T*)d, C, (T*)dg, (T*)du, rows, I, ldd, lddg, lddu);
   }
 }
