@@ -63,11 +63,6 @@ struct WriteArgs {
   Slots S;
   Cache K, V;
   unsigned int* err;
-  __device__ __forceinline__ const T* src(int64_t t, int h) const {
-    if (h < Hq) return q + t * ldq + (int64_t)h * D;
-    if (h < Hq + Hk) return k + t * ldk + (int64_t)(h - Hq) * D;
-    return v + t * ldv + (int64_t)(h - Hq - Hk) * D;
-  }
 };
 
 // ---------------------------------------------------------------------------
@@ -84,7 +79,8 @@ struct WriteArgs {
 // divisions of its K and V heads run side by side.  (With queries, K and V taken
 // alike, head after head, the chain of each one's reduction and division showed:
 // 95 us instead of 77 for 32768 tokens of 16 / 8 heads of 128, 70 us at the copy
-// rate.)
+// rate.)  65536 tokens of 32 / 8 heads of 128: 223 us, 219 us at the copy rate; 16
+// tokens 2.7 us.
 // ---------------------------------------------------------------------------
 // Head rows per lane and pass of a query warp: 8 measured 112 us, 6 119 and 4 117 for
 // 32768 tokens of 32 / 8 heads of 128 (110 us at the copy rate).
@@ -305,66 +301,104 @@ cache8_write_vec(const WriteArgs<T> A, const WriteShape W) {
 }
 
 // Element path (any head size, alignment and stride): a warp per head row, a
-// lane the pairs l, l + 32, ...; K and V are read twice, the second time from L1.
-template <typename T, bool IL, int FMT>
-__global__ void __launch_bounds__(256) cache8_write_elem(const WriteArgs<T> A) {
+// lane the pairs l, l + 32, ..., which wait in registers for the head's maximum
+// (FITS: heads of up to 2 * 32 * kElemPairs values; wider ones are read twice, the
+// second time from L1).  16384 tokens of 8 / 8 heads of 72: 174 us (14 us at the
+// copy rate): bound by the latency of its short warps.
+constexpr int kElemPairs = 4;
+
+template <typename T, bool IL, int FMT, bool FITS>
+__global__ void __launch_bounds__(256) cache8_write_elem(const WriteArgs<T> A, bool small) {
+  constexpr int K = FITS ? kElemPairs : 1;
   const int half = A.D / 2, HR = A.Hq + A.Hk, HT = HR + A.Hk;
   const int lane = threadIdx.x & 31;
-  const int64_t step = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  for (int64_t item = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; item < A.rows * HT; item += step) {
-    const int64_t t = item / HT;
+  const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
+  for (int64_t item = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp_index(); item < A.rows * HT; item += step) {
+    const int64_t t = small ? (int64_t)((uint32_t)item / (uint32_t)HT) : item / HT;
     const int h = (int)(item - t * HT);
-    int64_t off = 0;
-    const int64_t page = A.S.page_of(__ldg(A.S.slots + t), off);
+    const int64_t slot = __ldg(A.S.slots + t);
     const int p = __ldg(A.pos + t);
+    const T* src = h < A.Hq ? A.q + t * A.ldq + (int64_t)h * A.D
+                   : h < HR ? A.k + t * A.ldk + (int64_t)(h - A.Hq) * A.D
+                            : A.v + t * A.ldv + (int64_t)(h - HR) * A.D;
     const bool ok = p >= 0 && (int64_t)p < A.max_pos;
+    const float2* turns = A.table + (ok ? (size_t)p * half : 0);
+    auto load = [&](int i, float& x1, float& x2, float2& f) {
+      x1 = to_f32(src[IL ? 2 * i : i]);
+      x2 = to_f32(src[IL ? 2 * i + 1 : half + i]);
+      const float qnan = __int_as_float(0x7fc00000);
+      f = h >= HR ? make_float2(1.f, 0.f) : ok ? __ldg(turns + i) : make_float2(qnan, qnan);
+    };
+    // V is not rotated: it is taken as it is, whatever it holds
+    auto turned = [&](float x1, float x2, float2 f) {
+      return h >= HR ? make_float2(x1, x2) : make_float2(x1 * f.x - x2 * f.y, x2 * f.x + x1 * f.y);
+    };
+    float2 y[K];
+    if constexpr (FITS) {
+      float x1[K], x2[K];
+      float2 f[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (lane + 32 * k < half) load(lane + 32 * k, x1[k], x2[k], f[k]);
+#pragma unroll
+      for (int k = 0; k < K; ++k) y[k] = lane + 32 * k < half ? turned(x1[k], x2[k], f[k]) : both(0.f);
+    }
+    auto pair = [&](int i) {
+      float x1, x2;
+      float2 f;
+      load(i, x1, x2, f);
+      return turned(x1, x2, f);
+    };
+    int64_t off = 0;
+    const int64_t page = A.S.page_of(slot, off);
     if (h == 0 && lane == 0) {
       if (!ok && (A.Hq > 0 || page >= 0)) atomicOr(A.err, kErrBadPosition);
       if (page == -2) atomicOr(A.err, kErrBadSlot);
     }
-    if (h >= A.Hq && page < 0) continue;
-    const T* src = A.src(t, h);
-    auto pair = [&](int i, float& y1, float& y2) {
-      const float x1 = to_f32(src[IL ? 2 * i : i]), x2 = to_f32(src[IL ? 2 * i + 1 : half + i]);
-      if (h < HR) {
-        const float qnan = __int_as_float(0x7fc00000);
-        const float2 f = ok ? __ldg(A.table + (size_t)p * half + i) : make_float2(qnan, qnan);
-        y1 = x1 * f.x - x2 * f.y;
-        y2 = x2 * f.x + x1 * f.y;
-      } else {
-        y1 = x1;
-        y2 = x2;
-      }
-    };
     if (h < A.Hq) {
       T* dst = A.qo + t * A.ldqo + (int64_t)h * A.D;
-      for (int i = lane; i < half; i += 32) {
-        float y1, y2;
-        pair(i, y1, y2);
-        dst[IL ? 2 * i : i] = from_f32<T>(y1);
-        dst[IL ? 2 * i + 1 : half + i] = from_f32<T>(y2);
+      auto put = [&](int i, float2 v) {
+        dst[IL ? 2 * i : i] = from_f32<T>(v.x);
+        dst[IL ? 2 * i + 1 : half + i] = from_f32<T>(v.y);
+      };
+      if constexpr (FITS) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (lane + 32 * k < half) put(lane + 32 * k, y[k]);
+      } else {
+        for (int i = lane; i < half; i += 32) put(i, pair(i));
       }
       continue;
     }
+    if (page < 0) continue;
     uint32_t m = 0;
-    for (int i = lane; i < half; i += 32) {
-      float y1, y2;
-      pair(i, y1, y2);
-      m = max(m, max(abs_bits(y1), abs_bits(y2)));
+    if constexpr (FITS) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) m = max(m, max(abs_bits(y[k].x), abs_bits(y[k].y)));
+    } else {
+      for (int i = lane; i < half; i += 32) {
+        const float2 v = pair(i);
+        m = max(m, max(abs_bits(v.x), abs_bits(v.y)));
+      }
     }
     m = group_max<32>(m);
     const float am = q8_amax(m), inv = q8_inv<FMT>(am);
     const bool isk = h < HR;
     const int hk = h - (isk ? A.Hq : HR);
-    const Cache& C = isk ? A.K : A.V;
-    uint8_t* dst = C.q + C.cq.at(page, off, hk);
-    for (int i = lane; i < half; i += 32) {
-      float y1, y2;
-      pair(i, y1, y2);
-      dst[IL ? 2 * i : i] = (uint8_t)q8_code1<FMT>(y1, inv);
-      dst[IL ? 2 * i + 1 : half + i] = (uint8_t)q8_code1<FMT>(y2, inv);
+    uint8_t* dst = isk ? A.K.q + A.K.cq.at(page, off, hk) : A.V.q + A.V.cq.at(page, off, hk);
+    auto put = [&](int i, float2 v) {
+      dst[IL ? 2 * i : i] = (uint8_t)q8_code1<FMT>(v.x, inv);
+      dst[IL ? 2 * i + 1 : half + i] = (uint8_t)q8_code1<FMT>(v.y, inv);
+    };
+    if constexpr (FITS) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (lane + 32 * k < half) put(lane + 32 * k, y[k]);
+    } else {
+      for (int i = lane; i < half; i += 32) put(i, pair(i));
     }
-    if (lane == 0) C.sc[C.cs.at(page, off, hk)] = q8_scale<FMT>(am, m);
+    if (lane == 0)
+      *(isk ? A.K.sc + A.K.cs.at(page, off, hk) : A.V.sc + A.V.cs.at(page, off, hk)) = q8_scale<FMT>(am, m);
   }
 }
 
@@ -545,7 +579,10 @@ gbln_status write_launch(const WriteArgs<T>& A, bool cache_aligned, cudaStream_t
       return launch_status();
     }
   }
-  cache8_write_elem<T, IL, FMT><<<grid_for(A.rows * HT, 8, 1 << 20), 256, 0, s>>>(A);
+  const unsigned grid = grid_for(A.rows * HT, 8, 1 << 20);
+  const bool small = A.rows * HT <= 0xffffffffLL;
+  if (A.D <= 2 * 32 * kElemPairs) cache8_write_elem<T, IL, FMT, true><<<grid, 256, 0, s>>>(A, small);
+  else cache8_write_elem<T, IL, FMT, false><<<grid, 256, 0, s>>>(A, small);
   return launch_status();
 }
 
