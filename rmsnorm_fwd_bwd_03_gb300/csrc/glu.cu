@@ -19,6 +19,7 @@
 // 128 values of a row) that a backward pass reads.
 
 #include <atomic>
+#include <type_traits>
 
 #include <cooperative_groups.h>
 
@@ -862,80 +863,84 @@ glu_fwd_ckpt(const T* gate, const T* up, T* out, const GluCkpt C, int64_t T_, in
   }
 }
 
-// Any alignment and width: one warp per checkpoint group and pass, lane l the
-// values l, l + 32, l + 64, l + 96 of it, two groups in flight per warp.  8190 x
-// 4097 bf16 62 us, the backward 68 us (40 us at the copy rate): bound by their
-// instructions.
-constexpr int kElemFlight = 2;
+// Any alignment and width: a warp takes four consecutive checkpoint groups of a row,
+// lane l the values l, l + 32, l + 64, l + 96 of each; the groups share one division
+// and the 64-bit addresses, which two groups of their own addresses spent a tenth of
+// the time on.  8190 x 4097 bf16 55 us (that form 62), the backward 59 (68), of 40 us
+// at the copy rate: bound by their instructions.
+constexpr int kElemGroups = 4;
+
+// unit(F, FULL, first value, values) over a warp's `left` values: four groups at once
+// where they are whole, else one by one.
+template <typename Unit>
+__device__ __forceinline__ void row_groups(int left, Unit unit) {
+  using One = std::integral_constant<int, 1>;
+  if (left == kElemGroups * kCkptGroup) {
+    unit(std::integral_constant<int, kElemGroups>{}, std::true_type{}, 0, left);
+  } else {
+    int c = 0;
+    for (; c + kCkptGroup <= left; c += kCkptGroup) unit(One{}, std::true_type{}, c, kCkptGroup);
+    if (c < left) unit(One{}, std::false_type{}, c, left - c);
+  }
+}
+
+template <typename T, int ACT, int FMT, int F, bool FULL>
+__device__ __forceinline__ void glu_fwd_ckpt_unit(const T* gp, const T* up, T* op, uint8_t* gq, uint8_t* uq,
+                                                  float* gs, float* us, int left, int lane) {
+  T g[F][4], v[F][4];
+#pragma unroll
+  for (int f = 0; f < F; ++f) {
+    load_run<FULL>(gp + f * kCkptGroup, left - f * kCkptGroup - lane, g[f]);
+    load_run<FULL>(up + f * kCkptGroup, left - f * kCkptGroup - lane, v[f]);
+  }
+  // Lane 4 f divides for 1 / scale of gate's group f, lane 4 f + 2 of up's, the lane
+  // after each for the scale.
+  uint32_t mine = 0;
+#pragma unroll
+  for (int f = 0; f < F; ++f) {
+    const float gf[4] = {to_f32(g[f][0]), to_f32(g[f][1]), to_f32(g[f][2]), to_f32(g[f][3])};
+    const float uf[4] = {to_f32(v[f][0]), to_f32(v[f][1]), to_f32(v[f][2]), to_f32(v[f][3])};
+    const uint32_t gm = group_max<32>(abs_max_bits<4>(gf)), um = group_max<32>(abs_max_bits<4>(uf));
+    if (lane >> 2 == f) mine = lane & 2 ? um : gm;
+  }
+  const float a = q8_amax(mine);
+  const float d = __fdiv_rn(lane & 1 ? a : Q8Max<FMT>::v, lane & 1 ? Q8Max<FMT>::v : a);
+  if (lane < 4 * F && (lane & 1) && (FULL || (lane >> 2) * kCkptGroup < left))
+    (lane & 2 ? us : gs)[lane >> 2] = mine < kInfBits ? d : __int_as_float(0x7fc00000);
+#pragma unroll
+  for (int f = 0; f < F; ++f) {
+    const float gi = __shfl_sync(0xffffffffu, d, 4 * f), ui = __shfl_sync(0xffffffffu, d, 4 * f + 2);
+    const float gf[4] = {to_f32(g[f][0]), to_f32(g[f][1]), to_f32(g[f][2]), to_f32(g[f][3])};
+    const float uf[4] = {to_f32(v[f][0]), to_f32(v[f][1]), to_f32(v[f][2]), to_f32(v[f][3])};
+    const int rem = left - f * kCkptGroup - lane;
+    float o[4];
+    glu_values<T, ACT, 4>(gf, uf, o);
+    store_run<FULL>(op + f * kCkptGroup, rem, o);
+    store_run_codes<FULL, FMT>(gq + f * kCkptGroup, rem, gf, gi);
+    store_run_codes<FULL, FMT>(uq + f * kCkptGroup, rem, uf, ui);
+  }
+}
 
 template <typename T, int ACT, int FMT>
 __global__ void __launch_bounds__(kGluBlock)
 glu_fwd_ckpt_elem(const T* gate, const T* up, T* out, const GluCkpt C, int64_t T_, int64_t I, int64_t ldg,
                   int64_t ldu, int64_t ldo) {
-  constexpr int F = kElemFlight;
+  constexpr int W = kElemGroups * kCkptGroup;  // values per unit
   const int lane = threadIdx.x & 31;
-  const int64_t ng = (I + kCkptGroup - 1) / kCkptGroup, n = T_ * ng;
-  const bool small = n + F <= 0xffffffffLL;
-  const int64_t step = (int64_t)gridDim.x * (kGluBlock / 32) * F;
-  for (int64_t u = ((int64_t)blockIdx.x * (kGluBlock / 32) + warp_index()) * F; u < n; u += step) {
-    T g[F][4], v[F][4];
-    int64_t row[F], j0[F];
-#pragma unroll
-    for (int f = 0; f < F; ++f) {
-      row[f] = unit_div(u + f, ng, small);
-      j0[f] = (u + f - row[f] * ng) * kCkptGroup + lane;
-      if (u + f >= n) continue;
-      const T *gp = gate + row[f] * ldg + j0[f], *up_ = up + row[f] * ldu + j0[f];
-      const int rem = (int)(I - j0[f] < kCkptGroup ? I - j0[f] : (int64_t)kCkptGroup);
-      if (j0[f] - lane + kCkptGroup <= I) {
-        load_run<true>(gp, rem, g[f]);
-        load_run<true>(up_, rem, v[f]);
-      } else {
-        load_run<false>(gp, rem, g[f]);
-        load_run<false>(up_, rem, v[f]);
-      }
-    }
-    // Maxima of the F groups of gate and of up; lane 4 f + 2 (up) divides for that
-    // group's 1 / scale, the lane after it for the scale.
-    uint32_t gm[F], um[F];
-#pragma unroll
-    for (int f = 0; f < F; ++f) {
-      if (u + f >= n) {
-        gm[f] = um[f] = 0;
-        continue;  // uniform per warp
-      }
-      const float gf[4] = {to_f32(g[f][0]), to_f32(g[f][1]), to_f32(g[f][2]), to_f32(g[f][3])};
-      const float uf[4] = {to_f32(v[f][0]), to_f32(v[f][1]), to_f32(v[f][2]), to_f32(v[f][3])};
-      gm[f] = group_max<32>(abs_max_bits<4>(gf));
-      um[f] = group_max<32>(abs_max_bits<4>(uf));
-    }
-    static_assert(F == 2, "one lane bit names a group");
-    const uint32_t mine = lane & 4 ? (lane & 2 ? um[1] : gm[1]) : (lane & 2 ? um[0] : gm[0]);
-    const float a = q8_amax(mine);
-    const float d = __fdiv_rn(lane & 1 ? a : Q8Max<FMT>::v, lane & 1 ? Q8Max<FMT>::v : a);
-    if (lane < 8 && (lane & 1) && u + (lane >> 2) < n)
-      (lane & 2 ? C.us : C.gs)[u + (lane >> 2)] = mine < kInfBits ? d : __int_as_float(0x7fc00000);
-#pragma unroll
-    for (int f = 0; f < F; ++f) {
-      const float gi = __shfl_sync(0xffffffffu, d, 4 * f), ui = __shfl_sync(0xffffffffu, d, 4 * f + 2);
-      if (u + f >= n) break;  // uniform per warp
-      const float gf[4] = {to_f32(g[f][0]), to_f32(g[f][1]), to_f32(g[f][2]), to_f32(g[f][3])};
-      const float uf[4] = {to_f32(v[f][0]), to_f32(v[f][1]), to_f32(v[f][2]), to_f32(v[f][3])};
-      float o[4];
-      glu_values<T, ACT, 4>(gf, uf, o);
-      const int rem = (int)(I - j0[f] < kCkptGroup ? I - j0[f] : (int64_t)kCkptGroup);
-      T* op = out + row[f] * ldo + j0[f];
-      uint8_t *gq = C.gq + row[f] * I + j0[f], *uq = C.uq + row[f] * I + j0[f];
-      if (j0[f] - lane + kCkptGroup <= I) {
-        store_run<true>(op, rem, o);
-        store_run_codes<true, FMT>(gq, rem, gf, gi);
-        store_run_codes<true, FMT>(uq, rem, uf, ui);
-      } else {
-        store_run<false>(op, rem, o);
-        store_run_codes<false, FMT>(gq, rem, gf, gi);
-        store_run_codes<false, FMT>(uq, rem, uf, ui);
-      }
-    }
+  const int64_t ng = (I + kCkptGroup - 1) / kCkptGroup, nu = (I + W - 1) / W, n = T_ * nu;
+  const bool small = n <= 0xffffffffLL;
+  const int64_t step = (int64_t)gridDim.x * (kGluBlock / 32);
+  for (int64_t u = (int64_t)blockIdx.x * (kGluBlock / 32) + warp_index(); u < n; u += step) {
+    const int64_t row = unit_div(u, nu, small), c = (u - row * nu) * W;
+    const int left = I - c < W ? (int)(I - c) : W;
+    const T *gp = gate + row * ldg + c + lane, *vp = up + row * ldu + c + lane;
+    T* op = out + row * ldo + c + lane;
+    const int64_t at = row * I + c + lane, sc = row * ng + c / kCkptGroup;
+    auto unit = [&](auto f, auto full, int at0, int n) {
+      glu_fwd_ckpt_unit<T, ACT, FMT, f.value, full.value>(gp + at0, vp + at0, op + at0, C.gq + at + at0, C.uq + at + at0,
+                                                          C.gs + sc + at0 / kCkptGroup, C.us + sc + at0 / kCkptGroup, n, lane);
+    };
+    row_groups(left, unit);
   }
 }
 
@@ -996,64 +1001,62 @@ glu_bwd_ckpt(const T* dout, const GluCkptIn C, T* dgate, T* dup, int64_t T_, int
 }
 
 // Any alignment and width, as glu_fwd_ckpt_elem.
+template <typename T, int ACT, int FMT, int F, bool FULL>
+__device__ __forceinline__ void glu_bwd_ckpt_unit(const T* dp, const uint8_t* gq, const uint8_t* uq, const float* gs,
+                                                  const float* us, T* dgp, T* dup, int left, int lane) {
+  T d[F][4];
+  uint32_t g[F], v[F];
+  float sg[F], su[F];
+#pragma unroll
+  for (int f = 0; f < F; ++f) {
+    const int rem = left - f * kCkptGroup - lane;
+    load_run<FULL>(dp + f * kCkptGroup, rem, d[f]);
+    g[f] = load_run_codes<FULL>(gq + f * kCkptGroup, rem);
+    v[f] = load_run_codes<FULL>(uq + f * kCkptGroup, rem);
+    const bool in = FULL || f * kCkptGroup < left;
+    sg[f] = in ? __ldg(gs + f) : 0.f;
+    su[f] = in ? __ldg(us + f) : 0.f;
+  }
+#pragma unroll
+  for (int f = 0; f < F; ++f) {
+    float gf[4], uf[4], dg[4], du[4];
+    q8_decode4<FMT>(g[f], gf);
+    q8_decode4<FMT>(v[f], uf);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float df = to_f32(d[f][e]);
+      float fx, fp;
+      act_fd<T, ACT>(__fmul_rn(gf[e], sg[f]), fx, fp);
+      du[e] = df * fx;
+      dg[e] = df * __fmul_rn(uf[e], su[f]) * fp;
+    }
+    const int rem = left - f * kCkptGroup - lane;
+    store_run<FULL>(dgp + f * kCkptGroup, rem, dg);
+    store_run<FULL>(dup + f * kCkptGroup, rem, du);
+  }
+}
+
 template <typename T, int ACT, int FMT>
 __global__ void __launch_bounds__(kGluBlock)
 glu_bwd_ckpt_elem(const T* dout, const GluCkptIn C, T* dgate, T* dup, int64_t T_, int64_t I, int64_t ldd,
                   int64_t lddg, int64_t lddu) {
-  constexpr int F = kElemFlight;
+  constexpr int W = kElemGroups * kCkptGroup;
   const int lane = threadIdx.x & 31;
-  const int64_t ng = (I + kCkptGroup - 1) / kCkptGroup, n = T_ * ng;
-  const bool small = n + F <= 0xffffffffLL;
-  const int64_t step = (int64_t)gridDim.x * (kGluBlock / 32) * F;
-  for (int64_t u = ((int64_t)blockIdx.x * (kGluBlock / 32) + warp_index()) * F; u < n; u += step) {
-    T d[F][4];
-    uint32_t g[F], v[F];
-    float gs[F], us[F];
-    int64_t row[F], j0[F];
-#pragma unroll
-    for (int f = 0; f < F; ++f) {
-      row[f] = unit_div(u + f, ng, small);
-      j0[f] = (u + f - row[f] * ng) * kCkptGroup + lane;
-      if (u + f >= n) continue;
-      const T* dp = dout + row[f] * ldd + j0[f];
-      const uint8_t *gp = C.gq + row[f] * I + j0[f], *vp = C.uq + row[f] * I + j0[f];
-      const int rem = (int)(I - j0[f] < kCkptGroup ? I - j0[f] : (int64_t)kCkptGroup);
-      gs[f] = __ldg(C.gs + u + f);
-      us[f] = __ldg(C.us + u + f);
-      if (j0[f] - lane + kCkptGroup <= I) {
-        load_run<true>(dp, rem, d[f]);
-        g[f] = load_run_codes<true>(gp, rem);
-        v[f] = load_run_codes<true>(vp, rem);
-      } else {
-        load_run<false>(dp, rem, d[f]);
-        g[f] = load_run_codes<false>(gp, rem);
-        v[f] = load_run_codes<false>(vp, rem);
-      }
-    }
-#pragma unroll
-    for (int f = 0; f < F; ++f) {
-      if (u + f >= n) break;
-      float gf[4], uf[4], dg[4], du[4];
-      q8_decode4<FMT>(g[f], gf);
-      q8_decode4<FMT>(v[f], uf);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float df = to_f32(d[f][e]);
-        float fx, fp;
-        act_fd<T, ACT>(__fmul_rn(gf[e], gs[f]), fx, fp);
-        du[e] = df * fx;
-        dg[e] = df * __fmul_rn(uf[e], us[f]) * fp;
-      }
-      const int rem = (int)(I - j0[f] < kCkptGroup ? I - j0[f] : (int64_t)kCkptGroup);
-      T *gp = dgate + row[f] * lddg + j0[f], *up_ = dup + row[f] * lddu + j0[f];
-      if (j0[f] - lane + kCkptGroup <= I) {
-        store_run<true>(gp, rem, dg);
-        store_run<true>(up_, rem, du);
-      } else {
-        store_run<false>(gp, rem, dg);
-        store_run<false>(up_, rem, du);
-      }
-    }
+  const int64_t ng = (I + kCkptGroup - 1) / kCkptGroup, nu = (I + W - 1) / W, n = T_ * nu;
+  const bool small = n <= 0xffffffffLL;
+  const int64_t step = (int64_t)gridDim.x * (kGluBlock / 32);
+  for (int64_t u = (int64_t)blockIdx.x * (kGluBlock / 32) + warp_index(); u < n; u += step) {
+    const int64_t row = unit_div(u, nu, small), c = (u - row * nu) * W;
+    const int left = I - c < W ? (int)(I - c) : W;
+    const T* dp = dout + row * ldd + c + lane;
+    T *gp = dgate + row * lddg + c + lane, *vp = dup + row * lddu + c + lane;
+    const int64_t at = row * I + c + lane, sc = row * ng + c / kCkptGroup;
+    auto unit = [&](auto f, auto full, int at0, int n) {
+      glu_bwd_ckpt_unit<T, ACT, FMT, f.value, full.value>(dp + at0, C.gq + at + at0, C.uq + at + at0,
+                                                          C.gs + sc + at0 / kCkptGroup, C.us + sc + at0 / kCkptGroup,
+                                                          gp + at0, vp + at0, n, lane);
+    };
+    row_groups(left, unit);
   }
 }
 
@@ -1266,7 +1269,7 @@ void glu_fwd_ckpt_launch(const void* g, const void* u, void* o, GluCkpt C, int64
     glu_fwd_ckpt<T, ACT, FMT><<<grid_for(units, 1, (int64_t)sm_count() * kCkptGrid), cb, 0, s>>>((const T*)g, (const T*)u, (T*)o, C,
                                                                         rows, ncol, ldg, ldu, ldo);
   } else {
-    const int64_t units = rows * ((I + kCkptGroup - 1) / kCkptGroup), per = kGluBlock / 32 * kElemFlight;
+    const int64_t units = rows * ((I + kElemGroups * kCkptGroup - 1) / (kElemGroups * kCkptGroup)), per = kGluBlock / 32;
     glu_fwd_ckpt_elem<T, ACT, FMT><<<grid_for((units + per - 1) / per, 1, (int64_t)sm_count() * kCkptGrid), kGluBlock, 0, s>>>(
         (const T*)g, (const T*)u, (T*)o, C, rows, I, ldg, ldu, ldo);
   }
@@ -1285,7 +1288,7 @@ void glu_bwd_ckpt_launch(const void* d, GluCkptIn C, void* dg, void* du, int64_t
     const unsigned grid = grid_for((rows + U - 1) / U * ((ncol + cb - 1) / cb), 1, (int64_t)sm_count() * kCkptGrid);
     glu_bwd_ckpt<T, ACT, FMT, U><<<grid, cb, 0, s>>>((const T*)d, C, (T*)dg, (T*)du, rows, ncol, ldd, lddg, lddu);
   } else {
-    const int64_t units = rows * ((I + kCkptGroup - 1) / kCkptGroup), per = kGluBlock / 32 * kElemFlight;
+    const int64_t units = rows * ((I + kElemGroups * kCkptGroup - 1) / (kElemGroups * kCkptGroup)), per = kGluBlock / 32;
     glu_bwd_ckpt_elem<T, ACT, FMT><<<grid_for((units + per - 1) / per, 1, (int64_t)sm_count() * kCkptGrid), kGluBlock, 0, s>>>(
         (const T*)d, C, (T*)dg, (T*)du, rows, I, ldd, lddg, lddu);
   }
