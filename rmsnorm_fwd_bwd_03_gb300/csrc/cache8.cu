@@ -74,7 +74,8 @@ struct WriteArgs {
 // rotate-half pairing they turn into each other by VEC table entries, with
 // interleaved pairing each holds VEC / 2 pairs of its own.  A head row takes
 // nu = D / (2 VEC) lanes out of a group of the next power of two, so 80 or 96 wide
-// heads run here with idle lanes.  All of a lane's row loads are issued before
+// heads run here with idle lanes.  VEC fills 16 bytes, or 8 where a half head or an
+// address is a multiple of 8 bytes only (bf16 heads of 40 or 72 values).  All of a lane's row loads are issued before
 // anything that depends on the token's slot or position, and the maxima and
 // divisions of its K and V heads run side by side.  (With queries, K and V taken
 // alike, head after head, the chain of each one's reduction and division showed:
@@ -85,6 +86,7 @@ struct WriteArgs {
 // Head rows per lane and pass of a query warp: 8 measured 112 us, 6 119 and 4 117 for
 // 32768 tokens of 32 / 8 heads of 128 (110 us at the copy rate).
 constexpr int kWriteQ = 8;
+constexpr int kMaxVecHeads = 1 << 17;  // Q, K and V heads: at most 2^14 rows of blocks
 constexpr int kWriteWarps = 8;  // per block: chunks of a token, then tokens
 // A warp walks its tokens and asks for the next ones' rows in L2 while it works
 // on these.  Eight times the resident blocks leave a warp a few steps to do that
@@ -117,6 +119,34 @@ __device__ __forceinline__ void load_turns(const float2* table, int half, int p,
     for (int i = 0; i < VEC; ++i) cs[i] = make_float2(x, x);
   }
 }
+// VEC consecutive values of a head row: 16 bytes, or 8 of them.
+template <typename T, int VEC, bool WIDE = (VEC * sizeof(T) == 16)>
+struct HeadRun;
+template <typename T, int VEC>
+struct HeadRun<T, VEC, true> {
+  uint4 r;
+  __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void load(const T* p) { r = ld_stream(p); }
+  __device__ __forceinline__ void get(float (&v)[VEC]) const { unpack<VEC>(r, v); }
+  static __device__ __forceinline__ void store(T* p, const float (&v)[VEC]) { st_vec(p, pack<T, VEC>(v)); }
+};
+template <>
+struct HeadRun<bf16, 4, false> {
+  uint32_t a, b;
+  __device__ __forceinline__ void zero() { a = b = 0; }
+  __device__ __forceinline__ void load(const bf16* p) {
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "l"(p));
+  }
+  __device__ __forceinline__ void get(float (&v)[4]) const {
+    v[0] = bf16_lo(a);
+    v[1] = bf16_hi(a);
+    v[2] = bf16_lo(b);
+    v[3] = bf16_hi(b);
+  }
+  static __device__ __forceinline__ void store(bf16* p, const float (&v)[4]) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  }
+};
 template <int VEC, bool IL>
 __device__ __forceinline__ void turn(float (&xa)[VEC], float (&xb)[VEC], const float2 (&cs)[VEC]) {
   if constexpr (IL) {
@@ -140,10 +170,10 @@ __device__ __forceinline__ void turn(float (&xa)[VEC], float (&xb)[VEC], const f
   }
 }
 
-template <typename T, bool IL, int FMT, int KP>
+template <typename T, bool IL, int FMT, int VEC, int KP>
 __global__ void __launch_bounds__(32 * kWriteWarps, kWriteBlocks)
 cache8_write_vec(const WriteArgs<T> A, const WriteShape W) {
-  constexpr int VEC = VecOf<T>::N;
+  using Run = HeadRun<T, VEC>;
   constexpr int LINE = 128 / sizeof(T);
   const int half = A.D / 2;
   const int lanes = 1 << W.lg;
@@ -175,13 +205,13 @@ cache8_write_vec(const WriteArgs<T> A, const WriteShape W) {
       const bool live = on && t < A.rows;
       const T* qp = A.q + min(t, end) * A.ldq;
       T* qo = A.qo + min(t, end) * A.ldqo;
-      uint4 a[kWriteQ], b[kWriteQ];
+      Run a[kWriteQ], b[kWriteQ];
 #pragma unroll
       for (int j = 0; j < kWriteQ; ++j) {
         const int h = hb + G * j;
         if (j < W.qch && live && h < A.Hq) {
-          a[j] = ld_stream(qp + h * A.D + ia);
-          b[j] = ld_stream(qp + h * A.D + ia + half);
+          a[j].load(qp + h * A.D + ia);
+          b[j].load(qp + h * A.D + ia + half);
         }
       }
       const bool ok = p >= 0 && (int64_t)p < A.max_pos;
@@ -197,11 +227,11 @@ cache8_write_vec(const WriteArgs<T> A, const WriteShape W) {
         const int h = hb + G * j;
         if (j < W.qch && live && h < A.Hq) {
           float xa[VEC], xb[VEC];
-          unpack<VEC>(a[j], xa);
-          unpack<VEC>(b[j], xb);
+          a[j].get(xa);
+          b[j].get(xb);
           turn<VEC, IL>(xa, xb, cs);
-          st_vec(qo + h * A.D + ia, pack<T, VEC>(xa));
-          st_vec(qo + h * A.D + ia + half, pack<T, VEC>(xb));
+          Run::store(qo + h * A.D + ia, xa);
+          Run::store(qo + h * A.D + ia + half, xb);
         }
       }
     }
@@ -218,15 +248,16 @@ cache8_write_vec(const WriteArgs<T> A, const WriteShape W) {
     const bool live = on && t < A.rows;
     const T *kp = A.k + min(t, end) * A.ldk, *vp = A.v + min(t, end) * A.ldv;
     constexpr int N = 2 * KP;  // K of each head, then V of each
-    uint4 a[N], b[N];
+    Run a[N], b[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int h = hb + G * (j % KP);
-      a[j] = b[j] = make_uint4(0, 0, 0, 0);
+      a[j].zero();
+      b[j].zero();
       if (j % KP < W.kch && live && h < A.Hk) {
         const T* src = (j < KP ? kp : vp) + h * A.D + ia;
-        a[j] = ld_stream(src);
-        b[j] = ld_stream(src + half);
+        a[j].load(src);
+        b[j].load(src + half);
       }
     }
     const bool ok = p >= 0 && (int64_t)p < A.max_pos;
@@ -250,8 +281,8 @@ cache8_write_vec(const WriteArgs<T> A, const WriteShape W) {
     uint32_t m[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      unpack<VEC>(a[j], xa[j]);
-      unpack<VEC>(b[j], xb[j]);
+      a[j].get(xa[j]);
+      b[j].get(xb[j]);
       if (j < KP) turn<VEC, IL>(xa[j], xb[j], cs);
       m[j] = on ? max(abs_max_bits<VEC>(xa[j]), abs_max_bits<VEC>(xb[j])) : 0u;
     }
@@ -300,16 +331,117 @@ cache8_write_vec(const WriteArgs<T> A, const WriteShape W) {
   }
 }
 
-// Element path (any head size, alignment and stride): a warp per head row, a
-// lane the pairs l, l + 32, ..., which wait in registers for the head's maximum
-// (FITS: heads of up to 2 * 32 * kElemPairs values; wider ones are read twice, the
-// second time from L1).  16384 tokens of 8 / 8 heads of 72: 174 us (14 us at the
-// copy rate): bound by the latency of its short warps.
-constexpr int kElemPairs = 4;
+// Element path (any alignment and stride, heads of up to 256 values): a warp takes
+// four heads of one token, one value per access; lane l has the pairs l, l + 32, ...
+// (K of them) of each, which wait in registers for the heads' maxima.  The heads share
+// the token's slot, position and turns, and their loads, reductions and one
+// division run side by side: 86 us for 16384 tokens of 8 / 8 heads of 72, where a
+// warp per head, bound by its latency, took 174 and the 8-byte vector path takes 50
+// (14 us at the copy rate).  16384 tokens of 12 / 3 heads of 100: 70 us.
+constexpr int kElemHeads = 4;
 
-template <typename T, bool IL, int FMT, bool FITS>
+template <typename T, bool IL, int FMT, int K>
 __global__ void __launch_bounds__(256) cache8_write_elem(const WriteArgs<T> A, bool small) {
-  constexpr int K = FITS ? kElemPairs : 1;
+  constexpr int F = kElemHeads;
+  const int half = A.D / 2, HR = A.Hq + A.Hk, HT = HR + A.Hk, nc = (HT + F - 1) / F;
+  const int lane = threadIdx.x & 31;
+  const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
+  for (int64_t item = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp_index(); item < A.rows * nc; item += step) {
+    const int64_t t = small ? (int64_t)((uint32_t)item / (uint32_t)nc) : item / nc;
+    const int h0 = (int)(item - t * nc) * F;
+    const int64_t slot = __ldg(A.S.slots + t);
+    const int p = __ldg(A.pos + t);
+    T x1[F][K], x2[F][K];
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      const int h = h0 + f;
+      if (h >= HT) break;  // uniform per warp, as every test of h
+      const T* src = h < A.Hq ? A.q + t * A.ldq + h * A.D
+                     : h < HR ? A.k + t * A.ldk + (h - A.Hq) * A.D
+                              : A.v + t * A.ldv + (h - HR) * A.D;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int i = lane + 32 * k;
+        x1[f][k] = x2[f][k] = from_f32<T>(0.f);
+        if (i < half) {
+          x1[f][k] = src[IL ? 2 * i : i];
+          x2[f][k] = src[IL ? 2 * i + 1 : half + i];
+        }
+      }
+    }
+    const bool ok = p >= 0 && (int64_t)p < A.max_pos;
+    float2 cs[K];
+    if (h0 < HR) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int i = lane + 32 * k;
+        cs[k] = both(ok ? 0.f : __int_as_float(0x7fc00000));
+        if (ok && i < half) cs[k] = __ldg(A.table + (size_t)p * half + i);
+      }
+    }
+    int64_t off = 0;
+    const int64_t page = A.S.page_of(slot, off);
+    if (h0 == 0 && lane == 0) {
+      if (!ok && (A.Hq > 0 || page >= 0)) atomicOr(A.err, kErrBadPosition);
+      if (page == -2) atomicOr(A.err, kErrBadSlot);
+    }
+    float2 y[F][K];
+    uint32_t mine = 0;
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      const int h = h0 + f;
+      if (h >= HT) break;
+      uint32_t m = 0;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const float a = to_f32(x1[f][k]), b = to_f32(x2[f][k]);
+        // V is not rotated: it is taken as it is, whatever it holds
+        y[f][k] = h >= HR ? make_float2(a, b) : make_float2(a * cs[k].x - b * cs[k].y, b * cs[k].x + a * cs[k].y);
+        if (lane + 32 * k < half) m = max(m, max(abs_bits(y[f][k].x), abs_bits(y[f][k].y)));
+      }
+      if (h >= A.Hq) {
+        m = group_max<32>(m);
+        if (lane >> 1 == f) mine = m;  // lanes 2 f and 2 f + 1 divide for 1 / scale and scale
+      }
+    }
+    const float am = q8_amax(mine);
+    const float d = __fdiv_rn(lane & 1 ? am : Q8Max<FMT>::v, lane & 1 ? Q8Max<FMT>::v : am);
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      const int h = h0 + f;
+      const float inv = __shfl_sync(0xffffffffu, d, 2 * f);
+      if (h >= HT) break;
+      if (h < A.Hq) {
+        T* dst = A.qo + t * A.ldqo + h * A.D;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (const int i = lane + 32 * k; i < half) {
+            dst[IL ? 2 * i : i] = from_f32<T>(y[f][k].x);
+            dst[IL ? 2 * i + 1 : half + i] = from_f32<T>(y[f][k].y);
+          }
+      } else if (page >= 0) {
+        const bool isk = h < HR;
+        const int hk = h - (isk ? A.Hq : HR);
+        uint8_t* dst = isk ? A.K.q + A.K.cq.at(page, off, hk) : A.V.q + A.V.cq.at(page, off, hk);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (const int i = lane + 32 * k; i < half) {
+            dst[IL ? 2 * i : i] = (uint8_t)q8_code1<FMT>(y[f][k].x, inv);
+            dst[IL ? 2 * i + 1 : half + i] = (uint8_t)q8_code1<FMT>(y[f][k].y, inv);
+          }
+        if (lane == 2 * f + 1)
+          *(isk ? A.K.sc + A.K.cs.at(page, off, hk) : A.V.sc + A.V.cs.at(page, off, hk)) =
+              mine < kInfBits ? d : __int_as_float(0x7fc00000);
+      }
+    }
+  }
+}
+
+// Heads too wide for that: a warp per head row, read twice, the second time from L1.
+constexpr int kElemWidth = 256;
+
+template <typename T, bool IL, int FMT>
+__global__ void __launch_bounds__(256) cache8_write_wide(const WriteArgs<T> A, bool small) {
   const int half = A.D / 2, HR = A.Hq + A.Hk, HT = HR + A.Hk;
   const int lane = threadIdx.x & 31;
   const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
@@ -323,31 +455,11 @@ __global__ void __launch_bounds__(256) cache8_write_elem(const WriteArgs<T> A, b
                             : A.v + t * A.ldv + (int64_t)(h - HR) * A.D;
     const bool ok = p >= 0 && (int64_t)p < A.max_pos;
     const float2* turns = A.table + (ok ? (size_t)p * half : 0);
-    auto load = [&](int i, float& x1, float& x2, float2& f) {
-      x1 = to_f32(src[IL ? 2 * i : i]);
-      x2 = to_f32(src[IL ? 2 * i + 1 : half + i]);
-      const float qnan = __int_as_float(0x7fc00000);
-      f = h >= HR ? make_float2(1.f, 0.f) : ok ? __ldg(turns + i) : make_float2(qnan, qnan);
-    };
-    // V is not rotated: it is taken as it is, whatever it holds
-    auto turned = [&](float x1, float x2, float2 f) {
-      return h >= HR ? make_float2(x1, x2) : make_float2(x1 * f.x - x2 * f.y, x2 * f.x + x1 * f.y);
-    };
-    float2 y[K];
-    if constexpr (FITS) {
-      float x1[K], x2[K];
-      float2 f[K];
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (lane + 32 * k < half) load(lane + 32 * k, x1[k], x2[k], f[k]);
-#pragma unroll
-      for (int k = 0; k < K; ++k) y[k] = lane + 32 * k < half ? turned(x1[k], x2[k], f[k]) : both(0.f);
-    }
     auto pair = [&](int i) {
-      float x1, x2;
-      float2 f;
-      load(i, x1, x2, f);
-      return turned(x1, x2, f);
+      const float x1 = to_f32(src[IL ? 2 * i : i]), x2 = to_f32(src[IL ? 2 * i + 1 : half + i]);
+      if (h >= HR) return make_float2(x1, x2);  // V is not rotated
+      const float2 f = ok ? __ldg(turns + i) : both(__int_as_float(0x7fc00000));
+      return make_float2(x1 * f.x - x2 * f.y, x2 * f.x + x1 * f.y);
     };
     int64_t off = 0;
     const int64_t page = A.S.page_of(slot, off);
@@ -357,45 +469,28 @@ __global__ void __launch_bounds__(256) cache8_write_elem(const WriteArgs<T> A, b
     }
     if (h < A.Hq) {
       T* dst = A.qo + t * A.ldqo + (int64_t)h * A.D;
-      auto put = [&](int i, float2 v) {
+      for (int i = lane; i < half; i += 32) {
+        const float2 v = pair(i);
         dst[IL ? 2 * i : i] = from_f32<T>(v.x);
         dst[IL ? 2 * i + 1 : half + i] = from_f32<T>(v.y);
-      };
-      if constexpr (FITS) {
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-          if (lane + 32 * k < half) put(lane + 32 * k, y[k]);
-      } else {
-        for (int i = lane; i < half; i += 32) put(i, pair(i));
       }
       continue;
     }
     if (page < 0) continue;
     uint32_t m = 0;
-    if constexpr (FITS) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) m = max(m, max(abs_bits(y[k].x), abs_bits(y[k].y)));
-    } else {
-      for (int i = lane; i < half; i += 32) {
-        const float2 v = pair(i);
-        m = max(m, max(abs_bits(v.x), abs_bits(v.y)));
-      }
+    for (int i = lane; i < half; i += 32) {
+      const float2 v = pair(i);
+      m = max(m, max(abs_bits(v.x), abs_bits(v.y)));
     }
     m = group_max<32>(m);
     const float am = q8_amax(m), inv = q8_inv<FMT>(am);
     const bool isk = h < HR;
     const int hk = h - (isk ? A.Hq : HR);
     uint8_t* dst = isk ? A.K.q + A.K.cq.at(page, off, hk) : A.V.q + A.V.cq.at(page, off, hk);
-    auto put = [&](int i, float2 v) {
+    for (int i = lane; i < half; i += 32) {
+      const float2 v = pair(i);
       dst[IL ? 2 * i : i] = (uint8_t)q8_code1<FMT>(v.x, inv);
       dst[IL ? 2 * i + 1 : half + i] = (uint8_t)q8_code1<FMT>(v.y, inv);
-    };
-    if constexpr (FITS) {
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (lane + 32 * k < half) put(lane + 32 * k, y[k]);
-    } else {
-      for (int i = lane; i < half; i += 32) put(i, pair(i));
     }
     if (lane == 0)
       *(isk ? A.K.sc + A.K.cs.at(page, off, hk) : A.V.sc + A.V.cs.at(page, off, hk)) = q8_scale<FMT>(am, m);
@@ -533,9 +628,8 @@ Cache cache_of(const gbln_cache8* c) {
 bool strides_multiple(const gbln_cache8* c, int n) {
   return c->page_stride % n == 0 && c->slot_stride % n == 0 && c->head_stride % n == 0;
 }
-// Whether every head starts at a multiple of the codes of one access.
-bool codes_aligned(const gbln_cache8* k, const gbln_cache8* v, gbln_dtype io) {
-  const int n = io == GBLN_F32 ? 4 : 8;
+// Whether every head starts at a multiple of n codes.
+bool codes_aligned(const gbln_cache8* k, const gbln_cache8* v, int n) {
   return aligned_to(k->codes, n) && aligned_to(v->codes, n) && strides_multiple(k, n) && strides_multiple(v, n);
 }
 Slots slots_of(const gbln_cache8* c, const int64_t* slots) {
@@ -543,56 +637,69 @@ Slots slots_of(const gbln_cache8* c, const int64_t* slots) {
   return {slots, total, c->page_size, total < (1LL << 31) && c->page_size < (1LL << 31)};
 }
 
+// Whether runs of n values of a head row, and their codes, are aligned.
+template <typename T>
+bool runs_fit(const WriteArgs<T>& A, const gbln_cache8* k, const gbln_cache8* v, int n) {
+  const auto row = [&](const void* p, int64_t ld) { return aligned_to(p, n * sizeof(T)) && ld % n == 0; };
+  return A.D % (2 * n) == 0 && A.D / (2 * n) <= 32 && aligned16(A.table) && codes_aligned(k, v, n) &&
+         (A.Hq == 0 || (row(A.q, A.ldq) && row(A.qo, A.ldqo))) && row(A.k, A.ldk) && row(A.v, A.ldv);
+}
+
+template <typename T, bool IL, int FMT, int VEC>
+gbln_status write_vec_launch(const WriteArgs<T>& A, int sms, cudaStream_t s) {
+  WriteShape W{};
+  W.nu = A.D / (2 * VEC);
+  while ((1 << W.lg) < W.nu) ++W.lg;
+  const int lgG = 5 - W.lg, G = 1 << lgG;
+  // log2 of the tokens whose n heads share a warp's G groups
+  const auto tokens = [&](int n) {
+    int lt = lgG;
+    while (lt > 0 && (n << lt) > G) --lt;
+    return lt;
+  };
+  const int Lq = (A.Hq + G - 1) / G, Lk = (A.Hk + G - 1) / G;  // head rows per lane and token
+  W.nq = (Lq + kWriteQ - 1) / kWriteQ;
+  W.qch = W.nq ? (Lq + W.nq - 1) / W.nq : 0;
+  W.qlt = W.nq ? tokens(A.Hq) : 0;
+  W.nkv = (Lk + 1) / 2;
+  W.kch = (Lk + W.nkv - 1) / W.nkv;
+  W.klt = tokens(A.Hk);
+  const int n = W.nq + W.nkv, cy = n < kWriteWarps ? n : kWriteWarps, tz = kWriteWarps / cy;
+  const dim3 grid(grid_for(A.rows, tz, (int64_t)sms * kWriteGrid), (unsigned)((n + cy - 1) / cy)), block(32, cy, tz);
+  if (W.kch == 1) cache8_write_vec<T, IL, FMT, VEC, 1><<<grid, block, 0, s>>>(A, W);
+  else cache8_write_vec<T, IL, FMT, VEC, 2><<<grid, block, 0, s>>>(A, W);
+  return launch_status();
+}
+
+// 16-byte runs where the sizes and addresses allow them, else 8-byte ones (heads of
+// 40, 72 or 200 bf16 values), else single values.
 template <typename T, bool IL, int FMT>
-gbln_status write_launch(const WriteArgs<T>& A, bool cache_aligned, cudaStream_t s) {
+gbln_status write_launch(const WriteArgs<T>& A, const gbln_cache8* kc, const gbln_cache8* vc, cudaStream_t s) {
   constexpr int VEC = VecOf<T>::N;
   const int HT = A.Hq + 2 * A.Hk;
-  const auto row16 = [](const void* p, int64_t ld) { return aligned16(p) && (ld * (int64_t)sizeof(T)) % 16 == 0; };
-  const bool vec = A.D % (2 * VEC) == 0 && A.D / (2 * VEC) <= 32 && aligned16(A.table) && cache_aligned &&
-                   (A.Hq == 0 || (row16(A.q, A.ldq) && row16(A.qo, A.ldqo))) && row16(A.k, A.ldk) && row16(A.v, A.ldv);
-  if (vec) {
-    WriteShape W{};
-    W.nu = A.D / (2 * VEC);
-    while ((1 << W.lg) < W.nu) ++W.lg;
-    const int lgG = 5 - W.lg, G = 1 << lgG;
-    // log2 of the tokens whose n heads share a warp's G groups
-    const auto tokens = [&](int n) {
-      int lt = lgG;
-      while (lt > 0 && (n << lt) > G) --lt;
-      return lt;
-    };
-    const int Lq = (A.Hq + G - 1) / G, Lk = (A.Hk + G - 1) / G;  // head rows per lane and token
-    W.nq = (Lq + kWriteQ - 1) / kWriteQ;
-    W.qch = W.nq ? (Lq + W.nq - 1) / W.nq : 0;
-    W.qlt = W.nq ? tokens(A.Hq) : 0;
-    W.nkv = (Lk + 1) / 2;
-    W.kch = (Lk + W.nkv - 1) / W.nkv;
-    W.klt = tokens(A.Hk);
-    const int n = W.nq + W.nkv, cy = n < kWriteWarps ? n : kWriteWarps, tz = kWriteWarps / cy;
-    const int sms = sm_count();
-    if (sms <= 0) return GBLN_ERR_CUDA;
-    const int64_t gy = (n + cy - 1) / cy;
-    if (gy <= 65535) {
-      const dim3 grid(grid_for(A.rows, tz, (int64_t)sms * kWriteGrid), (unsigned)gy), block(32, cy, tz);
-      if (W.kch == 1) cache8_write_vec<T, IL, FMT, 1><<<grid, block, 0, s>>>(A, W);
-      else cache8_write_vec<T, IL, FMT, 2><<<grid, block, 0, s>>>(A, W);
-      return launch_status();
-    }
+  const int sms = sm_count();
+  if (sms <= 0) return GBLN_ERR_CUDA;
+  if (HT <= kMaxVecHeads) {
+    if (runs_fit(A, kc, vc, VEC)) return write_vec_launch<T, IL, FMT, VEC>(A, sms, s);
+    if constexpr (VEC == 8)
+      if (runs_fit(A, kc, vc, 4)) return write_vec_launch<T, IL, FMT, 4>(A, sms, s);
   }
-  const unsigned grid = grid_for(A.rows * HT, 8, 1 << 20);
-  const bool small = A.rows * HT <= 0xffffffffLL;
-  if (A.D <= 2 * 32 * kElemPairs) cache8_write_elem<T, IL, FMT, true><<<grid, 256, 0, s>>>(A, small);
-  else cache8_write_elem<T, IL, FMT, false><<<grid, 256, 0, s>>>(A, small);
+  const int64_t items = A.rows * (A.D > kElemWidth ? HT : (HT + kElemHeads - 1) / kElemHeads);  // one per warp
+  const unsigned grid = grid_for(items, 8, 1 << 20);
+  const bool small = items <= 0xffffffffLL;
+  if (A.D <= 64) cache8_write_elem<T, IL, FMT, 1><<<grid, 256, 0, s>>>(A, small);
+  else if (A.D <= 128) cache8_write_elem<T, IL, FMT, 2><<<grid, 256, 0, s>>>(A, small);
+  else if (A.D <= kElemWidth) cache8_write_elem<T, IL, FMT, 4><<<grid, 256, 0, s>>>(A, small);
+  else cache8_write_wide<T, IL, FMT><<<grid, 256, 0, s>>>(A, small);
   return launch_status();
 }
 
 template <typename T>
-gbln_status write_typed(const WriteArgs<T>& A, bool il, int fmt, bool cache_aligned, cudaStream_t s) {
+gbln_status write_typed(const WriteArgs<T>& A, bool il, int fmt, const gbln_cache8* kc, const gbln_cache8* vc,
+                        cudaStream_t s) {
   if (fmt == GBLN_Q8_INT8)
-    return il ? write_launch<T, true, GBLN_Q8_INT8>(A, cache_aligned, s)
-              : write_launch<T, false, GBLN_Q8_INT8>(A, cache_aligned, s);
-  return il ? write_launch<T, true, GBLN_Q8_E4M3>(A, cache_aligned, s)
-            : write_launch<T, false, GBLN_Q8_E4M3>(A, cache_aligned, s);
+    return il ? write_launch<T, true, GBLN_Q8_INT8>(A, kc, vc, s) : write_launch<T, false, GBLN_Q8_INT8>(A, kc, vc, s);
+  return il ? write_launch<T, true, GBLN_Q8_E4M3>(A, kc, vc, s) : write_launch<T, false, GBLN_Q8_E4M3>(A, kc, vc, s);
 }
 
 template <typename T>
@@ -660,7 +767,6 @@ extern "C" gbln_status gbln_rope_fwd_cache8(const void* q, const void* k, const 
   unsigned int* err = device_error_word();
   if (!err) return GBLN_ERR_CUDA;
   const bool il = pairing == GBLN_ROPE_INTERLEAVED;
-  const bool ca = codes_aligned(k_cache, v_cache, io);
   cudaStream_t s = (cudaStream_t)stream;
 #define GBLN_WRITE_ARGS(TY)                                                                               \
   const WriteArgs<TY> A{(const TY*)q, (const TY*)k, (const TY*)v, (TY*)q_out, positions, (const float2*)cos_sin, \
@@ -668,10 +774,10 @@ extern "C" gbln_status gbln_rope_fwd_cache8(const void* q, const void* k, const 
                         cache_of(k_cache), cache_of(v_cache), err}
   if (io == GBLN_F32) {
     GBLN_WRITE_ARGS(float);
-    return write_typed<float>(A, il, fmt, ca, s);
+    return write_typed<float>(A, il, fmt, k_cache, v_cache, s);
   }
   GBLN_WRITE_ARGS(bf16);
-  return write_typed<bf16>(A, il, fmt, ca, s);
+  return write_typed<bf16>(A, il, fmt, k_cache, v_cache, s);
 #undef GBLN_WRITE_ARGS
 }
 
@@ -692,7 +798,7 @@ extern "C" gbln_status gbln_cache8_read(const int64_t* slots, const gbln_cache8*
     return GBLN_ERR_INVALID_ARG;
   unsigned int* err = device_error_word();
   if (!err) return GBLN_ERR_CUDA;
-  const bool ca = codes_aligned(k_cache, v_cache, io);
+  const bool ca = codes_aligned(k_cache, v_cache, io == GBLN_F32 ? 4 : 8);
   cudaStream_t s = (cudaStream_t)stream;
 #define GBLN_READ_ARGS(TY)                                                                             \
   const ReadArgs<TY> A{slots_of(k_cache, slots), cache_of(k_cache), cache_of(v_cache), (TY*)k_out, (TY*)v_out, \

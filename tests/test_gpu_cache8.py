@@ -57,11 +57,12 @@ def _rotation_window(x64):
     return 8 * 2.0 ** -24 * np.abs(x64).max(axis=-1, keepdims=True)
 
 
-def _case(T, Hq, Hk, D, io, fmt, page=16, layout="NHD", pairing="half", packed=True, in_place=False, unaligned=False, seed=0):
+def _case(T, Hq, Hk, D, io, fmt, page=16, layout="NHD", pairing="half", packed=True, in_place=False, unaligned=False, seed=0,
+          shift=None):
     dt = IO[io]
     r = np.random.default_rng(seed + T + D)
     width = (Hq + 2 * Hk) * D
-    off = 1 if unaligned else 0
+    off = shift or (1 if unaligned else 0)  # values before the first token's row
     qkv = _randn((T, width + off), dt, seed)[:, off:]
     q, k, v = (t.unflatten(1, (-1, D)) if t.shape[1] else None for t in qkv.split([Hq * D, Hk * D, Hk * D], dim=1))
     if not packed:
@@ -129,6 +130,23 @@ def test_head_counts(Hq, Hk, fmt):
 def test_layouts_and_pages(layout, page, fmt):
     _case(70, 8, 4, 64, "bf16", fmt, page=page, layout=layout)
     _case(11, 2, 2, 40, "f32", fmt, page=page, layout=layout, pairing="interleaved")
+
+
+@pytest.mark.parametrize("pairing", ["half", "interleaved"])
+@pytest.mark.parametrize("D", [8, 24, 40, 72, 200, 256])
+def test_eight_byte_runs(D, pairing):
+    """bf16 heads that 8-byte, but not 16-byte, accesses divide."""
+    _case(37, 5, 3, D, "bf16", "int8", pairing=pairing, shift=4)
+    _case(300, 0, 2, D, "bf16", "e4m3", pairing=pairing, layout="HND", shift=4)
+    _case(9, 33, 8, D, "bf16", "int8", pairing=pairing, in_place=True, shift=4)
+
+
+@pytest.mark.parametrize("D", [18, 50, 100, 250])
+@pytest.mark.parametrize("Hq,Hk", [(0, 1), (1, 1), (5, 3), (7, 2), (2, 4)])
+def test_single_values_across_heads(D, Hq, Hk):
+    """Heads of single values, several of Q, K and V to a warp."""
+    _case(19, Hq, Hk, D, "bf16", "int8", layout="HND")
+    _case(6, Hq, Hk, D, "f32", "e4m3", pairing="interleaved", unaligned=True)
 
 
 @pytest.mark.parametrize("pairing", ["half", "interleaved"])
