@@ -93,6 +93,9 @@ constexpr int kWriteWarps = 8;  // per block: chunks of a token, then tokens
 // for and the scheduler something to balance.
 constexpr int kWriteBlocks = 2;               // resident per SM
 constexpr int kWriteGrid = kWriteBlocks * 8;  // blocks per SM
+// With 8-byte accesses half as many registers hold loads: three blocks measured 37 us
+// for 16384 tokens of 8 / 8 heads of 72, two 50, four (spilling) 40.
+constexpr int kWriteBlocks8 = 3;
 
 struct WriteShape {
   int nu, lg;         // lanes in use per head row, log2 of the lanes of its group
@@ -171,7 +174,7 @@ __device__ __forceinline__ void turn(float (&xa)[VEC], float (&xb)[VEC], const f
 }
 
 template <typename T, bool IL, int FMT, int VEC, int KP>
-__global__ void __launch_bounds__(32 * kWriteWarps, kWriteBlocks)
+__global__ void __launch_bounds__(32 * kWriteWarps, VEC * sizeof(T) == 16 ? kWriteBlocks : kWriteBlocks8)
 cache8_write_vec(const WriteArgs<T> A, const WriteShape W) {
   using Run = HeadRun<T, VEC>;
   constexpr int LINE = 128 / sizeof(T);
@@ -336,7 +339,7 @@ cache8_write_vec(const WriteArgs<T> A, const WriteShape W) {
 // (K of them) of each, which wait in registers for the heads' maxima.  The heads share
 // the token's slot, position and turns, and their loads, reductions and one
 // division run side by side: 86 us for 16384 tokens of 8 / 8 heads of 72, where a
-// warp per head, bound by its latency, took 174 and the 8-byte vector path takes 50
+// warp per head, bound by its latency, took 174 and the 8-byte vector path takes 37
 // (14 us at the copy rate).  16384 tokens of 12 / 3 heads of 100: 70 us.
 constexpr int kElemHeads = 4;
 
