@@ -96,6 +96,15 @@ constexpr int kWriteGrid = kWriteBlocks * 8;  // blocks per SM
 // With 8-byte accesses half as many registers hold loads: three blocks measured 37 us
 // for 16384 tokens of 8 / 8 heads of 72, two 50, four (spilling) 40.
 constexpr int kWriteBlocks8 = 3;
+// Few heads per token (a GPU's share of a model) leave most of a lane's registers
+// idle: up to 32 bytes of each query half and one head of K and V per lane run four
+// blocks per SM instead, at 64 registers.  32768 tokens, two and four blocks (copy
+// rate): 8 / 2 heads of 128 42 and 33 us (28), 14 / 2 of 64 38 and 28 (21), 7 / 1 of 96
+// 37 and 25 (16); five blocks spill, 51 us.  Beyond that the larger share per lane is
+// faster (32 / 8 heads of 128: 113 and 127 us), except for so few tokens that every
+// warp of the finer split runs at once (16 tokens: 3.0 and 2.4 us).
+constexpr int kFewBlocks = 4;
+constexpr int few_queries(int bytes) { return 32 / bytes; }  // per lane, in accesses of that many bytes
 
 struct WriteShape {
   int nu, lg;         // lanes in use per head row, log2 of the lanes of its group
@@ -173,8 +182,8 @@ __device__ __forceinline__ void turn(float (&xa)[VEC], float (&xb)[VEC], const f
   }
 }
 
-template <typename T, bool IL, int FMT, int VEC, int KP>
-__global__ void __launch_bounds__(32 * kWriteWarps, VEC * sizeof(T) == 16 ? kWriteBlocks : kWriteBlocks8)
+template <typename T, bool IL, int FMT, int VEC, int KP, int QP>
+__global__ void __launch_bounds__(32 * kWriteWarps, QP < kWriteQ ? kFewBlocks : VEC * sizeof(T) == 16 ? kWriteBlocks : kWriteBlocks8)
 cache8_write_vec(const WriteArgs<T> A, const WriteShape W) {
   using Run = HeadRun<T, VEC>;
   constexpr int LINE = 128 / sizeof(T);
@@ -208,9 +217,9 @@ cache8_write_vec(const WriteArgs<T> A, const WriteShape W) {
       const bool live = on && t < A.rows;
       const T* qp = A.q + min(t, end) * A.ldq;
       T* qo = A.qo + min(t, end) * A.ldqo;
-      Run a[kWriteQ], b[kWriteQ];
+      Run a[QP], b[QP];
 #pragma unroll
-      for (int j = 0; j < kWriteQ; ++j) {
+      for (int j = 0; j < QP; ++j) {
         const int h = hb + G * j;
         if (j < W.qch && live && h < A.Hq) {
           a[j].load(qp + h * A.D + ia);
@@ -226,7 +235,7 @@ cache8_write_vec(const WriteArgs<T> A, const WriteShape W) {
         for (int x = hf * A.D + li * LINE; x < last; x += (32 >> lt) * LINE) prefetch_line(A.q + n * A.ldq + x);
       }
 #pragma unroll
-      for (int j = 0; j < kWriteQ; ++j) {
+      for (int j = 0; j < QP; ++j) {
         const int h = hb + G * j;
         if (j < W.qch && live && h < A.Hq) {
           float xa[VEC], xb[VEC];
@@ -661,16 +670,21 @@ gbln_status write_vec_launch(const WriteArgs<T>& A, int sms, cudaStream_t s) {
     return lt;
   };
   const int Lq = (A.Hq + G - 1) / G, Lk = (A.Hk + G - 1) / G;  // head rows per lane and token
-  W.nq = (Lq + kWriteQ - 1) / kWriteQ;
+  constexpr int FQ = few_queries(VEC * sizeof(T));
+  const int finer = (Lq + FQ - 1) / FQ + Lk;  // warps per token (and as many tokens as share one)
+  const bool few = (Lq <= FQ && Lk <= 1) || A.rows * finer <= (int64_t)sms * kFewBlocks * kWriteWarps;
+  const int QP = few ? FQ : kWriteQ;
+  W.nq = (Lq + QP - 1) / QP;
   W.qch = W.nq ? (Lq + W.nq - 1) / W.nq : 0;
   W.qlt = W.nq ? tokens(A.Hq) : 0;
-  W.nkv = (Lk + 1) / 2;
+  W.nkv = few ? Lk : (Lk + 1) / 2;
   W.kch = (Lk + W.nkv - 1) / W.nkv;
   W.klt = tokens(A.Hk);
   const int n = W.nq + W.nkv, cy = n < kWriteWarps ? n : kWriteWarps, tz = kWriteWarps / cy;
   const dim3 grid(grid_for(A.rows, tz, (int64_t)sms * kWriteGrid), (unsigned)((n + cy - 1) / cy)), block(32, cy, tz);
-  if (W.kch == 1) cache8_write_vec<T, IL, FMT, VEC, 1><<<grid, block, 0, s>>>(A, W);
-  else cache8_write_vec<T, IL, FMT, VEC, 2><<<grid, block, 0, s>>>(A, W);
+  if (few) cache8_write_vec<T, IL, FMT, VEC, 1, FQ><<<grid, block, 0, s>>>(A, W);
+  else if (W.kch == 1) cache8_write_vec<T, IL, FMT, VEC, 1, kWriteQ><<<grid, block, 0, s>>>(A, W);
+  else cache8_write_vec<T, IL, FMT, VEC, 2, kWriteQ><<<grid, block, 0, s>>>(A, W);
   return launch_status();
 }
 

@@ -163,6 +163,16 @@ def test_token_counts(T):
     _case(T, 8, 2, 128, "bf16", "int8", page=16)
 
 
+@pytest.mark.parametrize("T,Hq,Hk,D,io", [
+    (5000, 32, 8, 128, "bf16"), (2501, 7, 12, 128, "bf16"), (5003, 16, 3, 128, "bf16"), (4999, 40, 4, 96, "bf16"),
+    (2600, 0, 5, 256, "bf16"), (5001, 12, 2, 64, "f32"), (2500, 17, 8, 64, "f32"), (2511, 9, 6, 72, "bf16"),
+    (1300, 70, 2, 40, "bf16"), (1703, 5, 3, 100, "bf16")])
+def test_more_tokens_than_run_at_once(T, Hq, Hk, D, io):
+    """Enough of them that the heads are dealt to few, busy lanes."""
+    _case(T, Hq, Hk, D, io, "int8", page=64, layout="HND")
+    _case(T, Hq, Hk, D, io, "e4m3", pairing="interleaved", packed=False)
+
+
 def test_rotation_equals_rope_fwd():
     # the queries are those of rope_fwd, bit for bit, and the keys quantised are its float32 rotation
     T, Hq, Hk, D = 100, 8, 4, 128
