@@ -173,6 +173,28 @@ def test_more_tokens_than_run_at_once(T, Hq, Hk, D, io):
     _case(T, Hq, Hk, D, io, "e4m3", pairing="interleaved", packed=False)
 
 
+@pytest.mark.parametrize("io,Hq,Hk,D", [("bf16", 32, 8, 128), ("bf16", 8, 8, 72), ("bf16", 12, 3, 100), ("f32", 12, 8, 64)])
+@pytest.mark.parametrize("pairing", ["half", "interleaved"])
+def test_chunks_of_a_prompt_give_the_same_bits(io, Hq, Hk, D, pairing):
+    T, page = 5000, 16
+    dt = IO[io]
+    qkv = _randn((T, (Hq + 2 * Hk) * D), dt, D)
+    q, k, v = (t.unflatten(1, (-1, D)) for t in qkv.split([Hq * D, Hk * D, Hk * D], dim=1))
+    pos = torch.arange(T, device="cuda", dtype=torch.int32)
+    slots = torch.randperm(T, device="cuda")
+    table = gb.rope_table(T, D, THETA)
+    whole = _caches(-(-T // page), page, Hk, D, "int8")
+    parts = _caches(-(-T // page), page, Hk, D, "int8")
+    qo = gb.rope_fwd_cache8(q, k, v, pos, table, slots, *whole, pairing=pairing)
+    got = torch.empty_like(qo)
+    for a, b in ((0, 1), (1, 17), (17, 500), (500, 2100), (2100, T)):
+        gb.rope_fwd_cache8(q[a:b], k[a:b], v[a:b], pos[a:b], table, slots[a:b], *parts, pairing=pairing, q_out=got[a:b])
+    assert torch.equal(got, qo)
+    for x, y in zip(parts, whole):
+        assert torch.equal(x, y)
+    assert gb.device_error() == 0
+
+
 def test_rotation_equals_rope_fwd():
     # the queries are those of rope_fwd, bit for bit, and the keys quantised are its float32 rotation
     T, Hq, Hk, D = 100, 8, 4, 128
