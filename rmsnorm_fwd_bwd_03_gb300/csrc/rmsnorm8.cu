@@ -191,11 +191,11 @@ __global__ void __launch_bounds__(BLOCK) rms8_fwd_vec(const Fwd8<T, W> A) {
 // Forward, element path (any alignment, rows of up to 16384 values).  A warp
 // takes chunks of 128 consecutive values, lane l the values l, l + 32, l + 64,
 // l + 96: every access of a warp is contiguous, and a chunk is a checkpoint
-// group.  NW warps per row take chunks wi, wi + NW, ..., at most kElemChunks
-// each, which stay in registers.  Offsets within a chunk are immediates and only
-// a row's last chunk is predicated: at one value per lane and access these
+// group.  NW warps per row take `per` consecutive chunks each, at most kElemChunks,
+// which stay in registers.  Offsets from a warp's first value are immediates and
+// only a row's last chunk is predicated: at one value per lane and access these
 // kernels are bound by their instructions, not by HBM.  65536 x 1021 bf16: row
-// scale 116 us, checkpoint 120 us (69 and 89 us at the copy rate).
+// scale 113 us, checkpoint 119 us (69 and 89 us at the copy rate).
 // ---------------------------------------------------------------------------
 constexpr int kElemChunks = 4;
 
@@ -242,7 +242,7 @@ __device__ __forceinline__ void chunk_of(int c0, int H, F&& f) {
 }
 
 template <typename T, typename W, bool RES, int MODE>
-__global__ void __launch_bounds__(1024) rms8_fwd_elem(const Fwd8<T, W> A, int NW) {
+__global__ void __launch_bounds__(1024) rms8_fwd_elem(const Fwd8<T, W> A, int NW, int per) {
   constexpr int FMT = mode_fmt(MODE);
   __shared__ float red[32];
   __shared__ uint32_t redm[32];
@@ -251,16 +251,17 @@ __global__ void __launch_bounds__(1024) rms8_fwd_elem(const Fwd8<T, W> A, int NW
   const int64_t row = (int64_t)blockIdx.x * (blockDim.x / (32 * NW)) + g;
   const bool live = row < A.rows;  // the barrier below is reached by every warp
   const int H = live ? A.H : 0;
-  const size_t at = (size_t)(live ? row : 0) * A.H + wi * kCkptGroup + lane;
-  const int c0 = wi * kCkptGroup, cs = NW * kCkptGroup;  // first chunk, and the step to the next
+  const size_t at = (size_t)(live ? row : 0) * A.H + wi * per * kCkptGroup + lane;
+  const int c0 = wi * per * kCkptGroup;  // the warp's first chunk
+  const int end = min(c0 + per * kCkptGroup, H);
 
   T xr[kElemChunks][4], rr[kElemChunks][4];
 #pragma unroll
   for (int k = 0; k < kElemChunks; ++k)
-    chunk_of(c0 + k * cs, H, [&](auto full) {
-      const int rem = H - (c0 + k * cs) - lane;
-      load_chunk<decltype(full)::v>(A.x + at + k * cs, rem, xr[k]);
-      if constexpr (RES) load_chunk<decltype(full)::v>(A.r + at + k * cs, rem, rr[k]);
+    chunk_of(c0 + k * kCkptGroup, end, [&](auto full) {
+      const int rem = end - (c0 + k * kCkptGroup) - lane;
+      load_chunk<decltype(full)::v>(A.x + at + k * kCkptGroup, rem, xr[k]);
+      if constexpr (RES) load_chunk<decltype(full)::v>(A.r + at + k * kCkptGroup, rem, rr[k]);
     });
   float2 h[kElemChunks][2];  // values l and l + 32, l + 64 and l + 96
   float2 sq = both(0.f);
@@ -268,20 +269,20 @@ __global__ void __launch_bounds__(1024) rms8_fwd_elem(const Fwd8<T, W> A, int NW
 #pragma unroll
   for (int k = 0; k < kElemChunks; ++k) {
     cm[k] = 0;
-    chunk_of(c0 + k * cs, H, [&](auto full) {
+    chunk_of(c0 + k * kCkptGroup, end, [&](auto full) {
       [[maybe_unused]] constexpr bool FULL = decltype(full)::v;
-      [[maybe_unused]] const int rem = H - (c0 + k * cs) - lane;
+      [[maybe_unused]] const int rem = end - (c0 + k * kCkptGroup) - lane;
       h[k][0] = make_float2(to_f32(xr[k][0]), to_f32(xr[k][1]));
       h[k][1] = make_float2(to_f32(xr[k][2]), to_f32(xr[k][3]));
       if constexpr (RES) {
         h[k][0] = round2<T>(add2(h[k][0], make_float2(to_f32(rr[k][0]), to_f32(rr[k][1]))));
         h[k][1] = round2<T>(add2(h[k][1], make_float2(to_f32(rr[k][2]), to_f32(rr[k][3]))));
-        store_chunk<FULL>(A.hout + at + k * cs, rem, h[k]);
+        store_chunk<FULL>(A.hout + at + k * kCkptGroup, rem, h[k]);
       }
       sq = fma2(h[k][0], h[k][0], fma2(h[k][1], h[k][1], sq));
       if constexpr (MODE == kRowE4m3) {
         W w[4];
-        load_chunk<FULL>(A.w + c0 + k * cs + lane, rem, w);
+        load_chunk<FULL>(A.w + c0 + k * kCkptGroup + lane, rem, w);
         const float2 u = mul2(make_float2(to_f32(w[0]), to_f32(w[1])), h[k][0]);
         const float2 v = mul2(make_float2(to_f32(w[2]), to_f32(w[3])), h[k][1]);
         am = max(am, __float_as_uint(max3_abs(max3_abs(u.x, u.y, v.x), v.y, v.y)));
@@ -298,13 +299,13 @@ __global__ void __launch_bounds__(1024) rms8_fwd_elem(const Fwd8<T, W> A, int NW
     const uint32_t mine = lane & 4 ? (lane & 2 ? cm[3] : cm[2]) : (lane & 2 ? cm[1] : cm[0]);
     const float a = q8_amax(mine);
     const float d = __fdiv_rn(lane & 1 ? a : Q8Max<FMT>::v, lane & 1 ? Q8Max<FMT>::v : a);
-    if (lane < 8 && (lane & 1) && c0 + (lane >> 1) * cs < H)
-      A.sc[(size_t)row * A.ng + wi + (lane >> 1) * NW] = mine < kInfBits ? d : __int_as_float(0x7fc00000);
+    if (lane < 8 && (lane & 1) && c0 + (lane >> 1) * kCkptGroup < end)
+      A.sc[(size_t)row * A.ng + wi * per + (lane >> 1)] = mine < kInfBits ? d : __int_as_float(0x7fc00000);
 #pragma unroll
     for (int k = 0; k < kElemChunks; ++k) {
       const float inv = __shfl_sync(0xffffffffu, d, 2 * k);
-      chunk_of(c0 + k * cs, H, [&](auto full) {
-        store_codes<decltype(full)::v, FMT>(A.q + at + k * cs, H - (c0 + k * cs) - lane, h[k], inv);
+      chunk_of(c0 + k * kCkptGroup, end, [&](auto full) {
+        store_codes<decltype(full)::v, FMT>(A.q + at + k * kCkptGroup, end - (c0 + k * kCkptGroup) - lane, h[k], inv);
       });
     }
   }
@@ -332,19 +333,19 @@ __global__ void __launch_bounds__(1024) rms8_fwd_elem(const Fwd8<T, W> A, int NW
   }
 #pragma unroll
   for (int k = 0; k < kElemChunks; ++k)
-    chunk_of(c0 + k * cs, H, [&](auto full) {
+    chunk_of(c0 + k * kCkptGroup, end, [&](auto full) {
       constexpr bool FULL = decltype(full)::v;
-      const int rem = H - (c0 + k * cs) - lane;
+      const int rem = end - (c0 + k * kCkptGroup) - lane;
       W w[4];
-      load_chunk<FULL>(A.w + c0 + k * cs + lane, rem, w);
+      load_chunk<FULL>(A.w + c0 + k * kCkptGroup + lane, rem, w);
       const float2 w0 = make_float2(to_f32(w[0]), to_f32(w[1])), w1 = make_float2(to_f32(w[2]), to_f32(w[3]));
       if (MODE != kRowE4m3 || A.y) {
         const float2 o[2] = {mul2(w0, mul2(h[k][0], both(rs))), mul2(w1, mul2(h[k][1], both(rs)))};
-        store_chunk<FULL>(A.y + at + k * cs, rem, o);
+        store_chunk<FULL>(A.y + at + k * kCkptGroup, rem, o);
       }
       if constexpr (MODE == kRowE4m3) {
         const float2 o[2] = {mul2(w0, h[k][0]), mul2(w1, h[k][1])};
-        store_codes<FULL, FMT>(A.q + at + k * cs, rem, o, inv);
+        store_codes<FULL, FMT>(A.q + at + k * kCkptGroup, rem, o, inv);
       }
     });
 }
@@ -570,13 +571,14 @@ __global__ void __launch_bounds__(TPR * GPB, GPB > 1 ? 3 : 512 / TPR) rms8_bwd_v
 // Backward, element path: chunks of 128 values per warp as in rms8_fwd_elem, two
 // per warp: with their weights, dW sums and inputs they fill 64 registers, and
 // 1024 threads per SM are resident.  The warp asks for its next row in L2 while
-// it works on this one.  Bound by its instructions: 65536 x 1021 bf16 123 us (69 us
-// at the copy rate), 8194 x 4095 80 us (35).
+// it works on this one.  Bound by its instructions: 65536 x 1021 bf16 118 us (69 us
+// at the copy rate; 123 with every NW-th chunk, whose addresses are not immediates),
+// 8194 x 4095 81 us (35).
 // ---------------------------------------------------------------------------
 constexpr int kElemBwdChunks = 2;
 
 template <typename T, typename W, bool DRES, int FMT, int BLOCK>
-__global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) rms8_bwd_elem(const Bwd8<T, W> A, int NW) {
+__global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) rms8_bwd_elem(const Bwd8<T, W> A, int NW, int per) {
   constexpr int C = kElemBwdChunks;
   constexpr int LINE = 128 / sizeof(T);
   extern __shared__ float sacc[];  // several row groups: one row of dW sums
@@ -587,15 +589,15 @@ __global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) rms8_bwd_elem(const Bwd8<
   const int H = A.H;
   const int64_t P = gridDim.x, p = blockIdx.x;
   const int64_t r0 = p * A.rows / P, r1 = (p + 1) * A.rows / P;
-  const int c0 = wi * kCkptGroup, cs = NW * kCkptGroup;
+  const int c0 = wi * per * kCkptGroup, end = min(c0 + per * kCkptGroup, H);
 
   float2 acc[C][2], w[C][2];
 #pragma unroll
   for (int k = 0; k < C; ++k) {
     acc[k][0] = acc[k][1] = w[k][0] = w[k][1] = both(0.f);
-    chunk_of(c0 + k * cs, H, [&](auto full) {
+    chunk_of(c0 + k * kCkptGroup, end, [&](auto full) {
       W v[4];
-      load_chunk<decltype(full)::v>(A.w + c0 + k * cs + lane, H - (c0 + k * cs) - lane, v);
+      load_chunk<decltype(full)::v>(A.w + c0 + k * kCkptGroup + lane, end - (c0 + k * kCkptGroup) - lane, v);
       w[k][0] = make_float2(to_f32(v[0]), to_f32(v[1]));
       w[k][1] = make_float2(to_f32(v[2]), to_f32(v[3]));
     });
@@ -609,19 +611,19 @@ __global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) rms8_bwd_elem(const Bwd8<
     const float rs = __ldg(A.rstd + row);
 #pragma unroll
     for (int k = 0; k < C; ++k)
-      chunk_of(c0 + k * cs, H, [&](auto full) {
+      chunk_of(c0 + k * kCkptGroup, end, [&](auto full) {
         constexpr bool FULL = decltype(full)::v;
-        const int rem = H - (c0 + k * cs) - lane;
-        load_chunk<FULL>(A.dy + at + k * cs, rem, dy[k]);
-        if constexpr (DRES) load_chunk<FULL>(A.dres + at + k * cs, rem, dr[k]);
+        const int rem = end - (c0 + k * kCkptGroup) - lane;
+        load_chunk<FULL>(A.dy + at + k * kCkptGroup, rem, dy[k]);
+        if constexpr (DRES) load_chunk<FULL>(A.dres + at + k * kCkptGroup, rem, dr[k]);
       });
 #pragma unroll
     for (int k = 0; k < C; ++k)
-      chunk_of(c0 + k * cs, H, [&](auto full) {
-        const int rem = H - (c0 + k * cs) - lane;
+      chunk_of(c0 + k * kCkptGroup, end, [&](auto full) {
+        const int rem = end - (c0 + k * kCkptGroup) - lane;
         uint8_t b[4];
-        load_chunk<decltype(full)::v>(A.hq + at + k * cs, rem, b);
-        const float sc = __ldg(A.hs + (size_t)row * A.ng + wi + k * NW);
+        load_chunk<decltype(full)::v>(A.hq + at + k * kCkptGroup, rem, b);
+        const float sc = __ldg(A.hs + (size_t)row * A.ng + wi * per + k);
         float v[4];
         q8_decode4<FMT>(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410), v);
         n[k][0] = mul2(mul2(make_float2(v[0], v[1]), both(sc)), both(rs));
@@ -638,7 +640,7 @@ __global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) rms8_bwd_elem(const Bwd8<
     float2 dot2 = both(0.f);
 #pragma unroll
     for (int k = 0; k < C; ++k)
-      if (c0 + k * cs < H) {
+      if (c0 + k * kCkptGroup < end) {
         const float2 d0 = make_float2(to_f32(dy[k][0]), to_f32(dy[k][1]));
         const float2 d1 = make_float2(to_f32(dy[k][2]), to_f32(dy[k][3]));
         dot2 = fma2(mul2(d0, w[k][0]), n[k][0], fma2(mul2(d1, w[k][1]), n[k][1], dot2));
@@ -656,8 +658,8 @@ __global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) rms8_bwd_elem(const Bwd8<
     const float2 mc = both(-dot * A.inv_H);
 #pragma unroll
     for (int k = 0; k < C; ++k)
-      chunk_of(c0 + k * cs, H, [&](auto full) {
-        const int rem = H - (c0 + k * cs) - lane;
+      chunk_of(c0 + k * kCkptGroup, end, [&](auto full) {
+        const int rem = end - (c0 + k * kCkptGroup) - lane;
         float2 o[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -665,7 +667,7 @@ __global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) rms8_bwd_elem(const Bwd8<
           o[i] = mul2(both(rs), fma2(n[k][i], mc, mul2(d, w[k][i])));
           if constexpr (DRES) o[i] = add2(o[i], make_float2(to_f32(dr[k][2 * i]), to_f32(dr[k][2 * i + 1])));
         }
-        store_chunk<decltype(full)::v>(A.dx + at + k * cs, rem, o);
+        store_chunk<decltype(full)::v>(A.dx + at + k * kCkptGroup, rem, o);
       });
   }
 
@@ -678,8 +680,8 @@ __global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) rms8_bwd_elem(const Bwd8<
         const float a[4] = {acc[k][0].x, acc[k][0].y, acc[k][1].x, acc[k][1].y};
 #pragma unroll
         for (int m = 0; m < 4; ++m)
-          if (c0 + k * cs + 32 * m + lane < H) {
-            const int j = k * cs + 32 * m;
+          if (c0 + k * kCkptGroup + 32 * m + lane < end) {
+            const int j = k * kCkptGroup + 32 * m;
             const float v = t == 0 ? a[m] : srow[j] + a[m];
             if (t == GPB - 1) prow[j] = v;
             else srow[j] = v;
@@ -737,15 +739,16 @@ constexpr int64_t kMaxVecPerRow = 2048;  // 512 threads x 4 vectors
 struct Elem {
   bool fits;
   int nw;      // warps per row
+  int per;     // chunks per warp
   int block;   // threads
   int groups;  // rows per block and pass
 };
 Elem elem_geometry(int64_t H, int chunks) {
   const int64_t nchunk = (H + kCkptGroup - 1) / kCkptGroup;
-  if (nchunk > 32 * chunks) return {false, kWideBlock / 32, kWideBlock, 1};
+  if (nchunk > 32 * chunks) return {false, kWideBlock / 32, 0, kWideBlock, 1};
   const int nw = (int)((nchunk + chunks - 1) / chunks);
   const int groups = nw < 8 ? 8 / nw : 1;
-  return {true, nw, 32 * nw * groups, groups};
+  return {true, nw, (int)((nchunk + nw - 1) / nw), 32 * nw * groups, groups};
 }
 
 bool vec_width(int64_t H, size_t io) {
@@ -760,8 +763,8 @@ BwdGeometry bwd_geometry(int64_t H, size_t io) {
   if (!vec_width(H, io)) {
     const Elem e = elem_geometry(H, kElemBwdChunks);
     // At 64 registers each of an SM's four partitions holds eight warps, and a
-    // block's warps go to them in turn: five warps fit four times, not six (99 us
-    // against 125 for 30476 rows of 1101 values).
+    // block's warps go to them in turn: five warps fit four times, not six (counting
+    // six took a quarter longer for 30476 rows of 1101 values, now 90 us).
     return {0, 0, e.groups, e.fits ? 8 / ((e.block + 127) / 128) : 2};
   }
   const int64_t nvec = H * (int64_t)io / 16;
@@ -789,7 +792,7 @@ gbln_status fwd_launch(const Fwd8<T, W>& A, cudaStream_t s) {
   if (!vec) {
     const Elem e = elem_geometry(A.H, kElemChunks);
     const int64_t blocks = (A.rows + e.groups - 1) / e.groups;
-    if (e.fits) rms8_fwd_elem<T, W, RES, MODE><<<(unsigned)blocks, e.block, 0, s>>>(A, e.nw);
+    if (e.fits) rms8_fwd_elem<T, W, RES, MODE><<<(unsigned)blocks, e.block, 0, s>>>(A, e.nw, e.per);
     else rms8_fwd_wide<T, W, RES, MODE><<<(unsigned)A.rows, kWideBlock, 0, s>>>(A);
     return launch_status();
   }
@@ -825,9 +828,9 @@ gbln_status bwd_launch(const Bwd8<T, W>& A, int64_t P, cudaStream_t s) {
   if (!vec) {
     const Elem e = elem_geometry(A.H, kElemBwdChunks);
     const size_t smem = e.groups > 1 ? (size_t)A.H * sizeof(float) : 0;  // at most 1024 values
-    if (e.fits && e.block <= 256) rms8_bwd_elem<T, W, DRES, FMT, 256><<<grid, e.block, smem, s>>>(A, e.nw);
-    else if (e.fits && e.block <= 512) rms8_bwd_elem<T, W, DRES, FMT, 512><<<grid, e.block, 0, s>>>(A, e.nw);
-    else if (e.fits) rms8_bwd_elem<T, W, DRES, FMT, 1024><<<grid, e.block, 0, s>>>(A, e.nw);
+    if (e.fits && e.block <= 256) rms8_bwd_elem<T, W, DRES, FMT, 256><<<grid, e.block, smem, s>>>(A, e.nw, e.per);
+    else if (e.fits && e.block <= 512) rms8_bwd_elem<T, W, DRES, FMT, 512><<<grid, e.block, 0, s>>>(A, e.nw, e.per);
+    else if (e.fits) rms8_bwd_elem<T, W, DRES, FMT, 1024><<<grid, e.block, 0, s>>>(A, e.nw, e.per);
     else rms8_bwd_wide<T, W, DRES, FMT><<<grid, kWideBlock, 0, s>>>(A);
     return launch_status();
   }
