@@ -175,8 +175,15 @@ def _io(t: torch.Tensor) -> int:
 # The checks below run on every call and stand beside kernels of a few
 # microseconds, so they ask torch only for plain integers: get_device() is -1 on a
 # CPU tensor, and the raw stream handle comes without a Stream object around it.
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# A torch built without CUDA lacks those two names; the public functions stand in,
+# so that the package imports there and a call says what is missing.
+def _device_and_stream(c):
+    """(current device, raw handle of a device's current stream) as torch's module c offers them."""
+    return (getattr(c, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device()),
+            getattr(c, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream))
+
+
+_current_device, _raw_stream = _device_and_stream(torch._C)
 
 
 def _on_device(t: torch.Tensor, name: str) -> None:
