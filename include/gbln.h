@@ -569,6 +569,9 @@ typedef struct {
  * gbln_rope_fwd_ex for serving: rotates q and k by their tokens' positions, and
  * instead of writing k back quantises the rotated k (float32, unrounded) and v into
  * their caches at the tokens' slots; a group is one head of one token.
+ * A rotated pair is fmaf(x1, c, -(x2 s)), fmaf(x2, c, x1 s) in float32, whatever the sizes,
+ * strides and alignment: the stored bits of a token do not depend on how a prompt is cut.
+ * (gbln_rope_fwd_ex leaves these roundings to its kernels: its values may differ by one.)
  * q [T, Hq, D], k, v [T, Hk, D] io with token strides ld_q, ld_k, ld_v (e.g. inside one
  * packed QKV row); q_out as q with ld_q_out (may alias q exactly).  Hq may be 0 (q and
  * q_out ignored); Hk >= 1.

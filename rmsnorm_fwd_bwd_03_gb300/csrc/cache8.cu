@@ -159,25 +159,29 @@ struct HeadRun<bf16, 4, false> {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
   }
 };
+// x1 c - x2 s and x2 c + x1 s, f = (c, s).  The roundings are written out (one product
+// rounded, the other exact within the multiply-add): chosen by the compiler they were
+// not the same in every kernel, and a token's codes depended on the call that stored it.
+__device__ __forceinline__ float2 turn1(float x1, float x2, float2 f) {
+  return make_float2(__fmaf_rn(x1, f.x, -__fmul_rn(x2, f.y)), __fmaf_rn(x2, f.x, __fmul_rn(x1, f.y)));
+}
 template <int VEC, bool IL>
 __device__ __forceinline__ void turn(float (&xa)[VEC], float (&xb)[VEC], const float2 (&cs)[VEC]) {
   if constexpr (IL) {
 #pragma unroll
     for (int e = 0; e < VEC; e += 2) {
-      const float2 f = cs[e / 2], f2 = cs[VEC / 2 + e / 2];
-      const float a = xa[e] * f.x - xa[e + 1] * f.y, b = xa[e + 1] * f.x + xa[e] * f.y;
-      const float c = xb[e] * f2.x - xb[e + 1] * f2.y, d = xb[e + 1] * f2.x + xb[e] * f2.y;
-      xa[e] = a;
-      xa[e + 1] = b;
-      xb[e] = c;
-      xb[e + 1] = d;
+      const float2 a = turn1(xa[e], xa[e + 1], cs[e / 2]), b = turn1(xb[e], xb[e + 1], cs[VEC / 2 + e / 2]);
+      xa[e] = a.x;
+      xa[e + 1] = a.y;
+      xb[e] = b.x;
+      xb[e + 1] = b.y;
     }
   } else {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      const float a = xa[e] * cs[e].x - xb[e] * cs[e].y, b = xb[e] * cs[e].x + xa[e] * cs[e].y;
-      xa[e] = a;
-      xb[e] = b;
+      const float2 a = turn1(xa[e], xb[e], cs[e]);
+      xa[e] = a.x;
+      xb[e] = a.y;
     }
   }
 }
@@ -408,7 +412,7 @@ __global__ void __launch_bounds__(256) cache8_write_elem(const WriteArgs<T> A, b
       for (int k = 0; k < K; ++k) {
         const float a = to_f32(x1[f][k]), b = to_f32(x2[f][k]);
         // V is not rotated: it is taken as it is, whatever it holds
-        y[f][k] = h >= HR ? make_float2(a, b) : make_float2(a * cs[k].x - b * cs[k].y, b * cs[k].x + a * cs[k].y);
+        y[f][k] = h >= HR ? make_float2(a, b) : turn1(a, b, cs[k]);
         if (lane + 32 * k < half) m = max(m, max(abs_bits(y[f][k].x), abs_bits(y[f][k].y)));
       }
       if (h >= A.Hq) {
@@ -470,8 +474,7 @@ __global__ void __launch_bounds__(256) cache8_write_wide(const WriteArgs<T> A, b
     auto pair = [&](int i) {
       const float x1 = to_f32(src[IL ? 2 * i : i]), x2 = to_f32(src[IL ? 2 * i + 1 : half + i]);
       if (h >= HR) return make_float2(x1, x2);  // V is not rotated
-      const float2 f = ok ? __ldg(turns + i) : both(__int_as_float(0x7fc00000));
-      return make_float2(x1 * f.x - x2 * f.y, x2 * f.x + x1 * f.y);
+      return turn1(x1, x2, ok ? __ldg(turns + i) : both(__int_as_float(0x7fc00000)));
     };
     int64_t off = 0;
     const int64_t page = A.S.page_of(slot, off);

@@ -448,3 +448,40 @@ def test_two_streams_write_and_read_the_same_caches():
             outs.append(gb.cache8_read(slots[s], *two))
     torch.cuda.synchronize()
     assert torch.equal(torch.cat([o[0] for o in outs]), ko) and torch.equal(torch.cat([o[1] for o in outs]), vo)
+
+
+def _rotated(x, cs, pairing):
+    """The rotation in float32 with its roundings: one product rounded, the other exact within a
+    multiply-add.  Products of float32 are exact in float64, and so is a sum but for one rounding far
+    below float32's."""
+    x64 = x.double()
+    c, s = (cs[..., i].double()[:, None] for i in (0, 1))
+    a, b = (x64[..., 0::2], x64[..., 1::2]) if pairing == "interleaved" else x64.chunk(2, dim=-1)
+    f32 = lambda t: t.float().double()  # noqa: E731
+    y = f32(a * c - f32(b * s)), f32(b * c + f32(a * s))
+    return (torch.stack(y, dim=-1).flatten(-2) if pairing == "interleaved" else torch.cat(y, dim=-1)).float()
+
+
+@pytest.mark.parametrize("pairing", ["half", "interleaved"])
+@pytest.mark.parametrize("io,T,Hq,Hk,D", [
+    ("f32", 16, 8, 2, 128), ("f32", 3000, 8, 2, 128), ("f32", 2001, 9, 8, 64), ("f32", 300, 4, 2, 50), ("f32", 200, 5, 3, 100),
+    ("f32", 60, 3, 2, 250), ("f32", 40, 3, 2, 576), ("bf16", 300, 8, 2, 64), ("bf16", 300, 3, 2, 40), ("bf16", 2500, 32, 8, 128),
+    ("bf16", 60, 3, 2, 50)])
+def test_rotation_is_the_same_on_every_path(io, T, Hq, Hk, D, pairing):
+    # the roundings of a rotated value depend on no launch: aligned rows and rows one value off
+    # give the same queries, and the same codes and scales of K and V
+    table = gb.rope_table(T, D, THETA)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    slots = torch.arange(T, device="cuda")
+    r = np.random.default_rng(D)
+    table = torch.cat([table, table])[torch.from_numpy(r.permutation(2 * T)[:T].copy()).cuda()].contiguous()
+    x = [_randn((T, h, D), IO[io], 3 + h) for h in (Hq, Hk, Hk)]
+    for off in (0, 1):
+        q, k, v = (torch.empty(t.numel() + off, dtype=t.dtype, device="cuda")[off:].view(t.shape).copy_(t) for t in x)
+        cache = _caches(T, 1, Hk, D, "int8")
+        qo = gb.rope_fwd_cache8(q, k, v, pos, table, slots, *cache, pairing=pairing)
+        assert torch.equal(qo, _rotated(q, table, pairing).to(IO[io])), f"queries, {off} off"
+        kr = to64(_rotated(k, table, pairing))
+        check_exact(cache[0][:, 0], cache[1][:, 0], kr, "int8", f"k, {off} off")
+        check_exact(cache[2][:, 0], cache[3][:, 0], to64(v), "int8", f"v, {off} off")
+    assert gb.device_error() == 0
