@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(TPR * GPB, GPB > 1 ? 3 : 512 / TPR) rms8_bwd_v
       }
     }
   } else {
-    __shared__ float sacc[GPB][TPR * VPT * VEC];
+    __shared__ __align__(16) float sacc[GPB][TPR * VPT * VEC];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int iv = l + v * TPR;
