@@ -92,8 +92,11 @@ __device__ __forceinline__ float gauss_cdf_as(float x, float& ex) {
   ex = exp_fast(-z * z);
   const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, kAsA5, kAsA4), kAsA3), kAsA2), kAsA1);
   const float half_erfc = 0.5f * poly * ex;
-  return x >= 0.f ? 1.0f - half_erfc : half_erfc;
+  return x >= 0.f ? __fsub_rn(1.0f, half_erfc) : half_erfc;
 }
+
+// 2 z of the tanh form.
+__device__ __forceinline__ float gelu_arg(float x) { return kGeluK * fmaf(kGeluC * x * x, x, x); }
 
 // Activation value f(x) and, for the backward pass, f(x) and f'(x) together.
 template <typename T, int ACT>
@@ -102,7 +105,7 @@ __device__ __forceinline__ float act_f(float x) {
     if constexpr (sizeof(T) == 4) return x / (1.0f + expf(-x));
     else return x * rcp_ftz(1.0f + exp_fast(-x));
   } else if constexpr (ACT == GBLN_ACT_GELU_TANH) {
-    return x * sigmoid<T>(kGeluK * (x + kGeluC * x * x * x));
+    return x * sigmoid<T>(gelu_arg(x));
   } else if constexpr (ACT == GBLN_ACT_GELU_ERF) {
     if constexpr (sizeof(T) == 4) {
       return 0.5f * x * (1.0f + erff(x * kInvSqrt2));
@@ -122,7 +125,7 @@ __device__ __forceinline__ void act_fd(float x, float& f, float& d) {
     f = x * s;
     d = s * (1.0f + x * (1.0f - s));
   } else if constexpr (ACT == GBLN_ACT_GELU_TANH) {
-    const float s = sigmoid<T>(kGeluK * (x + kGeluC * x * x * x));
+    const float s = sigmoid<T>(gelu_arg(x));
     f = x * s;
     d = s + x * s * (1.0f - s) * kGeluK * (1.0f + 3.0f * kGeluC * x * x);
   } else if constexpr (ACT == GBLN_ACT_GELU_ERF) {
@@ -406,8 +409,10 @@ glu_fwd_mx(const T* gate, const T* up, MxOut mx, int64_t T_, int64_t ncol, int64
 }
 
 // f(gate) * up of N values for the kernels that also quantise.  With bf16 inputs
-// the multiplications and additions of act_f go two at a time (the same
-// operations, so the same bits); the exponentials and reciprocals stay single.
+// the multiplications and additions of act_f go two at a time; the exponentials and
+// reciprocals stay single.  Where a product meets a sum, both write out whether it is
+// rounded in between (the tanh form's argument: no; 1 - erfc / 2: yes), so that they
+// give the same bits: out is glu_fwd's, and codes do not depend on a row's alignment.
 template <int ACT>
 __device__ __forceinline__ float2 act_f2(float2 x) {
   if constexpr (ACT == GBLN_ACT_RELU) {
@@ -427,8 +432,7 @@ __device__ __forceinline__ float2 act_f2(float2 x) {
     if constexpr (ACT == GBLN_ACT_SILU) {
       a = x;
     } else {
-      const float2 cube = mul2(mul2(mul2(both(kGeluC), x), x), x);
-      a = mul2(both(kGeluK), add2(x, cube));
+      a = mul2(both(kGeluK), fma2(mul2(mul2(both(kGeluC), x), x), x, x));
     }
     const float2 n = mul2(make_float2(-a.x, -a.y), both(kLog2e));
     const float2 d = add2(both(1.0f), make_float2(ex2_ftz(n.x), ex2_ftz(n.y)));

@@ -654,3 +654,19 @@ def test_two_streams_at_once():
     for g, (_, want) in zip(got, states):
         for p, q in zip(g, want):
             assert _same_bits(p, q)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("act", list(gb.ACT))
+def test_gated_units_give_the_same_bits_on_every_path(io, act):
+    # out of the forward that saves checkpoints is glu_fwd's, and the row-scaled codes do not
+    # depend on alignment; 20000 and 28672: unaligned rows are read twice
+    for T, I in ((2001, 1024), (301, 5000), (300, 20000), (200, 28672)):
+        gate, up = 2 * _randn((T, I), IO[io], 1), _randn((T, I), IO[io], 2)
+        want = gb.glu_fwd(gate, up, act)
+        q, s = gb.glu_fwd_fp8(gate, up, act)
+        for g, u in ((gate, up), (_unaligned(gate), _unaligned(up))):
+            assert _same_bits(gb.glu_fwd(g, u, act), want)
+            assert _same_bits(gb.glu_fwd_ckpt8(g, u, act)[0], want)
+            q2, s2 = gb.glu_fwd_fp8(g, u, act)
+            assert _same_bits(q2, q) and _same_bits(s2, s)
