@@ -460,8 +460,10 @@ gbln_status gbln_glu_fwd_mxfp8(const void* gate, const void* up, uint8_t* out_e4
  * float32 implementation of these steps.  An all-zero group has the scale
  * 2^-100 / qmax and codes 0.  A group that holds an infinity or a NaN gets the
  * scale NaN (its codes are unspecified): all of it reads back as NaN.
- * INT8 is off by at most a / 254 per value, E4M3 by 2^-4 of the value: INT8 is the
- * closer one for values of one size, E4M3 where a group holds outliers.
+ * A value is off by at most a / 254 with INT8, by the larger of 2^-4 of itself and
+ * a / 448 * 2^-10 with E4M3 (values below that last bound become 0), each plus 2^-21 of
+ * itself for the float32 roundings.  INT8 is the closer one for values of one size,
+ * E4M3 where a group holds outliers.
  */
 typedef enum { GBLN_Q8_INT8 = 0, GBLN_Q8_E4M3 = 1 } gbln_q8;
 
@@ -499,9 +501,10 @@ gbln_status gbln_glu_fwd_fp8(const void* gate, const void* up, uint8_t* out_e4m3
 /*
  * gbln_rmsnorm_fwd that also writes the checkpoint of h (= x + residual rounded to io,
  * or x) in the same pass: h8 [T, H] bytes, h8_scale [T, ceil(H / 128)] float32.  y, h
- * and rstd are those of gbln_rmsnorm_fwd.  Any H and alignment.  Arguments, aliasing
- * and errors as gbln_rmsnorm_fwd; INVALID_ARG also for an unknown fmt or a null h8 /
- * h8_scale.
+ * and rstd as gbln_rmsnorm_fwd: h to the bit; rstd may differ from it by the rounding of
+ * the row's sum, which these kernels take in another order where rows are unaligned or
+ * wide, and y with it.  Any H and alignment.  Arguments, aliasing and errors as
+ * gbln_rmsnorm_fwd; INVALID_ARG also for an unknown fmt or a null h8 / h8_scale.
  */
 gbln_status gbln_rmsnorm_fwd_ckpt8(const void* x, const void* residual, const void* weight,
                                    void* y, void* residual_out, float* rstd, uint8_t* h8,

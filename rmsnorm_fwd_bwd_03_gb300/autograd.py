@@ -16,8 +16,8 @@ computes anything itself.
 ``rms_norm`` and ``swiglu`` take ``checkpoint="int8"`` or ``"e4m3"``: what the backward
 pass needs of the input is then kept in 8 bits (one float32 scale per 128 values
 of a row, 1.03 bytes per value) instead of in the input's dtype, and the backward
-kernels read the codes.  The outputs are the same; the gradients are those of the
-8-bit values.  Memory is saved where nothing else keeps the input: the
+kernels read the codes.  The outputs are those without it (``rms_norm``'s up to the
+float32 rounding of a row's sum); the gradients are those of the 8-bit values.  Memory is saved where nothing else keeps the input: the
 normalised tensor where the residual stream moves on, gate and up always.
 """
 

@@ -10,9 +10,9 @@
 //
 // |v * inv| <= qmax (1 + 2^-22), which rounds to at most qmax: no clamp.  A
 // group that holds an infinity or a NaN gets the scale NaN, so that all of it
-// reads back as NaN.  The scale is exact to half a float32 step, so INT8 is off
-// by at most a / 254 per value and E4M3 by 2^-4 of the value (plus a / 448 * 2^-10
-// among its subnormals).
+// reads back as NaN.  INT8 is off by at most a / 254 per value and E4M3 by the larger
+// of 2^-4 of the value and a / 448 * 2^-10 (half a step of its subnormals), each plus
+// 2^-21 of the value: the roundings of inv, of v * inv, of the scale and of code * scale.
 #pragma once
 
 #include "common.cuh"

@@ -670,3 +670,45 @@ def test_gated_units_give_the_same_bits_on_every_path(io, act):
             assert _same_bits(gb.glu_fwd_ckpt8(g, u, act)[0], want)
             q2, s2 = gb.glu_fwd_fp8(g, u, act)
             assert _same_bits(q2, q) and _same_bits(s2, s)
+
+
+@pytest.mark.parametrize("io,wt", TYPES)
+@pytest.mark.parametrize("H", [64, 896, 1021, 4095, 4096, 8200, 16384, 20001])
+def test_norm_outputs_beside_the_plain_forward(io, wt, H):
+    # h to the bit.  rstd: the row's sum of squares takes at most 60 float32 additions in a row in any of
+    # the kernels (all terms positive: 60 * 2^-24 of it, half of that in rstd), the mean, eps and rsqrt
+    # another 6 * 2^-24: two kernels are within 2 * 36 * 2^-24 < 2^-17 of one another.  y adds two
+    # roundings, and at bf16 the final one may fall to the neighbour: 2^-7 of the value.
+    T, dt = 61, IO[io]
+    x, r, w = _randn((T, H), dt, 1), _randn((T, H), dt, 2), _weight(H, IO[wt])
+    tol_y = 2.0 ** -16 if io == "f32" else 2.0 ** -7 + 2.0 ** -14
+    for unaligned in (False, True):
+        a, b, c = (_unaligned(t) if unaligned else t for t in (x, r, w))
+        for res in (None, b):
+            y0, h0, rstd0 = gb.rmsnorm_fwd(a, c, 1e-5, res)
+            H64 = to64(h0)
+            ref = 1 / np.sqrt((H64 ** 2).mean(-1) + 1e-5)
+            y1, h1, rstd1, _, _ = gb.rmsnorm_fwd_ckpt8(a, c, 1e-5, res)
+            y2, yq, ys, h2, rstd2 = gb.rmsnorm_fwd_fp8(a, c, 1e-5, res)
+            for y, h, rstd in ((y1, h1, rstd1), (y2, h2, rstd2)):
+                assert _same_bits(h, h0)
+                assert ((rstd.double() - rstd0.double()).abs() <= 2.0 ** -17 * rstd0.double()).all()
+                assert ((y.double() - y0.double()).abs() <= tol_y * y0.double().abs()).all()
+            u = np.abs(H64.astype(np.float32) * to64(c).astype(np.float32)).astype(np.float64)
+            check_rstd(to64(ys), u.max(-1) * ref / 448, "row scale")
+            assert np.array_equal(codes64(yq), q8.rmsnorm_fwd_fp8(H64, None, to64(c), 1e-5, io)[0])
+    xa, ra, wa = (t.clone().requires_grad_() for t in (x, r, w))
+    y1, h1 = ga.rms_norm(xa, wa, 1e-5, ra, checkpoint="int8")
+    y0, h0 = ga.rms_norm(xa, wa, 1e-5, ra)
+    assert _same_bits(h1, h0) and ((y1.double() - y0.double()).abs() <= tol_y * y0.double().abs()).all()
+
+
+@pytest.mark.parametrize("H", [256, 777, 4096, 16384, 17001])
+def test_fp8_norm_residual_out_over_its_inputs(H):
+    T = 33
+    x, r, w = _randn((T, H), torch.bfloat16, 1), _randn((T, H), torch.bfloat16, 2), _weight(H, torch.bfloat16)
+    want = gb.rmsnorm_fwd_fp8(x, w, 1e-5, r)
+    for target in (0, 1):
+        a, b = x.clone(), r.clone()
+        for p, q in zip(gb.rmsnorm_fwd_fp8(a, w, 1e-5, b, residual_out=(a, b)[target]), want):
+            assert _same_bits(p, q)

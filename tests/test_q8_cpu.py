@@ -294,3 +294,24 @@ def test_binding_refuses_cache_tensors():
         gb.cache8_read(torch.zeros(3, dtype=torch.int32), codes, scale, codes, scale)
     with pytest.raises(ValueError, match="k_out"):
         gb.cache8_read(torch.zeros(3, dtype=torch.int64), codes, scale, codes, scale, k_out=_t(3, 2, 16, dtype=f32))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_stated_bounds_hold_beside_outliers(fmt):
+    # the bound the header states, in the group's largest magnitude a: values from 2^-30 of it to
+    # itself, where E4M3 codes run through its normal range, its subnormals and zero.  Four float32
+    # roundings (q / a, v * inv, a / q, code * scale): under 5 * 2^-24 < 2^-21 of the value
+    rng = np.random.default_rng(7)
+    a = 10.0 ** rng.uniform(-6, 6, (400, 1))
+    v = (a * 2.0 ** -rng.uniform(0, 30, (400, 96)) * rng.choice([-1.0, 1.0], (400, 96)))
+    v[:, :1] = a
+    v = v.astype(np.float32).astype(np.float64)
+    a = np.abs(v).max(-1, keepdims=True)
+    codes, scale = q8.quantize(v, fmt)
+    value = (codes.astype(np.float32) * scale.astype(np.float32)[:, None]).astype(np.float64)
+    own = a / 254 if fmt == "int8" else np.maximum(2.0 ** -4 * np.abs(v), a / 448 * 2.0 ** -10)
+    assert (np.abs(value - v) <= own + 2.0 ** -21 * np.abs(v)).all()
+    if fmt == "e4m3":
+        small = np.abs(v) < a / 448 * 2.0 ** -10 * (1 - 2.0 ** -20)
+        assert small.any() and (codes[small] == 0).all()
+        assert (np.abs(value - v) > 2.0 ** -4 * np.abs(v))[np.abs(v) < a * 2.0 ** -16].any()  # not 2^-4 of all values
