@@ -712,3 +712,84 @@ def test_fp8_norm_residual_out_over_its_inputs(H):
         a, b = x.clone(), r.clone()
         for p, q in zip(gb.rmsnorm_fwd_fp8(a, w, 1e-5, b, residual_out=(a, b)[target]), want):
             assert _same_bits(p, q)
+
+
+# ---------------------------------------------------------------------------
+# Launch geometries that small calls do not reach
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("act", list(gb.ACT))
+@pytest.mark.parametrize("io,I", [("bf16", 16392), ("bf16", 20000), ("bf16", 32760), ("bf16", 32768),
+                                  ("f32", 8196), ("f32", 12300), ("f32", 16384)])
+def test_glu_wide_rows_of_many_tokens(io, I, act):
+    # 2049 to 4096 vectors per row and more rows than SMs: rows stream through shared memory, the
+    # last stage of a row holding 16 bytes (2049 vectors), a part or a whole of its size
+    T = 3 * torch.cuda.get_device_properties(0).multi_processor_count + 1
+    gate, up = _randn((T, 2 * I), IO[io], 1).chunk(2, dim=-1)
+    q, s = gb.glu_fwd_fp8(gate, up, act)
+    r = torch.from_numpy(sample_rows(T, 12)).cuda()
+    G, U = to64(gate[r]), to64(up[r])
+    check_window(q[r], s[r], q8.glu_out(act, G, U), _glu_window(act, G, U, io), "e4m3", f"{io} {I} {act}")
+    q2, s2 = gb.glu_fwd_fp8(gate[:100], up[:100], act)  # the same rows, fewer than SMs: another kernel
+    assert _same_bits(q2, q[:100]) and _same_bits(s2, s[:100])
+    assert gb.device_error() == 0
+
+
+@pytest.mark.parametrize("io,I", [("bf16", 32776), ("bf16", 65536), ("bf16", 65544), ("bf16", 131072), ("bf16", 131080),
+                                  ("f32", 32768), ("f32", 32772), ("f32", 65536), ("f32", 65540)])
+def test_glu_rows_of_a_cluster_and_beyond(io, I):
+    # four and eight blocks per row, and rows too wide for those
+    T = 5
+    gate, up = _randn((T, 2 * I), IO[io], 3).chunk(2, dim=-1)
+    q, s = gb.glu_fwd_fp8(gate, up)
+    G, U = to64(gate), to64(up)
+    check_window(q, s, q8.glu_out("silu", G, U), _glu_window("silu", G, U, io), "e4m3", f"{io} {I}")
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_glu_checkpoints_of_more_groups_than_run_at_once(io, fmt):
+    # odd width: a warp takes several units one after the other
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    T, I = 8 * 64 * sms + 4321, 129
+    gate, up, dout = (_randn((T, I), IO[io], s) for s in (1, 2, 3))
+    out, gq, gs, uq, us = gb.glu_fwd_ckpt8(gate, up, "gelu_tanh", fmt=fmt)
+    dgate, dup = gb.glu_bwd_ckpt8(dout, gq, gs, uq, us, "gelu_tanh")
+    rows = sample_rows(T, 200, extra=(8 * 64 * sms - 1, 8 * 64 * sms))
+    r = torch.from_numpy(rows).cuda()
+    G, U = to64(gate[r]), to64(up[r])
+    check_io(to64(out[r]), q8.glu_out("gelu_tanh", G, U), io, "out")
+    check_exact(gq[r], gs[r], G, fmt, "gate8", 128)
+    check_exact(uq[r], us[r], U, fmt, "up8", 128)
+    dg, du = oracle.glu_bwd("gelu_tanh", to64(dout[r]), q8.values(codes64(gq[r]), codes64(gs[r]), 128),
+                            q8.values(codes64(uq[r]), codes64(us[r]), 128))
+    check_io(to64(dgate[r]), dg, io, "dgate")
+    check_io(to64(dup[r]), du, io, "dup")
+
+
+@pytest.mark.parametrize("T,H,io,wt", [
+    (1500, 2500, "bf16", "bf16"), (1201, 5001, "bf16", "f32"), (1001, 8190, "bf16", "bf16"),    # blocks of 320 to 1024 threads per row
+    (1500, 2050, "f32", "f32"), (1001, 8193, "bf16", "bf16"), (1003, 8200, "f32", "f32"), (1001, 20001, "bf16", "f32"),
+    (3001, 512, "f32", "f32"), (3001, 64, "bf16", "bf16"), (1001, 16384, "bf16", "bf16"), (5001, 257, "f32", "f32")])
+def test_norm_checkpoint_step_of_many_rows(T, H, io, wt):
+    # several rows per block of the backward, one after the other: dW over all of them in
+    # float64, the rest on sampled rows
+    dt, eps = IO[io], 1e-5
+    x, r, dy, dres = (_randn((T, H), dt, s) for s in (1, 2, 3, 4))
+    w = _weight(H, IO[wt])
+    W = to64(w)
+    for res, fmt in ((True, "int8"), (False, "e4m3")):
+        y, h, rstd, h8, hs = gb.rmsnorm_fwd_ckpt8(x, w, eps, r if res else None, fmt=fmt)
+        dx, part, P = gb.rmsnorm_bwd_ckpt8(dy, h8, hs, w, rstd, dres if res else None)
+        assert P < T
+        kept = h8.double() * hs.double().repeat_interleave(128, 1)[:, :H]
+        rs = 1 / torch.sqrt(h.double().square().mean(-1, keepdim=True) + eps)
+        check_dw(to64(gb.rmsnorm_dw_finalize(part, P)), (dy.double() * kept * rs).sum(0).cpu().numpy())
+        rows = sample_rows(T, 60)
+        i = torch.from_numpy(rows).cuda()
+        H64, RS = to64(h[i]), rs[i].cpu().numpy()[:, 0]
+        check_rstd(to64(rstd[i]), RS)
+        check_io(to64(y[i]), W * H64 * RS[:, None], io, "y")
+        check_exact(h8[i], hs[i], H64, fmt, "h8", 128)
+        dx64, _ = q8.rmsnorm_bwd_kept(to64(dy[i]), to64(dres[i]) if res else None, kept[i].cpu().numpy(), W, RS)
+        check_io(to64(dx[i]), dx64, io, "dx")
