@@ -461,7 +461,8 @@ __device__ __forceinline__ void glu_values(const float (&g)[N], const float (&u)
 // block: several rows per block when TPR is a warp; one row per block beyond;
 // one row per cluster of CL blocks for rows beyond 1024 threads' registers, whose
 // maxima meet through distributed shared memory.  32768 x 14336 bf16, SiLU: 345 us
-// (346 us at the copy rate); GeLU-erf 418 us, bound by its instructions.
+// (346 us at the copy rate); GeLU-erf 418 us: half as many instructions again, and 1.7
+// warps wait for an arithmetic pipe at every issue (0.4 in the unaligned SiLU form).
 // ---------------------------------------------------------------------------
 template <typename T, int ACT, int TPR, int VPT, int RPB, int CL>
 __device__ __forceinline__ void glu_row8(const T* gate, const T* up, uint8_t* q, float* sc, int64_t rows,
@@ -685,7 +686,8 @@ __device__ __forceinline__ void store_run_codes(uint8_t* p, int rem, const float
 // the values l, l + 32, l + 64, l + 96 of each; up to kRow8Runs runs per warp wait
 // in registers (blocks of up to 1024 threads: 16384 values), wider rows are read
 // a second time to write the codes.  8190 x 4097 bf16 38 us (25 us at the copy
-// rate): bound by its instructions, one value per lane and access.
+// rate): one value per lane and access, 70% of the issue slots and half of an SM's
+// warps in use, which wait for their loads.
 constexpr int kRow8Runs = 4;
 
 template <typename T, int ACT, bool FITS>
@@ -759,7 +761,7 @@ glu_fwd_row8_elem(const T* gate, const T* up, uint8_t* q, float* sc, int64_t row
 // eight reductions cost eight shuffles instead of thirty-two, and leave each
 // group's maximum with two lanes (four at float32): one divides for 1 / scale,
 // the other for the scale.  With a reduction and two divisions per lane and
-// group instead, the kernel ran at 81% of the copy rate, bound by instructions.
+// group instead, the kernel ran at 81% of the copy rate.
 // 32768 x 14336 bf16, SiLU: 555 us (558 us at the copy rate).
 // ---------------------------------------------------------------------------
 struct GluCkpt {
@@ -870,8 +872,8 @@ glu_fwd_ckpt(const T* gate, const T* up, T* out, const GluCkpt C, int64_t T_, in
 // Any alignment and width: a warp takes four consecutive checkpoint groups of a row,
 // lane l the values l, l + 32, l + 64, l + 96 of each; the groups share one division
 // and the 64-bit addresses, which two groups of their own addresses spent a tenth of
-// the time on.  8190 x 4097 bf16 55 us (that form 62), the backward 59 (68), of 40 us
-// at the copy rate: bound by their instructions.
+// the time on.  8190 x 4097 bf16 55 us (that form 62), the backward 60 (68), of 40 us
+// at the copy rate: issue slots 56 and 63%, 40 and 50% of an SM's warps, waiting for loads.
 constexpr int kElemGroups = 4;
 
 // unit(F, FULL, first value, values) over a warp's `left` values: four groups at once

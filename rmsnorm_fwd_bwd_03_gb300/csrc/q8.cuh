@@ -32,7 +32,7 @@ inline bool q8_ok(int fmt) { return fmt == GBLN_Q8_INT8 || fmt == GBLN_Q8_E4M3; 
 
 // Two float32 operations in one instruction (each rounded to nearest even by
 // itself): the codes cost two to three operations per value beside the kernels'
-// own arithmetic, and issue slots, not HBM, are what runs out first.
+// own arithmetic, and every instruction stands between a warp's loads.
 #define GBLN_F2_OP(name, op)                                                                           \
   __device__ __forceinline__ float2 name(float2 a, float2 b) {                                         \
     float2 r;                                                                                          \

@@ -193,9 +193,11 @@ __global__ void __launch_bounds__(BLOCK) rms8_fwd_vec(const Fwd8<T, W> A) {
 // l + 96: every access of a warp is contiguous, and a chunk is a checkpoint
 // group.  NW warps per row take `per` consecutive chunks each, at most kElemChunks,
 // which stay in registers.  Offsets from a warp's first value are immediates and
-// only a row's last chunk is predicated: at one value per lane and access these
-// kernels are bound by their instructions, not by HBM.  65536 x 1021 bf16: row
-// scale 113 us, checkpoint 119 us (69 and 89 us at the copy rate).
+// only a row's last chunk is predicated: at one value per lane and access a warp
+// issues 40 instructions per 32 values and has few bytes in flight.  Nothing is full
+// (issue slots 60 to 63%, load/store pipe 50%, half of an SM's warps): the warps wait
+// for their loads.  65536 x 1021 bf16: row scale 113 us, checkpoint 119 us (69 and 89 us
+// at the copy rate).
 // ---------------------------------------------------------------------------
 constexpr int kElemChunks = 4;
 
@@ -571,9 +573,10 @@ __global__ void __launch_bounds__(TPR * GPB, GPB > 1 ? 3 : 512 / TPR) rms8_bwd_v
 // Backward, element path: chunks of 128 values per warp as in rms8_fwd_elem, two
 // per warp: with their weights, dW sums and inputs they fill 64 registers, and
 // 1024 threads per SM are resident.  The warp asks for its next row in L2 while
-// it works on this one.  Bound by its instructions: 65536 x 1021 bf16 118 us (69 us
-// at the copy rate; 123 with every NW-th chunk, whose addresses are not immediates),
-// 8194 x 4095 81 us (35).
+// it works on this one.  As there, the warps wait for their loads: 65536 x 1021 bf16
+// 118 us (69 us at the copy rate; 123 with every NW-th chunk, whose addresses are not
+// immediates), 8194 x 4095 81 us (35).  A block of 18 warps is alone on its SM: 7708 x
+// 4353 110 us (35), with 28% of an SM's warps and 37% of its issue slots in use.
 // ---------------------------------------------------------------------------
 constexpr int kElemBwdChunks = 2;
 
