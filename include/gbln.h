@@ -558,7 +558,8 @@ gbln_status gbln_glu_bwd_ckpt8(const void* dout, const uint8_t* gate8, const flo
  *   codes + p * page_stride + o * slot_stride + h * head_stride               (bytes)
  *   scale + p * scale_page_stride + o * scale_slot_stride + h * scale_head_stride (floats)
  * so pages may be [page_size, Hk, D] or [Hk, page_size, D], and K and V may be
- * interleaved in one allocation.  The strides must keep pages, slots and heads apart.
+ * interleaved in one allocation.  The strides must keep pages, slots and heads apart, and
+ * K's from V's where they are written.
  */
 typedef struct {
   uint8_t* codes;
@@ -586,7 +587,8 @@ typedef struct {
  * their contents.  With two tokens on one slot, that slot's contents are unspecified.
  * k_cache, v_cache: host structs, read during the call; same pages and page_size.
  * Errors: INVALID_ARG as gbln_rope_fwd_ex, and for Hk < 1, an unknown fmt, a null or
- * inconsistent cache, strides that let pages, slots or heads overlap; CUDA.
+ * inconsistent cache, strides that let pages, slots or heads overlap, K and V caches at
+ * one address; CUDA.
  */
 gbln_status gbln_rope_fwd_cache8(const void* q, const void* k, const void* v, void* q_out,
                                  const int32_t* positions, const float* cos_sin, int64_t max_pos,

@@ -784,6 +784,8 @@ extern "C" gbln_status gbln_rope_fwd_cache8(const void* q, const void* k, const 
   if (k_cache->pages > 0 && (!k_cache->codes || !k_cache->scale || !v_cache->codes || !v_cache->scale))
     return GBLN_ERR_INVALID_ARG;
   if (!aligned_to(cos_sin, 8) || !aligned_to(slots, 8)) return GBLN_ERR_INVALID_ARG;  // float2, int64
+  // one cache for both would leave either's codes with the other's scale
+  if (k_cache->pages > 0 && (k_cache->codes == v_cache->codes || k_cache->scale == v_cache->scale)) return GBLN_ERR_INVALID_ARG;
   unsigned int* err = device_error_word();
   if (!err) return GBLN_ERR_CUDA;
   const bool il = pairing == GBLN_ROPE_INTERLEAVED;

@@ -315,3 +315,30 @@ def test_stated_bounds_hold_beside_outliers(fmt):
         small = np.abs(v) < a / 448 * 2.0 ** -10 * (1 - 2.0 ** -20)
         assert small.any() and (codes[small] == 0).all()
         assert (np.abs(value - v) > 2.0 ** -4 * np.abs(v))[np.abs(v) < a * 2.0 ** -16].any()  # not 2^-4 of all values
+
+
+def test_cache_write_refuses_one_cache_for_k_and_v(lib):
+    # stored into the same memory, K and V would leave either's codes with the other's scale; every
+    # other refusal stands with caches of their own too
+    f, ref = FAKE, ctypes.byref
+    own = {"codes": FAKE + (1 << 20), "scale": FAKE + (2 << 20)}
+
+    def write(q=f, k=f, v=f, qo=f, pos=f, cs=f, mp=9, sl=f, kc=None, vc=None, T=4, Hq=4, Hk=2, D=16, ldq=64, ldk=32,
+              ldv=32, ldqo=64, pairing=0, fmt=0, io=BF16):
+        kc, vc = kc or _cache(), vc or _cache(**own)
+        return lib.gbln_rope_fwd_cache8(q, k, v, qo, pos, cs, mp, sl, ref(kc), ref(vc), T, Hq, Hk, D, ldq, ldk, ldv, ldqo,
+                                        pairing, fmt, io, None)
+
+    for shared in ("codes", "scale"):
+        assert write(vc=_cache(**{**own, shared: FAKE})) == INVALID, shared
+    assert write(vc=_cache()) == INVALID
+    assert write(T=0, vc=_cache()) == OK  # nothing is written
+    for kw in ({"q": None}, {"k": None}, {"v": None}, {"qo": None}, {"pos": None}, {"cs": None}, {"sl": None},
+               {"cs": FAKE + 4}, {"sl": FAKE + 4}, {"mp": -1}, {"T": -1}, {"T": 1 << 34}, {"Hq": -1}, {"Hk": 0}, {"D": 7},
+               {"D": 0}, {"ldq": 63}, {"ldk": 31}, {"ldv": 31}, {"ldqo": 63}, {"ldk": 1 << 60}, {"pairing": 2},
+               {"fmt": 2}, {"io": 2}, {"Hq": 1 << 30, "ldq": 1 << 40, "ldqo": 1 << 40}):
+        assert write(**kw) == INVALID, kw
+    for bad in BAD_CACHES:
+        assert write(kc=_cache(**bad)) == INVALID, bad
+        assert write(vc=_cache(**{**own, **bad})) == INVALID, bad
+    assert write(vc=_cache(pages=3, **own)) == INVALID
