@@ -17,8 +17,9 @@ computes anything itself.
 pass needs of the input is then kept in 8 bits (one float32 scale per 128 values
 of a row, 1.03 bytes per value) instead of in the input's dtype, and the backward
 kernels read the codes.  The outputs are those without it (``rms_norm``'s up to the
-float32 rounding of a row's sum); the gradients are those of the 8-bit values.  Memory is saved where nothing else keeps the input: the
-normalised tensor where the residual stream moves on, gate and up always.
+float32 rounding of a row's sum); the gradients are those of the 8-bit values.
+Memory is saved where nothing else keeps the input: the normalised tensor where the
+residual stream moves on, gate and up always.
 """
 
 from __future__ import annotations

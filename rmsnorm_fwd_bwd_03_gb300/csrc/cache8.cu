@@ -79,9 +79,9 @@ struct WriteArgs {
 // anything that depends on the token's slot or position, and the maxima and
 // divisions of its K and V heads run side by side.  (With queries, K and V taken
 // alike, head after head, the chain of each one's reduction and division showed:
-// 95 us instead of 77 for 32768 tokens of 16 / 8 heads of 128, 70 us at the copy
+// 95 us instead of 79 for 32768 tokens of 16 / 8 heads of 128, 70 us at the copy
 // rate.)  65536 tokens of 32 / 8 heads of 128: 223 us, 219 us at the copy rate; 16
-// tokens 2.7 us.
+// tokens 2.3 us.
 // ---------------------------------------------------------------------------
 // Head rows per lane and pass of a query warp: 8 measured 112 us, 6 119 and 4 117 for
 // 32768 tokens of 32 / 8 heads of 128 (110 us at the copy rate).

@@ -425,7 +425,7 @@ __device__ __forceinline__ float2 act_f2(float2 x) {
     const float2 ex = make_float2(ex2_ftz(a.x), ex2_ftz(a.y));
     const float2 poly = mul2(t, fma2(t, fma2(t, fma2(t, fma2(t, both(kAsA5), both(kAsA4)), both(kAsA3)), both(kAsA2)), both(kAsA1)));
     const float2 h = mul2(mul2(both(0.5f), poly), ex);
-    const float2 up = add2(both(1.0f), make_float2(-h.x, -h.y));
+    const float2 up = make_float2(__fsub_rn(1.0f, h.x), __fsub_rn(1.0f, h.y));  // a paired sum may be fused
     return mul2(x, make_float2(x.x >= 0.f ? up.x : h.x, x.y >= 0.f ? up.y : h.y));
   } else {
     float2 a;  // argument of the sigmoid
@@ -461,7 +461,7 @@ __device__ __forceinline__ void glu_values(const float (&g)[N], const float (&u)
 // block: several rows per block when TPR is a warp; one row per block beyond;
 // one row per cluster of CL blocks for rows beyond 1024 threads' registers, whose
 // maxima meet through distributed shared memory.  32768 x 14336 bf16, SiLU: 345 us
-// (346 us at the copy rate); GeLU-erf 418 us: half as many instructions again, and 1.7
+// (346 us at the copy rate); GeLU-erf 406 us: half as many instructions again, and 1.5
 // warps wait for an arithmetic pipe at every issue (0.4 in the unaligned SiLU form).
 // ---------------------------------------------------------------------------
 template <typename T, int ACT, int TPR, int VPT, int RPB, int CL>
@@ -545,7 +545,8 @@ glu_fwd_row8_cluster(const T* gate, const T* up, uint8_t* q, float* sc, int64_t 
 // vectors of each per stage), and 512 consumer threads turn a stage into float32
 // outputs in registers, meet once per row for the maximum, and store the codes.
 // 16383 x 28672 bf16: 331 us (346 us at the copy rate; this pass mostly reads),
-// with a block of 1024 threads per row 497 us.
+// with a block of 1024 threads per row 497 us; 4000 rows of 16640 67 us (49), of 32768
+// 101 us (97).
 // ---------------------------------------------------------------------------
 constexpr int kRingThreads = 512;                             // consumers
 constexpr int kRingStages = 12;                               // 16 KB each
