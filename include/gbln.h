@@ -6,7 +6,8 @@
  * table, per-document positions) and SwiGLU (forward, backward); LayerNorm,
  * other gated and plain activations, MXFP8 and row-scaled FP8 outputs for the
  * next GEMM, 8-bit activation checkpoints with the backward passes that read
- * them, and a quantised K/V cache.
+ * them, and a quantised K/V cache; per-head norms of Q and K with the rotation in
+ * one pass and rotary embedding with several position axes.
  *
  * Sources that name these operators (they print no formulas; the standard
  * definitions are used and written out at each entry point):
@@ -608,6 +609,113 @@ gbln_status gbln_cache8_read(const int64_t* slots, const gbln_cache8* k_cache,
                              const gbln_cache8* v_cache, void* k_out, void* v_out, int64_t T,
                              int32_t Hk, int32_t D, int64_t ld_k_out, int64_t ld_v_out,
                              gbln_q8 fmt, gbln_dtype io, gbln_stream_t stream);
+
+/* ------------------------------------------------------------------------- */
+/* Between the QKV projection and attention: per-head RMSNorm of Q and K, rotary */
+/* embedding with several position axes, attention over the 8-bit cache          */
+/* ([FL] attention with RoPE, heads / head_groups; [LF] fused RMSNorm, fused     */
+/* RoPE; [HF] §Liger: one pass instead of two)                                   */
+/* ------------------------------------------------------------------------- */
+
+/*
+ * Position axes.  A token has n_axes positions (1 to 4; e.g. time, height, width), row a
+ * of positions [n_axes, T] int32 starting at positions + a * ld_positions (ld_positions >=
+ * T), and pair i of a head turns by its own axis' position:
+ *   (c, s) = cos_sin[positions[axis[i]][t], i].
+ * axis: HOST array of D / 2 bytes, each below n_axes, read during the call.  With n_axes
+ * = 1 axis and ld_positions are ignored: the plain rotary embedding.  cos_sin is
+ * gbln_rope_table's, or any table of its layout (axes with frequencies of their own).
+ * A token with any of its positions outside [0, max_pos) gets NaN and sets bit 2 of the
+ * error word.
+ *
+ * The five calls below take even D up to 512, any strides and alignment, and heads of q
+ * and k at t * ld + h * D as gbln_rope_fwd_ex; Hk may be 0 (k ignored).  Aligned rows
+ * (16 bytes, or 8 for bf16 heads such as 72) take the vector path.
+ */
+
+/* Rotation of q and k (gbln_rope_fwd_ex with position axes); in place allowed. */
+gbln_status gbln_rope_axes_fwd(const void* q, const void* k, void* q_out, void* k_out,
+                               const int32_t* positions, int64_t ld_positions, int32_t n_axes,
+                               const uint8_t* axis, const float* cos_sin, int64_t max_pos,
+                               int64_t T, int32_t Hq, int32_t Hk, int32_t D, int64_t ld_q,
+                               int64_t ld_k, int64_t ld_q_out, int64_t ld_k_out,
+                               gbln_rope_pairing pairing, gbln_dtype io, gbln_stream_t stream);
+
+/* Its backward: the inverse rotation of the gradients; in place allowed. */
+gbln_status gbln_rope_axes_bwd(const void* dq, const void* dk, void* dq_in, void* dk_in,
+                               const int32_t* positions, int64_t ld_positions, int32_t n_axes,
+                               const uint8_t* axis, const float* cos_sin, int64_t max_pos,
+                               int64_t T, int32_t Hq, int32_t Hk, int32_t D, int64_t ld_dq,
+                               int64_t ld_dk, int64_t ld_dq_in, int64_t ld_dk_in,
+                               gbln_rope_pairing pairing, gbln_dtype io, gbln_stream_t stream);
+
+/*
+ * RMSNorm of every head of q and of k, then the rotation, in one pass.  For one head x:
+ *   u = (x * rstd) * w,  rstd = 1 / sqrt(mean_D x^2 + eps),  out = rotation of u
+ * rounded once to io.  q_weight, k_weight [D] wt are shared by the heads.  q_out may alias
+ * q and k_out k exactly (a training step keeps them: the backward pass reads q and k).
+ * Errors: UNSUPPORTED for other dtype pairs than gbln_rmsnorm_fwd's; INVALID_ARG as
+ * gbln_rope_fwd_ex, for D > 512, bad axes, eps < 0 or not finite, null weights.
+ */
+gbln_status gbln_qk_norm_rope_fwd(const void* q, const void* k, const void* q_weight,
+                                  const void* k_weight, void* q_out, void* k_out,
+                                  const int32_t* positions, int64_t ld_positions, int32_t n_axes,
+                                  const uint8_t* axis, const float* cos_sin, int64_t max_pos,
+                                  int64_t T, int32_t Hq, int32_t Hk, int32_t D, int64_t ld_q,
+                                  int64_t ld_k, int64_t ld_q_out, int64_t ld_k_out, float eps,
+                                  gbln_rope_pairing pairing, gbln_dtype io, gbln_dtype wt,
+                                  gbln_stream_t stream);
+
+/*
+ * Rows P of the [P, 2 D] float32 dWq|dWk workspace of gbln_qk_norm_rope_bwd: by the sizes
+ * and the device's SM count alone.  0 for T == 0, -1 on invalid arguments.
+ */
+int64_t gbln_qk_norm_rope_bwd_num_partials(int64_t T, int32_t Hq, int32_t Hk, int32_t D);
+
+/*
+ * Backward of gbln_qk_norm_rope_fwd, first of two passes.  q and k are the forward's
+ * inputs (rstd is recomputed from them), dq and dk the gradients of its outputs.  With d =
+ * dq turned back, g = d * w, n = x * rstd, per head:
+ *   dq_in = rstd * (g - n * mean_D(g * n))
+ *   partial[p, 0:D] = sum over the heads of q of block p of d * n, [D:2D] the same of k
+ * dq_in may alias dq or q exactly, dk_in dk or k.  dw_partial [P_cap, 2 D] float32, rows
+ * 0..P-1 written; WORKSPACE if P_cap < P.  Bitwise reproducible for fixed sizes, alignment
+ * and GPU model.  Errors as the forward.
+ */
+gbln_status gbln_qk_norm_rope_bwd(const void* dq, const void* dk, const void* q, const void* k,
+                                  const void* q_weight, const void* k_weight, void* dq_in,
+                                  void* dk_in, float* dw_partial, int64_t P_cap,
+                                  const int32_t* positions, int64_t ld_positions, int32_t n_axes,
+                                  const uint8_t* axis, const float* cos_sin, int64_t max_pos,
+                                  int64_t T, int32_t Hq, int32_t Hk, int32_t D, int64_t ld_dq,
+                                  int64_t ld_dk, int64_t ld_q, int64_t ld_k, int64_t ld_dq_in,
+                                  int64_t ld_dk_in, float eps, gbln_rope_pairing pairing,
+                                  gbln_dtype io, gbln_dtype wt, gbln_stream_t stream);
+
+/* Second pass: dwq[j] (+)= sum_p partial[p, j], dwk[j] (+)= sum_p partial[p, D + j], fixed order; [D] float32. */
+gbln_status gbln_qk_norm_dw_finalize(const float* dw_partial, int64_t P, int32_t D, float* dwq,
+                                     float* dwk, int accumulate, gbln_stream_t stream);
+
+/*
+ * gbln_rope_fwd_cache8 with the norms and position axes: q is normalised, rotated and
+ * written, k normalised, rotated and quantised with v into their caches at the tokens'
+ * slots.  rstd cancels out of k's codes, which are those of t = rotation of x * w (float32,
+ * roundings written out), and goes into the scale: a = max(max |t|, 2^-100),
+ * scale = (a * rstd) / qmax.  q_weight and k_weight both NULL: no norms (then with one
+ * axis the same bits as gbln_rope_fwd_cache8).  Hq may be 0 (q, q_weight, q_out ignored);
+ * Hk >= 1.  Slots, positions, aliasing and errors as there, D up to 512.
+ */
+gbln_status gbln_qk_norm_rope_fwd_cache8(const void* q, const void* k, const void* v,
+                                         const void* q_weight, const void* k_weight, void* q_out,
+                                         const int32_t* positions, int64_t ld_positions,
+                                         int32_t n_axes, const uint8_t* axis, const float* cos_sin,
+                                         int64_t max_pos, const int64_t* slots,
+                                         const gbln_cache8* k_cache, const gbln_cache8* v_cache,
+                                         int64_t T, int32_t Hq, int32_t Hk, int32_t D,
+                                         int64_t ld_q, int64_t ld_k, int64_t ld_v,
+                                         int64_t ld_q_out, float eps, gbln_rope_pairing pairing,
+                                         gbln_q8 fmt, gbln_dtype io, gbln_dtype wt,
+                                         gbln_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -29,6 +29,8 @@ __all__ = [
     "ERR_BAD_POSITION", "PAIRING", "F32", "BF16", "rmsnorm_fwd_fp8", "glu_fwd_fp8",
     "rmsnorm_fwd_ckpt8", "rmsnorm_bwd_ckpt8", "rmsnorm_bwd_ckpt8_num_partials", "glu_fwd_ckpt8",
     "glu_bwd_ckpt8", "rope_fwd_cache8", "cache8_read", "ERR_BAD_SLOT", "Q8", "CKPT_GROUP",
+    "rope_axes", "rope_axes_fwd", "rope_axes_bwd", "qk_norm_rope_fwd", "qk_norm_rope_bwd",
+    "qk_norm_rope_bwd_num_partials", "qk_norm_dw_finalize", "qk_norm_rope_fwd_cache8",
 ]
 
 F32 = 0
@@ -97,6 +99,13 @@ _SIGNATURES = {
     "gbln_glu_fwd_ckpt8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp]),
     "gbln_glu_bwd_ckpt8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp]),
     "gbln_rope_fwd_cache8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i64, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp]),
+    "gbln_rope_axes_fwd": (ctypes.c_int, [_vp] * 5 + [_i64, _i32, _vp, _vp, _i64, _i64, _i32, _i32, _i32, _i64, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, _vp]),
+    "gbln_rope_axes_bwd": (ctypes.c_int, [_vp] * 5 + [_i64, _i32, _vp, _vp, _i64, _i64, _i32, _i32, _i32, _i64, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, _vp]),
+    "gbln_qk_norm_rope_fwd": (ctypes.c_int, [_vp] * 7 + [_i64, _i32, _vp, _vp, _i64, _i64, _i32, _i32, _i32, _i64, _i64, _i64, _i64, _f32, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp]),
+    "gbln_qk_norm_rope_bwd_num_partials": (_i64, [_i64, _i32, _i32, _i32]),
+    "gbln_qk_norm_rope_bwd": (ctypes.c_int, [_vp] * 9 + [_i64, _vp, _i64, _i32, _vp, _vp, _i64, _i64, _i32, _i32, _i32, _i64, _i64, _i64, _i64, _i64, _i64, _f32, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp]),
+    "gbln_qk_norm_dw_finalize": (ctypes.c_int, [_vp, _i64, _i32, _vp, _vp, ctypes.c_int, _vp]),
+    "gbln_qk_norm_rope_fwd_cache8": (ctypes.c_int, [_vp] * 7 + [_i64, _i32, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i64, _i64, _i64, _i64, _f32, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp]),
     "gbln_cache8_read": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i64, _i64, ctypes.c_int, ctypes.c_int, _vp]),
 }
 
@@ -991,3 +1000,219 @@ def cache8_read(slots, k_cache, k_scale, v_cache, v_scale, *, dtype=torch.bfloat
                                     ldk, ldv, fmt, _io(k_out), _raw_stream(dev))
     _check("gbln_cache8_read", st)
     return k_out, v_out
+
+
+# ---------------------------------------------------------------------------
+# Between the QKV projection and attention
+# ---------------------------------------------------------------------------
+
+def rope_axes(sections, order="blocks") -> bytes:
+    """The position axis of each pair of a head, for the ``axes`` of the functions below:
+    ``sections[a]`` pairs turn by axis a's positions, ``D / 2`` in all.  ``order`` "blocks" gives each
+    axis consecutive pairs; "cyclic" gives the axes pairs in turns, as long as each has some left."""
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= 4 or min(left) < 0:
+        raise ValueError(f"sections must be one to four counts of pairs, not {tuple(sections)}")
+    if order == "blocks":
+        return b"".join(bytes([a]) * n for a, n in enumerate(left))
+    if order != "cyclic":
+        raise ValueError(f"order must be 'blocks' or 'cyclic', not {order!r}")
+    out = bytearray()
+    while any(left):
+        for a, n in enumerate(left):
+            if n:
+                left[a] -= 1
+                out.append(a)
+    return bytes(out)
+
+
+def _axes(positions, axes, T, D, dev):
+    """(positions, ld_positions, n_axes, axis) of a call."""
+    if positions.dtype is not torch.int32:
+        raise TypeError(f"positions must be torch.int32, not {positions.dtype}")
+    if axes is None:
+        if positions.numel() != T:
+            raise ValueError(f"positions must hold {T} elements, not {positions.numel()}")
+        return _ptr(positions, dev, "positions"), 0, 1, None
+    n = positions.shape[0] if positions.dim() == 2 else 0
+    if not 1 <= n <= 4 or positions.shape[1] != T:
+        raise ValueError(f"positions must be [axes, {T}] with one to four axes, not {tuple(positions.shape)}")
+    if len(axes) != D // 2 or max(axes, default=0) >= n:
+        raise ValueError(f"axes must name one of the {n} axes for each of the {D // 2} pairs")
+    if positions.get_device() != dev:
+        raise ValueError(f"positions is on {positions.device}, not on cuda:{dev}")
+    if positions.stride(1) != 1 and T > 1 or positions.stride(0) < T and n > 1:
+        raise ValueError("each axis' positions must lie next to one another")
+    return positions.data_ptr(), positions.stride(0), n, bytes(axes)
+
+
+def _like_heads(o, ref, name):
+    """o, or a new contiguous tensor of ref's shape, and its token stride."""
+    if ref is None:
+        if o is not None:
+            raise ValueError(f"{name} without its input")
+        return None, 0, None
+    if o is None:
+        o = torch.empty(ref.shape, dtype=ref.dtype, device=ref.device)
+        return o, ref.shape[1] * ref.shape[2], o.data_ptr()
+    if o.shape != ref.shape or o.dtype is not ref.dtype:
+        raise ValueError(f"{name} must have the shape {tuple(ref.shape)} and dtype {ref.dtype}")
+    return o, _heads(o, name)[3], o.data_ptr()
+
+
+def _pair_of_heads(q, k, qn="q", kn="k"):
+    T, Hq, D, ldq = _heads(q, qn)
+    Tk, Hk, Dk, ldk = _heads(k, kn)
+    if k is not None and (Tk != T or Dk != D or k.dtype is not q.dtype):
+        raise ValueError(f"{kn} must be [T, Hk, D] with {qn}'s T, D and dtype")
+    return T, Hq, Hk, D, ldq, ldk, q.data_ptr(), None if k is None else k.data_ptr()
+
+
+def _rope_axes(name, q, k, positions, cos_sin, axes, q_out, k_out, pairing, names):
+    T, Hq, Hk, D, ldq, ldk, qp, kp = _pair_of_heads(q, k, *names[:2])
+    _table(cos_sin, D)
+    dev = q.get_device()
+    pos, ldp, n, axis = _axes(positions, axes, T, D, dev)
+    q_out, ldqo, qop = _like_heads(q_out, q, names[2])
+    k_out, ldko, kop = _like_heads(k_out, k, names[3])
+    st = getattr(library(), name)(qp, kp, qop, kop, pos, ldp, n, axis, _ptr(cos_sin, dev, "cos_sin"), cos_sin.shape[0], T, Hq,
+                                  Hk, D, ldq, ldk, ldqo, ldko, PAIRING[pairing], _io(q), _raw_stream(dev))
+    _check(name, st)
+    return q_out, k_out
+
+
+def rope_axes_fwd(q, k, positions, cos_sin, axes, *, q_out=None, k_out=None, pairing="half"):
+    """``gbln_rope_axes_fwd``: :func:`rope_fwd_ex` with several position axes.  positions: int32
+    [axes, T] (e.g. time, height, width), 1 to 4 rows; ``axes``: the axis of each of a head's D / 2
+    pairs, from :func:`rope_axes` or any sequence of small integers.  k may be None.  Pass ``q_out=q,
+    k_out=k`` to rotate in place.  Returns ``(q_out, k_out)``."""
+    return _rope_axes("gbln_rope_axes_fwd", q, k, positions, cos_sin, axes, q_out, k_out, pairing, ("q", "k", "q_out", "k_out"))
+
+
+def rope_axes_bwd(dq, dk, positions, cos_sin, axes, *, dq_in=None, dk_in=None, pairing="half"):
+    """``gbln_rope_axes_bwd``: inverse rotation of :func:`rope_axes_fwd`.  Returns ``(dq_in, dk_in)``."""
+    return _rope_axes("gbln_rope_axes_bwd", dq, dk, positions, cos_sin, axes, dq_in, dk_in, pairing, ("dq", "dk", "dq_in", "dk_in"))
+
+
+def _qk_weights(q_weight, k_weight, D, dev, need_k):
+    _vec(q_weight, D, "q_weight")
+    _vec(k_weight, D, "k_weight")
+    if k_weight is None:
+        if need_k:
+            raise ValueError("k_weight is missing")
+    elif k_weight.dtype is not q_weight.dtype:
+        raise TypeError("k_weight must have q_weight's dtype")
+    return _ptr(q_weight, dev, "q_weight"), None if k_weight is None else _ptr(k_weight, dev, "k_weight"), _io(q_weight)
+
+
+def qk_norm_rope_fwd(q, k, q_weight, k_weight, positions, cos_sin, eps, *, axes=None, q_out=None, k_out=None, pairing="half"):
+    """``gbln_qk_norm_rope_fwd``: RMSNorm of every head of q [T, Hq, D] and k [T, Hk, D] (weights [D],
+    shared by the heads), then the rotation, in one pass.  positions: int32 [T], or [axes, T] with
+    ``axes`` as :func:`rope_axes_fwd`.  q and k may have strided token rows (slices of one packed QKV
+    tensor); k may be None (then k_weight too).  Returns ``(q_out, k_out)``; the backward pass,
+    :func:`qk_norm_rope_bwd`, needs q and k."""
+    T, Hq, Hk, D, ldq, ldk, qp, kp = _pair_of_heads(q, k)
+    _table(cos_sin, D)
+    dev = q.get_device()
+    wq, wk, wt = _qk_weights(q_weight, k_weight, D, dev, k is not None)
+    pos, ldp, n, axis = _axes(positions, axes, T, D, dev)
+    q_out, ldqo, qop = _like_heads(q_out, q, "q_out")
+    k_out, ldko, kop = _like_heads(k_out, k, "k_out")
+    st = library().gbln_qk_norm_rope_fwd(qp, kp, wq, wk, qop, kop, pos, ldp, n, axis, _ptr(cos_sin, dev, "cos_sin"),
+                                         cos_sin.shape[0], T, Hq, Hk, D, ldq, ldk, ldqo, ldko, eps, PAIRING[pairing], _io(q),
+                                         wt, _raw_stream(dev))
+    _check("gbln_qk_norm_rope_fwd", st)
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd_num_partials(T: int, Hq: int, Hk: int, D: int) -> int:
+    """``gbln_qk_norm_rope_bwd_num_partials``: rows P of the [P, 2 D] float32 dWq|dWk workspace."""
+    P = library().gbln_qk_norm_rope_bwd_num_partials(T, Hq, Hk, D)
+    if P < 0:
+        raise GblnError("gbln_qk_norm_rope_bwd_num_partials", 1)
+    return P
+
+
+def qk_norm_rope_bwd(dq, dk, q, k, q_weight, k_weight, positions, cos_sin, eps, *, axes=None, dq_in=None, dk_in=None,
+                     dw_partial=None, pairing="half"):
+    """``gbln_qk_norm_rope_bwd``: gradients of q and k from those of :func:`qk_norm_rope_fwd`'s outputs
+    (q, k: its inputs).  All of them may have strided token rows; dq_in and dk_in may be slices of one
+    packed gradient.  Returns ``(dq_in, dk_in, dw_partial, P)``; finish the weights' gradients with
+    :func:`qk_norm_dw_finalize`."""
+    T, Hq, Hk, D, ldq, ldk, qp, kp = _pair_of_heads(q, k)
+    _, Gq, Gk, _, lddq, lddk, dqp, dkp = _pair_of_heads(dq, dk, "dq", "dk")
+    if dq.shape != q.shape or Gk != Hk or dq.dtype is not q.dtype:
+        raise ValueError("dq and dk must have the shapes and dtype of q and k")
+    _table(cos_sin, D)
+    dev = q.get_device()
+    wq, wk, wt = _qk_weights(q_weight, k_weight, D, dev, k is not None)
+    pos, ldp, n, axis = _axes(positions, axes, T, D, dev)
+    _rows_f32(dw_partial, 2 * D, "dw_partial")
+    P = qk_norm_rope_bwd_num_partials(T, Hq, Hk, D)
+    dq_in, ldqo, qop = _like_heads(dq_in, q, "dq_in")
+    dk_in, ldko, kop = _like_heads(dk_in, k, "dk_in")
+    if dw_partial is None:
+        dw_partial = torch.empty((P or 1, 2 * D), dtype=torch.float32, device=q.device)
+    st = library().gbln_qk_norm_rope_bwd(dqp, dkp, qp, kp, wq, wk, qop, kop, _ptr(dw_partial, dev, "dw_partial"),
+                                         dw_partial.shape[0], pos, ldp, n, axis, _ptr(cos_sin, dev, "cos_sin"),
+                                         cos_sin.shape[0], T, Hq, Hk, D, lddq, lddk, ldq, ldk, ldqo, ldko, eps,
+                                         PAIRING[pairing], _io(q), wt, _raw_stream(dev))
+    _check("gbln_qk_norm_rope_bwd", st)
+    return dq_in, dk_in, dw_partial, P
+
+
+def qk_norm_dw_finalize(dw_partial, P, dwq=None, dwk=None, accumulate=False):
+    """``gbln_qk_norm_dw_finalize``: float32 (dWq [D], dWk [D]) of the first P partial rows, summed in a
+    fixed order."""
+    D = dw_partial.shape[-1] // 2
+    _rows_f32(dw_partial, 2 * D, "dw_partial", P)
+    _vec(dwq, D, "dwq", torch.float32)
+    _vec(dwk, D, "dwk", torch.float32)
+    if accumulate and (dwq is None or dwk is None):
+        raise ValueError("accumulate needs dwq and dwk")
+    dev = _here(dw_partial, "dw_partial")
+    dwq = torch.empty(D, dtype=torch.float32, device=dw_partial.device) if dwq is None else dwq
+    dwk = torch.empty(D, dtype=torch.float32, device=dw_partial.device) if dwk is None else dwk
+    st = library().gbln_qk_norm_dw_finalize(_ptr(dw_partial, dev, "dw_partial"), P, D, _ptr(dwq, dev, "dwq"),
+                                            _ptr(dwk, dev, "dwk"), 1 if accumulate else 0, _raw_stream(dev))
+    _check("gbln_qk_norm_dw_finalize", st)
+    return dwq, dwk
+
+
+def qk_norm_rope_fwd_cache8(q, k, v, q_weight, k_weight, positions, cos_sin, eps, slots, k_cache, k_scale, v_cache, v_scale,
+                            *, axes=None, q_out=None, pairing="half"):
+    """``gbln_qk_norm_rope_fwd_cache8``: :func:`rope_fwd_cache8` with the per-head norms and position axes
+    of :func:`qk_norm_rope_fwd`: q is normalised and rotated, k normalised, rotated and quantised with v
+    into the paged caches at ``slots``.  q may be None (then q_weight too); both weights None: no norms.
+    Returns ``q_out`` (pass ``q_out=q`` to work in place)."""
+    T, Hk, D, ldk = _heads(k, "k")
+    Tv, Hv, Dv, ldv = _heads(v, "v")
+    if (Tv, Hv, Dv) != (T, Hk, D) or v.dtype is not k.dtype:
+        raise ValueError("v must have k's shape and dtype")
+    Hq = ldq = 0
+    qp = None
+    if q is not None:
+        Tq, Hq, Dq, ldq = _heads(q, "q")
+        if Tq != T or Dq != D or q.dtype is not k.dtype:
+            raise ValueError("q must be [T, Hq, D] with k's T, D and dtype")
+        qp = q.data_ptr()
+    _table(cos_sin, D)
+    dev = k.get_device()  # _heads has seen that it is the current one
+    wq = wk = None
+    wt = _io(k)
+    if k_weight is not None:
+        if q is not None and q_weight is None:
+            raise ValueError("q_weight is missing")
+        wq, wk, wt = _qk_weights(k_weight if q_weight is None else q_weight, k_weight, D, dev, True)
+    elif q_weight is not None:
+        raise ValueError("k_weight is missing")
+    pos, ldp, n, axis = _axes(positions, axes, T, D, dev)
+    _vec(slots, T, "slots", torch.int64)
+    kc, vc, fmt = _caches8(k_cache, k_scale, v_cache, v_scale, Hk, D)
+    q_out, ldqo, qop = _like_heads(q_out, q, "q_out")
+    st = library().gbln_qk_norm_rope_fwd_cache8(
+        qp, k.data_ptr(), v.data_ptr(), wq, wk, qop, pos, ldp, n, axis, _ptr(cos_sin, dev, "cos_sin"), cos_sin.shape[0],
+        _ptr(slots, dev, "slots"), kc, vc, T, Hq, Hk, D, ldq, ldk, ldv, ldqo, eps, PAIRING[pairing], fmt, _io(k), wt,
+        _raw_stream(dev))
+    _check("gbln_qk_norm_rope_fwd_cache8", st)
+    return q_out
