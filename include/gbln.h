@@ -7,7 +7,8 @@
  * other gated and plain activations, MXFP8 and row-scaled FP8 outputs for the
  * next GEMM, 8-bit activation checkpoints with the backward passes that read
  * them, and a quantised K/V cache; per-head norms of Q and K with the rotation in
- * one pass and rotary embedding with several position axes.
+ * one pass, rotary embedding with several position axes, and attention over the
+ * quantised cache.
  *
  * Sources that name these operators (they print no formulas; the standard
  * definitions are used and written out at each entry point):
@@ -716,6 +717,40 @@ gbln_status gbln_qk_norm_rope_fwd_cache8(const void* q, const void* k, const voi
                                          int64_t ld_q_out, float eps, gbln_rope_pairing pairing,
                                          gbln_q8 fmt, gbln_dtype io, gbln_dtype wt,
                                          gbln_stream_t stream);
+
+/*
+ * Attention of the new tokens of a ragged batch over the paged cache (decode steps, drafts,
+ * chunks of a prompt, whole prompts).  Sequence b has the rows cu_seqlens_q[b] ..
+ * cu_seqlens_q[b + 1] - 1 of q, its last new tokens, whose keys and values are in the cache
+ * already; kv_lens[b] tokens are cached in all, token j in slot j % page_size of page
+ * page_table[b, j / page_size].  A row at position p (the last one at kv_lens[b] - 1) sees
+ * the keys j <= p if causal, all if not, and of those with window > 0 only j > p - window:
+ *   out = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q . k_j),  lse = log sum_j w_j
+ * (k_j, v_j = code * scale).  Head h of q goes with K/V head h / (Hq / Hk).  A row that sees no
+ * key gives zeros and lse -infinity.  Scores, weights, their sums and results are float32;
+ * with bf16 rows and D 64, 96, 128 or 256 the weights times v's scales are rounded to bf16.
+ * Keys that a row does not see have no part in it, whatever the cache holds there; pages that
+ * no row of the sequence sees are not read (freed pages may hold any number in the table).
+ * cu_seqlens_q [B + 1], non-decreasing from 0, kv_lens [B], page_table [B, max_pages] int32,
+ * read on the device (a captured call follows them); values beyond T or max_pages * page_size
+ * are cut to it.  Rows behind cu_seqlens_q[B] are left as they are.  A page that is read and
+ * lies outside the cache makes the rows that see it NaN and sets bit 4 of the error word.
+ * q, out [T, Hq, D] io at t * ld + h * D; out may alias q exactly.  lse [T, Hq] float32 or NULL.
+ * workspace: gbln_attn_cache8_workspace bytes (by the sizes and the device's SM count; 0: none
+ * needed), 16-byte aligned, contents of no account; calls that may overlap need one each.
+ * Bitwise reproducible for fixed sizes, lengths, alignment and GPU model.
+ * Errors: INVALID_ARG for Hq not a multiple of Hk, D > 512, T * Hq or max_pages * page_size
+ * above 2^30, a scale that is not finite, window < 0 and as gbln_cache8_read; WORKSPACE.
+ */
+int64_t gbln_attn_cache8_workspace(int64_t T, int32_t B, int32_t Hq, int32_t Hk, int32_t D,
+                                   gbln_dtype io);
+gbln_status gbln_attn_cache8(const void* q, const int32_t* cu_seqlens_q, const int32_t* kv_lens,
+                             const int32_t* page_table, int64_t max_pages,
+                             const gbln_cache8* k_cache, const gbln_cache8* v_cache, void* out,
+                             float* lse, void* workspace, int64_t workspace_bytes, int64_t T,
+                             int32_t B, int32_t Hq, int32_t Hk, int32_t D, int64_t ld_q,
+                             int64_t ld_out, float scale, int32_t causal, int32_t window,
+                             gbln_q8 fmt, gbln_dtype io, gbln_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -31,6 +31,7 @@ __all__ = [
     "glu_bwd_ckpt8", "rope_fwd_cache8", "cache8_read", "ERR_BAD_SLOT", "Q8", "CKPT_GROUP",
     "rope_axes", "rope_axes_fwd", "rope_axes_bwd", "qk_norm_rope_fwd", "qk_norm_rope_bwd",
     "qk_norm_rope_bwd_num_partials", "qk_norm_dw_finalize", "qk_norm_rope_fwd_cache8",
+    "attn_cache8", "attn_cache8_workspace",
 ]
 
 F32 = 0
@@ -106,6 +107,8 @@ _SIGNATURES = {
     "gbln_qk_norm_rope_bwd": (ctypes.c_int, [_vp] * 9 + [_i64, _vp, _i64, _i32, _vp, _vp, _i64, _i64, _i32, _i32, _i32, _i64, _i64, _i64, _i64, _i64, _i64, _f32, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp]),
     "gbln_qk_norm_dw_finalize": (ctypes.c_int, [_vp, _i64, _i32, _vp, _vp, ctypes.c_int, _vp]),
     "gbln_qk_norm_rope_fwd_cache8": (ctypes.c_int, [_vp] * 7 + [_i64, _i32, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i64, _i64, _i64, _i64, _f32, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp]),
+    "gbln_attn_cache8_workspace": (_i64, [_i64, _i32, _i32, _i32, _i32, ctypes.c_int]),
+    "gbln_attn_cache8": (ctypes.c_int, [_vp] * 4 + [_i64] + [_vp] * 5 + [_i64, _i64, _i32, _i32, _i32, _i32, _i64, _i64, _f32, _i32, _i32, ctypes.c_int, ctypes.c_int, _vp]),
     "gbln_cache8_read": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i64, _i64, ctypes.c_int, ctypes.c_int, _vp]),
 }
 
@@ -1216,3 +1219,53 @@ def qk_norm_rope_fwd_cache8(q, k, v, q_weight, k_weight, positions, cos_sin, eps
         _raw_stream(dev))
     _check("gbln_qk_norm_rope_fwd_cache8", st)
     return q_out
+
+
+def attn_cache8_workspace(T: int, B: int, Hq: int, Hk: int, D: int, dtype=torch.bfloat16) -> int:
+    """``gbln_attn_cache8_workspace``: bytes of workspace of :func:`attn_cache8` on the current device."""
+    n = library().gbln_attn_cache8_workspace(T, B, Hq, Hk, D, _DTYPE[dtype])
+    if n < 0:
+        raise GblnError("gbln_attn_cache8_workspace", 1)
+    return n
+
+
+def attn_cache8(q, cu_seqlens_q, kv_lens, page_table, k_cache, k_scale, v_cache, v_scale, *, scale=None, causal=True, window=0,
+                out=None, lse=None, workspace=None):
+    """``gbln_attn_cache8``: attention of new tokens over the paged 8-bit cache.  q [T, Hq, D] holds the
+    new tokens of all sequences, those of sequence b at rows ``cu_seqlens_q[b]`` to ``cu_seqlens_q[b + 1]``
+    (int32 [B + 1]); ``kv_lens`` (int32 [B]) tokens of it are cached, the new ones (stored before by
+    :func:`rope_fwd_cache8` or :func:`qk_norm_rope_fwd_cache8`) the last of them; token j lies in slot
+    ``j % page_size`` of page ``page_table[b, j // page_size]`` (int32 [B, max_pages]).  The caches are those of
+    :func:`cache8_read`.  ``scale`` is ``D ** -0.5`` by default; ``causal``: a token sees its own and earlier
+    positions; ``window`` > 0: only the last ``window`` of them.  Hq is a multiple of Hk.  Rows behind
+    ``cu_seqlens_q[B]`` are left as they are in ``out``; ``out=q`` works in place.  ``lse`` (float32 [T, Hq]) receives
+    the logarithms of the weights' sums.  ``workspace``: uint8, :func:`attn_cache8_workspace` bytes (allocated
+    where it is not given).  Returns ``out``."""
+    T, Hq, D, ldq = _heads(q, "q")
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [pages, page_size, Hk, D]")
+    Hk = k_cache.shape[2]
+    B = kv_lens.numel()
+    dev = q.get_device()  # _heads has seen that it is the current one
+    _vec(cu_seqlens_q, B + 1, "cu_seqlens_q", torch.int32)
+    _vec(kv_lens, B, "kv_lens", torch.int32)
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table must be int32 [{B}, max_pages], not {page_table.dtype} {tuple(page_table.shape)}")
+    kc, vc, fmt = _caches8(k_cache, k_scale, v_cache, v_scale, Hk, D)
+    out, ldo, op = _like_heads(out, q, "out")
+    lp = None
+    if lse is not None:
+        _vec(lse, T * Hq, "lse", torch.float32)
+        lp = _ptr(lse, dev, "lse")
+    io = _io(q)
+    if workspace is None:
+        n = library().gbln_attn_cache8_workspace(T, B, Hq, Hk, D, io)
+        workspace = torch.empty(max(n, 0), dtype=torch.uint8, device=q.device)
+    elif workspace.dtype is not torch.uint8:
+        raise TypeError(f"workspace must be torch.uint8, not {workspace.dtype}")
+    st = library().gbln_attn_cache8(
+        q.data_ptr(), _ptr(cu_seqlens_q, dev, "cu_seqlens_q"), _ptr(kv_lens, dev, "kv_lens"), _ptr(page_table, dev, "page_table"),
+        page_table.shape[1], kc, vc, op, lp, _ptr(workspace, dev, "workspace"), workspace.numel(), T, B, Hq, Hk, D, ldq, ldo,
+        D ** -0.5 if scale is None else scale, 1 if causal else 0, window, fmt, io, _raw_stream(dev))
+    _check("gbln_attn_cache8", st)
+    return out

@@ -1,0 +1,682 @@
+// Attention of the new tokens of a ragged batch over the paged 8-bit K/V cache.
+//
+// Operator: "Fast-LLM: 高效大语言模型训练框架", §三 框架结构 (attention with RoPE; heads /
+// head_groups for grouped-query attention).  With codes k, v and scales a, b of key j:
+//   s_j = scale a_j (q . k_j),   o = sum_j p_j b_j v_j / sum_j p_j,   p_j = 2^(s_j log2 e - m).
+// INT8 and E4M3 codes are exact in bf16, so the products see the codes themselves: a_j goes
+// onto the score, b_j onto the weight p_j, which is rounded to bf16 for its product (2^-9 of
+// each weight, where the result is rounded to bf16 anyway); scores, weights' sums and results
+// are float32.  A row that sees a key of scale NaN is NaN; a key that it does not see has no
+// part in it.
+//
+// Few rows per sequence (decode, drafts): bound by the cache's bytes, D + 4 per K or V head
+// of a token.  A warp takes 16 rows (new tokens x heads of a group) of one K/V head and
+// streams its keys, 16 at a time, through a ring in shared memory of its own, without any
+// barrier between warps.  Codes go straight from there into the fragments of the 16 x 8 x 16
+// products: the order of D within a product is free as long as Q has the same, so that a
+// lane's codes are the bytes it finds next to one another.
+
+#include <atomic>
+
+#include "attn8.cuh"
+
+namespace gbln {
+
+namespace {
+
+constexpr int kFewWarps = 8;
+constexpr int kStep = 16;  // keys of a warp's step
+
+template <int D>
+struct FewShape {
+  static constexpr int STAGE = 2 * kStep * D + 2 * kStep * 4;  // K, V, their scales
+  static constexpr int NS = D <= 64 ? 8 : D <= 96 ? 7 : D <= 128 ? 6 : 3;
+  static constexpr int WARP = NS * STAGE;  // holds a warp's results (16 x (D + 2) floats) at a unit's end
+  static constexpr int SMEM = kFewWarps * WARP;
+  static_assert(WARP >= kFewRows * (D + 2) * 4, "results fit the ring");
+  // Where chunk ch (16 bytes) of row r lies: the lanes that read at once hit different banks.
+  static __device__ __forceinline__ int k_at(int r, int ch) {
+    if constexpr (D == 64) return r * D + 16 * (ch ^ ((r >> 1 & 1) << 1));
+    else if constexpr (D % 128 == 0) return r * D + 16 * (ch ^ ((r & 3) << 1));
+    else return r * D + 16 * ch;
+  }
+  static __device__ __forceinline__ int v_at(int r, int ch) {
+    if constexpr (D == 64) return r * D + 16 * (ch ^ ((r >> 1 & 1) << 1));
+    else if constexpr (D % 128 == 0) return r * D + 16 * (ch ^ ((r >> 1 & 3) << 1));
+    else return r * D + 16 * ch;
+  }
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ float2 lds_f2(uint32_t a) {
+  float2 r;
+  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(a));
+  return r;
+}
+
+// Bytes ea of a and eb of b as two bf16 values.  INT8: 0x4300 | (x & 0x7f) is 128 + the low
+// seven bits, 0x4300 | (x & 0x80) is 128 or 256: their difference is the code.  E4M3: its
+// exponent and fraction in bf16's places are the value times 2^-120 (a NaN code becomes 480:
+// it comes with the scale NaN).
+template <int FMT>
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t a, uint32_t b, int ea, int eb) {
+  if constexpr (FMT == GBLN_Q8_INT8) {
+    const uint32_t w = __byte_perm(a, b, 0x4440 + ea + 0x100 * eb);  // high bytes: any, cut below
+    const uint32_t u = (w & 0x007f007fu) | 0x43004300u, s = (w & 0x00800080u) | 0x43004300u;
+    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), *reinterpret_cast<const __nv_bfloat162*>(&s));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    const uint32_t w = __byte_perm(a, b, 0x4000 + 0x10 * ea + 0x1000 * eb);  // low bytes: any, cut below
+    const uint32_t u = (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u), s = 0x7b807b80u;  // 2^120
+    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u), *reinterpret_cast<const __nv_bfloat162*>(&s));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The keys that a warp's step brings in: page and slot of key (lane & 15).
+struct KeyAt {
+  int page;  // -1: none, -2: a page outside the cache
+  uint32_t off;
+};
+__device__ __forceinline__ KeyAt key_at(const AttnArgs& A, int b, int j, int hi) {
+  KeyAt k{-1, 0};
+  if (j < hi) {
+    uint32_t p;
+    A.page.split((uint32_t)j, p, k.off);
+    k.page = __ldg(A.pages + (int64_t)b * A.max_pages + p);
+    if (k.page < 0 || k.page >= A.n_pages) k.page = -2;
+  }
+  return k;
+}
+
+template <int D>
+__device__ __forceinline__ void few_load(const AttnArgs& A, uint32_t stage, const KeyAt& k, int h) {
+  using Sh = FewShape<D>;
+  const int lane = threadIdx.x & 31;
+  constexpr int CH = D / 16;               // chunks of a row
+  constexpr int N = (kStep * CH + 31) / 32;  // of K (and of V) per lane
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int x = i * 32 + lane, r = x / CH, ch = x - r * CH;
+    const int page = __shfl_sync(0xffffffffu, k.page, r & 15);
+    const uint32_t off = __shfl_sync(0xffffffffu, k.off, r & 15);
+    if (r < kStep) {
+      const bool on = page >= 0;
+      const int64_t p = on ? page : 0, o = on ? off : 0;
+      cp16(stage + Sh::k_at(r, ch), A.K.q + A.K.cq.at(p, o, h) + 16 * ch, on);
+      cp16(stage + kStep * D + Sh::v_at(r, ch), A.V.q + A.V.cq.at(p, o, h) + 16 * ch, on);
+    }
+  }
+  // lanes 0..15 K's scales, 16..31 V's
+  const bool on = k.page >= 0;
+  const int64_t p = on ? k.page : 0, o = on ? k.off : 0;
+  const uint32_t at = stage + 2 * kStep * D + 4 * lane;
+  const float* src = lane < 16 ? A.K.sc + A.K.cs.at(p, o, h) : A.V.sc + A.V.cs.at(p, o, h);
+  if (k.page == -2) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(0x7fc00000) : "memory");
+  else cp4(at, src, on);
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(32 * kFewWarps, 1) attn8_few(const __grid_constant__ AttnArgs A, bool q16) {
+  using Sh = FewShape<D>;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ Part plan;
+  launch_dependents();
+  const int lane = threadIdx.x & 31, warp = warp_index();
+  const int g = lane >> 2, c = lane & 3;
+  // warp -> K/V head of the block's group and slice of the keys
+  const int S = kFewWarps / A.HB;
+  const int wh = warp % A.HB, slice = warp / A.HB;
+  const bool works = slice < S;
+  if (warp == 0) {
+    Part p;
+    // a unit's tile is a step of each slice
+    p.total = 0;
+    switch (S) {
+      case 8: plan_part<kFewRows, 8 * kStep>(A, p); break;
+      case 4: plan_part<kFewRows, 4 * kStep>(A, p); break;
+      case 2: plan_part<kFewRows, 2 * kStep>(A, p); break;
+      default: plan_part<kFewRows, kStep>(A, p);
+    }
+    if (lane == 0) plan = p;
+  }
+  __syncthreads();
+  Unit u = plan.u;
+  int tile = plan.tile;
+  int64_t x = plan.x0;
+  const int64_t x1 = plan.x1;
+  if (threadIdx.x == 0) A.info[blockIdx.x * kAttnInfo] = -1;
+  if (x >= x1) return;
+  const uint32_t mine = smem_addr(ring) + warp * Sh::WARP;
+  float* res = reinterpret_cast<float*>(ring) + warp * (Sh::WARP / 4);
+
+  for (;;) {
+    const int t1 = (int)min((int64_t)u.tiles, tile + (x1 - x));  // this block's tiles of the unit: tile .. t1 - 1
+    const int h = u.hg * A.HB + wh;
+    const bool on = works && h < A.Hk;
+    const int nrows = u.r1 - u.r0;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+    if (on) {
+      const int first = u.s.kv - u.s.nq;  // position of the sequence's first new token
+      const auto base = [&](int t) { return u.lo + (t * S + slice) * kStep; };
+      // fill the ring
+      KeyAt next = key_at(A, u.b, base(tile) + (lane & 15), u.hi);
+#pragma unroll
+      for (int i = 0; i < Sh::NS - 1; ++i) {
+        if (tile + i < t1) {
+          const KeyAt k = next;
+          next = key_at(A, u.b, base(tile + i + 1) + (lane & 15), tile + i + 1 < t1 ? u.hi : 0);
+          if (k.page == -2) atomicOr(A.err, kErrBadSlot);
+          few_load<D>(A, mine + i * Sh::STAGE, k, h);
+        }
+        cp_commit();
+      }
+      // Q: rows g and g + 8, values 32 i + 8 c ..
+      uint32_t qa[D / 32][2][4];
+      int pos[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = min(u.r0 + g + 8 * e, u.r1 - 1), tok = r / A.G, hq = h * A.G + r - tok * A.G;
+        pos[e] = first + tok;
+        const bf16* src = (const bf16*)A.q + (u.s.q0 + tok) * A.ldq + (int64_t)hq * D + 8 * c;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint4 w;
+          if (q16) {
+            w = ld_reuse(src + 32 * i);
+          } else {
+            uint16_t v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = reinterpret_cast<const uint16_t*>(src)[32 * i + k];
+            w = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+          }
+          qa[i][0][e] = w.x;
+          qa[i][0][e + 2] = w.y;
+          qa[i][1][e] = w.z;
+          qa[i][1][e + 2] = w.w;
+        }
+      }
+      const int pos_min = first + u.r0 / A.G, pos_max = first + (u.r1 - 1) / A.G;
+      int stage = 0;
+#pragma unroll 1
+      for (int t = tile; t < t1; ++t) {
+        cp_wait<Sh::NS - 2>();
+        __syncwarp();  // all lanes' copies have landed, all lanes are done with the stage that is filled next
+        {
+          const int f = t + Sh::NS - 1;
+          if (f < t1) {
+            const KeyAt k = next;
+            next = key_at(A, u.b, base(f + 1) + (lane & 15), f + 1 < t1 ? u.hi : 0);
+            if (k.page == -2) atomicOr(A.err, kErrBadSlot);
+            few_load<D>(A, mine + (stage == 0 ? Sh::NS - 1 : stage - 1) * Sh::STAGE, k, h);
+          }
+          cp_commit();
+        }
+        const uint32_t st = mine + stage * Sh::STAGE;
+        stage = stage + 1 == Sh::NS ? 0 : stage + 1;
+        // scores of 2 x 8 keys
+        float s[2][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            const uint2 w = lds8(st + Sh::k_at(8 * n + g, 2 * i + (c >> 1)) + 8 * (c & 1));
+            mma16816(s[n], qa[i][0], codes_bf16<FMT>(w.x, w.x, 0, 1), codes_bf16<FMT>(w.x, w.x, 2, 3));
+            mma16816(s[n], qa[i][1], codes_bf16<FMT>(w.y, w.y, 0, 1), codes_bf16<FMT>(w.y, w.y, 2, 3));
+          }
+        }
+        const int j0 = base(t);
+        float vs[2][2];
+        float top[2] = {-INFINITY, -INFINITY};
+        const bool whole = j0 + kStep <= u.hi && (!A.causal || j0 + kStep - 1 <= pos_min) && (A.window <= 0 || j0 > pos_max - A.window);
+        unsigned hide = 0;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float2 ks = lds_f2(st + 2 * kStep * D + 4 * (8 * n + 2 * c));
+          const float2 vv = lds_f2(st + 2 * kStep * D + 4 * (kStep + 8 * n + 2 * c));
+          vs[n][0] = vv.x;
+          vs[n][1] = vv.y;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[n][e] *= (e & 1 ? ks.y : ks.x) * A.scale2;
+            if (!whole) {
+              const int j = j0 + 8 * n + 2 * c + (e & 1), p = pos[e >> 1];
+              const bool seen = j < u.hi && (!A.causal || j <= p) && (A.window <= 0 || j > p - A.window);
+              if (!seen) {
+                s[n][e] = -INFINITY;
+                hide |= 1u << (4 * n + e);
+              }
+            }
+            top[e >> 1] = fmaxf(top[e >> 1], s[n][e]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+          top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+        }
+        // The reference of a row's weights follows its maximum only when that has grown by more than 2^8:
+        // weights and sums have room for it, and the results are seldom rescaled.
+        if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float to = fmaxf(m[e], top[e]);
+            const float f = ex2(m[e] - finite_or_zero(to));
+            m[e] = to;
+            l[e] *= f;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+              o[i][2 * e] *= f;
+              o[i][2 * e + 1] *= f;
+            }
+          }
+        }
+        uint32_t pa[4];
+        const float ref[2] = {finite_or_zero(m[0]), finite_or_zero(m[1])};
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float p0 = ex2(s[n][2 * e] - ref[e]), p1 = ex2(s[n][2 * e + 1] - ref[e]);
+            l[e] += p0 + p1;
+            float w0 = p0 * vs[n][0], w1 = p1 * vs[n][1];
+            if (hide & (1u << (4 * n + 2 * e))) w0 = 0.f;  // whatever the scale of a key that is not seen
+            if (hide & (1u << (4 * n + 2 * e + 1))) w1 = 0.f;
+            pa[2 * n + e] = pack_bf16x2(w0, w1);
+          }
+        // results: keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9, values g D / 8 ..
+        constexpr int W = D / 32;  // words of a lane's slice of a key
+        uint32_t w[4][W];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = 2 * c + (k & 1) + 8 * (k >> 1);
+          const uint32_t vb = st + kStep * D;
+          if constexpr (W % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < W; i += 4) {
+              const uint32_t a = vb + Sh::v_at(r, g * (W / 4) + i / 4);
+              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[k][i]), "=r"(w[k][i + 1]), "=r"(w[k][i + 2]), "=r"(w[k][i + 3]) : "r"(a));
+            }
+          } else if constexpr (W == 2) {
+            const uint2 v = lds8(vb + Sh::v_at(r, g >> 1) + 8 * (g & 1));
+            w[k][0] = v.x;
+            w[k][1] = v.y;
+          } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[k][i]) : "r"(vb + Sh::v_at(r, 0) + 4 * (g * W + i)));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mma16816(o[4 * i + e], pa, codes_bf16<FMT>(w[0][i], w[1][i], e, e), codes_bf16<FMT>(w[2][i], w[3][i], e, e));
+      }
+      cp_wait<0>();
+      __syncwarp();  // the ring is the results' now
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+        const int r = g + 8 * e;
+        if (c == 0) *reinterpret_cast<float2*>(res + kFewRows * D + 2 * r) = make_float2(m[e], l[e]);
+        // value 4 i + k of slices 2 c and 2 c + 1
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int i = 0; i < D / 8; i += 4)
+            *reinterpret_cast<float4*>(res + r * D + (2 * c + q) * (D / 8) + i) =
+                make_float4(o[i][2 * e + q], o[i + 1][2 * e + q], o[i + 2][2 * e + q], o[i + 3][2 * e + q]);
+      }
+    }
+    const bool before = tile > 0, behind = t1 < u.tiles, split = before || behind;
+    if (S > 1) __syncthreads();
+    else __syncwarp();
+    if (on) {  // a warp writes rows slice, slice + S, ... of its head: the slices joined in order
+      const int slot = (int)blockIdx.x * 2 + (before ? 0 : 1);
+      for (int r = slice; r < nrows; r += S) {
+        float top = -INFINITY;
+        for (int k = 0; k < S; ++k) top = fmaxf(top, reinterpret_cast<float*>(ring)[(wh + k * A.HB) * (Sh::WARP / 4) + kFewRows * D + 2 * r]);
+        const float ref = finite_or_zero(top);
+        float sum = 0.f, acc[D / 32];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
+        for (int k = 0; k < S; ++k) {
+          const float* a = reinterpret_cast<float*>(ring) + (wh + k * A.HB) * (Sh::WARP / 4);
+          const float f = ex2(a[kFewRows * D + 2 * r] - ref);
+          sum += a[kFewRows * D + 2 * r + 1] * f;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) acc[i] += a[r * D + lane + 32 * i] * f;
+        }
+        if (split) {
+          const int64_t at = ((int64_t)slot * A.HB + wh) * kFewRows + r;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) A.part_o[at * D + lane + 32 * i] = acc[i];
+          if (lane == 0) *reinterpret_cast<float2*>(A.part_ml + 2 * at) = make_float2(top, sum);
+        } else {
+          const int row = u.r0 + r, tok = row / A.G, hq = h * A.G + row - tok * A.G;
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          bf16* dst = (bf16*)A.out + (u.s.q0 + tok) * A.ldo + (int64_t)hq * D;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) dst[lane + 32 * i] = __float2bfloat16_rn(sum == 0.f ? 0.f : acc[i] * inv);
+          if (A.lse && lane == 0) A.lse[(int64_t)(u.s.q0 + tok) * A.Hq + hq] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+        }
+      }
+    }
+    if (behind && !before && threadIdx.x == 0) {  // the first part of a unit that others continue
+      int* f = A.info + blockIdx.x * kAttnInfo;
+      f[1] = u.b;
+      f[2] = u.blk;
+      f[3] = u.hg;
+      f[0] = parts_behind(plan, x + (u.tiles - 1 - tile));
+    }
+    x += t1 - tile;
+    if (x >= x1) break;
+    tile = 0;
+    bool more;
+    switch (S) {
+      case 8: more = next_unit<kFewRows, 8 * kStep>(A, u); break;
+      case 4: more = next_unit<kFewRows, 4 * kStep>(A, u); break;
+      case 2: more = next_unit<kFewRows, 2 * kStep>(A, u); break;
+      default: more = next_unit<kFewRows, kStep>(A, u);
+    }
+    if (!more) break;
+    if (S > 1) __syncthreads();
+    else __syncwarp();
+  }
+}
+
+// Join the parts of the units that the plan divided.  Block (c, wh): head wh of the unit that
+// began in block c of the primary kernel; a warp per row, lanes over the values.
+template <int MR>
+__global__ void __launch_bounds__(256) attn8_join(const __grid_constant__ AttnArgs A) {
+  wait_for_primary();
+  const int c = blockIdx.x, wh = blockIdx.y, lane = threadIdx.x & 31;
+  const int n = A.info[c * kAttnInfo];  // parts in the blocks behind c
+  if (n < 1) return;
+  const int b = A.info[c * kAttnInfo + 1], blk = A.info[c * kAttnInfo + 2], h = A.info[c * kAttnInfo + 3] * A.HB + wh;
+  if (h >= A.Hk) return;
+  const Seq s = seq_at(A, b);
+  const int r0 = blk * MR, nrows = min(MR, s.nq * A.G - r0);
+  // part k: of block c its second place, of the blocks behind it their first
+  const auto place = [&](int k, int r) { return ((int64_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * A.HB + wh) * MR + r; };
+  for (int r = blockIdx.z * 8 + warp_index(); r < nrows; r += 8 * gridDim.z) {
+    float top = -INFINITY;
+    for (int k = lane; k <= n; k += 32) top = fmaxf(top, A.part_ml[2 * place(k, r)]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float ref = finite_or_zero(top);
+    float sum = 0.f, acc[kAttnMaxHeads / 32];
+#pragma unroll
+    for (int i = 0; i < kAttnMaxHeads / 32; ++i) acc[i] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k <= n; ++k) {
+      const int64_t at = place(k, r);
+      const float2 ml = *reinterpret_cast<const float2*>(A.part_ml + 2 * at);
+      const float f = ex2(ml.x - ref);
+      sum += ml.y * f;
+#pragma unroll
+      for (int i = 0; i < kAttnMaxHeads / 32; ++i)
+        if (lane + 32 * i < A.D) acc[i] += A.part_o[at * A.D + lane + 32 * i] * f;
+    }
+    const int row = r0 + r, tok = row / A.G, hq = h * A.G + row - tok * A.G;
+    const float inv = 1.f / sum;
+    bf16* dst = (bf16*)A.out + (s.q0 + tok) * A.ldo + (int64_t)hq * A.D;
+#pragma unroll
+    for (int i = 0; i < kAttnMaxHeads / 32; ++i)
+      if (lane + 32 * i < A.D) dst[lane + 32 * i] = __float2bfloat16_rn(sum == 0.f ? 0.f : acc[i] * inv);
+    if (A.lse && lane == 0) A.lse[(int64_t)(s.q0 + tok) * A.Hq + hq] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  }
+}
+
+// Element path: float32 rows, other head sizes, other alignments.  A warp per row: scores of
+// 32 keys at a time, a lane each; then lanes over the values.
+template <typename T, int FMT>
+__global__ void __launch_bounds__(128) attn8_elem(const __grid_constant__ AttnArgs A) {
+  __shared__ float qs[4][kAttnMaxHeads];
+  const int lane = threadIdx.x & 31, warp = warp_index();
+  const int64_t rows = (int64_t)A.T * A.Hq;
+  const int end = min(max(__ldg(A.cu + A.B), 0), A.T);
+  for (int64_t x = (int64_t)blockIdx.x * 4 + warp; x < rows; x += (int64_t)gridDim.x * 4) {
+    const int tok = (int)(x / A.Hq), hq = (int)(x - (int64_t)tok * A.Hq), h = hq / A.G;
+    if (tok >= end) return;  // rows behind the last sequence
+    // the last sequence that starts at or before the token
+    int lo = 0, hi = A.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (__ldg(A.cu + mid) <= tok) lo = mid;
+      else hi = mid - 1;
+    }
+    const int b = lo;
+    const Seq s = seq_at(A, b);
+    if (tok < s.q0 || tok >= s.q0 + s.nq) continue;
+    const T* src = (const T*)A.q + tok * A.ldq + (int64_t)hq * A.D;
+    __syncwarp();
+    for (int d = lane; d < A.D; d += 32) qs[warp][d] = to_f32(src[d]);
+    __syncwarp();
+    const int pos = s.kv - s.nq + tok - s.q0;
+    const int first = A.window > 0 ? max(0, pos - A.window + 1) : 0, last = A.causal ? min(s.kv, pos + 1) : s.kv;
+    float m = -INFINITY, l = 0.f, acc[kAttnMaxHeads / 32];
+#pragma unroll
+    for (int i = 0; i < kAttnMaxHeads / 32; ++i) acc[i] = 0.f;
+    for (int j0 = first; j0 < last; j0 += 32) {
+      const int j = j0 + lane;
+      KeyAt k = key_at(A, b, j, last);
+      if (k.page == -2) atomicOr(A.err, kErrBadSlot);
+      float sc = -INFINITY, vs = 0.f;
+      if (k.page >= 0) {
+        const uint8_t* kc = A.K.q + A.K.cq.at(k.page, k.off, h);
+        float dot = 0.f;
+        for (int d = 0; d < A.D; ++d) {
+          float t[4];
+          q8_decode4<FMT>(kc[d], t);
+          dot = fmaf(qs[warp][d], t[0], dot);
+        }
+        sc = dot * (A.K.sc[A.K.cs.at(k.page, k.off, h)] * A.scale2);
+        vs = A.V.sc[A.V.cs.at(k.page, k.off, h)];
+      } else if (k.page == -2) {
+        sc = vs = __int_as_float(0x7fc00000);
+      }
+      float top = sc;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float to = fmaxf(m, top), ref = finite_or_zero(to), f = ex2(m - ref);
+      m = to;
+      const float p = ex2(sc - ref);
+      l = l * f + p;
+#pragma unroll
+      for (int i = 0; i < kAttnMaxHeads / 32; ++i) acc[i] *= f;
+      const float w = p * vs;
+      const int n = min(32, last - j0);
+      for (int i = 0; i < n; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        const int page = __shfl_sync(0xffffffffu, k.page, i);
+        const uint32_t off = __shfl_sync(0xffffffffu, k.off, i);
+        const uint8_t* vc = A.V.q + A.V.cq.at(page >= 0 ? page : 0, page >= 0 ? off : 0, h);
+#pragma unroll
+        for (int e = 0; e < kAttnMaxHeads / 32; ++e)
+          if (lane + 32 * e < A.D) {
+            float t[4] = {0.f, 0.f, 0.f, 0.f};
+            if (page >= 0) q8_decode4<FMT>(vc[lane + 32 * e], t);
+            acc[e] = fmaf(wi, t[0], acc[e]);
+          }
+      }
+    }
+    l = group_sum<32>(l);
+    T* dst = (T*)A.out + tok * A.ldo + (int64_t)hq * A.D;
+#pragma unroll
+    for (int e = 0; e < kAttnMaxHeads / 32; ++e)
+      if (lane + 32 * e < A.D) dst[lane + 32 * e] = from_f32<T>(l == 0.f ? 0.f : acc[e] / l);
+    if (A.lse && lane == 0) A.lse[(int64_t)tok * A.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+FastDiv fast_div(uint32_t d) {
+  uint32_t l = 0;
+  while ((1ull << l) < d) ++l;
+  return {d, (uint32_t)(((1ull << (31 + l)) + d - 1) / d), 31 + l};
+}
+
+// K/V heads of a block of the kernel for few rows: all eight warps on heads of their own where
+// the batch fills the GPU (neighbouring heads' scales share their sectors), fewer, with the
+// keys of a head cut into slices, where it does not: less is left to be joined.
+int few_heads(int64_t B, int Hk, int sms) {
+  int hb = 1;
+  while (hb < kFewWarps && hb < Hk && B * Hk >= (int64_t)sms * hb) hb *= 2;
+  return hb;
+}
+
+template <int D, int FMT>
+gbln_status few_go(const AttnArgs& A, int blocks, bool q16, cudaStream_t s) {
+  using Sh = FewShape<D>;
+  static std::atomic<uint64_t> ready{0};  // devices whose limit is raised
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return GBLN_ERR_CUDA;
+  if (!(ready.load(std::memory_order_acquire) >> dev & 1)) {
+    if (cudaFuncSetAttribute(attn8_few<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM) != cudaSuccess) {
+      cudaGetLastError();
+      return GBLN_ERR_CUDA;
+    }
+    ready.fetch_or(1ull << dev, std::memory_order_release);
+  }
+  attn8_few<D, FMT><<<blocks, 32 * kFewWarps, Sh::SMEM, s>>>(A, q16);
+  if (cudaGetLastError() != cudaSuccess) return GBLN_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)blocks, (unsigned)A.HB, 1);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn8_join<kFewRows>, A) == cudaSuccess ? GBLN_OK : (cudaGetLastError(), GBLN_ERR_CUDA);
+}
+
+template <int FMT>
+gbln_status few_typed(const AttnArgs& A, int blocks, bool q16, cudaStream_t s) {
+  switch (A.D) {
+    case 64: return few_go<64, FMT>(A, blocks, q16, s);
+    case 96: return few_go<96, FMT>(A, blocks, q16, s);
+    case 128: return few_go<128, FMT>(A, blocks, q16, s);
+    default: return few_go<256, FMT>(A, blocks, q16, s);
+  }
+}
+
+bool fast_head(int32_t D, int io) { return io == GBLN_BF16 && (D == 64 || D == 96 || D == 128 || D == 256); }
+
+bool attn_sizes_ok(int64_t T, int32_t B, int32_t Hq, int32_t Hk, int32_t D) {
+  return T >= 0 && B >= 0 && Hk >= 1 && Hq >= 1 && Hq % Hk == 0 && D >= 1 && D <= kAttnMaxHeads && (int64_t)Hq * D <= (1 << 24) &&
+         T <= (1LL << 30) / Hq;
+}
+
+}  // namespace
+
+}  // namespace gbln
+
+using namespace gbln;
+
+extern "C" int64_t gbln_attn_cache8_workspace(int64_t T, int32_t B, int32_t Hq, int32_t Hk, int32_t D, gbln_dtype io) {
+  if (!dtype_ok(io) || !attn_sizes_ok(T, B, Hq, Hk, D)) return -1;
+  if (T == 0 || B == 0 || !fast_head(D, io)) return 0;
+  const int sms = sm_count();
+  if (sms <= 0) return -1;
+  const int hb = few_heads(B, Hk, sms);
+  return (int64_t)sms * (kAttnInfo * 4 + 2 * hb * kFewRows * (D + 2) * 4);
+}
+
+extern "C" gbln_status gbln_attn_cache8(const void* q, const int32_t* cu_seqlens_q, const int32_t* kv_lens,
+                                        const int32_t* page_table, int64_t max_pages, const gbln_cache8* k_cache,
+                                        const gbln_cache8* v_cache, void* out, float* lse, void* workspace,
+                                        int64_t workspace_bytes, int64_t T, int32_t B, int32_t Hq, int32_t Hk, int32_t D,
+                                        int64_t ld_q, int64_t ld_out, float scale, int32_t causal, int32_t window,
+                                        gbln_q8 fmt, gbln_dtype io, gbln_stream_t stream) {
+  if (!dtype_ok(io) || !q8_ok(fmt) || !attn_sizes_ok(T, B, Hq, Hk, D)) return GBLN_ERR_INVALID_ARG;
+  if (max_pages < 0 || window < 0 || !(scale >= -3.0e38f && scale <= 3.0e38f)) return GBLN_ERR_INVALID_ARG;
+  if (!ld_fits(T, (int64_t)Hq * D, ld_q) || !ld_fits(T, (int64_t)Hq * D, ld_out)) return GBLN_ERR_INVALID_ARG;
+  if (!cache_ok(k_cache, Hk, D) || !cache_ok(v_cache, Hk, D)) return GBLN_ERR_INVALID_ARG;
+  if (k_cache->pages != v_cache->pages || k_cache->page_size != v_cache->page_size) return GBLN_ERR_INVALID_ARG;
+  if (k_cache->pages >= (1LL << 31) || k_cache->page_size > (1LL << 30) || max_pages > (1LL << 30) / k_cache->page_size)
+    return GBLN_ERR_INVALID_ARG;
+  if (T == 0 || B == 0) return GBLN_OK;  // nothing is read or written: pointers are not examined
+  if (!q || !cu_seqlens_q || !kv_lens || !out || (max_pages > 0 && !page_table)) return GBLN_ERR_INVALID_ARG;
+  if (k_cache->pages > 0 && (!k_cache->codes || !k_cache->scale || !v_cache->codes || !v_cache->scale)) return GBLN_ERR_INVALID_ARG;
+  if (!aligned_to(cu_seqlens_q, 4) || !aligned_to(kv_lens, 4) || !aligned_to(page_table, 4) || !aligned_to(lse, 4)) return GBLN_ERR_INVALID_ARG;
+  const int sms = sm_count();
+  unsigned int* err = device_error_word();
+  if (sms <= 0 || !err) return GBLN_ERR_CUDA;
+  AttnArgs A{};
+  A.q = q;
+  A.out = out;
+  A.lse = lse;
+  A.cu = cu_seqlens_q;
+  A.kv = kv_lens;
+  A.pages = page_table;
+  A.max_pages = max_pages;
+  A.ldq = ld_q;
+  A.ldo = ld_out;
+  A.T = (int)T;
+  A.B = B;
+  A.Hq = Hq;
+  A.Hk = Hk;
+  A.G = Hq / Hk;
+  A.D = D;
+  A.scale2 = scale * 1.4426950408889634f;
+  A.causal = causal != 0;
+  A.window = window < (1 << 30) ? window : 0;  // no position is that far from another
+  A.n_pages = (int)k_cache->pages;
+  A.page = fast_div((uint32_t)k_cache->page_size);
+  A.K = cache_of(k_cache);
+  A.V = cache_of(v_cache);
+  A.err = err;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (fast_head(D, io) && codes_aligned(k_cache, v_cache, 16)) {
+    if (!workspace || !aligned16(workspace) || workspace_bytes < gbln_attn_cache8_workspace(T, B, Hq, Hk, D, io)) return GBLN_ERR_WORKSPACE;
+    A.HB = few_heads(B, Hk, sms);
+    A.NHG = (Hk + A.HB - 1) / A.HB;
+    A.info = (int*)workspace;
+    A.part_ml = (float*)workspace + (int64_t)sms * kAttnInfo;
+    A.part_o = A.part_ml + (int64_t)sms * 2 * A.HB * kFewRows * 2;
+    const bool q16 = aligned16(q) && ld_q % 8 == 0;
+    return fmt == GBLN_Q8_INT8 ? few_typed<GBLN_Q8_INT8>(A, sms, q16, s) : few_typed<GBLN_Q8_E4M3>(A, sms, q16, s);
+  }
+  const unsigned grid = grid_for(T * (int64_t)Hq, 4, (int64_t)sms * 32);
+  if (io == GBLN_F32) {
+    if (fmt == GBLN_Q8_INT8) attn8_elem<float, GBLN_Q8_INT8><<<grid, 128, 0, s>>>(A);
+    else attn8_elem<float, GBLN_Q8_E4M3><<<grid, 128, 0, s>>>(A);
+  } else {
+    if (fmt == GBLN_Q8_INT8) attn8_elem<bf16, GBLN_Q8_INT8><<<grid, 128, 0, s>>>(A);
+    else attn8_elem<bf16, GBLN_Q8_E4M3><<<grid, 128, 0, s>>>(A);
+  }
+  return launch_status();
+}

@@ -164,3 +164,23 @@ def test_qk_norm_rope_cache_rejects(lib):
         assert call(**b) == INVALID, b
     assert call(wt=5) == UNSUPPORTED
     assert call(T=0) == OK
+
+
+def test_attention_rejects(lib):
+    import rmsnorm_fwd_bwd_03_gb300 as gb
+
+    def cache(codes=FAKE, scale=FAKE, pages=4, page=16, head=8):
+        return gb._pack_cache8(codes, scale, pages, page, page * head, head, head, page, 1, 1)
+
+    def call(q=FAKE, cu=FAKE, kv=FAKE, table=FAKE, most=4, kc=cache(), vc=cache(FAKE * 2, FAKE * 2), out=FAKE, lse=None, T=4, B=2, Hq=2, Hk=1,
+             D=8, ldq=16, ldo=16, scale=1.0, window=0, fmt=0, io=BF16):
+        return lib.gbln_attn_cache8(q, cu, kv, table, most, kc, vc, out, lse, None, 0, T, B, Hq, Hk, D, ldq, ldo, scale, 1, window, fmt, io, None)
+    for b in (dict(q=None), dict(cu=None), dict(kv=None), dict(table=None), dict(out=None), dict(kc=None), dict(vc=None), dict(T=-1), dict(B=-1),
+              dict(Hq=3, Hk=2), dict(Hk=0), dict(D=0), dict(D=513), dict(ldq=15), dict(ldo=15), dict(scale=float("nan")), dict(scale=float("inf")),
+              dict(window=-1), dict(fmt=2), dict(io=4), dict(most=-1), dict(most=1 << 30), dict(vc=cache(pages=5)), dict(kc=cache(head=7)),
+              dict(kc=cache(0)), dict(cu=FAKE + 2), dict(kv=FAKE + 1), dict(table=FAKE + 2), dict(lse=FAKE + 2), dict(T=1 << 30)):
+        assert call(**b) == INVALID, b
+    assert call(T=0) == OK and call(B=0, q=None) == OK
+    assert lib.gbln_attn_cache8_workspace(4, 2, 3, 2, 64, BF16) == -1
+    assert lib.gbln_attn_cache8_workspace(4, 2, 2, 1, 80, BF16) == 0
+    assert lib.gbln_attn_cache8_workspace(0, 2, 2, 1, 64, BF16) == 0
