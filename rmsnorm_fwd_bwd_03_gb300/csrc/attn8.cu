@@ -570,17 +570,7 @@ gbln_status few_go(const AttnArgs& A, int blocks, bool q16, cudaStream_t s) {
     ready.fetch_or(1ull << dev, std::memory_order_release);
   }
   attn8_few<D, FMT><<<blocks, 32 * kFewWarps, Sh::SMEM, s>>>(A, q16);
-  if (cudaGetLastError() != cudaSuccess) return GBLN_ERR_CUDA;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)blocks, (unsigned)A.HB, 1);
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn8_join<kFewRows>, A) == cudaSuccess ? GBLN_OK : (cudaGetLastError(), GBLN_ERR_CUDA);
+  return cudaGetLastError() == cudaSuccess ? attn_join_launch(A, blocks, kFewRows, s) : GBLN_ERR_CUDA;
 }
 
 template <int FMT>
@@ -593,6 +583,10 @@ gbln_status few_typed(const AttnArgs& A, int blocks, bool q16, cudaStream_t s) {
   }
 }
 
+// Rows for the tensor-core kernel: where a sequence brings more rows on average than the other
+// kernel takes at once, so that K and V would be converted several times over there.
+bool many_rows(int64_t T, int32_t B, int G, int32_t D) { return D <= 128 && T * G > 2 * kFewRows * (int64_t)B; }
+
 bool fast_head(int32_t D, int io) { return io == GBLN_BF16 && (D == 64 || D == 96 || D == 128 || D == 256); }
 
 bool attn_sizes_ok(int64_t T, int32_t B, int32_t Hq, int32_t Hk, int32_t D) {
@@ -601,6 +595,22 @@ bool attn_sizes_ok(int64_t T, int32_t B, int32_t Hq, int32_t Hk, int32_t D) {
 }
 
 }  // namespace
+
+gbln_status attn_join_launch(const AttnArgs& A, int blocks, int rows, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)blocks, (unsigned)A.HB, rows == kFewRows ? 1 : 8);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = rows == kFewRows ? cudaLaunchKernelEx(&cfg, attn8_join<kFewRows>, A) : cudaLaunchKernelEx(&cfg, attn8_join<kManyUnit>, A);
+  if (e == cudaSuccess) return GBLN_OK;
+  cudaGetLastError();
+  return GBLN_ERR_CUDA;
+}
 
 }  // namespace gbln
 
@@ -611,8 +621,8 @@ extern "C" int64_t gbln_attn_cache8_workspace(int64_t T, int32_t B, int32_t Hq, 
   if (T == 0 || B == 0 || !fast_head(D, io)) return 0;
   const int sms = sm_count();
   if (sms <= 0) return -1;
-  const int hb = few_heads(B, Hk, sms);
-  return (int64_t)sms * (kAttnInfo * 4 + 2 * hb * kFewRows * (D + 2) * 4);
+  const int rows = many_rows(T, B, Hq / Hk, D) ? kManyUnit : few_heads(B, Hk, sms) * kFewRows;
+  return (int64_t)sms * (kAttnInfo * 4 + 2 * rows * (D + 2) * 4);
 }
 
 extern "C" gbln_status gbln_attn_cache8(const void* q, const int32_t* cu_seqlens_q, const int32_t* kv_lens,
@@ -662,11 +672,13 @@ extern "C" gbln_status gbln_attn_cache8(const void* q, const int32_t* cu_seqlens
   cudaStream_t s = (cudaStream_t)stream;
   if (fast_head(D, io) && codes_aligned(k_cache, v_cache, 16)) {
     if (!workspace || !aligned16(workspace) || workspace_bytes < gbln_attn_cache8_workspace(T, B, Hq, Hk, D, io)) return GBLN_ERR_WORKSPACE;
-    A.HB = few_heads(B, Hk, sms);
+    const bool many = many_rows(T, B, A.G, D);
+    A.HB = many ? 1 : few_heads(B, Hk, sms);
     A.NHG = (Hk + A.HB - 1) / A.HB;
     A.info = (int*)workspace;
     A.part_ml = (float*)workspace + (int64_t)sms * kAttnInfo;
-    A.part_o = A.part_ml + (int64_t)sms * 2 * A.HB * kFewRows * 2;
+    A.part_o = A.part_ml + (int64_t)sms * 2 * 2 * (many ? kManyUnit : A.HB * kFewRows);
+    if (many) return attn_many_launch(A, sms, fmt, s);
     const bool q16 = aligned16(q) && ld_q % 8 == 0;
     return fmt == GBLN_Q8_INT8 ? few_typed<GBLN_Q8_INT8>(A, sms, q16, s) : few_typed<GBLN_Q8_E4M3>(A, sms, q16, s);
   }

@@ -210,8 +210,11 @@ __device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontro
 constexpr int kAttnInfo = 4;        // ints of info per block
 constexpr int kAttnMaxHeads = 512;  // values of a head
 constexpr int kFewRows = 16;        // rows of a unit of the kernel for few rows
+constexpr int kManyUnit = 256;      // and of the kernel for many
 
-// Launches of the paths, each with the kernel that joins its parts.
-gbln_status attn_few_launch(const AttnArgs& A, int blocks, int fmt, cudaStream_t s);
+// The kernel for many rows (attn8_many.cu), with the one that joins its parts.
+gbln_status attn_many_launch(const AttnArgs& A, int blocks, int fmt, cudaStream_t s);
+// Joins the parts of a launch of `blocks` blocks whose units have `rows` rows.
+gbln_status attn_join_launch(const AttnArgs& A, int blocks, int rows, cudaStream_t s);
 
 }  // namespace gbln

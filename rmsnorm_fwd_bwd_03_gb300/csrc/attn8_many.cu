@@ -1,0 +1,599 @@
+// Attention over the 8-bit cache where sequences bring many rows (chunks of prompts, whole
+// prompts): bound by the tensor cores, 4 D operations per pair of row and key, beside one
+// exponential each.
+//
+// A block takes 256 rows (new tokens x heads of a group) of one K/V head as two tiles of
+// 128, and 128 keys at a time:
+//   * four warps fetch codes, turn them into bf16 (exactly) and lay K and V in shared
+//     memory, in the 128-byte swizzle that the tensor cores read;
+//   * one thread issues the products (tcgen05): S_t = Q_t K^T into tensor memory, later
+//     O_t += P_t V with P_t read from tensor memory;
+//   * four warps per tile turn S_t into P_t, a thread per row: no shuffles, and the row's
+//     maximum, sum and rescaling stay in its registers.  P_t overwrites S_t.
+// While one tile's weights are computed, the other's products run.  Tensor memory: S_0, S_1,
+// O_0, O_1, 128 columns each, all 512.
+
+#include <atomic>
+
+#include "attn8.cuh"
+
+namespace gbln {
+
+namespace {
+
+constexpr int kTile = 128;              // rows of a tile, keys of a step
+constexpr int kManyRows = 2 * kTile;    // rows of a unit
+static_assert(kManyRows == kManyUnit, "the joining kernel knows it too");
+constexpr int kConvWarps = 4;                    // one per scheduler
+constexpr int kConvRows = kTile / kConvWarps / 8;  // keys of a converting thread
+constexpr int kManyThreads = 32 * (8 + kConvWarps + 1);
+
+template <int D>
+struct ManyShape {
+  static constexpr int PLANES = (D + 63) / 64;      // of 64 values: 128 bytes of bf16
+  static constexpr int PLANE = kTile * 128;         // bytes
+  static constexpr int TILE = PLANES * PLANE;       // 128 rows or keys
+  static constexpr int SMEM = 6 * TILE + 1024;      // Q_0, Q_1, two stages of K and of V; alignment
+};
+
+// Barriers of a block.
+enum { kKFull = 0, kKFree = 2, kVFull = 4, kVFree = 6, kQFull = 8, kSFull = 10, kPFull = 12, kOFull = 14, kBars = 16 };
+
+struct Shared {
+  uint64_t bar[kBars];
+  __align__(16) float scale[2][2][kTile];  // [stage][K times the softmax scale, V][key]
+  Part plan;
+  uint32_t tmem;
+  int stop;
+};
+
+// --- tcgen05 ---------------------------------------------------------------
+// Shared memory matrix descriptor: 128-byte swizzle, start, leading and stride byte offsets.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// Instruction descriptor: bf16 x bf16 + float32, M = 128, N = n; B with its N values contiguous where `nmajor`.
+constexpr uint32_t inst_desc(int n, bool nmajor) {
+  return 1u << 4 | 1u << 7 | 1u << 10 | (nmajor ? 1u << 16 : 0u) | (uint32_t)(n / 8) << 17 | (uint32_t)(kTile / 16) << 24;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+               ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
+}
+// `bar` completes when all products issued by this thread so far have.
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+#define GBLN_R8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
+#define GBLN_W8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
+// 32 columns of the thread's lane.
+__device__ __forceinline__ void tm_ld32(uint32_t (&v)[32], uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,"
+      "%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : GBLN_R8(v, 0), GBLN_R8(v, 8), GBLN_R8(v, 16), GBLN_R8(v, 24)
+      : "r"(at));
+}
+__device__ __forceinline__ void tm_st32(uint32_t at, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
+      "%24,%25,%26,%27,%28,%29,%30,%31};" ::GBLN_W8(v, 0), GBLN_W8(v, 8), GBLN_W8(v, 16), GBLN_W8(v, 24), "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t at, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::GBLN_W8(v, 0), GBLN_W8(v, 8),
+      "r"(at)
+      : "memory");
+}
+
+// Bounded wait of a whole warp (or of one thread alone); false once any wait of the block has run out.
+__device__ __forceinline__ bool wait_thread(Shared& sh, int bar, uint32_t parity, unsigned int* err) {
+  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+    if (mbar_try_wait(&sh.bar[bar], parity)) return true;
+    if (*(volatile int*)&sh.stop) return false;
+  }
+  *(volatile int*)&sh.stop = 1;
+  atomicOr(err, kErrWaitTimeout);
+  return false;
+}
+__device__ __forceinline__ bool wait_warp(Shared& sh, int bar, uint32_t parity, unsigned int* err) {
+  return __all_sync(0xffffffffu, wait_thread(sh, bar, parity, err));
+}
+
+// --- codes -> bf16 in shared memory ------------------------------------------
+// Four codes as four bf16 values (the conversions are written out in attn8.cu's codes_bf16).
+template <int FMT>
+__device__ __forceinline__ uint2 codes4_bf16(uint32_t x) {
+  uint2 r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t u, s;
+    __nv_bfloat162 v;
+    if constexpr (FMT == GBLN_Q8_INT8) {
+      const uint32_t w = __byte_perm(x, 0x43u, 0x4140 + 0x0202 * i);
+      u = w & 0xff7fff7fu;
+      s = w & 0xff80ff80u;
+      v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), *reinterpret_cast<const __nv_bfloat162*>(&s));
+    } else {
+      const uint32_t w = __byte_perm(x, 0u, 0x1404 + 0x2020 * i);
+      u = (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u);
+      s = 0x7b807b80u;  // 2^120
+      v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u), *reinterpret_cast<const __nv_bfloat162*>(&s));
+    }
+    (i ? r.y : r.x) = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return r;
+}
+// Sixteen codes to the chunks 2 c and 2 c + 1 of row `row` of a plane.
+template <int FMT>
+__device__ __forceinline__ void store_codes(uint32_t plane, int row, int c, uint4 w) {
+  const uint2 a = codes4_bf16<FMT>(w.x), b = codes4_bf16<FMT>(w.y), e = codes4_bf16<FMT>(w.z), f = codes4_bf16<FMT>(w.w);
+  const uint32_t at = plane + row * 128;
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + 16 * ((2 * c) ^ (row & 7))), "r"(a.x), "r"(a.y), "r"(b.x), "r"(b.y) : "memory");
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + 16 * ((2 * c + 1) ^ (row & 7))), "r"(e.x), "r"(e.y), "r"(f.x), "r"(f.y) : "memory");
+}
+
+struct KeyPage {
+  int page;  // -1: none, -2: outside the cache
+  uint32_t off;
+};
+__device__ __forceinline__ KeyPage page_at(const AttnArgs& A, int b, int j, int hi) {
+  KeyPage k{-1, 0};
+  if (j < hi) {
+    uint32_t p;
+    A.page.split((uint32_t)j, p, k.off);
+    k.page = __ldg(A.pages + (int64_t)b * A.max_pages + p);
+    if (k.page < 0 || k.page >= A.n_pages) k.page = -2;
+  }
+  return k;
+}
+
+// The warps that bring K and V in.  Lane (r, c) = (lane / 4, lane % 4) of warp w has the chunks c, c + 4
+// (16 codes each) of keys 32 w + r, + 8, + 16, + 24: a store instruction's eight lanes at a time hit all banks.
+// Each tile's codes are on their way while the tile before is converted.
+template <int D, int FMT>
+__device__ __forceinline__ void convert(const AttnArgs& A, Shared& sh, uint32_t kv_smem, int w) {
+  using M = ManyShape<D>;
+  constexpr int NP = M::PLANES;
+  const int lane = threadIdx.x & 31, c = lane & 3;
+  const int row = 8 * kConvRows * w + (lane >> 2);  // + 8 i
+  Unit u = sh.plan.u;
+  int tile = sh.plan.tile;
+  const int64_t n_tiles = sh.plan.x1 - sh.plan.x0;
+  KeyPage kp[kConvRows];
+  int h = 0;
+  uint4 kr[kConvRows][NP], vr[kConvRows][NP];
+  float sc[kConvRows];
+  const auto pages = [&]() {
+#pragma unroll
+    for (int i = 0; i < kConvRows; ++i) {
+      kp[i] = page_at(A, u.b, u.lo + tile * kTile + row + 8 * i, u.hi);
+      if (kp[i].page == -2) atomicOr(A.err, kErrBadSlot);
+    }
+    h = u.hg;
+  };
+  const auto fetch = [&](const Cache& C, uint4 (&r)[kConvRows][NP]) {
+#pragma unroll
+    for (int i = 0; i < kConvRows; ++i) {
+      const uint8_t* src = C.q + C.cq.at(max(kp[i].page, 0), kp[i].off, h) + 16 * c;
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+        r[i][p] = kp[i].page >= 0 && 64 * p + 16 * c < D ? ld_stream(src + 64 * p) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  const auto scales = [&]() {
+    const Cache& C = c == 0 ? A.K : A.V;
+#pragma unroll
+    for (int i = 0; i < kConvRows; ++i) {
+      sc[i] = kp[i].page == -2 ? __int_as_float(0x7fc00000) : 0.f;
+      if (c < 2 && kp[i].page >= 0) sc[i] = __ldg(C.sc + C.cs.at(kp[i].page, kp[i].off, h)) * (c == 0 ? A.scale2 : 1.f);
+    }
+  };
+  pages();
+  fetch(A.K, kr);
+  fetch(A.V, vr);
+  scales();
+  for (int64_t n = 0; n < n_tiles; ++n) {
+    const int st = (int)(n & 1);
+    const uint32_t again = (uint32_t)(n >> 1 & 1) ^ 1u;
+    const bool more = n + 1 < n_tiles;
+    if (more) {
+      if (++tile == u.tiles) {
+        tile = 0;
+        next_unit<kManyRows, kTile>(A, u);
+      }
+      pages();
+    }
+    if (!wait_warp(sh, kKFree + st, again, A.err)) return;
+    const uint32_t ks = kv_smem + st * M::TILE, vs = kv_smem + (2 + st) * M::TILE;
+#pragma unroll
+    for (int i = 0; i < kConvRows; ++i)
+#pragma unroll
+      for (int p = 0; p < NP; ++p) store_codes<FMT>(ks + p * M::PLANE, row + 8 * i, c, kr[i][p]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.bar[kKFull + st]);
+    if (more) fetch(A.K, kr);
+    if (!wait_warp(sh, kVFree + st, again, A.err)) return;
+#pragma unroll
+    for (int i = 0; i < kConvRows; ++i) {
+#pragma unroll
+      for (int p = 0; p < NP; ++p) store_codes<FMT>(vs + p * M::PLANE, row + 8 * i, c, vr[i][p]);
+      if (c < 2) sh.scale[st][c][row + 8 * i] = sc[i];
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.bar[kVFull + st]);
+    if (more) {
+      fetch(A.V, vr);
+      scales();
+    }
+  }
+}
+
+// The thread that issues the products.
+template <int D>
+__device__ __forceinline__ void products(const AttnArgs& A, Shared& sh, uint32_t q_smem, uint32_t kv_smem) {
+  using M = ManyShape<D>;
+  constexpr uint32_t QK = inst_desc(kTile, false), PV = inst_desc(D, true);
+  const uint32_t tm = sh.tmem;
+  Unit u = sh.plan.u;
+  int tile = sh.plan.tile;
+  int64_t left = sh.plan.x1 - sh.plan.x0;
+  uint32_t n = 0;            // tiles so far
+  uint32_t rounds[2] = {0, 0};  // weights of each tile of rows so far
+  uint32_t units[2] = {0, 0};
+  const auto scores = [&](int t, uint32_t st) {
+    const uint32_t q = q_smem + t * M::TILE, k = kv_smem + st * M::TILE;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      const uint32_t at = (i / 4) * M::PLANE + (i % 4) * 32;
+      mma_ss(tm + t * kTile, smem_desc(q + at, 16, 1024), smem_desc(k + at, 16, 1024), QK, i > 0);
+    }
+    mma_commit(&sh.bar[kSFull + t]);
+  };
+  const auto results = [&](int t, uint32_t st, bool add) {
+    const uint32_t v = kv_smem + (2 + st) * M::TILE;
+#pragma unroll
+    for (int i = 0; i < kTile / 16; ++i)  // 16 keys: 16 rows of 128 bytes, 8 columns of weights
+      mma_ts(tm + 2 * kTile + t * kTile, tm + t * kTile + 8 * i, smem_desc(v + i * 2048, M::PLANE, 1024), PV, add || i > 0);
+  };
+  while (left > 0) {
+    const int nt = (int)min((int64_t)(u.tiles - tile), left), tiles_of_rows = u.r1 - u.r0 > kTile ? 2 : 1;
+    for (int t = 0; t < tiles_of_rows; ++t) {
+      if (!wait_thread(sh, kQFull + t, units[t] & 1, A.err)) return;
+      ++units[t];
+      if (t == 0 && !wait_thread(sh, kKFull + (n & 1), n >> 1 & 1, A.err)) return;
+      tc_after();
+      scores(t, n & 1);
+    }
+    mma_commit(&sh.bar[kKFree + (n & 1)]);
+    for (int i = 0; i < nt; ++i, ++n) {
+      const uint32_t st = n & 1, next = (n + 1) & 1;
+      if (!wait_thread(sh, kVFull + st, n >> 1 & 1, A.err)) return;
+      for (int t = 0; t < tiles_of_rows; ++t) {
+        if (!wait_thread(sh, kPFull + t, rounds[t] & 1, A.err)) return;
+        ++rounds[t];
+        tc_after();
+        results(t, st, i > 0);
+        if (i + 1 == nt) mma_commit(&sh.bar[kOFull + t]);
+        if (t + 1 == tiles_of_rows) mma_commit(&sh.bar[kVFree + st]);
+        if (i + 1 < nt) {
+          if (t == 0) {
+            if (!wait_thread(sh, kKFull + next, (n + 1) >> 1 & 1, A.err)) return;
+            tc_after();
+          }
+          scores(t, next);
+          if (t + 1 == tiles_of_rows) mma_commit(&sh.bar[kKFree + next]);
+        }
+      }
+    }
+    left -= nt;
+    tile = 0;
+    if (left > 0) next_unit<kManyRows, kTile>(A, u);
+  }
+}
+
+// Rows of tile t of a unit into shared memory (zeros behind the last one).
+template <int D>
+__device__ __forceinline__ void load_q(const AttnArgs& A, const Unit& u, int t, uint32_t q_smem, bool q16) {
+  using M = ManyShape<D>;
+  const int row = threadIdx.x & (kTile - 1), r = u.r0 + t * kTile + row;
+  const int tok = r / A.G, hq = u.hg * A.G + r - tok * A.G;
+  const bf16* src = (const bf16*)A.q + (int64_t)(u.s.q0 + tok) * A.ldq + (int64_t)hq * D;
+  const uint32_t at = q_smem + t * M::TILE + row * 128;
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (r < u.r1) {
+      if (q16) {
+        w = ld_reuse(src + 8 * i);
+      } else {
+        uint32_t v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = reinterpret_cast<const uint16_t*>(src)[8 * i + k];
+        w = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+      }
+    }
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + (i / 8) * M::PLANE + 16 * ((i % 8) ^ (row & 7))), "r"(w.x), "r"(w.y), "r"(w.z),
+                 "r"(w.w)
+                 : "memory");
+  }
+  fence_proxy_async_smem();
+}
+
+// A row's scores -> weights of one step.  s: 32 columns of scores, first key col (of the tile's 128).
+template <bool MASK>
+__device__ __forceinline__ float top_of(const uint32_t (&s)[32], const float* ks, int col, int from, int to, float top) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const float4 k = *reinterpret_cast<const float4*>(ks + col + i);
+    float2 a = mul2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(k.x, k.y));
+    float2 b = mul2(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), make_float2(k.z, k.w));
+    if constexpr (MASK) {
+      if (col + i < from || col + i >= to) a.x = -INFINITY;
+      if (col + i + 1 < from || col + i + 1 >= to) a.y = -INFINITY;
+      if (col + i + 2 < from || col + i + 2 >= to) b.x = -INFINITY;
+      if (col + i + 3 < from || col + i + 3 >= to) b.y = -INFINITY;
+    }
+    top = fmaxf(fmaxf(top, fmaxf(a.x, a.y)), fmaxf(b.x, b.y));
+  }
+  return top;
+}
+template <bool MASK>
+__device__ __forceinline__ void weights_of(const uint32_t (&s)[32], const float* ks, const float* vs, int col, int from, int to, float ref, float2& sum,
+                                           uint32_t (&w)[16]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const float4 k = *reinterpret_cast<const float4*>(ks + col + i), v = *reinterpret_cast<const float4*>(vs + col + i);
+    float2 a = fma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(k.x, k.y), both(-ref));
+    float2 b = fma2(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), make_float2(k.z, k.w), both(-ref));
+    a = make_float2(ex2(a.x), ex2(a.y));
+    b = make_float2(ex2(b.x), ex2(b.y));
+    float2 x = mul2(a, make_float2(v.x, v.y)), y = mul2(b, make_float2(v.z, v.w));
+    if constexpr (MASK) {  // whatever the scales of a key that is not seen
+      if (col + i < from || col + i >= to) a.x = x.x = 0.f;
+      if (col + i + 1 < from || col + i + 1 >= to) a.y = x.y = 0.f;
+      if (col + i + 2 < from || col + i + 2 >= to) b.x = y.x = 0.f;
+      if (col + i + 3 < from || col + i + 3 >= to) b.y = y.y = 0.f;
+    }
+    sum = add2(sum, add2(a, b));
+    w[i / 2] = pack_bf16x2(x.x, x.y);
+    w[i / 2 + 1] = pack_bf16x2(y.x, y.y);
+  }
+}
+
+// The four warps of tile t of rows.
+template <int D>
+__device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t q_smem, int t, bool q16, bool o16) {
+  const int warp = warp_index() & 3, lane = threadIdx.x & 31, row = 32 * warp + lane;
+  const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+  const uint32_t s_at = sh.tmem + t * kTile + lanes, o_at = sh.tmem + 2 * kTile + t * kTile + lanes;
+  Unit u = sh.plan.u;
+  int tile = sh.plan.tile;
+  int64_t x = sh.plan.x0;
+  const int64_t x1 = sh.plan.x1;
+  uint32_t n = 0, rounds = 0, units = 0;
+  bool have_q = false;
+  while (x < x1) {
+    const int nt = (int)min((int64_t)(u.tiles - tile), x1 - x);
+    const bool before = tile > 0, behind = tile + nt < u.tiles;
+    if (u.r0 + t * kTile < u.r1) {
+      if (!have_q) {
+        load_q<D>(A, u, t, q_smem, q16);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.bar[kQFull + t]);
+      }
+      have_q = false;
+      const int r = u.r0 + t * kTile + row, first = u.s.kv - u.s.nq;
+      const int pos = first + min(r, u.r1 - 1) / A.G;
+      const int wr = u.r0 + t * kTile + 32 * warp;  // the warp's rows
+      const int pos_min = first + min(wr, u.r1 - 1) / A.G, pos_max = first + min(wr + 31, u.r1 - 1) / A.G;
+      float m = -INFINITY;
+      float2 sum = make_float2(0.f, 0.f);
+      for (int i = 0; i < nt; ++i, ++rounds) {
+        const uint32_t g = n + i;
+        const int j0 = u.lo + (tile + i) * kTile;
+        if (!wait_warp(sh, kSFull + t, rounds & 1, A.err) || !wait_warp(sh, kVFull + (g & 1), g >> 1 & 1, A.err)) return;
+        tc_after();
+        const float *ks = sh.scale[g & 1][0], *vs = sh.scale[g & 1][1];
+        const bool whole = j0 + kTile <= u.hi && (!A.causal || j0 + kTile - 1 <= pos_min) && (A.window <= 0 || j0 > pos_max - A.window);
+        const int to = min(A.causal ? min(u.hi, pos + 1) : u.hi, j0 + kTile) - j0, from = A.window > 0 ? pos - A.window + 1 - j0 : 0;
+        uint32_t s[32];
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tm_ld32(s, s_at + 32 * c);
+          tm_wait_ld();
+          top = whole ? top_of<false>(s, ks, 32 * c, from, to, top) : top_of<true>(s, ks, 32 * c, from, to, top);
+        }
+        // The reference follows the maximum only when that has grown by more than 2^8 (weights and sums have
+        // room for it): results are seldom rescaled.  The products that wrote them are complete: the
+        // scores' barrier comes after all products issued before.
+        if (__any_sync(0xffffffffu, top > m + 8.f)) {
+          const float up = fmaxf(m, top), f = ex2(m - finite_or_zero(up));
+          m = up;
+          sum = mul2(sum, both(f));
+          if (i > 0) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              tm_ld32(s, o_at + 32 * c);
+              tm_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * f);
+              tm_st32(o_at + 32 * c, s);
+            }
+          }
+        }
+        const float ref = finite_or_zero(m);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
+          tm_ld32(s, s_at + 32 * c);
+          tm_wait_ld();
+          if (whole) weights_of<false>(s, ks, vs, 32 * c, from, to, ref, sum, w);
+          else weights_of<true>(s, ks, vs, 32 * c, from, to, ref, sum, w);
+          tm_st16(s_at + 16 * c, w);
+        }
+        tm_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.bar[kPFull + t]);
+      }
+      // the unit's results; Q's tile is free, its last scores have been read
+      Unit nu = u;
+      if (x + nt < x1 && next_unit<kManyRows, kTile>(A, nu) && nu.r0 + t * kTile < nu.r1) {
+        load_q<D>(A, nu, t, q_smem, q16);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.bar[kQFull + t]);
+        have_q = true;
+      }
+      if (!wait_warp(sh, kOFull + t, units & 1, A.err)) return;
+      ++units;
+      tc_after();
+      const float l = sum.x + sum.y, inv = l == 0.f ? 0.f : 1.f / l;
+      const int tok = r / A.G, hq = u.hg * A.G + r - tok * A.G;
+      const bool split = before || behind;
+      const int64_t at = (int64_t)(2 * blockIdx.x + (before ? 0 : 1)) * kManyRows + t * kTile + row;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t s[32];
+        tm_ld32(s, o_at + 32 * c);
+        tm_wait_ld();
+        if (r >= u.r1) {
+          // nothing to store
+        } else if (split) {
+          float4* dst = reinterpret_cast<float4*>(A.part_o + at * D + 32 * c);
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            dst[k / 4] = make_float4(__uint_as_float(s[k]), __uint_as_float(s[k + 1]), __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
+        } else {
+          bf16* dst = (bf16*)A.out + (int64_t)(u.s.q0 + tok) * A.ldo + (int64_t)hq * D + 32 * c;
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = l == 0.f ? 0.f : __uint_as_float(s[k + e]) * inv;
+            if (o16) {
+              store_n<bf16, 8>(dst + k, v);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) dst[k + e] = __float2bfloat16_rn(v[e]);
+            }
+          }
+        }
+        __syncwarp();  // the next load is the whole warp's
+      }
+      if (r < u.r1) {
+        if (split) *reinterpret_cast<float2*>(A.part_ml + 2 * at) = make_float2(m, l);
+        else if (A.lse) A.lse[(int64_t)(u.s.q0 + tok) * A.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      }
+      tc_before();
+    }
+    if (t == 0 && behind && !before && row == 0) {  // the first part of a unit that others continue
+      int* f = A.info + blockIdx.x * kAttnInfo;
+      f[1] = u.b;
+      f[2] = u.blk;
+      f[3] = u.hg;
+      f[0] = parts_behind(sh.plan, x + (u.tiles - 1 - tile));
+    }
+    n += nt;
+    x += nt;
+    tile = 0;
+    if (x < x1) next_unit<kManyRows, kTile>(A, u);
+  }
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kManyThreads, 1) attn8_many(const __grid_constant__ AttnArgs A, bool q16, bool o16) {
+  using M = ManyShape<D>;
+  extern __shared__ uint8_t many_smem[];
+  __shared__ Shared sh;
+  launch_dependents();
+  const int warp = warp_index();
+  const uint32_t q_smem = (smem_addr(many_smem) + 1023u) & ~1023u, kv_smem = q_smem + 2 * M::TILE;
+  if (threadIdx.x == 0) {
+    sh.stop = 0;
+    for (int i = 0; i < kBars; ++i) {
+      const bool conv = i < kKFree || (i >= kVFull && i < kVFree);                  // a converting warp each
+      const bool rows = (i >= kQFull && i < kSFull) || (i >= kPFull && i < kOFull);  // a warp of the tile each
+      mbar_init(&sh.bar[i], conv ? kConvWarps : rows ? 4 : 1);
+    }
+    mbar_init_fence();
+    A.info[blockIdx.x * kAttnInfo] = -1;
+  }
+  if (warp == 0) {
+    Part p;
+    plan_part<kManyRows, kTile>(A, p);
+    if ((threadIdx.x & 31) == 0) sh.plan = p;
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (sh.plan.x0 < sh.plan.x1) {
+    if (warp < 8) {
+      softmax<D>(A, sh, q_smem, warp >> 2, q16, o16);
+    } else if (warp < 8 + kConvWarps) {
+      convert<D, FMT>(A, sh, kv_smem, warp - 8);
+    } else if ((threadIdx.x & 31) == 0) {
+      products<D>(A, sh, q_smem, kv_smem);
+      if (*(volatile int*)&sh.stop) {  // given up: what is in flight ends before the memory is given back
+        __shared__ uint64_t last;
+        mbar_init(&last, 1);
+        mbar_init_fence();
+        mma_commit(&last);
+        mbar_wait(&last, 0, kWaitPolls);
+      }
+    }
+  }
+  __syncwarp();
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sh.tmem) : "memory");
+}
+
+template <int D, int FMT>
+gbln_status many_go(const AttnArgs& A, int blocks, bool q16, bool o16, cudaStream_t s) {
+  using M = ManyShape<D>;
+  static std::atomic<uint64_t> ready{0};  // devices whose limit is raised
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return GBLN_ERR_CUDA;
+  if (!(ready.load(std::memory_order_acquire) >> dev & 1)) {
+    if (cudaFuncSetAttribute(attn8_many<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, M::SMEM) != cudaSuccess) {
+      cudaGetLastError();
+      return GBLN_ERR_CUDA;
+    }
+    ready.fetch_or(1ull << dev, std::memory_order_release);
+  }
+  attn8_many<D, FMT><<<blocks, kManyThreads, M::SMEM, s>>>(A, q16, o16);
+  return cudaGetLastError() == cudaSuccess ? attn_join_launch(A, blocks, kManyRows, s) : GBLN_ERR_CUDA;
+}
+
+template <int FMT>
+gbln_status many_typed(const AttnArgs& A, int blocks, bool q16, bool o16, cudaStream_t s) {
+  return A.D == 64 ? many_go<64, FMT>(A, blocks, q16, o16, s) : A.D == 96 ? many_go<96, FMT>(A, blocks, q16, o16, s) : many_go<128, FMT>(A, blocks, q16, o16, s);
+}
+
+}  // namespace
+
+gbln_status attn_many_launch(const AttnArgs& A, int blocks, int fmt, cudaStream_t s) {
+  const bool q16 = aligned16(A.q) && A.ldq % 8 == 0, o16 = aligned16(A.out) && A.ldo % 8 == 0;
+  return fmt == GBLN_Q8_INT8 ? many_typed<GBLN_Q8_INT8>(A, blocks, q16, o16, s) : many_typed<GBLN_Q8_E4M3>(A, blocks, q16, o16, s);
+}
+
+}  // namespace gbln
