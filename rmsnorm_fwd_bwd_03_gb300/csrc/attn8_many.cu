@@ -13,6 +13,8 @@
 // While one tile's weights are computed, the other's products run.  Tensor memory: S_0, S_1,
 // O_0, O_1, 128 columns each, all 512.
 
+#include <climits>
+
 #include <atomic>
 
 #include "attn8.cuh"
@@ -26,7 +28,10 @@ constexpr int kManyRows = 2 * kTile;    // rows of a unit
 static_assert(kManyRows == kManyUnit, "the joining kernel knows it too");
 constexpr int kConvWarps = 4;                    // one per scheduler
 constexpr int kConvRows = kTile / kConvWarps / 8;  // keys of a converting thread
-constexpr int kManyThreads = 32 * (8 + kConvWarps + 1);
+constexpr int kManyThreads = 512;      // four groups of four warps: rows, rows, conversion, products
+// Registers of a thread in each group; together what the block is launched with (512 x 128).
+constexpr int kRegsRows = 176, kRegsConv = 96, kRegsMma = 64;
+static_assert(2 * kRegsRows + kRegsConv + kRegsMma <= 4 * 128, "a larger sum would wait forever");
 
 template <int D>
 struct ManyShape {
@@ -43,15 +48,19 @@ struct Shared {
   uint64_t bar[kBars];
   __align__(16) float scale[2][2][kTile];  // [stage][K times the softmax scale, V][key]
   Part plan;
+  Unit now[1 + kConvWarps];  // where the products and each converting warp are: their registers are short
   uint32_t tmem;
   int stop;
 };
 
 // --- tcgen05 ---------------------------------------------------------------
-// Shared memory matrix descriptor: 128-byte swizzle, start, leading and stride byte offsets.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
-  return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 | 1ull << 46 | 2ull << 61;
+// Shared memory matrix descriptor: 128-byte swizzle, eight rows of 128 bytes 1024 apart; the start and the
+// leading offset in the low word, which steps through a tile by bytes / 16.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t low) {
+  constexpr uint32_t high = (1024 >> 4) | 1u << 14 | 2u << 29;
+  return (uint64_t)high << 32 | low;
 }
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lead) { return (addr >> 4) | (lead >> 4) << 16; }
 // Instruction descriptor: bf16 x bf16 + float32, M = 128, N = n; B with its N values contiguous where `nmajor`.
 constexpr uint32_t inst_desc(int n, bool nmajor) {
   return 1u << 4 | 1u << 7 | 1u << 10 | (nmajor ? 1u << 16 : 0u) | (uint32_t)(n / 8) << 17 | (uint32_t)(kTile / 16) << 24;
@@ -83,17 +92,23 @@ __device__ __forceinline__ void tm_ld32(uint32_t (&v)[32], uint32_t at) {
       : GBLN_R8(v, 0), GBLN_R8(v, 8), GBLN_R8(v, 16), GBLN_R8(v, 24)
       : "r"(at));
 }
-__device__ __forceinline__ void tm_st32(uint32_t at, const uint32_t (&v)[32]) {
+__device__ __forceinline__ void tm_ld16(uint32_t (&v)[16], uint32_t at) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
-      "%24,%25,%26,%27,%28,%29,%30,%31};" ::GBLN_W8(v, 0), GBLN_W8(v, 8), GBLN_W8(v, 16), GBLN_W8(v, 24), "r"(at)
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : GBLN_R8(v, 0), GBLN_R8(v, 8)
+      : "r"(at));
 }
 __device__ __forceinline__ void tm_st16(uint32_t at, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::GBLN_W8(v, 0), GBLN_W8(v, 8),
       "r"(at)
       : "memory");
+}
+
+// A value that is not computed ahead of its place: all descriptors of a tile at once spill.
+__device__ __forceinline__ uint32_t here(uint32_t v) {
+  asm volatile("" : "+r"(v));
+  return v;
 }
 
 // Bounded wait of a whole warp (or of one thread alone); false once any wait of the block has run out.
@@ -143,21 +158,6 @@ __device__ __forceinline__ void store_codes(uint32_t plane, int row, int c, uint
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + 16 * ((2 * c + 1) ^ (row & 7))), "r"(e.x), "r"(e.y), "r"(f.x), "r"(f.y) : "memory");
 }
 
-struct KeyPage {
-  int page;  // -1: none, -2: outside the cache
-  uint32_t off;
-};
-__device__ __forceinline__ KeyPage page_at(const AttnArgs& A, int b, int j, int hi) {
-  KeyPage k{-1, 0};
-  if (j < hi) {
-    uint32_t p;
-    A.page.split((uint32_t)j, p, k.off);
-    k.page = __ldg(A.pages + (int64_t)b * A.max_pages + p);
-    if (k.page < 0 || k.page >= A.n_pages) k.page = -2;
-  }
-  return k;
-}
-
 // The warps that bring K and V in.  Lane (r, c) = (lane / 4, lane % 4) of warp w has the chunks c, c + 4
 // (16 codes each) of keys 32 w + r, + 8, + 16, + 24: a store instruction's eight lanes at a time hit all banks.
 // Each tile's codes are on their way while the tile before is converted.
@@ -167,53 +167,79 @@ __device__ __forceinline__ void convert(const AttnArgs& A, Shared& sh, uint32_t 
   constexpr int NP = M::PLANES;
   const int lane = threadIdx.x & 31, c = lane & 3;
   const int row = 8 * kConvRows * w + (lane >> 2);  // + 8 i
-  Unit u = sh.plan.u;
-  int tile = sh.plan.tile;
   const int64_t n_tiles = sh.plan.x1 - sh.plan.x0;
-  KeyPage kp[kConvRows];
-  int h = 0;
+  // The cursor runs two tiles ahead: a tile's pages are looked up while the codes of the one before it are on
+  // their way and the one before that is converted.
+  Unit& u = sh.now[1 + w];
+  if (lane == 0) u = sh.plan.u;
+  __syncwarp();
+  int tile = sh.plan.tile;
+  int64_t ahead = 0;
+  int lo = u.lo, hi = u.hi, tiles = u.tiles, hg = u.hg;
+  const int32_t* row_of = A.pages + (int64_t)u.b * A.max_pages;
+  int page[kConvRows], h = 0;  // of the tile looked up last; -1: no key, -2: outside the cache
+  uint32_t off[kConvRows];
   uint4 kr[kConvRows][NP], vr[kConvRows][NP];
   float sc[kConvRows];
-  const auto pages = [&]() {
+  const auto look_up = [&]() {  // the pages of the cursor's tile; the cursor moves on
+    if (ahead >= n_tiles) return;
 #pragma unroll
     for (int i = 0; i < kConvRows; ++i) {
-      kp[i] = page_at(A, u.b, u.lo + tile * kTile + row + 8 * i, u.hi);
-      if (kp[i].page == -2) atomicOr(A.err, kErrBadSlot);
+      const int j = lo + tile * kTile + row + 8 * i;
+      uint32_t q;
+      A.page.split((uint32_t)j, q, off[i]);
+      page[i] = j < hi ? __ldg(row_of + q) : INT_MIN;
     }
-    h = u.hg;
+    h = hg;
+    if (++ahead < n_tiles && ++tile == tiles) {
+      tile = 0;
+      __syncwarp();
+      if (lane == 0) next_unit<kManyRows, kTile>(A, u);
+      __syncwarp();
+      lo = u.lo;
+      hi = u.hi;
+      tiles = u.tiles;
+      hg = u.hg;
+      row_of = A.pages + (int64_t)u.b * A.max_pages;
+    }
+  };
+  const auto place = [&]() {
+#pragma unroll
+    for (int i = 0; i < kConvRows; ++i) {
+      if (page[i] == INT_MIN) {
+        page[i] = -1;
+      } else if (page[i] < 0 || page[i] >= A.n_pages) {
+        page[i] = -2;
+        atomicOr(A.err, kErrBadSlot);
+      }
+    }
   };
   const auto fetch = [&](const Cache& C, uint4 (&r)[kConvRows][NP]) {
 #pragma unroll
     for (int i = 0; i < kConvRows; ++i) {
-      const uint8_t* src = C.q + C.cq.at(max(kp[i].page, 0), kp[i].off, h) + 16 * c;
+      const uint8_t* src = C.q + C.cq.at(max(page[i], 0), off[i], h) + 16 * c;
 #pragma unroll
       for (int p = 0; p < NP; ++p)
-        r[i][p] = kp[i].page >= 0 && 64 * p + 16 * c < D ? ld_stream(src + 64 * p) : make_uint4(0, 0, 0, 0);
+        r[i][p] = page[i] >= 0 && 64 * p + 16 * c < D ? ld_stream(src + 64 * p) : make_uint4(0, 0, 0, 0);
     }
   };
-  const auto scales = [&]() {
-    const Cache& C = c == 0 ? A.K : A.V;
+  const auto scales = [&]() {  // of K for c = 0, of V for c = 1
 #pragma unroll
     for (int i = 0; i < kConvRows; ++i) {
-      sc[i] = kp[i].page == -2 ? __int_as_float(0x7fc00000) : 0.f;
-      if (c < 2 && kp[i].page >= 0) sc[i] = __ldg(C.sc + C.cs.at(kp[i].page, kp[i].off, h)) * (c == 0 ? A.scale2 : 1.f);
+      sc[i] = page[i] == -2 ? __int_as_float(0x7fc00000) : 0.f;
+      if (c < 2 && page[i] >= 0) sc[i] = c == 0 ? __ldg(A.K.sc + A.K.cs.at(page[i], off[i], h)) : __ldg(A.V.sc + A.V.cs.at(page[i], off[i], h));
     }
   };
-  pages();
+  look_up();
+  place();
   fetch(A.K, kr);
   fetch(A.V, vr);
   scales();
+  look_up();
   for (int64_t n = 0; n < n_tiles; ++n) {
     const int st = (int)(n & 1);
     const uint32_t again = (uint32_t)(n >> 1 & 1) ^ 1u;
     const bool more = n + 1 < n_tiles;
-    if (more) {
-      if (++tile == u.tiles) {
-        tile = 0;
-        next_unit<kManyRows, kTile>(A, u);
-      }
-      pages();
-    }
     if (!wait_warp(sh, kKFree + st, again, A.err)) return;
     const uint32_t ks = kv_smem + st * M::TILE, vs = kv_smem + (2 + st) * M::TILE;
 #pragma unroll
@@ -223,13 +249,16 @@ __device__ __forceinline__ void convert(const AttnArgs& A, Shared& sh, uint32_t 
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.bar[kKFull + st]);
-    if (more) fetch(A.K, kr);
+    if (more) {
+      place();
+      fetch(A.K, kr);
+    }
     if (!wait_warp(sh, kVFree + st, again, A.err)) return;
 #pragma unroll
     for (int i = 0; i < kConvRows; ++i) {
 #pragma unroll
       for (int p = 0; p < NP; ++p) store_codes<FMT>(vs + p * M::PLANE, row + 8 * i, c, vr[i][p]);
-      if (c < 2) sh.scale[st][c][row + 8 * i] = sc[i];
+      if (c < 2) sh.scale[st][c][row + 8 * i] = c == 0 ? sc[i] * A.scale2 : sc[i];
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -237,6 +266,7 @@ __device__ __forceinline__ void convert(const AttnArgs& A, Shared& sh, uint32_t 
     if (more) {
       fetch(A.V, vr);
       scales();
+      look_up();
     }
   }
 }
@@ -247,43 +277,46 @@ __device__ __forceinline__ void products(const AttnArgs& A, Shared& sh, uint32_t
   using M = ManyShape<D>;
   constexpr uint32_t QK = inst_desc(kTile, false), PV = inst_desc(D, true);
   const uint32_t tm = sh.tmem;
-  Unit u = sh.plan.u;
+  Unit& u = sh.now[0];
+  u = sh.plan.u;
   int tile = sh.plan.tile;
   int64_t left = sh.plan.x1 - sh.plan.x0;
   uint32_t n = 0;            // tiles so far
-  uint32_t rounds[2] = {0, 0};  // weights of each tile of rows so far
-  uint32_t units[2] = {0, 0};
+  uint32_t rounds = 0, units = 0;  // parities of the weights and of Q, bit t for tile t of rows
   const auto scores = [&](int t, uint32_t st) {
-    const uint32_t q = q_smem + t * M::TILE, k = kv_smem + st * M::TILE;
+    const uint32_t q = here(desc_low(q_smem + t * M::TILE, 16)), k = here(desc_low(kv_smem + st * M::TILE, 16));
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
-      const uint32_t at = (i / 4) * M::PLANE + (i % 4) * 32;
-      mma_ss(tm + t * kTile, smem_desc(q + at, 16, 1024), smem_desc(k + at, 16, 1024), QK, i > 0);
+      const uint32_t at = ((i / 4) * M::PLANE + (i % 4) * 32) >> 4;
+      mma_ss(tm + t * kTile, smem_desc(q + at), smem_desc(k + at), QK, i > 0);
     }
     mma_commit(&sh.bar[kSFull + t]);
   };
   const auto results = [&](int t, uint32_t st, bool add) {
-    const uint32_t v = kv_smem + (2 + st) * M::TILE;
+    const uint32_t v = here(desc_low(kv_smem + (2 + st) * M::TILE, M::PLANE));
 #pragma unroll
     for (int i = 0; i < kTile / 16; ++i)  // 16 keys: 16 rows of 128 bytes, 8 columns of weights
-      mma_ts(tm + 2 * kTile + t * kTile, tm + t * kTile + 8 * i, smem_desc(v + i * 2048, M::PLANE, 1024), PV, add || i > 0);
+      mma_ts(tm + 2 * kTile + t * kTile, tm + t * kTile + 8 * i, smem_desc(v + (i * 2048 >> 4)), PV, add || i > 0);
   };
   while (left > 0) {
     const int nt = (int)min((int64_t)(u.tiles - tile), left), tiles_of_rows = u.r1 - u.r0 > kTile ? 2 : 1;
+#pragma unroll 1
     for (int t = 0; t < tiles_of_rows; ++t) {
-      if (!wait_thread(sh, kQFull + t, units[t] & 1, A.err)) return;
-      ++units[t];
+      if (!wait_thread(sh, kQFull + t, units >> t & 1, A.err)) return;
+      units ^= 1u << t;
       if (t == 0 && !wait_thread(sh, kKFull + (n & 1), n >> 1 & 1, A.err)) return;
       tc_after();
       scores(t, n & 1);
     }
     mma_commit(&sh.bar[kKFree + (n & 1)]);
+#pragma unroll 1
     for (int i = 0; i < nt; ++i, ++n) {
       const uint32_t st = n & 1, next = (n + 1) & 1;
       if (!wait_thread(sh, kVFull + st, n >> 1 & 1, A.err)) return;
+#pragma unroll 1
       for (int t = 0; t < tiles_of_rows; ++t) {
-        if (!wait_thread(sh, kPFull + t, rounds[t] & 1, A.err)) return;
-        ++rounds[t];
+        if (!wait_thread(sh, kPFull + t, rounds >> t & 1, A.err)) return;
+        rounds ^= 1u << t;
         tc_after();
         results(t, st, i > 0);
         if (i + 1 == nt) mma_commit(&sh.bar[kOFull + t]);
@@ -332,9 +365,9 @@ __device__ __forceinline__ void load_q(const AttnArgs& A, const Unit& u, int t, 
   fence_proxy_async_smem();
 }
 
-// A row's scores -> weights of one step.  s: 32 columns of scores, first key col (of the tile's 128).
+// A row's scores, 32 columns from key col of the tile on: times K's scales, those not seen -infinity.
 template <bool MASK>
-__device__ __forceinline__ float top_of(const uint32_t (&s)[32], const float* ks, int col, int from, int to, float top) {
+__device__ __forceinline__ float scaled(uint32_t (&s)[32], const float* ks, int col, int from, int to, float top) {
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
     const float4 k = *reinterpret_cast<const float4*>(ks + col + i);
@@ -346,28 +379,32 @@ __device__ __forceinline__ float top_of(const uint32_t (&s)[32], const float* ks
       if (col + i + 2 < from || col + i + 2 >= to) b.x = -INFINITY;
       if (col + i + 3 < from || col + i + 3 >= to) b.y = -INFINITY;
     }
+    s[i] = __float_as_uint(a.x);
+    s[i + 1] = __float_as_uint(a.y);
+    s[i + 2] = __float_as_uint(b.x);
+    s[i + 3] = __float_as_uint(b.y);
     top = fmaxf(fmaxf(top, fmaxf(a.x, a.y)), fmaxf(b.x, b.y));
   }
   return top;
 }
+// Their weights times V's scales, in bf16; sum takes the weights.
 template <bool MASK>
-__device__ __forceinline__ void weights_of(const uint32_t (&s)[32], const float* ks, const float* vs, int col, int from, int to, float ref, float2& sum,
-                                           uint32_t (&w)[16]) {
+__device__ __forceinline__ void weights_of(const uint32_t (&s)[32], const float* vs, int col, int from, int to, float ref, float2& sum, uint32_t (&w)[16]) {
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
-    const float4 k = *reinterpret_cast<const float4*>(ks + col + i), v = *reinterpret_cast<const float4*>(vs + col + i);
-    float2 a = fma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(k.x, k.y), both(-ref));
-    float2 b = fma2(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), make_float2(k.z, k.w), both(-ref));
+    const float4 v = *reinterpret_cast<const float4*>(vs + col + i);
+    float2 a = add2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), both(-ref));
+    float2 b = add2(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), both(-ref));
     a = make_float2(ex2(a.x), ex2(a.y));
     b = make_float2(ex2(b.x), ex2(b.y));
-    float2 x = mul2(a, make_float2(v.x, v.y)), y = mul2(b, make_float2(v.z, v.w));
-    if constexpr (MASK) {  // whatever the scales of a key that is not seen
-      if (col + i < from || col + i >= to) a.x = x.x = 0.f;
-      if (col + i + 1 < from || col + i + 1 >= to) a.y = x.y = 0.f;
-      if (col + i + 2 < from || col + i + 2 >= to) b.x = y.x = 0.f;
-      if (col + i + 3 < from || col + i + 3 >= to) b.y = y.y = 0.f;
-    }
     sum = add2(sum, add2(a, b));
+    float2 x = mul2(a, make_float2(v.x, v.y)), y = mul2(b, make_float2(v.z, v.w));
+    if constexpr (MASK) {  // whatever the scale of a key that is not seen
+      if (col + i < from || col + i >= to) x.x = 0.f;
+      if (col + i + 1 < from || col + i + 1 >= to) x.y = 0.f;
+      if (col + i + 2 < from || col + i + 2 >= to) y.x = 0.f;
+      if (col + i + 3 < from || col + i + 3 >= to) y.y = 0.f;
+    }
     w[i / 2] = pack_bf16x2(x.x, x.y);
     w[i / 2 + 1] = pack_bf16x2(y.x, y.y);
   }
@@ -409,13 +446,17 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
         const float *ks = sh.scale[g & 1][0], *vs = sh.scale[g & 1][1];
         const bool whole = j0 + kTile <= u.hi && (!A.causal || j0 + kTile - 1 <= pos_min) && (A.window <= 0 || j0 > pos_max - A.window);
         const int to = min(A.causal ? min(u.hi, pos + 1) : u.hi, j0 + kTile) - j0, from = A.window > 0 ? pos - A.window + 1 - j0 : 0;
-        uint32_t s[32];
+        uint32_t s[4][32];
         float top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tm_ld32(s, s_at + 32 * c);
-          tm_wait_ld();
-          top = whole ? top_of<false>(s, ks, 32 * c, from, to, top) : top_of<true>(s, ks, 32 * c, from, to, top);
+        for (int c = 0; c < 4; ++c) tm_ld32(s[c], s_at + 32 * c);
+        tm_wait_ld();
+        if (whole) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) top = scaled<false>(s[c], ks, 32 * c, from, to, top);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) top = scaled<true>(s[c], ks, 32 * c, from, to, top);
         }
         // The reference follows the maximum only when that has grown by more than 2^8 (weights and sums have
         // room for it): results are seldom rescaled.  The products that wrote them are complete: the
@@ -426,12 +467,13 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
           sum = mul2(sum, both(f));
           if (i > 0) {
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              tm_ld32(s, o_at + 32 * c);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tm_ld16(o, o_at + 16 * c);
               tm_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * f);
-              tm_st32(o_at + 32 * c, s);
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tm_st16(o_at + 16 * c, o);
             }
           }
         }
@@ -439,10 +481,8 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t w[16];
-          tm_ld32(s, s_at + 32 * c);
-          tm_wait_ld();
-          if (whole) weights_of<false>(s, ks, vs, 32 * c, from, to, ref, sum, w);
-          else weights_of<true>(s, ks, vs, 32 * c, from, to, ref, sum, w);
+          if (whole) weights_of<false>(s[c], vs, 32 * c, from, to, ref, sum, w);
+          else weights_of<true>(s[c], vs, 32 * c, from, to, ref, sum, w);
           tm_st16(s_at + 16 * c, w);
         }
         tm_wait_st();
@@ -546,17 +586,22 @@ __global__ void __launch_bounds__(kManyThreads, 1) attn8_many(const __grid_const
   tc_after();
   if (sh.plan.x0 < sh.plan.x1) {
     if (warp < 8) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
       softmax<D>(A, sh, q_smem, warp >> 2, q16, o16);
-    } else if (warp < 8 + kConvWarps) {
+    } else if (warp < 12) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
       convert<D, FMT>(A, sh, kv_smem, warp - 8);
-    } else if ((threadIdx.x & 31) == 0) {
-      products<D>(A, sh, q_smem, kv_smem);
-      if (*(volatile int*)&sh.stop) {  // given up: what is in flight ends before the memory is given back
-        __shared__ uint64_t last;
-        mbar_init(&last, 1);
-        mbar_init_fence();
-        mma_commit(&last);
-        mbar_wait(&last, 0, kWaitPolls);
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
+      if (threadIdx.x == 32 * 12) {
+        products<D>(A, sh, q_smem, kv_smem);
+        if (*(volatile int*)&sh.stop) {  // given up: what is in flight ends before the memory is given back
+          __shared__ uint64_t last;
+          mbar_init(&last, 1);
+          mbar_init_fence();
+          mma_commit(&last);
+          mbar_wait(&last, 0, kWaitPolls);
+        }
       }
     }
   }
