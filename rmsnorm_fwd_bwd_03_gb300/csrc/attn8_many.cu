@@ -4,14 +4,15 @@
 //
 // A block takes 256 rows (new tokens x heads of a group) of one K/V head as two tiles of
 // 128, and 128 keys at a time:
-//   * four warps fetch codes, turn them into bf16 (exactly) and lay K and V in shared
+//   * eight warps fetch codes, turn them into bf16 (exactly) and lay K and V in shared
 //     memory, in the 128-byte swizzle that the tensor cores read;
-//   * one thread issues the products (tcgen05): S_t = Q_t K^T into tensor memory, later
+//   * a thread per tile issues the products (tcgen05): S_t = Q_t K^T into tensor memory, later
 //     O_t += P_t V with P_t read from tensor memory;
 //   * four warps per tile turn S_t into P_t, a thread per row: no shuffles, and the row's
 //     maximum, sum and rescaling stay in its registers.  P_t overwrites S_t.
-// While one tile's weights are computed, the other's products run.  Tensor memory: S_0, S_1,
-// O_0, O_1, 128 columns each, all 512.
+// A tile's scores come 64 keys at a time into two places in turn: while one step's weights are
+// computed, the products of the next step's scores and of the other tile run.  Tensor memory:
+// the two tiles' scores, 2 x 64 columns each, and O_0, O_1, 128 columns each: all 512.
 
 #include <climits>
 
@@ -23,15 +24,16 @@ namespace gbln {
 
 namespace {
 
-constexpr int kTile = 128;              // rows of a tile, keys of a step
+constexpr int kTile = 128;              // rows of a tile, keys that are fetched at a time
+constexpr int kHalf = kTile / 2;        // keys of a step
 constexpr int kManyRows = 2 * kTile;    // rows of a unit
 static_assert(kManyRows == kManyUnit, "the joining kernel knows it too");
-constexpr int kConvWarps = 4;                    // one per scheduler
+constexpr int kConvWarps = 8;
 constexpr int kConvRows = kTile / kConvWarps / 8;  // keys of a converting thread
-constexpr int kManyThreads = 512;      // four groups of four warps: rows, rows, conversion, products
-// Registers of a thread in each group; together what the block is launched with (512 x 128).
-constexpr int kRegsRows = 176, kRegsConv = 96, kRegsMma = 64;
-static_assert(2 * kRegsRows + kRegsConv + kRegsMma <= 4 * 128, "a larger sum would wait forever");
+constexpr int kManyThreads = 640;      // five groups of four warps: rows twice, conversion twice, products
+// Registers of a thread in each group; together what the block is launched with (640 x 96).
+constexpr int kRegsRows = 120, kRegsConv = 72, kRegsMma = 96;
+static_assert(2 * kRegsRows + 2 * kRegsConv + kRegsMma <= 5 * 96, "a larger sum would wait forever");
 
 template <int D>
 struct ManyShape {
@@ -41,14 +43,14 @@ struct ManyShape {
   static constexpr int SMEM = 6 * TILE + 1024;      // Q_0, Q_1, two stages of K and of V; alignment
 };
 
-// Barriers of a block.
-enum { kKFull = 0, kKFree = 2, kVFull = 4, kVFree = 6, kQFull = 8, kSFull = 10, kPFull = 12, kOFull = 14, kBars = 16 };
+// Barriers of a block: K and V per stage, Q and results per tile of rows, scores and weights per tile and place.
+enum { kKFull = 0, kKFree = 2, kVFull = 4, kVFree = 6, kQFull = 8, kODone = 10, kSFull = 12, kPFull = 16, kBars = 20 };
 
 struct Shared {
-  uint64_t bar[kBars];
+  uint64_t bar[kBars], last[2];
   __align__(16) float scale[2][2][kTile];  // [stage][K times the softmax scale, V][key]
   Part plan;
-  Unit now[1 + kConvWarps];  // where the products and each converting warp are: their registers are short
+  Unit now[2 + kConvWarps];  // where the threads of the products and each converting warp are: their registers are short
   uint32_t tmem;
   int stop;
 };
@@ -159,7 +161,7 @@ __device__ __forceinline__ void store_codes(uint32_t plane, int row, int c, uint
 }
 
 // The warps that bring K and V in.  Lane (r, c) = (lane / 4, lane % 4) of warp w has the chunks c, c + 4
-// (16 codes each) of keys 32 w + r, + 8, + 16, + 24: a store instruction's eight lanes at a time hit all banks.
+// (16 codes each) of keys 16 w + r and 16 w + r + 8: a store instruction's eight lanes at a time hit all banks.
 // Each tile's codes are on their way while the tile before is converted.
 template <int D, int FMT>
 __device__ __forceinline__ void convert(const AttnArgs& A, Shared& sh, uint32_t kv_smem, int w) {
@@ -170,7 +172,7 @@ __device__ __forceinline__ void convert(const AttnArgs& A, Shared& sh, uint32_t 
   const int64_t n_tiles = sh.plan.x1 - sh.plan.x0;
   // The cursor runs two tiles ahead: a tile's pages are looked up while the codes of the one before it are on
   // their way and the one before that is converted.
-  Unit& u = sh.now[1 + w];
+  Unit& u = sh.now[2 + w];
   if (lane == 0) u = sh.plan.u;
   __syncwarp();
   int tile = sh.plan.tile;
@@ -271,67 +273,76 @@ __device__ __forceinline__ void convert(const AttnArgs& A, Shared& sh, uint32_t 
   }
 }
 
-// The thread that issues the products.
+// Steps of the block's tiles tile .. tile + nt - 1 of a unit: the last tile may end in its first half.
+__device__ __forceinline__ int steps_of(const Unit& u, int tile, int nt) {
+  return 2 * nt - (tile + nt == u.tiles && u.hi - u.lo - (u.tiles - 1) * kTile <= kHalf ? 1 : 0);
+}
+
+// The thread that issues the products of tile t of rows, one for each tile: neither's waits hold up the other's
+// products.  A step's results, then the scores of the step after the next, which take its place.
 template <int D>
-__device__ __forceinline__ void products(const AttnArgs& A, Shared& sh, uint32_t q_smem, uint32_t kv_smem) {
+__device__ __forceinline__ void products(const AttnArgs& A, Shared& sh, uint32_t q_smem, uint32_t kv_smem, int t) {
   using M = ManyShape<D>;
-  constexpr uint32_t QK = inst_desc(kTile, false), PV = inst_desc(D, true);
-  const uint32_t tm = sh.tmem;
-  Unit& u = sh.now[0];
+  constexpr uint32_t QK = inst_desc(kHalf, false), PV = inst_desc(D, true);
+  const uint32_t s_at = sh.tmem + t * kTile, o_at = sh.tmem + 2 * kTile + t * kTile;
+  const uint32_t q_low = desc_low(q_smem + t * M::TILE, 16), k_low = desc_low(kv_smem, 16), v_low = desc_low(kv_smem + 2 * M::TILE, M::PLANE);
+  Unit& u = sh.now[t];
   u = sh.plan.u;
   int tile = sh.plan.tile;
   int64_t left = sh.plan.x1 - sh.plan.x0;
-  uint32_t n = 0;            // tiles so far
-  uint32_t rounds = 0, units = 0;  // parities of the weights and of Q, bit t for tile t of rows
-  const auto scores = [&](int t, uint32_t st) {
-    const uint32_t q = here(desc_low(q_smem + t * M::TILE, 16)), k = here(desc_low(kv_smem + st * M::TILE, 16));
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      const uint32_t at = ((i / 4) * M::PLANE + (i % 4) * 32) >> 4;
-      mma_ss(tm + t * kTile, smem_desc(q + at), smem_desc(k + at), QK, i > 0);
-    }
-    mma_commit(&sh.bar[kSFull + t]);
-  };
-  const auto results = [&](int t, uint32_t st, bool add) {
-    const uint32_t v = here(desc_low(kv_smem + (2 + st) * M::TILE, M::PLANE));
-#pragma unroll
-    for (int i = 0; i < kTile / 16; ++i)  // 16 keys: 16 rows of 128 bytes, 8 columns of weights
-      mma_ts(tm + 2 * kTile + t * kTile, tm + t * kTile + 8 * i, smem_desc(v + (i * 2048 >> 4)), PV, add || i > 0);
-  };
+  uint32_t n0 = 0;      // tiles of keys before the unit
+  uint32_t rs = 0, rp = 0;  // steps whose scores, and whose results, have been issued
+  uint32_t units = 0;
   while (left > 0) {
-    const int nt = (int)min((int64_t)(u.tiles - tile), left), tiles_of_rows = u.r1 - u.r0 > kTile ? 2 : 1;
+    const int nt = (int)min((int64_t)(u.tiles - tile), left);
+    if (u.r0 + t * kTile < u.r1) {
+      const int steps = steps_of(u, tile, nt);
+      if (!wait_thread(sh, kQFull + t, units & 1, A.err)) return;
+      ++units;
 #pragma unroll 1
-    for (int t = 0; t < tiles_of_rows; ++t) {
-      if (!wait_thread(sh, kQFull + t, units >> t & 1, A.err)) return;
-      units ^= 1u << t;
-      if (t == 0 && !wait_thread(sh, kKFull + (n & 1), n >> 1 & 1, A.err)) return;
-      tc_after();
-      scores(t, n & 1);
-    }
-    mma_commit(&sh.bar[kKFree + (n & 1)]);
-#pragma unroll 1
-    for (int i = 0; i < nt; ++i, ++n) {
-      const uint32_t st = n & 1, next = (n + 1) & 1;
-      if (!wait_thread(sh, kVFull + st, n >> 1 & 1, A.err)) return;
-#pragma unroll 1
-      for (int t = 0; t < tiles_of_rows; ++t) {
-        if (!wait_thread(sh, kPFull + t, rounds >> t & 1, A.err)) return;
-        rounds ^= 1u << t;
-        tc_after();
-        results(t, st, i > 0);
-        if (i + 1 == nt) mma_commit(&sh.bar[kOFull + t]);
-        if (t + 1 == tiles_of_rows) mma_commit(&sh.bar[kVFree + st]);
-        if (i + 1 < nt) {
-          if (t == 0) {
-            if (!wait_thread(sh, kKFull + next, (n + 1) >> 1 & 1, A.err)) return;
-            tc_after();
-          }
-          scores(t, next);
-          if (t + 1 == tiles_of_rows) mma_commit(&sh.bar[kKFree + next]);
+      for (int j = -2; j < steps; ++j) {
+        const uint32_t n = n0 + (j >> 1), st = n & 1, half = j & 1, ns = n + 1, sst = ns & 1;  // step j + 2 is of tile n + 1
+        const bool s_on = j + 2 < steps;
+        if (j >= 0) {
+          if (half == 0 && !wait_thread(sh, kVFull + st, n >> 1 & 1, A.err)) return;
+          const uint32_t b = rp & 1;
+          if (!wait_thread(sh, kPFull + 2 * t + b, rp >> 1 & 1, A.err)) return;
+          ++rp;
+          tc_after();
+          const uint32_t v = here(v_low + ((st * M::TILE + half * kHalf * 128) >> 4)), w = here(s_at + b * kHalf);
+#pragma unroll
+          for (int i = 0; i < kHalf / 16; ++i)  // 16 keys: 16 rows of 128 bytes, 8 columns of weights
+            mma_ts(o_at, w + 8 * i, smem_desc(v + (i * 2048 >> 4)), PV, j > 0 || i > 0);
+          if (half == 1 || j + 1 == steps) mma_commit(&sh.bar[kVFree + st]);
         }
+        if (s_on) {
+          if (half == 0 && !wait_thread(sh, kKFull + sst, ns >> 1 & 1, A.err)) return;
+          tc_after();
+          const uint32_t b = rs & 1;
+          ++rs;
+          const uint32_t q = here(q_low), k = here(k_low + ((sst * M::TILE + half * kHalf * 128) >> 4)), d = here(s_at + b * kHalf);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t at = ((i / 4) * M::PLANE + (i % 4) * 32) >> 4;
+            mma_ss(d, smem_desc(q + at), smem_desc(k + at), QK, i > 0);
+          }
+          mma_commit(&sh.bar[kSFull + 2 * t + b]);  // also after the results of step j
+          if (half == 1 || j + 3 == steps) mma_commit(&sh.bar[kKFree + sst]);
+        } else if (j >= 0) {
+          mma_commit(&sh.bar[kODone + t]);  // of the last two steps, which no scores follow
+        }
+      }
+    } else {  // no rows: keep step, so that no barrier gets two phases ahead
+      for (int i = 0; i < nt; ++i) {
+        const uint32_t n = n0 + i, st = n & 1, ph = n >> 1 & 1;
+        if (!wait_thread(sh, kKFull + st, ph, A.err)) return;
+        mbar_arrive(&sh.bar[kKFree + st]);
+        if (!wait_thread(sh, kVFull + st, ph, A.err)) return;
+        mbar_arrive(&sh.bar[kVFree + st]);
       }
     }
     left -= nt;
+    n0 += nt;
     tile = 0;
     if (left > 0) next_unit<kManyRows, kTile>(A, u);
   }
@@ -367,7 +378,8 @@ __device__ __forceinline__ void load_q(const AttnArgs& A, const Unit& u, int t, 
 
 // A row's scores, 32 columns from key col of the tile on: times K's scales, those not seen -infinity.
 template <bool MASK>
-__device__ __forceinline__ float scaled(uint32_t (&s)[32], const float* ks, int col, int from, int to, float top) {
+__device__ __forceinline__ float scaled(uint32_t (&s)[32], const float* ks, int col, int from, int to) {
+  float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // chains side by side
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
     const float4 k = *reinterpret_cast<const float4*>(ks + col + i);
@@ -383,9 +395,11 @@ __device__ __forceinline__ float scaled(uint32_t (&s)[32], const float* ks, int 
     s[i + 1] = __float_as_uint(a.y);
     s[i + 2] = __float_as_uint(b.x);
     s[i + 3] = __float_as_uint(b.y);
-    top = fmaxf(fmaxf(top, fmaxf(a.x, a.y)), fmaxf(b.x, b.y));
+    const int k2 = i / 4 & 1;
+    top[2 * k2] = fmaxf(fmaxf(top[2 * k2], a.x), a.y);
+    top[2 * k2 + 1] = fmaxf(fmaxf(top[2 * k2 + 1], b.x), b.y);
   }
-  return top;
+  return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
 }
 // Their weights times V's scales, in bf16; sum takes the weights.
 template <bool MASK>
@@ -420,7 +434,7 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
   int tile = sh.plan.tile;
   int64_t x = sh.plan.x0;
   const int64_t x1 = sh.plan.x1;
-  uint32_t n = 0, rounds = 0, units = 0;
+  uint32_t n = 0, rounds = 0, done = 0;  // tiles of keys, steps and phases of kODone so far
   bool have_q = false;
   while (x < x1) {
     const int nt = (int)min((int64_t)(u.tiles - tile), x1 - x);
@@ -438,34 +452,39 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
       const int pos_min = first + min(wr, u.r1 - 1) / A.G, pos_max = first + min(wr + 31, u.r1 - 1) / A.G;
       float m = -INFINITY;
       float2 sum = make_float2(0.f, 0.f);
-      for (int i = 0; i < nt; ++i, ++rounds) {
-        const uint32_t g = n + i;
-        const int j0 = u.lo + (tile + i) * kTile;
-        if (!wait_warp(sh, kSFull + t, rounds & 1, A.err) || !wait_warp(sh, kVFull + (g & 1), g >> 1 & 1, A.err)) return;
+      const int steps = steps_of(u, tile, nt);
+      for (int i = 0; i < steps; ++i, ++rounds) {
+        const uint32_t g = n + (i >> 1), buf = rounds & 1, at = s_at + buf * kHalf;
+        const int col0 = (i & 1) * kHalf, j0 = u.lo + (tile + (i >> 1)) * kTile + col0;
+        if (!wait_warp(sh, kSFull + 2 * t + buf, rounds >> 1 & 1, A.err) || !wait_warp(sh, kVFull + (g & 1), g >> 1 & 1, A.err)) return;
         tc_after();
-        const float *ks = sh.scale[g & 1][0], *vs = sh.scale[g & 1][1];
-        const bool whole = j0 + kTile <= u.hi && (!A.causal || j0 + kTile - 1 <= pos_min) && (A.window <= 0 || j0 > pos_max - A.window);
-        const int to = min(A.causal ? min(u.hi, pos + 1) : u.hi, j0 + kTile) - j0, from = A.window > 0 ? pos - A.window + 1 - j0 : 0;
-        uint32_t s[4][32];
-        float top = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tm_ld32(s[c], s_at + 32 * c);
+        const float *ks = sh.scale[g & 1][0] + col0, *vs = sh.scale[g & 1][1] + col0;
+        const bool whole = j0 + kHalf <= u.hi && (!A.causal || j0 + kHalf - 1 <= pos_min) && (A.window <= 0 || j0 > pos_max - A.window);
+        const int to = min(A.causal ? min(u.hi, pos + 1) : u.hi, j0 + kHalf) - j0, from = A.window > 0 ? pos - A.window + 1 - j0 : 0;
+        uint32_t s[2][32];
+        tm_ld32(s[0], at);
+        tm_ld32(s[1], at + 32);
         tm_wait_ld();
-        if (whole) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) top = scaled<false>(s[c], ks, 32 * c, from, to, top);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) top = scaled<true>(s[c], ks, 32 * c, from, to, top);
+        float top;
+        if (whole) top = fmaxf(scaled<false>(s[0], ks, 0, from, to), scaled<false>(s[1], ks, 32, from, to));
+        else top = fmaxf(scaled<true>(s[0], ks, 0, from, to), scaled<true>(s[1], ks, 32, from, to));
+        if (i > 0 && i + 1 == steps) {  // no scores follow: a barrier of its own
+          if (!wait_warp(sh, kODone + t, done & 1, A.err)) return;
+          ++done;
+          tc_after();
         }
         // The reference follows the maximum only when that has grown by more than 2^8 (weights and sums have
-        // room for it): results are seldom rescaled.  The products that wrote them are complete: the
-        // scores' barrier comes after all products issued before.
+        // room for it): results are seldom rescaled.
         if (__any_sync(0xffffffffu, top > m + 8.f)) {
           const float up = fmaxf(m, top), f = ex2(m - finite_or_zero(up));
           m = up;
           sum = mul2(sum, both(f));
           if (i > 0) {
+            // the results of the step before: the next scores' barrier comes after them
+            if (i + 1 < steps) {
+              if (!wait_warp(sh, kSFull + 2 * t + (buf ^ 1), (rounds + 1) >> 1 & 1, A.err)) return;
+              tc_after();
+            }
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               uint32_t o[16];
@@ -479,16 +498,16 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
         }
         const float ref = finite_or_zero(m);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t w[16];
           if (whole) weights_of<false>(s[c], vs, 32 * c, from, to, ref, sum, w);
           else weights_of<true>(s[c], vs, 32 * c, from, to, ref, sum, w);
-          tm_st16(s_at + 16 * c, w);
+          tm_st16(at + 16 * c, w);
         }
         tm_wait_st();
         tc_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.bar[kPFull + t]);
+        if (lane == 0) mbar_arrive(&sh.bar[kPFull + 2 * t + buf]);
       }
       // the unit's results; Q's tile is free, its last scores have been read
       Unit nu = u;
@@ -498,8 +517,8 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
         if (lane == 0) mbar_arrive(&sh.bar[kQFull + t]);
         have_q = true;
       }
-      if (!wait_warp(sh, kOFull + t, units & 1, A.err)) return;
-      ++units;
+      if (!wait_warp(sh, kODone + t, done & 1, A.err)) return;
+      ++done;
       tc_after();
       const float l = sum.x + sum.y, inv = l == 0.f ? 0.f : 1.f / l;
       const int tok = r / A.G, hq = u.hg * A.G + r - tok * A.G;
@@ -566,8 +585,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) attn8_many(const __grid_const
     sh.stop = 0;
     for (int i = 0; i < kBars; ++i) {
       const bool conv = i < kKFree || (i >= kVFull && i < kVFree);                  // a converting warp each
-      const bool rows = (i >= kQFull && i < kSFull) || (i >= kPFull && i < kOFull);  // a warp of the tile each
-      mbar_init(&sh.bar[i], conv ? kConvWarps : rows ? 4 : 1);
+      const bool rows = (i >= kQFull && i < kODone) || i >= kPFull;  // a warp of the tile each
+      const bool free = (i >= kKFree && i < kVFull) || (i >= kVFree && i < kQFull);  // a thread of the products each
+      mbar_init(&sh.bar[i], conv ? kConvWarps : rows ? 4 : free ? 2 : 1);
     }
     mbar_init_fence();
     A.info[blockIdx.x * kAttnInfo] = -1;
@@ -588,19 +608,19 @@ __global__ void __launch_bounds__(kManyThreads, 1) attn8_many(const __grid_const
     if (warp < 8) {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
       softmax<D>(A, sh, q_smem, warp >> 2, q16, o16);
-    } else if (warp < 12) {
+    } else if (warp < 8 + kConvWarps) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
       convert<D, FMT>(A, sh, kv_smem, warp - 8);
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
-      if (threadIdx.x == 32 * 12) {
-        products<D>(A, sh, q_smem, kv_smem);
+      const int t = warp - 8 - kConvWarps;
+      if (t < 2 && (threadIdx.x & 31) == 0) {
+        products<D>(A, sh, q_smem, kv_smem, t);
         if (*(volatile int*)&sh.stop) {  // given up: what is in flight ends before the memory is given back
-          __shared__ uint64_t last;
-          mbar_init(&last, 1);
+          mbar_init(&sh.last[t], 1);
           mbar_init_fence();
-          mma_commit(&last);
-          mbar_wait(&last, 0, kWaitPolls);
+          mma_commit(&sh.last[t]);
+          mbar_wait(&sh.last[t], 0, kWaitPolls);
         }
       }
     }
