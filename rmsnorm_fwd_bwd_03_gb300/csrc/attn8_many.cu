@@ -52,7 +52,6 @@ struct Shared {
   Part plan;
   Unit now[2 + kConvWarps];  // where the threads of the products and each converting warp are: their registers are short
   uint32_t tmem;
-  int stop;
 };
 
 // --- tcgen05 ---------------------------------------------------------------
@@ -113,18 +112,26 @@ __device__ __forceinline__ uint32_t here(uint32_t v) {
   return v;
 }
 
-// Bounded wait of a whole warp (or of one thread alone); false once any wait of the block has run out.
-__device__ __forceinline__ bool wait_thread(Shared& sh, int bar, uint32_t parity, unsigned int* err) {
-  for (uint32_t i = 0; i < kWaitPolls; ++i) {
-    if (mbar_try_wait(&sh.bar[bar], parity)) return true;
-    if (*(volatile int*)&sh.stop) return false;
-  }
-  *(volatile int*)&sh.stop = 1;
-  atomicOr(err, kErrWaitTimeout);
-  return false;
-}
-__device__ __forceinline__ bool wait_warp(Shared& sh, int bar, uint32_t parity, unsigned int* err) {
-  return __all_sync(0xffffffffu, wait_thread(sh, bar, parity, err));
+// Bounded wait.  One that runs out (seconds; a legitimate one takes microseconds) is remembered in `late`, and
+// the waits after it poll once: the block runs to its end on whatever it finds, all of it in bounds, and reports.
+// (Leaving the loops instead put branches around everything that follows a wait.)
+constexpr uint32_t kManyPolls = 1u << 20;
+__device__ __forceinline__ void wait_for(const Shared& sh, int bar, uint32_t parity, uint32_t& late) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, %3;\n"
+      "WAIT_%=:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE_%=;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "@q bra WAIT_%=;\n"
+      "DONE_%=:\n\t"
+      "selp.u32 %0, 0, 1, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(&sh.bar[bar])), "r"(parity), "r"(late ? 1u : kManyPolls)
+      : "memory");
+  late |= ok;
 }
 
 // --- codes -> bf16 in shared memory ------------------------------------------
@@ -164,7 +171,7 @@ __device__ __forceinline__ void store_codes(uint32_t plane, int row, int c, uint
 // (16 codes each) of keys 16 w + r and 16 w + r + 8: a store instruction's eight lanes at a time hit all banks.
 // Each tile's codes are on their way while the tile before is converted.
 template <int D, int FMT>
-__device__ __forceinline__ void convert(const AttnArgs& A, Shared& sh, uint32_t kv_smem, int w) {
+__device__ __forceinline__ void convert(const AttnArgs& A, Shared& sh, uint32_t kv_smem, int w, uint32_t& late) {
   using M = ManyShape<D>;
   constexpr int NP = M::PLANES;
   const int lane = threadIdx.x & 31, c = lane & 3;
@@ -242,7 +249,8 @@ __device__ __forceinline__ void convert(const AttnArgs& A, Shared& sh, uint32_t 
     const int st = (int)(n & 1);
     const uint32_t again = (uint32_t)(n >> 1 & 1) ^ 1u;
     const bool more = n + 1 < n_tiles;
-    if (!wait_warp(sh, kKFree + st, again, A.err)) return;
+    wait_for(sh, kKFree + st, again, late);
+    __syncwarp();
     const uint32_t ks = kv_smem + st * M::TILE, vs = kv_smem + (2 + st) * M::TILE;
 #pragma unroll
     for (int i = 0; i < kConvRows; ++i)
@@ -255,7 +263,8 @@ __device__ __forceinline__ void convert(const AttnArgs& A, Shared& sh, uint32_t 
       place();
       fetch(A.K, kr);
     }
-    if (!wait_warp(sh, kVFree + st, again, A.err)) return;
+    wait_for(sh, kVFree + st, again, late);
+    __syncwarp();
 #pragma unroll
     for (int i = 0; i < kConvRows; ++i) {
 #pragma unroll
@@ -281,7 +290,7 @@ __device__ __forceinline__ int steps_of(const Unit& u, int tile, int nt) {
 // The thread that issues the products of tile t of rows, one for each tile: neither's waits hold up the other's
 // products.  A step's results, then the scores of the step after the next, which take its place.
 template <int D>
-__device__ __forceinline__ void products(const AttnArgs& A, Shared& sh, uint32_t q_smem, uint32_t kv_smem, int t) {
+__device__ __forceinline__ void products(const AttnArgs& A, Shared& sh, uint32_t q_smem, uint32_t kv_smem, int t, uint32_t& late) {
   using M = ManyShape<D>;
   constexpr uint32_t QK = inst_desc(kHalf, false), PV = inst_desc(D, true);
   const uint32_t s_at = sh.tmem + t * kTile, o_at = sh.tmem + 2 * kTile + t * kTile;
@@ -297,16 +306,16 @@ __device__ __forceinline__ void products(const AttnArgs& A, Shared& sh, uint32_t
     const int nt = (int)min((int64_t)(u.tiles - tile), left);
     if (u.r0 + t * kTile < u.r1) {
       const int steps = steps_of(u, tile, nt);
-      if (!wait_thread(sh, kQFull + t, units & 1, A.err)) return;
+      wait_for(sh, kQFull + t, units & 1, late);
       ++units;
 #pragma unroll 1
       for (int j = -2; j < steps; ++j) {
         const uint32_t n = n0 + (j >> 1), st = n & 1, half = j & 1, ns = n + 1, sst = ns & 1;  // step j + 2 is of tile n + 1
         const bool s_on = j + 2 < steps;
         if (j >= 0) {
-          if (half == 0 && !wait_thread(sh, kVFull + st, n >> 1 & 1, A.err)) return;
+          if (half == 0) wait_for(sh, kVFull + st, n >> 1 & 1, late);
           const uint32_t b = rp & 1;
-          if (!wait_thread(sh, kPFull + 2 * t + b, rp >> 1 & 1, A.err)) return;
+          wait_for(sh, kPFull + 2 * t + b, rp >> 1 & 1, late);
           ++rp;
           tc_after();
           const uint32_t v = here(v_low + ((st * M::TILE + half * kHalf * 128) >> 4)), w = here(s_at + b * kHalf);
@@ -316,7 +325,7 @@ __device__ __forceinline__ void products(const AttnArgs& A, Shared& sh, uint32_t
           if (half == 1 || j + 1 == steps) mma_commit(&sh.bar[kVFree + st]);
         }
         if (s_on) {
-          if (half == 0 && !wait_thread(sh, kKFull + sst, ns >> 1 & 1, A.err)) return;
+          if (half == 0) wait_for(sh, kKFull + sst, ns >> 1 & 1, late);
           tc_after();
           const uint32_t b = rs & 1;
           ++rs;
@@ -335,9 +344,9 @@ __device__ __forceinline__ void products(const AttnArgs& A, Shared& sh, uint32_t
     } else {  // no rows: keep step, so that no barrier gets two phases ahead
       for (int i = 0; i < nt; ++i) {
         const uint32_t n = n0 + i, st = n & 1, ph = n >> 1 & 1;
-        if (!wait_thread(sh, kKFull + st, ph, A.err)) return;
+        wait_for(sh, kKFull + st, ph, late);
         mbar_arrive(&sh.bar[kKFree + st]);
-        if (!wait_thread(sh, kVFull + st, ph, A.err)) return;
+        wait_for(sh, kVFull + st, ph, late);
         mbar_arrive(&sh.bar[kVFree + st]);
       }
     }
@@ -426,7 +435,7 @@ __device__ __forceinline__ void weights_of(const uint32_t (&s)[32], const float*
 
 // The four warps of tile t of rows.
 template <int D>
-__device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t q_smem, int t, bool q16, bool o16) {
+__device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t q_smem, int t, bool q16, bool o16, uint32_t& late) {
   const int warp = warp_index() & 3, lane = threadIdx.x & 31, row = 32 * warp + lane;
   const uint32_t lanes = (uint32_t)(32 * warp) << 16;
   const uint32_t s_at = sh.tmem + t * kTile + lanes, o_at = sh.tmem + 2 * kTile + t * kTile + lanes;
@@ -456,7 +465,9 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
       for (int i = 0; i < steps; ++i, ++rounds) {
         const uint32_t g = n + (i >> 1), buf = rounds & 1, at = s_at + buf * kHalf;
         const int col0 = (i & 1) * kHalf, j0 = u.lo + (tile + (i >> 1)) * kTile + col0;
-        if (!wait_warp(sh, kSFull + 2 * t + buf, rounds >> 1 & 1, A.err) || !wait_warp(sh, kVFull + (g & 1), g >> 1 & 1, A.err)) return;
+        wait_for(sh, kSFull + 2 * t + buf, rounds >> 1 & 1, late);
+        if ((i & 1) == 0) wait_for(sh, kVFull + (g & 1), g >> 1 & 1, late);  // the scales
+        __syncwarp();
         tc_after();
         const float *ks = sh.scale[g & 1][0] + col0, *vs = sh.scale[g & 1][1] + col0;
         const bool whole = j0 + kHalf <= u.hi && (!A.causal || j0 + kHalf - 1 <= pos_min) && (A.window <= 0 || j0 > pos_max - A.window);
@@ -469,7 +480,8 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
         if (whole) top = fmaxf(scaled<false>(s[0], ks, 0, from, to), scaled<false>(s[1], ks, 32, from, to));
         else top = fmaxf(scaled<true>(s[0], ks, 0, from, to), scaled<true>(s[1], ks, 32, from, to));
         if (i > 0 && i + 1 == steps) {  // no scores follow: a barrier of its own
-          if (!wait_warp(sh, kODone + t, done & 1, A.err)) return;
+          wait_for(sh, kODone + t, done & 1, late);
+          __syncwarp();
           ++done;
           tc_after();
         }
@@ -482,7 +494,8 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
           if (i > 0) {
             // the results of the step before: the next scores' barrier comes after them
             if (i + 1 < steps) {
-              if (!wait_warp(sh, kSFull + 2 * t + (buf ^ 1), (rounds + 1) >> 1 & 1, A.err)) return;
+              wait_for(sh, kSFull + 2 * t + (buf ^ 1), (rounds + 1) >> 1 & 1, late);
+              __syncwarp();
               tc_after();
             }
 #pragma unroll
@@ -517,7 +530,8 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
         if (lane == 0) mbar_arrive(&sh.bar[kQFull + t]);
         have_q = true;
       }
-      if (!wait_warp(sh, kODone + t, done & 1, A.err)) return;
+      wait_for(sh, kODone + t, done & 1, late);
+      __syncwarp();
       ++done;
       tc_after();
       const float l = sum.x + sum.y, inv = l == 0.f ? 0.f : 1.f / l;
@@ -582,7 +596,6 @@ __global__ void __launch_bounds__(kManyThreads, 1) attn8_many(const __grid_const
   const int warp = warp_index();
   const uint32_t q_smem = (smem_addr(many_smem) + 1023u) & ~1023u, kv_smem = q_smem + 2 * M::TILE;
   if (threadIdx.x == 0) {
-    sh.stop = 0;
     for (int i = 0; i < kBars; ++i) {
       const bool conv = i < kKFree || (i >= kVFull && i < kVFree);                  // a converting warp each
       const bool rows = (i >= kQFull && i < kODone) || i >= kPFull;  // a warp of the tile each
@@ -605,25 +618,26 @@ __global__ void __launch_bounds__(kManyThreads, 1) attn8_many(const __grid_const
   __syncthreads();
   tc_after();
   if (sh.plan.x0 < sh.plan.x1) {
+    uint32_t late = 0;
     if (warp < 8) {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
-      softmax<D>(A, sh, q_smem, warp >> 2, q16, o16);
+      softmax<D>(A, sh, q_smem, warp >> 2, q16, o16, late);
     } else if (warp < 8 + kConvWarps) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
-      convert<D, FMT>(A, sh, kv_smem, warp - 8);
+      convert<D, FMT>(A, sh, kv_smem, warp - 8, late);
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
       const int t = warp - 8 - kConvWarps;
       if (t < 2 && (threadIdx.x & 31) == 0) {
-        products<D>(A, sh, q_smem, kv_smem, t);
-        if (*(volatile int*)&sh.stop) {  // given up: what is in flight ends before the memory is given back
-          mbar_init(&sh.last[t], 1);
-          mbar_init_fence();
-          mma_commit(&sh.last[t]);
-          mbar_wait(&sh.last[t], 0, kWaitPolls);
-        }
+        products<D>(A, sh, q_smem, kv_smem, t, late);
+        // all products are complete before the memory is given back, also where waits have run out
+        mbar_init(&sh.last[t], 1);
+        mbar_init_fence();
+        mma_commit(&sh.last[t]);
+        mbar_wait(&sh.last[t], 0, kWaitPolls);
       }
     }
+    if (late) atomicOr(A.err, kErrWaitTimeout);
   }
   __syncwarp();
   tc_before();
