@@ -32,7 +32,7 @@ constexpr int kConvWarps = 8;
 constexpr int kConvRows = kTile / kConvWarps / 8;  // keys of a converting thread
 constexpr int kManyThreads = 640;      // five groups of four warps: rows twice, conversion twice, products
 // Registers of a thread in each group; together what the block is launched with (640 x 96).
-constexpr int kRegsRows = 120, kRegsConv = 72, kRegsMma = 96;
+constexpr int kRegsRows = 128, kRegsConv = 72, kRegsMma = 80;
 static_assert(2 * kRegsRows + 2 * kRegsConv + kRegsMma <= 5 * 96, "a larger sum would wait forever");
 
 template <int D>
@@ -385,9 +385,9 @@ __device__ __forceinline__ void load_q(const AttnArgs& A, const Unit& u, int t, 
   fence_proxy_async_smem();
 }
 
-// A row's scores, 32 columns from key col of the tile on: times K's scales, those not seen -infinity.
+// The largest of a row's scores: 32 columns from key col of the step on, times K's scales, of the keys it sees.
 template <bool MASK>
-__device__ __forceinline__ float scaled(uint32_t (&s)[32], const float* ks, int col, int from, int to) {
+__device__ __forceinline__ float top_of(const uint32_t (&s)[32], const float* ks, int col, int from, int to) {
   float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // chains side by side
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
@@ -400,34 +400,32 @@ __device__ __forceinline__ float scaled(uint32_t (&s)[32], const float* ks, int 
       if (col + i + 2 < from || col + i + 2 >= to) b.x = -INFINITY;
       if (col + i + 3 < from || col + i + 3 >= to) b.y = -INFINITY;
     }
-    s[i] = __float_as_uint(a.x);
-    s[i + 1] = __float_as_uint(a.y);
-    s[i + 2] = __float_as_uint(b.x);
-    s[i + 3] = __float_as_uint(b.y);
-    const int k2 = i / 4 & 1;
-    top[2 * k2] = fmaxf(fmaxf(top[2 * k2], a.x), a.y);
-    top[2 * k2 + 1] = fmaxf(fmaxf(top[2 * k2 + 1], b.x), b.y);
+    top[0] = fmaxf(top[0], a.x);
+    top[1] = fmaxf(top[1], a.y);
+    top[2] = fmaxf(top[2], b.x);
+    top[3] = fmaxf(top[3], b.y);
   }
   return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
 }
 // Their weights times V's scales, in bf16; sum takes the weights.
 template <bool MASK>
-__device__ __forceinline__ void weights_of(const uint32_t (&s)[32], const float* vs, int col, int from, int to, float ref, float2& sum, uint32_t (&w)[16]) {
+__device__ __forceinline__ void weights_of(const uint32_t (&s)[32], const float* ks, const float* vs, int col, int from, int to, float ref, float2& sum,
+                                           uint32_t (&w)[16]) {
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
-    const float4 v = *reinterpret_cast<const float4*>(vs + col + i);
-    float2 a = add2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), both(-ref));
-    float2 b = add2(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), both(-ref));
+    const float4 k = *reinterpret_cast<const float4*>(ks + col + i), v = *reinterpret_cast<const float4*>(vs + col + i);
+    float2 a = fma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(k.x, k.y), both(-ref));
+    float2 b = fma2(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), make_float2(k.z, k.w), both(-ref));
     a = make_float2(ex2(a.x), ex2(a.y));
     b = make_float2(ex2(b.x), ex2(b.y));
-    sum = add2(sum, add2(a, b));
     float2 x = mul2(a, make_float2(v.x, v.y)), y = mul2(b, make_float2(v.z, v.w));
-    if constexpr (MASK) {  // whatever the scale of a key that is not seen
-      if (col + i < from || col + i >= to) x.x = 0.f;
-      if (col + i + 1 < from || col + i + 1 >= to) x.y = 0.f;
-      if (col + i + 2 < from || col + i + 2 >= to) y.x = 0.f;
-      if (col + i + 3 < from || col + i + 3 >= to) y.y = 0.f;
+    if constexpr (MASK) {  // whatever the scales of a key that is not seen
+      if (col + i < from || col + i >= to) a.x = x.x = 0.f;
+      if (col + i + 1 < from || col + i + 1 >= to) a.y = x.y = 0.f;
+      if (col + i + 2 < from || col + i + 2 >= to) b.x = y.x = 0.f;
+      if (col + i + 3 < from || col + i + 3 >= to) b.y = y.y = 0.f;
     }
+    sum = add2(sum, add2(a, b));
     w[i / 2] = pack_bf16x2(x.x, x.y);
     w[i / 2 + 1] = pack_bf16x2(y.x, y.y);
   }
@@ -476,18 +474,34 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
         tm_ld32(s[0], at);
         tm_ld32(s[1], at + 32);
         tm_wait_ld();
-        float top;
-        if (whole) top = fmaxf(scaled<false>(s[0], ks, 0, from, to), scaled<false>(s[1], ks, 32, from, to));
-        else top = fmaxf(scaled<true>(s[0], ks, 0, from, to), scaled<true>(s[1], ks, 32, from, to));
         if (i > 0 && i + 1 == steps) {  // no scores follow: a barrier of its own
           wait_for(sh, kODone + t, done & 1, late);
           __syncwarp();
           ++done;
           tc_after();
         }
-        // The reference follows the maximum only when that has grown by more than 2^8 (weights and sums have
-        // room for it): results are seldom rescaled.
-        if (__any_sync(0xffffffffu, top > m + 8.f)) {
+        // Weights by the reference that the row has: while their sum stays below 2^10, no key can be far above
+        // it, and neither the step's maximum nor a rescaling is needed.  That is the rule; the first step, and
+        // one whose sum says otherwise (or is not a number), takes the maximum and computes them anew.
+        float2 part = make_float2(0.f, 0.f);
+        const auto weigh = [&]() {
+          const float ref = finite_or_zero(m);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t w[16];
+            if (whole) weights_of<false>(s[c], ks, vs, 32 * c, from, to, ref, part, w);
+            else weights_of<true>(s[c], ks, vs, 32 * c, from, to, ref, part, w);
+            tm_st16(at + 16 * c, w);  // nobody reads them before the arrival below
+          }
+        };
+        bool anew = __any_sync(0xffffffffu, m == -INFINITY);
+        if (!anew) {
+          weigh();
+          anew = __any_sync(0xffffffffu, !(part.x + part.y <= 1024.f));
+        }
+        if (anew) {
+          const float top = whole ? fmaxf(top_of<false>(s[0], ks, 0, from, to), top_of<false>(s[1], ks, 32, from, to))
+                                  : fmaxf(top_of<true>(s[0], ks, 0, from, to), top_of<true>(s[1], ks, 32, from, to));
           const float up = fmaxf(m, top), f = ex2(m - finite_or_zero(up));
           m = up;
           sum = mul2(sum, both(f));
@@ -498,7 +512,7 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
               __syncwarp();
               tc_after();
             }
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
               uint32_t o[16];
               tm_ld16(o, o_at + 16 * c);
@@ -508,15 +522,10 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
               tm_st16(o_at + 16 * c, o);
             }
           }
+          part = make_float2(0.f, 0.f);
+          weigh();
         }
-        const float ref = finite_or_zero(m);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t w[16];
-          if (whole) weights_of<false>(s[c], vs, 32 * c, from, to, ref, sum, w);
-          else weights_of<true>(s[c], vs, 32 * c, from, to, ref, sum, w);
-          tm_st16(at + 16 * c, w);
-        }
+        sum = add2(sum, part);
         tm_wait_st();
         tc_before();
         __syncwarp();
