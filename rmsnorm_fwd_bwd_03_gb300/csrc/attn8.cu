@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kFewWarps = 8;
 constexpr int kStep = 16;  // keys of a warp's step
+constexpr int kFewBegin = 4;  // tiles that a unit's begin counts for
 
 template <int D>
 struct FewShape {
@@ -151,27 +152,25 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) attn8_few(const __grid_cons
   if (warp == 0) {
     Part p;
     // a unit's tile is a step of each slice
-    p.total = 0;
     switch (S) {
-      case 8: plan_part<kFewRows, 8 * kStep>(A, p); break;
-      case 4: plan_part<kFewRows, 4 * kStep>(A, p); break;
-      case 2: plan_part<kFewRows, 2 * kStep>(A, p); break;
-      default: plan_part<kFewRows, kStep>(A, p);
+      case 8: plan_part<kFewRows, 8 * kStep, kFewBegin>(A, p); break;
+      case 4: plan_part<kFewRows, 4 * kStep, kFewBegin>(A, p); break;
+      case 2: plan_part<kFewRows, 2 * kStep, kFewBegin>(A, p); break;
+      default: plan_part<kFewRows, kStep, kFewBegin>(A, p);
     }
     if (lane == 0) plan = p;
   }
   __syncthreads();
   Unit u = plan.u;
   int tile = plan.tile;
-  int64_t x = plan.x0;
-  const int64_t x1 = plan.x1;
+  int64_t left = plan.left, at = plan.at;
   if (threadIdx.x == 0) A.info[blockIdx.x * kAttnInfo] = -1;
-  if (x >= x1) return;
+  if (left <= 0) return;
   const uint32_t mine = smem_addr(ring) + warp * Sh::WARP;
   float* res = reinterpret_cast<float*>(ring) + warp * (Sh::WARP / 4);
 
   for (;;) {
-    const int t1 = (int)min((int64_t)u.tiles, tile + (x1 - x));  // this block's tiles of the unit: tile .. t1 - 1
+    const int t1 = (int)min((int64_t)u.tiles, tile + left);  // this block's tiles of the unit: tile .. t1 - 1
     const int h = u.hg * A.HB + wh;
     const bool on = works && h < A.Hk;
     const int nrows = u.r1 - u.r0;
@@ -201,7 +200,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) attn8_few(const __grid_cons
       int pos[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = min(u.r0 + g + 8 * e, u.r1 - 1), tok = r / A.G, hq = h * A.G + r - tok * A.G;
+        const int r = min(u.r0 + g + 8 * e, u.r1 - 1), tok = A.group.by(r), hq = h * A.G + r - tok * A.G;
         pos[e] = first + tok;
         const bf16* src = (const bf16*)A.q + (u.s.q0 + tok) * A.ldq + (int64_t)hq * D + 8 * c;
 #pragma unroll
@@ -221,7 +220,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) attn8_few(const __grid_cons
           qa[i][1][e + 2] = w.w;
         }
       }
-      const int pos_min = first + u.r0 / A.G, pos_max = first + (u.r1 - 1) / A.G;
+      const int pos_min = first + A.group.by(u.r0), pos_max = first + A.group.by(u.r1 - 1);
       int stage = 0;
 #pragma unroll 1
       for (int t = tile; t < t1; ++t) {
@@ -287,8 +286,9 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) attn8_few(const __grid_cons
         if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float to = fmaxf(m[e], top[e]);
-            const float f = ex2(m[e] - finite_or_zero(to));
+            const bool up = top[e] > m[e] + 8.f;  // each row for itself
+            const float to = up ? top[e] : m[e];
+            const float f = up ? ex2(m[e] - to) : 1.f;
             m[e] = to;
             l[e] *= f;
 #pragma unroll
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) attn8_few(const __grid_cons
           for (int i = 0; i < D / 32; ++i) A.part_o[at * D + lane + 32 * i] = acc[i];
           if (lane == 0) *reinterpret_cast<float2*>(A.part_ml + 2 * at) = make_float2(top, sum);
         } else {
-          const int row = u.r0 + r, tok = row / A.G, hq = h * A.G + row - tok * A.G;
+          const int row = u.r0 + r, tok = A.group.by(row), hq = h * A.G + row - tok * A.G;
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
           bf16* dst = (bf16*)A.out + (u.s.q0 + tok) * A.ldo + (int64_t)hq * D;
 #pragma unroll
@@ -395,17 +395,16 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) attn8_few(const __grid_cons
       f[1] = u.b;
       f[2] = u.blk;
       f[3] = u.hg;
-      f[0] = parts_behind(plan, x + (u.tiles - 1 - tile));
+      f[0] = parts_behind(plan, at + (u.tiles - 1 - tile));
     }
-    x += t1 - tile;
-    if (x >= x1) break;
-    tile = 0;
+    const int nt = t1 - tile;
+    at += nt + kFewBegin;
     bool more;
     switch (S) {
-      case 8: more = next_unit<kFewRows, 8 * kStep>(A, u); break;
-      case 4: more = next_unit<kFewRows, 4 * kStep>(A, u); break;
-      case 2: more = next_unit<kFewRows, 2 * kStep>(A, u); break;
-      default: more = next_unit<kFewRows, kStep>(A, u);
+      case 8: more = go_on<kFewRows, 8 * kStep, kFewBegin>(A, u, tile, left, nt); break;
+      case 4: more = go_on<kFewRows, 4 * kStep, kFewBegin>(A, u, tile, left, nt); break;
+      case 2: more = go_on<kFewRows, 2 * kStep, kFewBegin>(A, u, tile, left, nt); break;
+      default: more = go_on<kFewRows, kStep, kFewBegin>(A, u, tile, left, nt);
     }
     if (!more) break;
     if (S > 1) __syncthreads();
@@ -446,7 +445,7 @@ __global__ void __launch_bounds__(256) attn8_join(const __grid_constant__ AttnAr
       for (int i = 0; i < kAttnMaxHeads / 32; ++i)
         if (lane + 32 * i < A.D) acc[i] += A.part_o[at * A.D + lane + 32 * i] * f;
     }
-    const int row = r0 + r, tok = row / A.G, hq = h * A.G + row - tok * A.G;
+    const int row = r0 + r, tok = A.group.by(row), hq = h * A.G + row - tok * A.G;
     const float inv = 1.f / sum;
     bf16* dst = (bf16*)A.out + (s.q0 + tok) * A.ldo + (int64_t)hq * A.D;
 #pragma unroll
@@ -666,6 +665,7 @@ extern "C" gbln_status gbln_attn_cache8(const void* q, const int32_t* cu_seqlens
   A.window = window < (1 << 30) ? window : 0;  // no position is that far from another
   A.n_pages = (int)k_cache->pages;
   A.page = fast_div((uint32_t)k_cache->page_size);
+  A.group = fast_div((uint32_t)A.G);
   A.K = cache_of(k_cache);
   A.V = cache_of(v_cache);
   A.err = err;

@@ -13,6 +13,7 @@ struct FastDiv {
     q = (uint32_t)(((uint64_t)n * m) >> s);
     r = n - q * d;
   }
+  __device__ __forceinline__ int by(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> s); }
 };
 
 struct AttnArgs {
@@ -28,7 +29,7 @@ struct AttnArgs {
   float scale2;  // scale * log2(e)
   int causal, window;
   int n_pages;
-  FastDiv page;
+  FastDiv page, group;  // by the slots of a page, by G
   Cache K, V;
   int HB, NHG;     // K/V heads of a block, groups of them
   float* part_o;   // [2 C, HB, rows, D]
@@ -54,8 +55,8 @@ __device__ __forceinline__ Seq seq_at(const AttnArgs& A, int b) {
 // The keys [lo, hi) that any of a sequence's rows r0 .. r1 - 1 (row = token * G + head of the group) sees.
 __device__ __forceinline__ void keys_of(const AttnArgs& A, const Seq& s, int r0, int r1, int& lo, int& hi) {
   const int first = s.kv - s.nq;
-  lo = A.window > 0 ? max(0, first + r0 / A.G - A.window + 1) : 0;
-  hi = A.causal ? min(s.kv, first + (r1 - 1) / A.G + 1) : s.kv;
+  lo = A.window > 0 ? max(0, first + A.group.by(r0) - A.window + 1) : 0;
+  hi = A.causal ? min(s.kv, first + A.group.by(r1 - 1) + 1) : s.kv;
   hi = max(hi, lo);
 }
 
@@ -64,7 +65,8 @@ __device__ __forceinline__ void keys_of(const AttnArgs& A, const Seq& s, int r0,
 // K/V heads; it takes as many tiles of TK keys as it sees (one at least, so that rows that
 // see nothing are written too).  All units' tiles in a row are cut into as many equal
 // parts as there are blocks: a long context is shared by many, a short one is a piece of
-// one block's work, and no block waits for the longest sequence.  Lengths are read on the
+// one block's work, and no block waits for the longest sequence.  The begin of a unit counts as OV
+// more tiles (its rows are fetched, the results before it stored).  Lengths are read on the
 // device, so a captured graph follows them.  A unit that a cut divides leaves partial
 // results, which a second kernel joins in the order of its parts.
 // ---------------------------------------------------------------------------
@@ -108,9 +110,10 @@ __device__ __forceinline__ int warp_scan(int v) {
   return v;
 }
 
-// One warp walks all row blocks, 32 at a time.  Returns the number of tiles of the whole
-// batch (target < 0), or finds the unit that holds tile `target` and the tile's number in it.
-template <int MR, int TK>
+// One warp walks all row blocks, 32 at a time.  Returns the number of tiles of the whole batch
+// (target < 0), or finds the unit that holds number `target` and the tile's number in it (negative:
+// one of the OV that its begin counts for).
+template <int MR, int TK, int OV>
 __device__ __forceinline__ int64_t walk_units(const AttnArgs& A, int64_t target, Unit& u, int& tile) {
   const int lane = threadIdx.x & 31;
   int64_t run = 0;
@@ -138,7 +141,7 @@ __device__ __forceinline__ int64_t walk_units(const AttnArgs& A, int64_t target,
       x.tiles = 0;
       if (i < all) unit_range<MR, TK>(A, x);
       // 32 blocks' tiles fit 32 bits unless the context is beyond 2^26 tiles of a block
-      int64_t mine = (int64_t)x.tiles * A.NHG, sum = mine;
+      int64_t mine = i < all ? (int64_t)(x.tiles + OV) * A.NHG : 0, sum = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t t = __shfl_up_sync(0xffffffffu, sum, o);
@@ -157,8 +160,8 @@ __device__ __forceinline__ int64_t walk_units(const AttnArgs& A, int64_t target,
           u.s.kv = __shfl_sync(0xffffffffu, x.s.kv, l);
           const int64_t in = target - (__shfl_sync(0xffffffffu, end, l) - __shfl_sync(0xffffffffu, mine, l));
           unit_range<MR, TK>(A, u);
-          u.hg = (int)(in / u.tiles);
-          tile = (int)(in - (int64_t)u.hg * u.tiles);
+          u.hg = (int)(in / (u.tiles + OV));
+          tile = (int)(in - (int64_t)u.hg * (u.tiles + OV)) - OV;
           return run;
         }
       }
@@ -168,27 +171,40 @@ __device__ __forceinline__ int64_t walk_units(const AttnArgs& A, int64_t target,
   return run;
 }
 
-// A block's part of the plan.
+// A block's part of the plan: where it begins, and how many tiles are left to it.
 struct Part {
   Unit u;
-  int tile;        // the first of the unit's tiles that is the block's
-  int64_t x0, x1;  // the block's tiles of all
+  int tile;
+  int64_t at;    // the number of that tile among all
+  int64_t left;  // tiles, the begins of further units among them
   int64_t total;
-  int blocks;  // that have tiles: not more than there are tiles
+  int blocks;  // that have tiles: not more than there are numbers
 };
-template <int MR, int TK>
+template <int MR, int TK, int OV>
 __device__ __forceinline__ void plan_part(const AttnArgs& A, Part& p) {
-  p.total = walk_units<MR, TK>(A, -1, p.u, p.tile);
+  p.total = walk_units<MR, TK, OV>(A, -1, p.u, p.tile);
   p.blocks = (int)min((int64_t)gridDim.x, p.total);
-  p.x0 = p.x1 = 0;
+  p.at = p.left = 0;
   if ((int)blockIdx.x >= p.blocks) return;
-  p.x0 = p.total * blockIdx.x / p.blocks;
-  p.x1 = p.total * (blockIdx.x + 1) / p.blocks;
-  if (p.x0 < p.x1) walk_units<MR, TK>(A, p.x0, p.u, p.tile);
+  p.at = p.total * blockIdx.x / p.blocks;
+  p.left = p.total * (blockIdx.x + 1) / p.blocks - p.at;
+  walk_units<MR, TK, OV>(A, p.at, p.u, p.tile);
+  if (p.tile < 0) {
+    p.at -= p.tile;
+    p.left += p.tile;
+    p.tile = 0;
+  }
 }
-// The blocks behind block c that hold tiles of the unit whose last tile is number `last`.
+// To the next unit, nt tiles having been done; false where the block's part ends.
+template <int MR, int TK, int OV>
+__device__ __forceinline__ bool go_on(const AttnArgs& A, Unit& u, int& tile, int64_t& left, int nt) {
+  left -= nt + OV;
+  tile = 0;
+  return left > 0 && next_unit<MR, TK>(A, u);
+}
+// The blocks behind this one that hold tiles of the unit whose last tile is number `last`.
 __device__ __forceinline__ int parts_behind(const Part& p, int64_t last) {
-  // the block of tile x: the smallest c with total (c + 1) / blocks > x
+  // the block of number x: the smallest c with total (c + 1) / blocks > x
   int64_t c = ((last + 1) * p.blocks - 1) / p.total;
   while (p.total * (c + 1) / p.blocks <= last) ++c;
   while (c > 0 && p.total * c / p.blocks > last) --c;

@@ -28,6 +28,7 @@ constexpr int kTile = 128;              // rows of a tile, keys that are fetched
 constexpr int kHalf = kTile / 2;        // keys of a step
 constexpr int kManyRows = 2 * kTile;    // rows of a unit
 static_assert(kManyRows == kManyUnit, "the joining kernel knows it too");
+constexpr int kBegin = 1;               // tiles that a unit's begin counts for
 constexpr int kConvWarps = 8;
 constexpr int kConvRows = kTile / kConvWarps / 8;  // keys of a converting thread
 constexpr int kManyThreads = 640;      // five groups of four warps: rows twice, conversion twice, products
@@ -50,7 +51,9 @@ struct Shared {
   uint64_t bar[kBars], last[2];
   __align__(16) float scale[2][2][kTile];  // [stage][K times the softmax scale, V][key]
   Part plan;
-  Unit now[2 + kConvWarps];  // where the threads of the products and each converting warp are: their registers are short
+  // Where the threads of the products and each converting warp are, and each warp of rows (now and next): kept
+  // here, they leave the registers to the inner loops.
+  Unit now[2 + kConvWarps], rows[8][2];
   uint32_t tmem;
 };
 
@@ -176,14 +179,13 @@ __device__ __forceinline__ void convert(const AttnArgs& A, Shared& sh, uint32_t 
   constexpr int NP = M::PLANES;
   const int lane = threadIdx.x & 31, c = lane & 3;
   const int row = 8 * kConvRows * w + (lane >> 2);  // + 8 i
-  const int64_t n_tiles = sh.plan.x1 - sh.plan.x0;
   // The cursor runs two tiles ahead: a tile's pages are looked up while the codes of the one before it are on
   // their way and the one before that is converted.
   Unit& u = sh.now[2 + w];
   if (lane == 0) u = sh.plan.u;
   __syncwarp();
   int tile = sh.plan.tile;
-  int64_t ahead = 0;
+  int64_t left = sh.plan.left;  // at the cursor
   int lo = u.lo, hi = u.hi, tiles = u.tiles, hg = u.hg;
   const int32_t* row_of = A.pages + (int64_t)u.b * A.max_pages;
   int page[kConvRows], h = 0;  // of the tile looked up last; -1: no key, -2: outside the cache
@@ -191,7 +193,7 @@ __device__ __forceinline__ void convert(const AttnArgs& A, Shared& sh, uint32_t 
   uint4 kr[kConvRows][NP], vr[kConvRows][NP];
   float sc[kConvRows];
   const auto look_up = [&]() {  // the pages of the cursor's tile; the cursor moves on
-    if (ahead >= n_tiles) return;
+    if (left <= 0) return;
 #pragma unroll
     for (int i = 0; i < kConvRows; ++i) {
       const int j = lo + tile * kTile + row + 8 * i;
@@ -200,7 +202,9 @@ __device__ __forceinline__ void convert(const AttnArgs& A, Shared& sh, uint32_t 
       page[i] = j < hi ? __ldg(row_of + q) : INT_MIN;
     }
     h = hg;
-    if (++ahead < n_tiles && ++tile == tiles) {
+    --left;
+    if (++tile == tiles && left > kBegin) {
+      left -= kBegin;
       tile = 0;
       __syncwarp();
       if (lane == 0) next_unit<kManyRows, kTile>(A, u);
@@ -210,6 +214,8 @@ __device__ __forceinline__ void convert(const AttnArgs& A, Shared& sh, uint32_t 
       tiles = u.tiles;
       hg = u.hg;
       row_of = A.pages + (int64_t)u.b * A.max_pages;
+    } else if (tile == tiles) {
+      left = 0;
     }
   };
   const auto place = [&]() {
@@ -244,11 +250,11 @@ __device__ __forceinline__ void convert(const AttnArgs& A, Shared& sh, uint32_t 
   fetch(A.K, kr);
   fetch(A.V, vr);
   scales();
+  bool more = left > 0;
   look_up();
-  for (int64_t n = 0; n < n_tiles; ++n) {
+  for (int64_t n = 0;; ++n) {
     const int st = (int)(n & 1);
     const uint32_t again = (uint32_t)(n >> 1 & 1) ^ 1u;
-    const bool more = n + 1 < n_tiles;
     wait_for(sh, kKFree + st, again, late);
     __syncwarp();
     const uint32_t ks = kv_smem + st * M::TILE, vs = kv_smem + (2 + st) * M::TILE;
@@ -274,11 +280,11 @@ __device__ __forceinline__ void convert(const AttnArgs& A, Shared& sh, uint32_t 
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.bar[kVFull + st]);
-    if (more) {
-      fetch(A.V, vr);
-      scales();
-      look_up();
-    }
+    if (!more) break;
+    fetch(A.V, vr);
+    scales();
+    more = left > 0;
+    look_up();
   }
 }
 
@@ -298,11 +304,11 @@ __device__ __forceinline__ void products(const AttnArgs& A, Shared& sh, uint32_t
   Unit& u = sh.now[t];
   u = sh.plan.u;
   int tile = sh.plan.tile;
-  int64_t left = sh.plan.x1 - sh.plan.x0;
+  int64_t left = sh.plan.left;
   uint32_t n0 = 0;      // tiles of keys before the unit
   uint32_t rs = 0, rp = 0;  // steps whose scores, and whose results, have been issued
   uint32_t units = 0;
-  while (left > 0) {
+  for (;;) {
     const int nt = (int)min((int64_t)(u.tiles - tile), left);
     if (u.r0 + t * kTile < u.r1) {
       const int steps = steps_of(u, tile, nt);
@@ -350,39 +356,50 @@ __device__ __forceinline__ void products(const AttnArgs& A, Shared& sh, uint32_t
         mbar_arrive(&sh.bar[kVFree + st]);
       }
     }
-    left -= nt;
     n0 += nt;
-    tile = 0;
-    if (left > 0) next_unit<kManyRows, kTile>(A, u);
+    if (!go_on<kManyRows, kTile, kBegin>(A, u, tile, left, nt)) break;
   }
 }
 
-// Rows of tile t of a unit into shared memory (zeros behind the last one).
+// Tile t of a unit's rows into shared memory (zeros behind the last row), each of the tile's warps its own 32: eight
+// lanes take a row's 128 bytes, and all loads are under way before the first is stored.
 template <int D>
-__device__ __forceinline__ void load_q(const AttnArgs& A, const Unit& u, int t, uint32_t q_smem, bool q16) {
+__device__ __forceinline__ void load_q(const AttnArgs& A, Shared& sh, const Unit& u, int t, uint32_t q_smem, bool q16) {
   using M = ManyShape<D>;
-  const int row = threadIdx.x & (kTile - 1), r = u.r0 + t * kTile + row;
-  const int tok = r / A.G, hq = u.hg * A.G + r - tok * A.G;
-  const bf16* src = (const bf16*)A.q + (int64_t)(u.s.q0 + tok) * A.ldq + (int64_t)hq * D;
-  const uint32_t at = q_smem + t * M::TILE + row * 128;
+  const int lane = threadIdx.x & 31, c = lane & 7, row0 = 32 * (warp_index() & 3) + (lane >> 3);
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (r < u.r1) {
-      if (q16) {
-        w = ld_reuse(src + 8 * i);
-      } else {
-        uint32_t v[8];
+  for (int p = 0; p < M::PLANES; ++p) {
+    uint4 w[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = reinterpret_cast<const uint16_t*>(src)[8 * i + k];
-        w = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    for (int i = 0; i < 8; ++i) {
+      const int r = u.r0 + t * kTile + row0 + 4 * i;
+      w[i] = make_uint4(0, 0, 0, 0);
+      if (r < u.r1 && 64 * p + 8 * c < D) {
+        uint32_t tok, g;
+        A.group.split((uint32_t)r, tok, g);
+        const bf16* src = (const bf16*)A.q + (int64_t)(u.s.q0 + (int)tok) * A.ldq + (int64_t)(u.hg * A.G + (int)g) * D + 64 * p + 8 * c;
+        if (q16) {
+          w[i] = ld_reuse(src);
+        } else {
+          uint32_t v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = reinterpret_cast<const uint16_t*>(src)[k];
+          w[i] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+        }
       }
     }
-    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + (i / 8) * M::PLANE + 16 * ((i % 8) ^ (row & 7))), "r"(w.x), "r"(w.y), "r"(w.z),
-                 "r"(w.w)
-                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = row0 + 4 * i;
+      if (64 * p + 8 * c < D)
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(q_smem + t * M::TILE + p * M::PLANE + row * 128 + 16 * (c ^ (row & 7))), "r"(w[i].x),
+                     "r"(w[i].y), "r"(w[i].z), "r"(w[i].w)
+                     : "memory");
+    }
   }
   fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&sh.bar[kQFull + t]);
 }
 
 // The largest of a row's scores: 32 columns from key col of the step on, times K's scales, of the keys it sees.
@@ -437,39 +454,50 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
   const int warp = warp_index() & 3, lane = threadIdx.x & 31, row = 32 * warp + lane;
   const uint32_t lanes = (uint32_t)(32 * warp) << 16;
   const uint32_t s_at = sh.tmem + t * kTile + lanes, o_at = sh.tmem + 2 * kTile + t * kTile + lanes;
-  Unit u = sh.plan.u;
+  Unit* own = sh.rows[4 * t + warp];
+  int which = 0;
+  if (lane == 0) own[0] = sh.plan.u;
+  __syncwarp();
   int tile = sh.plan.tile;
-  int64_t x = sh.plan.x0;
-  const int64_t x1 = sh.plan.x1;
+  int64_t left = sh.plan.left, num = sh.plan.at;
   uint32_t n = 0, rounds = 0, done = 0;  // tiles of keys, steps and phases of kODone so far
-  bool have_q = false;
-  while (x < x1) {
-    const int nt = (int)min((int64_t)(u.tiles - tile), x1 - x);
-    const bool before = tile > 0, behind = tile + nt < u.tiles;
-    if (u.r0 + t * kTile < u.r1) {
-      if (!have_q) {
-        load_q<D>(A, u, t, q_smem, q16);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.bar[kQFull + t]);
+  if (own[0].r0 + t * kTile < own[0].r1) load_q<D>(A, sh, own[0], t, q_smem, q16);
+  for (;;) {
+    const Unit& u = own[which];
+    const int nt = (int)min((int64_t)(u.tiles - tile), left);
+    const bool before = tile > 0, behind = tile + nt < u.tiles, has = u.r0 + t * kTile < u.r1;
+    // the next unit
+    int64_t after = left;
+    {
+      int first_tile = tile;
+      bool ok = false;
+      if (lane == 0) {
+        own[which ^ 1] = u;
+        ok = go_on<kManyRows, kTile, kBegin>(A, own[which ^ 1], first_tile, after, nt);
       }
-      have_q = false;
+      after = __shfl_sync(0xffffffffu, (int)ok, 0) ? left - nt - kBegin : 0;
+      __syncwarp();
+    }
+    const Unit& nu = own[which ^ 1];
+    if (has) {
       const int r = u.r0 + t * kTile + row, first = u.s.kv - u.s.nq;
-      const int pos = first + min(r, u.r1 - 1) / A.G;
+      const int pos = first + A.group.by(min(r, u.r1 - 1));
       const int wr = u.r0 + t * kTile + 32 * warp;  // the warp's rows
-      const int pos_min = first + min(wr, u.r1 - 1) / A.G, pos_max = first + min(wr + 31, u.r1 - 1) / A.G;
+      const int pos_min = first + A.group.by(min(wr, u.r1 - 1)), pos_max = first + A.group.by(min(wr + 31, u.r1 - 1));
+      const int hi = u.hi, key0 = u.lo + tile * kTile;
       float m = -INFINITY;
       float2 sum = make_float2(0.f, 0.f);
       const int steps = steps_of(u, tile, nt);
       for (int i = 0; i < steps; ++i, ++rounds) {
         const uint32_t g = n + (i >> 1), buf = rounds & 1, at = s_at + buf * kHalf;
-        const int col0 = (i & 1) * kHalf, j0 = u.lo + (tile + (i >> 1)) * kTile + col0;
+        const int col0 = (i & 1) * kHalf, j0 = key0 + (i >> 1) * kTile + col0;
         wait_for(sh, kSFull + 2 * t + buf, rounds >> 1 & 1, late);
         if ((i & 1) == 0) wait_for(sh, kVFull + (g & 1), g >> 1 & 1, late);  // the scales
         __syncwarp();
         tc_after();
         const float *ks = sh.scale[g & 1][0] + col0, *vs = sh.scale[g & 1][1] + col0;
-        const bool whole = j0 + kHalf <= u.hi && (!A.causal || j0 + kHalf - 1 <= pos_min) && (A.window <= 0 || j0 > pos_max - A.window);
-        const int to = min(A.causal ? min(u.hi, pos + 1) : u.hi, j0 + kHalf) - j0, from = A.window > 0 ? pos - A.window + 1 - j0 : 0;
+        const bool whole = j0 + kHalf <= hi && (!A.causal || j0 + kHalf - 1 <= pos_min) && (A.window <= 0 || j0 > pos_max - A.window);
+        const int to = min(A.causal ? min(hi, pos + 1) : hi, j0 + kHalf) - j0, from = A.window > 0 ? pos - A.window + 1 - j0 : 0;
         uint32_t s[2][32];
         tm_ld32(s[0], at);
         tm_ld32(s[1], at + 32);
@@ -481,8 +509,9 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
           tc_after();
         }
         // Weights by the reference that the row has: while their sum stays below 2^10, no key can be far above
-        // it, and neither the step's maximum nor a rescaling is needed.  That is the rule; the first step, and
-        // one whose sum says otherwise (or is not a number), takes the maximum and computes them anew.
+        // it, and neither the step's maximum nor a rescaling is needed.  That is the rule; a row that has no
+        // reference yet, or whose sum says otherwise (or is not a number), takes the maximum and computes them
+        // anew: each row for itself, whatever the others of its warp do.
         float2 part = make_float2(0.f, 0.f);
         const auto weigh = [&]() {
           const float ref = finite_or_zero(m);
@@ -494,15 +523,15 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
             tm_st16(at + 16 * c, w);  // nobody reads them before the arrival below
           }
         };
-        bool anew = __any_sync(0xffffffffu, m == -INFINITY);
-        if (!anew) {
+        bool anew = true;
+        if (i > 0) {
           weigh();
-          anew = __any_sync(0xffffffffu, !(part.x + part.y <= 1024.f));
+          anew = m == -INFINITY || !(part.x + part.y <= 1024.f);
         }
-        if (anew) {
+        if (__any_sync(0xffffffffu, anew)) {
           const float top = whole ? fmaxf(top_of<false>(s[0], ks, 0, from, to), top_of<false>(s[1], ks, 32, from, to))
                                   : fmaxf(top_of<true>(s[0], ks, 0, from, to), top_of<true>(s[1], ks, 32, from, to));
-          const float up = fmaxf(m, top), f = ex2(m - finite_or_zero(up));
+          const float up = anew ? fmaxf(m, top) : m, f = anew ? ex2(m - finite_or_zero(up)) : 1.f;
           m = up;
           sum = mul2(sum, both(f));
           if (i > 0) {
@@ -531,20 +560,14 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.bar[kPFull + 2 * t + buf]);
       }
-      // the unit's results; Q's tile is free, its last scores have been read
-      Unit nu = u;
-      if (x + nt < x1 && next_unit<kManyRows, kTile>(A, nu) && nu.r0 + t * kTile < nu.r1) {
-        load_q<D>(A, nu, t, q_smem, q16);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.bar[kQFull + t]);
-        have_q = true;
-      }
+      // the next unit's rows (the last scores have been read: the place is free), then this one's results
+      if (after > 0 && nu.r0 + t * kTile < nu.r1) load_q<D>(A, sh, nu, t, q_smem, q16);
       wait_for(sh, kODone + t, done & 1, late);
       __syncwarp();
       ++done;
       tc_after();
       const float l = sum.x + sum.y, inv = l == 0.f ? 0.f : 1.f / l;
-      const int tok = r / A.G, hq = u.hg * A.G + r - tok * A.G;
+      const int tok = A.group.by(r), hq = u.hg * A.G + r - tok * A.G;
       const bool split = before || behind;
       const int64_t at = (int64_t)(2 * blockIdx.x + (before ? 0 : 1)) * kManyRows + t * kTile + row;
 #pragma unroll
@@ -587,12 +610,16 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
       f[1] = u.b;
       f[2] = u.blk;
       f[3] = u.hg;
-      f[0] = parts_behind(sh.plan, x + (u.tiles - 1 - tile));
+      f[0] = parts_behind(sh.plan, num + (u.tiles - 1 - tile));
     }
+    if (after <= 0) break;
+    if (!has && nu.r0 + t * kTile < nu.r1) load_q<D>(A, sh, nu, t, q_smem, q16);
     n += nt;
-    x += nt;
+    num += nt + kBegin;
+    left = after;
     tile = 0;
-    if (x < x1) next_unit<kManyRows, kTile>(A, u);
+    __syncwarp();  // all lanes are done with this unit: its place is the next but one's
+    which ^= 1;
   }
 }
 
@@ -616,7 +643,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) attn8_many(const __grid_const
   }
   if (warp == 0) {
     Part p;
-    plan_part<kManyRows, kTile>(A, p);
+    plan_part<kManyRows, kTile, kBegin>(A, p);
     if ((threadIdx.x & 31) == 0) sh.plan = p;
   }
   if (warp == 8) {
@@ -626,7 +653,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) attn8_many(const __grid_const
   tc_before();
   __syncthreads();
   tc_after();
-  if (sh.plan.x0 < sh.plan.x1) {
+  if (sh.plan.left > 0) {
     uint32_t late = 0;
     if (warp < 8) {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
