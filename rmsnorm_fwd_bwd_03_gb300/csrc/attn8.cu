@@ -10,11 +10,13 @@
 // part in it.
 //
 // Few rows per sequence (decode, drafts): bound by the cache's bytes, D + 4 per K or V head
-// of a token.  A warp takes 16 rows (new tokens x heads of a group) of one K/V head and
+// of a token.  A warp takes 8 or 16 rows (new tokens x heads of a group) of one K/V head and
 // streams its keys, 16 at a time, through a ring in shared memory of its own, without any
-// barrier between warps.  Codes go straight from there into the fragments of the 16 x 8 x 16
-// products: the order of D within a product is free as long as Q has the same, so that a
-// lane's codes are the bytes it finds next to one another.
+// barrier between warps.  Keys are the 16 rows and queries the 8 columns of the 16 x 8 x 16
+// products (S^T = K Q^T, O^T = V^T P^T): a decode step's few rows then waste little of them.
+// Codes go straight from the ring into the fragments: the order of D within a product is
+// free as long as Q has the same, so that a lane's codes are the bytes it finds next to one
+// another, and O's rows are the values of a lane's slice of V.
 
 #include <atomic>
 
@@ -24,17 +26,19 @@ namespace gbln {
 
 namespace {
 
-constexpr int kFewWarps = 8;
 constexpr int kStep = 16;  // keys of a warp's step
 constexpr int kFewBegin = 4;  // tiles that a unit's begin counts for
 
-template <int D>
+// NT: columns of eight rows.  One leaves room for sixteen warps, two for eight.
+template <int D, int NT>
 struct FewShape {
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int WARPS = NT == 1 && D <= 128 ? 16 : 8;
   static constexpr int STAGE = 2 * kStep * D + 2 * kStep * 4;  // K, V, their scales
-  static constexpr int NS = D <= 64 ? 8 : D <= 96 ? 7 : D <= 128 ? 6 : 3;
-  static constexpr int WARP = NS * STAGE;  // holds a warp's results (16 x (D + 2) floats) at a unit's end
-  static constexpr int SMEM = kFewWarps * WARP;
-  static_assert(WARP >= kFewRows * (D + 2) * 4, "results fit the ring");
+  static constexpr int NS = (WARPS == 16 ? (D <= 64 ? 6 : D <= 96 ? 4 : 3) : (D <= 64 ? 8 : D <= 96 ? 7 : D <= 128 ? 6 : 3));
+  static constexpr int WARP = NS * STAGE;  // holds a warp's results (ROWS x (D + 2) floats) at a unit's end
+  static constexpr int SMEM = WARPS * WARP;
+  static_assert(WARP >= ROWS * (D + 2) * 4 && SMEM <= 227 * 1024 - 512, "results fit the ring, the ring the SM");
   // Where chunk ch (16 bytes) of row r lies: the lanes that read at once hit different banks.
   static __device__ __forceinline__ int k_at(int r, int ch) {
     if constexpr (D == 64) return r * D + 16 * (ch ^ ((r >> 1 & 1) << 1));
@@ -63,12 +67,6 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
   return r;
 }
-__device__ __forceinline__ float2 lds_f2(uint32_t a) {
-  float2 r;
-  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(a));
-  return r;
-}
-
 // Bytes ea of a and eb of b as two bf16 values.  INT8: 0x4300 | (x & 0x7f) is 128 + the low
 // seven bits, 0x4300 | (x & 0x80) is 128 or 256: their difference is the code.  E4M3: its
 // exponent and fraction in bf16's places are the value times 2^-120 (a NaN code becomes 480:
@@ -94,14 +92,26 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The keys that a warp's step brings in: page and slot of key (lane & 15).
+// P^T's fragment out of P's: an 8 x 8 matrix of 16-bit values transposed across the warp.
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ float lds_f(uint32_t a) {
+  float r;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(a));
+  return r;
+}
+
+// The page and slot of key j of sequence b; -1: no key, -2: a page outside the cache.
 struct KeyAt {
-  int page;  // -1: none, -2: a page outside the cache
+  int page;
   uint32_t off;
 };
-__device__ __forceinline__ KeyAt key_at(const AttnArgs& A, int b, int j, int hi) {
+__device__ __forceinline__ KeyAt key_at(const AttnArgs& A, int b, int j, int lo, int hi) {
   KeyAt k{-1, 0};
-  if (j < hi) {
+  if (j >= lo && j < hi) {
     uint32_t p;
     A.page.split((uint32_t)j, p, k.off);
     k.page = __ldg(A.pages + (int64_t)b * A.max_pages + p);
@@ -110,60 +120,91 @@ __device__ __forceinline__ KeyAt key_at(const AttnArgs& A, int b, int j, int hi)
   return k;
 }
 
-template <int D>
-__device__ __forceinline__ void few_load(const AttnArgs& A, uint32_t stage, const KeyAt& k, int h) {
-  using Sh = FewShape<D>;
+// A step's sixteen keys into a stage.  Where pages are multiples of sixteen slots the step lies in one page
+// (ONE: k is the place of its first key that is seen, the same in all lanes, off of key 0); else k is the
+// place of key (lane & 15).
+template <int D, int NT, bool ONE>
+__device__ __forceinline__ void few_load(const AttnArgs& A, uint32_t stage, const KeyAt& k, int h, int j0, int lo, int hi) {
+  using Sh = FewShape<D, NT>;
   const int lane = threadIdx.x & 31;
-  constexpr int CH = D / 16;               // chunks of a row
+  constexpr int CH = D / 16;                 // chunks of a row
   constexpr int N = (kStep * CH + 31) / 32;  // of K (and of V) per lane
+  static_assert(kStep * CH % 32 == 0, "whole passes");
+  const bool there = k.page >= 0;
+  const int64_t p = there ? k.page : 0, o = there ? k.off : 0;
+  // lanes 0..15 K's scales, 16..31 V's
+  const uint32_t at = stage + 2 * kStep * D + 4 * lane;
+  const int key = lane & 15;
+  const bool seen = !ONE || (j0 + key >= lo && j0 + key < hi);
+  const int64_t so = ONE ? o + key : o;
+  const float* src = lane < 16 ? A.K.sc + A.K.cs.at(p, so, h) : A.V.sc + A.V.cs.at(p, so, h);
+  if (k.page == -2) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(0x7fc00000) : "memory");
+  else cp4(at, src, there && seen);
+  if constexpr (ONE) {
+    const uint8_t *kq = A.K.q + A.K.cq.at(p, o, h), *vq = A.V.q + A.V.cq.at(p, o, h);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int x = i * 32 + lane, r = x / CH, ch = x - r * CH;
-    const int page = __shfl_sync(0xffffffffu, k.page, r & 15);
-    const uint32_t off = __shfl_sync(0xffffffffu, k.off, r & 15);
-    if (r < kStep) {
+    for (int i = 0; i < N; ++i) {
+      const int x = i * 32 + lane, r = x / CH, ch = x - r * CH;
+      const bool on = there && j0 + r >= lo && j0 + r < hi;
+      cp16(stage + Sh::k_at(r, ch), kq + r * A.K.cq.slot + 16 * ch, on);
+      cp16(stage + kStep * D + Sh::v_at(r, ch), vq + r * A.V.cq.slot + 16 * ch, on);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int x = i * 32 + lane, r = x / CH, ch = x - r * CH;
+      const int page = __shfl_sync(0xffffffffu, k.page, r);
+      const uint32_t off = __shfl_sync(0xffffffffu, k.off, r);
       const bool on = page >= 0;
-      const int64_t p = on ? page : 0, o = on ? off : 0;
-      cp16(stage + Sh::k_at(r, ch), A.K.q + A.K.cq.at(p, o, h) + 16 * ch, on);
-      cp16(stage + kStep * D + Sh::v_at(r, ch), A.V.q + A.V.cq.at(p, o, h) + 16 * ch, on);
+      cp16(stage + Sh::k_at(r, ch), A.K.q + A.K.cq.at(on ? page : 0, on ? off : 0, h) + 16 * ch, on);
+      cp16(stage + kStep * D + Sh::v_at(r, ch), A.V.q + A.V.cq.at(on ? page : 0, on ? off : 0, h) + 16 * ch, on);
     }
   }
-  // lanes 0..15 K's scales, 16..31 V's
-  const bool on = k.page >= 0;
-  const int64_t p = on ? k.page : 0, o = on ? k.off : 0;
-  const uint32_t at = stage + 2 * kStep * D + 4 * lane;
-  const float* src = lane < 16 ? A.K.sc + A.K.cs.at(p, o, h) : A.V.sc + A.V.cs.at(p, o, h);
-  if (k.page == -2) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(0x7fc00000) : "memory");
-  else cp4(at, src, on);
 }
 
-template <int D, int FMT>
-__global__ void __launch_bounds__(32 * kFewWarps, 1) attn8_few(const __grid_constant__ AttnArgs A, bool q16) {
-  using Sh = FewShape<D>;
+// The plan's calls, S slices of the keys to a tile.
+template <int ROWS>
+__device__ __forceinline__ void few_plan(const AttnArgs& A, int S, Part& p) {
+  switch (S) {
+    case 16: plan_part<ROWS, 16 * kStep, kFewBegin>(A, p); break;
+    case 8: plan_part<ROWS, 8 * kStep, kFewBegin>(A, p); break;
+    case 4: plan_part<ROWS, 4 * kStep, kFewBegin>(A, p); break;
+    case 2: plan_part<ROWS, 2 * kStep, kFewBegin>(A, p); break;
+    default: plan_part<ROWS, kStep, kFewBegin>(A, p);
+  }
+}
+template <int ROWS>
+__device__ __forceinline__ bool few_go_on(const AttnArgs& A, int S, Unit& u, int& tile, int64_t& left, int nt) {
+  switch (S) {
+    case 16: return go_on<ROWS, 16 * kStep, kFewBegin>(A, u, tile, left, nt);
+    case 8: return go_on<ROWS, 8 * kStep, kFewBegin>(A, u, tile, left, nt);
+    case 4: return go_on<ROWS, 4 * kStep, kFewBegin>(A, u, tile, left, nt);
+    case 2: return go_on<ROWS, 2 * kStep, kFewBegin>(A, u, tile, left, nt);
+    default: return go_on<ROWS, kStep, kFewBegin>(A, u, tile, left, nt);
+  }
+}
+
+template <int D, int FMT, int NT, bool ONE>
+__global__ void __launch_bounds__(32 * FewShape<D, NT>::WARPS, 1) attn8_few(const __grid_constant__ AttnArgs A, bool q16) {
+  using Sh = FewShape<D, NT>;
+  constexpr int ROWS = Sh::ROWS, W = D / 32;  // words of a lane's slice of a key
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ Part plan;
   launch_dependents();
   const int lane = threadIdx.x & 31, warp = warp_index();
   const int g = lane >> 2, c = lane & 3;
   // warp -> K/V head of the block's group and slice of the keys
-  const int S = kFewWarps / A.HB;
+  const int S = Sh::WARPS / A.HB;
   const int wh = warp % A.HB, slice = warp / A.HB;
-  const bool works = slice < S;
   if (warp == 0) {
     Part p;
-    // a unit's tile is a step of each slice
-    switch (S) {
-      case 8: plan_part<kFewRows, 8 * kStep, kFewBegin>(A, p); break;
-      case 4: plan_part<kFewRows, 4 * kStep, kFewBegin>(A, p); break;
-      case 2: plan_part<kFewRows, 2 * kStep, kFewBegin>(A, p); break;
-      default: plan_part<kFewRows, kStep, kFewBegin>(A, p);
-    }
+    few_plan<ROWS>(A, S, p);
     if (lane == 0) plan = p;
   }
   __syncthreads();
   Unit u = plan.u;
   int tile = plan.tile;
-  int64_t left = plan.left, at = plan.at;
+  int64_t left = plan.left, num = plan.at;
   if (threadIdx.x == 0) A.info[blockIdx.x * kAttnInfo] = -1;
   if (left <= 0) return;
   const uint32_t mine = smem_addr(ring) + warp * Sh::WARP;
@@ -172,55 +213,72 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) attn8_few(const __grid_cons
   for (;;) {
     const int t1 = (int)min((int64_t)u.tiles, tile + left);  // this block's tiles of the unit: tile .. t1 - 1
     const int h = u.hg * A.HB + wh;
-    const bool on = works && h < A.Hk;
+    const bool on = h < A.Hk;
     const int nrows = u.r1 - u.r0;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float o[D / 8][4];
+    float m[NT][2], l[NT][2], o[NT][D / 16][4];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
+    }
     if (on) {
       const int first = u.s.kv - u.s.nq;  // position of the sequence's first new token
-      const auto base = [&](int t) { return u.lo + (t * S + slice) * kStep; };
+      const int pos_min = first + A.group.by(u.r0), pos_max = first + A.group.by(u.r1 - 1);
+      const int lo = u.lo, hi = u.hi;
+      // steps begin at multiples of sixteen keys, which pages of such a size hold whole
+      const int begin = (lo & ~(kStep - 1)) + slice * kStep;
+      const auto base = [&](int t) { return begin + t * S * kStep; };
+      const auto where = [&](int t) {
+        const int j = base(t);
+        if (t >= t1) return KeyAt{-1, 0};
+        if constexpr (ONE) {
+          KeyAt k = key_at(A, u.b, max(j, lo), lo, hi);
+          k.off -= (uint32_t)(max(j, lo) - j);  // of the step's key 0
+          return k;
+        } else {
+          return key_at(A, u.b, j + (lane & 15), lo, hi);
+        }
+      };
       // fill the ring
-      KeyAt next = key_at(A, u.b, base(tile) + (lane & 15), u.hi);
+      KeyAt next = where(tile);
 #pragma unroll
       for (int i = 0; i < Sh::NS - 1; ++i) {
         if (tile + i < t1) {
           const KeyAt k = next;
-          next = key_at(A, u.b, base(tile + i + 1) + (lane & 15), tile + i + 1 < t1 ? u.hi : 0);
+          next = where(tile + i + 1);
           if (k.page == -2) atomicOr(A.err, kErrBadSlot);
-          few_load<D>(A, mine + i * Sh::STAGE, k, h);
+          few_load<D, NT, ONE>(A, mine + i * Sh::STAGE, k, h, base(tile + i), lo, hi);
         }
         cp_commit();
       }
-      // Q: rows g and g + 8, values 32 i + 8 c ..
-      uint32_t qa[D / 32][2][4];
-      int pos[2];
+      // Q^T: rows g + 8 n, values 32 i + 8 c ..
+      uint32_t qb[NT][W][4];
+      int pos[NT][2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = min(u.r0 + g + 8 * e, u.r1 - 1), tok = A.group.by(r), hq = h * A.G + r - tok * A.G;
-        pos[e] = first + tok;
+      for (int n = 0; n < NT; ++n) {
+        const int r = min(u.r0 + g + 8 * n, u.r1 - 1), tok = A.group.by(r), hq = h * A.G + r - tok * A.G;
         const bf16* src = (const bf16*)A.q + (u.s.q0 + tok) * A.ldq + (int64_t)hq * D + 8 * c;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          uint4 w;
+        for (int i = 0; i < W; ++i) {
           if (q16) {
-            w = ld_reuse(src + 32 * i);
+            const uint4 w = ld_reuse(src + 32 * i);
+            qb[n][i][0] = w.x;
+            qb[n][i][1] = w.y;
+            qb[n][i][2] = w.z;
+            qb[n][i][3] = w.w;
           } else {
-            uint16_t v[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = reinterpret_cast<const uint16_t*>(src)[32 * i + k];
-            w = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+            for (int k = 0; k < 4; ++k)
+              qb[n][i][k] = reinterpret_cast<const uint16_t*>(src)[32 * i + 2 * k] | (uint32_t) reinterpret_cast<const uint16_t*>(src)[32 * i + 2 * k + 1] << 16;
           }
-          qa[i][0][e] = w.x;
-          qa[i][0][e + 2] = w.y;
-          qa[i][1][e] = w.z;
-          qa[i][1][e + 2] = w.w;
         }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) pos[n][e] = first + A.group.by(min(u.r0 + 8 * n + 2 * c + e, u.r1 - 1));
       }
-      const int pos_min = first + A.group.by(u.r0), pos_max = first + A.group.by(u.r1 - 1);
       int stage = 0;
 #pragma unroll 1
       for (int t = tile; t < t1; ++t) {
@@ -230,89 +288,94 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) attn8_few(const __grid_cons
           const int f = t + Sh::NS - 1;
           if (f < t1) {
             const KeyAt k = next;
-            next = key_at(A, u.b, base(f + 1) + (lane & 15), f + 1 < t1 ? u.hi : 0);
+            next = where(f + 1);
             if (k.page == -2) atomicOr(A.err, kErrBadSlot);
-            few_load<D>(A, mine + (stage == 0 ? Sh::NS - 1 : stage - 1) * Sh::STAGE, k, h);
+            few_load<D, NT, ONE>(A, mine + (stage == 0 ? Sh::NS - 1 : stage - 1) * Sh::STAGE, k, h, base(f), lo, hi);
           }
           cp_commit();
         }
         const uint32_t st = mine + stage * Sh::STAGE;
         stage = stage + 1 == Sh::NS ? 0 : stage + 1;
-        // scores of 2 x 8 keys
-        float s[2][4];
+        // scores: keys g and g + 8, rows 2 c and 2 c + 1
+        float s[NT][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            const uint2 w = lds8(st + Sh::k_at(8 * n + g, 2 * i + (c >> 1)) + 8 * (c & 1));
-            mma16816(s[n], qa[i][0], codes_bf16<FMT>(w.x, w.x, 0, 1), codes_bf16<FMT>(w.x, w.x, 2, 3));
-            mma16816(s[n], qa[i][1], codes_bf16<FMT>(w.y, w.y, 0, 1), codes_bf16<FMT>(w.y, w.y, 2, 3));
+        for (int i = 0; i < W; ++i) {
+          const uint2 x = lds8(st + Sh::k_at(g, 2 * i + (c >> 1)) + 8 * (c & 1)), y = lds8(st + Sh::k_at(g + 8, 2 * i + (c >> 1)) + 8 * (c & 1));
+          const uint32_t a0[4] = {codes_bf16<FMT>(x.x, x.x, 0, 1), codes_bf16<FMT>(y.x, y.x, 0, 1), codes_bf16<FMT>(x.x, x.x, 2, 3), codes_bf16<FMT>(y.x, y.x, 2, 3)};
+          const uint32_t a1[4] = {codes_bf16<FMT>(x.y, x.y, 0, 1), codes_bf16<FMT>(y.y, y.y, 0, 1), codes_bf16<FMT>(x.y, x.y, 2, 3), codes_bf16<FMT>(y.y, y.y, 2, 3)};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma16816(s[n], a0, qb[n][i][0], qb[n][i][1]);
+            mma16816(s[n], a1, qb[n][i][2], qb[n][i][3]);
           }
         }
         const int j0 = base(t);
-        float vs[2][2];
-        float top[2] = {-INFINITY, -INFINITY};
-        const bool whole = j0 + kStep <= u.hi && (!A.causal || j0 + kStep - 1 <= pos_min) && (A.window <= 0 || j0 > pos_max - A.window);
+        const uint32_t sc = st + 2 * kStep * D + 4 * g;
+        const float ks[2] = {lds_f(sc) * A.scale2, lds_f(sc + 32) * A.scale2}, vs[2] = {lds_f(sc + 64), lds_f(sc + 96)};
+        const bool whole = j0 + kStep <= hi && (!A.causal || j0 + kStep - 1 <= pos_min) && (A.window <= 0 || j0 > pos_max - A.window);
         unsigned hide = 0;
+        float top[NT][2];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float2 ks = lds_f2(st + 2 * kStep * D + 4 * (8 * n + 2 * c));
-          const float2 vv = lds_f2(st + 2 * kStep * D + 4 * (kStep + 8 * n + 2 * c));
-          vs[n][0] = vv.x;
-          vs[n][1] = vv.y;
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            s[n][e] *= (e & 1 ? ks.y : ks.x) * A.scale2;
+            s[n][e] *= ks[e >> 1];
             if (!whole) {
-              const int j = j0 + 8 * n + 2 * c + (e & 1), p = pos[e >> 1];
-              const bool seen = j < u.hi && (!A.causal || j <= p) && (A.window <= 0 || j > p - A.window);
+              const int j = j0 + g + 8 * (e >> 1), p = pos[n][e & 1];
+              const bool seen = j < hi && (!A.causal || j <= p) && (A.window <= 0 || j > p - A.window);
               if (!seen) {
                 s[n][e] = -INFINITY;
                 hide |= 1u << (4 * n + e);
               }
             }
-            top[e >> 1] = fmaxf(top[e >> 1], s[n][e]);
           }
-        }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
-          top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+          for (int e = 0; e < 2; ++e) {
+            float x = fmaxf(s[n][e], s[n][e + 2]);
+#pragma unroll
+            for (int k = 4; k < 32; k <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
+            top[n][e] = x;
+          }
         }
         // The reference of a row's weights follows its maximum only when that has grown by more than 2^8:
         // weights and sums have room for it, and the results are seldom rescaled.
-        if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
+        bool up = false;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const bool up = top[e] > m[e] + 8.f;  // each row for itself
-            const float to = up ? top[e] : m[e];
-            const float f = up ? ex2(m[e] - to) : 1.f;
-            m[e] = to;
-            l[e] *= f;
+        for (int n = 0; n < NT; ++n) up = up || top[n][0] > m[n][0] + 8.f || top[n][1] > m[n][1] + 8.f;
+        if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-              o[i][2 * e] *= f;
-              o[i][2 * e + 1] *= f;
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const bool mv = top[n][e] > m[n][e] + 8.f;  // each row for itself
+              const float to = mv ? top[n][e] : m[n][e], f = mv ? ex2(m[n][e] - to) : 1.f;
+              m[n][e] = to;
+              l[n][e] *= f;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                o[n][i][e] *= f;
+                o[n][i][e + 2] *= f;
+              }
             }
-          }
         }
-        uint32_t pa[4];
-        const float ref[2] = {finite_or_zero(m[0]), finite_or_zero(m[1])};
+        uint32_t pb[NT][2];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float p0 = ex2(s[n][2 * e] - ref[e]), p1 = ex2(s[n][2 * e + 1] - ref[e]);
-            l[e] += p0 + p1;
-            float w0 = p0 * vs[n][0], w1 = p1 * vs[n][1];
-            if (hide & (1u << (4 * n + 2 * e))) w0 = 0.f;  // whatever the scale of a key that is not seen
-            if (hide & (1u << (4 * n + 2 * e + 1))) w1 = 0.f;
-            pa[2 * n + e] = pack_bf16x2(w0, w1);
+          for (int k = 0; k < 2; ++k) {  // keys g + 8 k
+            const float p0 = ex2(s[n][2 * k] - finite_or_zero(m[n][0])), p1 = ex2(s[n][2 * k + 1] - finite_or_zero(m[n][1]));
+            l[n][0] += p0;
+            l[n][1] += p1;
+            float w0 = p0 * vs[k], w1 = p1 * vs[k];
+            if (hide & (1u << (4 * n + 2 * k))) w0 = 0.f;  // whatever the scale of a key that is not seen
+            if (hide & (1u << (4 * n + 2 * k + 1))) w1 = 0.f;
+            pb[n][k] = transposed(pack_bf16x2(w0, w1));
           }
         // results: keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9, values g D / 8 ..
-        constexpr int W = D / 32;  // words of a lane's slice of a key
         uint32_t w[4][W];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -334,27 +397,27 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) attn8_few(const __grid_cons
           }
         }
 #pragma unroll
-        for (int i = 0; i < W; ++i)
+        for (int i = 0; i < D / 16; ++i) {  // values 2 i and 2 i + 1 of the slices
+          const int x = i >> 1, e = 2 * (i & 1);
+          const uint32_t a[4] = {codes_bf16<FMT>(w[0][x], w[1][x], e, e), codes_bf16<FMT>(w[0][x], w[1][x], e + 1, e + 1),
+                                 codes_bf16<FMT>(w[2][x], w[3][x], e, e), codes_bf16<FMT>(w[2][x], w[3][x], e + 1, e + 1)};
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mma16816(o[4 * i + e], pa, codes_bf16<FMT>(w[0][i], w[1][i], e, e), codes_bf16<FMT>(w[2][i], w[3][i], e, e));
+          for (int n = 0; n < NT; ++n) mma16816(o[n][i], a, pb[n][0], pb[n][1]);
+        }
       }
       cp_wait<0>();
       __syncwarp();  // the ring is the results' now
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-        const int r = g + 8 * e;
-        if (c == 0) *reinterpret_cast<float2*>(res + kFewRows * D + 2 * r) = make_float2(m[e], l[e]);
-        // value 4 i + k of slices 2 c and 2 c + 1
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+        for (int e = 0; e < 2; ++e) {
 #pragma unroll
-          for (int i = 0; i < D / 8; i += 4)
-            *reinterpret_cast<float4*>(res + r * D + (2 * c + q) * (D / 8) + i) =
-                make_float4(o[i][2 * e + q], o[i + 1][2 * e + q], o[i + 2][2 * e + q], o[i + 3][2 * e + q]);
-      }
+          for (int k = 4; k < 32; k <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], k);
+          const int r = 8 * n + 2 * c + e;
+          if (g == 0) *reinterpret_cast<float2*>(res + ROWS * D + 2 * r) = make_float2(m[n][e], l[n][e]);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) *reinterpret_cast<float2*>(res + r * D + g * (D / 8) + 2 * i) = make_float2(o[n][i][e], o[n][i][e + 2]);
+        }
     }
     const bool before = tile > 0, behind = t1 < u.tiles, split = before || behind;
     if (S > 1) __syncthreads();
@@ -362,96 +425,111 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) attn8_few(const __grid_cons
     if (on) {  // a warp writes rows slice, slice + S, ... of its head: the slices joined in order
       const int slot = (int)blockIdx.x * 2 + (before ? 0 : 1);
       for (int r = slice; r < nrows; r += S) {
+        const float* heads = reinterpret_cast<float*>(ring) + wh * (Sh::WARP / 4);
+        const int next_slice = A.HB * (Sh::WARP / 4);
         float top = -INFINITY;
-        for (int k = 0; k < S; ++k) top = fmaxf(top, reinterpret_cast<float*>(ring)[(wh + k * A.HB) * (Sh::WARP / 4) + kFewRows * D + 2 * r]);
+        for (int k = 0; k < S; ++k) top = fmaxf(top, heads[k * next_slice + ROWS * D + 2 * r]);
         const float ref = finite_or_zero(top);
-        float sum = 0.f, acc[D / 32];
+        float sum = 0.f, acc[W];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
+        for (int i = 0; i < W; ++i) acc[i] = 0.f;
+#pragma unroll 4
         for (int k = 0; k < S; ++k) {
-          const float* a = reinterpret_cast<float*>(ring) + (wh + k * A.HB) * (Sh::WARP / 4);
-          const float f = ex2(a[kFewRows * D + 2 * r] - ref);
-          sum += a[kFewRows * D + 2 * r + 1] * f;
+          const float* a = heads + k * next_slice;
+          const float f = ex2(a[ROWS * D + 2 * r] - ref);
+          sum += a[ROWS * D + 2 * r + 1] * f;
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) acc[i] += a[r * D + lane + 32 * i] * f;
+          for (int i = 0; i < W; ++i) acc[i] += a[r * D + lane + 32 * i] * f;
         }
         if (split) {
-          const int64_t at = ((int64_t)slot * A.HB + wh) * kFewRows + r;
+          const int64_t at = ((int64_t)slot * A.HB + wh) * ROWS + r;
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) A.part_o[at * D + lane + 32 * i] = acc[i];
+          for (int i = 0; i < W; ++i) A.part_o[at * D + lane + 32 * i] = acc[i];
           if (lane == 0) *reinterpret_cast<float2*>(A.part_ml + 2 * at) = make_float2(top, sum);
         } else {
           const int row = u.r0 + r, tok = A.group.by(row), hq = h * A.G + row - tok * A.G;
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
           bf16* dst = (bf16*)A.out + (u.s.q0 + tok) * A.ldo + (int64_t)hq * D;
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) dst[lane + 32 * i] = __float2bfloat16_rn(sum == 0.f ? 0.f : acc[i] * inv);
+          for (int i = 0; i < W; ++i) dst[lane + 32 * i] = __float2bfloat16_rn(sum == 0.f ? 0.f : acc[i] * inv);
           if (A.lse && lane == 0) A.lse[(int64_t)(u.s.q0 + tok) * A.Hq + hq] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
         }
       }
     }
-    if (behind && !before && threadIdx.x == 0) {  // the first part of a unit that others continue
-      int* f = A.info + blockIdx.x * kAttnInfo;
-      f[1] = u.b;
-      f[2] = u.blk;
-      f[3] = u.hg;
-      f[0] = parts_behind(plan, at + (u.tiles - 1 - tile));
-    }
+    if (behind && !before && threadIdx.x == 0) tell_join(A, u, parts_behind(plan, num + (u.tiles - 1 - tile)));
     const int nt = t1 - tile;
-    at += nt + kFewBegin;
-    bool more;
-    switch (S) {
-      case 8: more = go_on<kFewRows, 8 * kStep, kFewBegin>(A, u, tile, left, nt); break;
-      case 4: more = go_on<kFewRows, 4 * kStep, kFewBegin>(A, u, tile, left, nt); break;
-      case 2: more = go_on<kFewRows, 2 * kStep, kFewBegin>(A, u, tile, left, nt); break;
-      default: more = go_on<kFewRows, kStep, kFewBegin>(A, u, tile, left, nt);
-    }
-    if (!more) break;
+    num += nt + kFewBegin;
+    if (!few_go_on<ROWS>(A, S, u, tile, left, nt)) break;
     if (S > 1) __syncthreads();
     else __syncwarp();
   }
 }
 
-// Join the parts of the units that the plan divided.  Block (c, wh): head wh of the unit that
-// began in block c of the primary kernel; a warp per row, lanes over the values.
-template <int MR>
-__global__ void __launch_bounds__(256) attn8_join(const __grid_constant__ AttnArgs A) {
+// Join the parts of the units that the plan divided.  A block takes one row after the other, its eight warps the
+// row's parts in turns (all parts of a row are under way at once), a lane D / 32 of the values.
+template <int D>
+__global__ void __launch_bounds__(256) attn8_join(const __grid_constant__ AttnArgs A, int MR, int blocks) {
+  constexpr int W = D / 32;
+  __shared__ int units[1024], count;  // the blocks of the primary kernel in which a divided unit began
+  __shared__ float2 ml[8];
+  __shared__ float part[8][D];
+  const int lane = threadIdx.x & 31, warp = warp_index();
   wait_for_primary();
-  const int c = blockIdx.x, wh = blockIdx.y, lane = threadIdx.x & 31;
-  const int n = A.info[c * kAttnInfo];  // parts in the blocks behind c
-  if (n < 1) return;
-  const int b = A.info[c * kAttnInfo + 1], blk = A.info[c * kAttnInfo + 2], h = A.info[c * kAttnInfo + 3] * A.HB + wh;
-  if (h >= A.Hk) return;
-  const Seq s = seq_at(A, b);
-  const int r0 = blk * MR, nrows = min(MR, s.nq * A.G - r0);
-  // part k: of block c its second place, of the blocks behind it their first
-  const auto place = [&](int k, int r) { return ((int64_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * A.HB + wh) * MR + r; };
-  for (int r = blockIdx.z * 8 + warp_index(); r < nrows; r += 8 * gridDim.z) {
-    float top = -INFINITY;
-    for (int k = lane; k <= n; k += 32) top = fmaxf(top, A.part_ml[2 * place(k, r)]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float ref = finite_or_zero(top);
-    float sum = 0.f, acc[kAttnMaxHeads / 32];
-#pragma unroll
-    for (int i = 0; i < kAttnMaxHeads / 32; ++i) acc[i] = 0.f;
-#pragma unroll 4
-    for (int k = 0; k <= n; ++k) {
-      const int64_t at = place(k, r);
-      const float2 ml = *reinterpret_cast<const float2*>(A.part_ml + 2 * at);
-      const float f = ex2(ml.x - ref);
-      sum += ml.y * f;
-#pragma unroll
-      for (int i = 0; i < kAttnMaxHeads / 32; ++i)
-        if (lane + 32 * i < A.D) acc[i] += A.part_o[at * A.D + lane + 32 * i] * f;
+  if (warp == 0) {
+    int n = 0;
+    for (int c0 = 0; c0 < blocks; c0 += 32) {
+      const bool first = c0 + lane < blocks && A.info[(c0 + lane) * kAttnInfo] > 0;
+      const unsigned b = __ballot_sync(0xffffffffu, first);
+      if (first) units[n + __popc(b & ((1u << lane) - 1u))] = c0 + lane;
+      n += __popc(b);
     }
-    const int row = r0 + r, tok = A.group.by(row), hq = h * A.G + row - tok * A.G;
-    const float inv = 1.f / sum;
-    bf16* dst = (bf16*)A.out + (s.q0 + tok) * A.ldo + (int64_t)hq * A.D;
+    if (lane == 0) count = n;
+  }
+  __syncthreads();
+  const int per = MR * A.HB, total = count * per;
+  for (int x = blockIdx.x; x < total; x += gridDim.x) {
+    const int c = units[x / per], y = x % per, wh = y / MR, r = y - wh * MR;
+    const int* f = A.info + c * kAttnInfo;
+    const int n = f[0], nrows = f[1], row = f[2] + r, q0 = f[3], h = f[4] * A.HB + wh;
+    if (r >= nrows || h >= A.Hk) continue;  // uniform in the block
+    float m = -INFINITY, l = 0.f, acc[W];
 #pragma unroll
-    for (int i = 0; i < kAttnMaxHeads / 32; ++i)
-      if (lane + 32 * i < A.D) dst[lane + 32 * i] = __float2bfloat16_rn(sum == 0.f ? 0.f : acc[i] * inv);
-    if (A.lse && lane == 0) A.lse[(int64_t)(s.q0 + tok) * A.Hq + hq] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    for (int i = 0; i < W; ++i) acc[i] = 0.f;
+#pragma unroll 4
+    for (int k = warp; k <= n; k += 8) {
+      // part k: of block c its second place, of the blocks behind it their first
+      const int64_t at = ((int64_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * A.HB + wh) * MR + r;
+      const float2 p = *reinterpret_cast<const float2*>(A.part_ml + 2 * at);
+      float v[W];
+#pragma unroll
+      for (int i = 0; i < W; ++i) v[i] = A.part_o[at * D + lane + 32 * i];
+      const float to = fmaxf(m, p.x), ref = finite_or_zero(to), f0 = ex2(m - ref), f1 = ex2(p.x - ref);
+      m = to;
+      l = l * f0 + p.y * f1;
+#pragma unroll
+      for (int i = 0; i < W; ++i) acc[i] = acc[i] * f0 + v[i] * f1;
+    }
+    if (lane == 0) ml[warp] = make_float2(m, l);
+#pragma unroll
+    for (int i = 0; i < W; ++i) part[warp][lane + 32 * i] = acc[i];
+    __syncthreads();
+    if ((int)threadIdx.x < D) {
+      float top = ml[0].x;
+#pragma unroll
+      for (int k = 1; k < 8; ++k) top = fmaxf(top, ml[k].x);
+      const float ref = finite_or_zero(top);
+      float sum = 0.f, v = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float e = ex2(ml[k].x - ref);
+        sum += ml[k].y * e;
+        v += part[k][threadIdx.x] * e;
+      }
+      const int tok = A.group.by(row), hq = h * A.G + row - tok * A.G;
+      ((bf16*)A.out)[(q0 + tok) * A.ldo + (int64_t)hq * D + threadIdx.x] = __float2bfloat16_rn(sum == 0.f ? 0.f : v / sum);
+      if (A.lse && threadIdx.x == 0) A.lse[(int64_t)(q0 + tok) * A.Hq + hq] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    }
+    __syncthreads();
   }
 }
 
@@ -487,7 +565,7 @@ __global__ void __launch_bounds__(128) attn8_elem(const __grid_constant__ AttnAr
     for (int i = 0; i < kAttnMaxHeads / 32; ++i) acc[i] = 0.f;
     for (int j0 = first; j0 < last; j0 += 32) {
       const int j = j0 + lane;
-      KeyAt k = key_at(A, b, j, last);
+      KeyAt k = key_at(A, b, j, first, last);
       if (k.page == -2) atomicOr(A.err, kErrBadSlot);
       float sc = -INFINITY, vs = 0.f;
       if (k.page >= 0) {
@@ -546,45 +624,55 @@ FastDiv fast_div(uint32_t d) {
   return {d, (uint32_t)(((1ull << (31 + l)) + d - 1) / d), 31 + l};
 }
 
-// K/V heads of a block of the kernel for few rows: all eight warps on heads of their own where
-// the batch fills the GPU (neighbouring heads' scales share their sectors), fewer, with the
-// keys of a head cut into slices, where it does not: less is left to be joined.
-int few_heads(int64_t B, int Hk, int sms) {
-  int hb = 1;
-  while (hb < kFewWarps && hb < Hk && B * Hk >= (int64_t)sms * hb) hb *= 2;
-  return hb;
+// How the kernel for few rows is used: NT columns of eight rows, and the K/V heads of a block, 1, 2, 4 or 8.  All
+// warps on heads of their own where the batch fills the GPU (neighbouring heads' scales share their sectors),
+// fewer, with the keys of a head cut into slices, where it does not: less is left to be joined.
+struct FewUse {
+  int nt, hb;
+};
+FewUse few_use(int64_t T, int64_t B, int G, int Hk, int sms) {
+  FewUse f{T * G > 8 * B ? 2 : 1, 1};
+  while (f.hb < 8 && f.hb < Hk && B * Hk >= (int64_t)sms * f.hb) f.hb *= 2;
+  return f;
 }
 
-template <int D, int FMT>
+template <int D, int FMT, int NT, bool ONE>
 gbln_status few_go(const AttnArgs& A, int blocks, bool q16, cudaStream_t s) {
-  using Sh = FewShape<D>;
+  using Sh = FewShape<D, NT>;
   static std::atomic<uint64_t> ready{0};  // devices whose limit is raised
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return GBLN_ERR_CUDA;
   if (!(ready.load(std::memory_order_acquire) >> dev & 1)) {
-    if (cudaFuncSetAttribute(attn8_few<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM) != cudaSuccess) {
+    if (cudaFuncSetAttribute(attn8_few<D, FMT, NT, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM) != cudaSuccess) {
       cudaGetLastError();
       return GBLN_ERR_CUDA;
     }
     ready.fetch_or(1ull << dev, std::memory_order_release);
   }
-  attn8_few<D, FMT><<<blocks, 32 * kFewWarps, Sh::SMEM, s>>>(A, q16);
-  return cudaGetLastError() == cudaSuccess ? attn_join_launch(A, blocks, kFewRows, s) : GBLN_ERR_CUDA;
+  attn8_few<D, FMT, NT, ONE><<<blocks, 32 * Sh::WARPS, Sh::SMEM, s>>>(A, q16);
+  return cudaGetLastError() == cudaSuccess ? attn_join_launch(A, blocks, Sh::ROWS, s) : GBLN_ERR_CUDA;
+}
+
+template <int D, int FMT>
+gbln_status few_sized(const AttnArgs& A, int nt, int blocks, bool q16, cudaStream_t s) {
+  const bool one = A.page.d % kStep == 0;
+  if (nt == 1) return one ? few_go<D, FMT, 1, true>(A, blocks, q16, s) : few_go<D, FMT, 1, false>(A, blocks, q16, s);
+  return one ? few_go<D, FMT, 2, true>(A, blocks, q16, s) : few_go<D, FMT, 2, false>(A, blocks, q16, s);
 }
 
 template <int FMT>
-gbln_status few_typed(const AttnArgs& A, int blocks, bool q16, cudaStream_t s) {
+gbln_status few_typed(const AttnArgs& A, int nt, int blocks, bool q16, cudaStream_t s) {
   switch (A.D) {
-    case 64: return few_go<64, FMT>(A, blocks, q16, s);
-    case 96: return few_go<96, FMT>(A, blocks, q16, s);
-    case 128: return few_go<128, FMT>(A, blocks, q16, s);
-    default: return few_go<256, FMT>(A, blocks, q16, s);
+    case 64: return few_sized<64, FMT>(A, nt, blocks, q16, s);
+    case 96: return few_sized<96, FMT>(A, nt, blocks, q16, s);
+    case 128: return few_sized<128, FMT>(A, nt, blocks, q16, s);
+    default: return few_sized<256, FMT>(A, nt, blocks, q16, s);
   }
 }
 
 // Rows for the tensor-core kernel: where a sequence brings more rows on average than the other
 // kernel takes at once, so that K and V would be converted several times over there.
-bool many_rows(int64_t T, int32_t B, int G, int32_t D) { return D <= 128 && T * G > 2 * kFewRows * (int64_t)B; }
+bool many_rows(int64_t T, int32_t B, int G, int32_t D) { return D <= 128 && T * G > 32 * (int64_t)B; }
 
 bool fast_head(int32_t D, int io) { return io == GBLN_BF16 && (D == 64 || D == 96 || D == 128 || D == 256); }
 
@@ -597,7 +685,7 @@ bool attn_sizes_ok(int64_t T, int32_t B, int32_t Hq, int32_t Hk, int32_t D) {
 
 gbln_status attn_join_launch(const AttnArgs& A, int blocks, int rows, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)blocks, (unsigned)A.HB, rows == kFewRows ? 1 : 8);
+  cfg.gridDim = dim3((unsigned)blocks * 4);
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute at{};
@@ -605,7 +693,10 @@ gbln_status attn_join_launch(const AttnArgs& A, int blocks, int rows, cudaStream
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  const cudaError_t e = rows == kFewRows ? cudaLaunchKernelEx(&cfg, attn8_join<kFewRows>, A) : cudaLaunchKernelEx(&cfg, attn8_join<kManyUnit>, A);
+  const cudaError_t e = A.D == 64    ? cudaLaunchKernelEx(&cfg, attn8_join<64>, A, rows, blocks)
+                        : A.D == 96  ? cudaLaunchKernelEx(&cfg, attn8_join<96>, A, rows, blocks)
+                        : A.D == 128 ? cudaLaunchKernelEx(&cfg, attn8_join<128>, A, rows, blocks)
+                                     : cudaLaunchKernelEx(&cfg, attn8_join<256>, A, rows, blocks);
   if (e == cudaSuccess) return GBLN_OK;
   cudaGetLastError();
   return GBLN_ERR_CUDA;
@@ -620,7 +711,8 @@ extern "C" int64_t gbln_attn_cache8_workspace(int64_t T, int32_t B, int32_t Hq, 
   if (T == 0 || B == 0 || !fast_head(D, io)) return 0;
   const int sms = sm_count();
   if (sms <= 0) return -1;
-  const int rows = many_rows(T, B, Hq / Hk, D) ? kManyUnit : few_heads(B, Hk, sms) * kFewRows;
+  const FewUse f = few_use(T, B, Hq / Hk, Hk, sms);
+  const int rows = many_rows(T, B, Hq / Hk, D) ? kManyUnit : f.hb * 8 * f.nt;
   return (int64_t)sms * (kAttnInfo * 4 + 2 * rows * (D + 2) * 4);
 }
 
@@ -643,7 +735,7 @@ extern "C" gbln_status gbln_attn_cache8(const void* q, const int32_t* cu_seqlens
   if (!aligned_to(cu_seqlens_q, 4) || !aligned_to(kv_lens, 4) || !aligned_to(page_table, 4) || !aligned_to(lse, 4)) return GBLN_ERR_INVALID_ARG;
   const int sms = sm_count();
   unsigned int* err = device_error_word();
-  if (sms <= 0 || !err) return GBLN_ERR_CUDA;
+  if (sms <= 0 || sms > 1024 || !err) return GBLN_ERR_CUDA;  // the joining kernel lists the blocks
   AttnArgs A{};
   A.q = q;
   A.out = out;
@@ -673,14 +765,15 @@ extern "C" gbln_status gbln_attn_cache8(const void* q, const int32_t* cu_seqlens
   if (fast_head(D, io) && codes_aligned(k_cache, v_cache, 16)) {
     if (!workspace || !aligned16(workspace) || workspace_bytes < gbln_attn_cache8_workspace(T, B, Hq, Hk, D, io)) return GBLN_ERR_WORKSPACE;
     const bool many = many_rows(T, B, A.G, D);
-    A.HB = many ? 1 : few_heads(B, Hk, sms);
+    const FewUse f = few_use(T, B, A.G, Hk, sms);
+    A.HB = many ? 1 : f.hb;
     A.NHG = (Hk + A.HB - 1) / A.HB;
     A.info = (int*)workspace;
     A.part_ml = (float*)workspace + (int64_t)sms * kAttnInfo;
-    A.part_o = A.part_ml + (int64_t)sms * 2 * 2 * (many ? kManyUnit : A.HB * kFewRows);
+    A.part_o = A.part_ml + (int64_t)sms * 2 * 2 * (many ? kManyUnit : A.HB * 8 * f.nt);
     if (many) return attn_many_launch(A, sms, fmt, s);
     const bool q16 = aligned16(q) && ld_q % 8 == 0;
-    return fmt == GBLN_Q8_INT8 ? few_typed<GBLN_Q8_INT8>(A, sms, q16, s) : few_typed<GBLN_Q8_E4M3>(A, sms, q16, s);
+    return fmt == GBLN_Q8_INT8 ? few_typed<GBLN_Q8_INT8>(A, f.nt, sms, q16, s) : few_typed<GBLN_Q8_E4M3>(A, f.nt, sms, q16, s);
   }
   const unsigned grid = grid_for(T * (int64_t)Hq, 4, (int64_t)sms * 32);
   if (io == GBLN_F32) {

@@ -6,6 +6,10 @@
 
 namespace gbln {
 
+constexpr int kAttnInfo = 8;        // ints of info per block
+
+constexpr int kManyUnit = 256;  // rows of a unit of the kernel for many rows
+
 // Division of n < 2^31 by a fixed d < 2^31: (n m) >> s.
 struct FastDiv {
   uint32_t d, m, s;
@@ -81,7 +85,8 @@ __device__ __forceinline__ void unit_range(const AttnArgs& A, Unit& u) {
   u.r0 = u.blk * MR;
   u.r1 = min(u.r0 + MR, u.s.nq * A.G);
   keys_of(A, u.s, u.r0, u.r1, u.lo, u.hi);
-  u.tiles = max(1, (u.hi - u.lo + TK - 1) / TK);
+  const int lo = MR < kManyUnit ? u.lo & ~15 : u.lo;  // the kernel for few rows begins at multiples of sixteen keys
+  u.tiles = max(1, (u.hi - lo + TK - 1) / TK);
 }
 // The next unit after u; false behind the last.
 template <int MR, int TK>
@@ -219,14 +224,22 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ float finite_or_zero(float m) { return m == -INFINITY ? 0.f : m; }
 
+// What the joining kernel has to know of a unit that began in this block and was divided: the parts in
+// the blocks behind, its rows, where its sequence begins, its heads.
+__device__ __forceinline__ void tell_join(const AttnArgs& A, const Unit& u, int behind) {
+  int* f = A.info + blockIdx.x * kAttnInfo;
+  f[1] = u.r1 - u.r0;
+  f[2] = u.r0;
+  f[3] = u.s.q0;
+  f[4] = u.hg;
+  f[0] = behind;
+}
+
 // Let the kernel that joins the parts come up while this one runs, and wait there for it.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-constexpr int kAttnInfo = 4;        // ints of info per block
 constexpr int kAttnMaxHeads = 512;  // values of a head
-constexpr int kFewRows = 16;        // rows of a unit of the kernel for few rows
-constexpr int kManyUnit = 256;      // and of the kernel for many
 
 // The kernel for many rows (attn8_many.cu), with the one that joins its parts.
 gbln_status attn_many_launch(const AttnArgs& A, int blocks, int fmt, cudaStream_t s);

@@ -605,13 +605,7 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
       }
       tc_before();
     }
-    if (t == 0 && behind && !before && row == 0) {  // the first part of a unit that others continue
-      int* f = A.info + blockIdx.x * kAttnInfo;
-      f[1] = u.b;
-      f[2] = u.blk;
-      f[3] = u.hg;
-      f[0] = parts_behind(sh.plan, num + (u.tiles - 1 - tile));
-    }
+    if (t == 0 && behind && !before && row == 0) tell_join(A, u, parts_behind(sh.plan, num + (u.tiles - 1 - tile)));
     if (after <= 0) break;
     if (!has && nu.r0 + t * kTile < nu.r1) load_q<D>(A, sh, nu, t, q_smem, q16);
     n += nt;
