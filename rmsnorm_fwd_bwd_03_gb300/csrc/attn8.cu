@@ -3,20 +3,29 @@
 // Operator: "Fast-LLM: 高效大语言模型训练框架", §三 框架结构 (attention with RoPE; heads /
 // head_groups for grouped-query attention).  With codes k, v and scales a, b of key j:
 //   s_j = scale a_j (q . k_j),   o = sum_j p_j b_j v_j / sum_j p_j,   p_j = 2^(s_j log2 e - m).
-// INT8 and E4M3 codes are exact in bf16, so the products see the codes themselves: a_j goes
-// onto the score, b_j onto the weight p_j, which is rounded to bf16 for its product (2^-9 of
-// each weight, where the result is rounded to bf16 anyway); scores, weights' sums and results
-// are float32.  A row that sees a key of scale NaN is NaN; a key that it does not see has no
-// part in it.
+// INT8 and E4M3 codes are exact in fp16 and in bf16, so the products see the codes themselves:
+// a_j goes onto the score, b_j onto the weight p_j, which is rounded to 16 bits for its product;
+// scores, weights' sums and results are float32.  A row that sees a key of scale NaN is NaN; a
+// key that it does not see has no part in it.
 //
 // Few rows per sequence (decode, drafts): bound by the cache's bytes, D + 4 per K or V head
 // of a token.  A warp takes 8 or 16 rows (new tokens x heads of a group) of one K/V head and
 // streams its keys, 16 at a time, through a ring in shared memory of its own, without any
 // barrier between warps.  Keys are the 16 rows and queries the 8 columns of the 16 x 8 x 16
 // products (S^T = K Q^T, O^T = V^T P^T): a decode step's few rows then waste little of them.
-// Codes go straight from the ring into the fragments: the order of D within a product is
-// free as long as Q has the same, so that a lane's codes are the bytes it finds next to one
-// another, and O's rows are the values of a lane's slice of V.
+// Codes go straight from the ring into the fragments.  What bounds the kernel beside the memory
+// are the integer instructions that turn codes into 16-bit values (in bf16, six for four codes,
+// they kept that pipe busy at 45% of the memory's rate); in fp16 three are enough:
+//   * INT8: (x & 0x00ff00ff) ^ 0x64806480 is 1152 + code of bytes 0 and 2, x >> 8 gives 1 and 3;
+//   * E4M3: the conversion of two codes at a time.
+// So the order of D within a product of Q and K is that of the bytes (Q is arranged to fit), V
+// comes out of shared memory transposed, four keys to a word, and the rows of the scores are the
+// keys in the order in which those words give them.  fp16's range: a row of Q is scaled by a
+// power of two (exact) to below 2^15; a weight is at most 4 (the row's reference follows its
+// maximum) and stands relative to R, a power of two above all of V's scales so far, times 2^13:
+// it keeps 11 bits down to 2^-27 of R, half a step of what is below is 2^-38 of R.
+
+#include <cuda_fp16.h>
 
 #include <atomic>
 
@@ -39,15 +48,18 @@ struct FewShape {
   static constexpr int WARP = NS * STAGE;  // holds a warp's results (ROWS x (D + 2) floats) at a unit's end
   static constexpr int SMEM = WARPS * WARP;
   static_assert(WARP >= ROWS * (D + 2) * 4 && SMEM <= 227 * 1024 - 512, "results fit the ring, the ring the SM");
-  // Where chunk ch (16 bytes) of row r lies: the lanes that read at once hit different banks.
+  // Where chunk ch (16 bytes) of row r lies: the lanes that read at once hit different banks.  K is read 8 bytes a
+  // lane, four lanes to each of the rows that key_row gives for four lane groups; V 16 bytes of eight rows at a time.
+  template <int FMT>
   static __device__ __forceinline__ int k_at(int r, int ch) {
-    if constexpr (D == 64) return r * D + 16 * (ch ^ ((r >> 1 & 1) << 1));
-    else if constexpr (D % 128 == 0) return r * D + 16 * (ch ^ ((r & 3) << 1));
+    const int x = FMT == GBLN_Q8_INT8 ? r >> 1 & 3 : (r & 1) | (r >> 1 & 2);
+    if constexpr (D % 128 == 0) return r * D + 16 * (ch ^ (x << 1));
+    else if constexpr (D == 64) return r * D + 16 * (ch ^ ((x >> 1) << 1));
     else return r * D + 16 * ch;
   }
   static __device__ __forceinline__ int v_at(int r, int ch) {
-    if constexpr (D == 64) return r * D + 16 * (ch ^ ((r >> 1 & 1) << 1));
-    else if constexpr (D % 128 == 0) return r * D + 16 * (ch ^ ((r >> 1 & 3) << 1));
+    if constexpr (D % 128 == 0) return r * D + 16 * (ch ^ (r & 7));
+    else if constexpr (D == 64) return r * D + 16 * (ch ^ (r >> 1 & 3));
     else return r * D + 16 * ch;
   }
 };
@@ -67,29 +79,41 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
   return r;
 }
-// Bytes ea of a and eb of b as two bf16 values.  INT8: 0x4300 | (x & 0x7f) is 128 + the low
-// seven bits, 0x4300 | (x & 0x80) is 128 or 256: their difference is the code.  E4M3: its
-// exponent and fraction in bf16's places are the value times 2^-120 (a NaN code becomes 480:
-// it comes with the scale NaN).
+// Four codes as two pairs of fp16 values: INT8 bytes (0, 2) and (1, 3), E4M3 bytes (0, 1) and (2, 3).
 template <int FMT>
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t a, uint32_t b, int ea, int eb) {
+__device__ __forceinline__ void codes_f16(uint32_t x, uint32_t& a, uint32_t& b) {
   if constexpr (FMT == GBLN_Q8_INT8) {
-    const uint32_t w = __byte_perm(a, b, 0x4440 + ea + 0x100 * eb);  // high bytes: any, cut below
-    const uint32_t u = (w & 0x007f007fu) | 0x43004300u, s = (w & 0x00800080u) | 0x43004300u;
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), *reinterpret_cast<const __nv_bfloat162*>(&s));
-    return *reinterpret_cast<const uint32_t*>(&r);
+    const __half2 k = __half2half2(__ushort_as_half(0x6480));  // 1152
+    const uint32_t u = (x & 0x00ff00ffu) ^ 0x64806480u, v = ((x >> 8) & 0x00ff00ffu) ^ 0x64806480u;
+    const __half2 p = __hsub2(*reinterpret_cast<const __half2*>(&u), k), q = __hsub2(*reinterpret_cast<const __half2*>(&v), k);
+    a = *reinterpret_cast<const uint32_t*>(&p);
+    b = *reinterpret_cast<const uint32_t*>(&q);
   } else {
-    const uint32_t w = __byte_perm(a, b, 0x4000 + 0x10 * ea + 0x1000 * eb);  // low bytes: any, cut below
-    const uint32_t u = (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u), s = 0x7b807b80u;  // 2^120
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u), *reinterpret_cast<const __nv_bfloat162*>(&s));
-    return *reinterpret_cast<const uint32_t*>(&r);
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}" : "=r"(a), "=r"(b) : "r"(x));
   }
 }
+// The key of a step that row g (half 0) or g + 8 (half 1) of the scores stands for: the pairs above, of a word that
+// holds keys 4 c .. 4 c + 3, are then the keys that a lane's weights have after their transposition.
+template <int FMT>
+__device__ __forceinline__ int key_row(int g, int half) {
+  return FMT == GBLN_Q8_INT8 ? 2 * g + half : 4 * (g >> 1) + (g & 1) + 2 * half;
+}
+// NaN codes of E4M3 as zeros.
+__device__ __forceinline__ uint32_t without_nan(uint32_t x) { return x & ~__vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu); }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two 16 x 16 matrices of bytes, transposed: lane (g, c) gets columns g (words 0, 2) and g + 8 (1, 3), rows 4 c .. 4 c + 3.
+// Lanes 0 .. 15 give the rows of the first, 16 .. 31 of the second.
+__device__ __forceinline__ void ldm_trans(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // P^T's fragment out of P's: an 8 x 8 matrix of 16-bit values transposed across the warp.
@@ -123,7 +147,7 @@ __device__ __forceinline__ KeyAt key_at(const AttnArgs& A, int b, int j, int lo,
 // A step's sixteen keys into a stage.  Where pages are multiples of sixteen slots the step lies in one page
 // (ONE: k is the place of its first key that is seen, the same in all lanes, off of key 0); else k is the
 // place of key (lane & 15).
-template <int D, int NT, bool ONE>
+template <int D, int FMT, int NT, bool ONE>
 __device__ __forceinline__ void few_load(const AttnArgs& A, uint32_t stage, const KeyAt& k, int h, int j0, int lo, int hi) {
   using Sh = FewShape<D, NT>;
   const int lane = threadIdx.x & 31;
@@ -146,7 +170,7 @@ __device__ __forceinline__ void few_load(const AttnArgs& A, uint32_t stage, cons
     for (int i = 0; i < N; ++i) {
       const int x = i * 32 + lane, r = x / CH, ch = x - r * CH;
       const bool on = there && j0 + r >= lo && j0 + r < hi;
-      cp16(stage + Sh::k_at(r, ch), kq + r * A.K.cq.slot + 16 * ch, on);
+      cp16(stage + Sh::template k_at<FMT>(r, ch), kq + r * A.K.cq.slot + 16 * ch, on);
       cp16(stage + kStep * D + Sh::v_at(r, ch), vq + r * A.V.cq.slot + 16 * ch, on);
     }
   } else {
@@ -156,7 +180,7 @@ __device__ __forceinline__ void few_load(const AttnArgs& A, uint32_t stage, cons
       const int page = __shfl_sync(0xffffffffu, k.page, r);
       const uint32_t off = __shfl_sync(0xffffffffu, k.off, r);
       const bool on = page >= 0;
-      cp16(stage + Sh::k_at(r, ch), A.K.q + A.K.cq.at(on ? page : 0, on ? off : 0, h) + 16 * ch, on);
+      cp16(stage + Sh::template k_at<FMT>(r, ch), A.K.q + A.K.cq.at(on ? page : 0, on ? off : 0, h) + 16 * ch, on);
       cp16(stage + kStep * D + Sh::v_at(r, ch), A.V.q + A.V.cq.at(on ? page : 0, on ? off : 0, h) + 16 * ch, on);
     }
   }
@@ -216,6 +240,7 @@ __global__ void __launch_bounds__(32 * FewShape<D, NT>::WARPS, 1) attn8_few(cons
     const bool on = h < A.Hk;
     const int nrows = u.r1 - u.r0;
     float m[NT][2], l[NT][2], o[NT][D / 16][4];
+    float R = 0x1p-100f;  // above all of V's scales so far, a power of two
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       m[n][0] = m[n][1] = -INFINITY;
@@ -251,17 +276,19 @@ __global__ void __launch_bounds__(32 * FewShape<D, NT>::WARPS, 1) attn8_few(cons
           const KeyAt k = next;
           next = where(tile + i + 1);
           if (k.page == -2) atomicOr(A.err, kErrBadSlot);
-          few_load<D, NT, ONE>(A, mine + i * Sh::STAGE, k, h, base(tile + i), lo, hi);
+          few_load<D, FMT, NT, ONE>(A, mine + i * Sh::STAGE, k, h, base(tile + i), lo, hi);
         }
         cp_commit();
       }
-      // Q^T: rows g + 8 n, values 32 i + 8 c ..
+      // Q^T: rows g + 8 n, values 32 i + 8 c .., times a power of two, in the codes' order
       uint32_t qb[NT][W][4];
       int pos[NT][2];
+      float back[NT][2];  // the softmax scale and what undoes that power, of rows 2 c and 2 c + 1
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int r = min(u.r0 + g + 8 * n, u.r1 - 1), tok = A.group.by(r), hq = h * A.G + r - tok * A.G;
         const bf16* src = (const bf16*)A.q + (u.s.q0 + tok) * A.ldq + (int64_t)hq * D + 8 * c;
+        uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < W; ++i) {
           if (q16) {
@@ -275,10 +302,29 @@ __global__ void __launch_bounds__(32 * FewShape<D, NT>::WARPS, 1) attn8_few(cons
             for (int k = 0; k < 4; ++k)
               qb[n][i][k] = reinterpret_cast<const uint16_t*>(src)[32 * i + 2 * k] | (uint32_t) reinterpret_cast<const uint16_t*>(src)[32 * i + 2 * k + 1] << 16;
           }
-        }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) pos[n][e] = first + A.group.by(min(u.r0 + 8 * n + 2 * c + e, u.r1 - 1));
+          for (int k = 0; k < 4; ++k) top = max(top, max(abs_bits(bf16_lo(qb[n][i][k])), abs_bits(bf16_hi(qb[n][i][k]))));
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^(14 - e) for a largest value of 2^e ..; 1 for a row of zeros, or one that is not finite anyway
+        const int e = top == 0 || top >= kInfBits ? 14 : max((int)(top >> 23) - 127, -100);
+        const float by = __uint_as_float((uint32_t)(127 + 14 - e) << 23), undo = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; k += 2) {
+            const float v[4] = {bf16_lo(qb[n][i][k]) * by, bf16_hi(qb[n][i][k]) * by, bf16_lo(qb[n][i][k + 1]) * by, bf16_hi(qb[n][i][k + 1]) * by};
+            qb[n][i][k] = FMT == GBLN_Q8_INT8 ? pack_f16x2(v[0], v[2]) : pack_f16x2(v[0], v[1]);
+            qb[n][i][k + 1] = FMT == GBLN_Q8_INT8 ? pack_f16x2(v[1], v[3]) : pack_f16x2(v[2], v[3]);
+          }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          pos[n][k] = first + A.group.by(min(u.r0 + 8 * n + 2 * c + k, u.r1 - 1));
+          back[n][k] = __shfl_sync(0xffffffffu, undo, 4 * (2 * c + k)) * A.scale2;
+        }
       }
+      const int key0 = key_row<FMT>(g, 0), key1 = key_row<FMT>(g, 1);
       int stage = 0;
 #pragma unroll 1
       for (int t = tile; t < t1; ++t) {
@@ -290,13 +336,13 @@ __global__ void __launch_bounds__(32 * FewShape<D, NT>::WARPS, 1) attn8_few(cons
             const KeyAt k = next;
             next = where(f + 1);
             if (k.page == -2) atomicOr(A.err, kErrBadSlot);
-            few_load<D, NT, ONE>(A, mine + (stage == 0 ? Sh::NS - 1 : stage - 1) * Sh::STAGE, k, h, base(f), lo, hi);
+            few_load<D, FMT, NT, ONE>(A, mine + (stage == 0 ? Sh::NS - 1 : stage - 1) * Sh::STAGE, k, h, base(f), lo, hi);
           }
           cp_commit();
         }
         const uint32_t st = mine + stage * Sh::STAGE;
         stage = stage + 1 == Sh::NS ? 0 : stage + 1;
-        // scores: keys g and g + 8, rows 2 c and 2 c + 1
+        // scores: keys key0 and key1, rows 2 c and 2 c + 1
         float s[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -304,9 +350,13 @@ __global__ void __launch_bounds__(32 * FewShape<D, NT>::WARPS, 1) attn8_few(cons
           for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-          const uint2 x = lds8(st + Sh::k_at(g, 2 * i + (c >> 1)) + 8 * (c & 1)), y = lds8(st + Sh::k_at(g + 8, 2 * i + (c >> 1)) + 8 * (c & 1));
-          const uint32_t a0[4] = {codes_bf16<FMT>(x.x, x.x, 0, 1), codes_bf16<FMT>(y.x, y.x, 0, 1), codes_bf16<FMT>(x.x, x.x, 2, 3), codes_bf16<FMT>(y.x, y.x, 2, 3)};
-          const uint32_t a1[4] = {codes_bf16<FMT>(x.y, x.y, 0, 1), codes_bf16<FMT>(y.y, y.y, 0, 1), codes_bf16<FMT>(x.y, x.y, 2, 3), codes_bf16<FMT>(y.y, y.y, 2, 3)};
+          const uint2 x = lds8(st + Sh::template k_at<FMT>(key0, 2 * i + (c >> 1)) + 8 * (c & 1));
+          const uint2 y = lds8(st + Sh::template k_at<FMT>(key1, 2 * i + (c >> 1)) + 8 * (c & 1));
+          uint32_t a0[4], a1[4];
+          codes_f16<FMT>(x.x, a0[0], a0[2]);
+          codes_f16<FMT>(y.x, a0[1], a0[3]);
+          codes_f16<FMT>(x.y, a1[0], a1[2]);
+          codes_f16<FMT>(y.y, a1[1], a1[3]);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             mma16816(s[n], a0, qb[n][i][0], qb[n][i][1]);
@@ -314,18 +364,19 @@ __global__ void __launch_bounds__(32 * FewShape<D, NT>::WARPS, 1) attn8_few(cons
           }
         }
         const int j0 = base(t);
-        const uint32_t sc = st + 2 * kStep * D + 4 * g;
-        const float ks[2] = {lds_f(sc) * A.scale2, lds_f(sc + 32) * A.scale2}, vs[2] = {lds_f(sc + 64), lds_f(sc + 96)};
+        const uint32_t sc = st + 2 * kStep * D;
+        const float ks[2] = {lds_f(sc + 4 * key0), lds_f(sc + 4 * key1)}, vs[2] = {lds_f(sc + 64 + 4 * key0), lds_f(sc + 64 + 4 * key1)};
         const bool whole = j0 + kStep <= hi && (!A.causal || j0 + kStep - 1 <= pos_min) && (A.window <= 0 || j0 > pos_max - A.window);
         unsigned hide = 0;
         float top[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[n][e] *= ks[e >> 1];
-            if (!whole) {
-              const int j = j0 + g + 8 * (e >> 1), p = pos[n][e & 1];
+          for (int e = 0; e < 4; ++e) s[n][e] = s[n][e] * ks[e >> 1] * back[n][e & 1];
+          if (!whole) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = j0 + (e >> 1 ? key1 : key0), p = pos[n][e & 1];
               const bool seen = j < hi && (!A.causal || j <= p) && (A.window <= 0 || j > p - A.window);
               if (!seen) {
                 s[n][e] = -INFINITY;
@@ -341,68 +392,66 @@ __global__ void __launch_bounds__(32 * FewShape<D, NT>::WARPS, 1) attn8_few(cons
             top[n][e] = x;
           }
         }
-        // The reference of a row's weights follows its maximum only when that has grown by more than 2^8:
-        // weights and sums have room for it, and the results are seldom rescaled.
-        bool up = false;
+        // The reference of a row's weights follows its maximum only when that has grown by more than 2^2, R V's
+        // scales when one is above it: weights have room for it, and the results are seldom rescaled.
+        bool up = vs[0] > R || vs[1] > R;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) up = up || top[n][0] > m[n][0] + 8.f || top[n][1] > m[n][1] + 8.f;
+        for (int n = 0; n < NT; ++n) up = up || top[n][0] > m[n][0] + 2.f || top[n][1] > m[n][1] + 2.f;
         if (__any_sync(0xffffffffu, up)) {
+          float v = fmaxf(fmaxf(vs[0], vs[1]), 0x1p-101f);
+#pragma unroll
+          for (int k = 4; k < 32; k <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, k));
+          const float r = fmaxf(R, __uint_as_float((__float_as_uint(fminf(v, 0x1p120f)) & 0x7f800000u) + 0x00800000u)), fr = R / r;
+          R = r;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const bool mv = top[n][e] > m[n][e] + 8.f;  // each row for itself
+              const bool mv = top[n][e] > m[n][e] + 2.f;  // each row for itself
               const float to = mv ? top[n][e] : m[n][e], f = mv ? ex2(m[n][e] - to) : 1.f;
               m[n][e] = to;
               l[n][e] *= f;
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
-                o[n][i][e] *= f;
-                o[n][i][e + 2] *= f;
+                o[n][i][e] *= f * fr;
+                o[n][i][e + 2] *= f * fr;
               }
             }
         }
+        const float unit = __uint_as_float(0x7f000000u - __float_as_uint(R)) * 8192.f;  // 2^13 / R
         uint32_t pb[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {  // keys g + 8 k
+          for (int k = 0; k < 2; ++k) {  // keys key0, key1
             const float p0 = ex2(s[n][2 * k] - finite_or_zero(m[n][0])), p1 = ex2(s[n][2 * k + 1] - finite_or_zero(m[n][1]));
             l[n][0] += p0;
             l[n][1] += p1;
-            float w0 = p0 * vs[k], w1 = p1 * vs[k];
+            float w0 = p0 * (vs[k] * unit), w1 = p1 * (vs[k] * unit);
             if (hide & (1u << (4 * n + 2 * k))) w0 = 0.f;  // whatever the scale of a key that is not seen
             if (hide & (1u << (4 * n + 2 * k + 1))) w1 = 0.f;
-            pb[n][k] = transposed(pack_bf16x2(w0, w1));
+            pb[n][k] = transposed(pack_f16x2(w0, w1));
           }
-        // results: keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9, values g D / 8 ..
-        uint32_t w[4][W];
+        // results: values 16 i + g and + 8, rows 2 c and 2 c + 1
+        const uint32_t vb = st + kStep * D;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = 2 * c + (k & 1) + 8 * (k >> 1);
-          const uint32_t vb = st + kStep * D;
-          if constexpr (W % 4 == 0) {
+        for (int i = 0; i < D / 16; i += 2) {
+          uint32_t w[4];
+          ldm_trans(w, vb + Sh::v_at(lane & 15, i + (lane >> 4)));
+          if constexpr (FMT != GBLN_Q8_INT8) {
+            if (!whole) {  // a NaN code of a key that some row does not see
 #pragma unroll
-            for (int i = 0; i < W; i += 4) {
-              const uint32_t a = vb + Sh::v_at(r, g * (W / 4) + i / 4);
-              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[k][i]), "=r"(w[k][i + 1]), "=r"(w[k][i + 2]), "=r"(w[k][i + 3]) : "r"(a));
+              for (int k = 0; k < 4; ++k) w[k] = without_nan(w[k]);
             }
-          } else if constexpr (W == 2) {
-            const uint2 v = lds8(vb + Sh::v_at(r, g >> 1) + 8 * (g & 1));
-            w[k][0] = v.x;
-            w[k][1] = v.y;
-          } else {
-#pragma unroll
-            for (int i = 0; i < W; ++i) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[k][i]) : "r"(vb + Sh::v_at(r, 0) + 4 * (g * W + i)));
           }
-        }
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {  // values 2 i and 2 i + 1 of the slices
-          const int x = i >> 1, e = 2 * (i & 1);
-          const uint32_t a[4] = {codes_bf16<FMT>(w[0][x], w[1][x], e, e), codes_bf16<FMT>(w[0][x], w[1][x], e + 1, e + 1),
-                                 codes_bf16<FMT>(w[2][x], w[3][x], e, e), codes_bf16<FMT>(w[2][x], w[3][x], e + 1, e + 1)};
+          for (int k = 0; k < 2; ++k) {
+            uint32_t a[4];
+            codes_f16<FMT>(w[2 * k], a[0], a[2]);
+            codes_f16<FMT>(w[2 * k + 1], a[1], a[3]);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816(o[n][i], a, pb[n][0], pb[n][1]);
+            for (int n = 0; n < NT; ++n) mma16816(o[n][i + k], a, pb[n][0], pb[n][1]);
+          }
         }
       }
       cp_wait<0>();
@@ -416,7 +465,10 @@ __global__ void __launch_bounds__(32 * FewShape<D, NT>::WARPS, 1) attn8_few(cons
           const int r = 8 * n + 2 * c + e;
           if (g == 0) *reinterpret_cast<float2*>(res + ROWS * D + 2 * r) = make_float2(m[n][e], l[n][e]);
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) *reinterpret_cast<float2*>(res + r * D + g * (D / 8) + 2 * i) = make_float2(o[n][i][e], o[n][i][e + 2]);
+          for (int i = 0; i < D / 16; ++i) {
+            res[r * D + 16 * i + g] = o[n][i][e] * (R * 0x1p-13f);
+            res[r * D + 16 * i + g + 8] = o[n][i][e + 2] * (R * 0x1p-13f);
+          }
         }
     }
     const bool before = tile > 0, behind = t1 < u.tiles, split = before || behind;

@@ -138,7 +138,9 @@ __device__ __forceinline__ void wait_for(const Shared& sh, int bar, uint32_t par
 }
 
 // --- codes -> bf16 in shared memory ------------------------------------------
-// Four codes as four bf16 values (the conversions are written out in attn8.cu's codes_bf16).
+// Four codes as four bf16 values.  INT8: 0x4300 | (x & 0x7f) is 128 + the low seven bits, 0x4300 | (x & 0x80) is
+// 128 or 256: their difference is the code.  E4M3: its exponent and fraction in bf16's places are the value
+// times 2^-120 (a NaN code becomes 480: it comes with the scale NaN).
 template <int FMT>
 __device__ __forceinline__ uint2 codes4_bf16(uint32_t x) {
   uint2 r;
