@@ -114,15 +114,82 @@ __device__ __forceinline__ void load_axes(const float2* table, int half, const P
   }
 }
 
+// turn() two values an instruction: the same roundings, each for itself.
+template <int VEC, bool IL>
+__device__ __forceinline__ void turn2(float (&xa)[VEC], float (&xb)[VEC], const float2 (&cs)[VEC]) {
+  if constexpr (IL) {
+    turn<VEC, true>(xa, xb, cs);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) {
+      const float2 a = make_float2(xa[e], xa[e + 1]), b = make_float2(xb[e], xb[e + 1]);
+      const float2 c = make_float2(cs[e].x, cs[e + 1].x), s = make_float2(cs[e].y, cs[e + 1].y);
+      const float2 p = mul2(b, s), y = fma2(a, c, make_float2(-p.x, -p.y)), z = fma2(b, c, mul2(a, s));
+      xa[e] = y.x;
+      xa[e + 1] = y.y;
+      xb[e] = z.x;
+      xb[e + 1] = z.y;
+    }
+  }
+}
+// v times r, then times w (each product rounded); without r: times w.
+template <int VEC>
+__device__ __forceinline__ void times(float (&v)[VEC], const float (&w)[VEC], float r) {
+#pragma unroll
+  for (int e = 0; e < VEC; e += 2) {
+    const float2 y = mul2(mul2(make_float2(v[e], v[e + 1]), both(r)), make_float2(w[e], w[e + 1]));
+    v[e] = y.x;
+    v[e + 1] = y.y;
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void times(float (&v)[VEC], const float (&w)[VEC]) {
+#pragma unroll
+  for (int e = 0; e < VEC; e += 2) {
+    const float2 y = mul2(make_float2(v[e], v[e + 1]), make_float2(w[e], w[e + 1]));
+    v[e] = y.x;
+    v[e + 1] = y.y;
+  }
+}
+
 __device__ __forceinline__ float weight_at(const void* w, int w32, int i) {
   return w32 ? __ldg((const float*)w + i) : to_f32(((const bf16*)w)[i]);
 }
+// VEC weights from i on; single loads where the weights are not aligned (w16).
+template <int VEC>
+__device__ __forceinline__ void weights_at(const void* w, int w32, bool w16, int i, float (&v)[VEC]) {
+  if (!w16) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = weight_at(w, w32, i + e);
+  } else if (w32) {
+#pragma unroll
+    for (int e = 0; e < VEC; e += 4) {
+      const float4 f = __ldg(reinterpret_cast<const float4*>((const float*)w + i + e));
+      v[e] = f.x;
+      v[e + 1] = f.y;
+      v[e + 2] = f.z;
+      v[e + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; e += 4) {
+      const uint2 f = __ldg(reinterpret_cast<const uint2*>((const bf16*)w + i + e));
+      v[e] = bf16_lo(f.x);
+      v[e + 1] = bf16_hi(f.x);
+      v[e + 2] = bf16_lo(f.y);
+      v[e + 3] = bf16_hi(f.y);
+    }
+  }
+}
 template <int VEC>
 __device__ __forceinline__ void load_weights(const void* w, int w32, int ia, int half, bool on, float (&wa)[VEC], float (&wb)[VEC]) {
+  if (w && on) {
+    const bool w16 = (reinterpret_cast<uintptr_t>(w) & 15u) == 0;
+    weights_at<VEC>(w, w32, w16, ia, wa);
+    weights_at<VEC>(w, w32, w16, half + ia, wb);
+  } else {
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    wa[e] = w && on ? weight_at(w, w32, ia + e) : 1.f;
-    wb[e] = w && on ? weight_at(w, w32, half + ia + e) : 1.f;
+    for (int e = 0; e < VEC; ++e) wa[e] = wb[e] = 1.f;
   }
 }
 template <int VEC>
@@ -141,7 +208,9 @@ __device__ __forceinline__ float rstd_of(float sum, int D, float eps) {
 
 // How a launch's warps share the work: every token has nq chunks of query head rows
 // and nk of K (and V) head rows; warp w of all has chunk w % (nq + nk) of the tokens
-// w / (nq + nk), that + stride, ...
+// w / (nq + nk), that + stride, ...  Neighbouring warps so read one token's row together.
+// (Warps given to the two kinds by their rows, the kinds apart, wasted none of them on small
+// chunks, but read Q and K of a token at different times: 65536 tokens of 32 / 8 heads of 128 230 and 244 us.)
 struct Split {
   int nu, lg;         // lanes in use per head row, log2 of the lanes of its group
   int nq, qch, qlt;   // chunks, head rows per lane in each, log2 of the tokens a warp takes at once
@@ -196,7 +265,7 @@ __device__ __forceinline__ void heads_rows(const HeadArgs<T>& A, const Split& W,
   Pos p;
   p.load(A.pos, A.ax, min(t0 + P.sub, end));
   float wa[VEC], wb[VEC];
-  load_weights<VEC>(w, A.w32, P.ia, half, P.on, wa, wb);
+  bool have = false;  // the weights: asked for behind the first rows, as most warps have one step
 #pragma unroll 1
   for (; t0 < A.rows; t0 += step) {
     const int64_t t = t0 + P.sub;
@@ -214,6 +283,8 @@ __device__ __forceinline__ void heads_rows(const HeadArgs<T>& A, const Split& W,
         b[j].load(src + h * A.D + half);
       }
     }
+    if (!have) load_weights<VEC>(w, A.w32, P.ia, half, P.on, wa, wb);
+    have = true;
     const bool ok = p.ok(A.max_pos);
     float2 cs[VEC];
     load_axes<VEC, IL>(A.table, half, p, A.ax, codes, ok, P.on, P.ia, A.sign, cs);
@@ -245,13 +316,10 @@ __device__ __forceinline__ void heads_rows(const HeadArgs<T>& A, const Split& W,
         b[j].get(xb);
         if (w) {
           const float r = rstd_of(ss[j], A.D, A.eps);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            xa[e] = __fmul_rn(__fmul_rn(xa[e], r), wa[e]);
-            xb[e] = __fmul_rn(__fmul_rn(xb[e], r), wb[e]);
-          }
+          times<VEC>(xa, wa, r);
+          times<VEC>(xb, wb, r);
         }
-        turn<VEC, IL>(xa, xb, cs);
+        turn2<VEC, IL>(xa, xb, cs);
         Run::store(dst + h * A.D, xa);
         Run::store(dst + h * A.D + half, xb);
       }
@@ -276,7 +344,7 @@ __device__ __forceinline__ void heads_cache(const HeadArgs<T>& A, const Split& W
   p.load(A.pos, A.ax, min(t0 + P.sub, end));
   int64_t slot = __ldg(A.S.slots + min(t0 + P.sub, end));
   float wa[VEC], wb[VEC];
-  load_weights<VEC>(A.wk, A.w32, P.ia, half, P.on, wa, wb);
+  bool have = false;
 #pragma unroll 1
   for (; t0 < A.rows; t0 += step) {
     const int64_t t = t0 + P.sub;
@@ -295,6 +363,8 @@ __device__ __forceinline__ void heads_cache(const HeadArgs<T>& A, const Split& W
         b[j].load(src + half);
       }
     }
+    if (!have) load_weights<VEC>(A.wk, A.w32, P.ia, half, P.on, wa, wb);
+    have = true;
     const bool ok = p.ok(A.max_pos);
     float2 cs[VEC];
     load_axes<VEC, IL>(A.table, half, p, A.ax, codes, ok, P.on, P.ia, 1.f, cs);
@@ -319,12 +389,9 @@ __device__ __forceinline__ void heads_cache(const HeadArgs<T>& A, const Split& W
       b[j].get(xb[j]);
       if (j < KP) {
         ss[j] = sum_squares<VEC>(xa[j], xb[j]);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {  // rstd is the head's: it goes into the scale
-          xa[j][e] = __fmul_rn(xa[j][e], wa[e]);
-          xb[j][e] = __fmul_rn(xb[j][e], wb[e]);
-        }
-        turn<VEC, IL>(xa[j], xb[j], cs);
+        times<VEC>(xa[j], wa);  // rstd is the head's: it goes into the scale
+        times<VEC>(xb[j], wb);
+        turn2<VEC, IL>(xa[j], xb[j], cs);
       }
       m[j] = P.on ? max(abs_max_bits<VEC>(xa[j]), abs_max_bits<VEC>(xb[j])) : 0u;
     }
@@ -384,7 +451,7 @@ __device__ __forceinline__ void heads_cache(const HeadArgs<T>& A, const Split& W
 
 // Rows per lane and blocks per SM: a large share of a token, or a small one where tokens
 // are few or narrow.
-constexpr int kRowsLarge = 6, kRowsSmall = 2, kSmallBlocks = 3;
+constexpr int kRowsLarge = 4, kRowsSmall = 2, kSmallBlocks = 3;
 constexpr int rows_of(bool small, int bytes) { return (small ? kRowsSmall : kRowsLarge) * (16 / bytes); }
 
 template <typename T, bool IL, int FMT, int VEC, bool SMALL>
@@ -777,7 +844,8 @@ gbln_status fwd_vec_launch(const HeadArgs<T>& A, int sms, cudaStream_t s) {
   constexpr int B = VEC * sizeof(T), SQ = rows_of(true, B), LQ = rows_of(false, B);
   Split W = split_of(A.Hq, A.Hk, A.D, VEC, SQ, FMT < 0 ? SQ : 1);
   const int64_t warps = token_groups(W, A.rows) * (W.nq + W.nk);
-  const bool small = warps <= (int64_t)sms * kSmallBlocks * kHeadWarps || W.nq + W.nk <= (FMT < 0 ? 1 : 2);
+  bool small = warps <= (int64_t)sms * kSmallBlocks * kHeadWarps;
+  if constexpr (B != 16) small = small || W.nq + W.nk <= (FMT < 0 ? 1 : 2);
   if (!small) W = split_of(A.Hq, A.Hk, A.D, VEC, LQ, FMT < 0 ? LQ : 2);
   const int n = W.nq + W.nk;
   // eight times the resident blocks leave a warp a few steps to ask ahead for and the scheduler something to balance
@@ -812,7 +880,7 @@ gbln_status fwd_typed(const HeadArgs<T>& A, bool il, int fmt, const gbln_cache8*
 
 // Blocks (partial rows) of the backward pass: by the sizes alone, whatever path the addresses allow.
 int64_t bwd_blocks(int64_t T, int32_t Hq, int32_t Hk, int sms) {
-  const int64_t rows = (int64_t)Hq + Hk, few = (rows + 31) / 32 + 1;  // a warp at least for every chunk
+  const int64_t rows = (int64_t)Hq + Hk, few = (rows + 15) / 16 + 1;  // a warp at least for every chunk of two rows
   const int64_t P = grid_for(T * rows, 4 * kHeadWarps, (int64_t)sms * kBwdBlocks);
   return rows <= kMaxRows && P < few ? few : P;
 }

@@ -108,6 +108,14 @@ def test_head_counts(Hq, Hk):
     _case(5, Hq, Hk, 128, "bf16", "f32", 1, packed=True)
 
 
+@pytest.mark.parametrize("D,Hq,Hk", [(512, 300, 3), (512, 40, 20), (256, 200, 8)])
+def test_many_wide_heads(D, Hq, Hk):
+    """More chunks of a token than a few tokens bring blocks."""
+    _case(1, Hq, Hk, D, "bf16", "bf16", 2)
+    _case(3, Hq, Hk, D, "f32" if D == 256 else "bf16", "f32", 1)
+    _case(150, Hq, Hk, D, "bf16", "f32", 1)
+
+
 @pytest.mark.parametrize("off", [1, 2, 4, 8])
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_alignment(io, off):
@@ -119,6 +127,14 @@ def test_alignment(io, off):
 def test_token_counts(T):
     _case(T, 16, 8, 128, "bf16", "bf16", 1, packed=True)
     _case(T, 14, 2, 64, "f32", "f32", 3)
+
+
+@pytest.mark.parametrize("Hq,Hk,D", [(16, 8, 128), (2, 1, 64), (7, 1, 96), (64, 8, 64), (1, 0, 128), (4, 4, 256), (3, 1, 72)])
+@pytest.mark.parametrize("pairing", ["half", "interleaved"])
+def test_many_tokens(Hq, Hk, D, pairing):
+    """Enough for the persistent kernels: warps that take several steps, several tokens at once."""
+    _case(9001, Hq, Hk, D, "bf16", "bf16", 1 + Hq % 3, pairing, packed=True)
+    _case(6007, Hq, Hk, D, "f32", "f32", 2, pairing)
 
 
 def test_in_place_and_packed_gradient():
@@ -189,7 +205,7 @@ def _norm_window(x64, w64):
                                         ("bf16", 128, 0, 8)])
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 def test_cache(io, D, Hq, Hk, fmt, pairing):
-    for T, n, norm in ((1, 1, True), (45, 3, True), (700, 1, True), (33, 2, False)):
+    for T, n, norm in ((1, 1, True), (45, 3, True), (700, 1, True), (5003, 2, True), (33, 2, False)):
         s = _setup(T, max(Hq, 1), Hk, D, io, "f32" if io == "f32" or n > 1 else "bf16", n, pairing, True, 0, T)
         q = s["q"] if Hq else None
         r = np.random.default_rng(T)
