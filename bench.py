@@ -614,7 +614,8 @@ def run_next_ops(args, wl, device):
     """Time the operators beyond the step (gated units with other activations and
     packed layouts, plain activations, strided / interleaved RoPE, LayerNorm,
     MXFP8 and row-scaled FP8 outputs of the RMSNorm and SwiGLU forwards, 8-bit
-    activation checkpoints with their backward passes, the quantised K/V cache) at
+    activation checkpoints with their backward passes, the quantised K/V cache,
+    per-head norms with the rotation, position axes, attention over the cache) at
     the workload's widths: K launches each, CUDA events around each launch, L2
     flushed in between.  One JSON line with per-operator time and GB/s."""
     import rmsnorm_fwd_bwd_03_gb300 as gb
@@ -708,6 +709,29 @@ def run_next_ops(args, wl, device):
     head8 = 2 * Hk * (D + 4)
     ops["rope_fwd_packed_qkv_cache8"] = (lib.gbln_rope_fwd_cache8, (p(qkv), p(qkv) + Hq * D * b, p(qkv) + (Hq + Hk) * D * b, p(q), p(pos), p(table), table.shape[0], p(slots), *kv8, T, Hq, Hk, D, W, W, W, Hq * D, 0, int8, io, s), T * (2 * Hq * D * b + 2 * Hk * D * b + head8 + 12))
     ops["cache8_read"] = (lib.gbln_cache8_read, (p(slots), *kv8, p(ko), p(k), T, Hk, D, Hk * D, Hk * D, int8, io, s), T * (head8 + 2 * Hk * D * b + 8))
+
+    # Between the QKV projection and attention: norms of the heads with the rotation, three
+    # position axes, the form that fills the cache; attention of a decode step of 32 tokens
+    # over the cache just filled (every sequence T / 32 tokens long).
+    wqk = [(1 + 0.1 * torch.randn(D, generator=g, device=device)).to(dt) for _ in range(2)]
+    three = gb.rope_axes((D // 2 - 2 * (D // 6), D // 6, D // 6))
+    pos3 = pos.repeat(3, 1)
+    plain, axes = (p(pos), 0, 1, None, p(table), table.shape[0]), (p(pos3), T, 3, three, p(table), table.shape[0])
+    packed_qk = (p(qkv), p(qkv) + Hq * D * b)
+    heads = T * (Hq + Hk) * D * b
+    ops["qk_norm_rope_fwd_packed_qkv"] = (lib.gbln_qk_norm_rope_fwd, (*packed_qk, p(wqk[0]), p(wqk[1]), p(qo), p(ko), *plain, T, Hq, Hk, D, W, W, Hq * D, Hk * D, wl.eps, 0, io, io, s), 2 * heads + 4 * T)
+    Pqk = gb.qk_norm_rope_bwd_num_partials(T, Hq, Hk, D)
+    partqk = f32(Pqk, 2 * D)
+    ops["qk_norm_rope_bwd"] = (lib.gbln_qk_norm_rope_bwd, (p(q), p(k), *packed_qk, p(wqk[0]), p(wqk[1]), p(qo), p(ko), p(partqk), Pqk, *plain, T, Hq, Hk, D, Hq * D, Hk * D, W, W, Hq * D, Hk * D, wl.eps, 0, io, io, s), 3 * heads + 4 * T)
+    ops["rope_axes_fwd_three"] = (lib.gbln_rope_axes_fwd, (p(q), p(k), p(qo), p(ko), *axes, T, Hq, Hk, D, Hq * D, Hk * D, Hq * D, Hk * D, 0, io, s), 2 * heads + 12 * T)
+    ops["qk_norm_rope_fwd_packed_qkv_cache8"] = (lib.gbln_qk_norm_rope_fwd_cache8, (*packed_qk, p(qkv) + (Hq + Hk) * D * b, p(wqk[0]), p(wqk[1]), p(qo), *plain, p(slots), *kv8, T, Hq, Hk, D, W, W, W, Hq * D, wl.eps, 0, int8, io, io, s), T * (2 * Hq * D * b + 2 * Hk * D * b + head8 + 12))
+    if T % (32 * page) == 0:
+        B = 32
+        cu = torch.arange(B + 1, dtype=torch.int32, device=device)
+        lens = torch.full((B,), T // B, dtype=torch.int32, device=device)
+        pt = torch.arange(T // page, dtype=torch.int32, device=device).view(B, -1)
+        ws = u8(max(1, gb.attn_cache8_workspace(B, B, Hq, Hk, D, dt)))
+        ops["attn_cache8_decode_32"] = (lib.gbln_attn_cache8, (p(q), p(cu), p(lens), p(pt), pt.shape[1], *kv8, p(qo), None, p(ws), ws.numel(), B, B, Hq, Hk, D, Hq * D, Hq * D, D ** -0.5, 1, 0, int8, io, s), T * (head8 + 4 / page) + 2 * B * Hq * D * b)
 
     flush = L2Flush(device)
     peak, peak_kind = _measured_peak()

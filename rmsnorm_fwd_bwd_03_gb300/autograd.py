@@ -10,7 +10,13 @@ computes anything itself.
   The weight gradient comes from the two-pass fixed-order reduction (float32,
   cast to the weight's dtype).
 * ``rotary(q, k, positions, cos_sin)`` -> ``(q', k')``: RoPE on Q and K
-  (rotate-half pairing); the backward pass is the inverse rotation.
+  (rotate-half pairing); the backward pass is the inverse rotation.  With ``axes``
+  (``rope_axes``) positions are [axes, T], a position for every axis.
+* ``qk_norm_rotary(q, k, q_weight, k_weight, positions, cos_sin, eps)`` -> ``(q', k')``:
+  RMSNorm of every head of Q and K, then the rotation, in one pass; q and k may be
+  slices of one packed projection output.  The backward pass reads q and k again
+  (nothing else is kept); the weights' gradients come from a fixed-order reduction
+  (float32, cast to the weights' dtype).
 * ``swiglu(gate, up)`` -> ``silu(gate) * up``.
 
 ``rms_norm`` and ``swiglu`` take ``checkpoint="int8"`` or ``"e4m3"``: what the backward
@@ -27,8 +33,9 @@ from __future__ import annotations
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (glu_bwd_ckpt8, glu_fwd_ckpt8, rmsnorm_bwd, rmsnorm_bwd_ckpt8, rmsnorm_dw_finalize,
-               rmsnorm_fwd, rmsnorm_fwd_ckpt8, rope_bwd, rope_fwd, swiglu_bwd, swiglu_fwd)
+from . import (glu_bwd_ckpt8, glu_fwd_ckpt8, qk_norm_dw_finalize, qk_norm_rope_bwd, qk_norm_rope_fwd, rmsnorm_bwd,
+               rmsnorm_bwd_ckpt8, rmsnorm_dw_finalize, rmsnorm_fwd, rmsnorm_fwd_ckpt8, rope_axes_bwd, rope_axes_fwd,
+               rope_bwd, rope_fwd, swiglu_bwd, swiglu_fwd)
 
 
 def _c(t):
@@ -94,8 +101,58 @@ class _Rotary(torch.autograd.Function):
         return dqi, dki, None, None
 
 
-def rotary(q, k, positions, cos_sin):
+def _heads_in_rows(t):
+    """t [T, H, D] with its heads next to one another in each token row, as it lies where it does so."""
+    ok = t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == t.shape[2]) and (t.shape[0] == 1 or t.stride(0) >= t.shape[1] * t.shape[2])
+    return t if ok else t.contiguous()
+
+
+class _RotaryAxes(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, positions, cos_sin, axes, pairing):
+        ctx.save_for_backward(positions, cos_sin)
+        ctx.how = (axes, pairing)
+        return rope_axes_fwd(_heads_in_rows(q), _heads_in_rows(k), positions, cos_sin, axes, pairing=pairing)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq, dk):
+        positions, cos_sin = ctx.saved_tensors
+        axes, pairing = ctx.how
+        dqi, dki = rope_axes_bwd(_heads_in_rows(dq), _heads_in_rows(dk), positions, cos_sin, axes, pairing=pairing)
+        return dqi, dki, None, None, None, None
+
+
+def rotary(q, k, positions, cos_sin, axes=None, pairing="half"):
+    if axes is not None:
+        return _RotaryAxes.apply(q, k, positions, cos_sin, bytes(axes), pairing)
+    if pairing != "half":
+        return _RotaryAxes.apply(q, k, positions[None], cos_sin, bytes(q.shape[-1] // 2), pairing)
     return _Rotary.apply(q, k, positions, cos_sin)
+
+
+class _QKNormRotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, positions, cos_sin, eps, axes, pairing):
+        q, k = _heads_in_rows(q), _heads_in_rows(k)
+        q_weight, k_weight = q_weight.contiguous(), k_weight.contiguous()
+        ctx.save_for_backward(q, k, q_weight, k_weight, positions, cos_sin)
+        ctx.how = (eps, axes, pairing)
+        return qk_norm_rope_fwd(q, k, q_weight, k_weight, positions, cos_sin, eps, axes=axes, pairing=pairing)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq, dk):
+        q, k, q_weight, k_weight, positions, cos_sin = ctx.saved_tensors
+        eps, axes, pairing = ctx.how
+        dqi, dki, part, P = qk_norm_rope_bwd(_heads_in_rows(dq), _heads_in_rows(dk), q, k, q_weight, k_weight, positions, cos_sin, eps,
+                                             axes=axes, pairing=pairing)
+        dwq, dwk = qk_norm_dw_finalize(part, P)
+        return dqi, dki, dwq.to(q_weight.dtype), dwk.to(k_weight.dtype), None, None, None, None, None
+
+
+def qk_norm_rotary(q, k, q_weight, k_weight, positions, cos_sin, eps, axes=None, pairing="half"):
+    return _QKNormRotary.apply(q, k, q_weight, k_weight, positions, cos_sin, float(eps), None if axes is None else bytes(axes), pairing)
 
 
 class _SwiGLU(torch.autograd.Function):

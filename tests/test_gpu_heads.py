@@ -332,3 +332,31 @@ def test_binding_refuses():
         gb.qk_norm_rope_fwd(*ok[:6], -1.0, **a)
     with pytest.raises(gb.GblnError):
         gb.qk_norm_rope_bwd(s["dq"], s["dk"], *ok, dw_partial=torch.zeros((0, 128), device="cuda"), **a)
+
+
+@pytest.mark.parametrize("n", [1, 3])
+@pytest.mark.parametrize("pairing", ["half", "interleaved"])
+def test_autograd(n, pairing):
+    """The wrappers on slices of one packed projection output: the gradients of the formulas."""
+    from rmsnorm_fwd_bwd_03_gb300 import autograd as ga
+    T, Hq, Hk, D = 40, 4, 2, 64
+    s = _setup(T, Hq, Hk, D, "bf16", "bf16", n, pairing, False, 0, 11)
+    qkv = _randn((T, (Hq + 2 * Hk) * D), torch.bfloat16, 12).requires_grad_()
+    wq, wk = s["wq"].clone().requires_grad_(), s["wk"].clone().requires_grad_()
+    q, k, v = (t.unflatten(1, (-1, D)) for t in qkv.split([Hq * D, Hk * D, Hk * D], dim=1))
+    yq, yk = ga.qk_norm_rotary(q, k, wq, wk, s["positions"], s["table"], EPS, axes=s["axes"], pairing=pairing)
+    torch.autograd.backward([yq, yk, v], [s["dq"], s["dk"], torch.ones_like(v)])
+    args = (s["pos"], s["axis"], THETA, EPS, pairing)
+    g64, x64 = to64(qkv.grad).reshape(T, -1, D), to64(qkv).reshape(T, -1, D)
+    for sl, y, d, w in ((slice(0, Hq), yq, s["dq"], wq), (slice(Hq, Hq + Hk), yk, s["dk"], wk)):
+        check_io(to64(y), heads.norm_rotate(x64[:, sl], to64(w), *args), "bf16", "y")
+        dx, dw = heads.norm_rotate_bwd(to64(d), x64[:, sl], to64(w), *args)
+        check_io(g64[:, sl], dx, "bf16", "dx")
+        check_io(to64(w.grad), dw, "bf16", "dw")
+    assert (g64[:, Hq + Hk:] == 1).all()
+    a, b = s["q"].clone().requires_grad_(), s["k"].clone().requires_grad_()
+    out = ga.rotary(a, b, s["positions"], s["table"], axes=s["axes"], pairing=pairing)
+    torch.autograd.backward(out, [s["dq"], s["dk"]])
+    for x, y, d in ((a, out[0], s["dq"]), (b, out[1], s["dk"])):
+        check_io(to64(y), heads.rotate(to64(x), *args[:3], pairing), "bf16", "rotated")
+        check_io(to64(x.grad), heads.rotate(to64(d), *args[:3], pairing, back=True), "bf16", "rotated back")
