@@ -109,6 +109,16 @@ __device__ __forceinline__ void tm_st16(uint32_t at, const uint32_t (&v)[16]) {
       : "memory");
 }
 
+// 16 bytes that come while other work goes on (zeros, and no read, where off).
+__device__ __forceinline__ void cp_async16(uint32_t to, const void* from, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// A whole sector: rows of results lie apart, and with half a sector per lane their stores took twice as long.
+__device__ __forceinline__ void store_32b(void* to, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), GBLN_W8(v, 0) : "memory");
+}
+
 // A value that is not computed ahead of its place: all descriptors of a tile at once spill.
 __device__ __forceinline__ uint32_t here(uint32_t v) {
   asm volatile("" : "+r"(v));
@@ -363,45 +373,44 @@ __device__ __forceinline__ void products(const AttnArgs& A, Shared& sh, uint32_t
   }
 }
 
-// Tile t of a unit's rows into shared memory (zeros behind the last row), each of the tile's warps its own 32: eight
-// lanes take a row's 128 bytes, and all loads are under way before the first is stored.
+// Tile t of a unit's rows on their way into shared memory (zeros behind the last row), each of the tile's warps its own
+// 32: eight lanes take a row's 128 bytes, no copy waits for another.
 template <int D>
-__device__ __forceinline__ void load_q(const AttnArgs& A, Shared& sh, const Unit& u, int t, uint32_t q_smem, bool q16) {
+__device__ __forceinline__ void fetch_q(const AttnArgs& A, const Unit& u, int t, uint32_t q_smem, bool q16) {
   using M = ManyShape<D>;
   const int lane = threadIdx.x & 31, c = lane & 7, row0 = 32 * (warp_index() & 3) + (lane >> 3);
+  const int r0 = u.r0 + t * kTile, r1 = u.r1, hg = u.hg;
+  const bf16* q = (const bf16*)A.q + (int64_t)u.s.q0 * A.ldq + (int64_t)hg * A.G * D + 8 * c;
+  const uint32_t to = q_smem + t * M::TILE;
+#pragma unroll 4
+  for (int i = 0; i < 8; ++i) {
+    const int row = row0 + 4 * i;
+    const bool on = r0 + row < r1;
+    uint32_t tok, g;
+    A.group.split((uint32_t)(on ? r0 + row : r0), tok, g);
+    const bf16* src = q + (int64_t)tok * A.ldq + (int)g * D;
 #pragma unroll
-  for (int p = 0; p < M::PLANES; ++p) {
-    uint4 w[8];
+    for (int p = 0; p < M::PLANES; ++p) {
+      if (64 * p + 8 * c >= D) continue;
+      const uint32_t at = to + p * M::PLANE + row * 128 + 16 * (c ^ (row & 7));
+      if (q16) {
+        cp_async16(at, src + 64 * p, on);
+      } else {
+        uint32_t v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = u.r0 + t * kTile + row0 + 4 * i;
-      w[i] = make_uint4(0, 0, 0, 0);
-      if (r < u.r1 && 64 * p + 8 * c < D) {
-        uint32_t tok, g;
-        A.group.split((uint32_t)r, tok, g);
-        const bf16* src = (const bf16*)A.q + (int64_t)(u.s.q0 + (int)tok) * A.ldq + (int64_t)(u.hg * A.G + (int)g) * D + 64 * p + 8 * c;
-        if (q16) {
-          w[i] = ld_reuse(src);
-        } else {
-          uint32_t v[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = reinterpret_cast<const uint16_t*>(src)[k];
-          w[i] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
-        }
+        for (int k = 0; k < 8; ++k) v[k] = on ? reinterpret_cast<const uint16_t*>(src)[64 * p + k] : 0;
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v[0] | v[1] << 16), "r"(v[2] | v[3] << 16), "r"(v[4] | v[5] << 16),
+                     "r"(v[6] | v[7] << 16)
+                     : "memory");
       }
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int row = row0 + 4 * i;
-      if (64 * p + 8 * c < D)
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(q_smem + t * M::TILE + p * M::PLANE + row * 128 + 16 * (c ^ (row & 7))), "r"(w[i].x),
-                     "r"(w[i].y), "r"(w[i].z), "r"(w[i].w)
-                     : "memory");
-    }
   }
+}
+__device__ __forceinline__ void q_has_come(Shared& sh, int t) {
+  cp_wait_all();
   fence_proxy_async_smem();
   __syncwarp();
-  if (lane == 0) mbar_arrive(&sh.bar[kQFull + t]);
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.bar[kQFull + t]);
 }
 
 // The largest of a row's scores: 32 columns from key col of the step on, times K's scales, of the keys it sees.
@@ -452,7 +461,7 @@ __device__ __forceinline__ void weights_of(const uint32_t (&s)[32], const float*
 
 // The four warps of tile t of rows.
 template <int D>
-__device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t q_smem, int t, bool q16, bool o16, uint32_t& late) {
+__device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t q_smem, int t, bool q16, int o_align, uint32_t& late) {
   const int warp = warp_index() & 3, lane = threadIdx.x & 31, row = 32 * warp + lane;
   const uint32_t lanes = (uint32_t)(32 * warp) << 16;
   const uint32_t s_at = sh.tmem + t * kTile + lanes, o_at = sh.tmem + 2 * kTile + t * kTile + lanes;
@@ -463,7 +472,10 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
   int tile = sh.plan.tile;
   int64_t left = sh.plan.left, num = sh.plan.at;
   uint32_t n = 0, rounds = 0, done = 0;  // tiles of keys, steps and phases of kODone so far
-  if (own[0].r0 + t * kTile < own[0].r1) load_q<D>(A, sh, own[0], t, q_smem, q16);
+  if (own[0].r0 + t * kTile < own[0].r1) {
+    fetch_q<D>(A, own[0], t, q_smem, q16);
+    q_has_come(sh, t);
+  }
   for (;;) {
     const Unit& u = own[which];
     const int nt = (int)min((int64_t)(u.tiles - tile), left);
@@ -562,10 +574,12 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.bar[kPFull + 2 * t + buf]);
       }
-      // the next unit's rows (the last scores have been read: the place is free), then this one's results
-      if (after > 0 && nu.r0 + t * kTile < nu.r1) load_q<D>(A, sh, nu, t, q_smem, q16);
+      // the next unit's rows (the last scores have been read: the place is free) before this one's results
+      const bool next = after > 0 && nu.r0 + t * kTile < nu.r1;
+      if (next) fetch_q<D>(A, nu, t, q_smem, q16);
       wait_for(sh, kODone + t, done & 1, late);
       __syncwarp();
+      if (next) q_has_come(sh, t);
       ++done;
       tc_after();
       const float l = sum.x + sum.y, inv = l == 0.f ? 0.f : 1.f / l;
@@ -587,15 +601,21 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
         } else {
           bf16* dst = (bf16*)A.out + (int64_t)(u.s.q0 + tok) * A.ldo + (int64_t)hq * D + 32 * c;
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            float v[8];
+          for (int k = 0; k < 32; k += 16) {
+            uint32_t w[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = l == 0.f ? 0.f : __uint_as_float(s[k + e]) * inv;
-            if (o16) {
-              store_n<bf16, 8>(dst + k, v);
+            for (int e = 0; e < 8; ++e) {
+              const float a = __uint_as_float(s[k + 2 * e]) * inv, b = __uint_as_float(s[k + 2 * e + 1]) * inv;
+              w[e] = l == 0.f ? 0u : pack_bf16x2(a, b);
+            }
+            if (o_align == 32) {
+              store_32b(dst + k, w);
+            } else if (o_align == 16) {
+              reinterpret_cast<uint4*>(dst + k)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              reinterpret_cast<uint4*>(dst + k)[1] = make_uint4(w[4], w[5], w[6], w[7]);
             } else {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) dst[k + e] = __float2bfloat16_rn(v[e]);
+              for (int e = 0; e < 16; ++e) reinterpret_cast<uint16_t*>(dst + k)[e] = (uint16_t)(w[e / 2] >> 16 * (e & 1));
             }
           }
         }
@@ -609,7 +629,10 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
     }
     if (t == 0 && behind && !before && row == 0) tell_join(A, u, parts_behind(sh.plan, num + (u.tiles - 1 - tile)));
     if (after <= 0) break;
-    if (!has && nu.r0 + t * kTile < nu.r1) load_q<D>(A, sh, nu, t, q_smem, q16);
+    if (!has && nu.r0 + t * kTile < nu.r1) {
+      fetch_q<D>(A, nu, t, q_smem, q16);
+      q_has_come(sh, t);
+    }
     n += nt;
     num += nt + kBegin;
     left = after;
@@ -620,7 +643,7 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
 }
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(kManyThreads, 1) attn8_many(const __grid_constant__ AttnArgs A, bool q16, bool o16) {
+__global__ void __launch_bounds__(kManyThreads, 1) attn8_many(const __grid_constant__ AttnArgs A, bool q16, int o_align) {
   using M = ManyShape<D>;
   extern __shared__ uint8_t many_smem[];
   __shared__ Shared sh;
@@ -653,7 +676,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) attn8_many(const __grid_const
     uint32_t late = 0;
     if (warp < 8) {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
-      softmax<D>(A, sh, q_smem, warp >> 2, q16, o16, late);
+      softmax<D>(A, sh, q_smem, warp >> 2, q16, o_align, late);
     } else if (warp < 8 + kConvWarps) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
       convert<D, FMT>(A, sh, kv_smem, warp - 8, late);
@@ -679,7 +702,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) attn8_many(const __grid_const
 }
 
 template <int D, int FMT>
-gbln_status many_go(const AttnArgs& A, int blocks, bool q16, bool o16, cudaStream_t s) {
+gbln_status many_go(const AttnArgs& A, int blocks, bool q16, int o_align, cudaStream_t s) {
   using M = ManyShape<D>;
   static std::atomic<uint64_t> ready{0};  // devices whose limit is raised
   int dev = 0;
@@ -691,20 +714,21 @@ gbln_status many_go(const AttnArgs& A, int blocks, bool q16, bool o16, cudaStrea
     }
     ready.fetch_or(1ull << dev, std::memory_order_release);
   }
-  attn8_many<D, FMT><<<blocks, kManyThreads, M::SMEM, s>>>(A, q16, o16);
+  attn8_many<D, FMT><<<blocks, kManyThreads, M::SMEM, s>>>(A, q16, o_align);
   return cudaGetLastError() == cudaSuccess ? attn_join_launch(A, blocks, kManyRows, s) : GBLN_ERR_CUDA;
 }
 
 template <int FMT>
-gbln_status many_typed(const AttnArgs& A, int blocks, bool q16, bool o16, cudaStream_t s) {
-  return A.D == 64 ? many_go<64, FMT>(A, blocks, q16, o16, s) : A.D == 96 ? many_go<96, FMT>(A, blocks, q16, o16, s) : many_go<128, FMT>(A, blocks, q16, o16, s);
+gbln_status many_typed(const AttnArgs& A, int blocks, bool q16, int o_align, cudaStream_t s) {
+  return A.D == 64 ? many_go<64, FMT>(A, blocks, q16, o_align, s) : A.D == 96 ? many_go<96, FMT>(A, blocks, q16, o_align, s) : many_go<128, FMT>(A, blocks, q16, o_align, s);
 }
 
 }  // namespace
 
 gbln_status attn_many_launch(const AttnArgs& A, int blocks, int fmt, cudaStream_t s) {
-  const bool q16 = aligned16(A.q) && A.ldq % 8 == 0, o16 = aligned16(A.out) && A.ldo % 8 == 0;
-  return fmt == GBLN_Q8_INT8 ? many_typed<GBLN_Q8_INT8>(A, blocks, q16, o16, s) : many_typed<GBLN_Q8_E4M3>(A, blocks, q16, o16, s);
+  const bool q16 = aligned16(A.q) && A.ldq % 8 == 0;
+  const int o_align = (uintptr_t)A.out % 32 == 0 && A.ldo % 16 == 0 ? 32 : aligned16(A.out) && A.ldo % 8 == 0 ? 16 : 2;
+  return fmt == GBLN_Q8_INT8 ? many_typed<GBLN_Q8_INT8>(A, blocks, q16, o_align, s) : many_typed<GBLN_Q8_E4M3>(A, blocks, q16, o_align, s);
 }
 
 }  // namespace gbln
