@@ -24,6 +24,8 @@
 // power of two (exact) to below 2^15; a weight is at most 4 (the row's reference follows its
 // maximum) and stands relative to R, a power of two above all of V's scales so far, times 2^13:
 // it keeps 11 bits down to 2^-27 of R, half a step of what is below is 2^-38 of R.
+// Measured: 64 sequences, 524288 cached tokens of 8 heads of 128, INT8 211 us (78% of the copy rate), E4M3
+// 185 us (88%).
 
 #include <cuda_fp16.h>
 
@@ -212,7 +214,7 @@ template <int D, int FMT, int NT, bool ONE>
 __global__ void __launch_bounds__(32 * FewShape<D, NT>::WARPS, 1) attn8_few(const __grid_constant__ AttnArgs A, bool q16) {
   using Sh = FewShape<D, NT>;
   constexpr int ROWS = Sh::ROWS, W = D / 32;  // words of a lane's slice of a key
-  extern __shared__ __align__(128) uint8_t ring[];
+  extern __shared__ __align__(128) unsigned char ring[];
   __shared__ Part plan;
   launch_dependents();
   const int lane = threadIdx.x & 31, warp = warp_index();
@@ -517,8 +519,32 @@ __global__ void __launch_bounds__(32 * FewShape<D, NT>::WARPS, 1) attn8_few(cons
   }
 }
 
+// Parts first, first + step, ... n of a row: part 0 is of block c, its second place, the others of the blocks behind it, their
+// first.  A lane has every 32nd value.
+template <int D>
+__device__ __forceinline__ void add_parts(const AttnArgs& A, int MR, int c, int n, int wh, int r, int first, int step, float& m, float& l,
+                                          float (&acc)[D / 32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 4
+  for (int k = first; k <= n; k += step) {
+    const int64_t at = ((int64_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * A.HB + wh) * MR + r;
+    const float2 p = *reinterpret_cast<const float2*>(A.part_ml + 2 * at);
+    float v[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) v[i] = A.part_o[at * D + lane + 32 * i];
+    const float to = fmaxf(m, p.x), ref = finite_or_zero(to), f0 = ex2(m - ref), f1 = ex2(p.x - ref);
+    m = to;
+    l = l * f0 + p.y * f1;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) acc[i] = acc[i] * f0 + v[i] * f1;
+  }
+}
+
 // Join the parts of the units that the plan divided.  A block takes one row after the other, its eight warps the
-// row's parts in turns (all parts of a row are under way at once), a lane D / 32 of the values.
+// row's parts in turns (all parts of a row are under way at once), a lane D / 32 of the values.  Where there are rows
+// for more than two rounds, units have few parts, and each warp takes rows of its own (2048 tokens over 32768, 38912 rows of
+// two or three parts: 76 us with a block per row, 17 so; 64
+// sequences of one token 11 and 6 us).
 template <int D>
 __global__ void __launch_bounds__(256) attn8_join(const __grid_constant__ AttnArgs A, int MR, int blocks) {
   constexpr int W = D / 32;
@@ -539,28 +565,25 @@ __global__ void __launch_bounds__(256) attn8_join(const __grid_constant__ AttnAr
   }
   __syncthreads();
   const int per = MR * A.HB, total = count * per;
-  for (int x = blockIdx.x; x < total; x += gridDim.x) {
+  const bool apart = total > 2 * (int)gridDim.x;
+  for (int x = apart ? 8 * blockIdx.x + warp : blockIdx.x; x < total; x += apart ? 8 * gridDim.x : gridDim.x) {
     const int c = units[x / per], y = x % per, wh = y / MR, r = y - wh * MR;
     const int* f = A.info + c * kAttnInfo;
     const int n = f[0], nrows = f[1], row = f[2] + r, q0 = f[3], h = f[4] * A.HB + wh;
-    if (r >= nrows || h >= A.Hk) continue;  // uniform in the block
+    if (r >= nrows || h >= A.Hk) continue;  // uniform in the block, or the warp
     float m = -INFINITY, l = 0.f, acc[W];
 #pragma unroll
     for (int i = 0; i < W; ++i) acc[i] = 0.f;
-#pragma unroll 4
-    for (int k = warp; k <= n; k += 8) {
-      // part k: of block c its second place, of the blocks behind it their first
-      const int64_t at = ((int64_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * A.HB + wh) * MR + r;
-      const float2 p = *reinterpret_cast<const float2*>(A.part_ml + 2 * at);
-      float v[W];
+    if (apart) {
+      add_parts<D>(A, MR, c, n, wh, r, 0, 1, m, l, acc);
+      const int tok = A.group.by(row), hq = h * A.G + row - tok * A.G;
+      bf16* dst = (bf16*)A.out + (q0 + tok) * A.ldo + (int64_t)hq * D + lane;
 #pragma unroll
-      for (int i = 0; i < W; ++i) v[i] = A.part_o[at * D + lane + 32 * i];
-      const float to = fmaxf(m, p.x), ref = finite_or_zero(to), f0 = ex2(m - ref), f1 = ex2(p.x - ref);
-      m = to;
-      l = l * f0 + p.y * f1;
-#pragma unroll
-      for (int i = 0; i < W; ++i) acc[i] = acc[i] * f0 + v[i] * f1;
+      for (int i = 0; i < W; ++i) dst[32 * i] = __float2bfloat16_rn(l == 0.f ? 0.f : acc[i] / l);
+      if (A.lse && lane == 0) A.lse[(int64_t)(q0 + tok) * A.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      continue;
     }
+    add_parts<D>(A, MR, c, n, wh, r, warp, 8, m, l, acc);
     if (lane == 0) ml[warp] = make_float2(m, l);
 #pragma unroll
     for (int i = 0; i < W; ++i) part[warp][lane + 32 * i] = acc[i];
@@ -585,15 +608,20 @@ __global__ void __launch_bounds__(256) attn8_join(const __grid_constant__ AttnAr
   }
 }
 
-// Element path: float32 rows, other head sizes, other alignments.  A warp per row: scores of
-// 32 keys at a time, a lane each; then lanes over the values.
-template <typename T, int FMT>
-__global__ void __launch_bounds__(128) attn8_elem(const __grid_constant__ AttnArgs A) {
-  __shared__ float qs[4][kAttnMaxHeads];
+// Any other rows (float32), head sizes and alignments.  A block per row, its warps on 32 keys at a time in turns: scores with a
+// lane per key, W codes at a load (16 or 4 where sizes and strides are multiples of them, else 1), then lanes over the
+// values, up to NVAL each; the warps' sums meet at the end.  Bound by instructions, about forty per key and warp.
+// (64 sequences of 1024 keys, 32 / 8 heads: of 80 265 us, of 33 402; of 96 in the kernel above 51.)
+constexpr int kElemWarps = 8;
+template <typename T, int FMT, int W, int NVAL>
+__global__ void __launch_bounds__(32 * kElemWarps, NVAL == 4 ? 4 : 3) attn8_elem(const __grid_constant__ AttnArgs A) {
+  constexpr int VW = W >= 4 ? 4 : 1, NW = NVAL / VW;
+  __shared__ __align__(16) float qs[32 * NVAL];
+  __shared__ float part[kElemWarps][32 * NVAL], ml[kElemWarps][2];
   const int lane = threadIdx.x & 31, warp = warp_index();
   const int64_t rows = (int64_t)A.T * A.Hq;
   const int end = min(max(__ldg(A.cu + A.B), 0), A.T);
-  for (int64_t x = (int64_t)blockIdx.x * 4 + warp; x < rows; x += (int64_t)gridDim.x * 4) {
+  for (int64_t x = blockIdx.x; x < rows; x += gridDim.x) {
     const int tok = (int)(x / A.Hq), hq = (int)(x - (int64_t)tok * A.Hq), h = hq / A.G;
     if (tok >= end) return;  // rows behind the last sequence
     // the last sequence that starts at or before the token
@@ -607,29 +635,53 @@ __global__ void __launch_bounds__(128) attn8_elem(const __grid_constant__ AttnAr
     const Seq s = seq_at(A, b);
     if (tok < s.q0 || tok >= s.q0 + s.nq) continue;
     const T* src = (const T*)A.q + tok * A.ldq + (int64_t)hq * A.D;
-    __syncwarp();
-    for (int d = lane; d < A.D; d += 32) qs[warp][d] = to_f32(src[d]);
-    __syncwarp();
+    __syncthreads();  // the row before is done
+    for (int d = threadIdx.x; d < A.D; d += 32 * kElemWarps) qs[d] = to_f32(src[d]);
+    __syncthreads();
     const int pos = s.kv - s.nq + tok - s.q0;
     const int first = A.window > 0 ? max(0, pos - A.window + 1) : 0, last = A.causal ? min(s.kv, pos + 1) : s.kv;
-    float m = -INFINITY, l = 0.f, acc[kAttnMaxHeads / 32];
+    float m = -INFINITY, l = 0.f, acc[NW][VW];
 #pragma unroll
-    for (int i = 0; i < kAttnMaxHeads / 32; ++i) acc[i] = 0.f;
-    for (int j0 = first; j0 < last; j0 += 32) {
-      const int j = j0 + lane;
-      KeyAt k = key_at(A, b, j, first, last);
+    for (int e = 0; e < NW; ++e)
+#pragma unroll
+      for (int k = 0; k < VW; ++k) acc[e][k] = 0.f;
+    for (int64_t begin = (int64_t)first + 32 * warp; begin < last; begin += 32 * kElemWarps) {
+      const int j0 = (int)begin;
+      const KeyAt k = key_at(A, b, j0 + lane, first, last);
       if (k.page == -2) atomicOr(A.err, kErrBadSlot);
       float sc = -INFINITY, vs = 0.f;
+      const uint8_t* vc = A.V.q;
       if (k.page >= 0) {
         const uint8_t* kc = A.K.q + A.K.cq.at(k.page, k.off, h);
-        float dot = 0.f;
-        for (int d = 0; d < A.D; ++d) {
-          float t[4];
-          q8_decode4<FMT>(kc[d], t);
-          dot = fmaf(qs[warp][d], t[0], dot);
-        }
-        sc = dot * (A.K.sc[A.K.cs.at(k.page, k.off, h)] * A.scale2);
+        vc += A.V.cq.at(k.page, k.off, h);
+        const float ks = A.K.sc[A.K.cs.at(k.page, k.off, h)];
         vs = A.V.sc[A.V.cs.at(k.page, k.off, h)];
+        float dot[4] = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (W == 1) {
+          for (int d = 0; d < A.D; ++d) {
+            float t[4];
+            q8_decode4<FMT>(kc[d], t);
+            dot[0] = fmaf(qs[d], t[0], dot[0]);
+          }
+        } else {
+#pragma unroll 2
+          for (int d = 0; d < A.D; d += W) {
+            uint32_t w[W / 4];
+            if constexpr (W == 16) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(kc + d);
+            else w[0] = *reinterpret_cast<const uint32_t*>(kc + d);
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i) {
+              float t[4];
+              q8_decode4<FMT>(w[i], t);
+              const float4 q = *reinterpret_cast<const float4*>(qs + d + 4 * i);
+              dot[0] = fmaf(q.x, t[0], dot[0]);
+              dot[1] = fmaf(q.y, t[1], dot[1]);
+              dot[2] = fmaf(q.z, t[2], dot[2]);
+              dot[3] = fmaf(q.w, t[3], dot[3]);
+            }
+          }
+        }
+        sc = ((dot[0] + dot[1]) + (dot[2] + dot[3])) * (ks * A.scale2);
       } else if (k.page == -2) {
         sc = vs = __int_as_float(0x7fc00000);
       }
@@ -641,29 +693,75 @@ __global__ void __launch_bounds__(128) attn8_elem(const __grid_constant__ AttnAr
       const float p = ex2(sc - ref);
       l = l * f + p;
 #pragma unroll
-      for (int i = 0; i < kAttnMaxHeads / 32; ++i) acc[i] *= f;
+      for (int e = 0; e < NW; ++e)
+#pragma unroll
+        for (int i = 0; i < VW; ++i) acc[e][i] *= f;
       const float w = p * vs;
       const int n = min(32, last - j0);
+#pragma unroll 4
       for (int i = 0; i < n; ++i) {
         const float wi = __shfl_sync(0xffffffffu, w, i);
-        const int page = __shfl_sync(0xffffffffu, k.page, i);
-        const uint32_t off = __shfl_sync(0xffffffffu, k.off, i);
-        const uint8_t* vc = A.V.q + A.V.cq.at(page >= 0 ? page : 0, page >= 0 ? off : 0, h);
+        const uint8_t* v = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, (unsigned long long)vc, i));
+        const bool there = __shfl_sync(0xffffffffu, k.page, i) >= 0;
 #pragma unroll
-        for (int e = 0; e < kAttnMaxHeads / 32; ++e)
-          if (lane + 32 * e < A.D) {
-            float t[4] = {0.f, 0.f, 0.f, 0.f};
-            if (page >= 0) q8_decode4<FMT>(vc[lane + 32 * e], t);
-            acc[e] = fmaf(wi, t[0], acc[e]);
+        for (int e = 0; e < NW; ++e) {
+          const int d = VW * (lane + 32 * e);
+          float t[4] = {0.f, 0.f, 0.f, 0.f};
+          if (there && d < A.D) {
+            if constexpr (VW == 4) q8_decode4<FMT>(*reinterpret_cast<const uint32_t*>(v + d), t);
+            else q8_decode4<FMT>(v[d], t);
           }
+#pragma unroll
+          for (int c = 0; c < VW; ++c) acc[e][c] = fmaf(wi, t[c], acc[e][c]);
+        }
       }
     }
     l = group_sum<32>(l);
-    T* dst = (T*)A.out + tok * A.ldo + (int64_t)hq * A.D;
+    if (lane == 0) {
+      ml[warp][0] = m;
+      ml[warp][1] = l;
+    }
 #pragma unroll
-    for (int e = 0; e < kAttnMaxHeads / 32; ++e)
-      if (lane + 32 * e < A.D) dst[lane + 32 * e] = from_f32<T>(l == 0.f ? 0.f : acc[e] / l);
-    if (A.lse && lane == 0) A.lse[(int64_t)tok * A.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    for (int e = 0; e < NW; ++e)
+#pragma unroll
+      for (int c = 0; c < VW; ++c) part[warp][VW * (lane + 32 * e) + c] = acc[e][c];
+    __syncthreads();
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kElemWarps; ++w) top = fmaxf(top, ml[w][0]);
+    const float ref = finite_or_zero(top);
+    float f[kElemWarps], sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kElemWarps; ++w) {
+      f[w] = ex2(ml[w][0] - ref);
+      sum += ml[w][1] * f[w];
+    }
+    T* dst = (T*)A.out + tok * A.ldo + (int64_t)hq * A.D;
+    for (int d = threadIdx.x; d < A.D; d += 32 * kElemWarps) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kElemWarps; ++w) v += part[w][d] * f[w];
+      dst[d] = from_f32<T>(sum == 0.f ? 0.f : v / sum);
+    }
+    if (A.lse && threadIdx.x == 0) A.lse[(int64_t)tok * A.Hq + hq] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  }
+}
+
+template <typename T, int FMT, int W>
+void elem_sized(const AttnArgs& A, unsigned grid, cudaStream_t s) {
+  if (A.D <= 128) attn8_elem<T, FMT, W, 4><<<grid, 32 * kElemWarps, 0, s>>>(A);
+  else attn8_elem<T, FMT, W, 16><<<grid, 32 * kElemWarps, 0, s>>>(A);
+}
+template <typename T>
+void elem_typed(const AttnArgs& A, int fmt, int w, unsigned grid, cudaStream_t s) {
+  if (fmt == GBLN_Q8_INT8) {
+    if (w == 16) elem_sized<T, GBLN_Q8_INT8, 16>(A, grid, s);
+    else if (w == 4) elem_sized<T, GBLN_Q8_INT8, 4>(A, grid, s);
+    else elem_sized<T, GBLN_Q8_INT8, 1>(A, grid, s);
+  } else {
+    if (w == 16) elem_sized<T, GBLN_Q8_E4M3, 16>(A, grid, s);
+    else if (w == 4) elem_sized<T, GBLN_Q8_E4M3, 4>(A, grid, s);
+    else elem_sized<T, GBLN_Q8_E4M3, 1>(A, grid, s);
   }
 }
 
@@ -679,6 +777,9 @@ FastDiv fast_div(uint32_t d) {
 // How the kernel for few rows is used: NT columns of eight rows, and the K/V heads of a block, 1, 2, 4 or 8.  All
 // warps on heads of their own where the batch fills the GPU (neighbouring heads' scales share their sectors),
 // fewer, with the keys of a head cut into slices, where it does not: less is left to be joined.
+// (262144 cached tokens of 8 heads: 128 sequences 164 us with one head a block, 137 with eight; 4 sequences 136 and 152.  Two
+// columns where a sequence has more than eight rows: 32 sequences of 4096 tokens, 8 rows each, 95 us with one column,
+// 107 with two; 16 rows 140 and 122.)
 struct FewUse {
   int nt, hb;
 };
@@ -724,7 +825,8 @@ gbln_status few_typed(const AttnArgs& A, int nt, int blocks, bool q16, cudaStrea
 
 // Rows for the tensor-core kernel: where a sequence brings more rows on average than the other
 // kernel takes at once, so that K and V would be converted several times over there.
-bool many_rows(int64_t T, int32_t B, int G, int32_t D) { return D <= 128 && T * G > 32 * (int64_t)B; }
+// (32 sequences of 4096 tokens, 4 heads a group: 24 rows each 157 us there, 190 here; 32 rows 204 and 190; 48 rows 332 and 231.)
+bool many_rows(int64_t T, int32_t B, int G, int32_t D) { return D <= 128 && T * G >= 32 * (int64_t)B; }
 
 bool fast_head(int32_t D, int io) { return io == GBLN_BF16 && (D == 64 || D == 96 || D == 128 || D == 256); }
 
@@ -827,13 +929,10 @@ extern "C" gbln_status gbln_attn_cache8(const void* q, const int32_t* cu_seqlens
     const bool q16 = aligned16(q) && ld_q % 8 == 0;
     return fmt == GBLN_Q8_INT8 ? few_typed<GBLN_Q8_INT8>(A, f.nt, sms, q16, s) : few_typed<GBLN_Q8_E4M3>(A, f.nt, sms, q16, s);
   }
-  const unsigned grid = grid_for(T * (int64_t)Hq, 4, (int64_t)sms * 32);
-  if (io == GBLN_F32) {
-    if (fmt == GBLN_Q8_INT8) attn8_elem<float, GBLN_Q8_INT8><<<grid, 128, 0, s>>>(A);
-    else attn8_elem<float, GBLN_Q8_E4M3><<<grid, 128, 0, s>>>(A);
-  } else {
-    if (fmt == GBLN_Q8_INT8) attn8_elem<bf16, GBLN_Q8_INT8><<<grid, 128, 0, s>>>(A);
-    else attn8_elem<bf16, GBLN_Q8_E4M3><<<grid, 128, 0, s>>>(A);
-  }
+  const unsigned grid = grid_for(T * (int64_t)Hq, 1, (int64_t)sms * 32);
+  const auto codes_by = [&](int n) { return D % n == 0 && codes_aligned(k_cache, v_cache, n); };
+  const int w = codes_by(16) ? 16 : codes_by(4) ? 4 : 1;
+  if (io == GBLN_F32) elem_typed<float>(A, fmt, w, grid, s);
+  else elem_typed<bf16>(A, fmt, w, grid, s);
   return launch_status();
 }

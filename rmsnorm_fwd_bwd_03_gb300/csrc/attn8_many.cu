@@ -13,6 +13,11 @@
 // A tile's scores come 64 keys at a time into two places in turn: while one step's weights are
 // computed, the products of the next step's scores and of the other tile run.  Tensor memory:
 // the two tiles' scores, 2 x 64 columns each, and O_0, O_1, 128 columns each: all 512.
+// Scores and sums are float32; weights times V's scales are rounded to bf16 (2^-9) for their product:
+// with fp16's range small weights would be lost beside large ones.
+// Measured, 32 / 8 heads of 128: 2048 tokens over 32768 1.21 ms (880 TFLOP/s), 19 prompts of 32768 tokens
+// 1.02 ms (695 TFLOP/s).  The tensor cores are busy 38% of the time, issue slots 54%: a row's chain of
+// tensor-memory loads, scales and exponentials bounds a step; begin and end of a unit take 6 us.
 
 #include <climits>
 
@@ -645,7 +650,7 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
 template <int D, int FMT>
 __global__ void __launch_bounds__(kManyThreads, 1) attn8_many(const __grid_constant__ AttnArgs A, bool q16, int o_align) {
   using M = ManyShape<D>;
-  extern __shared__ uint8_t many_smem[];
+  extern __shared__ unsigned char many_smem[];
   __shared__ Shared sh;
   launch_dependents();
   const int warp = warp_index();

@@ -13,6 +13,10 @@
 //   dx = rstd (g - n mean(g n)),  n = x rstd,  dW = sum over tokens and heads of d n.
 // rstd is not stored: the backward pass reads x anyway, and the sums of x^2 and g x
 // go through the same shuffles.  HBM-bound: forward 2, backward 3 accesses per value.
+// Measured, bf16 heads of 128: 32761 tokens of 64 / 8 heads with three axes 212 us forward, 349
+// backward (84 and 76% of the copy rate); 16384 of 16 / 8 heads 48 and 65 us (62 and 68%: issue slots
+// half used, warps waiting for their rows); axes alone, 65536 of 32 / 8 heads 229 us (87%); the
+// cache's write, 32768 tokens of 32 / 8 heads, three axes, 152 us.
 
 #include <type_traits>
 
@@ -450,7 +454,8 @@ __device__ __forceinline__ void heads_cache(const HeadArgs<T>& A, const Split& W
 }
 
 // Rows per lane and blocks per SM: a large share of a token, or a small one where tokens
-// are few or narrow.
+// are few or narrow.  (16 tokens of 16 / 8 heads of 128, bf16: small 3.5 us, large 3.8, into the cache 3.9
+// and 4.5; 1024 tokens of 64 / 8 float32 heads 13.7 and 12.7, 4096 into the cache 26.1 and 22.2.)
 constexpr int kRowsLarge = 4, kRowsSmall = 2, kSmallBlocks = 3;
 constexpr int rows_of(bool small, int bytes) { return (small ? kRowsSmall : kRowsLarge) * (16 / bytes); }
 
@@ -600,6 +605,7 @@ __device__ __forceinline__ void flush_dw(float* acc, int D, int which, bool firs
   for (int i = threadIdx.x; i < 2 * D; i += blockDim.x) out[i] = acc[i];
 }
 
+// Small where every warp has one chunk at most: 16 tokens of 16 / 8 heads of 128 6.2 us, large 6.9; 4096 23.7 and 19.4.
 constexpr int kRowsBwd = 2, kRowsBwdSmall = 1;
 constexpr int kBwdBlocks = 2;  // per SM
 constexpr int rows_bwd(bool small, int bytes) { return (small ? kRowsBwdSmall : kRowsBwd) * (16 / bytes); }
