@@ -97,13 +97,14 @@ int gbln_version(void);
 
 /*
  * Per-device error word of the current device, a set of bits:
- *   1  a kernel's bounded wait on its own asynchronous (TMA bulk) copies ran
- *      out; the kernel stopped early instead of hanging, so its outputs are
- *      incomplete;
+ *   1  a kernel's bounded wait on its own asynchronous (TMA bulk) copies, or
+ *      (attention) on another part of its block, ran out; the kernel stopped
+ *      early instead of hanging, so its outputs are incomplete;
  *   2  a RoPE call met a position outside [0, max_pos); that token's outputs
  *      are NaN (the table is not read);
- *   4  a cache call met a slot beyond the cache's last one: nothing was stored
- *      for that token, its read-back is NaN.
+ *   4  a cache call met a slot beyond the cache's last one (nothing was stored
+ *      for that token, its read-back is NaN), or attention a page outside the
+ *      cache (the rows that see it are NaN).
  * *code receives the word; clear != 0 resets it to zero.  Synchronous
  * (device-wide copy): call it outside hot loops.  Errors: INVALID_ARG for a
  * null code, CUDA if the device is unreachable.
@@ -728,7 +729,9 @@ gbln_status gbln_qk_norm_rope_fwd_cache8(const void* q, const void* k, const voi
  *   out = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q . k_j),  lse = log sum_j w_j
  * (k_j, v_j = code * scale).  Head h of q goes with K/V head h / (Hq / Hk).  A row that sees no
  * key gives zeros and lse -infinity.  Scores, weights, their sums and results are float32;
- * with bf16 rows and D 64, 96, 128 or 256 the weights times v's scales are rounded to bf16.
+ * with bf16 rows and D 64, 96, 128 or 256 the weights times v's scales are rounded to 16 bits
+ * for their products: with many rows to bf16, with few to fp16 relative to the power of two
+ * above the scales of v that the row has met (11 bits; what is below 2^-38 of it becomes 0).
  * Keys that a row does not see have no part in it, whatever the cache holds there; pages that
  * no row of the sequence sees are not read (freed pages may hold any number in the table).
  * cu_seqlens_q [B + 1], non-decreasing from 0, kv_lens [B], page_table [B, max_pages] int32,
@@ -739,8 +742,9 @@ gbln_status gbln_qk_norm_rope_fwd_cache8(const void* q, const void* k, const voi
  * workspace: gbln_attn_cache8_workspace bytes (by the sizes and the device's SM count; 0: none
  * needed), 16-byte aligned, contents of no account; calls that may overlap need one each.
  * Bitwise reproducible for fixed sizes, lengths, alignment and GPU model.
- * Errors: INVALID_ARG for Hq not a multiple of Hk, D > 512, T * Hq or max_pages * page_size
- * above 2^30, a scale that is not finite, window < 0 and as gbln_cache8_read; WORKSPACE.
+ * Errors: INVALID_ARG for Hq not a multiple of Hk, D > 512, Hq * D above 2^24, T * Hq or
+ * max_pages * page_size above 2^30, a scale that is not finite (or beyond 3e38), window < 0
+ * and as gbln_cache8_read; WORKSPACE.
  */
 int64_t gbln_attn_cache8_workspace(int64_t T, int32_t B, int32_t Hq, int32_t Hk, int32_t D,
                                    gbln_dtype io);
