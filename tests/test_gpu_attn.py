@@ -386,3 +386,32 @@ def test_a_layer_serves_prompts_then_decodes():
         o, _ = heads.attend(q, k, v, D ** -0.5, 0)
         # the cache's own rounding: K and V off by a / 254 each (1.4% of a normal head's standard deviation), q by 2^-9
         assert np.linalg.norm(to64(got[b]) - o) <= 0.02 * np.linalg.norm(o)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("io,D", [("bf16", 80), ("bf16", 72), ("bf16", 33), ("f32", 64), ("f32", 200)])
+def test_other_sizes_over_long_contexts(io, D, fmt):
+    """Rows whose keys several warps share, also where a window or the context leaves some of them none."""
+    _run([1, 6, 3], [700, 300, 2000], 4, 2, D, io=io, fmt=fmt, pad=1)
+    _run([2, 1, 40], [257, 31, 600], 4, 2, D, io=io, fmt=fmt, window=100)
+    _run([3, 1], [2, 0], 4, 2, D, io=io, fmt=fmt, causal=False)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("off", [1, 2, 4, 8, 16])
+def test_codes_at_any_address(off, fmt):
+    s = _make([1, 40], [300, 200], 4, 2, 128, fmt=fmt)
+    for i in (0, 2):
+        c = s["cache"][i]
+        moved = torch.empty(c.numel() + off, dtype=torch.uint8, device="cuda")[off:]
+        moved.copy_(c.view(torch.uint8).flatten())
+        s["cache"][i] = moved.view(c.dtype).view(c.shape)
+    _check(s, gb.attn_cache8(*_args(s)), what=f"{fmt} {off}")
+    assert gb.device_error() == 0
+
+
+@pytest.mark.parametrize("new,kv,Hq,Hk", [([1] * 64, [1024] * 64, 32, 8), ([80] * 12, [400] * 12, 8, 2), ([64], [2000], 4, 1), ([1], [3000], 4, 1)])
+def test_divided_units_are_joined(new, kv, Hq, Hk):
+    """Many units of few parts (warps with rows of their own), one unit of many (a block for a row)."""
+    _run(new, kv, Hq, Hk, 128)
+    _run(new, kv, Hq, Hk, 64, fmt="e4m3", window=300)
