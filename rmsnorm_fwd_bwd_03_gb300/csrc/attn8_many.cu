@@ -13,10 +13,10 @@
 // A tile's scores come 64 keys at a time into two places in turn: while one step's weights are
 // computed, the products of the next step's scores and of the other tile run.  Tensor memory:
 // the two tiles' scores, 2 x 64 columns each, and O_0, O_1, 128 columns each: all 512.
-// Scores and sums are float32; weights times V's scales are rounded to bf16 (2^-9) for their product:
+// Scores and sums are float32; weights times V's scales are rounded to bf16 (2^-8 at most) for their product:
 // with fp16's range small weights would be lost beside large ones.
-// Measured, 32 / 8 heads of 128: 2048 tokens over 32768 1.21 ms (880 TFLOP/s), 19 prompts of 32768 tokens
-// 1.02 ms (695 TFLOP/s).  The tensor cores are busy 38% of the time, issue slots 54%: a row's chain of
+// Measured, 32 / 8 heads of 128: 2048 tokens over 32768 1.23 ms (870 TFLOP/s), 19 prompts of 32768 tokens
+// 1.03 ms (690 TFLOP/s).  The tensor cores are busy 38% of the time, issue slots 54%: a row's chain of
 // tensor-memory loads, scales and exponentials bounds a step; begin and end of a unit take 6 us.
 
 #include <climits>
@@ -33,7 +33,7 @@ constexpr int kTile = 128;              // rows of a tile, keys that are fetched
 constexpr int kHalf = kTile / 2;        // keys of a step
 constexpr int kManyRows = 2 * kTile;    // rows of a unit
 static_assert(kManyRows == kManyUnit, "the joining kernel knows it too");
-constexpr int kBegin = 1;               // tiles that a unit's begin counts for
+constexpr int kBegin = 1;               // tiles that a unit's begin counts for (19 prompts of 32768 tokens: 2 the same, 3 1.06 ms)
 constexpr int kConvWarps = 8;
 constexpr int kConvRows = kTile / kConvWarps / 8;  // keys of a converting thread
 constexpr int kManyThreads = 640;      // five groups of four warps: rows twice, conversion twice, products
@@ -88,7 +88,6 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
 }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 #define GBLN_R8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
@@ -106,6 +105,14 @@ __device__ __forceinline__ void tm_ld16(uint32_t (&v)[16], uint32_t at) {
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : GBLN_R8(v, 0), GBLN_R8(v, 8)
       : "r"(at));
+}
+// Values on their way from tensor memory have come: the compiler takes none of them before.
+#define GBLN_T8(v, i) "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]), "+r"(v[i + 5]), "+r"(v[i + 6]), "+r"(v[i + 7])
+__device__ __forceinline__ void tm_wait_ld(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : GBLN_T8(v, 0), GBLN_T8(v, 8), GBLN_T8(v, 16), GBLN_T8(v, 24)::"memory");
+}
+__device__ __forceinline__ void tm_wait_ld(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : GBLN_T8(v, 0), GBLN_T8(v, 8)::"memory");
 }
 __device__ __forceinline__ void tm_st16(uint32_t at, const uint32_t (&v)[16]) {
   asm volatile(
@@ -520,7 +527,8 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
         uint32_t s[2][32];
         tm_ld32(s[0], at);
         tm_ld32(s[1], at + 32);
-        tm_wait_ld();
+        tm_wait_ld(s[0]);
+        tm_wait_ld(s[1]);
         if (i > 0 && i + 1 == steps) {  // no scores follow: a barrier of its own
           wait_for(sh, kODone + t, done & 1, late);
           __syncwarp();
@@ -564,7 +572,7 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
             for (int c = 0; c < D / 16; ++c) {
               uint32_t o[16];
               tm_ld16(o, o_at + 16 * c);
-              tm_wait_ld();
+              tm_wait_ld(o);
 #pragma unroll
               for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
               tm_st16(o_at + 16 * c, o);
@@ -595,7 +603,7 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
       for (int c = 0; c < D / 32; ++c) {
         uint32_t s[32];
         tm_ld32(s, o_at + 32 * c);
-        tm_wait_ld();
+        tm_wait_ld(s);
         if (r >= u.r1) {
           // nothing to store
         } else if (split) {

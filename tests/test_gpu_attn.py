@@ -1,6 +1,6 @@
 """GPU vs oracle: attention of the new tokens of a ragged batch over the paged 8-bit cache.
 
-Bounds, derived.  bf16 rows: the result is rounded to bf16 (2^-9 of it by the eps / 2 rule:
+Bounds, derived.  bf16 rows: the result is rounded to bf16 (half a step, by the eps / 2 rule:
 finfo(bf16).eps / 2 = 2^-8) and every weight times v's scale once to bf16 (2^-8 of the weight at
 most), so that with w_j the normalised weights
     |err| <= 2^-8 |o| + 2^-8 sum_j w_j |v_j| (1 + 2^-8) + float32 terms.
@@ -384,7 +384,7 @@ def test_a_layer_serves_prompts_then_decodes():
         q, k, v = np.split(to64(x[b]).reshape(n, -1, D), [Hq, Hq + Hk], axis=1)
         q, k = (heads.norm_rotate(t, to64(w), p, np.zeros(D // 2, int), theta, eps) for t, w in ((q, wq), (k, wk)))
         o, _ = heads.attend(q, k, v, D ** -0.5, 0)
-        # the cache's own rounding: K and V off by a / 254 each (1.4% of a normal head's standard deviation), q by 2^-9
+        # the cache's own rounding: K and V off by a / 254 each (1.4% of a normal head's standard deviation), q by 2^-8
         assert np.linalg.norm(to64(got[b]) - o) <= 0.02 * np.linalg.norm(o)
 
 
