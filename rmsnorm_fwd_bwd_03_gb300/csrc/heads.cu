@@ -15,7 +15,7 @@
 // go through the same shuffles.  HBM-bound: forward 2, backward 3 accesses per value.
 // Measured, bf16 heads of 128: 32761 tokens of 64 / 8 heads with three axes 212 us forward, 349
 // backward (84 and 76% of the copy rate); 16384 of 16 / 8 heads 48 and 65 us (62 and 68%: issue slots
-// half used, warps waiting for their rows); axes alone, 65536 of 32 / 8 heads 229 us (87%); the
+// half used, warps waiting for their rows); axes alone, 65536 of 32 / 8 heads 205 us (96%); the
 // cache's write, 32768 tokens of 32 / 8 heads, three axes, 152 us.
 
 #include <type_traits>
@@ -214,7 +214,7 @@ __device__ __forceinline__ float rstd_of(float sum, int D, float eps) {
 // and nk of K (and V) head rows; warp w of all has chunk w % (nq + nk) of the tokens
 // w / (nq + nk), that + stride, ...  Neighbouring warps so read one token's row together.
 // (Warps given to the two kinds by their rows, the kinds apart, wasted none of them on small
-// chunks, but read Q and K of a token at different times: 65536 tokens of 32 / 8 heads of 128 230 and 244 us.)
+// chunks, but read Q and K of a token at different times: 65536 tokens of 32 / 8 heads of 128, axes alone, 230 and 244 us at the time.)
 struct Split {
   int nu, lg;         // lanes in use per head row, log2 of the lanes of its group
   int nq, qch, qlt;   // chunks, head rows per lane in each, log2 of the tokens a warp takes at once
@@ -252,7 +252,7 @@ __device__ __forceinline__ void ask_ahead(const T* row, int first, int last, int
 // or KP heads of K and V to be quantised.  All row loads of a pass are issued before
 // anything depends on them; the sums of all rows go through the shuffles side by side.
 // ---------------------------------------------------------------------------
-template <typename T, bool IL, int VEC, int NQ>
+template <typename T, bool IL, int VEC, int NQ, bool NORM>
 __device__ __forceinline__ void heads_rows(const HeadArgs<T>& A, const Split& W, const T* x, int64_t ldx, T* y, int64_t ldy,
                                            const void* w, int H, int c, int ch, int lt, int64_t first, bool report) {
   using Run = HeadRun<T, VEC>;
@@ -287,8 +287,10 @@ __device__ __forceinline__ void heads_rows(const HeadArgs<T>& A, const Split& W,
         b[j].load(src + h * A.D + half);
       }
     }
-    if (!have) load_weights<VEC>(w, A.w32, P.ia, half, P.on, wa, wb);
-    have = true;
+    if constexpr (NORM) {
+      if (!have) load_weights<VEC>(w, A.w32, P.ia, half, P.on, wa, wb);
+      have = true;
+    }
     const bool ok = p.ok(A.max_pos);
     float2 cs[VEC];
     load_axes<VEC, IL>(A.table, half, p, A.ax, codes, ok, P.on, P.ia, A.sign, cs);
@@ -299,7 +301,7 @@ __device__ __forceinline__ void heads_rows(const HeadArgs<T>& A, const Split& W,
       ask_ahead(x + n * ldx, hf * A.D, last, P.li, 32 >> lt);
     }
     float ss[NQ];
-    if (w) {
+    if (NORM && w) {
 #pragma unroll
       for (int j = 0; j < NQ; ++j) {
         float xa[VEC], xb[VEC];
@@ -318,7 +320,7 @@ __device__ __forceinline__ void heads_rows(const HeadArgs<T>& A, const Split& W,
         float xa[VEC], xb[VEC];
         a[j].get(xa);
         b[j].get(xb);
-        if (w) {
+        if (NORM && w) {
           const float r = rstd_of(ss[j], A.D, A.eps);
           times<VEC>(xa, wa, r);
           times<VEC>(xb, wb, r);
@@ -459,8 +461,13 @@ __device__ __forceinline__ void heads_cache(const HeadArgs<T>& A, const Split& W
 constexpr int kRowsLarge = 4, kRowsSmall = 2, kSmallBlocks = 3;
 constexpr int rows_of(bool small, int bytes) { return (small ? kRowsSmall : kRowsLarge) * (16 / bytes); }
 
+// Rotations alone have no weights to hold: three blocks where norms leave room for two (65536 tokens of 32 / 8 heads of
+// 128, three axes: 205 us, with two blocks 226).
+constexpr int kRotate = -2;  // in the place of a format (-1: no cache): neither cache nor norms
+constexpr int fwd_blocks(int fmt, bool small) { return small ? kSmallBlocks : fmt == kRotate ? 3 : 2; }
+
 template <typename T, bool IL, int FMT, int VEC, bool SMALL>
-__global__ void __launch_bounds__(32 * kHeadWarps, SMALL ? kSmallBlocks : 2)
+__global__ void __launch_bounds__(32 * kHeadWarps, fwd_blocks(FMT, SMALL))
 heads_fwd_vec(const __grid_constant__ HeadArgs<T> A, const Split W) {
   constexpr int NQ = rows_of(SMALL, VEC * sizeof(T));
   const int64_t w = (int64_t)blockIdx.x * kHeadWarps + warp_index();
@@ -469,9 +476,9 @@ heads_fwd_vec(const __grid_constant__ HeadArgs<T> A, const Split W) {
   const int c = (int)(w - first * n);
   if (first >= W.stride) return;
   if (c < W.nq) {
-    heads_rows<T, IL, VEC, NQ>(A, W, A.q, A.ldq, A.qo, A.ldqo, A.wq, A.Hq, c, W.qch, W.qlt, first, c == 0);
+    heads_rows<T, IL, VEC, NQ, FMT != kRotate>(A, W, A.q, A.ldq, A.qo, A.ldqo, A.wq, A.Hq, c, W.qch, W.qlt, first, c == 0);
   } else if constexpr (FMT < 0) {
-    heads_rows<T, IL, VEC, NQ>(A, W, A.k, A.ldk, A.ko, A.ldko, A.wk, A.Hk, c - W.nq, W.kch, W.klt, first, c == 0);
+    heads_rows<T, IL, VEC, NQ, FMT != kRotate>(A, W, A.k, A.ldk, A.ko, A.ldko, A.wk, A.Hk, c - W.nq, W.kch, W.klt, first, c == 0);
   } else {
     heads_cache<T, IL, FMT, VEC, SMALL ? 1 : 2>(A, W, c - W.nq, first);
   }
@@ -855,7 +862,7 @@ gbln_status fwd_vec_launch(const HeadArgs<T>& A, int sms, cudaStream_t s) {
   if (!small) W = split_of(A.Hq, A.Hk, A.D, VEC, LQ, FMT < 0 ? LQ : 2);
   const int n = W.nq + W.nk;
   // eight times the resident blocks leave a warp a few steps to ask ahead for and the scheduler something to balance
-  const unsigned grid = grid_for(token_groups(W, A.rows) * n, kHeadWarps, (int64_t)sms * (small ? kSmallBlocks : 2) * 8 + (n + kHeadWarps - 1) / kHeadWarps);
+  const unsigned grid = grid_for(token_groups(W, A.rows) * n, kHeadWarps, (int64_t)sms * fwd_blocks(FMT, small) * 8 + (n + kHeadWarps - 1) / kHeadWarps);
   W.stride = (int64_t)grid * kHeadWarps / n;
   if (small) heads_fwd_vec<T, IL, FMT, VEC, true><<<grid, 32 * kHeadWarps, 0, s>>>(A, W);
   else heads_fwd_vec<T, IL, FMT, VEC, false><<<grid, 32 * kHeadWarps, 0, s>>>(A, W);
@@ -871,13 +878,15 @@ gbln_status fwd_launch(const HeadArgs<T>& A, const gbln_cache8* kc, const gbln_c
   if constexpr (VEC == 8)
     if (heads_fit(A, kc, vc, 4)) return fwd_vec_launch<T, IL, FMT, 4>(A, sms, s);
   const unsigned grid = grid_for(A.rows * (A.Hq + (FMT < 0 ? 1 : 2) * A.Hk), kHeadWarps, (int64_t)sms * 64);
-  if (A.D <= 128) heads_fwd_elem<T, IL, FMT, 2><<<grid, 256, 0, s>>>(A);
-  else heads_fwd_elem<T, IL, FMT, 8><<<grid, 256, 0, s>>>(A);
+  constexpr int F = FMT < 0 ? -1 : FMT;
+  if (A.D <= 128) heads_fwd_elem<T, IL, F, 2><<<grid, 256, 0, s>>>(A);
+  else heads_fwd_elem<T, IL, F, 8><<<grid, 256, 0, s>>>(A);
   return launch_status();
 }
 
 template <typename T>
 gbln_status fwd_typed(const HeadArgs<T>& A, bool il, int fmt, const gbln_cache8* kc, const gbln_cache8* vc, cudaStream_t s) {
+  if (fmt < 0 && !A.wq && !A.wk) return il ? fwd_launch<T, true, kRotate>(A, kc, vc, s) : fwd_launch<T, false, kRotate>(A, kc, vc, s);
   if (fmt < 0) return il ? fwd_launch<T, true, -1>(A, kc, vc, s) : fwd_launch<T, false, -1>(A, kc, vc, s);
   if (fmt == GBLN_Q8_INT8)
     return il ? fwd_launch<T, true, GBLN_Q8_INT8>(A, kc, vc, s) : fwd_launch<T, false, GBLN_Q8_INT8>(A, kc, vc, s);
