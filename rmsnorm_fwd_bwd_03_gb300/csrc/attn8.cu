@@ -22,8 +22,9 @@
 // comes out of shared memory transposed, four keys to a word, and the rows of the scores are the
 // keys in the order in which those words give them.  fp16's range: a row of Q is scaled by a
 // power of two (exact) to below 2^15; a weight is at most 4 (the row's reference follows its
-// maximum) and stands relative to R, a power of two above all of V's scales so far, times 2^13:
-// it keeps 11 bits down to 2^-27 of R, half a step of what is below is 2^-38 of R.
+// maximum) and stands relative to R, a power of two above V's scales of the keys that the row has
+// seen so far, times 2^13: it keeps 11 bits down to 2^-27 of R, half a step of what is below is 2^-38 of R.
+// Every row has an R of its own: with one for the warp a scale that only a neighbour sees took bits from its weights.
 // Measured: 64 sequences, 524288 cached tokens of 8 heads of 128, INT8 211 us (78% of the copy rate), E4M3
 // 185 us (88%).
 
@@ -124,6 +125,8 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
+// 1 / x of a power of two from 2^-126 to 2^126.
+__device__ __forceinline__ float power_inverse(float x) { return __uint_as_float(0x7f000000u - __float_as_uint(x)); }
 __device__ __forceinline__ float lds_f(uint32_t a) {
   float r;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(a));
@@ -242,9 +245,10 @@ __global__ void __launch_bounds__(32 * FewShape<D, NT>::WARPS, 1) attn8_few(cons
     const bool on = h < A.Hk;
     const int nrows = u.r1 - u.r0;
     float m[NT][2], l[NT][2], o[NT][D / 16][4];
-    float R = 0x1p-100f;  // above all of V's scales so far, a power of two
+    float U[NT][2];  // 2^13 / R of each row, R a power of two above the scales of V that it has seen
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      U[n][0] = U[n][1] = 0x1p113f;
       m[n][0] = m[n][1] = -INFINITY;
       l[n][0] = l[n][1] = 0.f;
 #pragma unroll
@@ -395,32 +399,44 @@ __global__ void __launch_bounds__(32 * FewShape<D, NT>::WARPS, 1) attn8_few(cons
           }
         }
         // The reference of a row's weights follows its maximum only when that has grown by more than 2^2, R V's
-        // scales when one is above it: weights have room for it, and the results are seldom rescaled.
-        bool up = vs[0] > R || vs[1] > R;
+        // scales when one is above it: weights have room for it, and the results are seldom rescaled.  A scale that is
+        // above R brings the warp here also where no row sees its key; each row then goes by the keys that it sees.
+        float vu[NT][4];
+        bool up = false;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) up = up || top[n][0] > m[n][0] + 2.f || top[n][1] > m[n][1] + 2.f;
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            vu[n][e] = vs[e >> 1] * U[n][e & 1];
+            up = up || fabsf(vu[n][e]) > 8192.f;
+          }
+          up = up || top[n][0] > m[n][0] + 2.f || top[n][1] > m[n][1] + 2.f;
+        }
         if (__any_sync(0xffffffffu, up)) {
-          float v = fmaxf(fmaxf(vs[0], vs[1]), 0x1p-101f);
-#pragma unroll
-          for (int k = 4; k < 32; k <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, k));
-          const float r = fmaxf(R, __uint_as_float((__float_as_uint(fminf(v, 0x1p120f)) & 0x7f800000u) + 0x00800000u)), fr = R / r;
-          R = r;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+              float v = hide & (1u << (4 * n + e)) ? 0.f : fabsf(vs[0]);
+              v = fmaxf(v, hide & (1u << (4 * n + 2 + e)) ? 0.f : fabsf(vs[1]));
+#pragma unroll
+              for (int k = 4; k < 32; k <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, k));
+              const uint32_t r = (__float_as_uint(fminf(v, 0x1p120f)) & 0x7f800000u) + 0x00800000u;  // the power of two above v
+              const float unit = fminf(U[n][e], power_inverse(__uint_as_float(r)) * 8192.f);
               const bool mv = top[n][e] > m[n][e] + 2.f;  // each row for itself
-              const float to = mv ? top[n][e] : m[n][e], f = mv ? ex2(m[n][e] - to) : 1.f;
+              const float to = mv ? top[n][e] : m[n][e], f = mv ? ex2(m[n][e] - to) : 1.f, fr = f * (unit * power_inverse(U[n][e]));
+              U[n][e] = unit;
+              vu[n][e] = vs[0] * unit;
+              vu[n][e + 2] = vs[1] * unit;
               m[n][e] = to;
               l[n][e] *= f;
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
-                o[n][i][e] *= f * fr;
-                o[n][i][e + 2] *= f * fr;
+                o[n][i][e] *= fr;
+                o[n][i][e + 2] *= fr;
               }
             }
         }
-        const float unit = __uint_as_float(0x7f000000u - __float_as_uint(R)) * 8192.f;  // 2^13 / R
         uint32_t pb[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -429,7 +445,7 @@ __global__ void __launch_bounds__(32 * FewShape<D, NT>::WARPS, 1) attn8_few(cons
             const float p0 = ex2(s[n][2 * k] - finite_or_zero(m[n][0])), p1 = ex2(s[n][2 * k + 1] - finite_or_zero(m[n][1]));
             l[n][0] += p0;
             l[n][1] += p1;
-            float w0 = p0 * (vs[k] * unit), w1 = p1 * (vs[k] * unit);
+            float w0 = p0 * vu[n][2 * k], w1 = p1 * vu[n][2 * k + 1];
             if (hide & (1u << (4 * n + 2 * k))) w0 = 0.f;  // whatever the scale of a key that is not seen
             if (hide & (1u << (4 * n + 2 * k + 1))) w1 = 0.f;
             pb[n][k] = transposed(pack_f16x2(w0, w1));
@@ -465,11 +481,12 @@ __global__ void __launch_bounds__(32 * FewShape<D, NT>::WARPS, 1) attn8_few(cons
 #pragma unroll
           for (int k = 4; k < 32; k <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], k);
           const int r = 8 * n + 2 * c + e;
+          const float back = power_inverse(U[n][e]);  // R / 2^13
           if (g == 0) *reinterpret_cast<float2*>(res + ROWS * D + 2 * r) = make_float2(m[n][e], l[n][e]);
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
-            res[r * D + 16 * i + g] = o[n][i][e] * (R * 0x1p-13f);
-            res[r * D + 16 * i + g + 8] = o[n][i][e + 2] * (R * 0x1p-13f);
+            res[r * D + 16 * i + g] = o[n][i][e] * back;
+            res[r * D + 16 * i + g + 8] = o[n][i][e + 2] * back;
           }
         }
     }
