@@ -19,8 +19,6 @@
 // 1.03 ms (690 TFLOP/s).  The tensor cores are busy 38% of the time, issue slots 54%: a row's chain of
 // tensor-memory loads, scales and exponentials bounds a step; begin and end of a unit take 6 us.
 
-#include <climits>
-
 #include <atomic>
 
 #include "attn8.cuh"
@@ -212,8 +210,9 @@ __device__ __forceinline__ void convert(const AttnArgs& A, Shared& sh, uint32_t 
   int64_t left = sh.plan.left;  // at the cursor
   int lo = u.lo, hi = u.hi, tiles = u.tiles, hg = u.hg;
   const int32_t* row_of = A.pages + (int64_t)u.b * A.max_pages;
-  int page[kConvRows], h = 0;  // of the tile looked up last; -1: no key, -2: outside the cache
-  uint32_t off[kConvRows];
+  int page[kConvRows], h = 0;  // of the tile looked up last, as the table has it; place(): -1 no key, -2 outside the cache
+  uint32_t off[kConvRows];     // kNoKey until then where there is no key: an entry of the table may be any number
+  constexpr uint32_t kNoKey = 0xffffffffu;
   uint4 kr[kConvRows][NP], vr[kConvRows][NP];
   float sc[kConvRows];
   const auto look_up = [&]() {  // the pages of the cursor's tile; the cursor moves on
@@ -223,7 +222,8 @@ __device__ __forceinline__ void convert(const AttnArgs& A, Shared& sh, uint32_t 
       const int j = lo + tile * kTile + row + 8 * i;
       uint32_t q;
       A.page.split((uint32_t)j, q, off[i]);
-      page[i] = j < hi ? __ldg(row_of + q) : INT_MIN;
+      page[i] = j < hi ? __ldg(row_of + q) : -1;
+      if (j >= hi) off[i] = kNoKey;
     }
     h = hg;
     --left;
@@ -245,8 +245,8 @@ __device__ __forceinline__ void convert(const AttnArgs& A, Shared& sh, uint32_t 
   const auto place = [&]() {
 #pragma unroll
     for (int i = 0; i < kConvRows; ++i) {
-      if (page[i] == INT_MIN) {
-        page[i] = -1;
+      if (off[i] == kNoKey) {
+        off[i] = 0;
       } else if (page[i] < 0 || page[i] >= A.n_pages) {
         page[i] = -2;
         atomicOr(A.err, kErrBadSlot);

@@ -1,4 +1,4 @@
-"""GPU: keys that a row does not see, in each of the kernels of attention over the paged 8-bit cache.
+"""GPU: keys that a row does not see and pages outside the cache, in each of the kernels of attention over the paged 8-bit cache.
 
 The first test compares calls with one another, bit for bit: a row's result may depend on nothing that
 the row does not see.  Where values are compared, the bounds are those of ``test_gpu_attn`` and, for
@@ -110,3 +110,22 @@ def test_scales_of_v_far_apart(D, Hq, Hk, new, kv, fmt):
         bad = np.abs(got[t:t + m] - o) > 2.0 ** -8 * np.abs(o) + (2.0 ** -8 * (1 + 2.0 ** -8) + F32_TERMS) * a + lost
         assert not bad.any(), f"sequence {b}: {int(bad.sum())} off, first at {tuple(np.argwhere(bad)[0])}"
         t += m
+
+
+@pytest.mark.parametrize("D,Hq,Hk,new,kv", [(128, 8, 2, [150, 30], [300, 40]), (64, 4, 2, [200], [200]), (128, 8, 2, [2, 1], [300, 40]), (80, 4, 2, [20, 3], [300, 40])])
+def test_any_entry_outside_the_cache_is_reported(D, Hq, Hk, new, kv):
+    s = _make(new, kv, Hq, Hk, D)
+    plain = _call(s)
+    pages = s["cache"][0].shape[0]
+    assert gb.device_error() == 0
+    for column in (3, (kv[0] - 1) // 16):  # in the middle, and the last page
+        kept = int(s["table"][0, column])
+        for bad in (-1, pages, -2 ** 31, 2 ** 31 - 1, -2 ** 31 + 1):
+            s["table"][0, column] = bad
+            got = _call(s)
+            assert gb.device_error(clear=True) == gb.ERR_BAD_SLOT, bad
+            see = torch.arange(new[0], device="cuda") + kv[0] - new[0] >= 16 * column
+            assert got[0][:new[0]][see].isnan().all(), bad
+            others = torch.cat([torch.nonzero(~see).flatten(), torch.arange(new[0], s["T"], device="cuda")])
+            assert _same(got, plain, others), bad
+        s["table"][0, column] = kept
