@@ -579,6 +579,7 @@ __device__ __forceinline__ void softmax(const AttnArgs& A, Shared& sh, uint32_t 
             }
           }
           part = make_float2(0.f, 0.f);
+          tm_wait_st();  // stores to tensor memory keep no order of their own: the first weights lie before the second come
           weigh();
         }
         sum = add2(sum, part);

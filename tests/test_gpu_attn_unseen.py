@@ -1,4 +1,5 @@
-"""GPU: keys that a row does not see and pages outside the cache, in each of the kernels of attention over the paged 8-bit cache.
+"""GPU: keys that a row does not see, pages outside the cache and rows whose reference moves in every step,
+in each of the kernels of attention over the paged 8-bit cache.
 
 The first test compares calls with one another, bit for bit: a row's result may depend on nothing that
 the row does not see.  Where values are compared, the bounds are those of ``test_gpu_attn`` and, for
@@ -14,7 +15,7 @@ import rmsnorm_fwd_bwd_03_gb300 as gb
 from oracle import heads
 
 from _checks import to64
-from test_gpu_attn import F32_TERMS, _args, _make
+from test_gpu_attn import F32_TERMS, _args, _check, _make
 
 pytestmark = pytest.mark.gpu
 
@@ -129,3 +130,26 @@ def test_any_entry_outside_the_cache_is_reported(D, Hq, Hk, new, kv):
             others = torch.cat([torch.nonzero(~see).flatten(), torch.arange(new[0], s["T"], device="cuda")])
             assert _same(got, plain, others), bad
         s["table"][0, column] = kept
+
+
+@pytest.mark.parametrize("D,new,kv", [(128, [130, 70], [700, 200]), (64, [300], [900]), (96, [64], [500])])
+def test_references_that_move_in_every_step(D, new, kv):
+    """Scores that rise by up to 9 from one 64 keys to the next (another rise for every third row): rows whose
+    weights are computed anew beside rows whose are not."""
+    s = _make(new, kv, 4, 2, D)
+    r = np.random.default_rng(1)
+    s["q"][:] = (torch.arange(s["T"], device="cuda") % 3 / 2).to(torch.bfloat16)[:, None, None]
+    for b, n in enumerate(kv):
+        scale = ((9.0 * (np.arange(n) // 64) + r.random(n)) / (127 * D ** 0.5)).astype(np.float32)
+        for j in range(n):
+            at = _place(s, b, j)
+            s["cache"][0][at] = 127
+            s["cache"][1][at] = float(scale[j])
+        s["values"][0][b] = np.broadcast_to(127.0 * scale.astype(np.float64)[:, None, None], s["values"][0][b].shape)
+    out, lse = _call(s)
+    # scores up to 130 here (188 in powers of two), sums of D equal products, exact; then five roundings of scales and
+    # products: 5 * 2^-24 * 188 = 2^-14 in a weight's exponent, below the bound's 2^-11
+    _check(s, out, lse)
+    for _ in range(3):
+        again = _call(s)
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
