@@ -35,9 +35,10 @@ constexpr int kBegin = 1;               // tiles that a unit's begin counts for 
 constexpr int kConvWarps = 8;
 constexpr int kConvRows = kTile / kConvWarps / 8;  // keys of a converting thread
 constexpr int kManyThreads = 640;      // five groups of four warps: rows twice, conversion twice, products
-// Registers of a thread in each group; together what the block is launched with (640 x 96).
-constexpr int kRegsRows = 128, kRegsConv = 72, kRegsMma = 80;
-static_assert(2 * kRegsRows + 2 * kRegsConv + kRegsMma <= 5 * 96, "a larger sum would wait forever");
+// Registers of a thread in each group; together what the block is launched with (640 x 96).  A launch with fewer would
+// wait forever for the rest, so the host asks what the kernel was compiled to before its first one.
+constexpr int kRegsRows = 128, kRegsConv = 72, kRegsMma = 80, kRegsLaunch = 96;
+static_assert(2 * kRegsRows + 2 * kRegsConv + kRegsMma <= 5 * kRegsLaunch, "a larger sum would wait forever");
 
 template <int D>
 struct ManyShape {
@@ -722,7 +723,9 @@ gbln_status many_go(const AttnArgs& A, int blocks, bool q16, int o_align, cudaSt
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return GBLN_ERR_CUDA;
   if (!(ready.load(std::memory_order_acquire) >> dev & 1)) {
-    if (cudaFuncSetAttribute(attn8_many<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, M::SMEM) != cudaSuccess) {
+    cudaFuncAttributes is{};
+    if (cudaFuncGetAttributes(&is, attn8_many<D, FMT>) != cudaSuccess || is.numRegs < kRegsLaunch ||
+        cudaFuncSetAttribute(attn8_many<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, M::SMEM) != cudaSuccess) {
       cudaGetLastError();
       return GBLN_ERR_CUDA;
     }
