@@ -14,9 +14,10 @@ computes anything itself.
   (``rope_axes``) positions are [axes, T], a position for every axis.
 * ``qk_norm_rotary(q, k, q_weight, k_weight, positions, cos_sin, eps)`` -> ``(q', k')``:
   RMSNorm of every head of Q and K, then the rotation, in one pass; q and k may be
-  slices of one packed projection output.  The backward pass reads q and k again
-  (nothing else is kept); the weights' gradients come from a fixed-order reduction
-  (float32, cast to the weights' dtype).
+  slices of one packed projection output.  k may be None here (then k_weight too) and in
+  ``rotary``: k' is None then.  The backward pass reads q and k again (nothing else is
+  kept); the weights' gradients come from a fixed-order reduction (float32, cast to the
+  weights' dtype).
 * ``swiglu(gate, up)`` -> ``silu(gate) * up``.
 
 ``rms_norm`` and ``swiglu`` take ``checkpoint="int8"`` or ``"e4m3"``: what the backward
@@ -92,17 +93,19 @@ class _Rotary(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, positions, cos_sin):
         ctx.save_for_backward(positions, cos_sin)
-        return rope_fwd(q.contiguous(), k.contiguous(), positions, cos_sin)
+        return rope_fwd(q.contiguous(), _c(k), positions, cos_sin)
 
     @staticmethod
     def backward(ctx, dq, dk):
         positions, cos_sin = ctx.saved_tensors
-        dqi, dki = rope_bwd(dq.contiguous(), dk.contiguous(), positions, cos_sin)
+        dqi, dki = rope_bwd(dq.contiguous(), _c(dk), positions, cos_sin)
         return dqi, dki, None, None
 
 
 def _heads_in_rows(t):
-    """t [T, H, D] with its heads next to one another in each token row, as it lies where it does so."""
+    """t [T, H, D] (or None) with its heads next to one another in each token row, as it lies where it does so."""
+    if t is None:
+        return None
     ok = t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == t.shape[2]) and (t.shape[0] == 1 or t.stride(0) >= t.shape[1] * t.shape[2])
     return t if ok else t.contiguous()
 
@@ -135,7 +138,7 @@ class _QKNormRotary(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, q_weight, k_weight, positions, cos_sin, eps, axes, pairing):
         q, k = _heads_in_rows(q), _heads_in_rows(k)
-        q_weight, k_weight = q_weight.contiguous(), k_weight.contiguous()
+        q_weight, k_weight = q_weight.contiguous(), _c(k_weight)
         ctx.save_for_backward(q, k, q_weight, k_weight, positions, cos_sin)
         ctx.how = (eps, axes, pairing)
         return qk_norm_rope_fwd(q, k, q_weight, k_weight, positions, cos_sin, eps, axes=axes, pairing=pairing)
@@ -148,7 +151,7 @@ class _QKNormRotary(torch.autograd.Function):
         dqi, dki, part, P = qk_norm_rope_bwd(_heads_in_rows(dq), _heads_in_rows(dk), q, k, q_weight, k_weight, positions, cos_sin, eps,
                                              axes=axes, pairing=pairing)
         dwq, dwk = qk_norm_dw_finalize(part, P)
-        return dqi, dki, dwq.to(q_weight.dtype), dwk.to(k_weight.dtype), None, None, None, None, None
+        return dqi, dki, dwq.to(q_weight.dtype), None if k is None else dwk.to(k_weight.dtype), None, None, None, None, None
 
 
 def qk_norm_rotary(q, k, q_weight, k_weight, positions, cos_sin, eps, axes=None, pairing="half"):

@@ -92,3 +92,32 @@ def test_autograd_layer_chain():
     check_dw(to64(w.grad), dW, "weight.grad")
     check_dw(to64(wg.grad), Y.T @ dG, "wg.grad")
     check_dw(to64(wq.grad), Y.T @ dQ, "wq.grad")
+
+
+@pytest.mark.parametrize("pairing", ["half", "interleaved"])
+@pytest.mark.parametrize("axes", [False, True])
+def test_autograd_of_queries_alone(axes, pairing):
+    """k may be None, as in the calls below the wrappers: rotation, and norm with rotation."""
+    from oracle import heads
+    T, H, D, theta, eps = 33, 4, 64, 1e4, 1e-6
+    q, dq = _randn((T, H, D), torch.bfloat16, 31), _randn((T, H, D), torch.bfloat16, 32)
+    w = (1 + 0.1 * _randn((D,), torch.float32, 33)).bfloat16().requires_grad_()
+    pos = torch.stack([torch.arange(T), torch.arange(T).flip(0)]).int().cuda()
+    table = gb.rope_table(T, D, theta)
+    how, axis = (pos, {"axes": gb.rope_axes((D // 4, D // 4))}) if axes else (pos[0], {}), np.repeat([0, int(axes)], D // 4)
+    for norm in (True, False):
+        x = q.clone().requires_grad_()
+        w.grad = None
+        y, none = (ga.qk_norm_rotary(x, None, w, None, how[0], table, eps, pairing=pairing, **how[1]) if norm
+                   else ga.rotary(x, None, how[0], table, pairing=pairing, **how[1]))
+        assert none is None
+        y.backward(dq)
+        args = (pos.cpu().numpy(), axis, theta)
+        if norm:
+            check_io(to64(y), heads.norm_rotate(to64(q), to64(w), *args, eps, pairing), "bf16", "y")
+            dx, dw = heads.norm_rotate_bwd(to64(dq), to64(q), to64(w), *args, eps, pairing)
+            check_io(to64(w.grad), dw, "bf16", "dw")
+        else:
+            check_io(to64(y), heads.rotate(to64(q), *args, pairing), "bf16", "y")
+            dx = heads.rotate(to64(dq), *args, pairing, back=True)
+        check_io(to64(x.grad), dx, "bf16", "dx")
