@@ -743,7 +743,7 @@ gbln_status gbln_qk_norm_rope_fwd_cache8(const void* q, const void* k, const voi
  * needed), 16-byte aligned, contents of no account; calls that may overlap need one each.
  * Bitwise reproducible for fixed sizes, lengths, alignment and GPU model.
  * Errors: INVALID_ARG for Hq not a multiple of Hk, D > 512, Hq * D above 2^24, T * Hq or
- * max_pages * page_size above 2^30, a scale that is not finite (or beyond 3e38), window < 0
+ * max_pages * page_size above 2^30, a scale that is not finite (or beyond 2e38), window < 0
  * and as gbln_cache8_read; WORKSPACE.
  */
 int64_t gbln_attn_cache8_workspace(int64_t T, int32_t B, int32_t Hq, int32_t Hk, int32_t D,

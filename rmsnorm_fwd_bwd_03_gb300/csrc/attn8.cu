@@ -894,7 +894,8 @@ extern "C" gbln_status gbln_attn_cache8(const void* q, const int32_t* cu_seqlens
                                         int64_t ld_q, int64_t ld_out, float scale, int32_t causal, int32_t window,
                                         gbln_q8 fmt, gbln_dtype io, gbln_stream_t stream) {
   if (!dtype_ok(io) || !q8_ok(fmt) || !attn_sizes_ok(T, B, Hq, Hk, D)) return GBLN_ERR_INVALID_ARG;
-  if (max_pages < 0 || window < 0 || !(scale >= -3.0e38f && scale <= 3.0e38f)) return GBLN_ERR_INVALID_ARG;
+  // the scale is taken to powers of two: 2e38 * log2(e) is finite, 3e38 * log2(e) is not
+  if (max_pages < 0 || window < 0 || !(scale >= -2.0e38f && scale <= 2.0e38f)) return GBLN_ERR_INVALID_ARG;
   if (!ld_fits(T, (int64_t)Hq * D, ld_q) || !ld_fits(T, (int64_t)Hq * D, ld_out)) return GBLN_ERR_INVALID_ARG;
   if (!cache_ok(k_cache, Hk, D) || !cache_ok(v_cache, Hk, D)) return GBLN_ERR_INVALID_ARG;
   if (k_cache->pages != v_cache->pages || k_cache->page_size != v_cache->page_size) return GBLN_ERR_INVALID_ARG;

@@ -184,3 +184,14 @@ def test_attention_rejects(lib):
     assert lib.gbln_attn_cache8_workspace(4, 2, 3, 2, 64, BF16) == -1
     assert lib.gbln_attn_cache8_workspace(4, 2, 2, 1, 80, BF16) == 0
     assert lib.gbln_attn_cache8_workspace(0, 2, 2, 1, 64, BF16) == 0
+
+
+def test_attention_scales_stay_finite_in_powers_of_two(lib):
+    """The largest scale that is taken, times log2(e), is a float32; a larger one is refused."""
+    import rmsnorm_fwd_bwd_03_gb300 as gb
+    c = gb._pack_cache8(FAKE, FAKE, 4, 16, 128, 8, 8, 16, 1, 1), gb._pack_cache8(2 * FAKE, 2 * FAKE, 4, 16, 128, 8, 8, 16, 1, 1)
+    call = lambda scale: lib.gbln_attn_cache8(None, None, None, None, 4, *c, None, None, None, 0, 0, 2, 2, 1, 8, 16, 16, scale, 1, 0, 0, BF16, None)  # noqa: E731
+    for sign in (1.0, -1.0):
+        assert call(sign * 2e38) == OK
+        assert call(sign * 2.4e38) == INVALID
+    assert np.float32(2e38) * np.float32(np.log2(np.e)) < np.inf
