@@ -98,8 +98,9 @@ int gbln_version(void);
 /*
  * Per-device error word of the current device, a set of bits:
  *   1  a kernel's bounded wait on its own asynchronous (TMA bulk) copies, or
- *      (attention) on another part of its block, ran out; the kernel stopped
- *      early instead of hanging, so its outputs are incomplete;
+ *      (attention) on another part of its block, ran out; instead of hanging the
+ *      kernel stopped early, or (attention) ran on to its end with what it had,
+ *      all of it in bounds: its outputs are not valid;
  *   2  a RoPE call met a position outside [0, max_pos); that token's outputs
  *      are NaN (the table is not read);
  *   4  a cache call met a slot beyond the cache's last one (nothing was stored
@@ -730,10 +731,12 @@ gbln_status gbln_qk_norm_rope_fwd_cache8(const void* q, const void* k, const voi
  * (k_j, v_j = code * scale).  Head h of q goes with K/V head h / (Hq / Hk).  A row that sees no
  * key gives zeros and lse -infinity.  Scores, weights, their sums and results are float32;
  * with bf16 rows and D 64, 96, 128 or 256 the weights times v's scales are rounded to 16 bits
- * for their products: with many rows to bf16, with few to fp16 relative to the power of two
- * above the scales of v that the row has met (11 bits; what is below 2^-38 of it becomes 0).
+ * for their products: to bf16 with many rows and D up to 128, else to fp16 relative to the power
+ * of two above the scales of v that the row has met (11 bits; what is below 2^-38 of it becomes 0).
  * Keys that a row does not see have no part in it, whatever the cache holds there; pages that
  * no row of the sequence sees are not read (freed pages may hold any number in the table).
+ * A row that sees a key with a scale of NaN is NaN.  What a row is that sees an E4M3 code of NaN
+ * with another scale (no call here stores one) is not specified; other rows do not change.
  * cu_seqlens_q [B + 1], non-decreasing from 0, kv_lens [B], page_table [B, max_pages] int32,
  * read on the device (a captured call follows them); values beyond T or max_pages * page_size
  * are cut to it.  Rows behind cu_seqlens_q[B] are left as they are.  A page that is read and

@@ -38,7 +38,7 @@ struct AttnArgs {
   int HB, NHG;     // K/V heads of a block, groups of them
   float* part_o;   // [2 C, HB, rows, D]
   float* part_ml;  // [2 C, HB, rows, 2]
-  int* info;       // [C, 4]
+  int* info;       // [C, kAttnInfo]
   unsigned int* err;
 };
 
@@ -145,7 +145,7 @@ __device__ __forceinline__ int64_t walk_units(const AttnArgs& A, int64_t target,
       x.hg = 0;
       x.tiles = 0;
       if (i < all) unit_range<MR, TK>(A, x);
-      // 32 blocks' tiles fit 32 bits unless the context is beyond 2^26 tiles of a block
+      // in 64 bits: a block of rows alone may see 2^26 tiles
       int64_t mine = i < all ? (int64_t)(x.tiles + OV) * A.NHG : 0, sum = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -216,12 +216,12 @@ __device__ __forceinline__ int parts_behind(const Part& p, int64_t last) {
   return (int)c - (int)blockIdx.x;
 }
 
-// exp2(a - b) where b may be -infinity (nothing seen yet): 0 for a = -infinity.
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// The reference b of ex2(a - b) where nothing has been seen yet (b = -infinity): a = -infinity then gives 0, not NaN.
 __device__ __forceinline__ float finite_or_zero(float m) { return m == -INFINITY ? 0.f : m; }
 
 // What the joining kernel has to know of a unit that began in this block and was divided: the parts in

@@ -82,6 +82,14 @@ def test_a_neighbours_key_changes_nothing(io, D, Hq, Hk, new, kv, fmt, window):
         for c, k in zip(s["cache"], kept):
             c[page, off] = k
         assert _same(got, plain, others) and got[0][row].isnan().all()
+        if fmt == "e4m3":  # such codes alone
+            for i in (0, 2):
+                codes = s["cache"][i].view(torch.uint8)[page, off]
+                kept = codes.clone()
+                codes.fill_(0xff)
+                got = _call(s, window=window)
+                codes.copy_(kept)
+                assert _same(got, plain, others), f"sequence {b} key {j}: codes of NaN"
     assert _same(_call(s, window=window), plain, np.arange(s["T"]))
     assert gb.device_error() == 0
 
