@@ -16,8 +16,9 @@
 // Scores and sums are float32; weights times V's scales are rounded to bf16 (2^-8 at most) for their product:
 // with fp16's range small weights would be lost beside large ones.
 // Measured, 32 / 8 heads of 128: 2048 tokens over 32768 1.23 ms (870 TFLOP/s), 19 prompts of 32768 tokens
-// 1.03 ms (690 TFLOP/s).  The tensor cores are busy 38% of the time, issue slots 54%: a row's chain of
-// tensor-memory loads, scales and exponentials bounds a step; begin and end of a unit take 6 us.
+// 1.03 ms (690 TFLOP/s).  The tensor cores are busy 38% of the time, issue slots 54%, the shared-memory data pipe
+// (operands of the products, codes, scales) 74%: that and a row's chain of tensor-memory loads, scales and
+// exponentials bound a step; begin and end of a unit take 6 us.
 
 #include <atomic>
 
